@@ -4,6 +4,8 @@ stride-decomposed implicit GEMM, behind a C ABI (include/conv_bwd_data.h).
 Modules:
   binding    ctypes binding of the C ABI (loads lib/libconv_bwd_data.so; raises
              if it is missing -- there is no CPU fallback)
+  train      training-step operators on the same library (include/conv_bwd_train.h):
+             products grouped by expert, gradient clipping, the clipped policy loss
   build      in-tree nvcc build of the library
   workloads  seeded synthetic inputs and the named problem shapes
 
@@ -11,7 +13,7 @@ Modules:
 machines where the CUDA library has not been built.
 """
 
-__all__ = ["binding", "build", "workloads"]
+__all__ = ["binding", "build", "train", "workloads"]
 
 
 def __getattr__(name):

@@ -21,7 +21,8 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libconv_bwd_data.so")
 SOURCES = ["capi.cpp", "simt.cu", "tc_sm103.cu", "tc2_sm103.cu", "tc_fwd_sm103.cu", "tf32_sm103.cu", "grouped.cu",
-           "tc_grouped_sm103.cu", "tc_band_sm103.cu", "noalloc.cu"]
+           "tc_grouped_sm103.cu", "tc_band_sm103.cu", "noalloc.cu",
+           "train_capi.cpp", "experts_simt.cu", "grad_clip.cu", "policy_loss.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -33,7 +34,7 @@ def nvcc() -> str:
 
 
 def _deps_mtime() -> float:
-    paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "conv_bwd_data.h")]
+    paths = [os.path.join(d, f) for d in (CSRC, os.path.join(ROOT, "include")) for f in os.listdir(d)]
     return max(os.path.getmtime(p) for p in paths)
 
 

@@ -1,0 +1,71 @@
+// train.h -- types shared by the C ABI and the kernels of the training-step
+// operators (include/conv_bwd_train.h).
+#pragma once
+#include <stdint.h>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace cbd {
+
+constexpr int kMaxExperts = 1024;  // the expert tables of a launch live in shared memory
+
+enum : int { kExpForward = 0, kExpData = 1, kExpWeight = 2 };
+
+// Expert product on CUDA cores (any sizes, strides and alignment).
+struct ExpertSimtParams {
+    const void *a;           // x (forward), dy (data, weight)
+    const void *b;           // w (forward, data), x (weight)
+    void *out;               // y, dx or dw
+    const int32_t *offsets;  // [experts + 1]
+    int32_t *status;
+    int64_t lda, ldb, ldo;   // row strides of the row-sorted tensors (ldb: weight only; ldo: forward, data)
+    int32_t experts, rows, K, N;
+    int32_t accumulate;
+};
+cudaError_t launch_experts_simt(const ExpertSimtParams &p, int dtype, int dir, int num_sms, cudaStream_t s);
+
+// Gradient clipping: the tensors are cut into chunks of kClipChunk bytes.
+constexpr int kClipChunk = 32768;
+constexpr int kClipPtrs = 1000;  // tensors per launch (their pointers travel as kernel parameters)
+struct ClipChunk {
+    int32_t tensor;  // index within the launch's pointer table
+    int32_t index;   // chunk of that tensor
+};
+struct ClipParams {
+    const ClipChunk *chunks;
+    const int64_t *sizes;    // [tensors of this launch]
+    const int32_t *dtypes;
+    double *partials;        // one per block of every norm launch
+    uint32_t *ticket;
+    float *norm, *coef;
+    int32_t num_chunks;
+    int32_t partial_base;    // first partial of this launch
+    int32_t partial_total;   // partials of all launches (the last launch sums them), 0: not the last
+    int32_t want_coef;
+    float max_norm;
+    const void *g[kClipPtrs];
+    void *o[kClipPtrs];
+};
+cudaError_t launch_clip_norm(const ClipParams &p, int grid, cudaStream_t s);
+cudaError_t launch_clip_scale(const ClipParams &p, int grid, cudaStream_t s);
+
+// Policy loss.
+enum : int { kPolForward = 0, kPolBackward = 1, kPolBoth = 2 };
+struct PolicyParams {
+    const void *logits;
+    void *dlogits;
+    const int32_t *actions;
+    const float *advantage, *weight, *old_logp, *ref_logp;
+    const float *lse_in, *coef_in, *grad;  // backward
+    float *loss, *logp, *lse, *coef;       // forward (lse and coef NULL in the fused form)
+    double *partials;                      // one per block
+    uint32_t *ticket;
+    int32_t *status;
+    int64_t ld, ldd;
+    int32_t tokens, vocab;
+    float clip_lo, clip_hi, kl, scale;     // clamp bounds 1 - clip_low, 1 + clip_high
+};
+int policy_max_blocks(int num_sms);        // upper bound of any launch's blocks
+cudaError_t launch_policy(const PolicyParams &p, int dtype, int mode, int num_sms, cudaStream_t s);
+
+}  // namespace cbd

@@ -1,0 +1,319 @@
+"""Training-step operators: products grouped by expert, gradient clipping, the
+clipped policy loss (ctypes binding of include/conv_bwd_train.h).
+
+Argument checks and marshalling only, as in ``binding``: every step of the
+computation runs in the CUDA library.  Tensors are torch CUDA tensors; shapes,
+types and strides are checked here (ValueError), addresses and the rest by the
+library (ConvBwdError).  Outputs that are not passed in are allocated on the
+call's stream.  A plan owns a workspace that its calls share: calls of one plan
+must not overlap on the GPU, so keep one plan per stream.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import binding as _b
+from .binding import ConvBwdError, BF16, F32, OK  # noqa: F401  (part of this module's interface)
+
+_TORCH = {F32: torch.float32, BF16: torch.bfloat16}
+_NAMES = {"f32": F32, "bf16": BF16, torch.float32: F32, torch.bfloat16: BF16, F32: F32, BF16: BF16}
+_vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+
+EXPORTED = [
+    "conv_bwd_experts_create", "conv_bwd_experts_destroy", "conv_bwd_experts_forward", "conv_bwd_experts_data",
+    "conv_bwd_experts_weight", "conv_bwd_experts_get_status", "conv_bwd_clip_create", "conv_bwd_clip_destroy",
+    "conv_bwd_clip_norm", "conv_bwd_clip_run", "conv_bwd_policy_create", "conv_bwd_policy_destroy",
+    "conv_bwd_policy_forward", "conv_bwd_policy_backward", "conv_bwd_policy_forward_backward",
+    "conv_bwd_policy_get_status",
+]
+
+
+class ExpertsDesc(ctypes.Structure):
+    _fields_ = [("experts", _i64), ("K", _i64), ("N", _i64), ("dtype", _i32)]
+
+
+class PolicyDesc(ctypes.Structure):
+    _fields_ = [("vocab", _i64), ("dtype", _i32), ("clip_low", _f32), ("clip_high", _f32), ("kl", _f32),
+                ("scale", _f32)]
+
+
+def _declare():
+    lib = _b.lib()
+    P = ctypes.POINTER
+    sig = {
+        "conv_bwd_experts_create": [P(ExpertsDesc), P(_vp)],
+        "conv_bwd_experts_destroy": [_vp],
+        "conv_bwd_experts_forward": [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp],
+        "conv_bwd_experts_data": [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp],
+        "conv_bwd_experts_weight": [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp],
+        "conv_bwd_experts_get_status": [_vp, _vp, P(_i32)],
+        "conv_bwd_clip_create": [_i32, P(_i64), P(_i32), P(_vp)],
+        "conv_bwd_clip_destroy": [_vp],
+        "conv_bwd_clip_norm": [_vp, _vp, _vp, _vp],
+        "conv_bwd_clip_run": [_vp, _vp, _vp, _f32, _vp, _vp, _vp],
+        "conv_bwd_policy_create": [P(PolicyDesc), P(_vp)],
+        "conv_bwd_policy_destroy": [_vp],
+        "conv_bwd_policy_forward": [_vp, _i64, _vp, _i64] + [_vp] * 10,
+        "conv_bwd_policy_backward": [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp],
+        "conv_bwd_policy_forward_backward": [_vp, _i64, _vp, _i64] + [_vp] * 8 + [_i64, _vp],
+        "conv_bwd_policy_get_status": [_vp, _vp, P(_i32)],
+    }
+    for name, args in sig.items():
+        f = getattr(lib, name)
+        f.argtypes = args
+        f.restype = ctypes.c_int
+    return lib
+
+
+_lib = _declare()
+
+
+def _dtype(d):
+    try:
+        return _NAMES[d]
+    except (KeyError, TypeError):
+        raise ValueError(f"dtype {d!r}: f32 or bf16 wanted") from None
+
+
+def _check(status, what):
+    if status != OK:
+        raise ConvBwdError(status, what)
+
+
+def _stream(stream):
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor whose memory belongs to the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(t, width, dtype, what):
+    """Checks a matrix of rows with unit column stride; returns (rows, row stride)."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[1] != width or not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA {dtype} matrix with {width} columns wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    rows = t.shape[0]
+    ld, unit = t.stride()
+    if unit != 1 and width > 1 or (rows > 1 and ld < width):
+        raise ValueError(f"{what}: unit column stride and rows that do not overlap wanted, got strides {t.stride()}")
+    return rows, max(ld, width)
+
+
+def _vector(t, n, dtype, what):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_cuda or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what}: a contiguous CUDA {dtype} vector of {n} wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+class _Plan:
+    _destroy = None
+    _h = None
+
+    def close(self):
+        h, self._h = self._h, None
+        if h:
+            self._destroy(h)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Experts(_Plan):
+    """Matrix products grouped by expert with ragged sizes.
+
+    Rows are sorted by expert; ``offsets`` (int32 CUDA tensor of experts + 1) says where each expert's rows begin, and
+    stays on the GPU.  ``w`` is [experts, n, k].  Rows of no expert give zero rows.
+    """
+    _destroy = staticmethod(_lib.conv_bwd_experts_destroy)
+
+    def __init__(self, experts, k, n, dtype="bf16"):
+        self.experts, self.k, self.n = int(experts), int(k), int(n)
+        self._code = _dtype(dtype)
+        self.dtype = _TORCH[self._code]
+        desc, h = ExpertsDesc(self.experts, self.k, self.n, self._code), _vp()
+        _check(_lib.conv_bwd_experts_create(ctypes.byref(desc), ctypes.byref(h)), "conv_bwd_experts_create")
+        self._h = h.value
+
+    def _w(self, w):
+        if w.dtype != self.dtype or w.shape != (self.experts, self.n, self.k) or not w.is_contiguous() or not w.is_cuda:
+            raise ValueError(f"w: a contiguous CUDA {self.dtype} tensor [{self.experts}, {self.n}, {self.k}] wanted, got {w.dtype} {tuple(w.shape)}")
+        return w.data_ptr()
+
+    def _product(self, call, what, a, wa, w, offsets, out, wo, stream):
+        rows, lda = _rows(a, wa, self.dtype, what)
+        off = _vector(offsets, self.experts + 1, torch.int32, "offsets")
+        wp = self._w(w)
+        if out is None:
+            out = _empty((rows, wo), self.dtype, a.device, stream)
+            ldo = wo
+        else:
+            r, ldo = _rows(out, wo, self.dtype, "out")
+            _need(r == rows, f"out: {rows} rows wanted, got {r}")
+        _check(call(self._h, rows, a.data_ptr(), lda, wp, off, out.data_ptr(), ldo, _stream(stream)), call.__name__)
+        return out
+
+    def forward(self, x, w, offsets, out=None, stream=None):
+        """y[i] = w[e] x[i] for the rows i of every expert e; x [rows, k] -> y [rows, n]."""
+        return self._product(_lib.conv_bwd_experts_forward, "x", x, self.k, w, offsets, out, self.n, stream)
+
+    def backward_data(self, dy, w, offsets, out=None, stream=None):
+        """dx[i] = w[e]^T dy[i]; dy [rows, n] -> dx [rows, k]."""
+        return self._product(_lib.conv_bwd_experts_data, "dy", dy, self.n, w, offsets, out, self.k, stream)
+
+    def backward_weight(self, dy, x, offsets, out=None, accumulate=False, stream=None):
+        """dw[e] = sum of dy[i] x[i]^T over the rows of e, in fp32 [experts, n, k]; added to ``out`` with ``accumulate``."""
+        rows, lddy = _rows(dy, self.n, self.dtype, "dy")
+        r, ldx = _rows(x, self.k, self.dtype, "x")
+        _need(r == rows, f"x: {rows} rows wanted as in dy, got {r}")
+        off = _vector(offsets, self.experts + 1, torch.int32, "offsets")
+        if out is None:
+            _need(not accumulate, "accumulate wants the gradients to add to in out")
+            out = _empty((self.experts, self.n, self.k), torch.float32, dy.device, stream)
+        elif out.dtype != torch.float32 or out.shape != (self.experts, self.n, self.k) or not out.is_contiguous() or not out.is_cuda:
+            raise ValueError(f"out: a contiguous CUDA fp32 tensor [{self.experts}, {self.n}, {self.k}] wanted, got {out.dtype} {tuple(out.shape)}")
+        _check(_lib.conv_bwd_experts_weight(self._h, rows, dy.data_ptr(), lddy, x.data_ptr(), ldx, off, out.data_ptr(),
+                                            1 if accumulate else 0, _stream(stream)), "conv_bwd_experts_weight")
+        return out
+
+    def status(self, stream=None):
+        """(status, detail) of the calls since the last one; synchronises the stream."""
+        det = _i32()
+        return _lib.conv_bwd_experts_get_status(self._h, _stream(stream), ctypes.byref(det)), det.value
+
+
+class GradClip(_Plan):
+    """Global L2 norm over many tensors, and clipping.
+
+    ``sizes`` and ``dtypes`` list the tensors' element counts and types; each call passes the tensors (contiguous, any
+    shape) in that order.
+    """
+    _destroy = staticmethod(_lib.conv_bwd_clip_destroy)
+
+    def __init__(self, sizes, dtypes):
+        sizes = [int(n) for n in sizes]
+        codes = [_dtype(d) for d in dtypes]
+        _need(len(sizes) == len(codes), f"{len(sizes)} sizes and {len(codes)} dtypes")
+        self._want = list(zip(sizes, (_TORCH[c] for c in codes)))
+        self.count = n = len(sizes)
+        h = _vp()
+        _check(_lib.conv_bwd_clip_create(n, (_i64 * max(n, 1))(*sizes), (_i32 * max(n, 1))(*codes), ctypes.byref(h)), "conv_bwd_clip_create")
+        self._h = h.value
+        self._array = _vp * max(n, 1)
+
+    @classmethod
+    def like(cls, tensors):
+        """A plan for tensors of these sizes and types."""
+        return cls([t.numel() for t in tensors], [t.dtype for t in tensors])
+
+    def _pointers(self, tensors, what):
+        if len(tensors) != self.count:
+            raise ValueError(f"{what}: {self.count} tensors wanted, got {len(tensors)}")
+        for i, (t, (n, d)) in enumerate(zip(tensors, self._want)):
+            if t.numel() != n or t.dtype != d or not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{what}[{i}]: a contiguous CUDA {d} tensor of {n} elements wanted, got {t.dtype} {tuple(t.shape)}")
+        return self._array(*[t.data_ptr() for t in tensors])
+
+    def _scalar(self, device, stream):
+        return _empty((1,), torch.float32, device, stream)
+
+    def norm(self, grads, stream=None):
+        """The norm as a CUDA fp32 tensor [1]."""
+        g = self._pointers(grads, "grads")
+        norm = self._scalar(grads[0].device if grads else "cuda", stream)
+        _check(_lib.conv_bwd_clip_norm(self._h, g, norm.data_ptr(), _stream(stream)), "conv_bwd_clip_norm")
+        return norm
+
+    def clip(self, grads, max_norm, out=None, stream=None):
+        """Scales ``grads`` by coef = min(1, max_norm / (norm + 1e-6)), in place or into ``out``; returns (norm, coef)."""
+        max_norm = float(max_norm)
+        _need(not math.isnan(max_norm) and max_norm >= 0, f"max_norm {max_norm}: a number >= 0 wanted")
+        g = self._pointers(grads, "grads")
+        o = g if out is None else self._pointers(out, "out")
+        both = _empty((2,), torch.float32, grads[0].device if grads else "cuda", stream)
+        at = both.data_ptr()
+        _check(_lib.conv_bwd_clip_run(self._h, g, o, max_norm, at, at + 4, _stream(stream)), "conv_bwd_clip_run")
+        return both[:1], both[1:]
+
+
+class PolicyLoss(_Plan):
+    """Clipped policy loss with a KL term, from logits.
+
+    loss = sum_t weight_t (-min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A) + kl (exp(d) - d - 1)) with
+    r = exp(logp - old_logp), d = ref_logp - logp and logp the log-probability of the chosen token under
+    softmax(scale * logits).  Tokens with weight 0 or a negative action are masked.
+    """
+    _destroy = staticmethod(_lib.conv_bwd_policy_destroy)
+
+    def __init__(self, vocab, dtype="bf16", clip_low=0.2, clip_high=0.2, kl=0.0, scale=1.0):
+        self.vocab = int(vocab)
+        self._code = _dtype(dtype)
+        self.dtype = _TORCH[self._code]
+        desc, h = PolicyDesc(self.vocab, self._code, clip_low, clip_high, kl, scale), _vp()
+        _check(_lib.conv_bwd_policy_create(ctypes.byref(desc), ctypes.byref(h)), "conv_bwd_policy_create")
+        self._h = h.value
+
+    def _inputs(self, logits, actions, advantage, weight, old_logp, ref_logp):
+        t, ld = _rows(logits, self.vocab, self.dtype, "logits")
+        f = torch.float32
+        return t, (self._h, t, logits.data_ptr(), ld, _vector(actions, t, torch.int32, "actions"),
+                   _vector(advantage, t, f, "advantage"), _vector(weight, t, f, "weight"),
+                   None if old_logp is None else _vector(old_logp, t, f, "old_logp"),
+                   None if ref_logp is None else _vector(ref_logp, t, f, "ref_logp"))
+
+    def _grad_out(self, logits, t, out, stream):
+        if out is None:
+            return _empty((t, self.vocab), self.dtype, logits.device, stream), self.vocab
+        r, ld = _rows(out, self.vocab, self.dtype, "out")
+        _need(r == t, f"out: {t} rows wanted, got {r}")
+        return out, ld
+
+    def forward(self, logits, actions, advantage, weight, old_logp=None, ref_logp=None, stream=None):
+        """(loss [1], logp, lse, coef [tokens]); lse and coef are what ``backward`` needs."""
+        t, args = self._inputs(logits, actions, advantage, weight, old_logp, ref_logp)
+        pad = (t + 3) // 4 * 4
+        s = _empty((3 * pad + 1,), torch.float32, logits.device, stream)
+        at = s.data_ptr()
+        _check(_lib.conv_bwd_policy_forward(*args, at + 12 * pad, at, at + 4 * pad, at + 8 * pad, _stream(stream)), "conv_bwd_policy_forward")
+        return s[3 * pad:], s[:t], s[pad:pad + t], s[2 * pad:2 * pad + t]
+
+    def backward(self, logits, actions, lse, coef, grad=None, out=None, stream=None):
+        """dlogits from the forward's lse and coef; ``grad`` [1] is the loss's upstream gradient; ``out`` may be logits."""
+        t, ld = _rows(logits, self.vocab, self.dtype, "logits")
+        f = torch.float32
+        args = (self._h, t, logits.data_ptr(), ld, _vector(actions, t, torch.int32, "actions"), _vector(lse, t, f, "lse"),
+                _vector(coef, t, f, "coef"), None if grad is None else _vector(grad, 1, f, "grad"))
+        out, ldd = self._grad_out(logits, t, out, stream)
+        _check(_lib.conv_bwd_policy_backward(*args, out.data_ptr(), ldd, _stream(stream)), "conv_bwd_policy_backward")
+        return out
+
+    def forward_backward(self, logits, actions, advantage, weight, old_logp=None, ref_logp=None, out=None, stream=None):
+        """(loss [1], logp [tokens], dlogits) in one launch; ``out`` may be logits."""
+        t, args = self._inputs(logits, actions, advantage, weight, old_logp, ref_logp)
+        out, ldd = self._grad_out(logits, t, out, stream)
+        s = _empty((t + 1,), torch.float32, logits.device, stream)
+        at = s.data_ptr()
+        _check(_lib.conv_bwd_policy_forward_backward(*args, at + 4 * t, at, out.data_ptr(), ldd, _stream(stream)), "conv_bwd_policy_forward_backward")
+        return s[t:], s[:t], out
+
+    def status(self, stream=None):
+        """(status, detail) of the calls since the last one; synchronises the stream."""
+        det = _i32()
+        return _lib.conv_bwd_policy_get_status(self._h, _stream(stream), ctypes.byref(det)), det.value
