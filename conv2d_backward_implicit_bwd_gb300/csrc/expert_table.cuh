@@ -11,48 +11,50 @@
 namespace cbd {
 
 struct ExpertTable {
-    int32_t begin[kMaxExperts];      // first row of the expert
-    int32_t len[kMaxExperts];        // its rows
-    int32_t tile[kMaxExperts + 1];   // first tile of the expert; tile[experts] = all tiles
+    int32_t off[kMaxExperts + 1];   // expert e owns rows [off[e], off[e + 1])
+    int32_t tile[kMaxExperts + 1];  // first tile of expert e; tile[experts] = all tiles
+    __device__ __forceinline__ int len(int e) const { return off[e + 1] - off[e]; }
 };
 
 // Filled by one warp.  `per`: rows per tile, `mult`: tiles per block of `per`
-// rows.  An expert whose offsets are out of [0, rows] or fall below an earlier
-// offset is empty and recorded as a fault, so that the experts' rows are
-// disjoint and no later access leaves the tensors.
+// rows.  Offsets below an earlier one or out of [0, rows] are recorded as a
+// fault and read as the running maximum clamped to that range: the experts'
+// rows stay disjoint and inside the tensors whatever the offsets hold.
 __device__ __forceinline__ void build_expert_table(ExpertTable &t, const int32_t *offsets, int experts, int rows,
                                                    int per, int mult, int32_t *status) {
     const int lane = threadIdx.x & 31;
-    int base_tile = 0, top = 0;  // top: largest offset so far
-    for (int e0 = 0; e0 < experts; e0 += 32) {
+    int top = 0;  // largest offset so far
+    for (int e0 = 0; e0 <= experts; e0 += 32) {
         const int e = e0 + lane;
-        int lo = e < experts ? offsets[e] : 0, hi = e < experts ? offsets[e + 1] : 0;
-        int most = max(top, lo);
+        const int raw = e <= experts ? offsets[e] : 0;
+        int most = max(top, raw);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, most, d);
             if (lane >= d) most = max(most, v);
         }
         top = __shfl_sync(0xffffffffu, most, 31);
-        if (e < experts && (lo < most || hi < lo || hi > rows)) {
-            record_status(status, kDevFaultIndex);
-            lo = hi = 0;
+        const int o = min(most, rows);
+        if (e <= experts) {
+            if (o != raw) record_status(status, kDevFaultIndex);
+            t.off[e] = o;
         }
-        int n = (int)(((int64_t)(hi - lo) + per - 1) / per) * mult;
+    }
+    __syncwarp();
+    int base = 0;
+    for (int e0 = 0; e0 < experts; e0 += 32) {
+        const int e = e0 + lane;
+        const int n = e < experts ? (int)(((int64_t)t.len(e) + per - 1) / per) * mult : 0;
         int incl = n;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, incl, d);
             if (lane >= d) incl += v;
         }
-        if (e < experts) {
-            t.begin[e] = lo;
-            t.len[e] = hi - lo;
-            t.tile[e] = base_tile + incl - n;
-        }
-        base_tile += __shfl_sync(0xffffffffu, incl, 31);
+        if (e < experts) t.tile[e] = base + incl - n;
+        base += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) t.tile[experts] = base_tile;
+    if (lane == 0) t.tile[experts] = base;
 }
 
 // Expert of tile t (tile[e] <= t < tile[e + 1]), by bisection.
@@ -66,12 +68,6 @@ __device__ __forceinline__ int expert_of_tile(const ExpertTable &tab, int expert
             hi = mid - 1;
     }
     return lo;
-}
-
-// Rows of no expert: [0, fill_lo) and [fill_hi, rows).
-__device__ __forceinline__ void fill_bounds(const int32_t *offsets, int experts, int rows, int &fill_lo, int &fill_hi) {
-    fill_lo = min(max(offsets[0], 0), rows);
-    fill_hi = min(max(offsets[experts], fill_lo), rows);
 }
 
 }  // namespace cbd

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(NT) experts_simt_kernel(const ExpertSimtParams
             mb = (t - tab.tile[e]) / n_tiles;
             nb = (t - tab.tile[e]) % n_tiles;
         }
-        const int64_t r0 = tab.begin[e], len = tab.len[e];
+        const int64_t r0 = tab.off[e], len = tab.len(e);
         const int64_t L = DIR == kExpForward ? p.K : DIR == kExpData ? p.N : len;
         if (DIR == kExpWeight && p.accumulate && len == 0) continue;
         const int i_lim = (int)min((int64_t)BT, (DIR == kExpWeight ? (int64_t)p.N : len) - (int64_t)mb * BT);
@@ -134,8 +134,7 @@ __global__ void __launch_bounds__(NT) experts_simt_kernel(const ExpertSimtParams
     }
 
     if constexpr (DIR != kExpWeight) {
-        int lo, hi;
-        fill_bounds(p.offsets, p.experts, p.rows, lo, hi);
+        const int lo = tab.off[0], hi = tab.off[p.experts];
         const int64_t nfill = (int64_t)lo + (p.rows - hi);
         for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
             O *row = out + (f < lo ? f : hi + (f - lo)) * p.ldo;

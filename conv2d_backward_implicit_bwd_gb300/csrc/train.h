@@ -24,6 +24,22 @@ struct ExpertSimtParams {
 };
 cudaError_t launch_experts_simt(const ExpertSimtParams &p, int dtype, int dir, int num_sms, cudaStream_t s);
 
+// Expert product on tensor cores over pairs of SMs (bf16, 16-byte aligned rows).
+struct ExpertPairParams {  // 128-byte aligned through CUtensorMap
+    CUtensorMap a;           // forward, data: w {K, N, experts}; weight: dy {N, rows}
+    CUtensorMap b;           // forward: x {K, rows}; data: dy {N, rows}; weight: x {K, rows}
+    CUtensorMap o;           // weight: dw {K, N, experts} in fp32
+    void *out;               // forward, data: y, dx
+    const int32_t *offsets;
+    int32_t *status;
+    int64_t wait_budget;
+    int64_t ldo;
+    int32_t experts, rows, K, N;
+    int32_t wide;            // second-operand columns of a tile: 512 or 256
+    int32_t accumulate;
+};
+cudaError_t launch_experts_pair(const ExpertPairParams &p, int dir, int grid, cudaStream_t s);
+
 // Gradient clipping: the tensors are cut into chunks of kClipChunk bytes.
 constexpr int kClipChunk = 32768;
 constexpr int kClipPtrs = 1000;  // tensors per launch (their pointers travel as kernel parameters)

@@ -110,6 +110,49 @@ conv_bwd_status create_plan(P **out, F &&init) {
 
 }  // namespace
 
+namespace {
+
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+    static EncodeTiled fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = (EncodeTiled)f;
+    });
+    return fn;
+}
+
+// Map of a matrix of rows {width, rows} (bf16, row stride ld elements), box 64 x box_rows.
+bool map_rows(CUtensorMap *m, const void *ptr, int64_t width, int64_t rows, int64_t ld, uint32_t box_rows) {
+    EncodeTiled enc = encode_tiled();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+    cuuint32_t box[2] = {64, box_rows}, one[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Map of [experts][N][K] (bf16, or fp32 for the gradients), box bk x bn of one expert, 128 bytes wide.
+bool map_filters(CUtensorMap *m, const void *ptr, const conv_bwd_experts_desc &d, bool f32, uint32_t bk, uint32_t bn) {
+    EncodeTiled enc = encode_tiled();
+    if (!enc) return false;
+    const cuuint64_t es = f32 ? 4 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)d.K, (cuuint64_t)d.N, (cuuint64_t)d.experts};
+    cuuint64_t strides[2] = {(cuuint64_t)d.K * es, (cuuint64_t)d.K * (cuuint64_t)d.N * es};
+    cuuint32_t box[3] = {bk, bn, 1}, one[3] = {1, 1, 1};
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr),
+               dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
 struct conv_bwd_experts_plan_s {
     conv_bwd_experts_desc d;
     DevicePart dev;
@@ -182,6 +225,33 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
         return CONV_BWD_ERR_INVALID_ARG;
     if (!p->dev.has_device) return CONV_BWD_ERR_CUDA;
     if (rows == 0 && (!weight || accumulate)) return CONV_BWD_OK;
+    // Tensor cores where TMA can load the operands: bf16, widths, strides and addresses on 16 bytes.
+    if (d.dtype == CONV_BWD_BF16 && d.K % 8 == 0 && d.N % 8 == 0 && lda % 8 == 0 && ldo % 8 == 0 && ldb % 8 == 0 &&
+        ((uintptr_t)a | (uintptr_t)b | (uintptr_t)out) % 16 == 0 && rows > 0 && d.K * d.N < (1LL << 37)) {
+        const int64_t mt = ((dir == kExpData ? d.K : d.N) + 255) / 256, pairs = std::max(1, p->dev.num_sms / 2);
+        // one half per tile where two would leave pairs without a tile
+        const int64_t est = weight ? d.experts * mt * ((d.K + 511) / 512) : mt * std::max<int64_t>(rows / 512, 1);
+        ExpertPairParams pp;
+        std::memset(&pp, 0, sizeof(pp));
+        pp.wide = est >= 2 * pairs ? 512 : 256;
+        bool ok;
+        if (dir == kExpForward)
+            ok = map_filters(&pp.a, b, d, false, 64, 128) && map_rows(&pp.b, a, d.K, rows, lda, 64);
+        else if (dir == kExpData)
+            ok = map_filters(&pp.a, b, d, false, 64, 64) && map_rows(&pp.b, a, d.N, rows, lda, 64);
+        else
+            ok = map_rows(&pp.a, a, d.N, rows, lda, 64) && map_rows(&pp.b, b, d.K, rows, ldb, 64) &&
+                 map_filters(&pp.o, out, d, true, 32, 32);
+        if (!ok) return CONV_BWD_ERR_CUDA;
+        pp.out = out; pp.offsets = offsets; pp.status = p->dev.status();
+        pp.wait_budget = (int64_t)p->dev.clock_khz * 2000;  // two seconds of SM clocks
+        pp.ldo = ldo;
+        pp.experts = (int32_t)d.experts; pp.rows = (int32_t)rows; pp.K = (int32_t)d.K; pp.N = (int32_t)d.N;
+        pp.accumulate = accumulate ? 1 : 0;
+        const int64_t most = weight ? d.experts * mt * ((d.K + pp.wide - 1) / pp.wide) : mt * (rows / pp.wide + std::min<int64_t>(d.experts, rows));
+        const int grid = (int)(2 * std::max<int64_t>(1, std::min(pairs, most)));
+        return launch_experts_pair(pp, dir, grid, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
+    }
     ExpertSimtParams sp;
     std::memset(&sp, 0, sizeof(sp));
     sp.a = a; sp.b = b; sp.out = out; sp.offsets = offsets; sp.status = p->dev.status();

@@ -51,8 +51,8 @@ extern "C" {
  * expert's results, NaN or infinity included.  One expert is a plain
  * linear layer.
  *
- * Offsets must be non-decreasing within [0, rows].  An expert whose pair of
- * offsets is not is treated as empty and recorded as a DEVICE_FAULT.
+ * Offsets must be non-decreasing within [0, rows].  Others are recorded as a
+ * DEVICE_FAULT and read as their running maximum clamped to that range.
  *
  * ld* are row strides in elements (>= the row's width; 0 means dense).
  * bf16 products are accumulated in fp32 and rounded once. */
