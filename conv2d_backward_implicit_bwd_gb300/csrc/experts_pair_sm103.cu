@@ -94,10 +94,7 @@ __device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
     return done != 0;
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // One tile: the same for every role.
@@ -434,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = 0u;
                         }
-                        if (lane == 0) bulk_wait_read<0>();
+                        if (lane == 0) bulk_wait_read();
                         __syncwarp();
                         const uint32_t sb = smem_u32(slab) + (uint32_t)lane * 128u;
 #pragma unroll
@@ -466,9 +463,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                 }
             } else {
                 // columns of the accumulator are rows of the output: 32 of them at a time are turned around in
-                // shared memory ([row][128 of the M dimension], 256 bytes) and leave as one bulk copy per row
+                // shared memory ([row][128 of the M dimension], 256 bytes) and leave in 16-byte stores, two
+                // whole row segments to an instruction.  (A bulk copy per row took 95 clocks each: 25 us a tile.)
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
-                const int width = min(128, mdim - m);  // may be <= 0: nothing to store
+                const int col = (lane & 15) * 8;
+                const bool col_ok = m + col < mdim;
                 for (int h = 0; h < w.halves; ++h, ++use) {
                     const uint32_t slot = use & 1;
                     // after a wait that ran out the warps go on meeting at their barriers, storing nothing
@@ -476,27 +475,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                     ok = __all_sync(0xffffffffu, ok);
                     tc_fence_after();
                     const int at = h ? w.at1 : 0, valid = min(h ? w.n1 : w.n0, w.ntok - at);
-                    const int64_t row0 = (int64_t)w.row0 + at;
+                    __nv_bfloat16 *dst = out + ((int64_t)w.row0 + at) * p.ldo + m + col;
 #pragma unroll 1
                     for (int g = 0; g < valid; g += 32, buf ^= 1) {
                         uint32_t v[32];
                         tmem_ld32(lane_base + slot * 256 + g, v);
-                        if (warp == 0) bulk_wait_read<1>();  // the buffer's copies of two groups ago have been read
-                        asm volatile("bar.sync 1, 128;" ::: "memory");
-                        const uint32_t sb = smem_u32(stage) + buf * 8192u + (uint32_t)(warp * 32 + lane) * 2u;
+                        const uint32_t sb = smem_u32(stage) + buf * 8192u;
+                        const uint32_t sw = sb + (uint32_t)(warp * 32 + lane) * 2u;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const __nv_bfloat16 x = __float2bfloat16_rn(__uint_as_float(v[i]));
-                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(sb + (uint32_t)i * 256u), "h"(*reinterpret_cast<const uint16_t *>(&x)) : "memory");
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(sw + (uint32_t)i * 256u), "h"(*reinterpret_cast<const uint16_t *>(&x)) : "memory");
                         }
-                        fence_proxy_async_smem();
+                        // one barrier per group: a buffer is written again after the next group's barrier,
+                        // which every warp reaches after reading it
                         asm volatile("bar.sync 1, 128;" ::: "memory");
-                        if (warp == 0) {
-                            if (ok && width > 0 && g + lane < valid)
-                                asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(out + (row0 + g + lane) * p.ldo + m),
-                                             "r"(smem_u32(stage) + buf * 8192u + (uint32_t)lane * 256u), "r"(width * 2)
-                                             : "memory");
-                            bulk_commit();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int r = warp * 8 + q * 2 + (lane >> 4);
+                            uint4 x;
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                         : "r"(sb + (uint32_t)r * 256u + (uint32_t)col * 2u)
+                                         : "memory");
+                            if (ok && col_ok && g + r < valid) *reinterpret_cast<uint4 *>(dst + (int64_t)(g + r) * p.ldo) = x;
                         }
                     }
                     tc_fence_before();
@@ -506,7 +508,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
             }
             if (DIR == kExpWeight && !__all_sync(0xffffffffu, ok)) break;
         }
-        bulk_wait_all();
+        if constexpr (DIR == kExpWeight) bulk_wait_all();
     }
 
     // no remote arrive or MMA may target a CTA that has left
