@@ -17,14 +17,11 @@
 //   data     w columns k, MN-major       dy rows i, K-major        n
 //   weight   dy columns n, MN-major      x columns k, MN-major     i
 //
-// A tile has up to 512 columns of B in two halves of up to 256, each with its
-// own 256 TMEM columns ("slot").  Slots are used in turn by the halves of all
-// tiles, so that a one-half tile is double-buffered against the next and a
-// two-half tile's successor starts on the first half while the epilogue drains
-// the second.  A two-half tile moves 48 KB per CTA for each 64-deep step of
-// 1024 MMA clocks, a one-half tile 32 KB for 512: the operands come from L2 at
-// about 45 bytes per SM clock, so wide tiles run nearer the MMA rate and narrow
-// ones spread over more pairs.
+// A tile is 256 x up to 256 with two accumulators in TMEM, so the epilogue of
+// one tile runs under the next one's MMAs.  (512 wide, single-buffered tiles
+// move 48 KB instead of 64 KB per CTA for the same work, but their exposed
+// epilogues cost more: 16384 x 1024 x 2048 forward 78 against 58 us, data
+// 32768 x 2048 x 2048 217 against 189 us, weight 103 against 79 us.)
 //
 // Ragged ends.  Rows past an expert's end that a box brings along are other
 // columns of D (forward, data), never stored.  For weight they would be
@@ -33,9 +30,14 @@
 // memory after they have landed (both operands: 0 x NaN is NaN) before the MMA
 // may read them.
 //
+// Schedule.  The tiles of all experts in falling cost order; a pair starts on
+// the tile of its own number and then draws the next one from a counter when it
+// begins loading the current one.  Which pair computes a tile does not change
+// the tile's bits.
+//
 // Roles per CTA: warps 0-3 epilogue, 4 A loads, 5 MMA (leader CTA) and TMEM,
-// 6-7 B loads (one half each), 8 helper of weight's last blocks.  Persistent over the
-// tiles of all experts; every wait is bounded.
+// 6-7 B loads, 8 helper of weight's last blocks, 9 schedule (leader CTA).
+// Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -50,21 +52,26 @@ namespace cbd {
 
 namespace {
 
-constexpr int S = 4;  // pipeline stages
+constexpr int S = 6;     // pipeline stages
+constexpr int RING = 4;  // tiles between the schedule and its readers
+constexpr int WIDE = 256;
 constexpr int A_BYTES = 128 * 64 * 2;
-constexpr int HALF_BYTES = 128 * 64 * 2;  // one half's B rows (or columns) of one CTA
-constexpr int B_BYTES = 2 * HALF_BYTES;
-constexpr int OUT_BYTES = 16384;  // epilogue staging
-constexpr int THREADS = 9 * 32;
+constexpr int B_BYTES = 128 * 64 * 2;  // one CTA's half of the tile's columns
+constexpr int OUT_BYTES = 16384;       // epilogue staging
+constexpr int THREADS = 10 * 32;
 
 struct Bars {
     uint64_t full[S], empty[S];
     uint64_t tail[S], peer[S];  // weight: last blocks landed in this CTA; peer's rows zeroed
     uint64_t tfull[2], tempty[2];
+    uint64_t given[RING], taken[RING];  // schedule: entry written; entry read by every role of the pair
+    uint64_t want;                      // the next tile may be drawn
+    int32_t ring[RING];
+    int32_t vote[8];  // forward, data: what each epilogue warp drew, two tiles in turn
     uint32_t tmem;
     int32_t abort;
 };
-constexpr int SMEM = 1024 + S * (A_BYTES + B_BYTES) + OUT_BYTES + (int)sizeof(ExpertTable) + (int)sizeof(Bars);
+constexpr int SMEM = 1024 + S * (A_BYTES + B_BYTES) + OUT_BYTES + (int)sizeof(ExpertTable) + 8 + (int)sizeof(Bars);
 static_assert(SMEM <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
@@ -82,64 +89,44 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
         : "memory");
 }
-__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// what the other CTA wrote before its release-arrive on a barrier of this one
+__device__ __forceinline__ void acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 
 // One tile: the same for every role.
 struct Tile {
-    int e, m0;          // expert, first row of the M dimension
-    int row0, ntok;     // forward, data: first row, rows of the tile
-    int c0;             // weight: first column
-    int halves;         // 0: weight tile of an expert without rows
-    int n0, n1;         // MMA width of each half
-    int at1;            // first row (column) of the second half within the tile
-    int nkb, last;      // k-blocks, valid depth of the last one
+    int e, m0;       // expert, first index of the M dimension
+    int row0, ntok;  // first row; forward, data: rows of the tile
+    int c0;          // weight: first column
+    int n;           // MMA width
+    int nkb, last;   // k-blocks, valid depth of the last one
 };
 
 template <int DIR>
-__device__ __forceinline__ Tile tile_of(const ExpertPairParams &p, const ExpertTable &tab, int mt, int nt, int t) {
+__device__ __forceinline__ Tile tile_of(const ExpertPairParams &p, const ExpertTable &tab, int mt, int t) {
     Tile r;
+    const int i = position_of_tile(tab, p.experts, t);
+    r.e = tab.order[i];
+    const int l = t - tab.tile[i], len = tab.len(r.e);
+    r.m0 = (l % mt) * 256;
     if constexpr (DIR == kExpWeight) {
-        r.e = t / (mt * nt);
-        const int l = t - r.e * mt * nt;
-        r.m0 = (l % mt) * 256;
-        r.c0 = (l / mt) * p.wide;
+        r.c0 = (l / mt) * WIDE;
         r.row0 = tab.off[r.e];
-        const int len = tab.len(r.e);
-        r.nkb = (len + 63) / 64;
+        r.nkb = (len + 63) / 64;  // 0: an expert without rows
         r.last = len - (r.nkb - 1) * 64;
-        r.halves = len == 0 ? 0 : (p.wide > 256 && r.c0 + 256 < p.K) ? 2 : 1;
-        r.n0 = r.n1 = 256;
-        r.at1 = 256;
+        r.n = WIDE;
         r.ntok = 0;
     } else {
-        r.e = expert_of_tile(tab, p.experts, t);
-        const int l = t - tab.tile[r.e], len = tab.len(r.e);
-        r.m0 = (l % mt) * 256;
-        // an expert's rows in equal chunks, a chunk in equal halves, rounded up to 32
-        const int chunks = (len + p.wide - 1) / p.wide;
-        const int size = ((len + chunks - 1) / chunks + 31) & ~31;
-        const int first = (l / mt) * size;
+        const int size = chunk_rows(len, WIDE), first = (l / mt) * size;
         r.row0 = tab.off[r.e] + first;
         r.ntok = min(size, len - first);
-        r.halves = r.ntok > 256 ? 2 : 1;
-        r.n0 = r.halves == 2 ? ((r.ntok + 1) / 2 + 31) & ~31 : (r.ntok + 31) & ~31;
-        r.at1 = r.n0;
-        r.n1 = r.halves == 2 ? (r.ntok - r.n0 + 31) & ~31 : 0;
-        const int depth = DIR == kExpForward ? p.K : p.N;
-        r.nkb = (depth + 63) / 64;
+        r.n = (r.ntok + 31) & ~31;
+        r.nkb = ((DIR == kExpForward ? p.K : p.N) + 63) / 64;
         r.last = 64;  // past the depth both operands read as zero
         r.c0 = 0;
     }
@@ -152,20 +139,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sA = smem, *sB = smem + S * A_BYTES;
     uint8_t *stage = sB + S * B_BYTES;
-    ExpertTable &tab = *reinterpret_cast<ExpertTable *>(stage + OUT_BYTES);
-    Bars &bars = *reinterpret_cast<Bars *>(stage + OUT_BYTES + sizeof(ExpertTable));
-    static_assert(sizeof(ExpertTable) % 8 == 0, "barriers on 8 bytes");
+    Bars &bars = *reinterpret_cast<Bars *>(stage + OUT_BYTES);
+    ExpertTable &tab = *reinterpret_cast<ExpertTable *>(stage + OUT_BYTES + (sizeof(Bars) + 7) / 8 * 8);
     volatile int32_t *abort_flag = &bars.abort;
 
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const uint32_t full0 = smem_u32(bars.full), empty0 = smem_u32(bars.empty), tail0 = smem_u32(bars.tail),
-                   peer0 = smem_u32(bars.peer), tfull0 = smem_u32(bars.tfull), tempty0 = smem_u32(bars.tempty);
+                   peer0 = smem_u32(bars.peer), tfull0 = smem_u32(bars.tfull), tempty0 = smem_u32(bars.tempty),
+                   given0 = smem_u32(bars.given), taken0 = smem_u32(bars.taken), want0 = smem_u32(&bars.want);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
     const int mdim = DIR == kExpData ? p.K : p.N;
     const int mt = (mdim + 255) / 256;
-    const int nt = DIR == kExpWeight ? (p.K + p.wide - 1) / p.wide : 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -178,6 +164,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
             mbar_init(tfull0 + 8 * b, 1);
             mbar_init(tempty0 + 8 * b, 8);  // 4 epilogue warps of each CTA
         }
+        for (int r = 0; r < RING; ++r) {
+            mbar_init(given0 + 8 * r, 1);
+            // loads (3) and epilogue (4) of both CTAs, the MMA, weight's helpers
+            mbar_init(taken0 + 8 * r, DIR == kExpWeight ? 17 : 15);
+        }
+        mbar_init(want0, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -191,7 +183,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
     }
     if (warp == 0)
-        build_expert_table(tab, p.offsets, p.experts, p.rows, p.wide, mt, blockIdx.x == 0 ? p.status : nullptr);
+        build_expert_table(tab, p.offsets, p.experts, p.rows, WIDE, DIR == kExpWeight ? mt * ((p.K + WIDE - 1) / WIDE) : mt,
+                           DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesByDepth,
+                           blockIdx.x == 0 ? p.status : nullptr);
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = bars.tmem;
@@ -199,23 +193,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         // the pair's MMAs write this CTA's rows at the leader's TMEM address
         if (ld_shared_cluster_u32(mapa_shared(smem_u32(&bars.tmem), 0)) != tmem_base) record_status(p.status, kDevFaultIndex);
     }
-    const int total = DIR == kExpWeight ? p.experts * mt * nt : tab.tile[p.experts];
+    const int total = tab.tile[p.experts];
 
-    if (warp == 4 || warp == 6 || warp == 7) {
+    // The i-th tile of this pair, for one reader (a thread, or a warp whose
+    // lane 0 does the waiting); -1 after a wait that ran out.
+    const uint32_t taken_leader0 = mapa_shared(taken0, 0);
+    auto next_tile = [&](int i, int32_t code) {
+        const uint32_t r = (uint32_t)i % RING, ph = ((uint32_t)i / RING) & 1;
+        if (!mbar_wait_bounded(given0 + 8 * r, ph, p.wait_budget, abort_flag, p.status, code)) return -1;
+        acquire_cluster();
+        const int t = *reinterpret_cast<volatile int32_t *>(&bars.ring[r]);
+        mbar_arrive_remote(taken_leader0 + 8 * r);
+        return t < total ? t : -1;
+    };
+
+    if (warp == 9) {
+        // ------------------------------------------------------------ schedule (leader)
+        if (leader && lane == 0) {
+            const uint32_t ring_peer = mapa_shared(smem_u32(bars.ring), 1), given_peer = mapa_shared(given0, 1);
+            int t = pair;
+            for (int i = 0;; ++i) {
+                const uint32_t r = (uint32_t)i % RING, ph = ((uint32_t)i / RING) & 1;
+                if (!mbar_wait_bounded(taken0 + 8 * r, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) break;
+                *reinterpret_cast<volatile int32_t *>(&bars.ring[r]) = t;
+                st_cluster(ring_peer + 4 * r, t);
+                mbar_arrive(given0 + 8 * r);
+                mbar_arrive_remote(given_peer + 8 * r);
+                if (t >= total) break;
+                if (!mbar_wait_bounded(want0, (uint32_t)i & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) break;
+                t = npairs + atomicAdd(p.next, 1);
+            }
+            // the last pair to finish its schedule leaves the counters as it found them
+            if (atomicAdd(p.next + 1, 1) == npairs - 1) {
+                p.next[0] = 0;
+                p.next[1] = 0;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 4 || warp == 6 || warp == 7) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
             const uint32_t full_leader0 = mapa_shared(full0, 0);
-            const int h = warp - 6;  // B half of this warp
             uint32_t it = 0;
             bool ok = true, issued = false;
-            for (int t = pair; t < total && ok; t += npairs) {
-                const Tile w = tile_of<DIR>(p, tab, mt, nt, t);
-                const int half_rows = DIR == kExpWeight ? 128 : (h == 1 ? w.n1 : w.n0) / 2;
-                const int half_at = h == 1 ? w.at1 : 0;
-                const int boxes0 = DIR == kExpWeight ? 2 : (w.n0 / 2 + 63) / 64;
-                const int boxes1 = w.halves < 2 ? 0 : DIR == kExpWeight ? 2 : (w.n1 / 2 + 63) / 64;
-                const uint32_t bytes = (uint32_t)A_BYTES + 8192u * (uint32_t)(boxes0 + boxes1);  // of one CTA
-                const int my_boxes = h == 0 ? boxes0 : h == 1 ? boxes1 : 0;
+            for (int i = 0; ok; ++i) {
+                const int t = next_tile(i, kDevTimeoutProducer);
+                if (t < 0) break;
+                if (warp == 4 && leader) mbar_arrive(want0);
+                const Tile w = tile_of<DIR>(p, tab, mt, t);
+                // B columns of this CTA in boxes of 64, one for each B warp
+                const int half = w.n / 2, boxes = (half + 63) / 64, q = warp - 6;
+                const uint32_t bytes = (uint32_t)A_BYTES + 8192u * (uint32_t)boxes;  // of one CTA
+                const int at = (int)rank * half + 64 * q;
                 for (int kb = 0; kb < w.nkb; ++kb, ++it) {
                     const uint32_t s = it % S, ph = (it / S) & 1;
                     if (!mbar_wait_bounded(empty0 + 8 * s, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) {
@@ -238,27 +267,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                             tma_load_3d_pair(dst, &p.a, bar, m, kb * 64, w.e);
                             tma_load_3d_pair(dst + 8192, &p.a, bar, m + 64, kb * 64, w.e);
                         } else {
-                            for (int q = 0; q < 2; ++q)
+                            for (int b = 0; b < 2; ++b)
                                 if (fix)
-                                    tma_load_2d(dst + 8192 * q, &p.a, bar, m + 64 * q, w.row0 + kb * 64);
+                                    tma_load_2d(dst + 8192 * b, &p.a, bar, m + 64 * b, w.row0 + kb * 64);
                                 else
-                                    tma_load_2d_pair(dst + 8192 * q, &p.a, bar, m + 64 * q, w.row0 + kb * 64);
+                                    tma_load_2d_pair(dst + 8192 * b, &p.a, bar, m + 64 * b, w.row0 + kb * 64);
                         }
-                    } else {
-                        const uint32_t dst = smem_u32(sB + s * B_BYTES + h * HALF_BYTES);
-                        for (int q = 0; q < my_boxes; ++q) {
-                            const int at = half_at + (int)rank * half_rows + 64 * q;
-                            if constexpr (DIR == kExpWeight) {
-                                if (fix)
-                                    tma_load_2d(dst + 8192 * q, &p.b, bar, w.c0 + at, w.row0 + kb * 64);
-                                else
-                                    tma_load_2d_pair(dst + 8192 * q, &p.b, bar, w.c0 + at, w.row0 + kb * 64);
-                            } else {
-                                tma_load_2d_pair(dst + 8192 * q, &p.b, bar, kb * 64, w.row0 + at);
-                            }
+                        issued = true;
+                    } else if (q < boxes) {
+                        const uint32_t dst = smem_u32(sB + s * B_BYTES + 8192 * q);
+                        if constexpr (DIR == kExpWeight) {
+                            if (fix)
+                                tma_load_2d(dst, &p.b, bar, w.c0 + at, w.row0 + kb * 64);
+                            else
+                                tma_load_2d_pair(dst, &p.b, bar, w.c0 + at, w.row0 + kb * 64);
+                        } else {
+                            tma_load_2d_pair(dst, &p.b, bar, kb * 64, w.row0 + at);
                         }
+                        issued = true;
                     }
-                    issued = true;
                 }
             }
             if (!ok && issued) {
@@ -274,35 +301,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
             const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((A_K ? 0u : 1u) << 15) | ((B_K ? 0u : 1u) << 16) | ((uint32_t)(256 >> 4) << 24);
             const uint64_t a_desc0 = smem_desc_sw128(smem_u32(sA), A_K ? 16 : 8192, 1024);
             const uint64_t b_desc0 = smem_desc_sw128(smem_u32(sB), B_K ? 16 : 8192, 1024);
-            uint32_t it = 0, use = 0;  // stages and slots used so far
+            uint32_t it = 0, use = 0;  // stages and accumulators used so far
             bool ok = true, issued = false;
-            for (int t = pair; t < total && ok; t += npairs) {
-                const Tile w = tile_of<DIR>(p, tab, mt, nt, t);
-                if (w.halves == 0) continue;
-                const uint32_t s0 = use & 1, p0 = ((use >> 1) & 1) ^ 1;
-                const uint32_t s1 = s0 ^ 1, p1 = (((use + 1) >> 1) & 1) ^ 1;
-                if (!mbar_wait_bounded(tempty0 + 8 * s0, p0, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
+            for (int i = 0; ok; ++i) {
+                const int t = next_tile(i, kDevTimeoutMma);
+                if (t < 0) break;
+                const Tile w = tile_of<DIR>(p, tab, mt, t);
+                if (w.nkb == 0) continue;
+                const uint32_t b = use & 1, bph = (use >> 1) & 1;
+                ++use;
+                if (!mbar_wait_bounded(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t id0 = idesc0 | ((uint32_t)(w.n0 >> 3) << 17), id1 = idesc0 | ((uint32_t)(w.n1 >> 3) << 17);
-                const uint32_t d0 = tmem_base + s0 * 256, d1 = tmem_base + s1 * 256;
-                const uint32_t it0 = it;
-                int pend = 0;  // first k-block whose second half is pending
-                bool h1 = false;
-                const bool two = w.halves == 2;
-                auto steps = [&](int kb) { return DIR == kExpWeight && kb == w.nkb - 1 ? (w.last + 15) / 16 : 4; };
-                auto second = [&](int kb) {
-                    const uint32_t sq = (it0 + (uint32_t)kb) % S;
-                    const uint64_t ad = a_desc0 + (uint64_t)((sq * A_BYTES) >> 4);
-                    const uint64_t bd = b_desc0 + (uint64_t)((sq * B_BYTES + HALF_BYTES) >> 4);
-                    const int n = steps(kb);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (kk < n) tc_mma2(d1, ad + A_STEP * kk, bd + B_STEP * kk, id1, (kb | kk) != 0 ? 1u : 0u);
-                    tc_commit2_mc(empty0 + 8 * sq, (uint16_t)0x3);
-                };
+                const uint32_t id = idesc0 | ((uint32_t)(w.n >> 3) << 17), d = tmem_base + b * 256;
                 for (int kb = 0; kb < w.nkb; ++kb, ++it) {
                     const uint32_t s = it % S, ph = (it / S) & 1;
                     if (!mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
@@ -310,43 +323,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                         break;
                     }
                     const uint64_t ad = a_desc0 + (uint64_t)((s * A_BYTES) >> 4), bd = b_desc0 + (uint64_t)((s * B_BYTES) >> 4);
-                    const int n = steps(kb);
+                    const int n = DIR == kExpWeight && kb == w.nkb - 1 ? (w.last + 15) / 16 : 4;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        if (kk < n) tc_mma2(d0, ad + A_STEP * kk, bd + B_STEP * kk, id0, (kb | kk) != 0 ? 1u : 0u);
+                        if (kk < n) tc_mma2(d, ad + A_STEP * kk, bd + B_STEP * kk, id, (kb | kk) != 0 ? 1u : 0u);
                     issued = true;
-                    if (!two) {
-                        tc_commit2_mc(empty0 + 8 * s, (uint16_t)0x3);
-                        continue;
-                    }
-                    if (!h1) {
-                        h1 = test_wait(tempty0 + 8 * s1, p1);
-                        if (!h1 && kb + 1 - pend >= S) {  // every stage is held for the second half
-                            if (!mbar_wait_bounded(tempty0 + 8 * s1, p1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
-                                ok = false;
-                                break;
-                            }
-                            h1 = true;
-                        }
-                        if (h1) tc_fence_after();
-                    }
-                    if (h1)
-                        for (; pend <= kb; ++pend) second(pend);
+                    tc_commit2_mc(empty0 + 8 * s, (uint16_t)0x3);
                 }
-                if (!ok) break;
-                tc_commit2_mc(tfull0 + 8 * s0, (uint16_t)0x3);
-                if (two) {
-                    if (pend < w.nkb) {
-                        if (!mbar_wait_bounded(tempty0 + 8 * s1, p1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        for (; pend < w.nkb; ++pend) second(pend);
-                    }
-                    tc_commit2_mc(tfull0 + 8 * s1, (uint16_t)0x3);
-                }
-                use += (uint32_t)w.halves;
+                if (ok) tc_commit2_mc(tfull0 + 8 * b, (uint16_t)0x3);
             }
             if (!ok && issued) {
                 for (int q = 0; q < 100; ++q) __nanosleep(1000);
@@ -357,8 +341,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         // ------------------------------------------------------------ weight: rows past the expert's end
         if constexpr (DIR == kExpWeight) {
             uint32_t it = 0, phase = 0;  // bit s: parity of the next use of tail[s] and peer[s]
-            for (int t = pair; t < total; t += npairs) {
-                const Tile w = tile_of<DIR>(p, tab, mt, nt, t);
+            for (int i = 0;; ++i) {
+                const int t = __shfl_sync(0xffffffffu, lane == 0 ? next_tile(i, kDevTimeoutProducer) : 0, 0);
+                if (t < 0) break;
+                const Tile w = tile_of<DIR>(p, tab, mt, t);
                 it += (uint32_t)w.nkb;
                 if (w.nkb == 0 || (w.last & 15) == 0) continue;
                 const uint32_t s = (it - 1) % S, ph = (phase >> s) & 1;
@@ -368,9 +354,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                 // rows [last, next multiple of 16) of each 64 x 64 block: whole 128-byte lines, so the swizzle
                 // within a line does not matter
                 const int lo = w.last, n = ((lo + 15) & ~15) - lo;
-                const int blocks = 2 + 2 * w.halves;
-                for (int i = lane; i < blocks * n * 8; i += 32) {
-                    const int blk = i / (n * 8), r = i / 8 % n, c = i % 8;
+                for (int j = lane; j < 4 * n * 8; j += 32) {
+                    const int blk = j / (n * 8), r = j / 8 % n, c = j % 8;
                     uint8_t *base = blk < 2 ? sA + s * A_BYTES + blk * 8192 : sB + s * B_BYTES + (blk - 2) * 8192;
                     *reinterpret_cast<uint4 *>(base + (lo + r) * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -381,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                         mbar_arrive_remote(mapa_shared(peer0 + 8 * s, 0));
                     } else {
                         ok = mbar_wait_bounded(peer0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
-                        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                        acquire_cluster();
                         if (ok) mbar_arrive(full0 + 8 * s);
                     }
                 }
@@ -392,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         // ------------------------------------------------------------ epilogue (both CTAs)
         const uint32_t tempty_leader0 = mapa_shared(tempty0, 0);
         const uint32_t lane_base = tmem_base + ((uint32_t)(warp * 32) << 16);
-        uint32_t use = 0;
+        uint32_t use = 0, buf = 0;
         if constexpr (DIR != kExpWeight) {
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
             // rows of no expert: zeros (16-byte stores; the width is a multiple of 8)
@@ -403,110 +388,104 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                 for (int c = threadIdx.x; c < vec; c += 128) row[c] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
-        uint32_t buf = 0;
         bool ok = true;
-        for (int t = pair; t < total; t += npairs) {
-            const Tile w = tile_of<DIR>(p, tab, mt, nt, t);
+        for (int i = 0;; ++i) {
+            int t = __shfl_sync(0xffffffffu, lane == 0 ? next_tile(i, kDevTimeoutEpilogue) : 0, 0);
+            if constexpr (DIR != kExpWeight) {
+                // the four warps meet at barriers below: they go on or stop together
+                volatile int32_t *vote = bars.vote + (i & 1) * 4;
+                if (lane == 0) vote[warp] = t;
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                t = min(min(vote[0], vote[1]), min(vote[2], vote[3]));
+            }
+            if (t < 0) break;
+            const Tile w = tile_of<DIR>(p, tab, mt, t);
             const int m = w.m0 + (int)rank * 128;
+            const uint32_t b = use & 1;
+            if (w.nkb > 0) {
+                // after a wait that ran out the warps go on meeting at their barriers, storing nothing
+                if (ok) ok = mbar_wait_bounded(tfull0 + 8 * b, (use >> 1) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                ++use;
+            }
+            const uint32_t acc = lane_base + b * 256;
             if constexpr (DIR == kExpWeight) {
                 // 32 x 32 fp32 pieces (a warp's rows, 128 bytes each) through swizzled staging and TMA stores,
                 // added in L2 when accumulating: one writer per element, so the order is fixed
-                const int halves = w.halves ? w.halves : (p.accumulate ? 0 : (p.wide > 256 && w.c0 + 256 < p.K) ? 2 : 1);
                 const int mrow = m + warp * 32;
                 uint8_t *slab = stage + warp * 4096;
-                for (int h = 0; h < halves; ++h) {
-                    const uint32_t slot = use & 1;
-                    if (w.halves) {
-                        ok = mbar_wait_bounded(tfull0 + 8 * slot, (use >> 1) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
-                        if (!__all_sync(0xffffffffu, ok)) break;
-                        tc_fence_after();
-                    }
-                    const int c0 = w.c0 + (h ? w.at1 : 0);
 #pragma unroll 1
-                    for (int g = 0; g < 8; ++g) {
-                        uint32_t v[32];
-                        if (w.halves) {
-                            tmem_ld32(lane_base + slot * 256 + g * 32, v);
-                        } else {
+                for (int g = 0; g < WIDE / 32; ++g) {
+                    uint32_t v[32];
+                    if (w.nkb > 0) {
+                        tmem_ld32(acc + g * 32, v);
+                    } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = 0u;
-                        }
-                        if (lane == 0) bulk_wait_read();
-                        __syncwarp();
-                        const uint32_t sb = smem_u32(slab) + (uint32_t)lane * 128u;
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sb + (((uint32_t)q ^ (lane & 7)) << 4)),
-                                         "r"(v[4 * q]), "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
-                                         : "memory");
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0 && mrow < p.N && c0 + g * 32 < p.K) {
-                            const uint64_t map = reinterpret_cast<uint64_t>(&p.o);
-                            if (p.accumulate)
-                                asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-                                             "r"(c0 + g * 32), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
-                                             : "memory");
-                            else
-                                asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-                                             "r"(c0 + g * 32), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
-                                             : "memory");
-                            bulk_commit();
-                        }
+                        for (int q = 0; q < 32; ++q) v[q] = 0u;
                     }
-                    if (w.halves) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8 * slot);
-                        ++use;
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
+                    const uint32_t sb = smem_u32(slab) + (uint32_t)lane * 128u;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sb + (((uint32_t)q ^ (lane & 7)) << 4)),
+                                     "r"(v[4 * q]), "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                                     : "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (ok && lane == 0 && mrow < p.N && w.c0 + g * 32 < p.K) {
+                        const uint64_t map = reinterpret_cast<uint64_t>(&p.o);
+                        if (p.accumulate)
+                            asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+                                         "r"(w.c0 + g * 32), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
+                                         : "memory");
+                        else
+                            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
+                                         "r"(w.c0 + g * 32), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
+                                         : "memory");
+                        bulk_commit();
                     }
                 }
             } else {
                 // columns of the accumulator are rows of the output: 32 of them at a time are turned around in
                 // shared memory ([row][128 of the M dimension], 256 bytes) and leave in 16-byte stores, two
-                // whole row segments to an instruction.  (A bulk copy per row took 95 clocks each: 25 us a tile.)
-                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
+                // whole row segments to an instruction.  (A bulk copy per row took 95 clocks each: 25 us for
+                // 512 rows.)
                 const int col = (lane & 15) * 8;
                 const bool col_ok = m + col < mdim;
-                for (int h = 0; h < w.halves; ++h, ++use) {
-                    const uint32_t slot = use & 1;
-                    // after a wait that ran out the warps go on meeting at their barriers, storing nothing
-                    if (ok) ok = mbar_wait_bounded(tfull0 + 8 * slot, (use >> 1) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
-                    ok = __all_sync(0xffffffffu, ok);
-                    tc_fence_after();
-                    const int at = h ? w.at1 : 0, valid = min(h ? w.n1 : w.n0, w.ntok - at);
-                    __nv_bfloat16 *dst = out + ((int64_t)w.row0 + at) * p.ldo + m + col;
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + (int64_t)w.row0 * p.ldo + m + col;
 #pragma unroll 1
-                    for (int g = 0; g < valid; g += 32, buf ^= 1) {
-                        uint32_t v[32];
-                        tmem_ld32(lane_base + slot * 256 + g, v);
-                        const uint32_t sb = smem_u32(stage) + buf * 8192u;
-                        const uint32_t sw = sb + (uint32_t)(warp * 32 + lane) * 2u;
+                for (int g = 0; g < w.ntok; g += 32, buf ^= 1) {
+                    uint32_t v[32];
+                    tmem_ld32(acc + g, v);
+                    const uint32_t sb = smem_u32(stage) + buf * 8192u;
+                    const uint32_t sw = sb + (uint32_t)(warp * 32 + lane) * 2u;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const __nv_bfloat16 x = __float2bfloat16_rn(__uint_as_float(v[i]));
-                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(sw + (uint32_t)i * 256u), "h"(*reinterpret_cast<const uint16_t *>(&x)) : "memory");
-                        }
-                        // one barrier per group: a buffer is written again after the next group's barrier,
-                        // which every warp reaches after reading it
-                        asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int r = warp * 8 + q * 2 + (lane >> 4);
-                            uint4 x;
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                                         : "r"(sb + (uint32_t)r * 256u + (uint32_t)col * 2u)
-                                         : "memory");
-                            if (ok && col_ok && g + r < valid) *reinterpret_cast<uint4 *>(dst + (int64_t)(g + r) * p.ldo) = x;
-                        }
+                    for (int q = 0; q < 32; ++q) {
+                        const __nv_bfloat16 x = __float2bfloat16_rn(__uint_as_float(v[q]));
+                        asm volatile("st.shared.b16 [%0], %1;" ::"r"(sw + (uint32_t)q * 256u), "h"(*reinterpret_cast<const uint16_t *>(&x)) : "memory");
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8 * slot);
+                    // one barrier per group: a buffer is written again after the next group's barrier, which
+                    // every warp reaches after reading it
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int r = warp * 8 + q * 2 + (lane >> 4);
+                        uint4 x;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                     : "r"(sb + (uint32_t)r * 256u + (uint32_t)col * 2u)
+                                     : "memory");
+                        if (ok && col_ok && g + r < w.ntok) *reinterpret_cast<uint4 *>(dst + (int64_t)(g + r) * p.ldo) = x;
+                    }
                 }
             }
-            if (DIR == kExpWeight && !__all_sync(0xffffffffu, ok)) break;
+            if (w.nkb > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8 * b);
+            }
         }
         if constexpr (DIR == kExpWeight) bulk_wait_all();
     }

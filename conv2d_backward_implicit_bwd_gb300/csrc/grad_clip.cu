@@ -14,6 +14,7 @@
 // number, at fp32 speed (fp64 adds are 1/64 of the rate).
 #include <cuda_bf16.h>
 #include <math.h>
+#include <string.h>
 
 #include "train.h"
 
@@ -176,16 +177,25 @@ __device__ __forceinline__ double block_sum(double v, double *sh) {
     return v;
 }
 
-__global__ void __launch_bounds__(NT) clip_norm_kernel(const __grid_constant__ ClipParams p) {
+// The tensors' addresses travel as kernel parameters: nothing to copy or keep
+// between calls, and a captured launch holds its own.
+template <int N, bool OUT>
+struct Pointers {
+    const void *g[N];
+    void *o[OUT ? N : 1];
+};
+
+template <int N>
+__global__ void __launch_bounds__(NT) clip_norm_kernel(const __grid_constant__ ClipParams p, const __grid_constant__ Pointers<N, false> at) {
     __shared__ double sh[NT / 32];
     __shared__ bool last;
     double sum = 0.0;
     for (int i = blockIdx.x; i < p.num_chunks; i += gridDim.x) {
         const Chunk ch = chunk_of(p, i);
         if (ch.dtype == 1)
-            sum += chunk_squares(static_cast<const __nv_bfloat16 *>(p.g[ch.tensor]) + ch.start, ch.n);
+            sum += chunk_squares(static_cast<const __nv_bfloat16 *>(at.g[ch.tensor]) + ch.start, ch.n);
         else
-            sum += chunk_squares(static_cast<const float *>(p.g[ch.tensor]) + ch.start, ch.n);
+            sum += chunk_squares(static_cast<const float *>(at.g[ch.tensor]) + ch.start, ch.n);
     }
     sum = block_sum(sum, sh);
     if (threadIdx.x == 0) {
@@ -210,29 +220,46 @@ __global__ void __launch_bounds__(NT) clip_norm_kernel(const __grid_constant__ C
     }
 }
 
-__global__ void __launch_bounds__(NT) clip_scale_kernel(const __grid_constant__ ClipParams p) {
+template <int N>
+__global__ void __launch_bounds__(NT) clip_scale_kernel(const __grid_constant__ ClipParams p, const __grid_constant__ Pointers<N, true> at) {
     const float c = *p.coef;
     for (int i = p.num_chunks - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
         const Chunk ch = chunk_of(p, i);
-        if (c == 1.f && p.g[ch.tensor] == p.o[ch.tensor]) continue;  // in place and nothing to clip
+        if (c == 1.f && at.g[ch.tensor] == at.o[ch.tensor]) continue;  // in place and nothing to clip
         if (ch.dtype == 1)
-            chunk_scale(static_cast<const __nv_bfloat16 *>(p.g[ch.tensor]) + ch.start,
-                        static_cast<__nv_bfloat16 *>(p.o[ch.tensor]) + ch.start, ch.n, c);
+            chunk_scale(static_cast<const __nv_bfloat16 *>(at.g[ch.tensor]) + ch.start,
+                        static_cast<__nv_bfloat16 *>(at.o[ch.tensor]) + ch.start, ch.n, c);
         else
-            chunk_scale(static_cast<const float *>(p.g[ch.tensor]) + ch.start,
-                        static_cast<float *>(p.o[ch.tensor]) + ch.start, ch.n, c);
+            chunk_scale(static_cast<const float *>(at.g[ch.tensor]) + ch.start,
+                        static_cast<float *>(at.o[ch.tensor]) + ch.start, ch.n, c);
     }
+}
+
+constexpr int FEW = 64;  // a small table for few tensors: the parameters are copied at every launch
+
+template <int N>
+cudaError_t norm_with(const ClipParams &p, const void *const *g, int tensors, int grid, cudaStream_t s) {
+    Pointers<N, false> at;
+    memcpy(at.g, g, (size_t)tensors * sizeof(void *));
+    clip_norm_kernel<N><<<grid, NT, 0, s>>>(p, at);
+    return cudaGetLastError();
+}
+template <int N>
+cudaError_t scale_with(const ClipParams &p, const void *const *g, void *const *o, int tensors, int grid, cudaStream_t s) {
+    Pointers<N, true> at;
+    memcpy(at.g, g, (size_t)tensors * sizeof(void *));
+    memcpy(at.o, o, (size_t)tensors * sizeof(void *));
+    clip_scale_kernel<N><<<grid, NT, 0, s>>>(p, at);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_clip_norm(const ClipParams &p, int grid, cudaStream_t s) {
-    clip_norm_kernel<<<grid, NT, 0, s>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_clip_norm(const ClipParams &p, const void *const *g, int tensors, int grid, cudaStream_t s) {
+    return tensors <= FEW ? norm_with<FEW>(p, g, tensors, grid, s) : norm_with<kClipPtrs>(p, g, tensors, grid, s);
 }
-cudaError_t launch_clip_scale(const ClipParams &p, int grid, cudaStream_t s) {
-    clip_scale_kernel<<<grid, NT, 0, s>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_clip_scale(const ClipParams &p, const void *const *g, void *const *o, int tensors, int grid, cudaStream_t s) {
+    return tensors <= FEW ? scale_with<FEW>(p, g, o, tensors, grid, s) : scale_with<kClipPtrs>(p, g, o, tensors, grid, s);
 }
 
 }  // namespace cbd

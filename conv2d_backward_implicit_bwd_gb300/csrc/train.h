@@ -35,8 +35,8 @@ struct ExpertPairParams {  // 128-byte aligned through CUtensorMap
     int64_t wait_budget;
     int64_t ldo;
     int32_t experts, rows, K, N;
-    int32_t wide;            // second-operand columns of a tile: 512 or 256
     int32_t accumulate;
+    int32_t *next;           // tile counter and finished pairs, 0 between launches
 };
 cudaError_t launch_experts_pair(const ExpertPairParams &p, int dir, int grid, cudaStream_t s);
 
@@ -59,11 +59,10 @@ struct ClipParams {
     int32_t partial_total;   // partials of all launches (the last launch sums them), 0: not the last
     int32_t want_coef;
     float max_norm;
-    const void *g[kClipPtrs];
-    void *o[kClipPtrs];
 };
-cudaError_t launch_clip_norm(const ClipParams &p, int grid, cudaStream_t s);
-cudaError_t launch_clip_scale(const ClipParams &p, int grid, cudaStream_t s);
+// `g` and `o` (NULL for the norm): the launch's `tensors` pointers, on the host
+cudaError_t launch_clip_norm(const ClipParams &p, const void *const *g, int tensors, int grid, cudaStream_t s);
+cudaError_t launch_clip_scale(const ClipParams &p, const void *const *g, void *const *o, int tensors, int grid, cudaStream_t s);
 
 // Policy loss.
 enum : int { kPolForward = 0, kPolBackward = 1, kPolBoth = 2 };

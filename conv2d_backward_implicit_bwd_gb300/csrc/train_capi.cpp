@@ -168,7 +168,6 @@ struct conv_bwd_clip_plan_s {
     std::vector<Launch> launches;
     int32_t partial_total = 0;
     size_t off_chunks = 0, off_sizes = 0, off_dtypes = 0;
-    std::unique_ptr<ClipParams> params;
     std::mutex mu;
     DevicePart dev;
 };
@@ -229,11 +228,8 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
     if (d.dtype == CONV_BWD_BF16 && d.K % 8 == 0 && d.N % 8 == 0 && lda % 8 == 0 && ldo % 8 == 0 && ldb % 8 == 0 &&
         ((uintptr_t)a | (uintptr_t)b | (uintptr_t)out) % 16 == 0 && rows > 0 && d.K * d.N < (1LL << 37)) {
         const int64_t mt = ((dir == kExpData ? d.K : d.N) + 255) / 256, pairs = std::max(1, p->dev.num_sms / 2);
-        // one half per tile where two would leave pairs without a tile
-        const int64_t est = weight ? d.experts * mt * ((d.K + 511) / 512) : mt * std::max<int64_t>(rows / 512, 1);
         ExpertPairParams pp;
         std::memset(&pp, 0, sizeof(pp));
-        pp.wide = est >= 2 * pairs ? 512 : 256;
         bool ok;
         if (dir == kExpForward)
             ok = map_filters(&pp.a, b, d, false, 64, 128) && map_rows(&pp.b, a, d.K, rows, lda, 64);
@@ -248,7 +244,8 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
         pp.ldo = ldo;
         pp.experts = (int32_t)d.experts; pp.rows = (int32_t)rows; pp.K = (int32_t)d.K; pp.N = (int32_t)d.N;
         pp.accumulate = accumulate ? 1 : 0;
-        const int64_t most = weight ? d.experts * mt * ((d.K + pp.wide - 1) / pp.wide) : mt * (rows / pp.wide + std::min<int64_t>(d.experts, rows));
+        pp.next = reinterpret_cast<int32_t *>(p->dev.ticket());
+        const int64_t most = weight ? d.experts * mt * ((d.K + 255) / 256) : mt * (rows / 256 + std::min<int64_t>(d.experts, rows));
         const int grid = (int)(2 * std::max<int64_t>(1, std::min(pairs, most)));
         return launch_experts_pair(pp, dir, grid, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
     }
@@ -305,7 +302,6 @@ conv_bwd_status conv_bwd_clip_create(int32_t count, const int64_t *sizes, const 
         p.count = count;
         p.sizes.assign(sizes, sizes + count);
         p.dtypes.assign(dtypes, dtypes + count);
-        p.params.reset(new ClipParams());
         int sms = 148, dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
@@ -373,7 +369,8 @@ static conv_bwd_status clip_launch(conv_bwd_clip_plan p, const void *const *grad
     if (!p->dev.has_device) return CONV_BWD_ERR_CUDA;
     std::lock_guard<std::mutex> lock(p->mu);
     char *m = static_cast<char *>(p->dev.mem);
-    ClipParams &cp = *p->params;
+    ClipParams cp;
+    std::memset(&cp, 0, sizeof(cp));
     cp.partials = reinterpret_cast<double *>(p->dev.rest());
     cp.ticket = p->dev.ticket();
     cp.norm = norm;
@@ -390,11 +387,10 @@ static conv_bwd_status clip_launch(conv_bwd_clip_plan p, const void *const *grad
             cp.num_chunks = l.chunks;
             cp.partial_base = l.partial_base;
             cp.partial_total = k + 1 == nl ? p->partial_total : 0;
-            if (l.tensors > 0) std::memcpy(cp.g, grads + l.first, (size_t)l.tensors * sizeof(void *));
-            if (scale && l.tensors > 0) std::memcpy(cp.o, outs + l.first, (size_t)l.tensors * sizeof(void *));
             if (pass && l.chunks == 0) continue;
-            const cudaError_t e = pass ? launch_clip_scale(cp, l.grid, (cudaStream_t)stream)
-                                       : launch_clip_norm(cp, l.grid, (cudaStream_t)stream);
+            const void *const *g = grads + l.first;
+            const cudaError_t e = pass ? launch_clip_scale(cp, g, outs + l.first, l.tensors, l.grid, (cudaStream_t)stream)
+                                       : launch_clip_norm(cp, g, l.tensors, l.grid, (cudaStream_t)stream);
             if (e != cudaSuccess) return CONV_BWD_ERR_CUDA;
         }
     return CONV_BWD_OK;

@@ -83,9 +83,14 @@ def _check(status, what):
         raise ConvBwdError(status, what)
 
 
-def _stream(stream):
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 0.1 us instead of 3 for a Stream object
+
+
+def _stream(stream, device):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is not None:
+            return _raw_stream(device.index)
+        return torch.cuda.current_stream(device).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -105,17 +110,18 @@ def _need(ok, what):
 
 def _rows(t, width, dtype, what):
     """Checks a matrix of rows with unit column stride; returns (rows, row stride)."""
-    if t.dtype != dtype or t.dim() != 2 or t.shape[1] != width or not t.is_cuda:
-        raise ValueError(f"{what}: a CUDA {dtype} matrix with {width} columns wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    rows = t.shape[0]
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != 2 or shape[1] != width or not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA {dtype} matrix with {width} columns wanted, got {t.dtype} {tuple(shape)} on {t.device}")
+    rows = shape[0]
     ld, unit = t.stride()
-    if unit != 1 and width > 1 or (rows > 1 and ld < width):
+    if (unit != 1 and width > 1) or (ld < width and rows > 1):
         raise ValueError(f"{what}: unit column stride and rows that do not overlap wanted, got strides {t.stride()}")
-    return rows, max(ld, width)
+    return rows, ld if ld > width else width
 
 
 def _vector(t, n, dtype, what):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_cuda or (n > 1 and t.stride(0) != 1):
+    if t.dtype != dtype or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous CUDA {dtype} vector of {n} wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -136,6 +142,12 @@ class _Plan:
             pass
 
 
+def _status(call, handle, stream):
+    det = _i32()
+    device = torch.device("cuda", torch.cuda.current_device())
+    return call(handle, _stream(stream, device), ctypes.byref(det)), det.value
+
+
 class Experts(_Plan):
     """Matrix products grouped by expert with ragged sizes.
 
@@ -148,35 +160,35 @@ class Experts(_Plan):
         self.experts, self.k, self.n = int(experts), int(k), int(n)
         self._code = _dtype(dtype)
         self.dtype = _TORCH[self._code]
+        self._shape = (self.experts, self.n, self.k)
         desc, h = ExpertsDesc(self.experts, self.k, self.n, self._code), _vp()
         _check(_lib.conv_bwd_experts_create(ctypes.byref(desc), ctypes.byref(h)), "conv_bwd_experts_create")
         self._h = h.value
 
-    def _w(self, w):
-        if w.dtype != self.dtype or w.shape != (self.experts, self.n, self.k) or not w.is_contiguous() or not w.is_cuda:
-            raise ValueError(f"w: a contiguous CUDA {self.dtype} tensor [{self.experts}, {self.n}, {self.k}] wanted, got {w.dtype} {tuple(w.shape)}")
-        return w.data_ptr()
-
-    def _product(self, call, what, a, wa, w, offsets, out, wo, stream):
+    def _product(self, call, name, what, a, wa, w, offsets, out, wo, stream):
         rows, lda = _rows(a, wa, self.dtype, what)
         off = _vector(offsets, self.experts + 1, torch.int32, "offsets")
-        wp = self._w(w)
+        if w.dtype != self.dtype or w.shape != self._shape or not w.is_contiguous() or not w.is_cuda:
+            raise ValueError(f"w: a contiguous CUDA {self.dtype} tensor {list(self._shape)} wanted, got {w.dtype} {tuple(w.shape)}")
+        device = a.device
         if out is None:
-            out = _empty((rows, wo), self.dtype, a.device, stream)
+            out = _empty((rows, wo), self.dtype, device, stream)
             ldo = wo
         else:
             r, ldo = _rows(out, wo, self.dtype, "out")
             _need(r == rows, f"out: {rows} rows wanted, got {r}")
-        _check(call(self._h, rows, a.data_ptr(), lda, wp, off, out.data_ptr(), ldo, _stream(stream)), call.__name__)
+        st = call(self._h, rows, a.data_ptr(), lda, w.data_ptr(), off, out.data_ptr(), ldo, _stream(stream, device))
+        if st != OK:
+            raise ConvBwdError(st, name)
         return out
 
     def forward(self, x, w, offsets, out=None, stream=None):
         """y[i] = w[e] x[i] for the rows i of every expert e; x [rows, k] -> y [rows, n]."""
-        return self._product(_lib.conv_bwd_experts_forward, "x", x, self.k, w, offsets, out, self.n, stream)
+        return self._product(_lib.conv_bwd_experts_forward, "conv_bwd_experts_forward", "x", x, self.k, w, offsets, out, self.n, stream)
 
     def backward_data(self, dy, w, offsets, out=None, stream=None):
         """dx[i] = w[e]^T dy[i]; dy [rows, n] -> dx [rows, k]."""
-        return self._product(_lib.conv_bwd_experts_data, "dy", dy, self.n, w, offsets, out, self.k, stream)
+        return self._product(_lib.conv_bwd_experts_data, "conv_bwd_experts_data", "dy", dy, self.n, w, offsets, out, self.k, stream)
 
     def backward_weight(self, dy, x, offsets, out=None, accumulate=False, stream=None):
         """dw[e] = sum of dy[i] x[i]^T over the rows of e, in fp32 [experts, n, k]; added to ``out`` with ``accumulate``."""
@@ -186,17 +198,16 @@ class Experts(_Plan):
         off = _vector(offsets, self.experts + 1, torch.int32, "offsets")
         if out is None:
             _need(not accumulate, "accumulate wants the gradients to add to in out")
-            out = _empty((self.experts, self.n, self.k), torch.float32, dy.device, stream)
-        elif out.dtype != torch.float32 or out.shape != (self.experts, self.n, self.k) or not out.is_contiguous() or not out.is_cuda:
-            raise ValueError(f"out: a contiguous CUDA fp32 tensor [{self.experts}, {self.n}, {self.k}] wanted, got {out.dtype} {tuple(out.shape)}")
+            out = _empty(self._shape, torch.float32, dy.device, stream)
+        elif out.dtype != torch.float32 or out.shape != self._shape or not out.is_contiguous() or not out.is_cuda:
+            raise ValueError(f"out: a contiguous CUDA fp32 tensor {list(self._shape)} wanted, got {out.dtype} {tuple(out.shape)}")
         _check(_lib.conv_bwd_experts_weight(self._h, rows, dy.data_ptr(), lddy, x.data_ptr(), ldx, off, out.data_ptr(),
-                                            1 if accumulate else 0, _stream(stream)), "conv_bwd_experts_weight")
+                                            1 if accumulate else 0, _stream(stream, dy.device)), "conv_bwd_experts_weight")
         return out
 
     def status(self, stream=None):
         """(status, detail) of the calls since the last one; synchronises the stream."""
-        det = _i32()
-        return _lib.conv_bwd_experts_get_status(self._h, _stream(stream), ctypes.byref(det)), det.value
+        return _status(_lib.conv_bwd_experts_get_status, self._h, stream)
 
 
 class GradClip(_Plan):
@@ -211,7 +222,7 @@ class GradClip(_Plan):
         sizes = [int(n) for n in sizes]
         codes = [_dtype(d) for d in dtypes]
         _need(len(sizes) == len(codes), f"{len(sizes)} sizes and {len(codes)} dtypes")
-        self._want = list(zip(sizes, (_TORCH[c] for c in codes)))
+        self._want = [(n, _TORCH[c], True, True) for n, c in zip(sizes, codes)]
         self.count = n = len(sizes)
         h = _vp()
         _check(_lib.conv_bwd_clip_create(n, (_i64 * max(n, 1))(*sizes), (_i32 * max(n, 1))(*codes), ctypes.byref(h)), "conv_bwd_clip_create")
@@ -224,21 +235,23 @@ class GradClip(_Plan):
         return cls([t.numel() for t in tensors], [t.dtype for t in tensors])
 
     def _pointers(self, tensors, what):
-        if len(tensors) != self.count:
-            raise ValueError(f"{what}: {self.count} tensors wanted, got {len(tensors)}")
-        for i, (t, (n, d)) in enumerate(zip(tensors, self._want)):
-            if t.numel() != n or t.dtype != d or not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"{what}[{i}]: a contiguous CUDA {d} tensor of {n} elements wanted, got {t.dtype} {tuple(t.shape)}")
+        if [(t.numel(), t.dtype, t.is_cuda, t.is_contiguous()) for t in tensors] != self._want:
+            if len(tensors) != self.count:
+                raise ValueError(f"{what}: {self.count} tensors wanted, got {len(tensors)}")
+            for i, (t, want) in enumerate(zip(tensors, self._want)):
+                if (t.numel(), t.dtype, t.is_cuda, t.is_contiguous()) != want:
+                    raise ValueError(f"{what}[{i}]: a contiguous CUDA {want[1]} tensor of {want[0]} elements wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
         return self._array(*[t.data_ptr() for t in tensors])
 
-    def _scalar(self, device, stream):
-        return _empty((1,), torch.float32, device, stream)
+    def _device(self, grads):
+        return grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
 
     def norm(self, grads, stream=None):
         """The norm as a CUDA fp32 tensor [1]."""
         g = self._pointers(grads, "grads")
-        norm = self._scalar(grads[0].device if grads else "cuda", stream)
-        _check(_lib.conv_bwd_clip_norm(self._h, g, norm.data_ptr(), _stream(stream)), "conv_bwd_clip_norm")
+        device = self._device(grads)
+        norm = _empty((1,), torch.float32, device, stream)
+        _check(_lib.conv_bwd_clip_norm(self._h, g, norm.data_ptr(), _stream(stream, device)), "conv_bwd_clip_norm")
         return norm
 
     def clip(self, grads, max_norm, out=None, stream=None):
@@ -247,10 +260,11 @@ class GradClip(_Plan):
         _need(not math.isnan(max_norm) and max_norm >= 0, f"max_norm {max_norm}: a number >= 0 wanted")
         g = self._pointers(grads, "grads")
         o = g if out is None else self._pointers(out, "out")
-        both = _empty((2,), torch.float32, grads[0].device if grads else "cuda", stream)
+        device = self._device(grads)
+        both = _empty((2, 1), torch.float32, device, stream)
         at = both.data_ptr()
-        _check(_lib.conv_bwd_clip_run(self._h, g, o, max_norm, at, at + 4, _stream(stream)), "conv_bwd_clip_run")
-        return both[:1], both[1:]
+        _check(_lib.conv_bwd_clip_run(self._h, g, o, max_norm, at, at + 4, _stream(stream, device)), "conv_bwd_clip_run")
+        return both.unbind(0)
 
 
 class PolicyLoss(_Plan):
@@ -288,11 +302,12 @@ class PolicyLoss(_Plan):
     def forward(self, logits, actions, advantage, weight, old_logp=None, ref_logp=None, stream=None):
         """(loss [1], logp, lse, coef [tokens]); lse and coef are what ``backward`` needs."""
         t, args = self._inputs(logits, actions, advantage, weight, old_logp, ref_logp)
-        pad = (t + 3) // 4 * 4
-        s = _empty((3 * pad + 1,), torch.float32, logits.device, stream)
-        at = s.data_ptr()
-        _check(_lib.conv_bwd_policy_forward(*args, at + 12 * pad, at, at + 4 * pad, at + 8 * pad, _stream(stream)), "conv_bwd_policy_forward")
-        return s[3 * pad:], s[:t], s[pad:pad + t], s[2 * pad:2 * pad + t]
+        device = logits.device
+        rows = _empty((3, t), torch.float32, device, stream)
+        loss = _empty((1,), torch.float32, device, stream)
+        at = rows.data_ptr()
+        _check(_lib.conv_bwd_policy_forward(*args, loss.data_ptr(), at, at + 4 * t, at + 8 * t, _stream(stream, device)), "conv_bwd_policy_forward")
+        return loss, *rows.unbind(0)
 
     def backward(self, logits, actions, lse, coef, grad=None, out=None, stream=None):
         """dlogits from the forward's lse and coef; ``grad`` [1] is the loss's upstream gradient; ``out`` may be logits."""
@@ -301,19 +316,19 @@ class PolicyLoss(_Plan):
         args = (self._h, t, logits.data_ptr(), ld, _vector(actions, t, torch.int32, "actions"), _vector(lse, t, f, "lse"),
                 _vector(coef, t, f, "coef"), None if grad is None else _vector(grad, 1, f, "grad"))
         out, ldd = self._grad_out(logits, t, out, stream)
-        _check(_lib.conv_bwd_policy_backward(*args, out.data_ptr(), ldd, _stream(stream)), "conv_bwd_policy_backward")
+        _check(_lib.conv_bwd_policy_backward(*args, out.data_ptr(), ldd, _stream(stream, logits.device)), "conv_bwd_policy_backward")
         return out
 
     def forward_backward(self, logits, actions, advantage, weight, old_logp=None, ref_logp=None, out=None, stream=None):
         """(loss [1], logp [tokens], dlogits) in one launch; ``out`` may be logits."""
         t, args = self._inputs(logits, actions, advantage, weight, old_logp, ref_logp)
         out, ldd = self._grad_out(logits, t, out, stream)
-        s = _empty((t + 1,), torch.float32, logits.device, stream)
-        at = s.data_ptr()
-        _check(_lib.conv_bwd_policy_forward_backward(*args, at + 4 * t, at, out.data_ptr(), ldd, _stream(stream)), "conv_bwd_policy_forward_backward")
-        return s[t:], s[:t], out
+        device = logits.device
+        logp = _empty((t,), torch.float32, device, stream)
+        loss = _empty((1,), torch.float32, device, stream)
+        _check(_lib.conv_bwd_policy_forward_backward(*args, loss.data_ptr(), logp.data_ptr(), out.data_ptr(), ldd, _stream(stream, device)), "conv_bwd_policy_forward_backward")
+        return loss, logp, out
 
     def status(self, stream=None):
         """(status, detail) of the calls since the last one; synchronises the stream."""
-        det = _i32()
-        return _lib.conv_bwd_policy_get_status(self._h, _stream(stream), ctypes.byref(det)), det.value
+        return _status(_lib.conv_bwd_policy_get_status, self._h, stream)
