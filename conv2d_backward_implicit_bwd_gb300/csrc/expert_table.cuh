@@ -29,19 +29,24 @@ enum ExpertTiles : int {
     kTilesNonEmpty, // as kTilesByDepth without the experts that have no rows
 };
 
-// Filled by one warp.  Offsets below an earlier one or out of [0, rows] are
+// Step 1, all threads of the block: the offsets as they are.
+__device__ __forceinline__ void load_expert_offsets(ExpertTable &t, const int32_t *offsets, int experts) {
+    for (int e = threadIdx.x; e <= experts; e += blockDim.x) t.off[e] = offsets[e];
+}
+
+// Step 2, one warp, after a block barrier.  Offsets below an earlier one or out of [0, rows] are
 // recorded as a fault and read as the running maximum clamped to that range:
 // the experts' rows stay disjoint and inside the tensors whatever the offsets
 // hold.  Tiles go by falling cost in eight classes, so that the last ones to be
 // handed out are the short ones.
-__device__ __forceinline__ void build_expert_table(ExpertTable &t, const int32_t *offsets, int experts, int rows,
-                                                   int per, int mult, ExpertTiles kind, int32_t *status) {
+__device__ __forceinline__ void build_expert_table(ExpertTable &t, int experts, int rows, int per, int mult,
+                                                   ExpertTiles kind, int32_t *status) {
     constexpr int CLASSES = 8;
     const int lane = threadIdx.x & 31;
     int top = 0, longest = 0;  // largest offset so far
     for (int e0 = 0; e0 <= experts; e0 += 32) {
         const int e = e0 + lane;
-        const int raw = e <= experts ? offsets[e] : 0;
+        const int raw = e <= experts ? t.off[e] : 0;
         int most = max(top, raw);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {

@@ -60,13 +60,23 @@ constexpr int B_BYTES = 128 * 64 * 2;  // one CTA's half of the tile's columns
 constexpr int OUT_BYTES = 16384;       // epilogue staging
 constexpr int THREADS = 10 * 32;
 
+// One tile: decoded once by the schedule, read by every role of the pair.
+struct __align__(16) Tile {
+    int e, m0;       // expert, first index of the M dimension
+    int row0, ntok;  // first row; forward, data: rows of the tile
+    int c0;          // weight: first column
+    int n;           // MMA width; 0: no more tiles
+    int nkb, last;   // k-blocks (0: an expert without rows), valid depth of the last one
+};
+static_assert(sizeof(Tile) == 32, "two 16-byte stores");
+
 struct Bars {
+    Tile ring[RING];
     uint64_t full[S], empty[S];
     uint64_t tail[S], peer[S];  // weight: last blocks landed in this CTA; peer's rows zeroed
     uint64_t tfull[2], tempty[2];
     uint64_t given[RING], taken[RING];  // schedule: entry written; entry read by every role of the pair
     uint64_t want;                      // the next tile may be drawn
-    int32_t ring[RING];
     int32_t vote[8];  // forward, data: what each epilogue warp drew, two tiles in turn
     uint32_t tmem;
     int32_t abort;
@@ -92,20 +102,37 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// what the other CTA wrote before its release-arrive on a barrier of this one
-__device__ __forceinline__ void acquire_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
-    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ void st_cluster(uint32_t addr, int a, int b, int c, int d) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
-
-// One tile: the same for every role.
-struct Tile {
-    int e, m0;       // expert, first index of the M dimension
-    int row0, ntok;  // first row; forward, data: rows of the tile
-    int c0;          // weight: first column
-    int n;           // MMA width
-    int nkb, last;   // k-blocks, valid depth of the last one
-};
+// mbar_wait_bounded that also acquires what the arriving thread of either CTA of the pair wrote before
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, int64_t budget, volatile int32_t *abort,
+                                             int32_t *status, int32_t code) {
+    if (try_wait_cluster(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (try_wait_cluster(bar, parity)) return true;
+        if ((it & 63) == 0) {
+            if (*abort) return false;
+            if (clock64() - t0 > budget) {
+                record_status(status, code);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
+}
 
 template <int DIR>
 __device__ __forceinline__ Tile tile_of(const ExpertPairParams &p, const ExpertTable &tab, int mt, int t) {
@@ -182,8 +209,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
     }
+    load_expert_offsets(tab, p.offsets, p.experts);
+    __syncthreads();
     if (warp == 0)
-        build_expert_table(tab, p.offsets, p.experts, p.rows, WIDE, DIR == kExpWeight ? mt * ((p.K + WIDE - 1) / WIDE) : mt,
+        build_expert_table(tab, p.experts, p.rows, WIDE, DIR == kExpWeight ? mt * ((p.K + WIDE - 1) / WIDE) : mt,
                            DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesByDepth,
                            blockIdx.x == 0 ? p.status : nullptr);
     cluster_sync_all();
@@ -196,15 +225,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
     const int total = tab.tile[p.experts];
 
     // The i-th tile of this pair, for one reader (a thread, or a warp whose
-    // lane 0 does the waiting); -1 after a wait that ran out.
+    // lane 0 reports the reading); n = 0 at the end or after a wait that ran out.
     const uint32_t taken_leader0 = mapa_shared(taken0, 0);
-    auto next_tile = [&](int i, int32_t code) {
+    auto next_tile = [&](int i, int32_t code, bool report) {
         const uint32_t r = (uint32_t)i % RING, ph = ((uint32_t)i / RING) & 1;
-        if (!mbar_wait_bounded(given0 + 8 * r, ph, p.wait_budget, abort_flag, p.status, code)) return -1;
-        acquire_cluster();
-        const int t = *reinterpret_cast<volatile int32_t *>(&bars.ring[r]);
-        mbar_arrive_remote(taken_leader0 + 8 * r);
-        return t < total ? t : -1;
+        Tile w;
+        w.n = 0;
+        if (!wait_cluster(given0 + 8 * r, ph, p.wait_budget, abort_flag, p.status, code)) return w;
+        const int4 *e = reinterpret_cast<const int4 *>(&bars.ring[r]);
+        const int4 x = e[0], y = e[1];
+        w.e = x.x; w.m0 = x.y; w.row0 = x.z; w.ntok = x.w;
+        w.c0 = y.x; w.n = y.y; w.nkb = y.z; w.last = y.w;
+        if (report) mbar_arrive_remote(taken_leader0 + 8 * r);
+        return w;
     };
 
     if (warp == 9) {
@@ -212,11 +245,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         if (leader && lane == 0) {
             const uint32_t ring_peer = mapa_shared(smem_u32(bars.ring), 1), given_peer = mapa_shared(given0, 1);
             int t = pair;
+            Tile w;
             for (int i = 0;; ++i) {
                 const uint32_t r = (uint32_t)i % RING, ph = ((uint32_t)i / RING) & 1;
                 if (!mbar_wait_bounded(taken0 + 8 * r, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) break;
-                *reinterpret_cast<volatile int32_t *>(&bars.ring[r]) = t;
-                st_cluster(ring_peer + 4 * r, t);
+                if (t < total)
+                    w = tile_of<DIR>(p, tab, mt, t);
+                else
+                    w.e = w.m0 = w.row0 = w.ntok = w.c0 = w.n = w.nkb = w.last = 0;
+                bars.ring[r] = w;
+                st_cluster(ring_peer + 32 * r, w.e, w.m0, w.row0, w.ntok);
+                st_cluster(ring_peer + 32 * r + 16, w.c0, w.n, w.nkb, w.last);
                 mbar_arrive(given0 + 8 * r);
                 mbar_arrive_remote(given_peer + 8 * r);
                 if (t >= total) break;
@@ -237,10 +276,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
             uint32_t it = 0;
             bool ok = true, issued = false;
             for (int i = 0; ok; ++i) {
-                const int t = next_tile(i, kDevTimeoutProducer);
-                if (t < 0) break;
+                const Tile w = next_tile(i, kDevTimeoutProducer, true);
+                if (w.n == 0) break;
                 if (warp == 4 && leader) mbar_arrive(want0);
-                const Tile w = tile_of<DIR>(p, tab, mt, t);
                 // B columns of this CTA in boxes of 64, one for each B warp
                 const int half = w.n / 2, boxes = (half + 63) / 64, q = warp - 6;
                 const uint32_t bytes = (uint32_t)A_BYTES + 8192u * (uint32_t)boxes;  // of one CTA
@@ -304,9 +342,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
             uint32_t it = 0, use = 0;  // stages and accumulators used so far
             bool ok = true, issued = false;
             for (int i = 0; ok; ++i) {
-                const int t = next_tile(i, kDevTimeoutMma);
-                if (t < 0) break;
-                const Tile w = tile_of<DIR>(p, tab, mt, t);
+                const Tile w = next_tile(i, kDevTimeoutMma, true);
+                if (w.n == 0) break;
                 if (w.nkb == 0) continue;
                 const uint32_t b = use & 1, bph = (use >> 1) & 1;
                 ++use;
@@ -342,9 +379,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         if constexpr (DIR == kExpWeight) {
             uint32_t it = 0, phase = 0;  // bit s: parity of the next use of tail[s] and peer[s]
             for (int i = 0;; ++i) {
-                const int t = __shfl_sync(0xffffffffu, lane == 0 ? next_tile(i, kDevTimeoutProducer) : 0, 0);
-                if (t < 0) break;
-                const Tile w = tile_of<DIR>(p, tab, mt, t);
+                const Tile w = next_tile(i, kDevTimeoutProducer, false);
+                const bool more = __all_sync(0xffffffffu, w.n != 0);
+                if (lane == 0) mbar_arrive_remote(taken_leader0 + 8 * ((uint32_t)i % RING));
+                if (!more) break;
                 it += (uint32_t)w.nkb;
                 if (w.nkb == 0 || (w.last & 15) == 0) continue;
                 const uint32_t s = (it - 1) % S, ph = (phase >> s) & 1;
@@ -365,8 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                     if (!leader) {
                         mbar_arrive_remote(mapa_shared(peer0 + 8 * s, 0));
                     } else {
-                        ok = mbar_wait_bounded(peer0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
-                        acquire_cluster();
+                        ok = wait_cluster(peer0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
                         if (ok) mbar_arrive(full0 + 8 * s);
                     }
                 }
@@ -390,16 +427,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         }
         bool ok = true;
         for (int i = 0;; ++i) {
-            int t = __shfl_sync(0xffffffffu, lane == 0 ? next_tile(i, kDevTimeoutEpilogue) : 0, 0);
+            const Tile w = next_tile(i, kDevTimeoutEpilogue, false);
+            bool more = __all_sync(0xffffffffu, w.n != 0);
+            if (lane == 0) mbar_arrive_remote(taken_leader0 + 8 * ((uint32_t)i % RING));
             if constexpr (DIR != kExpWeight) {
                 // the four warps meet at barriers below: they go on or stop together
                 volatile int32_t *vote = bars.vote + (i & 1) * 4;
-                if (lane == 0) vote[warp] = t;
+                if (lane == 0) vote[warp] = more;
                 asm volatile("bar.sync 1, 128;" ::: "memory");
-                t = min(min(vote[0], vote[1]), min(vote[2], vote[3]));
+                more = vote[0] & vote[1] & vote[2] & vote[3];
             }
-            if (t < 0) break;
-            const Tile w = tile_of<DIR>(p, tab, mt, t);
+            if (!more) break;
             const int m = w.m0 + (int)rank * 128;
             const uint32_t b = use & 1;
             if (w.nkb > 0) {

@@ -56,7 +56,10 @@ __global__ void __launch_bounds__(NT) experts_simt_kernel(const ExpertSimtParams
     __shared__ __align__(16) float sb[BL][BT + 4];
     const int cols = DIR == kExpForward ? p.N : p.K;
     const int n_tiles = (cols + BT - 1) / BT, m_tiles = (p.N + BT - 1) / BT;  // m_tiles: weight only
-    if (threadIdx.x < 32) build_expert_table(tab, p.offsets, p.experts, p.rows, BT, DIR == kExpWeight ? m_tiles * n_tiles : n_tiles,
+    load_expert_offsets(tab, p.offsets, p.experts);
+    __syncthreads();
+    if (threadIdx.x < 32)
+        build_expert_table(tab, p.experts, p.rows, BT, DIR == kExpWeight ? m_tiles * n_tiles : n_tiles,
                            DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesByDepth,
                            blockIdx.x == 0 ? p.status : nullptr);
     __syncthreads();
