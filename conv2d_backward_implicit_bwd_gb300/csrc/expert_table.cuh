@@ -27,6 +27,7 @@ enum ExpertTiles : int {
     kTilesByRows,   // ceil(rows / per) x mult tiles, dearer ones (more rows each) first
     kTilesByDepth,  // mult tiles each, more rows first
     kTilesNonEmpty, // as kTilesByDepth without the experts that have no rows
+    kTilesInOrder,  // ceil(rows / per) x mult tiles in the order of the experts (`order` is not written)
 };
 
 // Step 1, all threads of the block: the offsets as they are.
@@ -74,7 +75,8 @@ __device__ __forceinline__ void build_expert_table(ExpertTable &t, int experts, 
     int base[CLASSES];
 #pragma unroll
     for (int c = 0; c < CLASSES; ++c) base[c] = 0;
-    for (int e0 = 0; e0 < experts; e0 += 32) {
+    const int sorted = kind == kTilesInOrder ? 0 : experts;
+    for (int e0 = 0; e0 < sorted; e0 += 32) {
         const int mine = e0 + lane < experts ? cls(e0 + lane) : -1;
 #pragma unroll
         for (int c = 0; c < CLASSES; ++c) base[c] += __popc(__ballot_sync(0xffffffffu, mine == c));
@@ -86,7 +88,7 @@ __device__ __forceinline__ void build_expert_table(ExpertTable &t, int experts, 
         base[c] = sum;
         sum += n;
     }
-    for (int e0 = 0; e0 < experts; e0 += 32) {
+    for (int e0 = 0; e0 < sorted; e0 += 32) {
         const int mine = e0 + lane < experts ? cls(e0 + lane) : -1;
 #pragma unroll
         for (int c = 0; c < CLASSES; ++c) {
@@ -101,8 +103,8 @@ __device__ __forceinline__ void build_expert_table(ExpertTable &t, int experts, 
         const int i = i0 + lane;
         int n = 0;
         if (i < experts) {
-            const int len = t.len(t.order[i]);
-            n = kind == kTilesByRows ? (int)(((int64_t)len + per - 1) / per) * mult : kind == kTilesNonEmpty && len == 0 ? 0 : mult;
+            const int len = t.len(kind == kTilesInOrder ? i : t.order[i]);
+            n = kind == kTilesByRows || kind == kTilesInOrder ? (int)(((int64_t)len + per - 1) / per) * mult : kind == kTilesNonEmpty && len == 0 ? 0 : mult;
         }
         int incl = n;
 #pragma unroll

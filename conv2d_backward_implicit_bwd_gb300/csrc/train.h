@@ -40,6 +40,21 @@ struct ExpertPairParams {  // 128-byte aligned through CUtensorMap
 };
 cudaError_t launch_experts_pair(const ExpertPairParams &p, int dir, int grid, cudaStream_t s);
 
+// Expert product for few rows per expert (bf16, forward and data).
+struct ExpertStreamParams {
+    CUtensorMap a;  // w {K, N, experts}
+    CUtensorMap b;  // x {K, rows} or dy {N, rows}
+    void *out;
+    const int32_t *offsets;
+    int32_t *status;
+    float *parts;      // [blocks][2][bt][128] parts of tiles that several blocks share
+    int32_t *arrived;  // [blocks] arrivals of the tile that starts in a block and ends in another, 0 between launches
+    int64_t wait_budget, ldo;
+    int32_t experts, rows, K, N;
+};
+constexpr int kStreamRows = 64;  // most rows of a tile
+cudaError_t launch_experts_stream(const ExpertStreamParams &p, int dir, int bt, int grid, cudaStream_t s);
+
 // Gradient clipping: the tensors are cut into chunks of kClipChunk bytes.
 constexpr int kClipChunk = 32768;
 constexpr int kClipPtrs = 1000;  // tensors per launch (their pointers travel as kernel parameters)

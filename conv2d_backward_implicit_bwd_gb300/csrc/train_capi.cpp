@@ -93,6 +93,7 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
 size_t extent(int64_t rows, int64_t ld, int64_t width, size_t es) {
     return rows > 0 ? ((size_t)(rows - 1) * (size_t)ld + (size_t)width) * es : 0;
 }
+constexpr int64_t kFewRows = 32;  // rows per expert, on average, up to which the filters' bytes are the time
 bool known_dtype(int32_t d) { return d == CONV_BWD_F32 || d == CONV_BWD_BF16; }
 
 template <typename P, typename F>
@@ -155,6 +156,7 @@ bool map_filters(CUtensorMap *m, const void *ptr, const conv_bwd_experts_desc &d
 
 struct conv_bwd_experts_plan_s {
     conv_bwd_experts_desc d;
+    size_t off_parts = 0;
     DevicePart dev;
 };
 struct conv_bwd_clip_plan_s {
@@ -188,7 +190,14 @@ conv_bwd_status conv_bwd_experts_create(const conv_bwd_experts_desc *d, conv_bwd
         return CONV_BWD_ERR_UNSUPPORTED;
     return create_plan(out, [&](conv_bwd_experts_plan_s &p) {
         p.d = *d;
-        return p.dev.init(64);
+        int sms = 0, dev = 0;
+        if (d->dtype == CONV_BWD_BF16 && cudaGetDevice(&dev) == cudaSuccess &&
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            sms = 0;
+        cudaGetLastError();
+        // status and counters, a counter per SM, the parts of tiles that several SMs share (10 MB)
+        p.off_parts = 64 + ((size_t)sms * 4 + 255) / 256 * 256 + 192;
+        return p.dev.init(p.off_parts + (size_t)sms * 2 * kStreamRows * 128 * 4);
     });
 }
 
@@ -227,6 +236,26 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
     // Tensor cores where TMA can load the operands: bf16, widths, strides and addresses on 16 bytes.
     if (d.dtype == CONV_BWD_BF16 && d.K % 8 == 0 && d.N % 8 == 0 && lda % 8 == 0 && ldo % 8 == 0 && ldb % 8 == 0 &&
         ((uintptr_t)a | (uintptr_t)b | (uintptr_t)out) % 16 == 0 && rows > 0 && d.K * d.N < (1LL << 37)) {
+        // Few rows per expert: the time is the filters' bytes, cut evenly over the SMs.  With more the pairs' wide
+        // tiles use an operand for more products.
+        if (!weight && rows <= kFewRows * d.experts) {
+            const int bt = rows <= 8 * d.experts ? 16 : kStreamRows;
+            ExpertStreamParams sp;
+            std::memset(&sp, 0, sizeof(sp));
+            const bool ok = map_filters(&sp.a, b, d, false, 64, dir == kExpForward ? 128 : 64) &&
+                            map_rows(&sp.b, a, dir == kExpForward ? d.K : d.N, rows, lda, (uint32_t)bt);
+            if (!ok) return CONV_BWD_ERR_CUDA;
+            sp.out = out; sp.offsets = offsets; sp.status = p->dev.status();
+            sp.arrived = reinterpret_cast<int32_t *>(p->dev.rest());
+            sp.parts = reinterpret_cast<float *>(static_cast<char *>(p->dev.mem) + p->off_parts);
+            sp.wait_budget = (int64_t)p->dev.clock_khz * 2000;
+            sp.ldo = ldo;
+            sp.experts = (int32_t)d.experts; sp.rows = (int32_t)rows; sp.K = (int32_t)d.K; sp.N = (int32_t)d.N;
+            // at least four blocks of 16 KB for an SM
+            const int64_t blocks = ((rows / bt + std::min<int64_t>(d.experts, rows)) * ((wo + 127) / 128)) * ((wa + 63) / 64);
+            const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(p->dev.num_sms, blocks / 4));
+            return launch_experts_stream(sp, dir, bt, grid, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
+        }
         const int64_t mt = ((dir == kExpData ? d.K : d.N) + 255) / 256, pairs = std::max(1, p->dev.num_sms / 2);
         ExpertPairParams pp;
         std::memset(&pp, 0, sizeof(pp));

@@ -123,7 +123,8 @@ def test_small(T, dtype, way, split, k, n):
 
 @pytest.mark.parametrize("way", WAYS)
 @pytest.mark.parametrize("k,n", [(256, 512), (520, 1000), (1024, 264)])
-@pytest.mark.parametrize("split", [[300, 513, 0, 1024, 77], [40] * 20, [3] * 33, [1100]])
+@pytest.mark.parametrize("split", [[300, 513, 0, 1024, 77], [40] * 20, [3] * 33, [1100], [25] * 16, [1] * 64,
+                                   [0, 0, 150, 0, 0, 0, 0, 0, 3], [0] * 60 + [17, 16, 1, 33], [0] * 1020 + [2, 0, 0, 1]])
 def test_bf16_larger(T, way, k, n, split):
     off = offsets(split)
     run_way(T, T.Experts(len(split), k, n), way, k, n, off, off[-1], "bf16", seed=n)
