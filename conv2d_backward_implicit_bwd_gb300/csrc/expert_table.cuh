@@ -1,6 +1,11 @@
 // expert_table.cuh -- the tile table of a launch grouped by expert, built by
-// each block from the device-side offsets: the host never learns the rows of
-// an expert, so a router's output feeds the products without a copy back.
+// each block from the device-side offsets (the host never learns the rows of an
+// expert, so a router's output feeds the products without a copy back), and the
+// ring through which one warp hands decoded tiles to the others.
+//
+// The start of a launch runs cold: an instruction line costs a fetch from L2, so
+// straight code is slow there (a table that sorted the experts by cost in some
+// 600 instructions took 6.4 us, this one 0.5 us at 64 experts).
 #pragma once
 #include <stdint.h>
 
@@ -12,116 +17,69 @@ namespace cbd {
 
 struct ExpertTable {
     int32_t off[kMaxExperts + 1];   // expert e owns rows [off[e], off[e + 1])
-    int32_t tile[kMaxExperts + 1];  // first tile of the i-th expert in tile order; tile[experts] = all tiles
-    uint16_t order[kMaxExperts];    // experts by falling cost of their tiles
+    int32_t tile[kMaxExperts + 1];  // first tile of expert e; tile[experts] = all tiles
     __device__ __forceinline__ int len(int e) const { return off[e + 1] - off[e]; }
 };
 
-// Rows in equal chunks of at most `per`, rounded up to 32.
-__device__ __forceinline__ int chunk_rows(int len, int per) {
-    const int chunks = (len + per - 1) / per;
-    return ((len + chunks - 1) / chunks + 31) & ~31;
-}
-
 enum ExpertTiles : int {
-    kTilesByRows,   // ceil(rows / per) x mult tiles, dearer ones (more rows each) first
-    kTilesByDepth,  // mult tiles each, more rows first
-    kTilesNonEmpty, // as kTilesByDepth without the experts that have no rows
-    kTilesInOrder,  // ceil(rows / per) x mult tiles in the order of the experts (`order` is not written)
+    kTilesByRows,    // ceil(rows / per) x mult tiles
+    kTilesEach,      // mult tiles
+    kTilesNonEmpty,  // mult tiles, none for an expert without rows
 };
 
-// Step 1, all threads of the block: the offsets as they are.
-__device__ __forceinline__ void load_expert_offsets(ExpertTable &t, const int32_t *offsets, int experts) {
-    for (int e = threadIdx.x; e <= experts; e += blockDim.x) t.off[e] = offsets[e];
-}
-
-// Step 2, one warp, after a block barrier.  Offsets below an earlier one or out of [0, rows] are
-// recorded as a fault and read as the running maximum clamped to that range:
-// the experts' rows stay disjoint and inside the tensors whatever the offsets
-// hold.  Tiles go by falling cost in eight classes, so that the last ones to be
-// handed out are the short ones.
-__device__ __forceinline__ void build_expert_table(ExpertTable &t, int experts, int rows, int per, int mult,
-                                                   ExpertTiles kind, int32_t *status) {
-    constexpr int CLASSES = 8;
+// By one warp.  Offsets below an earlier one or out of [0, rows] are recorded as
+// a fault and read as the running maximum clamped to that range: the experts'
+// rows stay disjoint and inside the tensors whatever the offsets hold.
+template <int PER>
+__device__ __forceinline__ void build_expert_table(ExpertTable &t, const int32_t *offsets, int experts, int rows,
+                                                   int mult, ExpertTiles kind, int32_t *status) {
     const int lane = threadIdx.x & 31;
-    int top = 0, longest = 0;  // largest offset so far
+#pragma unroll 4
+    for (int e = lane; e <= experts; e += 32) t.off[e] = offsets[e];
+    __syncwarp();
+    int top = 0, tiles = 0;  // last offset, tiles so far
+#pragma unroll 1
     for (int e0 = 0; e0 <= experts; e0 += 32) {
         const int e = e0 + lane;
-        const int raw = e <= experts ? t.off[e] : 0;
-        int most = max(top, raw);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, most, d);
-            if (lane >= d) most = max(most, v);
-        }
-        const int o = min(most, rows);
+        int o = e <= experts ? t.off[e] : rows;
         int before = __shfl_up_sync(0xffffffffu, o, 1);
-        if (lane == 0) before = min(top, rows);
-        if (e > 0 && e <= experts) longest = max(longest, o - before);
-        top = __shfl_sync(0xffffffffu, most, 31);
-        if (e <= experts) {
-            if (o != raw) record_status(status, kDevFaultIndex);
-            t.off[e] = o;
+        if (lane == 0) before = top;
+        if (__any_sync(0xffffffffu, o < before || o > rows)) {
+            const int raw = o;
+            o = max(o, top);
+#pragma unroll 1
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, o, d);
+                if (lane >= d) o = max(o, v);
+            }
+            o = min(o, rows);
+            if (e <= experts && o != raw) record_status(status, kDevFaultIndex);
+            before = __shfl_up_sync(0xffffffffu, o, 1);
+            if (lane == 0) before = top;
         }
-    }
-    longest = __reduce_max_sync(0xffffffffu, longest);
-    __syncwarp();
-    auto cls = [&](int e) {
-        const int len = t.len(e);
-        const int cost = kind == kTilesByRows ? (len ? chunk_rows(len, per) : 0) : len;
-        const int most = kind == kTilesByRows ? per : longest;
-        return CLASSES - 1 - min(CLASSES - 1, (int)(((int64_t)max(cost - 1, 0) * CLASSES) / max(most, 1)));
-    };
-    int base[CLASSES];
-#pragma unroll
-    for (int c = 0; c < CLASSES; ++c) base[c] = 0;
-    const int sorted = kind == kTilesInOrder ? 0 : experts;
-    for (int e0 = 0; e0 < sorted; e0 += 32) {
-        const int mine = e0 + lane < experts ? cls(e0 + lane) : -1;
-#pragma unroll
-        for (int c = 0; c < CLASSES; ++c) base[c] += __popc(__ballot_sync(0xffffffffu, mine == c));
-    }
-    int sum = 0;
-#pragma unroll
-    for (int c = 0; c < CLASSES; ++c) {
-        const int n = base[c];
-        base[c] = sum;
-        sum += n;
-    }
-    for (int e0 = 0; e0 < sorted; e0 += 32) {
-        const int mine = e0 + lane < experts ? cls(e0 + lane) : -1;
-#pragma unroll
-        for (int c = 0; c < CLASSES; ++c) {
-            const uint32_t m = __ballot_sync(0xffffffffu, mine == c);
-            if (mine == c) t.order[base[c] + __popc(m & ((1u << lane) - 1))] = (uint16_t)(e0 + lane);
-            base[c] += __popc(m);
-        }
-    }
-    __syncwarp();
-    int tiles = 0;
-    for (int i0 = 0; i0 < experts; i0 += 32) {
-        const int i = i0 + lane;
-        int n = 0;
-        if (i < experts) {
-            const int len = t.len(kind == kTilesInOrder ? i : t.order[i]);
-            n = kind == kTilesByRows || kind == kTilesInOrder ? (int)(((int64_t)len + per - 1) / per) * mult : kind == kTilesNonEmpty && len == 0 ? 0 : mult;
-        }
-        int incl = n;
-#pragma unroll
+        top = __shfl_sync(0xffffffffu, o, 31);
+        // tiles of expert e - 1
+        const uint32_t len = e > 0 && e <= experts ? (uint32_t)(o - before) : 0u;
+        int n = kind == kTilesByRows ? (int)((len + PER - 1) / PER) * mult : e > 0 && e <= experts && (kind == kTilesEach || len) ? mult : 0;
+#pragma unroll 1
         for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += v;
+            const int v = __shfl_up_sync(0xffffffffu, n, d);
+            if (lane >= d) n += v;
         }
-        if (i < experts) t.tile[i] = tiles + incl - n;
-        tiles += __shfl_sync(0xffffffffu, incl, 31);
+        if (e <= experts) {
+            t.off[e] = o;
+            t.tile[e] = tiles + n;
+        }
+        tiles += __shfl_sync(0xffffffffu, n, 31);
     }
-    if (lane == 0) t.tile[experts] = tiles;
+    __syncwarp();
 }
 
-// Position in tile order of the expert that tile t belongs to: the last i with
-// tile[i] <= t (experts without tiles share a bound with the next one).
-__device__ __forceinline__ int position_of_tile(const ExpertTable &tab, int experts, int t) {
+// Expert of tile t: the last e with tile[e] <= t (experts without tiles share a
+// bound with the next one).
+__device__ __forceinline__ int expert_of_tile(const ExpertTable &tab, int experts, int t) {
     int lo = 0, hi = experts - 1;
+#pragma unroll 1
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (tab.tile[mid] <= t)
@@ -131,5 +89,61 @@ __device__ __forceinline__ int position_of_tile(const ExpertTable &tab, int expe
     }
     return lo;
 }
+
+// An expert's rows in equal chunks of at most 256, in units of 32: chunks =
+// ceil(units / 8), and the smallest size s <= 8 units with s chunks >= units
+// (counted instead of divided).  (chunks - 1) s < units, so no chunk is empty.
+__device__ __forceinline__ int chunk_rows(int len) {
+    const uint32_t units = ((uint32_t)len + 31) / 32, chunks = (units + 7) / 8;
+    uint32_t s = 1;
+#pragma unroll
+    for (uint32_t k = 1; k < 8; ++k) s += k * chunks < units;
+    return (int)(s * 32);
+}
+
+// A piece of work as the schedule hands it out.
+struct __align__(16) ExpertWork {
+    int e, m0;       // expert, first index of the M dimension
+    int row0, ntok;  // first row; rows of the piece (weight: first column)
+    int n;           // MMA width; 0: no more work
+    int kb0, kb1;    // k-blocks
+    int last;        // weight: valid depth of the last k-block; few-rows kernel: tile number
+};
+static_assert(sizeof(ExpertWork) == 32, "two 16-byte accesses");
+
+template <int N>
+struct ExpertRing {
+    ExpertWork work[N];
+    uint64_t given[N], taken[N];
+    // one thread, before the block's barrier; `readers`: arrivals that free an entry
+    __device__ __forceinline__ void init(uint32_t readers) {
+        for (int i = 0; i < N; ++i) {
+            mbar_init(smem_u32(&given[i]), 1);
+            mbar_init(smem_u32(&taken[i]), readers);
+        }
+    }
+    // the schedule's side: waits for entry i to be free, fills it
+    __device__ __forceinline__ bool give(uint32_t i, const ExpertWork &w, int64_t budget, volatile int32_t *abort, int32_t *status) {
+        const uint32_t r = i % N, ph = (i / N) & 1;
+        if (!mbar_wait_bounded(smem_u32(&taken[r]), ph ^ 1, budget, abort, status, kDevTimeoutProducer)) return false;
+        work[r] = w;
+        mbar_arrive(smem_u32(&given[r]));
+        return true;
+    }
+    // a reader's side; n = 0 at the end or after a wait that ran out
+    __device__ __forceinline__ ExpertWork take(uint32_t i, int64_t budget, volatile int32_t *abort, int32_t *status, int32_t code) {
+        const uint32_t r = i % N, ph = (i / N) & 1;
+        ExpertWork w;
+        w.n = 0;
+        if (!mbar_wait_bounded(smem_u32(&given[r]), ph, budget, abort, status, code)) return w;
+        const int4 *p = reinterpret_cast<const int4 *>(&work[r]);
+        const int4 x = p[0], y = p[1];
+        w.e = x.x; w.m0 = x.y; w.row0 = x.z; w.ntok = x.w;
+        w.n = y.x; w.kb0 = y.y; w.kb1 = y.z; w.last = y.w;
+        return w;
+    }
+    // ... and afterwards, by one thread of each reader
+    __device__ __forceinline__ void done(uint32_t i) { mbar_arrive(smem_u32(&taken[i % N])); }
+};
 
 }  // namespace cbd

@@ -30,14 +30,15 @@
 // memory after they have landed (both operands: 0 x NaN is NaN) before the MMA
 // may read them.
 //
-// Schedule.  The tiles of all experts in falling cost order; a pair starts on
-// the tile of its own number and then draws the next one from a counter when it
-// begins loading the current one.  Which pair computes a tile does not change
-// the tile's bits.
+// Schedule.  Pair b of P takes tiles b, 2P - 1 - b, 2P + b, ... (back and forth,
+// so that a fall or rise of the tiles' cost along the experts evens out).  One
+// warp of each CTA builds the table and decodes the tiles ahead of the others.
+// (Drawing tiles from a counter in falling cost order was no faster: the
+// hand-over between the two CTAs took 0.65 us of every role's time per tile.)
 //
 // Roles per CTA: warps 0-3 epilogue, 4 A loads, 5 MMA (leader CTA) and TMEM,
-// 6-7 B loads, 8 helper of weight's last blocks, 9 schedule (leader CTA).
-// Every wait is bounded.
+// 6-7 B loads, 8 helper of weight's last blocks, 9 schedule.  Every wait is
+// bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -60,23 +61,11 @@ constexpr int B_BYTES = 128 * 64 * 2;  // one CTA's half of the tile's columns
 constexpr int OUT_BYTES = 16384;       // epilogue staging
 constexpr int THREADS = 10 * 32;
 
-// One tile: decoded once by the schedule, read by every role of the pair.
-struct __align__(16) Tile {
-    int e, m0;       // expert, first index of the M dimension
-    int row0, ntok;  // first row; forward, data: rows of the tile
-    int c0;          // weight: first column
-    int n;           // MMA width; 0: no more tiles
-    int nkb, last;   // k-blocks (0: an expert without rows), valid depth of the last one
-};
-static_assert(sizeof(Tile) == 32, "two 16-byte stores");
-
 struct Bars {
-    Tile ring[RING];
+    ExpertRing<RING> ring;
     uint64_t full[S], empty[S];
     uint64_t tail[S], peer[S];  // weight: last blocks landed in this CTA; peer's rows zeroed
     uint64_t tfull[2], tempty[2];
-    uint64_t given[RING], taken[RING];  // schedule: entry written; entry read by every role of the pair
-    uint64_t want;                      // the next tile may be drawn
     int32_t vote[8];  // forward, data: what each epilogue warp drew, two tiles in turn
     uint32_t tmem;
     int32_t abort;
@@ -102,9 +91,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void st_cluster(uint32_t addr, int a, int b, int c, int d) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 // mbar_wait_bounded that also acquires what the arriving thread of either CTA of the pair wrote before
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -135,29 +121,27 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, int6
 }
 
 template <int DIR>
-__device__ __forceinline__ Tile tile_of(const ExpertPairParams &p, const ExpertTable &tab, int mt, int t) {
-    Tile r;
-    const int i = position_of_tile(tab, p.experts, t);
-    r.e = tab.order[i];
-    const int l = t - tab.tile[i], len = tab.len(r.e);
-    r.m0 = (l % mt) * 256;
+__device__ __forceinline__ ExpertWork decode(const ExpertPairParams &p, const ExpertTable &tab, int mt, int t) {
+    ExpertWork w;
+    w.e = expert_of_tile(tab, p.experts, t);
+    const int l = t - tab.tile[w.e], len = tab.len(w.e), q = l / mt;
+    w.m0 = (l - q * mt) * 256;
+    w.kb0 = 0;
     if constexpr (DIR == kExpWeight) {
-        r.c0 = (l / mt) * WIDE;
-        r.row0 = tab.off[r.e];
-        r.nkb = (len + 63) / 64;  // 0: an expert without rows
-        r.last = len - (r.nkb - 1) * 64;
-        r.n = WIDE;
-        r.ntok = 0;
+        w.row0 = tab.off[w.e];
+        w.ntok = q * WIDE;  // first column
+        w.kb1 = (len + 63) / 64;  // 0: an expert without rows
+        w.last = len - (w.kb1 - 1) * 64;
+        w.n = WIDE;
     } else {
-        const int size = chunk_rows(len, WIDE), first = (l / mt) * size;
-        r.row0 = tab.off[r.e] + first;
-        r.ntok = min(size, len - first);
-        r.n = (r.ntok + 31) & ~31;
-        r.nkb = ((DIR == kExpForward ? p.K : p.N) + 63) / 64;
-        r.last = 64;  // past the depth both operands read as zero
-        r.c0 = 0;
+        const int size = chunk_rows(len), first = q * size;
+        w.row0 = tab.off[w.e] + first;
+        w.ntok = min(size, len - first);
+        w.n = (w.ntok + 31) & ~31;
+        w.kb1 = ((DIR == kExpForward ? p.K : p.N) + 63) / 64;
+        w.last = 64;  // past the depth both operands read as zero
     }
-    return r;
+    return w;
 }
 
 template <int DIR>
@@ -173,8 +157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const uint32_t full0 = smem_u32(bars.full), empty0 = smem_u32(bars.empty), tail0 = smem_u32(bars.tail),
-                   peer0 = smem_u32(bars.peer), tfull0 = smem_u32(bars.tfull), tempty0 = smem_u32(bars.tempty),
-                   given0 = smem_u32(bars.given), taken0 = smem_u32(bars.taken), want0 = smem_u32(&bars.want);
+                   peer0 = smem_u32(bars.peer), tfull0 = smem_u32(bars.tfull), tempty0 = smem_u32(bars.tempty);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
     const int mdim = DIR == kExpData ? p.K : p.N;
@@ -191,12 +174,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
             mbar_init(tfull0 + 8 * b, 1);
             mbar_init(tempty0 + 8 * b, 8);  // 4 epilogue warps of each CTA
         }
-        for (int r = 0; r < RING; ++r) {
-            mbar_init(given0 + 8 * r, 1);
-            // loads (3) and epilogue (4) of both CTAs, the MMA, weight's helpers
-            mbar_init(taken0 + 8 * r, DIR == kExpWeight ? 17 : 15);
-        }
-        mbar_init(want0, 1);
+        // loads (3), epilogue (4), the leader's MMA, weight's helper
+        bars.ring.init(7 + (leader ? 1 : 0) + (DIR == kExpWeight ? 1 : 0));
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -209,12 +188,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
     }
-    load_expert_offsets(tab, p.offsets, p.experts);
-    __syncthreads();
-    if (warp == 0)
-        build_expert_table(tab, p.experts, p.rows, WIDE, DIR == kExpWeight ? mt * ((p.K + WIDE - 1) / WIDE) : mt,
-                           DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesByDepth,
-                           blockIdx.x == 0 ? p.status : nullptr);
+    if (warp == 9)
+        build_expert_table<WIDE>(tab, p.offsets, p.experts, p.rows, DIR == kExpWeight ? mt * ((p.K + WIDE - 1) / WIDE) : mt,
+                                 DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesEach,
+                                 blockIdx.x == 0 ? p.status : nullptr);
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = bars.tmem;
@@ -222,50 +199,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         // the pair's MMAs write this CTA's rows at the leader's TMEM address
         if (ld_shared_cluster_u32(mapa_shared(smem_u32(&bars.tmem), 0)) != tmem_base) record_status(p.status, kDevFaultIndex);
     }
-    const int total = tab.tile[p.experts];
-
-    // The i-th tile of this pair, for one reader (a thread, or a warp whose
-    // lane 0 reports the reading); n = 0 at the end or after a wait that ran out.
-    const uint32_t taken_leader0 = mapa_shared(taken0, 0);
-    auto next_tile = [&](int i, int32_t code, bool report) {
-        const uint32_t r = (uint32_t)i % RING, ph = ((uint32_t)i / RING) & 1;
-        Tile w;
-        w.n = 0;
-        if (!wait_cluster(given0 + 8 * r, ph, p.wait_budget, abort_flag, p.status, code)) return w;
-        const int4 *e = reinterpret_cast<const int4 *>(&bars.ring[r]);
-        const int4 x = e[0], y = e[1];
-        w.e = x.x; w.m0 = x.y; w.row0 = x.z; w.ntok = x.w;
-        w.c0 = y.x; w.n = y.y; w.nkb = y.z; w.last = y.w;
-        if (report) mbar_arrive_remote(taken_leader0 + 8 * r);
-        return w;
-    };
 
     if (warp == 9) {
-        // ------------------------------------------------------------ schedule (leader)
-        if (leader && lane == 0) {
-            const uint32_t ring_peer = mapa_shared(smem_u32(bars.ring), 1), given_peer = mapa_shared(given0, 1);
-            int t = pair;
-            Tile w;
-            for (int i = 0;; ++i) {
-                const uint32_t r = (uint32_t)i % RING, ph = ((uint32_t)i / RING) & 1;
-                if (!mbar_wait_bounded(taken0 + 8 * r, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) break;
-                if (t < total)
-                    w = tile_of<DIR>(p, tab, mt, t);
-                else
-                    w.e = w.m0 = w.row0 = w.ntok = w.c0 = w.n = w.nkb = w.last = 0;
-                bars.ring[r] = w;
-                st_cluster(ring_peer + 32 * r, w.e, w.m0, w.row0, w.ntok);
-                st_cluster(ring_peer + 32 * r + 16, w.c0, w.n, w.nkb, w.last);
-                mbar_arrive(given0 + 8 * r);
-                mbar_arrive_remote(given_peer + 8 * r);
-                if (t >= total) break;
-                if (!mbar_wait_bounded(want0, (uint32_t)i & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) break;
-                t = npairs + atomicAdd(p.next, 1);
-            }
-            // the last pair to finish its schedule leaves the counters as it found them
-            if (atomicAdd(p.next + 1, 1) == npairs - 1) {
-                p.next[0] = 0;
-                p.next[1] = 0;
+        // ------------------------------------------------------------ schedule
+        if (lane == 0) {
+            const int total = tab.tile[p.experts];
+            for (uint32_t i = 0;; ++i) {
+                const int t = (int)i * npairs + ((i & 1) ? npairs - 1 - pair : pair);
+                ExpertWork w;
+                w.n = 0;
+                // (the last round may be short: a pair beyond it has nothing there and nothing after)
+                if (t < total) w = decode<DIR>(p, tab, mt, t);
+                if (!bars.ring.give(i, w, p.wait_budget, abort_flag, p.status) || w.n == 0) break;
             }
         }
         __syncwarp();
@@ -275,22 +220,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
             const uint32_t full_leader0 = mapa_shared(full0, 0);
             uint32_t it = 0;
             bool ok = true, issued = false;
-            for (int i = 0; ok; ++i) {
-                const Tile w = next_tile(i, kDevTimeoutProducer, true);
+            for (uint32_t i = 0; ok; ++i) {
+                const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
                 if (w.n == 0) break;
-                if (warp == 4 && leader) mbar_arrive(want0);
+                bars.ring.done(i);
                 // B columns of this CTA in boxes of 64, one for each B warp
                 const int half = w.n / 2, boxes = (half + 63) / 64, q = warp - 6;
                 const uint32_t bytes = (uint32_t)A_BYTES + 8192u * (uint32_t)boxes;  // of one CTA
                 const int at = (int)rank * half + 64 * q;
-                for (int kb = 0; kb < w.nkb; ++kb, ++it) {
+                for (int kb = 0; kb < w.kb1; ++kb, ++it) {
                     const uint32_t s = it % S, ph = (it / S) & 1;
                     if (!mbar_wait_bounded(empty0 + 8 * s, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) {
                         ok = false;
                         break;
                     }
                     // weight: a partial last step goes through the helper warp, on this CTA's own barrier
-                    const bool fix = DIR == kExpWeight && kb == w.nkb - 1 && (w.last & 15) != 0;
+                    const bool fix = DIR == kExpWeight && kb == w.kb1 - 1 && (w.last & 15) != 0;
                     const uint32_t bar = fix ? tail0 + 8 * s : full_leader0 + 8 * s;
                     if (warp == 4) {
                         if (fix)
@@ -316,9 +261,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                         const uint32_t dst = smem_u32(sB + s * B_BYTES + 8192 * q);
                         if constexpr (DIR == kExpWeight) {
                             if (fix)
-                                tma_load_2d(dst, &p.b, bar, w.c0 + at, w.row0 + kb * 64);
+                                tma_load_2d(dst, &p.b, bar, w.ntok + at, w.row0 + kb * 64);
                             else
-                                tma_load_2d_pair(dst, &p.b, bar, w.c0 + at, w.row0 + kb * 64);
+                                tma_load_2d_pair(dst, &p.b, bar, w.ntok + at, w.row0 + kb * 64);
                         } else {
                             tma_load_2d_pair(dst, &p.b, bar, kb * 64, w.row0 + at);
                         }
@@ -341,10 +286,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
             const uint64_t b_desc0 = smem_desc_sw128(smem_u32(sB), B_K ? 16 : 8192, 1024);
             uint32_t it = 0, use = 0;  // stages and accumulators used so far
             bool ok = true, issued = false;
-            for (int i = 0; ok; ++i) {
-                const Tile w = next_tile(i, kDevTimeoutMma, true);
+            for (uint32_t i = 0; ok; ++i) {
+                const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutMma);
                 if (w.n == 0) break;
-                if (w.nkb == 0) continue;
+                bars.ring.done(i);
+                if (w.kb1 == 0) continue;
                 const uint32_t b = use & 1, bph = (use >> 1) & 1;
                 ++use;
                 if (!mbar_wait_bounded(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
@@ -353,14 +299,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                 }
                 tc_fence_after();
                 const uint32_t id = idesc0 | ((uint32_t)(w.n >> 3) << 17), d = tmem_base + b * 256;
-                for (int kb = 0; kb < w.nkb; ++kb, ++it) {
+                for (int kb = 0; kb < w.kb1; ++kb, ++it) {
                     const uint32_t s = it % S, ph = (it / S) & 1;
                     if (!mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
                         ok = false;
                         break;
                     }
                     const uint64_t ad = a_desc0 + (uint64_t)((s * A_BYTES) >> 4), bd = b_desc0 + (uint64_t)((s * B_BYTES) >> 4);
-                    const int n = DIR == kExpWeight && kb == w.nkb - 1 ? (w.last + 15) / 16 : 4;
+                    const int n = DIR == kExpWeight && kb == w.kb1 - 1 ? (w.last + 15) / 16 : 4;
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         if (kk < n) tc_mma2(d, ad + A_STEP * kk, bd + B_STEP * kk, id, (kb | kk) != 0 ? 1u : 0u);
@@ -378,13 +324,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         // ------------------------------------------------------------ weight: rows past the expert's end
         if constexpr (DIR == kExpWeight) {
             uint32_t it = 0, phase = 0;  // bit s: parity of the next use of tail[s] and peer[s]
-            for (int i = 0;; ++i) {
-                const Tile w = next_tile(i, kDevTimeoutProducer, false);
-                const bool more = __all_sync(0xffffffffu, w.n != 0);
-                if (lane == 0) mbar_arrive_remote(taken_leader0 + 8 * ((uint32_t)i % RING));
-                if (!more) break;
-                it += (uint32_t)w.nkb;
-                if (w.nkb == 0 || (w.last & 15) == 0) continue;
+            for (uint32_t i = 0;; ++i) {
+                const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
+                if (!__all_sync(0xffffffffu, w.n != 0)) break;
+                if (lane == 0) bars.ring.done(i);
+                it += (uint32_t)w.kb1;
+                if (w.kb1 == 0 || (w.last & 15) == 0) continue;
                 const uint32_t s = (it - 1) % S, ph = (phase >> s) & 1;
                 phase ^= 1u << s;
                 bool ok = mbar_wait_bounded(tail0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
@@ -415,21 +360,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         const uint32_t tempty_leader0 = mapa_shared(tempty0, 0);
         const uint32_t lane_base = tmem_base + ((uint32_t)(warp * 32) << 16);
         uint32_t use = 0, buf = 0;
-        if constexpr (DIR != kExpWeight) {
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
-            // rows of no expert: zeros (16-byte stores; the width is a multiple of 8)
-            const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
-            const int64_t nfill = (int64_t)lo + (p.rows - hi);
-            for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
-                uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
-                for (int c = threadIdx.x; c < vec; c += 128) row[c] = make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
         bool ok = true;
-        for (int i = 0;; ++i) {
-            const Tile w = next_tile(i, kDevTimeoutEpilogue, false);
+        for (uint32_t i = 0;; ++i) {
+            const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
             bool more = __all_sync(0xffffffffu, w.n != 0);
-            if (lane == 0) mbar_arrive_remote(taken_leader0 + 8 * ((uint32_t)i % RING));
+            if (more && lane == 0) bars.ring.done(i);
             if constexpr (DIR != kExpWeight) {
                 // the four warps meet at barriers below: they go on or stop together
                 volatile int32_t *vote = bars.vote + (i & 1) * 4;
@@ -440,7 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
             if (!more) break;
             const int m = w.m0 + (int)rank * 128;
             const uint32_t b = use & 1;
-            if (w.nkb > 0) {
+            if (w.kb1 > 0) {
                 // after a wait that ran out the warps go on meeting at their barriers, storing nothing
                 if (ok) ok = mbar_wait_bounded(tfull0 + 8 * b, (use >> 1) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
                 ok = __all_sync(0xffffffffu, ok);
@@ -456,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
 #pragma unroll 1
                 for (int g = 0; g < WIDE / 32; ++g) {
                     uint32_t v[32];
-                    if (w.nkb > 0) {
+                    if (w.kb1 > 0) {
                         tmem_ld32(acc + g * 32, v);
                     } else {
 #pragma unroll
@@ -472,15 +407,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                                      : "memory");
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (ok && lane == 0 && mrow < p.N && w.c0 + g * 32 < p.K) {
+                    if (ok && lane == 0 && mrow < p.N && w.ntok + g * 32 < p.K) {
                         const uint64_t map = reinterpret_cast<uint64_t>(&p.o);
                         if (p.accumulate)
                             asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-                                         "r"(w.c0 + g * 32), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
+                                         "r"(w.ntok + g * 32), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
                                          : "memory");
                         else
                             asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-                                         "r"(w.c0 + g * 32), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
+                                         "r"(w.ntok + g * 32), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
                                          : "memory");
                         bulk_commit();
                     }
@@ -519,10 +454,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                     }
                 }
             }
-            if (w.nkb > 0) {
+            if (w.kb1 > 0) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8 * b);
+            }
+        }
+        if constexpr (DIR != kExpWeight) {
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
+            // rows of no expert: zeros (16-byte stores; the width is a multiple of 8)
+            const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
+            const int64_t nfill = (int64_t)lo + (p.rows - hi);
+            for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
+                uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
+                for (int c = threadIdx.x; c < vec; c += 128) row[c] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
         if constexpr (DIR == kExpWeight) bulk_wait_all();

@@ -56,12 +56,10 @@ __global__ void __launch_bounds__(NT) experts_simt_kernel(const ExpertSimtParams
     __shared__ __align__(16) float sb[BL][BT + 4];
     const int cols = DIR == kExpForward ? p.N : p.K;
     const int n_tiles = (cols + BT - 1) / BT, m_tiles = (p.N + BT - 1) / BT;  // m_tiles: weight only
-    load_expert_offsets(tab, p.offsets, p.experts);
-    __syncthreads();
     if (threadIdx.x < 32)
-        build_expert_table(tab, p.experts, p.rows, BT, DIR == kExpWeight ? m_tiles * n_tiles : n_tiles,
-                           DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesByDepth,
-                           blockIdx.x == 0 ? p.status : nullptr);
+        build_expert_table<BT>(tab, p.offsets, p.experts, p.rows, DIR == kExpWeight ? m_tiles * n_tiles : n_tiles,
+                               DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesEach,
+                               blockIdx.x == 0 ? p.status : nullptr);
     __syncthreads();
     const int total = tab.tile[p.experts];
     const T *A = static_cast<const T *>(p.a), *B = static_cast<const T *>(p.b);
@@ -69,8 +67,7 @@ __global__ void __launch_bounds__(NT) experts_simt_kernel(const ExpertSimtParams
     const int ti = (threadIdx.x / 16) * 4, tj = (threadIdx.x % 16) * 4;
 
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
-        const int i = position_of_tile(tab, p.experts, t);
-        const int e = tab.order[i], mb = (t - tab.tile[i]) / n_tiles, nb = (t - tab.tile[i]) % n_tiles;
+        const int e = expert_of_tile(tab, p.experts, t), mb = (t - tab.tile[e]) / n_tiles, nb = (t - tab.tile[e]) % n_tiles;
         const int64_t r0 = tab.off[e], len = tab.len(e);
         const int64_t L = DIR == kExpForward ? p.K : DIR == kExpData ? p.N : len;
         const int i_lim = (int)min((int64_t)BT, (DIR == kExpWeight ? (int64_t)p.N : len) - (int64_t)mb * BT);

@@ -15,7 +15,8 @@
 // last of them to arrive (a counter per tile) adds the parts in the order of k
 // and stores.  No SM waits for another, and the sum's order is fixed.
 //
-// Roles: warps 0-3 epilogue, 4 filter loads, 5 MMA and TMEM, 6 row loads.
+// Roles: warps 0-3 epilogue, 4 filter loads, 5 MMA and TMEM, 6 row loads, 7
+// table and schedule.  Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -30,6 +31,8 @@ namespace cbd {
 
 namespace {
 
+constexpr int RING = 4;
+
 template <int BT>
 struct Cfg {
     static constexpr int S = BT == 16 ? 11 : 8;  // stages
@@ -37,14 +40,16 @@ struct Cfg {
     static constexpr int B_BYTES = BT * 128;
     static constexpr int TMEM_COLS = 2 * BT;  // two accumulators (32 or 128 columns)
     struct Bars {
+        ExpertRing<RING> ring;
         uint64_t full[S], empty[S], tfull[2], tempty[2];
         uint32_t tmem;
-        int32_t abort, last;
+        int32_t abort, last, vote[8];
+        uint32_t share[2];  // of the schedule: units of a block, blocks with one more
     };
     static constexpr int SMEM = 1024 + S * (A_BYTES + B_BYTES) + (int)sizeof(ExpertTable) + (int)sizeof(Bars) + 8;
     static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
-constexpr int THREADS = 7 * 32;
+constexpr int THREADS = 8 * 32;
 
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
     asm volatile(
@@ -61,26 +66,17 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *map, ui
         : "memory");
 }
 
-// A block's stretch of the sequence (tile, k-block), tile by tile.
-struct Stretch {
-    int64_t u, hi;
-    int nkb;
-    int t, kb0, kb1;  // current segment
-    __device__ __forceinline__ Stretch(int64_t units, int nkb_, int b, int g) : nkb(nkb_) {
-        u = units * b / g;
-        hi = b < g ? units * (b + 1) / g : u;
-    }
-    __device__ __forceinline__ bool next() {
-        if (u >= hi) return false;
-        t = (int)(u / nkb);
-        kb0 = (int)(u - (int64_t)t * nkb);
-        kb1 = (int)min((int64_t)nkb, kb0 + (hi - u));
-        u += kb1 - kb0;
-        return true;
+// The blocks' equal stretches of `units` things: the first units % g have one more.
+struct Share {
+    uint32_t each, more;
+    __device__ __forceinline__ Share(uint32_t units, uint32_t g) : each(units / g), more(units - each * g) {}
+    __device__ __forceinline__ Share(uint32_t each_, uint32_t more_, int) : each(each_), more(more_) {}
+    __device__ __forceinline__ uint32_t begin(uint32_t b) const { return b * each + min(b, more); }
+    __device__ __forceinline__ uint32_t block_of(uint32_t u) const {
+        const uint32_t longer = more * (each + 1);
+        return u < longer ? u / (each + 1) : more + (u - longer) / each;
     }
 };
-// block whose stretch holds unit u
-__device__ __forceinline__ int block_of(int64_t u, int64_t units, int g) { return (int)(((u + 1) * g - 1) / units); }
 
 template <int DIR, int BT>
 __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid_constant__ ExpertStreamParams p) {
@@ -97,7 +93,6 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
     const int mdim = DIR == kExpData ? p.K : p.N, depth = DIR == kExpData ? p.N : p.K;
     const int mt = (mdim + 127) / 128, nkb = (depth + 63) / 64;
 
-    load_expert_offsets(tab, p.offsets, p.experts);
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full0 + 8 * s, 1);
@@ -107,6 +102,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
             mbar_init(tfull0 + 8 * b, 1);
             mbar_init(tempty0 + 8 * b, 4);
         }
+        bars.ring.init(7);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -119,39 +115,57 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
     }
-    __syncthreads();
-    if (warp == 0)
-        build_expert_table(tab, p.experts, p.rows, BT, mt, kTilesInOrder, blockIdx.x == 0 ? p.status : nullptr);
+    if (warp == 7) build_expert_table<BT>(tab, p.offsets, p.experts, p.rows, mt, kTilesByRows, blockIdx.x == 0 ? p.status : nullptr);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = bars.tmem;
-    const int64_t units = (int64_t)tab.tile[p.experts] * nkb;
-    // no more blocks than units: every block between a tile's first and last has a part of it
-    const int nblocks = (int)min((int64_t)gridDim.x, max(units, (int64_t)1));
-    Stretch seg(units, nkb, min((int)blockIdx.x, nblocks), nblocks);
 
-    // rows and M block of tile t
-    struct Where {
-        int e, row0, ntok, m0;
-    };
-    auto where = [&](int t) {
-        Where w;
-        w.e = position_of_tile(tab, p.experts, t);
-        const int l = t - tab.tile[w.e], len = tab.len(w.e), first = (l / mt) * BT;
-        w.row0 = tab.off[w.e] + first;
-        w.ntok = min(BT, len - first);
-        w.m0 = (l % mt) * 128;
-        return w;
-    };
-
-    if (warp == 4 || warp == 6) {
+    if (warp == 7) {
+        // ------------------------------------------------------------ schedule
+        if (lane == 0) {
+            // Cut tiles where their k-blocks spread more evenly over the SMs than whole tiles by more than a join
+            // takes: 2.3 us, the time of about eight 16 KB blocks of an SM.
+            const uint32_t ntiles = (uint32_t)tab.tile[p.experts], g = gridDim.x;
+            const uint32_t whole_most = (ntiles + g - 1) / g * nkb, cut_most = (ntiles * nkb + g - 1) / g;
+            const uint32_t grain = whole_most <= cut_most + 8 ? nkb : 1;  // k-blocks handed out at a time
+            const uint32_t units = ntiles * (grain == 1 ? nkb : 1);
+            // no more blocks than units: every block between a tile's first and last has a part of it
+            const uint32_t nblocks = max(1u, min(g, units));
+            const Share share(units, nblocks);
+            bars.share[0] = share.each;
+            bars.share[1] = share.more;
+            uint32_t u = blockIdx.x < nblocks ? share.begin(blockIdx.x) * grain : 0u;
+            const uint32_t hi = blockIdx.x < nblocks ? share.begin(blockIdx.x + 1) * grain : 0u;
+            int t = (int)(u / (uint32_t)nkb), kb0 = (int)u - t * nkb;
+            for (uint32_t i = 0;; ++i, ++t, kb0 = 0) {
+                ExpertWork w;
+                w.n = 0;
+                if (u < hi) {
+                    w.e = expert_of_tile(tab, p.experts, t);
+                    const int l = t - tab.tile[w.e], q = l / mt, first = q * BT;
+                    w.row0 = tab.off[w.e] + first;
+                    w.ntok = min(BT, tab.len(w.e) - first);
+                    w.m0 = (l - q * mt) * 128;
+                    w.n = (w.ntok + 15) & ~15;
+                    w.kb0 = kb0;
+                    w.kb1 = (int)min((uint32_t)nkb, (uint32_t)kb0 + (hi - u));
+                    w.last = t;
+                    u += (uint32_t)(w.kb1 - kb0);
+                }
+                if (!bars.ring.give(i, w, p.wait_budget, abort_flag, p.status) || w.n == 0) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 4 || warp == 6) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            while (ok && seg.next()) {
-                const Where w = where(seg.t);
-                for (int kb = seg.kb0; kb < seg.kb1; ++kb, ++it) {
+            for (uint32_t i = 0; ok; ++i) {
+                const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
+                if (w.n == 0) break;
+                bars.ring.done(i);
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                     const uint32_t s = it % S, ph = (it / S) & 1, bar = full0 + 8 * s;
                     if (!mbar_wait_bounded(empty0 + 8 * s, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) {
                         ok = false;
@@ -186,16 +200,18 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
             const uint64_t b_desc0 = smem_desc_sw128(smem_u32(sB), 16, 1024);
             uint32_t it = 0;
             bool ok = true;
-            for (uint32_t use = 0; ok && seg.next(); ++use) {
-                const Where w = where(seg.t);
+            for (uint32_t use = 0; ok; ++use) {
+                const ExpertWork w = bars.ring.take(use, p.wait_budget, abort_flag, p.status, kDevTimeoutMma);
+                if (w.n == 0) break;
+                bars.ring.done(use);
                 const uint32_t b = use & 1, bph = (use >> 1) & 1;
                 if (!mbar_wait_bounded(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t id = idesc0 | ((uint32_t)(((w.ntok + 15) & ~15) >> 3) << 17), d = tmem_base + b * BT;
-                for (int kb = seg.kb0; kb < seg.kb1; ++kb, ++it) {
+                const uint32_t id = idesc0 | ((uint32_t)(w.n >> 3) << 17), d = tmem_base + b * BT;
+                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                     const uint32_t s = it % S, ph = (it / S) & 1;
                     if (!mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
                         ok = false;
@@ -203,7 +219,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
                     }
                     const uint64_t ad = a_desc0 + (uint64_t)((s * C::A_BYTES) >> 4), bd = b_desc0 + (uint64_t)((s * C::B_BYTES) >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) tc_mma(d, ad + A_STEP * kk, bd + 2 * kk, id, (kb != seg.kb0 || kk != 0) ? 1u : 0u);
+                    for (int kk = 0; kk < 4; ++kk) tc_mma(d, ad + A_STEP * kk, bd + 2 * kk, id, (kb != w.kb0 || kk != 0) ? 1u : 0u);
                     tc_commit(empty0 + 8 * s);
                 }
                 if (ok) tc_commit(tfull0 + 8 * b);
@@ -216,27 +232,25 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
     } else {
         // ------------------------------------------------------------ epilogue
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
-        {
-            // rows of no expert: zeros
-            const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
-            const int64_t nfill = (int64_t)lo + (p.rows - hi);
-            for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
-                uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
-                for (int c = threadIdx.x; c < vec; c += 128) row[c] = make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
         const uint32_t lane_base = tmem_base + ((uint32_t)(warp * 32) << 16);
         bool ok = true;  // after a wait that ran out: no stores, but every barrier and counter as usual
-        for (uint32_t use = 0; seg.next(); ++use) {
-            const Where w = where(seg.t);
+        for (uint32_t use = 0;; ++use) {
+            const ExpertWork w = bars.ring.take(use, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
+            bool more = __all_sync(0xffffffffu, w.n != 0);
+            if (more && lane == 0) bars.ring.done(use);
+            // the four warps meet at barriers below: they go on or stop together
+            volatile int32_t *vote = bars.vote + (use & 1) * 4;
+            if (lane == 0) vote[warp] = more;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (!(vote[0] & vote[1] & vote[2] & vote[3])) break;
             const uint32_t b = use & 1;
             if (ok) ok = mbar_wait_bounded(tfull0 + 8 * b, (use >> 1) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
-            const bool whole = seg.kb0 == 0 && seg.kb1 == nkb;
+            const bool whole = w.kb0 == 0 && w.kb1 == nkb;
             const int m = w.m0 + (int)threadIdx.x;
             __nv_bfloat16 *dst = out + (int64_t)w.row0 * p.ldo + m;
-            float *slot = p.parts + ((int64_t)blockIdx.x * 2 + (seg.kb0 == 0 ? 1 : 0)) * (BT * 128) + threadIdx.x;
+            float *slot = p.parts + ((int64_t)blockIdx.x * 2 + (w.kb0 == 0 ? 1 : 0)) * (BT * 128) + threadIdx.x;
             constexpr int G = BT < 32 ? BT : 32;
 #pragma unroll 1
             for (int g = 0; g < w.ntok; g += G) {
@@ -260,8 +274,9 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
             if (lane == 0) mbar_arrive(tempty0 + 8 * b);
             if (whole) continue;
 
-            const int64_t first = (int64_t)seg.t * nkb;
-            const int c0 = block_of(first, units, nblocks), c1 = block_of(first + nkb - 1, units, nblocks);
+            const uint32_t first = (uint32_t)w.last * nkb;  // (grain 1)
+            const Share share(bars.share[0], bars.share[1], 0);
+            const int c0 = (int)share.block_of(first), c1 = (int)share.block_of(first + nkb - 1);
             __threadfence();
             asm volatile("bar.sync 1, 128;" ::: "memory");
             if (threadIdx.x == 0) {
@@ -292,6 +307,15 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
                 }
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");  // bars.last is written again
+        }
+        {
+            // rows of no expert: zeros
+            const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
+            const int64_t nfill = (int64_t)lo + (p.rows - hi);
+            for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
+                uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
+                for (int c = threadIdx.x; c < vec; c += 128) row[c] = make_uint4(0u, 0u, 0u, 0u);
+            }
         }
     }
 

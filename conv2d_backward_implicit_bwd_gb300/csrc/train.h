@@ -36,7 +36,6 @@ struct ExpertPairParams {  // 128-byte aligned through CUtensorMap
     int64_t ldo;
     int32_t experts, rows, K, N;
     int32_t accumulate;
-    int32_t *next;           // tile counter and finished pairs, 0 between launches
 };
 cudaError_t launch_experts_pair(const ExpertPairParams &p, int dir, int grid, cudaStream_t s);
 

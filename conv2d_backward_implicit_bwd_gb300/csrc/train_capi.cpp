@@ -238,7 +238,9 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
         ((uintptr_t)a | (uintptr_t)b | (uintptr_t)out) % 16 == 0 && rows > 0 && d.K * d.N < (1LL << 37)) {
         // Few rows per expert: the time is the filters' bytes, cut evenly over the SMs.  With more the pairs' wide
         // tiles use an operand for more products.
-        if (!weight && rows <= kFewRows * d.experts) {
+        const int64_t stream_blocks =
+            (rows / 16 + std::min<int64_t>(d.experts, rows)) * ((wo + 127) / 128) * ((wa + 63) / 64);
+        if (!weight && rows <= kFewRows * d.experts && stream_blocks <= 0x7fffffff) {
             const int bt = rows <= 8 * d.experts ? 16 : kStreamRows;
             ExpertStreamParams sp;
             std::memset(&sp, 0, sizeof(sp));
@@ -252,8 +254,7 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
             sp.ldo = ldo;
             sp.experts = (int32_t)d.experts; sp.rows = (int32_t)rows; sp.K = (int32_t)d.K; sp.N = (int32_t)d.N;
             // at least four blocks of 16 KB for an SM
-            const int64_t blocks = ((rows / bt + std::min<int64_t>(d.experts, rows)) * ((wo + 127) / 128)) * ((wa + 63) / 64);
-            const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(p->dev.num_sms, blocks / 4));
+            const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(p->dev.num_sms, stream_blocks / 4));
             return launch_experts_stream(sp, dir, bt, grid, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
         }
         const int64_t mt = ((dir == kExpData ? d.K : d.N) + 255) / 256, pairs = std::max(1, p->dev.num_sms / 2);
@@ -273,7 +274,6 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
         pp.ldo = ldo;
         pp.experts = (int32_t)d.experts; pp.rows = (int32_t)rows; pp.K = (int32_t)d.K; pp.N = (int32_t)d.N;
         pp.accumulate = accumulate ? 1 : 0;
-        pp.next = reinterpret_cast<int32_t *>(p->dev.ticket());
         const int64_t most = weight ? d.experts * mt * ((d.K + 255) / 256) : mt * (rows / 256 + std::min<int64_t>(d.experts, rows));
         const int grid = (int)(2 * std::max<int64_t>(1, std::min(pairs, most)));
         return launch_experts_pair(pp, dir, grid, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
