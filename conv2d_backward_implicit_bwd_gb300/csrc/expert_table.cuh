@@ -61,7 +61,7 @@ __device__ __forceinline__ void build_expert_table(ExpertTable &t, const int32_t
         // tiles of expert e - 1
         const uint32_t len = e > 0 && e <= experts ? (uint32_t)(o - before) : 0u;
         int n = kind == kTilesByRows ? (int)((len + PER - 1) / PER) * mult : e > 0 && e <= experts && (kind == kTilesEach || len) ? mult : 0;
-#pragma unroll 1
+#pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, n, d);
             if (lane >= d) n += v;

@@ -37,7 +37,7 @@
 // hand-over between the two CTAs took 0.65 us of every role's time per tile.)
 //
 // Roles per CTA: warps 0-3 epilogue, 4 A loads, 5 MMA (leader CTA) and TMEM,
-// 6-7 B loads, 8 helper of weight's last blocks, 9 schedule.  Every wait is
+// 6-7 B loads, 8 helper (weight: last blocks; else rows of no expert), 9 schedule.  Every wait is
 // bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -321,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         }
         __syncwarp();
     } else if (warp == 8) {
-        // ------------------------------------------------------------ weight: rows past the expert's end
+        // ------------------------------------------------------------ helper: rows past an expert's end, rows of none
         if constexpr (DIR == kExpWeight) {
             uint32_t it = 0, phase = 0;  // bit s: parity of the next use of tail[s] and peer[s]
             for (uint32_t i = 0;; ++i) {
@@ -353,6 +353,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                     }
                 }
                 if (!__all_sync(0xffffffffu, ok)) break;
+            }
+        } else {
+            // forward, data: rows of no expert get zeros (16-byte stores; the width is a multiple of 8)
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
+            const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
+            const int64_t nfill = (int64_t)lo + (p.rows - hi);
+            for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
+                uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
+                for (int c = lane; c < vec; c += 32) row[c] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
     } else {
@@ -458,16 +467,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8 * b);
-            }
-        }
-        if constexpr (DIR != kExpWeight) {
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
-            // rows of no expert: zeros (16-byte stores; the width is a multiple of 8)
-            const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
-            const int64_t nfill = (int64_t)lo + (p.rows - hi);
-            for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
-                uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
-                for (int c = threadIdx.x; c < vec; c += 128) row[c] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
         if constexpr (DIR == kExpWeight) bulk_wait_all();

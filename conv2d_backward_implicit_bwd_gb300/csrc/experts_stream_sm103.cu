@@ -16,7 +16,7 @@
 // and stores.  No SM waits for another, and the sum's order is fixed.
 //
 // Roles: warps 0-3 epilogue, 4 filter loads, 5 MMA and TMEM, 6 row loads, 7
-// table and schedule.  Every wait is bounded.
+// table and schedule, 8 rows of no expert.  Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -49,7 +49,7 @@ struct Cfg {
     static constexpr int SMEM = 1024 + S * (A_BYTES + B_BYTES) + (int)sizeof(ExpertTable) + (int)sizeof(Bars) + 8;
     static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
-constexpr int THREADS = 8 * 32;
+constexpr int THREADS = 9 * 32;
 
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
     asm volatile(
@@ -156,6 +156,15 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
             }
         }
         __syncwarp();
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ rows of no expert: zeros
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
+        const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
+        const int64_t nfill = (int64_t)lo + (p.rows - hi);
+        for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
+            uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
+            for (int c = lane; c < vec; c += 32) row[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
     } else if (warp == 4 || warp == 6) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
@@ -307,15 +316,6 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
                 }
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");  // bars.last is written again
-        }
-        {
-            // rows of no expert: zeros
-            const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
-            const int64_t nfill = (int64_t)lo + (p.rows - hi);
-            for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
-                uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
-                for (int c = threadIdx.x; c < vec; c += 128) row[c] = make_uint4(0u, 0u, 0u, 0u);
-            }
         }
     }
 
