@@ -88,6 +88,28 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
         : "memory");
 }
+// One lane of a warp that runs converged issues; the operands stay warp-uniform.
+// (Issued by a single thread in a divergent branch, the MMA loop took 612 clocks
+// for a 64-deep step of 512, loads and epilogue aside; this way 540.)
+__device__ __forceinline__ void mma_pair_elect(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// arrives on the barrier at this offset in both CTAs when the lane's MMAs so far are done
+__device__ __forceinline__ void commit_pair_elect(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)0x3)
+        : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
@@ -278,42 +300,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         __syncwarp();
     } else if (warp == 5) {
         // ------------------------------------------------------------ MMA (leader)
-        if (leader && lane == 0) {
+        if (leader) {
             constexpr bool A_K = DIR == kExpForward, B_K = DIR != kExpWeight;
             constexpr uint32_t A_STEP = A_K ? 2 : 128, B_STEP = B_K ? 2 : 128;  // a 16-deep step, in 16 bytes
             const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((A_K ? 0u : 1u) << 15) | ((B_K ? 0u : 1u) << 16) | ((uint32_t)(256 >> 4) << 24);
             const uint64_t a_desc0 = smem_desc_sw128(smem_u32(sA), A_K ? 16 : 8192, 1024);
             const uint64_t b_desc0 = smem_desc_sw128(smem_u32(sB), B_K ? 16 : 8192, 1024);
-            uint32_t it = 0, use = 0;  // stages and accumulators used so far
+            const uint32_t a_lo = (uint32_t)a_desc0, a_hi = (uint32_t)(a_desc0 >> 32), b_lo = (uint32_t)b_desc0, b_hi = (uint32_t)(b_desc0 >> 32);
+            uint32_t s = 0, ph = 0, use = 0;  // stage and its phase, accumulators used so far
             bool ok = true, issued = false;
             for (uint32_t i = 0; ok; ++i) {
-                const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutMma);
+                ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutMma);
+                w.n = __shfl_sync(0xffffffffu, w.n, 0);
+                w.kb1 = __shfl_sync(0xffffffffu, w.kb1, 0);
+                w.last = __shfl_sync(0xffffffffu, w.last, 0);
                 if (w.n == 0) break;
-                bars.ring.done(i);
+                if (lane == 0) bars.ring.done(i);
                 if (w.kb1 == 0) continue;
                 const uint32_t b = use & 1, bph = (use >> 1) & 1;
                 ++use;
-                if (!mbar_wait_bounded(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
-                    ok = false;
-                    break;
-                }
+                ok = mbar_wait_bounded(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t id = idesc0 | ((uint32_t)(w.n >> 3) << 17), d = tmem_base + b * 256;
-                for (int kb = 0; kb < w.kb1; ++kb, ++it) {
-                    const uint32_t s = it % S, ph = (it / S) & 1;
-                    if (!mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
+                uint32_t acc = 0;
+                for (int left = w.kb1; left > 0; --left) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma))) {
                         ok = false;
                         break;
                     }
-                    const uint64_t ad = a_desc0 + (uint64_t)((s * A_BYTES) >> 4), bd = b_desc0 + (uint64_t)((s * B_BYTES) >> 4);
-                    const int n = DIR == kExpWeight && kb == w.kb1 - 1 ? (w.last + 15) / 16 : 4;
+                    const uint32_t ad = a_lo + s * (A_BYTES >> 4), bd = b_lo + s * (B_BYTES >> 4);
+                    const int n = DIR == kExpWeight && left == 1 ? (w.last + 15) / 16 : 4;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (kk < n) tc_mma2(d, ad + A_STEP * kk, bd + B_STEP * kk, id, (kb | kk) != 0 ? 1u : 0u);
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk < n) mma_pair_elect(d, ad + A_STEP * kk, a_hi, bd + B_STEP * kk, b_hi, id, acc);
+                        acc = 1;
+                    }
                     issued = true;
-                    tc_commit2_mc(empty0 + 8 * s, (uint16_t)0x3);
+                    commit_pair_elect(empty0 + 8 * s);
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1;
+                    }
                 }
-                if (ok) tc_commit2_mc(tfull0 + 8 * b, (uint16_t)0x3);
+                if (ok) commit_pair_elect(tfull0 + 8 * b);
             }
             if (!ok && issued) {
                 for (int q = 0; q < 100; ++q) __nanosleep(1000);

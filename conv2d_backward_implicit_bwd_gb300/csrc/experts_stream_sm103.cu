@@ -66,6 +66,25 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *map, ui
         : "memory");
 }
 
+// One lane of a warp that runs converged issues; the operands stay warp-uniform.
+__device__ __forceinline__ void mma_elect(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit_elect(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+
 // The blocks' equal stretches of `units` things: the first units % g have one more.
 struct Share {
     uint32_t each, more;
@@ -201,41 +220,45 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
         __syncwarp();
     } else if (warp == 5) {
         // ------------------------------------------------------------ MMA
-        if (lane == 0) {
-            constexpr bool A_K = DIR == kExpForward;
-            constexpr uint32_t A_STEP = A_K ? 2 : 128;
-            const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((A_K ? 0u : 1u) << 15) | ((uint32_t)(128 >> 4) << 24);
-            const uint64_t a_desc0 = smem_desc_sw128(smem_u32(sA), A_K ? 16 : 8192, 1024);
-            const uint64_t b_desc0 = smem_desc_sw128(smem_u32(sB), 16, 1024);
-            uint32_t it = 0;
-            bool ok = true;
-            for (uint32_t use = 0; ok; ++use) {
-                const ExpertWork w = bars.ring.take(use, p.wait_budget, abort_flag, p.status, kDevTimeoutMma);
-                if (w.n == 0) break;
-                bars.ring.done(use);
-                const uint32_t b = use & 1, bph = (use >> 1) & 1;
-                if (!mbar_wait_bounded(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t id = idesc0 | ((uint32_t)(w.n >> 3) << 17), d = tmem_base + b * BT;
-                for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-                    const uint32_t s = it % S, ph = (it / S) & 1;
-                    if (!mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint64_t ad = a_desc0 + (uint64_t)((s * C::A_BYTES) >> 4), bd = b_desc0 + (uint64_t)((s * C::B_BYTES) >> 4);
+        constexpr bool A_K = DIR == kExpForward;
+        constexpr uint32_t A_STEP = A_K ? 2 : 128;
+        const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((A_K ? 0u : 1u) << 15) | ((uint32_t)(128 >> 4) << 24);
+        const uint64_t a_desc0 = smem_desc_sw128(smem_u32(sA), A_K ? 16 : 8192, 1024);
+        const uint64_t b_desc0 = smem_desc_sw128(smem_u32(sB), 16, 1024);
+        const uint32_t a_lo = (uint32_t)a_desc0, a_hi = (uint32_t)(a_desc0 >> 32), b_lo = (uint32_t)b_desc0, b_hi = (uint32_t)(b_desc0 >> 32);
+        uint32_t s = 0, ph = 0;
+        bool ok = true;
+        for (uint32_t use = 0; ok; ++use) {
+            ExpertWork w = bars.ring.take(use, p.wait_budget, abort_flag, p.status, kDevTimeoutMma);
+            w.n = __shfl_sync(0xffffffffu, w.n, 0);
+            const int count = __shfl_sync(0xffffffffu, w.kb1 - w.kb0, 0);
+            if (w.n == 0) break;
+            if (lane == 0) bars.ring.done(use);
+            const uint32_t b = use & 1, bph = (use >> 1) & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t id = idesc0 | ((uint32_t)(w.n >> 3) << 17), d = tmem_base + b * BT;
+            uint32_t acc = 0;
+            for (int left = count; left > 0; --left) {
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
+                if (!ok) break;
+                const uint32_t ad = a_lo + s * (C::A_BYTES >> 4), bd = b_lo + s * (C::B_BYTES >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) tc_mma(d, ad + A_STEP * kk, bd + 2 * kk, id, (kb != w.kb0 || kk != 0) ? 1u : 0u);
-                    tc_commit(empty0 + 8 * s);
+                for (int kk = 0; kk < 4; ++kk) {
+                    mma_elect(d, ad + A_STEP * kk, a_hi, bd + 2 * kk, b_hi, id, acc);
+                    acc = 1;
                 }
-                if (ok) tc_commit(tfull0 + 8 * b);
+                commit_elect(empty0 + 8 * s);
+                if (++s == (uint32_t)S) {
+                    s = 0;
+                    ph ^= 1;
+                }
             }
-            if (!ok) {
-                for (int q = 0; q < 100; ++q) __nanosleep(1000);
-            }
+            if (ok) commit_elect(tfull0 + 8 * b);
+        }
+        if (!ok) {
+            for (int q = 0; q < 100; ++q) __nanosleep(1000);
         }
         __syncwarp();
     } else {
