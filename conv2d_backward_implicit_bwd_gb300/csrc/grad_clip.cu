@@ -68,6 +68,13 @@ struct Elem<__nv_bfloat16> {
     }
 };
 
+// (volatile: all of a chunk's loads are issued before the first is used)
+__device__ __forceinline__ uint4 ld16(const uint4 *p) {
+    uint4 u;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+    return u;
+}
+
 // n elements from src: elements before the first 16-byte boundary, vectors, the rest
 template <typename T>
 struct Span {
@@ -96,7 +103,8 @@ __device__ __forceinline__ double chunk_squares(const T *src, int n) {
 #pragma unroll
     for (int q = 0; q < MOST; ++q) {
         const int i = threadIdx.x + q * NT;
-        u[q] = i < sp.nv ? v[i] : make_uint4(0u, 0u, 0u, 0u);
+        u[q] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < sp.nv) u[q] = ld16(v + i);
     }
 #pragma unroll
     for (int q = 0; q < MOST; ++q) {
@@ -140,29 +148,13 @@ __device__ __forceinline__ void chunk_scale(const T *src, T *dst, int n, float c
 #pragma unroll
     for (int q = 0; q < MOST; ++q) {
         const int i = threadIdx.x + q * NT;
-        if (i < sp.nv) u[q] = v[i];
+        if (i < sp.nv) u[q] = ld16(v + i);
     }
 #pragma unroll
     for (int q = 0; q < MOST; ++q) {
         const int i = threadIdx.x + q * NT;
         if (i < sp.nv) o[i] = Elem<T>::scaled(u[q], c);
     }
-}
-
-// A chunk: 32 KB of a tensor, counted from its first element.
-struct Chunk {
-    int tensor, dtype, n;
-    int64_t start;
-};
-__device__ __forceinline__ Chunk chunk_of(const ClipParams &p, int i) {
-    const ClipChunk ch = p.chunks[i];
-    Chunk r;
-    r.tensor = ch.tensor;
-    r.dtype = p.dtypes[ch.tensor];
-    const int per = r.dtype == 1 ? kClipChunk / 2 : kClipChunk / 4;
-    r.start = (int64_t)ch.index * per;
-    r.n = (int)min((int64_t)per, p.sizes[ch.tensor] - r.start);
-    return r;
 }
 
 __device__ __forceinline__ double block_sum(double v, double *sh) {
@@ -190,9 +182,11 @@ __global__ void __launch_bounds__(NT) clip_norm_kernel(const __grid_constant__ C
     __shared__ double sh[NT / 32];
     __shared__ bool last;
     double sum = 0.0;
+    ClipChunk next = p.chunks[max(min((int)blockIdx.x, p.num_chunks - 1), 0)];
     for (int i = blockIdx.x; i < p.num_chunks; i += gridDim.x) {
-        const Chunk ch = chunk_of(p, i);
-        if (ch.dtype == 1)
+        const ClipChunk ch = next;
+        next = p.chunks[min(i + (int)gridDim.x, p.num_chunks - 1)];
+        if (ch.bf16)
             sum += chunk_squares(static_cast<const __nv_bfloat16 *>(at.g[ch.tensor]) + ch.start, ch.n);
         else
             sum += chunk_squares(static_cast<const float *>(at.g[ch.tensor]) + ch.start, ch.n);
@@ -223,10 +217,12 @@ __global__ void __launch_bounds__(NT) clip_norm_kernel(const __grid_constant__ C
 template <int N>
 __global__ void __launch_bounds__(NT) clip_scale_kernel(const __grid_constant__ ClipParams p, const __grid_constant__ Pointers<N, true> at) {
     const float c = *p.coef;
+    ClipChunk next = p.chunks[max(p.num_chunks - 1 - (int)blockIdx.x, 0)];
     for (int i = p.num_chunks - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
-        const Chunk ch = chunk_of(p, i);
+        const ClipChunk ch = next;
+        next = p.chunks[max(i - (int)gridDim.x, 0)];
         if (c == 1.f && at.g[ch.tensor] == at.o[ch.tensor]) continue;  // in place and nothing to clip
-        if (ch.dtype == 1)
+        if (ch.bf16)
             chunk_scale(static_cast<const __nv_bfloat16 *>(at.g[ch.tensor]) + ch.start,
                         static_cast<__nv_bfloat16 *>(at.o[ch.tensor]) + ch.start, ch.n, c);
         else

@@ -56,15 +56,16 @@ cudaError_t launch_experts_stream(const ExpertStreamParams &p, int dir, int bt, 
 
 // Gradient clipping: the tensors are cut into chunks of kClipChunk bytes.
 constexpr int kClipChunk = 32768;
+constexpr int kClipBlocks = 6;     // blocks per SM
 constexpr int kClipPtrs = 1000;  // tensors per launch (their pointers travel as kernel parameters)
-struct ClipChunk {
-    int32_t tensor;  // index within the launch's pointer table
-    int32_t index;   // chunk of that tensor
+struct __align__(16) ClipChunk {
+    int64_t start;   // first element
+    int32_t n;       // elements
+    int16_t tensor;  // index within the launch's pointer table
+    int16_t bf16;
 };
 struct ClipParams {
-    const ClipChunk *chunks;
-    const int64_t *sizes;    // [tensors of this launch]
-    const int32_t *dtypes;
+    const ClipChunk *chunks;  // of this launch's tensors; at least one entry
     double *partials;        // one per block of every norm launch
     uint32_t *ticket;
     float *norm, *coef;
@@ -91,6 +92,7 @@ struct PolicyParams {
     uint32_t *ticket;
     int32_t *status;
     int64_t ld, ldd;
+    int64_t wait_budget;
     int32_t tokens, vocab;
     float clip_lo, clip_hi, kl, scale;     // clamp bounds 1 - clip_low, 1 + clip_high
 };

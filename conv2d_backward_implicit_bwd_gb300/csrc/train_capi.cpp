@@ -169,7 +169,7 @@ struct conv_bwd_clip_plan_s {
     };
     std::vector<Launch> launches;
     int32_t partial_total = 0;
-    size_t off_chunks = 0, off_sizes = 0, off_dtypes = 0;
+    size_t off_chunks = 0;
     std::mutex mu;
     DevicePart dev;
 };
@@ -344,33 +344,24 @@ conv_bwd_status conv_bwd_clip_create(int32_t count, const int64_t *sizes, const 
             l.tensors = std::min(kClipPtrs, count - first);
             l.chunk_off = chunks.size();
             for (int32_t t = 0; t < l.tensors; ++t) {
-                const int64_t bytes = sizes[first + t] * (int64_t)esize(dtypes[first + t]);
-                for (int64_t c = 0; c * kClipChunk < bytes; ++c) chunks.push_back({t, (int32_t)c});
+                const int64_t per = kClipChunk / (int64_t)esize(dtypes[first + t]), size = sizes[first + t];
+                for (int64_t at = 0; at < size; at += per)
+                    chunks.push_back({at, (int32_t)std::min(per, size - at), (int16_t)t, (int16_t)(dtypes[first + t] == CONV_BWD_BF16)});
             }
             const size_t n = chunks.size() - l.chunk_off;
             if (n > 0x7fffffff) return CONV_BWD_ERR_UNSUPPORTED;
             l.chunks = (int32_t)n;
-            l.grid = (int32_t)std::max<int64_t>(1, std::min<int64_t>(l.chunks, (int64_t)sms * 4));
+            l.grid = (int32_t)std::max<int64_t>(1, std::min<int64_t>(l.chunks, (int64_t)sms * kClipBlocks));
             l.partial_base = p.partial_total;
             p.partial_total += l.grid;
             p.launches.push_back(l);
         }
-        size_t at = 64 + (size_t)p.partial_total * 8;
-        p.off_chunks = at;
-        at += chunks.size() * sizeof(ClipChunk);
-        at = (at + 7) / 8 * 8;
-        p.off_sizes = at;
-        at += (size_t)count * 8;
-        p.off_dtypes = at;
-        at += (size_t)count * 4;
-        const conv_bwd_status st = p.dev.init(at + 8);
+        chunks.push_back({0, 0, 0, 0});  // a launch without chunks still reads one entry
+        p.off_chunks = (64 + (size_t)p.partial_total * 8 + 15) / 16 * 16;
+        const conv_bwd_status st = p.dev.init(p.off_chunks + chunks.size() * sizeof(ClipChunk));
         if (st != CONV_BWD_OK || !p.dev.has_device) return st;
-        char *m = static_cast<char *>(p.dev.mem);
-        if ((!chunks.empty() && cudaMemcpy(m + p.off_chunks, chunks.data(), chunks.size() * sizeof(ClipChunk),
-                                           cudaMemcpyHostToDevice) != cudaSuccess) ||
-            (count > 0 &&
-             (cudaMemcpy(m + p.off_sizes, sizes, (size_t)count * 8, cudaMemcpyHostToDevice) != cudaSuccess ||
-              cudaMemcpy(m + p.off_dtypes, dtypes, (size_t)count * 4, cudaMemcpyHostToDevice) != cudaSuccess)))
+        if (cudaMemcpy(static_cast<char *>(p.dev.mem) + p.off_chunks, chunks.data(), chunks.size() * sizeof(ClipChunk),
+                       cudaMemcpyHostToDevice) != cudaSuccess)
             return CONV_BWD_ERR_CUDA;
         return CONV_BWD_OK;
     });
@@ -411,8 +402,6 @@ static conv_bwd_status clip_launch(conv_bwd_clip_plan p, const void *const *grad
         for (size_t k = 0; k < nl; ++k) {
             const auto &l = p->launches[pass ? nl - 1 - k : k];
             cp.chunks = reinterpret_cast<const ClipChunk *>(m + p->off_chunks) + l.chunk_off;
-            cp.sizes = reinterpret_cast<const int64_t *>(m + p->off_sizes) + l.first;
-            cp.dtypes = reinterpret_cast<const int32_t *>(m + p->off_dtypes) + l.first;
             cp.num_chunks = l.chunks;
             cp.partial_base = l.partial_base;
             cp.partial_total = k + 1 == nl ? p->partial_total : 0;
@@ -500,6 +489,7 @@ static conv_bwd_status policy_run(conv_bwd_policy_plan p, int mode, PolicyParams
     pp.clip_hi = 1.f + p->d.clip_high;
     pp.kl = p->d.kl;
     pp.scale = p->d.scale;
+    pp.wait_budget = (int64_t)p->dev.clock_khz * 2000;
     return launch_policy(pp, p->d.dtype, mode, p->dev.num_sms, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK
                                                                                                     : CONV_BWD_ERR_CUDA;
 }

@@ -10,8 +10,10 @@ must not overlap on the GPU, so keep one plan per stream.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
+import operator
 
 import torch
 
@@ -210,6 +212,11 @@ class Experts(_Plan):
         return _status(_lib.conv_bwd_experts_get_status, self._h, stream)
 
 
+# (over hundreds of tensors a call, mapped in C)
+_numel, _contiguous, _data_ptr = torch.Tensor.numel, torch.Tensor.is_contiguous, torch.Tensor.data_ptr
+_type_device = operator.attrgetter("dtype", "is_cuda")
+
+
 class GradClip(_Plan):
     """Global L2 norm over many tensors, and clipping.
 
@@ -222,12 +229,11 @@ class GradClip(_Plan):
         sizes = [int(n) for n in sizes]
         codes = [_dtype(d) for d in dtypes]
         _need(len(sizes) == len(codes), f"{len(sizes)} sizes and {len(codes)} dtypes")
-        self._want = [(n, _TORCH[c], True, True) for n, c in zip(sizes, codes)]
+        self._sizes, self._types = sizes, [(_TORCH[c], True) for c in codes]
         self.count = n = len(sizes)
         h = _vp()
         _check(_lib.conv_bwd_clip_create(n, (_i64 * max(n, 1))(*sizes), (_i32 * max(n, 1))(*codes), ctypes.byref(h)), "conv_bwd_clip_create")
         self._h = h.value
-        self._array = _vp * max(n, 1)
 
     @classmethod
     def like(cls, tensors):
@@ -235,13 +241,14 @@ class GradClip(_Plan):
         return cls([t.numel() for t in tensors], [t.dtype for t in tensors])
 
     def _pointers(self, tensors, what):
-        if [(t.numel(), t.dtype, t.is_cuda, t.is_contiguous()) for t in tensors] != self._want:
+        if (list(map(_numel, tensors)) != self._sizes or list(map(_type_device, tensors)) != self._types
+                or not all(map(_contiguous, tensors))):
             if len(tensors) != self.count:
                 raise ValueError(f"{what}: {self.count} tensors wanted, got {len(tensors)}")
-            for i, (t, want) in enumerate(zip(tensors, self._want)):
-                if (t.numel(), t.dtype, t.is_cuda, t.is_contiguous()) != want:
-                    raise ValueError(f"{what}[{i}]: a contiguous CUDA {want[1]} tensor of {want[0]} elements wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
-        return self._array(*[t.data_ptr() for t in tensors])
+            for i, t in enumerate(tensors):
+                if t.numel() != self._sizes[i] or _type_device(t) != self._types[i] or not t.is_contiguous():
+                    raise ValueError(f"{what}[{i}]: a contiguous CUDA {self._types[i][0]} tensor of {self._sizes[i]} elements wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return array.array("Q", map(_data_ptr, tensors))
 
     def _device(self, grads):
         return grads[0].device if grads else torch.device("cuda", torch.cuda.current_device())
@@ -251,7 +258,7 @@ class GradClip(_Plan):
         g = self._pointers(grads, "grads")
         device = self._device(grads)
         norm = _empty((1,), torch.float32, device, stream)
-        _check(_lib.conv_bwd_clip_norm(self._h, g, norm.data_ptr(), _stream(stream, device)), "conv_bwd_clip_norm")
+        _check(_lib.conv_bwd_clip_norm(self._h, g.buffer_info()[0], norm.data_ptr(), _stream(stream, device)), "conv_bwd_clip_norm")
         return norm
 
     def clip(self, grads, max_norm, out=None, stream=None):
@@ -263,7 +270,7 @@ class GradClip(_Plan):
         device = self._device(grads)
         both = _empty((2, 1), torch.float32, device, stream)
         at = both.data_ptr()
-        _check(_lib.conv_bwd_clip_run(self._h, g, o, max_norm, at, at + 4, _stream(stream, device)), "conv_bwd_clip_run")
+        _check(_lib.conv_bwd_clip_run(self._h, g.buffer_info()[0], o.buffer_info()[0], max_norm, at, at + 4, _stream(stream, device)), "conv_bwd_clip_run")
         return both.unbind(0)
 
 
