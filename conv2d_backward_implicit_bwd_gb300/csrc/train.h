@@ -56,7 +56,7 @@ cudaError_t launch_experts_stream(const ExpertStreamParams &p, int dir, int bt, 
 
 // Gradient clipping: the tensors are cut into chunks of kClipChunk bytes.
 constexpr int kClipChunk = 32768;
-constexpr int kClipBlocks = 6;     // blocks per SM
+constexpr int kNormBlocks = 3, kScaleBlocks = 2;  // blocks per SM
 constexpr int kClipPtrs = 1000;  // tensors per launch (their pointers travel as kernel parameters)
 struct __align__(16) ClipChunk {
     int64_t start;   // first element
@@ -67,7 +67,9 @@ struct __align__(16) ClipChunk {
 struct ClipParams {
     const ClipChunk *chunks;  // of this launch's tensors; at least one entry
     double *partials;        // one per block of every norm launch
-    uint32_t *ticket;
+    uint32_t *ticket, *turn;
+    int32_t *status;
+    int64_t wait_budget;
     float *norm, *coef;
     int32_t num_chunks;
     int32_t partial_base;    // first partial of this launch
@@ -78,6 +80,9 @@ struct ClipParams {
 // `g` and `o` (NULL for the norm): the launch's `tensors` pointers, on the host
 cudaError_t launch_clip_norm(const ClipParams &p, const void *const *g, int tensors, int grid, cudaStream_t s);
 cudaError_t launch_clip_scale(const ClipParams &p, const void *const *g, void *const *o, int tensors, int grid, cudaStream_t s);
+// norm and scaling in one launch of num_chunks blocks, at most clip_fused_blocks
+int clip_fused_blocks(int num_sms);
+cudaError_t launch_clip_fused(const ClipParams &p, const void *const *g, void *const *o, int tensors, cudaStream_t s);
 
 // Policy loss.
 enum : int { kPolForward = 0, kPolBackward = 1, kPolBoth = 2 };

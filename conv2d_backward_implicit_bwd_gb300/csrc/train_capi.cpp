@@ -170,6 +170,7 @@ struct conv_bwd_clip_plan_s {
     std::vector<Launch> launches;
     int32_t partial_total = 0;
     size_t off_chunks = 0;
+    int fused_blocks = 0;  // blocks of the one-launch kernel that are resident at once
     std::mutex mu;
     DevicePart dev;
 };
@@ -351,13 +352,17 @@ conv_bwd_status conv_bwd_clip_create(int32_t count, const int64_t *sizes, const 
             const size_t n = chunks.size() - l.chunk_off;
             if (n > 0x7fffffff) return CONV_BWD_ERR_UNSUPPORTED;
             l.chunks = (int32_t)n;
-            l.grid = (int32_t)std::max<int64_t>(1, std::min<int64_t>(l.chunks, (int64_t)sms * kClipBlocks));
+            l.grid = (int32_t)std::max<int64_t>(1, std::min<int64_t>(l.chunks, (int64_t)sms * kNormBlocks));
             l.partial_base = p.partial_total;
             p.partial_total += l.grid;
             p.launches.push_back(l);
         }
         chunks.push_back({0, 0, 0, 0});  // a launch without chunks still reads one entry
-        p.off_chunks = (64 + (size_t)p.partial_total * 8 + 15) / 16 * 16;
+        int cooperative = 0;
+        if (cudaDeviceGetAttribute(&cooperative, cudaDevAttrCooperativeLaunch, dev) == cudaSuccess && cooperative)
+            p.fused_blocks = clip_fused_blocks(sms);
+        cudaGetLastError();
+        p.off_chunks = (64 + (size_t)std::max(p.partial_total, p.fused_blocks) * 8 + 15) / 16 * 16;
         const conv_bwd_status st = p.dev.init(p.off_chunks + chunks.size() * sizeof(ClipChunk));
         if (st != CONV_BWD_OK || !p.dev.has_device) return st;
         if (cudaMemcpy(static_cast<char *>(p.dev.mem) + p.off_chunks, chunks.data(), chunks.size() * sizeof(ClipChunk),
@@ -397,7 +402,16 @@ static conv_bwd_status clip_launch(conv_bwd_clip_plan p, const void *const *grad
     cp.coef = coef;
     cp.want_coef = scale ? 1 : 0;
     cp.max_norm = max_norm;
+    cp.turn = p->dev.ticket() + 1;
+    cp.status = p->dev.status();
+    cp.wait_budget = (int64_t)p->dev.clock_khz * 2000;
     const size_t nl = p->launches.size();
+    // Gradients that fit the SMs' registers are read once.
+    if (scale && nl == 1 && p->launches[0].chunks > 0 && p->launches[0].chunks <= p->fused_blocks) {
+        cp.chunks = reinterpret_cast<const ClipChunk *>(m + p->off_chunks);
+        cp.num_chunks = p->launches[0].chunks;
+        return launch_clip_fused(cp, grads, outs, p->count, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
+    }
     for (int pass = 0; pass < (scale ? 2 : 1); ++pass)
         for (size_t k = 0; k < nl; ++k) {
             const auto &l = p->launches[pass ? nl - 1 - k : k];
@@ -407,7 +421,7 @@ static conv_bwd_status clip_launch(conv_bwd_clip_plan p, const void *const *grad
             cp.partial_total = k + 1 == nl ? p->partial_total : 0;
             if (pass && l.chunks == 0) continue;
             const void *const *g = grads + l.first;
-            const cudaError_t e = pass ? launch_clip_scale(cp, g, outs + l.first, l.tensors, l.grid, (cudaStream_t)stream)
+            const cudaError_t e = pass ? launch_clip_scale(cp, g, outs + l.first, l.tensors, std::min(l.chunks, p->dev.num_sms * kScaleBlocks), (cudaStream_t)stream)
                                        : launch_clip_norm(cp, g, l.tensors, l.grid, (cudaStream_t)stream);
             if (e != cudaSuccess) return CONV_BWD_ERR_CUDA;
         }
@@ -423,6 +437,11 @@ conv_bwd_status conv_bwd_clip_run(conv_bwd_clip_plan p, const void *const *grads
     Range range("conv_bwd_clip_run");
     if (!coef) return CONV_BWD_ERR_INVALID_ARG;
     return clip_launch(p, grads, out, max_norm, norm, coef, stream);
+}
+
+conv_bwd_status conv_bwd_clip_get_status(conv_bwd_clip_plan p, void *stream, int32_t *detail) {
+    if (!p) return CONV_BWD_ERR_INVALID_ARG;
+    return read_status(p->dev, stream, detail);
 }
 
 // ---- policy loss --------------------------------------------------------------

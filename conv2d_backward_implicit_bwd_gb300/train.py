@@ -27,7 +27,7 @@ _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.
 EXPORTED = [
     "conv_bwd_experts_create", "conv_bwd_experts_destroy", "conv_bwd_experts_forward", "conv_bwd_experts_data",
     "conv_bwd_experts_weight", "conv_bwd_experts_get_status", "conv_bwd_clip_create", "conv_bwd_clip_destroy",
-    "conv_bwd_clip_norm", "conv_bwd_clip_run", "conv_bwd_policy_create", "conv_bwd_policy_destroy",
+    "conv_bwd_clip_norm", "conv_bwd_clip_run", "conv_bwd_clip_get_status", "conv_bwd_policy_create", "conv_bwd_policy_destroy",
     "conv_bwd_policy_forward", "conv_bwd_policy_backward", "conv_bwd_policy_forward_backward",
     "conv_bwd_policy_get_status",
 ]
@@ -56,6 +56,7 @@ def _declare():
         "conv_bwd_clip_destroy": [_vp],
         "conv_bwd_clip_norm": [_vp, _vp, _vp, _vp],
         "conv_bwd_clip_run": [_vp, _vp, _vp, _f32, _vp, _vp, _vp],
+        "conv_bwd_clip_get_status": [_vp, _vp, P(_i32)],
         "conv_bwd_policy_create": [P(PolicyDesc), P(_vp)],
         "conv_bwd_policy_destroy": [_vp],
         "conv_bwd_policy_forward": [_vp, _i64, _vp, _i64] + [_vp] * 10,
@@ -273,6 +274,10 @@ class GradClip(_Plan):
         _check(_lib.conv_bwd_clip_run(self._h, g.buffer_info()[0], o.buffer_info()[0], max_norm, at, at + 4, _stream(stream, device)), "conv_bwd_clip_run")
         return both.unbind(0)
 
+    def status(self, stream=None):
+        """(status, detail) of the calls since the last one; synchronises the stream."""
+        return _status(_lib.conv_bwd_clip_get_status, self._h, stream)
+
 
 class PolicyLoss(_Plan):
     """Clipped policy loss with a KL term, from logits.
@@ -310,11 +315,11 @@ class PolicyLoss(_Plan):
         """(loss [1], logp, lse, coef [tokens]); lse and coef are what ``backward`` needs."""
         t, args = self._inputs(logits, actions, advantage, weight, old_logp, ref_logp)
         device = logits.device
-        rows = _empty((3, t), torch.float32, device, stream)
-        loss = _empty((1,), torch.float32, device, stream)
-        at = rows.data_ptr()
-        _check(_lib.conv_bwd_policy_forward(*args, loss.data_ptr(), at, at + 4 * t, at + 8 * t, _stream(stream, device)), "conv_bwd_policy_forward")
-        return loss, *rows.unbind(0)
+        s = _empty((3 * t + 1,), torch.float32, device, stream)
+        at = s.data_ptr()
+        _check(_lib.conv_bwd_policy_forward(*args, at + 12 * t, at, at + 4 * t, at + 8 * t, _stream(stream, device)), "conv_bwd_policy_forward")
+        logp, lse, coef, loss = s.split((t, t, t, 1))
+        return loss, logp, lse, coef
 
     def backward(self, logits, actions, lse, coef, grad=None, out=None, stream=None):
         """dlogits from the forward's lse and coef; ``grad`` [1] is the loss's upstream gradient; ``out`` may be logits."""

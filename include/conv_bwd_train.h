@@ -121,6 +121,8 @@ conv_bwd_status conv_bwd_clip_norm(conv_bwd_clip_plan plan, const void *const *g
 conv_bwd_status conv_bwd_clip_run(conv_bwd_clip_plan plan, const void *const *grads, void *const *out, float max_norm,
                                   float *norm, float *coef, void *stream);
 
+conv_bwd_status conv_bwd_clip_get_status(conv_bwd_clip_plan plan, void *stream, int32_t *detail);
+
 /* ---- clipped policy loss with a KL term -------------------------------------
  *
  * Per token t with logits row z_t [vocab], chosen token a_t:

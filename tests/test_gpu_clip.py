@@ -65,7 +65,7 @@ def check_clip(T, grads, max_norm, inplace, out_shift=0):
     ([1], ["f32"]), ([1], ["bf16"]), ([0, 5, 0], ["f32", "bf16", "bf16"]),
     ([8192, 8193, 16384, 16385, 3], ["f32", "f32", "bf16", "bf16", "f32"]),
     ([100_000, 7, 250_001, 64], ["bf16", "f32", "f32", "bf16"]),
-    ([3_000_017], ["bf16"]), ([1_500_003], ["f32"]),
+    ([3_000_017], ["bf16"]), ([1_500_003], ["f32"]), ([9_000_001, 5, 4_000_003], ["bf16", "f32", "f32"]),
 ])
 def test_norm_and_clip(T, sizes, dtypes, inplace):
     check_clip(T, tensors(sizes, dtypes), 0.5, inplace)
@@ -75,6 +75,12 @@ def test_norm_and_clip(T, sizes, dtypes, inplace):
 @pytest.mark.parametrize("inplace", [True, False])
 def test_any_alignment(T, shift, out_shift, inplace):
     check_clip(T, tensors([9000, 17, 40_000, 1], ["f32", "bf16", "bf16", "f32"], shift=shift), 2.0, inplace, out_shift)
+
+
+@pytest.mark.parametrize("out_shift", [0, 1])
+def test_any_alignment_large(T, out_shift):
+    """More than the SMs' registers hold: the norm and the scaling in launches of their own."""
+    check_clip(T, tensors([7_000_003, 3_000_001], ["bf16", "f32"], shift=3), 2.0, False, out_shift)
 
 
 def test_many_tensors(T):
