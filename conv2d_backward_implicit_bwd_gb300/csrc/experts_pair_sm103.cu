@@ -210,6 +210,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
     }
+    pdl_next();
+    pdl_wait();
     if (warp == 9)
         build_expert_table<WIDE>(tab, p.offsets, p.experts, p.rows, DIR == kExpWeight ? mt * ((p.K + WIDE - 1) / WIDE) : mt,
                                  DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesEach,
@@ -521,8 +523,7 @@ cudaError_t launch_dir(const ExpertPairParams &p, int grid, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    experts_pair_kernel<DIR><<<grid, THREADS, SMEM, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(experts_pair_kernel<DIR>, grid, THREADS, SMEM, s, p);
 }
 
 }  // namespace

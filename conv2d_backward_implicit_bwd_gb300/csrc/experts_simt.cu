@@ -56,6 +56,8 @@ __global__ void __launch_bounds__(NT) experts_simt_kernel(const ExpertSimtParams
     __shared__ __align__(16) float sb[BL][BT + 4];
     const int cols = DIR == kExpForward ? p.N : p.K;
     const int n_tiles = (cols + BT - 1) / BT, m_tiles = (p.N + BT - 1) / BT;  // m_tiles: weight only
+    pdl_next();
+    pdl_wait();
     if (threadIdx.x < 32)
         build_expert_table<BT>(tab, p.offsets, p.experts, p.rows, DIR == kExpWeight ? m_tiles * n_tiles : n_tiles,
                                DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesEach,
@@ -138,13 +140,9 @@ __global__ void __launch_bounds__(NT) experts_simt_kernel(const ExpertSimtParams
 
 template <typename T>
 cudaError_t launch_dir(const ExpertSimtParams &p, int dir, int grid, cudaStream_t s) {
-    if (dir == kExpForward)
-        experts_simt_kernel<T, T, kExpForward><<<grid, NT, 0, s>>>(p);
-    else if (dir == kExpData)
-        experts_simt_kernel<T, T, kExpData><<<grid, NT, 0, s>>>(p);
-    else
-        experts_simt_kernel<T, float, kExpWeight><<<grid, NT, 0, s>>>(p);
-    return cudaGetLastError();
+    if (dir == kExpForward) return launch_early(experts_simt_kernel<T, T, kExpForward>, grid, NT, 0, s, p);
+    if (dir == kExpData) return launch_early(experts_simt_kernel<T, T, kExpData>, grid, NT, 0, s, p);
+    return launch_early(experts_simt_kernel<T, float, kExpWeight>, grid, NT, 0, s, p);
 }
 
 }  // namespace

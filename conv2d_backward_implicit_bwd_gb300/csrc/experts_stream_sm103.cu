@@ -134,6 +134,8 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
     }
+    pdl_next();
+    pdl_wait();
     if (warp == 7) build_expert_table<BT>(tab, p.offsets, p.experts, p.rows, mt, kTilesByRows, blockIdx.x == 0 ? p.status : nullptr);
     __syncthreads();
     tc_fence_after();
@@ -359,8 +361,7 @@ cudaError_t launch_bt(const ExpertStreamParams &p, int grid, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    experts_stream_kernel<DIR, BT><<<grid, THREADS, Cfg<BT>::SMEM, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(experts_stream_kernel<DIR, BT>, grid, THREADS, Cfg<BT>::SMEM, s, p);
 }
 
 }  // namespace

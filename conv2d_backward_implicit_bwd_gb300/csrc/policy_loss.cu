@@ -267,6 +267,8 @@ __global__ void __launch_bounds__(NT) policy_warp_kernel(const PolicyParams p) {
     const float c = p.scale * kLog2e;
     double loss = 0.0;
 
+    pdl_next();
+    pdl_wait();
     const int64_t step = (int64_t)gridDim.x * ROWS;
     RowIn next = {};
     if (p.tokens > 0) next = row_in<MODE>(p, min((int64_t)blockIdx.x * ROWS + sub, (int64_t)p.tokens - 1));
@@ -422,6 +424,8 @@ __global__ void __launch_bounds__(WORKERS + 32, RING_BLOCKS) policy_ring_kernel(
         abort_ = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    pdl_next();
+    pdl_wait();
     __syncthreads();
     double loss = 0.0;
     if (warp == WORKERS / 32) {
@@ -614,13 +618,9 @@ template <typename T>
 cudaError_t launch_warp(const PolicyParams &p, int mode, int num_sms, cudaStream_t s) {
     const int64_t need = (p.tokens + NT / 32 - 1) / (NT / 32);
     const int grid = (int)(need < 1 ? 1 : need < policy_max_blocks(num_sms) ? need : policy_max_blocks(num_sms));
-    if (mode == kPolForward)
-        policy_warp_kernel<T, kPolForward><<<grid, NT, 0, s>>>(p);
-    else if (mode == kPolBackward)
-        policy_warp_kernel<T, kPolBackward><<<grid, NT, 0, s>>>(p);
-    else
-        policy_warp_kernel<T, kPolBoth><<<grid, NT, 0, s>>>(p);
-    return cudaGetLastError();
+    if (mode == kPolForward) return launch_early(policy_warp_kernel<T, kPolForward>, grid, NT, 0, s, p);
+    if (mode == kPolBackward) return launch_early(policy_warp_kernel<T, kPolBackward>, grid, NT, 0, s, p);
+    return launch_early(policy_warp_kernel<T, kPolBoth>, grid, NT, 0, s, p);
 }
 template <typename T, int MODE>
 cudaError_t launch_ring_mode(const PolicyParams &p, int num_sms, cudaStream_t s) {
@@ -637,8 +637,7 @@ cudaError_t launch_ring_mode(const PolicyParams &p, int num_sms, cudaStream_t s)
         const int64_t rows = (64LL << 20) / ((int64_t)p.vocab * (int64_t)sizeof(T));
         if (rows < grid) grid = rows > num_sms ? (int)rows : num_sms;
     }
-    policy_ring_kernel<T, MODE><<<p.tokens < grid ? p.tokens : grid, WORKERS + 32, kRingSmem, s>>>(p);
-    return cudaGetLastError();
+    return launch_early(policy_ring_kernel<T, MODE>, p.tokens < grid ? p.tokens : grid, WORKERS + 32, kRingSmem, s, p);
 }
 template <typename T>
 cudaError_t launch_ring(const PolicyParams &p, int mode, int num_sms, cudaStream_t s) {

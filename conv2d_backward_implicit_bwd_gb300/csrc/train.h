@@ -7,6 +7,30 @@
 
 namespace cbd {
 
+// Launch that may begin while the kernel before it in the stream still runs: the
+// kernel sets itself up (barriers, tensor memory) and then waits in pdl_wait()
+// before it touches global memory.
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*kernel)(P...), int grid, int block, size_t smem, cudaStream_t s, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#ifdef __CUDACC__
+// every thread: the kernels before this one are done and their writes visible
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// the next kernel may set itself up
+__device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+
 constexpr int kMaxExperts = 1024;  // the expert tables of a launch live in shared memory
 
 enum : int { kExpForward = 0, kExpData = 1, kExpWeight = 2 };

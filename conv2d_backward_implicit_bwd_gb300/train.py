@@ -12,7 +12,6 @@ from __future__ import annotations
 
 import array
 import ctypes
-import math
 import operator
 
 import torch
@@ -106,11 +105,6 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
 def _rows(t, width, dtype, what):
     """Checks a matrix of rows with unit column stride; returns (rows, row stride)."""
     shape = t.shape
@@ -179,7 +173,8 @@ class Experts(_Plan):
             ldo = wo
         else:
             r, ldo = _rows(out, wo, self.dtype, "out")
-            _need(r == rows, f"out: {rows} rows wanted, got {r}")
+            if r != rows:
+                raise ValueError(f"out: {rows} rows wanted, got {r}")
         st = call(self._h, rows, a.data_ptr(), lda, w.data_ptr(), off, out.data_ptr(), ldo, _stream(stream, device))
         if st != OK:
             raise ConvBwdError(st, name)
@@ -197,10 +192,12 @@ class Experts(_Plan):
         """dw[e] = sum of dy[i] x[i]^T over the rows of e, in fp32 [experts, n, k]; added to ``out`` with ``accumulate``."""
         rows, lddy = _rows(dy, self.n, self.dtype, "dy")
         r, ldx = _rows(x, self.k, self.dtype, "x")
-        _need(r == rows, f"x: {rows} rows wanted as in dy, got {r}")
+        if r != rows:
+            raise ValueError(f"x: {rows} rows wanted as in dy, got {r}")
         off = _vector(offsets, self.experts + 1, torch.int32, "offsets")
         if out is None:
-            _need(not accumulate, "accumulate wants the gradients to add to in out")
+            if accumulate:
+                raise ValueError("accumulate wants the gradients to add to in out")
             out = _empty(self._shape, torch.float32, dy.device, stream)
         elif out.dtype != torch.float32 or out.shape != self._shape or not out.is_contiguous() or not out.is_cuda:
             raise ValueError(f"out: a contiguous CUDA fp32 tensor {list(self._shape)} wanted, got {out.dtype} {tuple(out.shape)}")
@@ -229,7 +226,8 @@ class GradClip(_Plan):
     def __init__(self, sizes, dtypes):
         sizes = [int(n) for n in sizes]
         codes = [_dtype(d) for d in dtypes]
-        _need(len(sizes) == len(codes), f"{len(sizes)} sizes and {len(codes)} dtypes")
+        if len(sizes) != len(codes):
+            raise ValueError(f"{len(sizes)} sizes and {len(codes)} dtypes")
         self._sizes, self._types = sizes, [(_TORCH[c], True) for c in codes]
         self.count = n = len(sizes)
         h = _vp()
@@ -265,7 +263,8 @@ class GradClip(_Plan):
     def clip(self, grads, max_norm, out=None, stream=None):
         """Scales ``grads`` by coef = min(1, max_norm / (norm + 1e-6)), in place or into ``out``; returns (norm, coef)."""
         max_norm = float(max_norm)
-        _need(not math.isnan(max_norm) and max_norm >= 0, f"max_norm {max_norm}: a number >= 0 wanted")
+        if not max_norm >= 0:
+            raise ValueError(f"max_norm {max_norm}: a number >= 0 wanted")
         g = self._pointers(grads, "grads")
         o = g if out is None else self._pointers(out, "out")
         device = self._device(grads)
@@ -308,7 +307,8 @@ class PolicyLoss(_Plan):
         if out is None:
             return _empty((t, self.vocab), self.dtype, logits.device, stream), self.vocab
         r, ld = _rows(out, self.vocab, self.dtype, "out")
-        _need(r == t, f"out: {t} rows wanted, got {r}")
+        if r != t:
+            raise ValueError(f"out: {t} rows wanted, got {r}")
         return out, ld
 
     def forward(self, logits, actions, advantage, weight, old_logp=None, ref_logp=None, stream=None):
