@@ -25,10 +25,12 @@
 //
 // Ragged ends.  Rows past an expert's end that a box brings along are other
 // columns of D (forward, data), never stored.  For weight they would be
-// summed: the last block multiplies only its valid 16-row steps, and where the
+// summed: the partial block multiplies only its valid 16-row steps, and where the
 // last step is partial a helper warp of each CTA zeroes its rows in shared
 // memory after they have landed (both operands: 0 x NaN is NaN) before the MMA
-// may read them.
+// may read them.  That block is the first of its tile, so that the zeroing runs
+// while the MMAs still work on the tile before (as the last one it cost 1.3 us a
+// tile).
 //
 // Schedule.  Pair b of P takes tiles b, 2P - 1 - b, 2P + b, ... (back and forth,
 // so that a fall or rise of the tiles' cost along the experts evens out).  One
@@ -36,9 +38,15 @@
 // (Drawing tiles from a counter in falling cost order was no faster: the
 // hand-over between the two CTAs took 0.65 us of every role's time per tile.)
 //
-// Roles per CTA: warps 0-3 epilogue, 4 A loads, 5 MMA (leader CTA) and TMEM,
-// 6-7 B loads, 8 helper (weight: last blocks; else rows of no expert), 9 schedule.  Every wait is
-// bounded.
+// Precision of weight.  The tensor core's accumulator truncates: over r rows the
+// sum loses about r 2^-30 of itself (1.2e-6 measured at 1024 rows).  So weight
+// starts a new accumulator every 256 rows and its epilogue adds those in fp32
+// registers, which holds the error below 5e-7 for any number of rows; the add
+// runs under the other accumulator's MMAs.
+//
+// Roles per CTA, in warps: epilogue 4 (weight 8, with most of the registers), A
+// loads 1, MMA (leader CTA) and TMEM 1, B loads 2, helper 1 (weight: partial
+// blocks; else rows of no expert), schedule 1.  Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -53,25 +61,33 @@ namespace cbd {
 
 namespace {
 
-constexpr int S = 6;     // pipeline stages
 constexpr int RING = 4;  // tiles between the schedule and its readers
 constexpr int WIDE = 256;
 constexpr int A_BYTES = 128 * 64 * 2;
 constexpr int B_BYTES = 128 * 64 * 2;  // one CTA's half of the tile's columns
-constexpr int OUT_BYTES = 16384;       // epilogue staging
-constexpr int THREADS = 10 * 32;
+constexpr int SEGMENT = 8;             // weight: k-blocks (of 64 rows) of one accumulator
+constexpr int MAX_STAGES = 6;
 
 struct Bars {
     ExpertRing<RING> ring;
-    uint64_t full[S], empty[S];
-    uint64_t tail[S], peer[S];  // weight: last blocks landed in this CTA; peer's rows zeroed
+    uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+    uint64_t tail[MAX_STAGES], peer[MAX_STAGES];  // weight: partial blocks landed in this CTA; peer's rows zeroed
     uint64_t tfull[2], tempty[2];
     int32_t vote[8];  // forward, data: what each epilogue warp drew, two tiles in turn
     uint32_t tmem;
     int32_t abort;
 };
-constexpr int SMEM = 1024 + S * (A_BYTES + B_BYTES) + OUT_BYTES + (int)sizeof(ExpertTable) + 8 + (int)sizeof(Bars);
-static_assert(SMEM <= 232448, "shared memory of one CTA");
+template <int DIR>
+struct Cfg {
+    static constexpr bool W = DIR == kExpWeight;
+    static constexpr int S = W ? 5 : 6;                  // pipeline stages
+    static constexpr int OUT_BYTES = W ? 32768 : 16384;  // epilogue staging
+    static constexpr int EPI = W ? 8 : 4;                // epilogue warps 0 .. EPI - 1
+    static constexpr int LOAD_A = EPI, MMA = EPI + 1, LOAD_B = EPI + 2, HELP = EPI + 4, SCHED = EPI + 5;
+    static constexpr int THREADS = W ? 512 : 320;  // weight: two warpgroups of epilogue, two of the others
+    static constexpr int SMEM = 1024 + S * (A_BYTES + B_BYTES) + OUT_BYTES + (int)sizeof(ExpertTable) + 8 + (int)sizeof(Bars);
+    static_assert(SMEM <= 232448, "shared memory of one CTA");
+};
 
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
     asm volatile(
@@ -167,13 +183,15 @@ __device__ __forceinline__ ExpertWork decode(const ExpertPairParams &p, const Ex
 }
 
 template <int DIR>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_pair_kernel(const __grid_constant__ ExpertPairParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1) experts_pair_kernel(const __grid_constant__ ExpertPairParams p) {
+    using C = Cfg<DIR>;
+    constexpr int S = C::S;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sA = smem, *sB = smem + S * A_BYTES;
     uint8_t *stage = sB + S * B_BYTES;
-    Bars &bars = *reinterpret_cast<Bars *>(stage + OUT_BYTES);
-    ExpertTable &tab = *reinterpret_cast<ExpertTable *>(stage + OUT_BYTES + (sizeof(Bars) + 7) / 8 * 8);
+    Bars &bars = *reinterpret_cast<Bars *>(stage + C::OUT_BYTES);
+    ExpertTable &tab = *reinterpret_cast<ExpertTable *>(stage + C::OUT_BYTES + (sizeof(Bars) + 7) / 8 * 8);
     volatile int32_t *abort_flag = &bars.abort;
 
     const uint32_t rank = cluster_ctarank();
@@ -194,25 +212,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
-            mbar_init(tempty0 + 8 * b, 8);  // 4 epilogue warps of each CTA
+            mbar_init(tempty0 + 8 * b, 2 * C::EPI);  // epilogue warps of both CTAs
         }
-        // loads (3), epilogue (4), the leader's MMA, weight's helper
-        bars.ring.init(7 + (leader ? 1 : 0) + (DIR == kExpWeight ? 1 : 0));
+        // loads (3), epilogue, the leader's MMA, weight's helper
+        bars.ring.init(3 + C::EPI + (leader ? 1 : 0) + (DIR == kExpWeight ? 1 : 0));
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
     }
-    if (warp == 5) {
+    if (warp == C::MMA) {
         tmem_alloc2(smem_u32(&bars.tmem), 512);
         tc_fence_before();
     }
-    if (warp == 4 && lane == 0) {
+    if (warp == C::LOAD_A && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
     }
     pdl_next();
     pdl_wait();
-    if (warp == 9)
+    if (warp == C::SCHED)
         build_expert_table<WIDE>(tab, p.offsets, p.experts, p.rows, DIR == kExpWeight ? mt * ((p.K + WIDE - 1) / WIDE) : mt,
                                  DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesEach,
                                  blockIdx.x == 0 ? p.status : nullptr);
@@ -224,183 +242,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
         if (ld_shared_cluster_u32(mapa_shared(smem_u32(&bars.tmem), 0)) != tmem_base) record_status(p.status, kDevFaultIndex);
     }
 
-    if (warp == 9) {
-        // ------------------------------------------------------------ schedule
-        if (lane == 0) {
-            const int total = tab.tile[p.experts];
-            for (uint32_t i = 0;; ++i) {
-                const int t = (int)i * npairs + ((i & 1) ? npairs - 1 - pair : pair);
-                ExpertWork w;
-                w.n = 0;
-                // (the last round may be short: a pair beyond it has nothing there and nothing after)
-                if (t < total) w = decode<DIR>(p, tab, mt, t);
-                if (!bars.ring.give(i, w, p.wait_budget, abort_flag, p.status) || w.n == 0) break;
-            }
-        }
-        __syncwarp();
-    } else if (warp == 4 || warp == 6 || warp == 7) {
-        // ------------------------------------------------------------ loads
-        if (lane == 0) {
-            const uint32_t full_leader0 = mapa_shared(full0, 0);
-            uint32_t it = 0;
-            bool ok = true, issued = false;
-            for (uint32_t i = 0; ok; ++i) {
-                const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
-                if (w.n == 0) break;
-                bars.ring.done(i);
-                // B columns of this CTA in boxes of 64, one for each B warp
-                const int half = w.n / 2, boxes = (half + 63) / 64, q = warp - 6;
-                const uint32_t bytes = (uint32_t)A_BYTES + 8192u * (uint32_t)boxes;  // of one CTA
-                const int at = (int)rank * half + 64 * q;
-                for (int kb = 0; kb < w.kb1; ++kb, ++it) {
-                    const uint32_t s = it % S, ph = (it / S) & 1;
-                    if (!mbar_wait_bounded(empty0 + 8 * s, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) {
-                        ok = false;
-                        break;
-                    }
-                    // weight: a partial last step goes through the helper warp, on this CTA's own barrier
-                    const bool fix = DIR == kExpWeight && kb == w.kb1 - 1 && (w.last & 15) != 0;
-                    const uint32_t bar = fix ? tail0 + 8 * s : full_leader0 + 8 * s;
-                    if (warp == 4) {
-                        if (fix)
-                            mbar_arrive_expect_tx(tail0 + 8 * s, bytes);
-                        else if (leader)
-                            mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
-                        const uint32_t dst = smem_u32(sA + s * A_BYTES);
-                        const int m = w.m0 + (int)rank * 128;
-                        if constexpr (DIR == kExpForward) {
-                            tma_load_3d_pair(dst, &p.a, bar, kb * 64, m, w.e);
-                        } else if constexpr (DIR == kExpData) {
-                            tma_load_3d_pair(dst, &p.a, bar, m, kb * 64, w.e);
-                            tma_load_3d_pair(dst + 8192, &p.a, bar, m + 64, kb * 64, w.e);
-                        } else {
-                            for (int b = 0; b < 2; ++b)
-                                if (fix)
-                                    tma_load_2d(dst + 8192 * b, &p.a, bar, m + 64 * b, w.row0 + kb * 64);
-                                else
-                                    tma_load_2d_pair(dst + 8192 * b, &p.a, bar, m + 64 * b, w.row0 + kb * 64);
-                        }
-                        issued = true;
-                    } else if (q < boxes) {
-                        const uint32_t dst = smem_u32(sB + s * B_BYTES + 8192 * q);
-                        if constexpr (DIR == kExpWeight) {
-                            if (fix)
-                                tma_load_2d(dst, &p.b, bar, w.ntok + at, w.row0 + kb * 64);
-                            else
-                                tma_load_2d_pair(dst, &p.b, bar, w.ntok + at, w.row0 + kb * 64);
-                        } else {
-                            tma_load_2d_pair(dst, &p.b, bar, kb * 64, w.row0 + at);
-                        }
-                        issued = true;
-                    }
-                }
-            }
-            if (!ok && issued) {
-                for (int q = 0; q < 100; ++q) __nanosleep(1000);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 5) {
-        // ------------------------------------------------------------ MMA (leader)
-        if (leader) {
-            constexpr bool A_K = DIR == kExpForward, B_K = DIR != kExpWeight;
-            constexpr uint32_t A_STEP = A_K ? 2 : 128, B_STEP = B_K ? 2 : 128;  // a 16-deep step, in 16 bytes
-            const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((A_K ? 0u : 1u) << 15) | ((B_K ? 0u : 1u) << 16) | ((uint32_t)(256 >> 4) << 24);
-            const uint64_t a_desc0 = smem_desc_sw128(smem_u32(sA), A_K ? 16 : 8192, 1024);
-            const uint64_t b_desc0 = smem_desc_sw128(smem_u32(sB), B_K ? 16 : 8192, 1024);
-            const uint32_t a_lo = (uint32_t)a_desc0, a_hi = (uint32_t)(a_desc0 >> 32), b_lo = (uint32_t)b_desc0, b_hi = (uint32_t)(b_desc0 >> 32);
-            uint32_t s = 0, ph = 0, use = 0;  // stage and its phase, accumulators used so far
-            bool ok = true, issued = false;
-            for (uint32_t i = 0; ok; ++i) {
-                ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutMma);
-                w.n = __shfl_sync(0xffffffffu, w.n, 0);
-                w.kb1 = __shfl_sync(0xffffffffu, w.kb1, 0);
-                w.last = __shfl_sync(0xffffffffu, w.last, 0);
-                if (w.n == 0) break;
-                if (lane == 0) bars.ring.done(i);
-                if (w.kb1 == 0) continue;
-                const uint32_t b = use & 1, bph = (use >> 1) & 1;
-                ++use;
-                ok = mbar_wait_bounded(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t id = idesc0 | ((uint32_t)(w.n >> 3) << 17), d = tmem_base + b * 256;
-                uint32_t acc = 0;
-                for (int left = w.kb1; left > 0; --left) {
-                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma))) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t ad = a_lo + s * (A_BYTES >> 4), bd = b_lo + s * (B_BYTES >> 4);
-                    const int n = DIR == kExpWeight && left == 1 ? (w.last + 15) / 16 : 4;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        if (kk < n) mma_pair_elect(d, ad + A_STEP * kk, a_hi, bd + B_STEP * kk, b_hi, id, acc);
-                        acc = 1;
-                    }
-                    issued = true;
-                    commit_pair_elect(empty0 + 8 * s);
-                    if (++s == S) {
-                        s = 0;
-                        ph ^= 1;
-                    }
-                }
-                if (ok) commit_pair_elect(tfull0 + 8 * b);
-            }
-            if (!ok && issued) {
-                for (int q = 0; q < 100; ++q) __nanosleep(1000);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 8) {
-        // ------------------------------------------------------------ helper: rows past an expert's end, rows of none
-        if constexpr (DIR == kExpWeight) {
-            uint32_t it = 0, phase = 0;  // bit s: parity of the next use of tail[s] and peer[s]
-            for (uint32_t i = 0;; ++i) {
-                const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
-                if (!__all_sync(0xffffffffu, w.n != 0)) break;
-                if (lane == 0) bars.ring.done(i);
-                it += (uint32_t)w.kb1;
-                if (w.kb1 == 0 || (w.last & 15) == 0) continue;
-                const uint32_t s = (it - 1) % S, ph = (phase >> s) & 1;
-                phase ^= 1u << s;
-                bool ok = mbar_wait_bounded(tail0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                // rows [last, next multiple of 16) of each 64 x 64 block: whole 128-byte lines, so the swizzle
-                // within a line does not matter
-                const int lo = w.last, n = ((lo + 15) & ~15) - lo;
-                for (int j = lane; j < 4 * n * 8; j += 32) {
-                    const int blk = j / (n * 8), r = j / 8 % n, c = j % 8;
-                    uint8_t *base = blk < 2 ? sA + s * A_BYTES + blk * 8192 : sB + s * B_BYTES + (blk - 2) * 8192;
-                    *reinterpret_cast<uint4 *>(base + (lo + r) * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    if (!leader) {
-                        mbar_arrive_remote(mapa_shared(peer0 + 8 * s, 0));
-                    } else {
-                        ok = wait_cluster(peer0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
-                        if (ok) mbar_arrive(full0 + 8 * s);
-                    }
-                }
-                if (!__all_sync(0xffffffffu, ok)) break;
-            }
-        } else {
-            // forward, data: rows of no expert get zeros (16-byte stores; the width is a multiple of 8)
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
-            const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
-            const int64_t nfill = (int64_t)lo + (p.rows - hi);
-            for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
-                uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
-                for (int c = lane; c < vec; c += 32) row[c] = make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
-    } else {
+    // weight: 128 registers a thread at launch (512 threads), 192 for the epilogue with its sums, 64 for the others
+    if (warp < C::EPI) {
+        if constexpr (DIR == kExpWeight) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         // ------------------------------------------------------------ epilogue (both CTAs)
         const uint32_t tempty_leader0 = mapa_shared(tempty0, 0);
-        const uint32_t lane_base = tmem_base + ((uint32_t)(warp * 32) << 16);
+        const uint32_t lane_base = tmem_base + ((uint32_t)((warp % 4) * 32) << 16);
         uint32_t use = 0, buf = 0;
         bool ok = true;
         for (uint32_t i = 0;; ++i) {
@@ -416,53 +263,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
             }
             if (!more) break;
             const int m = w.m0 + (int)rank * 128;
-            const uint32_t b = use & 1;
-            if (w.kb1 > 0) {
-                // after a wait that ran out the warps go on meeting at their barriers, storing nothing
-                if (ok) ok = mbar_wait_bounded(tfull0 + 8 * b, (use >> 1) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
-                ok = __all_sync(0xffffffffu, ok);
-                tc_fence_after();
-                ++use;
-            }
-            const uint32_t acc = lane_base + b * 256;
             if constexpr (DIR == kExpWeight) {
-                // 32 x 32 fp32 pieces (a warp's rows, 128 bytes each) through swizzled staging and TMA stores,
-                // added in L2 when accumulating: one writer per element, so the order is fixed
-                const int mrow = m + warp * 32;
-                uint8_t *slab = stage + warp * 4096;
-#pragma unroll 1
-                for (int g = 0; g < WIDE / 32; ++g) {
-                    uint32_t v[32];
-                    if (w.kb1 > 0) {
-                        tmem_ld32(acc + g * 32, v);
-                    } else {
+                // this warp's 32 rows x 128 columns, summed over the accumulators in registers
+                constexpr int COLS = WIDE / 2;
+                const int mrow = m + (warp % 4) * 32, col0 = (warp / 4) * COLS;
+                float sum[COLS];
 #pragma unroll
-                        for (int q = 0; q < 32; ++q) v[q] = 0u;
+                for (int q = 0; q < COLS; ++q) sum[q] = 0.f;
+                for (int left = w.kb1; left > 0; left -= SEGMENT, ++use) {
+                    const uint32_t b = use & 1;
+                    if (ok) ok = mbar_wait_bounded(tfull0 + 8 * b, (use >> 1) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
+                    ok = __all_sync(0xffffffffu, ok);
+                    tc_fence_after();
+#pragma unroll
+                    for (int g = 0; g < COLS / 16; ++g) {
+                        uint32_t v[16];
+                        tmem_ld16(lane_base + b * 256 + col0 + g * 16, v);
+#pragma unroll
+                        for (int q = 0; q < 16; ++q) sum[g * 16 + q] += __uint_as_float(v[q]);
                     }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8 * b);
+                }
+                // 32 x 32 pieces (128 bytes of a row) through swizzled staging and TMA stores, added in L2 when
+                // accumulating: one writer per element, so the order is fixed
+                uint8_t *slab = stage + warp * 4096;
+#pragma unroll
+                for (int g = 0; g < COLS / 32; ++g) {
+                    const int col = w.ntok + col0 + g * 32;
                     if (lane == 0) bulk_wait_read();
                     __syncwarp();
                     const uint32_t sb = smem_u32(slab) + (uint32_t)lane * 128u;
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sb + (((uint32_t)q ^ (lane & 7)) << 4)),
-                                     "r"(v[4 * q]), "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(sb + (((uint32_t)q ^ (lane & 7)) << 4)),
+                                     "f"(sum[g * 32 + 4 * q]), "f"(sum[g * 32 + 4 * q + 1]), "f"(sum[g * 32 + 4 * q + 2]), "f"(sum[g * 32 + 4 * q + 3])
                                      : "memory");
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (ok && lane == 0 && mrow < p.N && w.ntok + g * 32 < p.K) {
+                    if (ok && lane == 0 && mrow < p.N && col < p.K) {
                         const uint64_t map = reinterpret_cast<uint64_t>(&p.o);
                         if (p.accumulate)
                             asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-                                         "r"(w.ntok + g * 32), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
+                                         "r"(col), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
                                          : "memory");
                         else
                             asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map),
-                                         "r"(w.ntok + g * 32), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
+                                         "r"(col), "r"(mrow), "r"(w.e), "r"(smem_u32(slab))
                                          : "memory");
                         bulk_commit();
                     }
                 }
             } else {
+                const uint32_t b = use & 1, acc = lane_base + b * 256;
+                // after a wait that ran out the warps go on meeting at their barriers, storing nothing
+                if (ok) ok = mbar_wait_bounded(tfull0 + 8 * b, (use >> 1) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                ++use;
                 // columns of the accumulator are rows of the output: 32 of them at a time are turned around in
                 // shared memory ([row][128 of the M dimension], 256 bytes) and leave in 16-byte stores, two
                 // whole row segments to an instruction.  (A bulk copy per row took 95 clocks each: 25 us for
@@ -495,19 +354,199 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) experts_
                         if (ok && col_ok && g + r < w.ntok) *reinterpret_cast<uint4 *>(dst + (int64_t)(g + r) * p.ldo) = x;
                     }
                 }
-            }
-            if (w.kb1 > 0) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8 * b);
             }
         }
         if constexpr (DIR == kExpWeight) bulk_wait_all();
+    } else {
+        if constexpr (DIR == kExpWeight) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == C::SCHED) {
+            // ------------------------------------------------------------ schedule
+            if (lane == 0) {
+                const int total = tab.tile[p.experts];
+                for (uint32_t i = 0;; ++i) {
+                    const int t = (int)i * npairs + ((i & 1) ? npairs - 1 - pair : pair);
+                    ExpertWork w;
+                    w.n = 0;
+                    // (the last round may be short: a pair beyond it has nothing there and nothing after)
+                    if (t < total) w = decode<DIR>(p, tab, mt, t);
+                    if (!bars.ring.give(i, w, p.wait_budget, abort_flag, p.status) || w.n == 0) break;
+                }
+            }
+            __syncwarp();
+        } else if (warp == C::LOAD_A || warp == C::LOAD_B || warp == C::LOAD_B + 1) {
+            // ------------------------------------------------------------ loads
+            if (lane == 0) {
+                const uint32_t full_leader0 = mapa_shared(full0, 0);
+                uint32_t it = 0;
+                bool ok = true, issued = false;
+                for (uint32_t i = 0; ok; ++i) {
+                    const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
+                    if (w.n == 0) break;
+                    bars.ring.done(i);
+                    // B columns of this CTA in boxes of 64, one for each B warp
+                    const int half = w.n / 2, boxes = (half + 63) / 64, q = warp - C::LOAD_B;
+                    const uint32_t bytes = (uint32_t)A_BYTES + 8192u * (uint32_t)boxes;  // of one CTA
+                    const int at = (int)rank * half + 64 * q;
+                    for (int kb = 0; kb < w.kb1; ++kb, ++it) {
+                        const uint32_t s = it % S, ph = (it / S) & 1;
+                        if (!mbar_wait_bounded(empty0 + 8 * s, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) {
+                            ok = false;
+                            break;
+                        }
+                        // weight: the partial block first, with a partial last step through the helper warp, on
+                        // this CTA's own barrier
+                        const bool fix = DIR == kExpWeight && kb == 0 && (w.last & 15) != 0;
+                        const int row = w.row0 + (kb == 0 ? w.kb1 - 1 : kb - 1) * 64;  // (weight)
+                        const uint32_t bar = fix ? tail0 + 8 * s : full_leader0 + 8 * s;
+                        if (warp == C::LOAD_A) {
+                            if (fix)
+                                mbar_arrive_expect_tx(tail0 + 8 * s, bytes);
+                            else if (leader)
+                                mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
+                            const uint32_t dst = smem_u32(sA + s * A_BYTES);
+                            const int m = w.m0 + (int)rank * 128;
+                            if constexpr (DIR == kExpForward) {
+                                tma_load_3d_pair(dst, &p.a, bar, kb * 64, m, w.e);
+                            } else if constexpr (DIR == kExpData) {
+                                tma_load_3d_pair(dst, &p.a, bar, m, kb * 64, w.e);
+                                tma_load_3d_pair(dst + 8192, &p.a, bar, m + 64, kb * 64, w.e);
+                            } else {
+                                for (int b = 0; b < 2; ++b)
+                                    if (fix)
+                                        tma_load_2d(dst + 8192 * b, &p.a, bar, m + 64 * b, row);
+                                    else
+                                        tma_load_2d_pair(dst + 8192 * b, &p.a, bar, m + 64 * b, row);
+                            }
+                            issued = true;
+                        } else if (q < boxes) {
+                            const uint32_t dst = smem_u32(sB + s * B_BYTES + 8192 * q);
+                            if constexpr (DIR == kExpWeight) {
+                                if (fix)
+                                    tma_load_2d(dst, &p.b, bar, w.ntok + at, row);
+                                else
+                                    tma_load_2d_pair(dst, &p.b, bar, w.ntok + at, row);
+                            } else {
+                                tma_load_2d_pair(dst, &p.b, bar, kb * 64, w.row0 + at);
+                            }
+                            issued = true;
+                        }
+                    }
+                }
+                if (!ok && issued) {
+                    for (int q = 0; q < 100; ++q) __nanosleep(1000);
+                }
+            }
+            __syncwarp();
+        } else if (warp == C::MMA) {
+            // ------------------------------------------------------------ MMA (leader)
+            if (leader) {
+                constexpr bool A_K = DIR == kExpForward, B_K = DIR != kExpWeight;
+                constexpr uint32_t A_STEP = A_K ? 2 : 128, B_STEP = B_K ? 2 : 128;  // a 16-deep step, in 16 bytes
+                const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((A_K ? 0u : 1u) << 15) | ((B_K ? 0u : 1u) << 16) | ((uint32_t)(256 >> 4) << 24);
+                const uint64_t a_desc0 = smem_desc_sw128(smem_u32(sA), A_K ? 16 : 8192, 1024);
+                const uint64_t b_desc0 = smem_desc_sw128(smem_u32(sB), B_K ? 16 : 8192, 1024);
+                const uint32_t a_lo = (uint32_t)a_desc0, a_hi = (uint32_t)(a_desc0 >> 32), b_lo = (uint32_t)b_desc0, b_hi = (uint32_t)(b_desc0 >> 32);
+                uint32_t s = 0, ph = 0, use = 0;  // stage and its phase, accumulators used so far
+                bool ok = true, issued = false;
+                for (uint32_t i = 0; ok; ++i) {
+                    ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutMma);
+                    w.n = __shfl_sync(0xffffffffu, w.n, 0);
+                    w.kb1 = __shfl_sync(0xffffffffu, w.kb1, 0);
+                    w.last = __shfl_sync(0xffffffffu, w.last, 0);
+                    if (w.n == 0) break;
+                    if (lane == 0) bars.ring.done(i);
+                    if (w.kb1 == 0) continue;
+                    const uint32_t id = idesc0 | ((uint32_t)(w.n >> 3) << 17);
+                    for (int left = w.kb1; left > 0 && ok;) {
+                        // one accumulator: the whole depth, or a segment of it (weight)
+                        const uint32_t b = use & 1, bph = (use >> 1) & 1, d = tmem_base + b * 256;
+                        ++use;
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
+                        if (!ok) break;
+                        tc_fence_after();
+                        uint32_t acc = 0;
+                        const int end = DIR == kExpWeight && left > SEGMENT ? left - SEGMENT : 0;
+                        for (; left > end; --left) {
+                            ok = __all_sync(0xffffffffu, mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
+                            if (!ok) break;
+                            const uint32_t ad = a_lo + s * (A_BYTES >> 4), bd = b_lo + s * (B_BYTES >> 4);
+                            const int n = DIR == kExpWeight && left == w.kb1 ? (w.last + 15) / 16 : 4;
+    #pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                if (kk < n) mma_pair_elect(d, ad + A_STEP * kk, a_hi, bd + B_STEP * kk, b_hi, id, acc);
+                                acc = 1;
+                            }
+                            issued = true;
+                            commit_pair_elect(empty0 + 8 * s);
+                            if (++s == (uint32_t)S) {
+                                s = 0;
+                                ph ^= 1;
+                            }
+                        }
+                        if (ok) commit_pair_elect(tfull0 + 8 * b);
+                    }
+                }
+                if (!ok && issued) {
+                    for (int q = 0; q < 100; ++q) __nanosleep(1000);
+                }
+            }
+            __syncwarp();
+        } else if (warp == C::HELP) {
+            // ------------------------------------------------------------ helper: rows past an expert's end, rows of none
+            if constexpr (DIR == kExpWeight) {
+                uint32_t it = 0, phase = 0;  // bit s: parity of the next use of tail[s] and peer[s]
+                for (uint32_t i = 0;; ++i) {
+                    const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
+                    if (!__all_sync(0xffffffffu, w.n != 0)) break;
+                    if (lane == 0) bars.ring.done(i);
+                    const uint32_t s = it % S, ph = (phase >> s) & 1;
+                    it += (uint32_t)w.kb1;
+                    if (w.kb1 == 0 || (w.last & 15) == 0) continue;
+                    phase ^= 1u << s;
+                    bool ok = mbar_wait_bounded(tail0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    // rows [last, next multiple of 16) of each 64 x 64 block: whole 128-byte lines, so the swizzle
+                    // within a line does not matter
+                    const int lo = w.last, n = ((lo + 15) & ~15) - lo;
+                    uint8_t *line = sA + s * A_BYTES + lo * 128 + lane * 16;
+                    uint8_t *line_b = sB + s * B_BYTES + lo * 128 + lane * 16;
+                    for (int j = lane; j < n * 8; j += 32, line += 512, line_b += 512) {
+                        *reinterpret_cast<uint4 *>(line) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(line + 8192) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(line_b) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(line_b + 8192) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (!leader) {
+                            mbar_arrive_remote(mapa_shared(peer0 + 8 * s, 0));
+                        } else {
+                            ok = wait_cluster(peer0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
+                            if (ok) mbar_arrive(full0 + 8 * s);
+                        }
+                    }
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                }
+            } else {
+                // forward, data: rows of no expert get zeros (16-byte stores; the width is a multiple of 8)
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
+                const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
+                const int64_t nfill = (int64_t)lo + (p.rows - hi);
+                for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
+                    uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
+                    for (int c = lane; c < vec; c += 32) row[c] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        }
     }
 
     // no remote arrive or MMA may target a CTA that has left
     cluster_sync_all();
-    if (warp == 5) {
+    if (warp == C::MMA) {
         tc_fence_after();
         tmem_dealloc2(tmem_base, 512);
     }
@@ -519,11 +558,11 @@ cudaError_t launch_dir(const ExpertPairParams &p, int grid, cudaStream_t s) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(experts_pair_kernel<DIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(experts_pair_kernel<DIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DIR>::SMEM);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    return launch_early(experts_pair_kernel<DIR>, grid, THREADS, SMEM, s, p);
+    return launch_early(experts_pair_kernel<DIR>, grid, Cfg<DIR>::THREADS, Cfg<DIR>::SMEM, s, p);
 }
 
 }  // namespace
