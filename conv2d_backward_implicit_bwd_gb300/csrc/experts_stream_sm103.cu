@@ -6,9 +6,8 @@
 // Every filter that has a row is read once and that read is the time: the floor
 // is filter bytes / memory rate.  So the work is cut by filter bytes, not by
 // tiles: the 16 KB blocks (128 of the filter's M dimension x 64 deep) of all
-// tiles in one sequence, an equal stretch to each SM, eight to eleven blocks in
-// flight.  A tile is 128 x up to BT rows of one expert; the rows are the MMA's N
-// (steps of 16), so one row costs 16 columns.
+// tiles in one sequence, an equal stretch to each SM, eleven blocks in flight.  A
+// tile is 128 x up to 16 rows of one expert, which are the MMA's N.
 //
 // A tile that lies inside one SM's stretch is stored from there.  A tile cut by a
 // stretch's end is joined: each SM writes its fp32 part to the workspace and the
@@ -33,22 +32,20 @@ namespace {
 
 constexpr int RING = 4;
 
-template <int BT>
-struct Cfg {
-    static constexpr int S = BT == 16 ? 11 : 8;  // stages
-    static constexpr int A_BYTES = 128 * 64 * 2;
-    static constexpr int B_BYTES = BT * 128;
-    static constexpr int TMEM_COLS = 2 * BT;  // two accumulators (32 or 128 columns)
-    struct Bars {
-        ExpertRing<RING> ring;
-        uint64_t full[S], empty[S], tfull[2], tempty[2];
-        uint32_t tmem;
-        int32_t abort, last, vote[8];
-        uint32_t share[2];  // of the schedule: units of a block, blocks with one more
-    };
-    static constexpr int SMEM = 1024 + S * (A_BYTES + B_BYTES) + (int)sizeof(ExpertTable) + (int)sizeof(Bars) + 8;
-    static_assert(SMEM <= 232448, "shared memory of one CTA");
+constexpr int BT = kStreamRows;  // rows of a tile
+constexpr int S = 11;            // stages
+constexpr int A_BYTES = 128 * 64 * 2;
+constexpr int B_BYTES = BT * 128;
+constexpr int TMEM_COLS = 2 * BT;  // two accumulators
+struct Bars {
+    ExpertRing<RING> ring;
+    uint64_t full[S], empty[S], tfull[2], tempty[2];
+    uint32_t tmem;
+    int32_t abort, last, vote[8];
+    uint32_t share[2];  // of the schedule: units of a block, blocks with one more
 };
+constexpr int SMEM = 1024 + S * (A_BYTES + B_BYTES) + (int)sizeof(ExpertTable) + (int)sizeof(Bars) + 8;
+static_assert(SMEM <= 232448, "shared memory of one CTA");
 constexpr int THREADS = 9 * 32;
 
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
@@ -97,15 +94,13 @@ struct Share {
     }
 };
 
-template <int DIR, int BT>
+template <int DIR>
 __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid_constant__ ExpertStreamParams p) {
-    using C = Cfg<BT>;
-    constexpr int S = C::S;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *sA = smem, *sB = smem + S * C::A_BYTES;
-    typename C::Bars &bars = *reinterpret_cast<typename C::Bars *>(sB + S * C::B_BYTES);
-    ExpertTable &tab = *reinterpret_cast<ExpertTable *>(sB + S * C::B_BYTES + (sizeof(typename C::Bars) + 7) / 8 * 8);
+    uint8_t *sA = smem, *sB = smem + S * A_BYTES;
+    Bars &bars = *reinterpret_cast<Bars *>(sB + S * B_BYTES);
+    ExpertTable &tab = *reinterpret_cast<ExpertTable *>(sB + S * B_BYTES + (sizeof(Bars) + 7) / 8 * 8);
     volatile int32_t *abort_flag = &bars.abort;
     const uint32_t full0 = smem_u32(bars.full), empty0 = smem_u32(bars.empty), tfull0 = smem_u32(bars.tfull), tempty0 = smem_u32(bars.tempty);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -127,7 +122,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
         fence_proxy_async_smem();
     }
     if (warp == 5) {
-        tmem_alloc(smem_u32(&bars.tmem), C::TMEM_COLS);
+        tmem_alloc(smem_u32(&bars.tmem), TMEM_COLS);
         tc_fence_before();
     }
     if (warp == 4 && lane == 0) {
@@ -202,8 +197,8 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
                         break;
                     }
                     if (warp == 4) {
-                        mbar_arrive_expect_tx(bar, C::A_BYTES + C::B_BYTES);
-                        const uint32_t dst = smem_u32(sA + s * C::A_BYTES);
+                        mbar_arrive_expect_tx(bar, A_BYTES + B_BYTES);
+                        const uint32_t dst = smem_u32(sA + s * A_BYTES);
                         if constexpr (DIR == kExpForward) {
                             load_3d(dst, &p.a, bar, kb * 64, w.m0, w.e);
                         } else {
@@ -211,7 +206,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
                             load_3d(dst + 8192, &p.a, bar, w.m0 + 64, kb * 64, w.e);
                         }
                     } else {
-                        load_2d(smem_u32(sB + s * C::B_BYTES), &p.b, bar, kb * 64, w.row0);
+                        load_2d(smem_u32(sB + s * B_BYTES), &p.b, bar, kb * 64, w.row0);
                     }
                 }
             }
@@ -245,7 +240,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
             for (int left = count; left > 0; --left) {
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
                 if (!ok) break;
-                const uint32_t ad = a_lo + s * (C::A_BYTES >> 4), bd = b_lo + s * (C::B_BYTES >> 4);
+                const uint32_t ad = a_lo + s * (A_BYTES >> 4), bd = b_lo + s * (B_BYTES >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     mma_elect(d, ad + A_STEP * kk, a_hi, bd + 2 * kk, b_hi, id, acc);
@@ -285,22 +280,15 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
             const int m = w.m0 + (int)threadIdx.x;
             __nv_bfloat16 *dst = out + (int64_t)w.row0 * p.ldo + m;
             float *slot = p.parts + ((int64_t)blockIdx.x * 2 + (w.kb0 == 0 ? 1 : 0)) * (BT * 128) + threadIdx.x;
-            constexpr int G = BT < 32 ? BT : 32;
-#pragma unroll 1
-            for (int g = 0; g < w.ntok; g += G) {
-                uint32_t v[G];
-                if constexpr (G == 16)
-                    tmem_ld16(lane_base + b * BT + g, v);
-                else
-                    tmem_ld32(lane_base + b * BT + g, v);
+            uint32_t v[BT];
+            tmem_ld16(lane_base + b * BT, v);
 #pragma unroll
-                for (int q = 0; q < G; ++q) {
-                    if (g + q >= w.ntok) break;
-                    if (whole) {
-                        if (ok && m < mdim) dst[(int64_t)(g + q) * p.ldo] = __float2bfloat16_rn(__uint_as_float(v[q]));
-                    } else {
-                        __stcg(slot + (g + q) * 128, __uint_as_float(v[q]));
-                    }
+            for (int q = 0; q < BT; ++q) {
+                if (q >= w.ntok) break;
+                if (whole) {
+                    if (ok && m < mdim) dst[(int64_t)q * p.ldo] = __float2bfloat16_rn(__uint_as_float(v[q]));
+                } else {
+                    __stcg(slot + q * 128, __uint_as_float(v[q]));
                 }
             }
             tc_fence_before();
@@ -322,23 +310,20 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
             asm volatile("bar.sync 1, 128;" ::: "memory");
             if (*(volatile int32_t *)&bars.last) {
                 __threadfence();
-#pragma unroll 1
-                for (int g = 0; g < w.ntok; g += 16) {
-                    float a[16];
+                float a[BT];
 #pragma unroll
-                    for (int q = 0; q < 16; ++q) a[q] = 0.f;
-                    for (int c = c0; c <= c1; ++c) {
-                        const float *part = p.parts + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * (BT * 128) + threadIdx.x;
-                        float x[16];
+                for (int q = 0; q < BT; ++q) a[q] = 0.f;
+                for (int c = c0; c <= c1; ++c) {
+                    const float *part = p.parts + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * (BT * 128) + threadIdx.x;
+                    float x[BT];
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) x[q] = g + q < w.ntok ? __ldcg(part + (g + q) * 128) : 0.f;
+                    for (int q = 0; q < BT; ++q) x[q] = q < w.ntok ? __ldcg(part + q * 128) : 0.f;
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) a[q] += x[q];
-                    }
-#pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        if (ok && g + q < w.ntok && m < mdim) dst[(int64_t)(g + q) * p.ldo] = __float2bfloat16_rn(a[q]);
+                    for (int q = 0; q < BT; ++q) a[q] += x[q];
                 }
+#pragma unroll
+                for (int q = 0; q < BT; ++q)
+                    if (ok && q < w.ntok && m < mdim) dst[(int64_t)q * p.ldo] = __float2bfloat16_rn(a[q]);
             }
             asm volatile("bar.sync 1, 128;" ::: "memory");  // bars.last is written again
         }
@@ -347,28 +332,27 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
     __syncthreads();
     if (warp == 5) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, C::TMEM_COLS);
+        tmem_dealloc(tmem_base, TMEM_COLS);
     }
 }
 
-template <int DIR, int BT>
-cudaError_t launch_bt(const ExpertStreamParams &p, int grid, cudaStream_t s) {
+template <int DIR>
+cudaError_t launch_dir(const ExpertStreamParams &p, int grid, cudaStream_t s) {
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(experts_stream_kernel<DIR, BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<BT>::SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(experts_stream_kernel<DIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    return launch_early(experts_stream_kernel<DIR, BT>, grid, THREADS, Cfg<BT>::SMEM, s, p);
+    return launch_early(experts_stream_kernel<DIR>, grid, THREADS, SMEM, s, p);
 }
 
 }  // namespace
 
-cudaError_t launch_experts_stream(const ExpertStreamParams &p, int dir, int bt, int grid, cudaStream_t s) {
-    if (dir == kExpForward) return bt == 16 ? launch_bt<kExpForward, 16>(p, grid, s) : launch_bt<kExpForward, 64>(p, grid, s);
-    return bt == 16 ? launch_bt<kExpData, 16>(p, grid, s) : launch_bt<kExpData, 64>(p, grid, s);
+cudaError_t launch_experts_stream(const ExpertStreamParams &p, int dir, int grid, cudaStream_t s) {
+    return dir == kExpForward ? launch_dir<kExpForward>(p, grid, s) : launch_dir<kExpData>(p, grid, s);
 }
 
 }  // namespace cbd

@@ -70,13 +70,13 @@ struct ExpertStreamParams {
     void *out;
     const int32_t *offsets;
     int32_t *status;
-    float *parts;      // [blocks][2][bt][128] parts of tiles that several blocks share
+    float *parts;      // [blocks][2][kStreamRows][128] parts of tiles that several blocks share
     int32_t *arrived;  // [blocks] arrivals of the tile that starts in a block and ends in another, 0 between launches
     int64_t wait_budget, ldo;
     int32_t experts, rows, K, N;
 };
-constexpr int kStreamRows = 64;  // most rows of a tile
-cudaError_t launch_experts_stream(const ExpertStreamParams &p, int dir, int bt, int grid, cudaStream_t s);
+constexpr int kStreamRows = 16;  // most rows of a tile
+cudaError_t launch_experts_stream(const ExpertStreamParams &p, int dir, int grid, cudaStream_t s);
 
 // Gradient clipping: the tensors are cut into chunks of kClipChunk bytes.
 constexpr int kClipChunk = 32768;

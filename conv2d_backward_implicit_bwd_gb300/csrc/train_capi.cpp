@@ -93,7 +93,6 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
 size_t extent(int64_t rows, int64_t ld, int64_t width, size_t es) {
     return rows > 0 ? ((size_t)(rows - 1) * (size_t)ld + (size_t)width) * es : 0;
 }
-constexpr int64_t kFewRows = 32;  // rows per expert, on average, up to which the filters' bytes are the time
 bool known_dtype(int32_t d) { return d == CONV_BWD_F32 || d == CONV_BWD_BF16; }
 
 template <typename P, typename F>
@@ -196,7 +195,7 @@ conv_bwd_status conv_bwd_experts_create(const conv_bwd_experts_desc *d, conv_bwd
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             sms = 0;
         cudaGetLastError();
-        // status and counters, a counter per SM, the parts of tiles that several SMs share (10 MB)
+        // status and counters, a counter per SM, the parts of tiles that several SMs share (2.5 MB)
         p.off_parts = 64 + ((size_t)sms * 4 + 255) / 256 * 256 + 192;
         return p.dev.init(p.off_parts + (size_t)sms * 2 * kStreamRows * 128 * 4);
     });
@@ -237,16 +236,19 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
     // Tensor cores where TMA can load the operands: bf16, widths, strides and addresses on 16 bytes.
     if (d.dtype == CONV_BWD_BF16 && d.K % 8 == 0 && d.N % 8 == 0 && lda % 8 == 0 && ldo % 8 == 0 && ldb % 8 == 0 &&
         ((uintptr_t)a | (uintptr_t)b | (uintptr_t)out) % 16 == 0 && rows > 0 && d.K * d.N < (1LL << 37)) {
-        // Few rows per expert: the time is the filters' bytes, cut evenly over the SMs.  With more the pairs' wide
-        // tiles use an operand for more products.
+        const int64_t mt = ((dir == kExpData ? d.K : d.N) + 255) / 256, pairs = std::max(1, p->dev.num_sms / 2);
+        // Up to eight rows per expert and too few 256-wide tiles for two rounds of the SM pairs: the filters' bytes
+        // are the time, and the few-rows kernel cuts them evenly over the SMs.  Measured (us, it against the pairs),
+        // 8 experts of 1024 x 4096: data 12.6 to 18.8 at one row per expert, 18.8 to 19.7 at eight, forward (128
+        // tiles) 11.5 to 12.0 and 15.0 to 15.2; at 16 rows forward 18.6 to 15.5.  64 experts of 2048 x 1024 (256
+        // and 512 tiles): 49 to 49 at four rows, data 48 to 45.
         const int64_t stream_blocks =
-            (rows / 16 + std::min<int64_t>(d.experts, rows)) * ((wo + 127) / 128) * ((wa + 63) / 64);
-        if (!weight && rows <= kFewRows * d.experts && stream_blocks <= 0x7fffffff) {
-            const int bt = rows <= 8 * d.experts ? 16 : kStreamRows;
+            (rows / kStreamRows + std::min<int64_t>(d.experts, rows)) * ((wo + 127) / 128) * ((wa + 63) / 64);
+        if (!weight && rows <= 8 * d.experts && mt * std::min<int64_t>(d.experts, rows) <= 2 * pairs && stream_blocks <= 0x7fffffff) {
             ExpertStreamParams sp;
             std::memset(&sp, 0, sizeof(sp));
             const bool ok = map_filters(&sp.a, b, d, false, 64, dir == kExpForward ? 128 : 64) &&
-                            map_rows(&sp.b, a, dir == kExpForward ? d.K : d.N, rows, lda, (uint32_t)bt);
+                            map_rows(&sp.b, a, dir == kExpForward ? d.K : d.N, rows, lda, kStreamRows);
             if (!ok) return CONV_BWD_ERR_CUDA;
             sp.out = out; sp.offsets = offsets; sp.status = p->dev.status();
             sp.arrived = reinterpret_cast<int32_t *>(p->dev.rest());
@@ -256,9 +258,8 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
             sp.experts = (int32_t)d.experts; sp.rows = (int32_t)rows; sp.K = (int32_t)d.K; sp.N = (int32_t)d.N;
             // at least four blocks of 16 KB for an SM
             const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(p->dev.num_sms, stream_blocks / 4));
-            return launch_experts_stream(sp, dir, bt, grid, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
+            return launch_experts_stream(sp, dir, grid, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
         }
-        const int64_t mt = ((dir == kExpData ? d.K : d.N) + 255) / 256, pairs = std::max(1, p->dev.num_sms / 2);
         ExpertPairParams pp;
         std::memset(&pp, 0, sizeof(pp));
         bool ok;

@@ -342,3 +342,40 @@ def test_refusals(T):
     with pytest.raises(ConvBwdError) as err:
         plan.forward(both[:, :64], w, o, out=both[:, 64:])       # rows interleave: refused as overlapping
     assert err.value.status == 1
+
+
+def test_more_than_32_bit_offsets(T):
+    """Rows whose elements lie past 2^31: first and last rows of a tall matrix on one expert, each way."""
+    k, n, rows = 1024, 16, (1 << 21) + 40
+    x = torch.zeros(rows, k, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    ends = torch.cat([torch.arange(300), torch.arange(rows - 300, rows)]).cuda()
+    x[ends] = torch.randn(600, k, generator=g, device="cuda").bfloat16()
+    dy = torch.zeros(rows, n, dtype=torch.bfloat16, device="cuda")
+    dy[ends] = torch.randn(600, n, generator=g, device="cuda").bfloat16()
+    w = torch.randn(2, n, k, generator=g, device="cuda").bfloat16()
+    off = [0, 250, rows]
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    plan = T.Experts(2, k, n)
+    y, dx, dw = plan.forward(x, w, o), plan.backward_data(dy, w, o), plan.backward_weight(dy, x, o)
+    e = (torch.arange(600, device="cuda") >= 250).long()
+    for got, a, b, length in ((y[ends], x[ends], w.transpose(1, 2), k), (dx[ends], dy[ends], w, n)):
+        want = torch.einsum("ij,ijk->ik", a.double(), b[e].double())
+        check(got, want, torch.einsum("ij,ijk->ik", a.double().abs(), b[e].double().abs()), length, True)
+    assert (y[300:-300] == 0).all() and (dx[300:-300] == 0).all()
+    want, mag = reference("weight", dy[ends], x[ends], [0, 250, 600], 2, k, n, 600)
+    check(dw, want, mag, 600, False)
+    assert plan.status() == (0, 0)
+
+
+def test_long_sums_keep_their_precision(T):
+    """fp32 gradients over many rows: within 2^-20 of the norm, however many rows are summed (a truncating
+    accumulator would lose about r 2^-30)."""
+    plan = T.Experts(1, 128, 256)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for rows in (500, 4000, 30000):
+        x = torch.randn(rows, 128, generator=g, device="cuda").bfloat16()
+        dy = torch.randn(rows, 256, generator=g, device="cuda").bfloat16()
+        o = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+        want = dy.double().T @ x.double()
+        assert float((plan.backward_weight(dy, x, o)[0].double() - want).norm() / want.norm()) <= 2.0 ** -20

@@ -295,3 +295,18 @@ def test_refusals(T):
               lambda: plan.backward(z, a, adv, w, out=z[:3]), lambda: plan.backward(z, a, adv, w, grad=adv)):
         with pytest.raises(ValueError):
             g()
+
+
+def test_more_than_32_bit_offsets(T):
+    """Logits past 2^31 elements: the last rows."""
+    t, v = 34000, 65536
+    z = torch.zeros(t, v, dtype=torch.bfloat16, device="cuda")
+    zl, al, advl, wl, ol, fl = inputs(8, v, "bf16")
+    z[-8:] = zl
+    put = lambda x, fill=0.0: torch.cat([torch.full((t - 8,), fill, device="cuda"), x])  # noqa: E731
+    a = torch.cat([torch.full((t - 8,), -1, dtype=torch.int32, device="cuda"), al])
+    plan = T.PolicyLoss(v, clip_low=LO, clip_high=HI, kl=0.1)
+    want = reference(zl, al, advl, wl, ol, fl, 0.1, 1.0)
+    loss, logp, dz = plan.forward_backward(z, a, put(advl), put(wl), put(ol), put(fl))
+    check(dict(loss=loss, logp=logp[-8:], dz=dz[-8:]), want, 0.1, 1.0, advl, wl, ol, "bf16")
+    assert (dz[:16] == 0).all() and (dz[-16:-8] == 0).all()
