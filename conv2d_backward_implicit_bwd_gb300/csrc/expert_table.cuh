@@ -5,7 +5,7 @@
 //
 // The start of a launch runs cold: an instruction line costs a fetch from L2, so
 // straight code is slow there (a table that sorted the experts by cost in some
-// 600 instructions took 6.4 us, this one 0.5 us at 64 experts).
+// 600 instructions took 6.4 us, this one 0.8 us, at 13 experts).
 #pragma once
 #include <stdint.h>
 

@@ -6,16 +6,19 @@
 // loss and its derivative c = dloss/dlogp from four floats, then
 // dz_v = c scale ([v = a] - exp(scale (z_v - m)) / s) in a second pass.
 //
-// Wide rows (32 KB and more) stream through a ring of 16 KB buffers in shared
-// memory that one thread fills with bulk copies, three blocks per SM: up to 192 KB
-// of reads stay in flight whatever the arithmetic does.  The fused form's second
-// pass reads the row again, from L2 where its block has just had it: memory sees
-// each logit once and each gradient once.  Narrower rows take a warp or a block
-// each and load into registers.  Measured (us, against registers): 1021 rows of
-// 50257 fp32 forward 38 (43), 300 rows of 128000 bf16 backward 25 (32), 8192 rows
-// of 32768 bf16 fused 190 (204).  Two blocks of 512 workers took 225 fused, with
-// the row kept in the ring between its passes 268: the ends of a pass, which only
-// other rows' work can hide, weigh more than the second read from L2.
+// Rows above 16 KB stream through a ring of 16 KB buffers in shared memory that
+// one thread fills with bulk copies, three blocks per SM: up to 192 KB of reads
+// stay in flight whatever the arithmetic does.  The fused form's second pass reads
+// the row again, from L2 where its block has just had it: memory sees each logit
+// once and each gradient once.  Narrower rows take a warp each and load into
+// registers.  Bound by memory; measured at 6.68 TB/s: 8192 rows of 32768 bf16 fused
+// 184 us (0.87), 1021 rows of 50257 fp32 forward 37 us (0.83), 300 rows of 128000
+// bf16 backward 23.5 us (0.98, part of the logits still in L2).
+// What the choice rests on (us, before launches were overlapped; the ring against
+// rows loaded into registers): fused 190 (204), forward 38 (43), backward 25 (32).
+// Two blocks of 512 workers took 225 fused, with the row kept in the ring between
+// its passes 268: the ends of a pass, which only other rows' work can hide, weigh
+// more than the second read from L2.
 #include <cuda_bf16.h>
 #include <math.h>
 

@@ -271,7 +271,7 @@ class GradClip(_Plan):
         both = _empty((2, 1), torch.float32, device, stream)
         at = both.data_ptr()
         _check(_lib.conv_bwd_clip_run(self._h, g.buffer_info()[0], o.buffer_info()[0], max_norm, at, at + 4, _stream(stream, device)), "conv_bwd_clip_run")
-        return both.unbind(0)
+        return both[0], both[1]
 
     def status(self, stream=None):
         """(status, detail) of the calls since the last one; synchronises the stream."""
@@ -318,7 +318,7 @@ class PolicyLoss(_Plan):
         s = _empty((3 * t + 1,), torch.float32, device, stream)
         at = s.data_ptr()
         _check(_lib.conv_bwd_policy_forward(*args, at + 12 * t, at, at + 4 * t, at + 8 * t, _stream(stream, device)), "conv_bwd_policy_forward")
-        logp, lse, coef, loss = s.split((t, t, t, 1))
+        logp, lse, coef, loss = s.split_with_sizes((t, t, t, 1))
         return loss, logp, lse, coef
 
     def backward(self, logits, actions, lse, coef, grad=None, out=None, stream=None):
