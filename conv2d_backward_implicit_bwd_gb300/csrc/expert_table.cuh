@@ -75,6 +75,19 @@ __device__ __forceinline__ void build_expert_table(ExpertTable &t, const int32_t
     __syncwarp();
 }
 
+// The same after pdl_wait().  What comes before it overlaps the kernel before this
+// one, so an empty list goes through the code first and its instructions are there
+// when the offsets are (``zero``: any 0 in shared memory).
+template <int PER>
+__device__ __forceinline__ void build_expert_table_early(ExpertTable &t, const int32_t *offsets, const int32_t *zero, int experts,
+                                                         int rows, int mult, ExpertTiles kind, int32_t *status) {
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        if (pass) pdl_wait();
+        build_expert_table<PER>(t, pass ? offsets : zero, pass ? experts : 0, pass ? rows : 0, mult, kind, status);
+    }
+}
+
 // Expert of tile t: the last e with tile[e] <= t (experts without tiles share a
 // bound with the next one).
 __device__ __forceinline__ int expert_of_tile(const ExpertTable &tab, int experts, int t) {

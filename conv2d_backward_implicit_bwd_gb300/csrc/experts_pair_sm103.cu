@@ -236,14 +236,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
     }
-    pdl_next();
-    pdl_wait();
-    if (warp == C::SCHED)
-        build_expert_table<WIDE>(tab, p.offsets, p.experts, p.rows, DIR == kExpWeight ? mt * ((p.K + WIDE - 1) / WIDE) : mt,
-                                 DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesEach,
-                                 blockIdx.x == 0 ? p.status : nullptr);
     cluster_sync_all();
     tc_fence_after();
+    pdl_next();
+    if (warp == C::SCHED)
+        build_expert_table_early<WIDE>(tab, p.offsets, &bars.abort, p.experts, p.rows, DIR == kExpWeight ? mt * ((p.K + WIDE - 1) / WIDE) : mt,
+                                       DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesEach,
+                                       blockIdx.x == 0 ? p.status : nullptr);
+    else
+        pdl_wait();
     const uint32_t tmem_base = bars.tmem;
     if (threadIdx.x == 0 && !leader) {
         // the pair's MMAs write this CTA's rows at the leader's TMEM address
@@ -372,6 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
         if constexpr (DIR == kExpWeight) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == C::SCHED) {
             // ------------------------------------------------------------ schedule
+            if constexpr (DIR != kExpWeight) asm volatile("bar.arrive 2, 64;" ::: "memory");
             if (lane == 0) {
                 const int total = tab.tile[p.experts];
                 for (uint32_t i = 0;; ++i) {
@@ -541,6 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
                 }
             } else {
                 // forward, data: rows of no expert get zeros (16-byte stores; the width is a multiple of 8)
+                asm volatile("bar.sync 2, 64;" ::: "memory");  // the table
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
                 const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
                 const int64_t nfill = (int64_t)lo + (p.rows - hi);

@@ -129,14 +129,14 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
     }
-    pdl_next();
-    pdl_wait();
-    if (warp == 7) build_expert_table<BT>(tab, p.offsets, p.experts, p.rows, mt, kTilesByRows, blockIdx.x == 0 ? p.status : nullptr);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = bars.tmem;
+    pdl_next();
 
     if (warp == 7) {
+        build_expert_table_early<BT>(tab, p.offsets, &bars.abort, p.experts, p.rows, mt, kTilesByRows, blockIdx.x == 0 ? p.status : nullptr);
+        asm volatile("bar.arrive 2, 64;" ::: "memory");
         // ------------------------------------------------------------ schedule
         if (lane == 0) {
             // Cut tiles where their k-blocks spread more evenly over the SMs than whole tiles by more than a join
@@ -173,6 +173,8 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
         }
         __syncwarp();
     } else if (warp == 8) {
+        pdl_wait();
+        asm volatile("bar.sync 2, 64;" ::: "memory");  // the table
         // ------------------------------------------------------------ rows of no expert: zeros
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
         const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
@@ -183,6 +185,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
         }
     } else if (warp == 4 || warp == 6) {
         // ------------------------------------------------------------ loads
+        pdl_wait();
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
@@ -217,6 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
         __syncwarp();
     } else if (warp == 5) {
         // ------------------------------------------------------------ MMA
+        pdl_wait();
         constexpr bool A_K = DIR == kExpForward;
         constexpr uint32_t A_STEP = A_K ? 2 : 128;
         const uint32_t idesc0 = (1u << 4) | (1u << 7) | (1u << 10) | ((A_K ? 0u : 1u) << 15) | ((uint32_t)(128 >> 4) << 24);
@@ -260,6 +264,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
         __syncwarp();
     } else {
         // ------------------------------------------------------------ epilogue
+        pdl_wait();
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
         const uint32_t lane_base = tmem_base + ((uint32_t)(warp * 32) << 16);
         bool ok = true;  // after a wait that ran out: no stores, but every barrier and counter as usual
