@@ -21,18 +21,12 @@ struct ExpertTable {
     __device__ __forceinline__ int len(int e) const { return off[e + 1] - off[e]; }
 };
 
-enum ExpertTiles : int {
-    kTilesByRows,    // ceil(rows / per) x mult tiles
-    kTilesEach,      // mult tiles
-    kTilesNonEmpty,  // mult tiles, none for an expert without rows
-};
-
-// By one warp.  Offsets below an earlier one or out of [0, rows] are recorded as
+// By one warp: expert e has ceil(rows / per) x mult tiles, with `each` mult tiles
+// if it has no rows.  Offsets below an earlier one or out of [0, rows] are recorded as
 // a fault and read as the running maximum clamped to that range: the experts'
 // rows stay disjoint and inside the tensors whatever the offsets hold.
-template <int PER>
 __device__ __forceinline__ void build_expert_table(ExpertTable &t, const int32_t *offsets, int experts, int rows,
-                                                   int mult, ExpertTiles kind, int32_t *status) {
+                                                   uint32_t per, int mult, bool each, int32_t *status) {
     const int lane = threadIdx.x & 31;
 #pragma unroll 4
     for (int e = lane; e <= experts; e += 32) t.off[e] = offsets[e];
@@ -60,7 +54,8 @@ __device__ __forceinline__ void build_expert_table(ExpertTable &t, const int32_t
         top = __shfl_sync(0xffffffffu, o, 31);
         // tiles of expert e - 1
         const uint32_t len = e > 0 && e <= experts ? (uint32_t)(o - before) : 0u;
-        int n = kind == kTilesByRows ? (int)((len + PER - 1) / PER) * mult : e > 0 && e <= experts && (kind == kTilesEach || len) ? mult : 0;
+        int n = (int)((len + per - 1) / per) * mult;
+        if (each && len == 0 && e > 0 && e <= experts) n = mult;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int v = __shfl_up_sync(0xffffffffu, n, d);
@@ -78,13 +73,12 @@ __device__ __forceinline__ void build_expert_table(ExpertTable &t, const int32_t
 // The same after pdl_wait().  What comes before it overlaps the kernel before this
 // one, so an empty list goes through the code first and its instructions are there
 // when the offsets are (``zero``: any 0 in shared memory).
-template <int PER>
 __device__ __forceinline__ void build_expert_table_early(ExpertTable &t, const int32_t *offsets, const int32_t *zero, int experts,
-                                                         int rows, int mult, ExpertTiles kind, int32_t *status) {
+                                                         int rows, uint32_t per, int mult, bool each, int32_t *status) {
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         if (pass) pdl_wait();
-        build_expert_table<PER>(t, pass ? offsets : zero, pass ? experts : 0, pass ? rows : 0, mult, kind, status);
+        build_expert_table(t, pass ? offsets : zero, pass ? experts : 0, pass ? rows : 0, per, mult, each, status);
     }
 }
 

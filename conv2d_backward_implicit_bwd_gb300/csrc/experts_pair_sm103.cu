@@ -240,9 +240,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
     tc_fence_after();
     pdl_next();
     if (warp == C::SCHED)
-        build_expert_table_early<WIDE>(tab, p.offsets, &bars.abort, p.experts, p.rows, DIR == kExpWeight ? mt * ((p.K + WIDE - 1) / WIDE) : mt,
-                                       DIR != kExpWeight ? kTilesByRows : p.accumulate ? kTilesNonEmpty : kTilesEach,
-                                       blockIdx.x == 0 ? p.status : nullptr);
+        build_expert_table_early(tab, p.offsets, &bars.abort, p.experts, p.rows, DIR == kExpWeight ? kMaxRows : WIDE,
+                                 DIR == kExpWeight ? mt * ((p.K + WIDE - 1) / WIDE) : mt, DIR == kExpWeight && !p.accumulate,
+                                 blockIdx.x == 0 ? p.status : nullptr);
     else
         pdl_wait();
     const uint32_t tmem_base = bars.tmem;

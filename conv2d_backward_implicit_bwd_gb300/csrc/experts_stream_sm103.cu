@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
     pdl_next();
 
     if (warp == 7) {
-        build_expert_table_early<BT>(tab, p.offsets, &bars.abort, p.experts, p.rows, mt, kTilesByRows, blockIdx.x == 0 ? p.status : nullptr);
+        build_expert_table_early(tab, p.offsets, &bars.abort, p.experts, p.rows, BT, mt, false, blockIdx.x == 0 ? p.status : nullptr);
         asm volatile("bar.arrive 2, 64;" ::: "memory");
         // ------------------------------------------------------------ schedule
         if (lane == 0) {

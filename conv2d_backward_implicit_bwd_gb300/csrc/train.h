@@ -36,6 +36,7 @@ constexpr int kMaxExperts = 1024;  // the expert tables of a launch live in shar
 enum : int { kExpForward = 0, kExpData = 1, kExpWeight = 2 };
 
 // Expert product on CUDA cores (any sizes, strides and alignment).
+constexpr int kMaxRows = 0x7fffffff;
 struct ExpertSimtParams {
     const void *a;           // x (forward), dy (data, weight)
     const void *b;           // w (forward, data), x (weight)
@@ -45,8 +46,16 @@ struct ExpertSimtParams {
     int64_t lda, ldb, ldo;   // row strides of the row-sorted tensors (ldb: weight only; ldo: forward, data)
     int32_t experts, rows, K, N;
     int32_t accumulate;
+    int32_t wide;            // 1: tiles of 128 x 128, else 64 x 64
+    int32_t chunk;           // contraction indices of a piece (kMaxRows: a tile is not split)
+    int32_t grid;
+    float *parts;            // 64 x 64 sums of each piece of split tiles
+    int32_t *arrived;        // their counters
 };
-cudaError_t launch_experts_simt(const ExpertSimtParams &p, int dtype, int dir, int num_sms, cudaStream_t s);
+// most pieces of a launch with split tiles, for an SM
+constexpr int kSimtPieces = 2;
+cudaError_t launch_experts_f32(const ExpertSimtParams &p, int dir, cudaStream_t s);
+cudaError_t launch_experts_b16(const ExpertSimtParams &p, int dir, cudaStream_t s);
 
 // Expert product on tensor cores over pairs of SMs (bf16, 16-byte aligned rows).
 struct ExpertPairParams {  // 128-byte aligned through CUtensorMap

@@ -191,13 +191,14 @@ conv_bwd_status conv_bwd_experts_create(const conv_bwd_experts_desc *d, conv_bwd
     return create_plan(out, [&](conv_bwd_experts_plan_s &p) {
         p.d = *d;
         int sms = 0, dev = 0;
-        if (d->dtype == CONV_BWD_BF16 && cudaGetDevice(&dev) == cudaSuccess &&
+        if (cudaGetDevice(&dev) == cudaSuccess &&
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             sms = 0;
         cudaGetLastError();
-        // status and counters, a counter per SM, the parts of tiles that several SMs share (2.5 MB)
-        p.off_parts = 64 + ((size_t)sms * 4 + 255) / 256 * 256 + 192;
-        return p.dev.init(p.off_parts + (size_t)sms * 2 * kStreamRows * 128 * 4);
+        // status, counters, the parts of tiles that several blocks share (5 MB)
+        static_assert(kSimtPieces * 64 * 64 >= 2 * kStreamRows * 128, "parts of either kind");
+        p.off_parts = 64 + ((size_t)sms * kSimtPieces * 4 + 255) / 256 * 256 + 192;
+        return p.dev.init(p.off_parts + (size_t)sms * kSimtPieces * 64 * 64 * 4);
     });
 }
 
@@ -237,14 +238,17 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
     if (d.dtype == CONV_BWD_BF16 && d.K % 8 == 0 && d.N % 8 == 0 && lda % 8 == 0 && ldo % 8 == 0 && ldb % 8 == 0 &&
         ((uintptr_t)a | (uintptr_t)b | (uintptr_t)out) % 16 == 0 && rows > 0 && d.K * d.N < (1LL << 37)) {
         const int64_t mt = ((dir == kExpData ? d.K : d.N) + 255) / 256, pairs = std::max(1, p->dev.num_sms / 2);
-        // Up to eight rows per expert and too few 256-wide tiles for two rounds of the SM pairs: the filters' bytes
-        // are the time, and the few-rows kernel cuts them evenly over the SMs.  Measured (us, it against the pairs),
-        // 8 experts of 1024 x 4096: data 12.6 to 18.8 at one row per expert, 18.8 to 19.7 at eight, forward (128
-        // tiles) 11.5 to 12.0 and 15.0 to 15.2; at 16 rows forward 18.6 to 15.5.  64 experts of 2048 x 1024 (256
-        // and 512 tiles): 49 to 49 at four rows, data 48 to 45.
+        // Up to eight rows per expert: the filters' bytes are the time, and the few-rows kernel cuts them evenly over
+        // the SMs.  It is the faster one where the 256-wide tiles do not fill two rounds of the SM pairs, where they
+        // are too shallow to fill the pairs' pipeline, and where half of their width is idle.  Measured (us, it
+        // against the pairs), 8 experts of 1024 x 4096: data 12.6 to 18.8 at one row per expert, 18.8 to 19.7 at
+        // eight, forward (128 tiles) 11.5 to 12.0 and 15.0 to 15.2; at 16 rows forward 18.6 to 15.5.  64 experts:
+        // 128 deep x 16384 45 to 86 at one row, 48 to 89 at eight; 512 x 4096 47 to 51 and 48 to 49; 8192 wide x 256
+        // deep 48 to 70; 16384 deep x 128 wide 48 to 63; but 1024 x 2048 47 to 45, 2048 deep x 1024 49 to 47.
         const int64_t stream_blocks =
             (rows / kStreamRows + std::min<int64_t>(d.experts, rows)) * ((wo + 127) / 128) * ((wa + 63) / 64);
-        if (!weight && rows <= 8 * d.experts && mt * std::min<int64_t>(d.experts, rows) <= 2 * pairs && stream_blocks <= 0x7fffffff) {
+        if (!weight && rows <= 8 * d.experts &&
+            (mt * std::min<int64_t>(d.experts, rows) <= 2 * pairs || wa <= 512 || wo <= 128) && stream_blocks <= 0x7fffffff) {
             ExpertStreamParams sp;
             std::memset(&sp, 0, sizeof(sp));
             const bool ok = map_filters(&sp.a, b, d, false, 64, dir == kExpForward ? 128 : 64) &&
@@ -280,14 +284,36 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
         const int grid = (int)(2 * std::max<int64_t>(1, std::min(pairs, most)));
         return launch_experts_pair(pp, dir, grid, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
     }
+    const int64_t sms = std::max(1, p->dev.num_sms);
+    auto tiles_of = [&](int64_t bt) {
+        const int64_t cols = (wo + bt - 1) / bt;
+        return weight ? d.experts * ((d.N + bt - 1) / bt) * cols : (rows / bt + std::min<int64_t>(d.experts, rows)) * cols;
+    };
     ExpertSimtParams sp;
     std::memset(&sp, 0, sizeof(sp));
     sp.a = a; sp.b = b; sp.out = out; sp.offsets = offsets; sp.status = p->dev.status();
     sp.lda = lda; sp.ldb = ldb; sp.ldo = ldo;
     sp.experts = (int32_t)d.experts; sp.rows = (int32_t)rows; sp.K = (int32_t)d.K; sp.N = (int32_t)d.N;
     sp.accumulate = accumulate ? 1 : 0;
-    return launch_experts_simt(sp, d.dtype, dir, p->dev.num_sms, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK
-                                                                                                      : CONV_BWD_ERR_CUDA;
+    sp.chunk = kMaxRows;
+    // wide tiles where they fill the SMs and the tiles' two sides
+    sp.wide = tiles_of(128) >= sms && wo > 64 && (weight ? d.N > 64 : rows >= 96 * d.experts);
+    int64_t pieces = std::max<int64_t>(1, tiles_of(sp.wide ? 128 : 64));
+    if (!sp.wide && pieces <= sms) {
+        // few tiles: their contraction in chunks of at least 128, at most two pieces for an SM
+        const int64_t depth = weight ? rows : wa, room = kSimtPieces * sms;
+        const int64_t least = weight ? rows * pieces / d.experts / (room - pieces) + 1 : (depth + room / pieces - 1) / (room / pieces);
+        const int64_t chunk = (std::max<int64_t>(least, 128) + 31) / 32 * 32;
+        if (chunk < depth) {
+            sp.chunk = (int32_t)chunk;
+            pieces = weight ? pieces + depth / chunk * (pieces / d.experts) : pieces * ((depth + chunk - 1) / chunk);
+        }
+    }
+    sp.grid = (int32_t)std::min<int64_t>(pieces, 2 * sms);
+    sp.arrived = reinterpret_cast<int32_t *>(p->dev.rest());
+    sp.parts = reinterpret_cast<float *>(static_cast<char *>(p->dev.mem) + p->off_parts);
+    const cudaError_t e = d.dtype == CONV_BWD_BF16 ? launch_experts_b16(sp, dir, (cudaStream_t)stream) : launch_experts_f32(sp, dir, (cudaStream_t)stream);
+    return e == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
 }
 
 conv_bwd_status conv_bwd_experts_forward(conv_bwd_experts_plan p, int64_t rows, const void *x, int64_t ldx,
