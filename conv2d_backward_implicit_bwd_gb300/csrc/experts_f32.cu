@@ -14,9 +14,23 @@ namespace {
 constexpr int NT = 256, ST = 4;
 
 // BT x BL elements of an operand: element (i, l) at src[i * stride + l], or at src[l * stride + i], to s[l][i];
-// zeros past i_lim and past `left`.
+// zeros past `left`; what lies past i_lim only reaches sums that nobody stores (narrow tiles leave it as it was).  `quads`: four neighbours at a time (the latter layout, on 16 bytes).
 template <bool L_CONTIG, int BT, int BL>
-__device__ __forceinline__ void copy(float *s, const float *src, int64_t stride, int i_lim, int left) {
+__device__ __forceinline__ void copy(float *s, const float *src, int64_t stride, int i_lim, int left, bool quads) {
+    if (!L_CONTIG && quads) {
+        constexpr int W = BT / 4, STEP = NT / W;
+        const int u = (int)threadIdx.x % W * 4, v = (int)threadIdx.x / W, bytes = max(0, min(4, i_lim - u)) * 4;
+        const float *at = src + v * stride + u;
+        uint32_t dst = smem_u32(s + v * (BT + 4) + u);
+#pragma unroll
+        for (int q = 0; q < BL / STEP; ++q) {
+            const bool ok = v + q * STEP < left && bytes;
+            if (BT == 128 || bytes) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(ok ? at : src), "r"(ok ? bytes : 0) : "memory");
+            at += STEP * stride;
+            dst += STEP * (BT + 4) * 4;
+        }
+        return;
+    }
     constexpr int Q = BT * BL / NT, W = L_CONTIG ? BL : BT, STEP = NT / W;
     const int u = (int)threadIdx.x % W, v = (int)threadIdx.x / W;
     const float *at = src + v * stride + u;
@@ -24,8 +38,8 @@ __device__ __forceinline__ void copy(float *s, const float *src, int64_t stride,
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         const int x = v + q * STEP;
-        const bool ok = L_CONTIG ? (x < i_lim && u < left) : (u < i_lim && x < left);
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(ok ? at : src), "r"(ok ? 4 : 0) : "memory");
+        const bool in = (L_CONTIG ? x : u) < i_lim, ok = in && (L_CONTIG ? u : x) < left;
+        if (BT == 128 || in) asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(ok ? at : src), "r"(ok ? 4 : 0) : "memory");
         at += STEP * stride;
         dst += L_CONTIG ? STEP * 4 : STEP * (BT + 4) * 4;
     }
@@ -65,12 +79,15 @@ __global__ void __launch_bounds__(NT, 2) experts_f32_kernel(const __grid_constan
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
         const ExpertPiece<DIR, BT, float> w(p, tab, ps, t);
         const int slices = (w.depth + BL - 1) / BL;
+        const bool quads_a = !A_L && ((reinterpret_cast<uintptr_t>(w.a) | (uintptr_t)w.stride_a * 4) & 15) == 0;
+        const bool quads_b = !B_L && ((reinterpret_cast<uintptr_t>(w.b) | (uintptr_t)w.stride_b * 4) & 15) == 0;
+        const bool busy = BT == 128 || (int)threadIdx.x / 32 * 8 < w.i_lim;  // any of this warp's 8 rows
         auto issue = [&](int k) {
             if (k < slices) {
                 float *s = stages + (k % ST) * (2 * BL * LD);
                 const int64_t l = (int64_t)k * BL;
-                copy<A_L, BT, BL>(s, w.a + (A_L ? l : l * w.stride_a), w.stride_a, w.i_lim, w.depth - k * BL);
-                copy<B_L, BT, BL>(s + BL * LD, w.b + (B_L ? l : l * w.stride_b), w.stride_b, w.j_lim, w.depth - k * BL);
+                copy<A_L, BT, BL>(s, w.a + (A_L ? l : l * w.stride_a), w.stride_a, w.i_lim, w.depth - k * BL, quads_a);
+                copy<B_L, BT, BL>(s + BL * LD, w.b + (B_L ? l : l * w.stride_b), w.stride_b, w.j_lim, w.depth - k * BL, quads_b);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
@@ -87,6 +104,7 @@ __global__ void __launch_bounds__(NT, 2) experts_f32_kernel(const __grid_constan
             asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
             __syncthreads();
             issue(k + ST - 1);
+            if (!busy) continue;
             const float *sa = stages + (k % ST) * (2 * BL * LD) + ti, *sb = stages + (k % ST) * (2 * BL * LD) + BL * LD + tj;
 #pragma unroll
             for (int l = 0; l < BL; ++l) {
