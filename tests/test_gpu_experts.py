@@ -379,3 +379,45 @@ def test_long_sums_keep_their_precision(T):
         o = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
         want = dy.double().T @ x.double()
         assert float((plan.backward_weight(dy, x, o)[0].double() - want).norm() / want.norm()) <= 2.0 ** -20
+
+
+# Enough tiles for the wide ones of the plain-load kernels: 128 x 128 tiles that end inside on each side; odd widths load
+# single elements, even ones pairs.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("narrow,wide", [(70, 2801), (66, 2802), (131, 2564)])
+@pytest.mark.parametrize("way", WAYS)
+def test_plain_loads_wide(T, way, dtype, narrow, wide):
+    if way == "weight":
+        k, n, rows_of = wide // 2, wide // 2 - 301, [300, 95]
+    else:
+        (k, n), rows_of = ((narrow, wide) if way == "forward" else (wide, narrow)), [700, 3, 300]
+    off = offsets(rows_of)
+    plan = T.Experts(len(rows_of), k, n, dtype)
+    for pad in (0, 3):
+        run_way(T, plan, way, k, n, off, off[-1], dtype, 21, ld_pad=pad, accumulate=pad > 0)
+
+
+# Few tiles and a long contraction: its pieces are joined, in the same order every time.
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("way", WAYS)
+def test_plain_loads_split(T, way, dtype):
+    for k, n, rows_of in ((70, 51, [3001, 17, 0, 1]), (2003, 70, [40]), (70, 2003, [1, 0, 65]), (129, 127, [127, 128, 129, 5000])):
+        off = offsets(rows_of)
+        plan = T.Experts(len(rows_of), k, n, dtype)
+        a = run_way(T, plan, way, k, n, off, off[-1], dtype, 22, ld_pad=1)
+        b = run_way(T, plan, way, k, n, off, off[-1], dtype, 22, ld_pad=1)
+        assert torch.equal(a, b)
+        if way == "weight":
+            run_way(T, plan, way, k, n, off, off[-1], dtype, 23, accumulate=True)
+
+
+# Few rows, filters that are shallow or narrow against their other side.
+@pytest.mark.parametrize("deep,wide", [(72, 4104), (512, 1000), (2056, 96), (8, 8)])
+@pytest.mark.parametrize("way", ["forward", "data"])
+def test_few_rows_shallow_and_narrow(T, way, deep, wide):
+    k, n = (deep, wide) if way == "forward" else (wide, deep)
+    experts = 160
+    plan = T.Experts(experts, k, n)
+    for rows_of in ([1] * experts, [0, 3] * (experts // 2), [0] * (experts - 1) + [8 * experts]):
+        off = offsets(rows_of)
+        run_way(T, plan, way, k, n, off, off[-1], "bf16", 24)
