@@ -35,8 +35,8 @@
 // Schedule.  Pair b of P takes tiles b, 2P - 1 - b, 2P + b, ... (back and forth,
 // so that a fall or rise of the tiles' cost along the experts evens out).  One
 // warp of each CTA builds the table and decodes the tiles ahead of the others.
-// (Drawing tiles from a counter in falling cost order was no faster: the
-// hand-over between the two CTAs took 0.65 us of every role's time per tile.)
+// (Drawn from a counter by the leader, which hands them to both CTAs a tile ahead,
+// they took 1% less; in falling cost order the sort took more than it gave.)
 //
 // Precision of weight.  The tensor core's accumulator truncates: over r rows the
 // sum loses about r 2^-30 of itself (1.2e-6 measured at 1024 rows).  So weight
@@ -45,12 +45,12 @@
 // runs under the other accumulator's MMAs.
 //
 // Bounds, measured at 6.68 TB/s and 1963 TFLOP/s.  Tensor pipe: forward of 16384
-// rows by 16 filters of 1024 x 2048 48.5 us (0.72 of the rate), data of 32768 rows
+// rows by 16 filters of 1024 x 2048 47 us (0.74 of the rate), data of 32768 rows
 // by 32 of 2048 x 2048 163 us (0.86, the rows of each expert uneven).  Memory: 256
 // rows by 64 filters of 2048 x 1024 49 us (0.79; four rounds for 3.4 rounds' tiles);
-// weight of the first of these, adding to fp32 gradients, 79 us (0.70).  Adding by
+// weight of the first of these, adding to fp32 gradients, 77 us (0.72).  Adding by
 // reading the old gradient into the epilogue's staging and storing the sum was no
-// faster (82 to 86 us): the mix of reads and writes is the time.
+// faster (82 to 86 us against 78): the mix of reads and writes is the time.
 //
 // Roles per CTA, in warps: epilogue 4 (weight 8, with most of the registers), A
 // loads 1, MMA (leader CTA) and TMEM 1, B loads 2, helper 1 (weight: partial
@@ -137,6 +137,11 @@ __device__ __forceinline__ void commit_pair_elect(uint32_t bar) {
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+// Hands an accumulator back: only reads of TMEM came before, which the tcgen05 fence orders.  (A release at cluster
+// scope waits for the warp's global stores: 49.0 against 47.5 us, 16384 rows by 16 filters of 1024 x 2048.)
+__device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // mbar_wait_bounded that also acquires what the arriving thread of either CTA of the pair wrote before
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -293,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8 * b);
+                    if (lane == 0) arrive_relaxed(tempty_leader0 + 8 * b);
                 }
                 // 32 x 32 pieces (128 bytes of a row) through swizzled staging and TMA stores, added in L2 when
                 // accumulating: one writer per element, so the order is fixed
@@ -365,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(tempty_leader0 + 8 * b);
+                if (lane == 0) arrive_relaxed(tempty_leader0 + 8 * b);
             }
         }
         if constexpr (DIR == kExpWeight) bulk_wait_all();

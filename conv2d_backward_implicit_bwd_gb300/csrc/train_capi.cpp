@@ -42,6 +42,7 @@ struct DevicePart {
     bool has_device = false;
     int device = -1, num_sms = 0, clock_khz = 0;
     void *mem = nullptr;
+    size_t counters = 64;  // status word and the counters that are 0 between launches
     conv_bwd_status init(size_t bytes) {
         int n = 0;
         if (cudaGetDeviceCount(&n) != cudaSuccess || n == 0) {
@@ -79,7 +80,8 @@ conv_bwd_status read_status(const DevicePart &d, void *stream, int32_t *detail) 
     if (cudaStreamSynchronize(s) != cudaSuccess) return CONV_BWD_ERR_CUDA;
     if (h == 0) return CONV_BWD_OK;
     if (detail) *detail = h;
-    if (cudaMemsetAsync(d.status(), 0, 4, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+    // (a wait that ran out may have left counters behind)
+    if (cudaMemsetAsync(d.mem, 0, d.counters, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
         return CONV_BWD_ERR_CUDA;
     return (h & 0xF00) == 0x200 ? CONV_BWD_ERR_DEVICE_FAULT : CONV_BWD_ERR_DEVICE_TIMEOUT;
 }
@@ -198,6 +200,7 @@ conv_bwd_status conv_bwd_experts_create(const conv_bwd_experts_desc *d, conv_bwd
         // status, counters, the parts of tiles that several blocks share (5 MB)
         static_assert(kSimtPieces * 64 * 64 >= 2 * kStreamRows * 128, "parts of either kind");
         p.off_parts = 64 + ((size_t)sms * kSimtPieces * 4 + 255) / 256 * 256 + 192;
+        p.dev.counters = p.off_parts;
         return p.dev.init(p.off_parts + (size_t)sms * kSimtPieces * 64 * 64 * 4);
     });
 }
