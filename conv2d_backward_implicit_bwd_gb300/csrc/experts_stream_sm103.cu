@@ -4,12 +4,18 @@
 //   dx[i][k] = sum_n dy[i][n] w[e][n][k]
 //
 // Every filter that has a row is read once and that read is the time: the floor
-// is filter bytes / memory rate.  So the work is cut by filter bytes, not by
-// tiles: the 16 KB blocks (128 of the filter's M dimension x 64 deep) of all
-// tiles in one sequence, an equal stretch to each SM, eleven blocks in flight.  A
-// tile is 128 x up to 16 rows of one expert, which are the MMA's N.
+// is filter bytes / memory rate.  A tile is 128 of the filter's M dimension x up to
+// 16 rows of one expert, which are the MMA's N; its filter comes in blocks of 16 KB
+// (64 deep), eleven in flight.
 //
-// A tile that lies inside one SM's stretch is stored from there.  A tile cut by a
+// Three tiles for an SM and more: drawn from a counter, each when the loads of the
+// one before begin, because the SMs' shares of the memory differ (an even share of
+// 107 blocks takes 31 to 42 us).  64 experts of 2048 x 1024, 4 rows each: 45.5 us
+// (0.85 of the memory rate; 50 by even shares), 4.5 of them before the first data.
+// Drawing the last tiles in pieces of 512 or 1024 deep: 46 to 57, for their joins.
+//
+// Fewer, or tiles too shallow to hide a draw: cut by filter bytes, the blocks of all
+// tiles in one sequence and an equal stretch to each SM.  A tile that lies inside one SM's stretch is stored from there.  A tile cut by a
 // stretch's end is joined: each SM writes its fp32 part to the workspace and the
 // last of them to arrive (a counter per tile) adds the parts in the order of k
 // and stores.  No SM waits for another, and the sum's order is fixed.
@@ -42,6 +48,7 @@ struct Bars {
     uint64_t full[S], empty[S], tfull[2], tempty[2];
     uint32_t tmem;
     int32_t abort, last, vote[8];
+    uint64_t want;      // the filter loads took another tile
     uint32_t share[2];  // of the schedule: units of a block, blocks with one more
 };
 constexpr int SMEM = 1024 + S * (A_BYTES + B_BYTES) + (int)sizeof(ExpertTable) + (int)sizeof(Bars) + 8;
@@ -117,6 +124,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
             mbar_init(tempty0 + 8 * b, 4);
         }
         bars.ring.init(7);
+        mbar_init(smem_u32(&bars.want), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -139,9 +147,35 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
         asm volatile("bar.arrive 2, 64;" ::: "memory");
         // ------------------------------------------------------------ schedule
         if (lane == 0) {
+            const uint32_t ntiles = (uint32_t)tab.tile[p.experts], g = gridDim.x;
+            auto tile = [&](int t, int kb0, int kb1) {
+                ExpertWork w;
+                w.e = expert_of_tile(tab, p.experts, t);
+                const int l = t - tab.tile[w.e], q = l / mt, first = q * BT;
+                w.row0 = tab.off[w.e] + first;
+                w.ntok = min(BT, tab.len(w.e) - first);
+                w.m0 = (l - q * mt) * 128;
+                w.n = (w.ntok + 15) & ~15;
+                w.kb0 = kb0;
+                w.kb1 = kb1;
+                w.last = t;
+                return w;
+            };
+            ExpertWork none;
+            none.n = 0;
+            const bool draw = ntiles >= 3 * g && nkb >= 8;
+            for (uint32_t i = 0, t = blockIdx.x; draw; ++i) {
+                const ExpertWork w = t < ntiles ? tile((int)t, 0, nkb) : none;
+                if (!bars.ring.give(i, w, p.wait_budget, abort_flag, p.status) || w.n == 0) break;
+                // the next one once the loads have begun with this one
+                if (!mbar_wait_bounded(smem_u32(&bars.want), i & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) break;
+                const uint32_t drawn = (uint32_t)atomicAdd(p.drawn, 1);
+                // every block draws one too many: ntiles draws in all, and the last one clears
+                if (drawn == ntiles - 1) atomicExch(p.drawn, 0);
+                t = g + drawn;
+            }
             // Cut tiles where their k-blocks spread more evenly over the SMs than whole tiles by more than a join
             // takes: 2.3 us, the time of about eight 16 KB blocks of an SM.
-            const uint32_t ntiles = (uint32_t)tab.tile[p.experts], g = gridDim.x;
             const uint32_t whole_most = (ntiles + g - 1) / g * nkb, cut_most = (ntiles * nkb + g - 1) / g;
             const uint32_t grain = whole_most <= cut_most + 8 ? nkb : 1;  // k-blocks handed out at a time
             const uint32_t units = ntiles * (grain == 1 ? nkb : 1);
@@ -153,19 +187,10 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
             uint32_t u = blockIdx.x < nblocks ? share.begin(blockIdx.x) * grain : 0u;
             const uint32_t hi = blockIdx.x < nblocks ? share.begin(blockIdx.x + 1) * grain : 0u;
             int t = (int)(u / (uint32_t)nkb), kb0 = (int)u - t * nkb;
-            for (uint32_t i = 0;; ++i, ++t, kb0 = 0) {
-                ExpertWork w;
-                w.n = 0;
+            for (uint32_t i = 0; !draw; ++i, ++t, kb0 = 0) {
+                ExpertWork w = none;
                 if (u < hi) {
-                    w.e = expert_of_tile(tab, p.experts, t);
-                    const int l = t - tab.tile[w.e], q = l / mt, first = q * BT;
-                    w.row0 = tab.off[w.e] + first;
-                    w.ntok = min(BT, tab.len(w.e) - first);
-                    w.m0 = (l - q * mt) * 128;
-                    w.n = (w.ntok + 15) & ~15;
-                    w.kb0 = kb0;
-                    w.kb1 = (int)min((uint32_t)nkb, (uint32_t)kb0 + (hi - u));
-                    w.last = t;
+                    w = tile(t, kb0, (int)min((uint32_t)nkb, (uint32_t)kb0 + (hi - u)));
                     u += (uint32_t)(w.kb1 - kb0);
                 }
                 if (!bars.ring.give(i, w, p.wait_budget, abort_flag, p.status) || w.n == 0) break;
@@ -193,6 +218,7 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
                 const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
                 if (w.n == 0) break;
                 bars.ring.done(i);
+                if (warp == 4) mbar_arrive(smem_u32(&bars.want));
                 for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                     const uint32_t s = it % S, ph = (it / S) & 1, bar = full0 + 8 * s;
                     if (!mbar_wait_bounded(empty0 + 8 * s, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) {

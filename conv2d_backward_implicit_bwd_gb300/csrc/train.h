@@ -81,6 +81,7 @@ struct ExpertStreamParams {
     int32_t *status;
     float *parts;      // [blocks][2][kStreamRows][128] parts of tiles that several blocks share
     int32_t *arrived;  // [blocks] arrivals of the tile that starts in a block and ends in another, 0 between launches
+    int32_t *drawn;    // counter of the tiles that blocks drew, 0 between launches
     int64_t wait_budget, ldo;
     int32_t experts, rows, K, N;
 };

@@ -241,17 +241,17 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
     if (d.dtype == CONV_BWD_BF16 && d.K % 8 == 0 && d.N % 8 == 0 && lda % 8 == 0 && ldo % 8 == 0 && ldb % 8 == 0 &&
         ((uintptr_t)a | (uintptr_t)b | (uintptr_t)out) % 16 == 0 && rows > 0 && d.K * d.N < (1LL << 37)) {
         const int64_t mt = ((dir == kExpData ? d.K : d.N) + 255) / 256, pairs = std::max(1, p->dev.num_sms / 2);
-        // Up to eight rows per expert: the filters' bytes are the time, and the few-rows kernel cuts them evenly over
-        // the SMs.  It is the faster one where the 256-wide tiles do not fill two rounds of the SM pairs, where they
-        // are too shallow to fill the pairs' pipeline, and where half of their width is idle.  Measured (us, it
-        // against the pairs), 8 experts of 1024 x 4096: data 12.6 to 18.8 at one row per expert, 18.8 to 19.7 at
-        // eight, forward (128 tiles) 11.5 to 12.0 and 15.0 to 15.2; at 16 rows forward 18.6 to 15.5.  64 experts:
-        // 128 deep x 16384 45 to 86 at one row, 48 to 89 at eight; 512 x 4096 47 to 51 and 48 to 49; 8192 wide x 256
-        // deep 48 to 70; 16384 deep x 128 wide 48 to 63; but 1024 x 2048 47 to 45, 2048 deep x 1024 49 to 47.
+        // Up to eight rows per expert: the filters' bytes are the time.  The few-rows kernel shares them out better where
+        // its tiles are many enough to be drawn, or so few that the pairs' 256-wide tiles do not fill two rounds, or
+        // where half of a pair's tile would be idle.  Measured (us, it against the pairs; one row per expert, eight
+        // rows).  64 experts, drawn: 2048 deep x 1024 44.6 to 47.3, 45.6 to 48.8; 1024 x 2048 43.7 to 44.0, 45.6 to
+        // 45.8; 128 x 16384 44.9 to 49.3, 47.4 to 49.9.  Between: 4096 x 512 47.6 to 44.4, 49.8 to 45.6.  Narrow: 16384 x
+        // 128 47.5 to 63.0, 52.0 to 63.5.  Few tiles, 8 experts: 4096 deep x 1024 12.6 to 18.8, 18.8 to 19.7; 1024 x
+        // 4096 11.5 to 12.0, 15.0 to 15.2, at 16 rows 18.6 to 15.5.
         const int64_t stream_blocks =
             (rows / kStreamRows + std::min<int64_t>(d.experts, rows)) * ((wo + 127) / 128) * ((wa + 63) / 64);
-        if (!weight && rows <= 8 * d.experts &&
-            (mt * std::min<int64_t>(d.experts, rows) <= 2 * pairs || wa <= 512 || wo <= 128) && stream_blocks <= 0x7fffffff) {
+        const int64_t used = std::min<int64_t>(d.experts, rows);
+        if (!weight && rows <= 8 * d.experts && (mt * used <= 2 * pairs || (wo + 127) / 128 * used >= 6 * pairs || wo <= 128) && stream_blocks <= 0x7fffffff) {
             ExpertStreamParams sp;
             std::memset(&sp, 0, sizeof(sp));
             const bool ok = map_filters(&sp.a, b, d, false, 64, dir == kExpForward ? 128 : 64) &&
@@ -260,6 +260,7 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
             sp.out = out; sp.offsets = offsets; sp.status = p->dev.status();
             sp.arrived = reinterpret_cast<int32_t *>(p->dev.rest());
             sp.parts = reinterpret_cast<float *>(static_cast<char *>(p->dev.mem) + p->off_parts);
+            sp.drawn = reinterpret_cast<int32_t *>(p->dev.ticket());
             sp.wait_budget = (int64_t)p->dev.clock_khz * 2000;
             sp.ldo = ldo;
             sp.experts = (int32_t)d.experts; sp.rows = (int32_t)rows; sp.K = (int32_t)d.K; sp.N = (int32_t)d.N;

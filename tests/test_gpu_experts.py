@@ -421,3 +421,19 @@ def test_few_rows_shallow_and_narrow(T, way, deep, wide):
     for rows_of in ([1] * experts, [0, 3] * (experts // 2), [0] * (experts - 1) + [8 * experts]):
         off = offsets(rows_of)
         run_way(T, plan, way, k, n, off, off[-1], "bf16", 24)
+
+
+# Few rows and enough tiles (128 of the filter's side each) to be drawn from a counter: every tile exactly once, call after
+# call, the same bits whatever block drew it.
+@pytest.mark.parametrize("way", ["forward", "data"])
+def test_few_rows_drawn_tiles(T, way):
+    deep, wide, experts = 576, 1040, 96
+    k, n = (deep, wide) if way == "forward" else (wide, deep)
+    plan = T.Experts(experts, k, n)
+    first = None
+    for rows_of in ([1] * experts, [5, 0, 17, 1] * (experts // 4), [5, 0, 17, 1] * (experts // 4), [8 * experts] + [0] * (experts - 1)):
+        off = offsets(rows_of)
+        got = run_way(T, plan, way, k, n, off, off[-1], "bf16", 25)
+        if rows_of[0] == 5:
+            assert first is None or torch.equal(first, got)
+            first = got
