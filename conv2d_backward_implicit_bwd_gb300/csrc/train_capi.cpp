@@ -210,6 +210,9 @@ conv_bwd_status conv_bwd_experts_destroy(conv_bwd_experts_plan p) {
     return CONV_BWD_OK;
 }
 
+// of rows and of tiles: the kernels step past the last one by up to a grid or a slice, in 32 bits
+constexpr int64_t kMostRows = 0x7fff0000;
+
 static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t rows, const void *a, int64_t lda,
                                    const void *b, int64_t ldb, const int32_t *offsets, void *out, int64_t ldo,
                                    int32_t accumulate, void *stream) {
@@ -226,11 +229,11 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
     const bool weight = dir == CONV_BWD_EXPERTS_WEIGHT;
     if (((uintptr_t)a | (uintptr_t)b) % es || (uintptr_t)offsets % 4 || (uintptr_t)out % (weight ? 4 : es))
         return CONV_BWD_ERR_MISALIGNED;
-    if (rows > 0x7fffffff || lda > (1LL << 31) || ldb > (1LL << 31) || ldo > (1LL << 31)) return CONV_BWD_ERR_UNSUPPORTED;
+    if (rows > kMostRows || lda > (1LL << 31) || ldb > (1LL << 31) || ldo > (1LL << 31)) return CONV_BWD_ERR_UNSUPPORTED;
     // most tiles of any kernel: 64 rows x 64 columns
     const int64_t nt = (wo + 63) / 64;
     const int64_t tiles = weight ? d.experts * ((d.N + 63) / 64) * nt : (rows / 64 + d.experts) * nt;
-    if (tiles > 0x7fffffff) return CONV_BWD_ERR_UNSUPPORTED;
+    if (tiles > kMostRows) return CONV_BWD_ERR_UNSUPPORTED;
     const size_t na = extent(rows, lda, wa, es), nb = weight ? extent(rows, ldb, d.K, es) : nw * es,
                  no = weight ? nw * 4 : extent(rows, ldo, wo, es);
     if (overlap(a, na, out, no) || overlap(b, nb, out, no) || overlap(offsets, (size_t)(d.experts + 1) * 4, out, no))

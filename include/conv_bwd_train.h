@@ -74,7 +74,7 @@ conv_bwd_status conv_bwd_experts_destroy(conv_bwd_experts_plan plan);
  * writes zeros or, accumulating, nothing).
  * Errors: INVALID_ARG (NULL pointer, rows < 0, ld smaller than the row,
  * output overlapping an input), MISALIGNED (a pointer not aligned to its
- * element), UNSUPPORTED (rows >= 2^31 or more than 2^31 - 1 output tiles),
+ * element), UNSUPPORTED (rows or output tiles > 2^31 - 2^16),
  * CUDA. */
 conv_bwd_status conv_bwd_experts_forward(conv_bwd_experts_plan plan, int64_t rows, const void *x, int64_t ldx,
                                          const void *w, const int32_t *offsets, void *y, int64_t ldy, void *stream);
@@ -85,7 +85,8 @@ conv_bwd_status conv_bwd_experts_weight(conv_bwd_experts_plan plan, int64_t rows
                                         int32_t accumulate, void *stream);
 
 /* Synchronise `stream`, read and clear the plan's status word, as
- * conv_bwd_data_get_status. */
+ * conv_bwd_data_get_status.  After a wait that ran out this also makes the
+ * plan's workspace ready for the next run. */
 conv_bwd_status conv_bwd_experts_get_status(conv_bwd_experts_plan plan, void *stream, int32_t *detail);
 
 /* ---- global gradient norm and clipping --------------------------------------
