@@ -10,8 +10,6 @@
 // 1001 x 1001 381 us (43 TFLOP/s; single FMAs 416 us, A stored twice to save the
 // broadcasts 544 us, one block of 255 registers an SM 409 us).  Small products wait
 // on latency: 1500 rows as one expert, weight of 100 x 100, 10 us (unsplit 71 us).
-// A few rows per expert leave most of a tile idle: 64 filters of 2048 x 1024, one
-// row each, 200 us, 0.4 of the memory rate.
 #include "expert_pieces.cuh"
 
 namespace cbd {

@@ -54,6 +54,7 @@ struct ExpertSimtParams {
 };
 // most pieces of a launch with split tiles, for an SM
 constexpr int kSimtPieces = 2;
+cudaError_t launch_experts_few_f32(const ExpertSimtParams &p, int dir, int num_sms, cudaStream_t s);
 cudaError_t launch_experts_f32(const ExpertSimtParams &p, int dir, cudaStream_t s);
 cudaError_t launch_experts_b16(const ExpertSimtParams &p, int dir, cudaStream_t s);
 

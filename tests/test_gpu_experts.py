@@ -437,3 +437,15 @@ def test_few_rows_drawn_tiles(T, way):
         if rows_of[0] == 5:
             assert first is None or torch.equal(first, got)
             first = got
+
+
+# fp32 with few rows: vector and single loads, groups of eight rows that end inside, narrow and wide sides.
+@pytest.mark.parametrize("way", ["forward", "data"])
+@pytest.mark.parametrize("k,n", [(132, 1028), (2052, 96), (33, 130), (1, 7), (131, 1), (514, 513)])
+def test_few_rows_fp32(T, way, k, n):
+    experts = 24
+    plan = T.Experts(experts, k, n, "f32")
+    for rows_of in ([1] * experts, [0, 9, 3] * (experts // 3), [0] * (experts - 1) + [8 * experts - 1]):
+        off = offsets(rows_of)
+        for pad in (0, 1, 4):
+            run_way(T, plan, way, k, n, off, off[-1], "f32", 26, ld_pad=pad)
