@@ -85,14 +85,15 @@ struct Bars {
     uint32_t tmem;
     int32_t abort;
 };
-template <int DIR>
+template <int DIR, bool LOOSE>
 struct Cfg {
     static constexpr bool W = DIR == kExpWeight;
+    static constexpr int B_WARPS = LOOSE ? 8 : 2;
     static constexpr int S = W ? 5 : 6;                  // pipeline stages
     static constexpr int OUT_BYTES = W ? 32768 : 16384;  // epilogue staging
     static constexpr int EPI = W ? 8 : 4;                // epilogue warps 0 .. EPI - 1
-    static constexpr int LOAD_A = EPI, MMA = EPI + 1, LOAD_B = EPI + 2, HELP = EPI + 4, SCHED = EPI + 5;
-    static constexpr int THREADS = W ? 512 : 320;  // weight: two warpgroups of epilogue, two of the others
+    static constexpr int LOAD_A = EPI, MMA = EPI + 1, HELP = EPI + 2, SCHED = EPI + 3, LOAD_B = EPI + 4;
+    static constexpr int THREADS = W || LOOSE ? 512 : 320;  // weight: two warpgroups of epilogue, two of the others
     static constexpr int SMEM = 1024 + S * (A_BYTES + B_BYTES) + OUT_BYTES + (int)sizeof(ExpertTable) + 8 + (int)sizeof(Bars);
     static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
@@ -142,6 +143,11 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// What this CTA's fence.proxy.async has made visible to the MMA is ready.  (A release at cluster scope would wait for
+// the loads in flight as well.)
+__device__ __forceinline__ void arrive_written(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // mbar_wait_bounded that also acquires what the arriving thread of either CTA of the pair wrote before
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;
@@ -171,6 +177,30 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, int6
     }
 }
 
+// The elements of a 16-byte line that lie in [begin, end), zeros elsewhere.
+__device__ __noinline__ uint4 line_by_element(uintptr_t line, uintptr_t begin, uintptr_t end) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uintptr_t q = line + 4 * i;
+        const uint32_t a = q >= begin && q < end ? *reinterpret_cast<const uint16_t *>(q) : 0u;
+        const uint32_t b = q + 2 >= begin && q + 2 < end ? *reinterpret_cast<const uint16_t *>(q + 2) : 0u;
+        w[i] = a | b << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// eight elements from element s of lo on, over two lines
+__device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, int s) {
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = s & 4 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = s & 2 ? w[i + 1] : w[i];
+    const uint32_t by = (s & 1) * 16;
+    return make_uint4(__funnelshift_r(w[0], w[1], by), __funnelshift_r(w[1], w[2], by), __funnelshift_r(w[2], w[3], by),
+                      __funnelshift_r(w[3], w[4], by));
+}
+
 template <int DIR>
 __device__ __forceinline__ ExpertWork decode(const ExpertPairParams &p, const ExpertTable &tab, int mt, int t) {
     ExpertWork w;
@@ -195,9 +225,10 @@ __device__ __forceinline__ ExpertWork decode(const ExpertPairParams &p, const Ex
     return w;
 }
 
-template <int DIR>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1) experts_pair_kernel(const __grid_constant__ ExpertPairParams p) {
-    using C = Cfg<DIR>;
+template <int DIR, bool LOOSE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THREADS, 1) experts_pair_kernel(const __grid_constant__ ExpertPairParams p) {
+    using C = Cfg<DIR, LOOSE>;
+    static_assert(!LOOSE || DIR != kExpWeight, "weight loads both operands with TMA");
     constexpr int S = C::S;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -218,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full0 + 8 * s, 1);
+            mbar_init(full0 + 8 * s, LOOSE ? 1 + 2 * C::B_WARPS : 1);
             mbar_init(empty0 + 8 * s, 1);
             mbar_init(tail0 + 8 * s, 1);
             mbar_init(peer0 + 8 * s, 1);
@@ -227,8 +258,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
             mbar_init(tfull0 + 8 * b, 1);
             mbar_init(tempty0 + 8 * b, 2 * C::EPI);  // epilogue warps of both CTAs
         }
-        // loads (3), epilogue, the leader's MMA, weight's helper
-        bars.ring.init(3 + C::EPI + (leader ? 1 : 0) + (DIR == kExpWeight ? 1 : 0));
+        // loads, epilogue, the leader's MMA, weight's helper
+        bars.ring.init(1 + C::B_WARPS + C::EPI + (leader ? 1 : 0) + (DIR == kExpWeight ? 1 : 0));
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -239,7 +270,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
     }
     if (warp == C::LOAD_A && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
+        if (!LOOSE) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
     }
     cluster_sync_all();
     tc_fence_after();
@@ -357,6 +388,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
                     // one barrier per group: a buffer is written again after the next group's barrier, which
                     // every warp reaches after reading it
                     asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (LOOSE && !p.out_lines) {
+                        // element by element, 32 neighbours an instruction
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) {
+                            const int r = warp * 8 + q / 4, c = q % 4 * 32 + lane;
+                            uint16_t x;
+                            asm volatile("ld.shared.b16 %0, [%1];" : "=h"(x) : "r"(sb + (uint32_t)r * 256u + (uint32_t)c * 2u) : "memory");
+                            if (ok && m + c < mdim && g + r < w.ntok) *reinterpret_cast<uint16_t *>(dst - col + c + (int64_t)(g + r) * p.ldo) = x;
+                        }
+                        continue;
+                    }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const int r = warp * 8 + q * 2 + (lane >> 4);
@@ -391,6 +433,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
                 }
             }
             __syncwarp();
+        } else if (LOOSE && warp >= C::LOAD_B) {
+            if constexpr (LOOSE) {
+                // -------------------------------------------------------- rows that TMA cannot load
+                // A thread takes line c of a row's 128 bytes of a k-block, of rows 32 apart, two k-blocks in flight; the
+                // eight elements that belong together lie on its line and the next thread's (of the last, the next
+                // k-block's first).  Shifted, they go where TMA would put them.  Rows past the tile are other columns of
+                // D: they stay as they are.
+                const int th = threadIdx.x - C::LOAD_B * 32, c = th & 7, r0 = th >> 3;
+                const uint32_t full_leader0 = mapa_shared(full0, 0);
+                const uint32_t to = (uint32_t)r0 * 128u + (uint32_t)((c ^ (r0 & 7)) << 4);
+                const int depth = DIR == kExpForward ? p.K : p.N;
+                const uintptr_t begin = reinterpret_cast<uintptr_t>(p.rows_at), end = reinterpret_cast<uintptr_t>(p.rows_end);
+                uint32_t it = 0;
+                bool ok = true;
+                for (uint32_t i = 0; ok; ++i) {
+                    const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
+                    if (!__all_sync(0xffffffffu, w.n != 0)) break;
+                    if (lane == 0) bars.ring.done(i);
+                    const int half = w.n / 2, at = (int)rank * half;
+                    uintptr_t src[4];  // first line of the row, in its low bits the row's first element there
+                    bool in[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = r0 + 32 * j;
+                        in[j] = r < half && at + r < w.ntok;
+                        src[j] = begin + (uintptr_t)((int64_t)(w.row0 + (in[j] ? at + r : 0)) * p.ldb * 2);
+                    }
+                    auto fetch = [&](int kb, uint4 (&x)[4]) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int off = kb * 128 + c * 16, s2 = (int)(src[j] & 15);
+                            x[j] = make_uint4(0u, 0u, 0u, 0u);
+                            if (in[j] && off < depth * 2 + s2) {
+                                const uintptr_t line = src[j] - s2 + off;
+                                if (line >= begin && line + 16 <= end)
+                                    x[j] = *reinterpret_cast<const uint4 *>(line);
+                                else
+                                    x[j] = line_by_element(line, src[j], src[j] + 2 * (uintptr_t)depth);
+                            }
+                        }
+                    };
+                    auto park = [&](int kb, const uint4 (&x)[4], const uint4 (&next)[4]) {
+                        const uint32_t s = it % S, ph = (it / S) & 1;
+                        ++it;
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty0 + 8 * s, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer));
+                        if (!ok) return;
+                        const uint32_t dst = smem_u32(sB + s * B_BYTES) + to;
+                        const bool deep = kb * 64 + c * 8 < depth;  // (the depth is a multiple of 8)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int from = (lane & 24) | ((lane + 1) & 7);
+                            uint4 hi;
+                            hi.x = __shfl_sync(0xffffffffu, c == 0 ? next[j].x : x[j].x, from);
+                            hi.y = __shfl_sync(0xffffffffu, c == 0 ? next[j].y : x[j].y, from);
+                            hi.z = __shfl_sync(0xffffffffu, c == 0 ? next[j].z : x[j].z, from);
+                            hi.w = __shfl_sync(0xffffffffu, c == 0 ? next[j].w : x[j].w, from);
+                            if (in[j]) {
+                                uint4 v = shifted(x[j], hi, (int)(src[j] & 15) / 2);
+                                if (!deep) v = make_uint4(0u, 0u, 0u, 0u);
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (uint32_t)j * 4096u), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) arrive_written(full_leader0 + 8 * s);
+                    };
+                    uint4 x0[4], x1[4], x2[4], x3[4];
+                    fetch(0, x0);
+                    fetch(1, x1);
+                    fetch(2, x2);
+#pragma unroll 1
+                    for (int kb = 0; kb < w.kb1 && ok; kb += 4) {
+                        fetch(kb + 3, x3);
+                        park(kb, x0, x1);
+                        if (kb + 1 >= w.kb1 || !ok) break;
+                        fetch(kb + 4, x0);
+                        park(kb + 1, x1, x2);
+                        if (kb + 2 >= w.kb1 || !ok) break;
+                        fetch(kb + 5, x1);
+                        park(kb + 2, x2, x3);
+                        if (kb + 3 >= w.kb1 || !ok) break;
+                        fetch(kb + 6, x2);
+                        park(kb + 3, x3, x0);
+                    }
+                }
+            }
+            __syncwarp();
         } else if (warp == C::LOAD_A || warp == C::LOAD_B || warp == C::LOAD_B + 1) {
             // ------------------------------------------------------------ loads
             if (lane == 0) {
@@ -420,7 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
                             if (fix)
                                 mbar_arrive_expect_tx(tail0 + 8 * s, bytes);
                             else if (leader)
-                                mbar_arrive_expect_tx(full0 + 8 * s, 2 * bytes);
+                                mbar_arrive_expect_tx(full0 + 8 * s, LOOSE ? 2u * A_BYTES : 2 * bytes);
                             const uint32_t dst = smem_u32(sA + s * A_BYTES);
                             const int m = w.m0 + (int)rank * 128;
                             if constexpr (DIR == kExpForward) {
@@ -485,7 +614,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
                         uint32_t acc = 0;
                         const int end = DIR == kExpWeight && left > SEGMENT ? left - SEGMENT : 0;
                         for (; left > end; --left) {
-                            ok = __all_sync(0xffffffffu, mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
+                            // (LOOSE: the other CTA's warps wrote their half themselves)
+                            const bool full = LOOSE ? wait_cluster(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma)
+                                                    : mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma);
+                            ok = __all_sync(0xffffffffu, full);
                             if (!ok) break;
                             const uint32_t ad = a_lo + s * (A_BYTES >> 4), bd = b_lo + s * (B_BYTES >> 4);
                             const int n = DIR == kExpWeight && left == w.kb1 ? (w.last + 15) / 16 : 4;
@@ -553,7 +685,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
                 const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
                 const int64_t nfill = (int64_t)lo + (p.rows - hi);
                 for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
-                    uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
+                    __nv_bfloat16 *at = out + (f < lo ? f : hi + (f - lo)) * p.ldo;
+                    if (LOOSE && !p.out_lines) {
+                        for (int c = lane; c < mdim; c += 32) at[c] = __nv_bfloat16(0.f);
+                        continue;
+                    }
+                    uint4 *row = reinterpret_cast<uint4 *>(at);
                     for (int c = lane; c < vec; c += 32) row[c] = make_uint4(0u, 0u, 0u, 0u);
                 }
             }
@@ -568,23 +705,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR>::THREADS, 1
     }
 }
 
-template <int DIR>
+template <int DIR, bool LOOSE>
 cudaError_t launch_dir(const ExpertPairParams &p, int grid, cudaStream_t s) {
+    using C = Cfg<DIR, LOOSE>;
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(experts_pair_kernel<DIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DIR>::SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(experts_pair_kernel<DIR, LOOSE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    return launch_early(experts_pair_kernel<DIR>, grid, Cfg<DIR>::THREADS, Cfg<DIR>::SMEM, s, p);
+    return launch_early(experts_pair_kernel<DIR, LOOSE>, grid, C::THREADS, C::SMEM, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_experts_pair(const ExpertPairParams &p, int dir, int grid, cudaStream_t s) {
-    return dir == kExpForward ? launch_dir<kExpForward>(p, grid, s) : dir == kExpData ? launch_dir<kExpData>(p, grid, s) : launch_dir<kExpWeight>(p, grid, s);
+    if (p.rows_at) return dir == kExpForward ? launch_dir<kExpForward, true>(p, grid, s) : launch_dir<kExpData, true>(p, grid, s);
+    return dir == kExpForward ? launch_dir<kExpForward, false>(p, grid, s) : dir == kExpData ? launch_dir<kExpData, false>(p, grid, s) : launch_dir<kExpWeight, false>(p, grid, s);
 }
 
 }  // namespace cbd

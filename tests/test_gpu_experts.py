@@ -449,3 +449,34 @@ def test_few_rows_fp32(T, way, k, n):
         off = offsets(rows_of)
         for pad in (0, 1, 4):
             run_way(T, plan, way, k, n, off, off[-1], "f32", 26, ld_pad=pad)
+
+
+# Rows that no 16-byte line begins: odd and even strides and starts, tiles of one to many rows, all rows at both ends of the
+# tensor; the output on lines or not.
+@pytest.mark.parametrize("way", ["forward", "data"])
+@pytest.mark.parametrize("k,n", [(64, 256), (200, 520), (1032, 72), (8, 8)])
+def test_rows_off_the_lines(T, way, k, n):
+    plan = T.Experts(6, k, n)
+    for rows_of in ([1, 0, 2, 0, 0, 5], [300, 0, 64, 257, 1, 31], [0, 0, 1500, 0, 3, 0]):
+        off = offsets(rows_of)
+        for pad in (1, 2, 4, 17):
+            run_way(T, plan, way, k, n, off, off[-1], "bf16", 27, ld_pad=pad)
+    # only the input, only the output, only the first row's address
+    off = offsets([70, 0, 33, 1, 0, 129])
+    rows = off[-1]
+    wa, wo = (k, n) if way == "forward" else (n, k)
+    g = torch.Generator(device="cuda").manual_seed(28)
+    w = torch.randn(6, n, k, generator=g, device="cuda").bfloat16()
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+    call = plan.forward if way == "forward" else plan.backward_data
+    for pad_in, pad_out, first in ((3, 0, 0), (0, 3, 0), (0, 0, 1), (0, 8, 5), (8, 2, 3)):
+        flat = torch.full((first + rows * (wa + pad_in),), float("nan"), device="cuda").bfloat16()
+        a = flat[first:].view(rows, wa + pad_in)[:, :wa]
+        a.copy_(torch.randn(rows, wa, generator=g, device="cuda"))
+        out = torch.full((rows, wo + pad_out), float("nan"), device="cuda").bfloat16()[:, :wo]
+        got = call(a, w, o, out=out)
+        want, mag = reference(way, a, w, off, 6, k, n, rows)
+        check(got, want, mag, wa, True, f"{way} {pad_in} {pad_out} {first}")
+        if pad_out:
+            assert torch.isnan(out._base[:, wo:]).all()
+    assert plan.status() == (0, 0)
