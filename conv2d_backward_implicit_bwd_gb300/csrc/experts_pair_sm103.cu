@@ -52,9 +52,15 @@
 // reading the old gradient into the epilogue's staging and storing the sum was no
 // faster (82 to 86 us against 78): the mix of reads and writes is the time.
 //
+// Rows off the 16-byte lines (strides or addresses; forward and data) cannot come by
+// TMA.  Eight warps read them in whole lines, shift them into place in registers and
+// write the swizzled tile themselves; only lines inside the tensor are read whole.
+// The 16384 rows above with a stride of 1041: 123 us forward, 135 data (on warp-level
+// MMAs 511 and 475).  Bound by the way of a k-block through a warp: two in flight.
+//
 // Roles per CTA, in warps: epilogue 4 (weight 8, with most of the registers), A
-// loads 1, MMA (leader CTA) and TMEM 1, B loads 2, helper 1 (weight: partial
-// blocks; else rows of no expert), schedule 1.  Every wait is bounded.
+// loads 1, MMA (leader CTA) and TMEM 1, B loads 2 (off the lines 8), helper 1 (weight:
+// partial blocks; else rows of no expert), schedule 1.  Every wait is bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -62,6 +68,7 @@
 #include "device_util.cuh"
 #include "expert_table.cuh"
 #include "internal.h"
+#include "lines.cuh"
 #include "tc_common.cuh"
 #include "train.h"
 
@@ -175,30 +182,6 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, int6
             }
         }
     }
-}
-
-// The elements of a 16-byte line that lie in [begin, end), zeros elsewhere.
-__device__ __noinline__ uint4 line_by_element(uintptr_t line, uintptr_t begin, uintptr_t end) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uintptr_t q = line + 4 * i;
-        const uint32_t a = q >= begin && q < end ? *reinterpret_cast<const uint16_t *>(q) : 0u;
-        const uint32_t b = q + 2 >= begin && q + 2 < end ? *reinterpret_cast<const uint16_t *>(q + 2) : 0u;
-        w[i] = a | b << 16;
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-// eight elements from element s of lo on, over two lines
-__device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, int s) {
-    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = s & 4 ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = s & 2 ? w[i + 1] : w[i];
-    const uint32_t by = (s & 1) * 16;
-    return make_uint4(__funnelshift_r(w[0], w[1], by), __funnelshift_r(w[1], w[2], by), __funnelshift_r(w[2], w[3], by),
-                      __funnelshift_r(w[3], w[4], by));
 }
 
 template <int DIR>

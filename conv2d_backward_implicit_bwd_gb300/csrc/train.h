@@ -40,6 +40,7 @@ constexpr int kMaxRows = 0x7fffffff;
 struct ExpertSimtParams {
     const void *a;           // x (forward), dy (data, weight)
     const void *b;           // w (forward, data), x (weight)
+    const void *a_end, *b_end;
     void *out;               // y, dx or dw
     const int32_t *offsets;  // [experts + 1]
     int32_t *status;

@@ -306,7 +306,7 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
     };
     ExpertSimtParams sp;
     std::memset(&sp, 0, sizeof(sp));
-    sp.a = a; sp.b = b; sp.out = out; sp.offsets = offsets; sp.status = p->dev.status();
+    sp.a = a; sp.b = b; sp.a_end = static_cast<const char *>(a) + na; sp.b_end = static_cast<const char *>(b) + nb; sp.out = out; sp.offsets = offsets; sp.status = p->dev.status();
     sp.lda = lda; sp.ldb = ldb; sp.ldo = ldo;
     sp.experts = (int32_t)d.experts; sp.rows = (int32_t)rows; sp.K = (int32_t)d.K; sp.N = (int32_t)d.N;
     sp.accumulate = accumulate ? 1 : 0;
