@@ -268,10 +268,9 @@ class GradClip(_Plan):
         g = self._pointers(grads, "grads")
         o = g if out is None else self._pointers(out, "out")
         device = self._device(grads)
-        both = _empty((2, 1), torch.float32, device, stream)
-        at = both.data_ptr()
-        _check(_lib.conv_bwd_clip_run(self._h, g.buffer_info()[0], o.buffer_info()[0], max_norm, at, at + 4, _stream(stream, device)), "conv_bwd_clip_run")
-        return both[0], both[1]
+        norm, coef = _empty((1,), torch.float32, device, stream), _empty((1,), torch.float32, device, stream)
+        _check(_lib.conv_bwd_clip_run(self._h, g.buffer_info()[0], o.buffer_info()[0], max_norm, norm.data_ptr(), coef.data_ptr(), _stream(stream, device)), "conv_bwd_clip_run")
+        return norm, coef
 
     def status(self, stream=None):
         """(status, detail) of the calls since the last one; synchronises the stream."""
@@ -315,10 +314,10 @@ class PolicyLoss(_Plan):
         """(loss [1], logp, lse, coef [tokens]); lse and coef are what ``backward`` needs."""
         t, args = self._inputs(logits, actions, advantage, weight, old_logp, ref_logp)
         device = logits.device
-        s = _empty((3 * t + 1,), torch.float32, device, stream)
-        at = s.data_ptr()
-        _check(_lib.conv_bwd_policy_forward(*args, at + 12 * t, at, at + 4 * t, at + 8 * t, _stream(stream, device)), "conv_bwd_policy_forward")
-        logp, lse, coef, loss = s.split_with_sizes((t, t, t, 1))
+        # (four tensors: views of one that is new cost more than its memory)
+        logp, lse, coef = (_empty((t,), torch.float32, device, stream) for _ in range(3))
+        loss = _empty((1,), torch.float32, device, stream)
+        _check(_lib.conv_bwd_policy_forward(*args, loss.data_ptr(), logp.data_ptr(), lse.data_ptr(), coef.data_ptr(), _stream(stream, device)), "conv_bwd_policy_forward")
         return loss, logp, lse, coef
 
     def backward(self, logits, actions, lse, coef, grad=None, out=None, stream=None):
