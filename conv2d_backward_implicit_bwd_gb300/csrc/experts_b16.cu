@@ -1,5 +1,5 @@
-// experts_b16.cu -- matrix products grouped by expert for bf16 tensors that TMA
-// cannot load: widths, strides or addresses that are no multiple of 16 bytes.
+// experts_b16.cu -- matrix products grouped by expert for bf16 tensors whose widths,
+// filters or filter gradients are no multiple of 16 bytes (TMA cannot move those).
 //
 // The loads are the time here: single elements, two where the addresses allow it, or
 // (weight) 16-byte lines that are shifted into place.  So the matrix instruction is the warp-level m16n8k16 on shared memory that

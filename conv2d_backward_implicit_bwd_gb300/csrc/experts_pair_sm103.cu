@@ -52,11 +52,13 @@
 // reading the old gradient into the epilogue's staging and storing the sum was no
 // faster (82 to 86 us against 78): the mix of reads and writes is the time.
 //
-// Rows off the 16-byte lines (strides or addresses; forward and data) cannot come by
-// TMA.  Eight warps read them in whole lines, shift them into place in registers and
-// write the swizzled tile themselves; only lines inside the tensor are read whole.
-// The 16384 rows above with a stride of 1041: 123 us forward, 135 data (on warp-level
-// MMAs 511 and 475).  Bound by the way of a k-block through a warp: two in flight.
+// Rows off the 16-byte lines (strides or addresses) cannot come by TMA.  Warps (eight;
+// weight four, for both operands) read them in whole lines, shift them into place in
+// registers and write the swizzled tile themselves; only lines inside the tensor are
+// read whole.  The 16384 rows above with a stride of 1041: 123 us forward, 135 data,
+// 370 weight (on warp-level MMAs 511, 475 and 547).  Bound by the way of a k-block
+// through a warp, its shuffles and shifts: two in flight, in weight three batches of
+// eight, with the registers that the sums leave.
 //
 // Roles per CTA, in warps: epilogue 4 (weight 8, with most of the registers), A
 // loads 1, MMA (leader CTA) and TMEM 1, B loads 2 (off the lines 8), helper 1 (weight:
@@ -95,7 +97,7 @@ struct Bars {
 template <int DIR, bool LOOSE>
 struct Cfg {
     static constexpr bool W = DIR == kExpWeight;
-    static constexpr int B_WARPS = LOOSE ? 8 : 2;
+    static constexpr int B_WARPS = !LOOSE ? 2 : W ? 4 : 8;  // (weight off the lines: of both operands)
     static constexpr int S = W ? 5 : 6;                  // pipeline stages
     static constexpr int OUT_BYTES = W ? 32768 : 16384;  // epilogue staging
     static constexpr int EPI = W ? 8 : 4;                // epilogue warps 0 .. EPI - 1
@@ -211,7 +213,6 @@ __device__ __forceinline__ ExpertWork decode(const ExpertPairParams &p, const Ex
 template <int DIR, bool LOOSE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THREADS, 1) experts_pair_kernel(const __grid_constant__ ExpertPairParams p) {
     using C = Cfg<DIR, LOOSE>;
-    static_assert(!LOOSE || DIR != kExpWeight, "weight loads both operands with TMA");
     constexpr int S = C::S;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -232,7 +233,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full0 + 8 * s, LOOSE ? 1 + 2 * C::B_WARPS : 1);
+            mbar_init(full0 + 8 * s, (LOOSE && C::W ? 0 : 1) + (LOOSE ? 2 * C::B_WARPS : 0));
             mbar_init(empty0 + 8 * s, 1);
             mbar_init(tail0 + 8 * s, 1);
             mbar_init(peer0 + 8 * s, 1);
@@ -241,8 +242,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
             mbar_init(tfull0 + 8 * b, 1);
             mbar_init(tempty0 + 8 * b, 2 * C::EPI);  // epilogue warps of both CTAs
         }
-        // loads, epilogue, the leader's MMA, weight's helper
-        bars.ring.init(1 + C::B_WARPS + C::EPI + (leader ? 1 : 0) + (DIR == kExpWeight ? 1 : 0));
+        // B loads, epilogue, the leader's MMA; A loads, weight's helper (neither in weight off the lines)
+        bars.ring.init(C::B_WARPS + C::EPI + (leader ? 1 : 0) + (LOOSE && C::W ? 0 : C::W ? 2 : 1));
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -252,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
         tc_fence_before();
     }
     if (warp == C::LOAD_A && lane == 0) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
+        if (!(LOOSE && C::W)) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.a)) : "memory");
         if (!LOOSE) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.b)) : "memory");
     }
     cluster_sync_all();
@@ -270,9 +271,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
         if (ld_shared_cluster_u32(mapa_shared(smem_u32(&bars.tmem), 0)) != tmem_base) record_status(p.status, kDevFaultIndex);
     }
 
-    // weight: 128 registers a thread at launch (512 threads), 192 for the epilogue with its sums, 64 for the others
+    // weight: 128 registers a thread at launch (512 threads), 192 for the epilogue with its sums, 64 for the others (off
+    // the lines 160 and 96)
     if (warp < C::EPI) {
-        if constexpr (DIR == kExpWeight) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        if constexpr (DIR == kExpWeight) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LOOSE ? 160 : 192));
         // ------------------------------------------------------------ epilogue (both CTAs)
         const uint32_t tempty_leader0 = mapa_shared(tempty0, 0);
         const uint32_t lane_base = tmem_base + ((uint32_t)((warp % 4) * 32) << 16);
@@ -400,7 +402,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
         }
         if constexpr (DIR == kExpWeight) bulk_wait_all();
     } else {
-        if constexpr (DIR == kExpWeight) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if constexpr (DIR == kExpWeight) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LOOSE ? 96 : 64));
         if (warp == C::SCHED) {
             // ------------------------------------------------------------ schedule
             if constexpr (DIR != kExpWeight) asm volatile("bar.arrive 2, 64;" ::: "memory");
@@ -417,7 +419,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
             }
             __syncwarp();
         } else if (LOOSE && warp >= C::LOAD_B) {
-            if constexpr (LOOSE) {
+            if constexpr (LOOSE && DIR == kExpWeight) {
+                // -------------------------------------------------------- weight: rows that TMA cannot load, both operands
+                // A k-block in eight batches of 16 rows, four of dy and four of x, three in flight.  A thread takes line
+                // c of each half of a row's 256 bytes; what follows the second half's last is c = 0's third line.  Rows
+                // past the expert's end are zeros.
+                const int th = threadIdx.x - C::LOAD_B * 32, c = th & 7, r0 = th >> 3;
+                const uint32_t full_leader0 = mapa_shared(full0, 0);
+                const uint32_t to = (uint32_t)r0 * 128u + (uint32_t)((c ^ (r0 & 7)) << 4);
+                const int from = (lane & 24) | ((lane + 1) & 7);
+                struct Batch {
+                    uint4 x0, x1, after;
+                    int shift;
+                };
+                uint32_t it = 0;
+                bool ok = true;
+                for (uint32_t i = 0; ok; ++i) {
+                    const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
+                    if (!__all_sync(0xffffffffu, w.n != 0)) break;
+                    if (lane == 0) bars.ring.done(i);
+                    // batch f of the tile: k-block f / 8 (the partial one first), rows 16 (f & 3) on, of dy if !(f & 4)
+                    const int batches = w.kb1 * 8;
+                    auto fetch = [&](int f, Batch &x) {
+                        const int kb = f >> 3, r = (f & 3) * 16 + r0, valid = kb == 0 ? w.last : 64;
+                        x.x0 = x.x1 = x.after = make_uint4(0u, 0u, 0u, 0u);
+                        x.shift = 0;
+                        if (f >= batches || r >= valid) return;
+                        const bool b = f & 4;
+                        const uintptr_t begin = reinterpret_cast<uintptr_t>(b ? p.rows2_at : p.rows_at), end = reinterpret_cast<uintptr_t>(b ? p.rows2_end : p.rows_end);
+                        const int col = (b ? w.ntok : w.m0) + (int)rank * 128;
+                        const int64_t row = (int64_t)w.row0 + (kb == 0 ? w.kb1 - 1 : kb - 1) * 64 + r;
+                        const uintptr_t at = begin + (uintptr_t)((row * (b ? p.ldb2 : p.ldb) + col) * 2), line = (at & ~uintptr_t(15)) + 16 * c;
+                        x.shift = (int)(at & 15) / 2;
+                        if (line >= begin && line + 144 <= end) {
+                            x.x0 = *reinterpret_cast<const uint4 *>(line);
+                            x.x1 = *reinterpret_cast<const uint4 *>(line + 128);
+                        } else {
+                            x.x0 = line_by_element(line, begin, end);
+                            x.x1 = line_by_element(line + 128, begin, end);
+                        }
+                        if (c == 0 && x.shift) x.after = load_line(line + 256, begin, end);
+                    };
+                    auto park = [&](int f, const Batch &x) {
+                        const uint32_t s = it % S, ph = (it / S) & 1;
+                        if ((f & 7) == 0) {
+                            ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty0 + 8 * s, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer));
+                            if (!ok) return;
+                        }
+                        const uint4 a = c == 0 ? x.x1 : x.x0, b = c == 0 ? x.after : x.x1;
+                        uint4 h0, h1;
+                        h0.x = __shfl_sync(0xffffffffu, a.x, from);
+                        h0.y = __shfl_sync(0xffffffffu, a.y, from);
+                        h0.z = __shfl_sync(0xffffffffu, a.z, from);
+                        h0.w = __shfl_sync(0xffffffffu, a.w, from);
+                        h1.x = __shfl_sync(0xffffffffu, b.x, from);
+                        h1.y = __shfl_sync(0xffffffffu, b.y, from);
+                        h1.z = __shfl_sync(0xffffffffu, b.z, from);
+                        h1.w = __shfl_sync(0xffffffffu, b.w, from);
+                        const uint4 v0 = shifted(x.x0, h0, x.shift), v1 = shifted(x.x1, h1, x.shift);
+                        const uint32_t dst = ((f & 4) ? smem_u32(sB + s * B_BYTES) : smem_u32(sA + s * A_BYTES)) + (uint32_t)(f & 3) * 2048u + to;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v0.x), "r"(v0.y), "r"(v0.z), "r"(v0.w) : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 8192u), "r"(v1.x), "r"(v1.y), "r"(v1.z), "r"(v1.w) : "memory");
+                        if ((f & 7) == 7) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) arrive_written(full_leader0 + 8 * s);
+                            ++it;
+                        }
+                    };
+                    Batch b0, b1, b2, b3;
+                    fetch(0, b0);
+                    fetch(1, b1);
+                    fetch(2, b2);
+#pragma unroll 1
+                    for (int f = 0; f < batches && ok; f += 4) {
+                        fetch(f + 3, b3);
+                        park(f, b0);
+                        if (!ok) break;
+                        fetch(f + 4, b0);
+                        park(f + 1, b1);
+                        fetch(f + 5, b1);
+                        park(f + 2, b2);
+                        fetch(f + 6, b2);
+                        park(f + 3, b3);
+                    }
+                }
+            } else if constexpr (LOOSE) {
                 // -------------------------------------------------------- rows that TMA cannot load
                 // A thread takes line c of a row's 128 bytes of a k-block, of rows 32 apart, two k-blocks in flight; the
                 // eight elements that belong together lie on its line and the next thread's (of the last, the next
@@ -453,7 +540,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                                 if (line >= begin && line + 16 <= end)
                                     x[j] = *reinterpret_cast<const uint4 *>(line);
                                 else
-                                    x[j] = line_by_element(line, src[j], src[j] + 2 * (uintptr_t)depth);
+                                    x[j] = line_by_element_call(line, src[j], src[j] + 2 * (uintptr_t)depth);
                             }
                         }
                     };
@@ -503,6 +590,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                 }
             }
             __syncwarp();
+        } else if (LOOSE && C::W && (warp == C::LOAD_A || warp == C::HELP)) {
+            // (the warps above load both operands, with their zeros)
         } else if (warp == C::LOAD_A || warp == C::LOAD_B || warp == C::LOAD_B + 1) {
             // ------------------------------------------------------------ loads
             if (lane == 0) {
@@ -705,7 +794,8 @@ cudaError_t launch_dir(const ExpertPairParams &p, int grid, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_experts_pair(const ExpertPairParams &p, int dir, int grid, cudaStream_t s) {
-    if (p.rows_at) return dir == kExpForward ? launch_dir<kExpForward, true>(p, grid, s) : launch_dir<kExpData, true>(p, grid, s);
+    if (p.rows_at)
+        return dir == kExpForward ? launch_dir<kExpForward, true>(p, grid, s) : dir == kExpData ? launch_dir<kExpData, true>(p, grid, s) : launch_dir<kExpWeight, true>(p, grid, s);
     return dir == kExpForward ? launch_dir<kExpForward, false>(p, grid, s) : dir == kExpData ? launch_dir<kExpData, false>(p, grid, s) : launch_dir<kExpWeight, false>(p, grid, s);
 }
 

@@ -4,18 +4,19 @@
 
 namespace cbd {
 
-// The elements of a 16-byte line that lie in [begin, end), zeros elsewhere.
-static __device__ __noinline__ uint4 line_by_element(uintptr_t line, uintptr_t begin, uintptr_t end) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uintptr_t q = line + 4 * i;
-        const uint32_t a = q >= begin && q < end ? *reinterpret_cast<const uint16_t *>(q) : 0u;
-        const uint32_t b = q + 2 >= begin && q + 2 < end ? *reinterpret_cast<const uint16_t *>(q + 2) : 0u;
-        w[i] = a | b << 16;
+// The elements of a 16-byte line that lie in [begin, end), zeros elsewhere.  (Only at the ends of a tensor: short code.)
+__device__ __forceinline__ uint4 line_by_element(uintptr_t line, uintptr_t begin, uintptr_t end) {
+    uint64_t a = 0, b = 0;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        const uintptr_t u = line + 2 * q, v = u + 8;
+        if (u >= begin && u < end) a |= (uint64_t)*reinterpret_cast<const uint16_t *>(u) << (16 * q);
+        if (v >= begin && v < end) b |= (uint64_t)*reinterpret_cast<const uint16_t *>(v) << (16 * q);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4((uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32));
 }
+// (as a call: in a loop over many loads the code of each would stand in the way)
+static __device__ __noinline__ uint4 line_by_element_call(uintptr_t line, uintptr_t begin, uintptr_t end) { return line_by_element(line, begin, end); }
 // eight elements from element s of lo on, over two lines
 __device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, int s) {
     uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};

@@ -480,3 +480,30 @@ def test_rows_off_the_lines(T, way, k, n):
         if pad_out:
             assert torch.isnan(out._base[:, wo:]).all()
     assert plan.status() == (0, 0)
+
+
+# The same for the weight gradient: both operands, one of them, first addresses; rows that end inside a step of 16, 64 and 512.
+@pytest.mark.parametrize("k,n", [(64, 256), (200, 520), (1032, 72), (8, 8)])
+def test_weight_of_rows_off_the_lines(T, k, n):
+    plan = T.Experts(6, k, n)
+    for rows_of in ([1, 0, 2, 0, 0, 5], [300, 0, 64, 257, 1, 31], [0, 0, 1500, 0, 3, 0]):
+        off = offsets(rows_of)
+        for pad in (1, 2, 4, 17):
+            run_way(T, plan, "weight", k, n, off, off[-1], "bf16", 29, ld_pad=pad, accumulate=pad > 2)
+    off = offsets([70, 0, 33, 1, 0, 600])
+    rows = off[-1]
+    g = torch.Generator(device="cuda").manual_seed(30)
+    o = torch.tensor(off, dtype=torch.int32, device="cuda")
+
+    def mat(width, pad, first):
+        flat = torch.full((first + rows * (width + pad),), float("nan"), device="cuda").bfloat16()
+        t = flat[first:].view(rows, width + pad)[:, :width]
+        t.copy_(torch.randn(rows, width, generator=g, device="cuda"))
+        return t
+    for pads in ((3, 0), (0, 3), (0, 0), (8, 8)):
+        for first in ((0, 1), (5, 0), (3, 7)):
+            dy, x = mat(n, pads[0], first[0]), mat(k, pads[1], first[1])
+            got = plan.backward_weight(dy, x, o)
+            want, mag = reference("weight", dy, x, off, 6, k, n, rows)
+            check(got, want, mag, 600, False, f"{pads} {first}")
+    assert plan.status() == (0, 0)
