@@ -373,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                     // one barrier per group: a buffer is written again after the next group's barrier, which
                     // every warp reaches after reading it
                     asm volatile("bar.sync 1, 128;" ::: "memory");
-                    if (LOOSE && !p.out_lines) {
+                    if (!p.out_lines) {
                         // element by element, 32 neighbours an instruction
 #pragma unroll
                         for (int q = 0; q < 32; ++q) {
@@ -530,6 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                         in[j] = r < half && at + r < w.ntok;
                         src[j] = begin + (uintptr_t)((int64_t)(w.row0 + (in[j] ? at + r : 0)) * p.ldb * 2);
                     }
+                    const bool any = __any_sync(0xffffffffu, in[0]), more = __any_sync(0xffffffffu, in[1]);
                     auto fetch = [&](int kb, uint4 (&x)[4]) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -551,19 +552,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                         if (!ok) return;
                         const uint32_t dst = smem_u32(sB + s * B_BYTES) + to;
                         const bool deep = kb * 64 + c * 8 < depth;  // (the depth is a multiple of 8)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int from = (lane & 24) | ((lane + 1) & 7);
+                        const int from = (lane & 24) | ((lane + 1) & 7);
+                        auto one = [&](int j) {
                             uint4 hi;
                             hi.x = __shfl_sync(0xffffffffu, c == 0 ? next[j].x : x[j].x, from);
                             hi.y = __shfl_sync(0xffffffffu, c == 0 ? next[j].y : x[j].y, from);
                             hi.z = __shfl_sync(0xffffffffu, c == 0 ? next[j].z : x[j].z, from);
                             hi.w = __shfl_sync(0xffffffffu, c == 0 ? next[j].w : x[j].w, from);
-                            if (in[j]) {
-                                uint4 v = shifted(x[j], hi, (int)(src[j] & 15) / 2);
-                                if (!deep) v = make_uint4(0u, 0u, 0u, 0u);
+                            uint4 v = shifted(x[j], hi, (int)(src[j] & 15) / 2);
+                            if (!deep) v = make_uint4(0u, 0u, 0u, 0u);
+                            if (in[j])
                                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (uint32_t)j * 4096u), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-                            }
+                        };
+                        // (a warp's four rows of j = 0 are the first to be there; without branches the four overlap)
+                        if (more) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) one(j);
+                        } else if (any) {
+                            one(0);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -758,7 +764,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                 const int64_t nfill = (int64_t)lo + (p.rows - hi);
                 for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
                     __nv_bfloat16 *at = out + (f < lo ? f : hi + (f - lo)) * p.ldo;
-                    if (LOOSE && !p.out_lines) {
+                    if (!p.out_lines) {
                         for (int c = lane; c < mdim; c += 32) at[c] = __nv_bfloat16(0.f);
                         continue;
                     }

@@ -204,9 +204,13 @@ __global__ void __launch_bounds__(THREADS, 1) experts_stream_kernel(const __grid
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
         const int lo = tab.off[0], hi = tab.off[p.experts], vec = mdim / 8;
         const int64_t nfill = (int64_t)lo + (p.rows - hi);
+        const bool lines = ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)p.ldo * 2) & 15) == 0;
         for (int64_t f = blockIdx.x; f < nfill; f += gridDim.x) {
-            uint4 *row = reinterpret_cast<uint4 *>(out + (f < lo ? f : hi + (f - lo)) * p.ldo);
-            for (int c = lane; c < vec; c += 32) row[c] = make_uint4(0u, 0u, 0u, 0u);
+            __nv_bfloat16 *row = out + (f < lo ? f : hi + (f - lo)) * p.ldo;
+            if (lines)
+                for (int c = lane; c < vec; c += 32) reinterpret_cast<uint4 *>(row)[c] = make_uint4(0u, 0u, 0u, 0u);
+            else
+                for (int c = lane; c < mdim; c += 32) row[c] = __nv_bfloat16(0.f);
         }
     } else if (warp == 4 || warp == 6) {
         // ------------------------------------------------------------ loads

@@ -71,12 +71,12 @@ struct ExpertPairParams {  // 128-byte aligned through CUtensorMap
     int64_t ldo;
     int32_t experts, rows, K, N;
     int32_t accumulate;
+    int32_t out_lines;       // forward, data: the output rows take 16-byte stores
     // where TMA cannot load the rows (else null): x (forward) or dy, its end and row stride
     const void *rows_at, *rows_end;
     int64_t ldb;
     const void *rows2_at, *rows2_end;  // weight: x
     int64_t ldb2;
-    int32_t out_lines;       // forward, data: the output rows take 16-byte stores
 };
 cudaError_t launch_experts_pair(const ExpertPairParams &p, int dir, int grid, cudaStream_t s);
 

@@ -242,9 +242,9 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
     if (rows == 0 && (!weight || accumulate)) return CONV_BWD_OK;
     // Tensor cores on pairs of SMs where TMA can load the filters or store their gradients (bf16, widths and address on 16 bytes); the rows come
     // by TMA if their strides and addresses are on 16 bytes too, else through registers.
-    const bool lines = lda % 8 == 0 && ldo % 8 == 0 && ldb % 8 == 0 && ((uintptr_t)a | (uintptr_t)b | (uintptr_t)out) % 16 == 0;
+    const bool rows_lines = lda % 8 == 0 && (uintptr_t)a % 16 == 0 && (!weight || (ldb % 8 == 0 && (uintptr_t)b % 16 == 0));
     if (d.dtype == CONV_BWD_BF16 && d.K % 8 == 0 && d.N % 8 == 0 && rows > 0 && d.K * d.N < (1LL << 37) &&
-        (lines || (uintptr_t)(weight ? out : b) % 16 == 0)) {
+        (uintptr_t)(weight ? out : b) % 16 == 0) {
         const int64_t mt = ((dir == kExpData ? d.K : d.N) + 255) / 256, pairs = std::max(1, p->dev.num_sms / 2);
         // Up to eight rows per expert: the filters' bytes are the time.  The few-rows kernel shares them out better where
         // its tiles are many enough to be drawn, or so few that the pairs' 256-wide tiles do not fill two rounds, or
@@ -256,7 +256,7 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
         const int64_t stream_blocks =
             (rows / kStreamRows + std::min<int64_t>(d.experts, rows)) * ((wo + 127) / 128) * ((wa + 63) / 64);
         const int64_t used = std::min<int64_t>(d.experts, rows);
-        if (lines && !weight && rows <= 8 * d.experts && (mt * used <= 2 * pairs || (wo + 127) / 128 * used >= 6 * pairs || wo <= 128) && stream_blocks <= 0x7fffffff) {
+        if (rows_lines && !weight && rows <= 8 * d.experts && (mt * used <= 2 * pairs || (wo + 127) / 128 * used >= 6 * pairs || wo <= 128) && stream_blocks <= 0x7fffffff) {
             ExpertStreamParams sp;
             std::memset(&sp, 0, sizeof(sp));
             const bool ok = map_filters(&sp.a, b, d, false, 64, dir == kExpForward ? 128 : 64) &&
@@ -277,11 +277,11 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
         std::memset(&pp, 0, sizeof(pp));
         bool ok;
         if (dir == kExpForward)
-            ok = map_filters(&pp.a, b, d, false, 64, 128) && (!lines || map_rows(&pp.b, a, d.K, rows, lda, 64));
+            ok = map_filters(&pp.a, b, d, false, 64, 128) && (!rows_lines || map_rows(&pp.b, a, d.K, rows, lda, 64));
         else if (dir == kExpData)
-            ok = map_filters(&pp.a, b, d, false, 64, 64) && (!lines || map_rows(&pp.b, a, d.N, rows, lda, 64));
+            ok = map_filters(&pp.a, b, d, false, 64, 64) && (!rows_lines || map_rows(&pp.b, a, d.N, rows, lda, 64));
         else
-            ok = (!lines || (map_rows(&pp.a, a, d.N, rows, lda, 64) && map_rows(&pp.b, b, d.K, rows, ldb, 64))) &&
+            ok = (!rows_lines || (map_rows(&pp.a, a, d.N, rows, lda, 64) && map_rows(&pp.b, b, d.K, rows, ldb, 64))) &&
                  map_filters(&pp.o, out, d, true, 32, 32);
         if (!ok) return CONV_BWD_ERR_CUDA;
         pp.out = out; pp.offsets = offsets; pp.status = p->dev.status();
@@ -289,14 +289,14 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
         pp.ldo = ldo;
         pp.experts = (int32_t)d.experts; pp.rows = (int32_t)rows; pp.K = (int32_t)d.K; pp.N = (int32_t)d.N;
         pp.accumulate = accumulate ? 1 : 0;
-        if (!lines) {
+        pp.out_lines = ldo % 8 == 0 && (uintptr_t)out % 16 == 0;
+        if (!rows_lines) {
             pp.rows_at = a;
             pp.rows_end = static_cast<const char *>(a) + na;
             pp.ldb = lda;
             pp.rows2_at = b;
             pp.rows2_end = static_cast<const char *>(b) + nb;
             pp.ldb2 = ldb;
-            pp.out_lines = ldo % 8 == 0 && (uintptr_t)out % 16 == 0;
         }
         const int64_t most = weight ? d.experts * mt * ((d.K + 255) / 256) : mt * (rows / 256 + std::min<int64_t>(d.experts, rows));
         const int grid = (int)(2 * std::max<int64_t>(1, std::min(pairs, most)));
