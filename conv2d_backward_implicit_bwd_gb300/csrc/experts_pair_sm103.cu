@@ -89,6 +89,7 @@ struct Bars {
     ExpertRing<RING> ring;
     uint64_t full[MAX_STAGES], empty[MAX_STAGES];
     uint64_t tail[MAX_STAGES], peer[MAX_STAGES];  // weight: partial blocks landed in this CTA; peer's rows zeroed
+                                                  // (off the lines, tail: this CTA's warps have written)
     uint64_t tfull[2], tempty[2];
     int32_t vote[8];  // forward, data: what each epilogue warp drew, two tiles in turn
     uint32_t tmem;
@@ -233,17 +234,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full0 + 8 * s, (LOOSE && C::W ? 0 : 1) + (LOOSE ? 2 * C::B_WARPS : 0));
+            mbar_init(full0 + 8 * s, (LOOSE && C::W ? 0 : 1) + (LOOSE ? 2 : 0));
             mbar_init(empty0 + 8 * s, 1);
-            mbar_init(tail0 + 8 * s, 1);
+            mbar_init(tail0 + 8 * s, LOOSE ? C::B_WARPS : 1);
             mbar_init(peer0 + 8 * s, 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
             mbar_init(tempty0 + 8 * b, 2 * C::EPI);  // epilogue warps of both CTAs
         }
-        // B loads, epilogue, the leader's MMA; A loads, weight's helper (neither in weight off the lines)
-        bars.ring.init(C::B_WARPS + C::EPI + (leader ? 1 : 0) + (LOOSE && C::W ? 0 : C::W ? 2 : 1));
+        // B loads, epilogue, the leader's MMA; A loads (not in weight off the lines); the helper (weight, off the lines)
+        bars.ring.init(C::B_WARPS + C::EPI + (leader ? 1 : 0) + (LOOSE && C::W ? 0 : 1) + (LOOSE || C::W ? 1 : 0));
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -425,7 +426,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                 // c of each half of a row's 256 bytes; what follows the second half's last is c = 0's third line.  Rows
                 // past the expert's end are zeros.
                 const int th = threadIdx.x - C::LOAD_B * 32, c = th & 7, r0 = th >> 3;
-                const uint32_t full_leader0 = mapa_shared(full0, 0);
                 const uint32_t to = (uint32_t)r0 * 128u + (uint32_t)((c ^ (r0 & 7)) << 4);
                 const int from = (lane & 24) | ((lane + 1) & 7);
                 struct Batch {
@@ -481,9 +481,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v0.x), "r"(v0.y), "r"(v0.z), "r"(v0.w) : "memory");
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 8192u), "r"(v1.x), "r"(v1.y), "r"(v1.z), "r"(v1.w) : "memory");
                         if ((f & 7) == 7) {
-                            fence_proxy_async_smem();
                             __syncwarp();
-                            if (lane == 0) arrive_written(full_leader0 + 8 * s);
+                            if (lane == 0) mbar_arrive(tail0 + 8 * s);
                             ++it;
                         }
                     };
@@ -511,7 +510,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                 // k-block's first).  Shifted, they go where TMA would put them.  Rows past the tile are other columns of
                 // D: they stay as they are.
                 const int th = threadIdx.x - C::LOAD_B * 32, c = th & 7, r0 = th >> 3;
-                const uint32_t full_leader0 = mapa_shared(full0, 0);
                 const uint32_t to = (uint32_t)r0 * 128u + (uint32_t)((c ^ (r0 & 7)) << 4);
                 const int depth = DIR == kExpForward ? p.K : p.N;
                 const uintptr_t begin = reinterpret_cast<uintptr_t>(p.rows_at), end = reinterpret_cast<uintptr_t>(p.rows_end);
@@ -571,9 +569,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                         } else if (any) {
                             one(0);
                         }
-                        fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) arrive_written(full_leader0 + 8 * s);
+                        if (lane == 0) mbar_arrive(tail0 + 8 * s);
                     };
                     uint4 x0[4], x1[4], x2[4], x3[4];
                     fetch(0, x0);
@@ -596,8 +593,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                 }
             }
             __syncwarp();
-        } else if (LOOSE && C::W && (warp == C::LOAD_A || warp == C::HELP)) {
-            // (the warps above load both operands, with their zeros)
+        } else if (LOOSE && C::W && warp == C::LOAD_A) {
+            // (the warps above load both operands)
         } else if (warp == C::LOAD_A || warp == C::LOAD_B || warp == C::LOAD_B + 1) {
             // ------------------------------------------------------------ loads
             if (lane == 0) {
@@ -721,7 +718,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
             __syncwarp();
         } else if (warp == C::HELP) {
             // ------------------------------------------------------------ helper: rows past an expert's end, rows of none
-            if constexpr (DIR == kExpWeight) {
+            if constexpr (LOOSE) {
+                // What the load warps have written is made visible to the MMA from here: their own fence would wait for
+                // the loads that they have in flight.
+                if (lane == 0) {
+                    const uint32_t full_leader0 = mapa_shared(full0, 0);
+                    uint32_t it = 0;
+                    bool ok = true;
+                    for (uint32_t i = 0; ok; ++i) {
+                        const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
+                        if (w.n == 0) break;
+                        bars.ring.done(i);
+                        for (int kb = 0; kb < w.kb1 && ok; ++kb, ++it) {
+                            const uint32_t s = it % S, ph = (it / S) & 1;
+                            ok = mbar_wait_bounded(tail0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
+                            if (!ok) break;
+                            fence_proxy_async_smem();
+                            arrive_written(full_leader0 + 8 * s);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            if constexpr (DIR == kExpWeight && !LOOSE) {
                 uint32_t it = 0, phase = 0;  // bit s: parity of the next use of tail[s] and peer[s]
                 for (uint32_t i = 0;; ++i) {
                     const ExpertWork w = bars.ring.take(i, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
@@ -756,7 +775,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                     }
                     if (!__all_sync(0xffffffffu, ok)) break;
                 }
-            } else {
+            }
+            if constexpr (DIR != kExpWeight) {
                 // forward, data: rows of no expert get zeros (16-byte stores; the width is a multiple of 8)
                 asm volatile("bar.sync 2, 64;" ::: "memory");  // the table
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out);
