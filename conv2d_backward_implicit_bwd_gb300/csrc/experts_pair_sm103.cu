@@ -55,10 +55,11 @@
 // Rows off the 16-byte lines (strides or addresses) cannot come by TMA.  Warps (eight;
 // weight four, for both operands) read them in whole lines, shift them into place in
 // registers and write the swizzled tile themselves; only lines inside the tensor are
-// read whole.  The 16384 rows above with a stride of 1041: 123 us forward, 135 data,
-// 370 weight (on warp-level MMAs 511, 475 and 547).  Bound by the way of a k-block
-// through a warp, its shuffles and shifts: two in flight, in weight three batches of
-// eight, with the registers that the sums leave.
+// read whole.  The 16384 rows above with a stride of 1041: 98 us forward, 325 weight
+// (on warp-level MMAs 511 and 547).  Bound by the way of a k-block through a warp, its
+// shuffles and shifts: two in flight, in weight three batches of eight, with the
+// registers that the sums leave.  Output rows off the lines leave in single elements:
+// 66 us.
 //
 // Roles per CTA, in warps: epilogue 4 (weight 8, with most of the registers), A
 // loads 1, MMA (leader CTA) and TMEM 1, B loads 2 (off the lines 8), helper 1 (weight:
@@ -66,6 +67,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
+#include <type_traits>
 
 #include "device_util.cuh"
 #include "expert_table.cuh"
@@ -440,25 +442,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                     if (lane == 0) bars.ring.done(i);
                     // batch f of the tile: k-block f / 8 (the partial one first), rows 16 (f & 3) on, of dy if !(f & 4)
                     const int batches = w.kb1 * 8;
-                    auto fetch = [&](int f, Batch &x) {
+                    auto within = [&](const void *first, const void *last, int64_t ld, int col) {
+                        const uintptr_t b = reinterpret_cast<uintptr_t>(first), head = b + (uintptr_t)(((int64_t)w.row0 * ld + col) * 2);
+                        const uintptr_t tail = head + (uintptr_t)((int64_t)((w.kb1 - 1) * 64 + w.last - 1) * ld * 2);
+                        return (head & ~uintptr_t(15)) >= b && (tail & ~uintptr_t(15)) + 272 <= reinterpret_cast<uintptr_t>(last);
+                    };
+                    const bool inside = within(p.rows_at, p.rows_end, p.ldb, w.m0 + (int)rank * 128) && within(p.rows2_at, p.rows2_end, p.ldb2, w.ntok + (int)rank * 128);
+                    auto fetch = [&](auto whole, int f, Batch &x) {
                         const int kb = f >> 3, r = (f & 3) * 16 + r0, valid = kb == 0 ? w.last : 64;
                         x.x0 = x.x1 = x.after = make_uint4(0u, 0u, 0u, 0u);
                         x.shift = 0;
-                        if (f >= batches || r >= valid) return;
+                        const bool there = f < batches && r < valid;
                         const bool b = f & 4;
                         const uintptr_t begin = reinterpret_cast<uintptr_t>(b ? p.rows2_at : p.rows_at), end = reinterpret_cast<uintptr_t>(b ? p.rows2_end : p.rows_end);
                         const int col = (b ? w.ntok : w.m0) + (int)rank * 128;
                         const int64_t row = (int64_t)w.row0 + (kb == 0 ? w.kb1 - 1 : kb - 1) * 64 + r;
                         const uintptr_t at = begin + (uintptr_t)((row * (b ? p.ldb2 : p.ldb) + col) * 2), line = (at & ~uintptr_t(15)) + 16 * c;
                         x.shift = (int)(at & 15) / 2;
-                        if (line >= begin && line + 144 <= end) {
-                            x.x0 = *reinterpret_cast<const uint4 *>(line);
-                            x.x1 = *reinterpret_cast<const uint4 *>(line + 128);
-                        } else {
-                            x.x0 = line_by_element(line, begin, end);
-                            x.x1 = line_by_element(line + 128, begin, end);
+                        if constexpr (decltype(whole)::value) {
+                            if (there) {
+                                x.x0 = *reinterpret_cast<const uint4 *>(line);
+                                x.x1 = *reinterpret_cast<const uint4 *>(line + 128);
+                            }
+                            if (there && c == 0) x.after = *reinterpret_cast<const uint4 *>(line + 256);
+                        } else if (there) {
+                            x.x0 = load_line(line, begin, end);
+                            x.x1 = load_line(line + 128, begin, end);
+                            if (c == 0 && x.shift) x.after = load_line(line + 256, begin, end);
                         }
-                        if (c == 0 && x.shift) x.after = load_line(line + 256, begin, end);
                     };
                     auto park = [&](int f, const Batch &x) {
                         const uint32_t s = it % S, ph = (it / S) & 1;
@@ -486,22 +497,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                             ++it;
                         }
                     };
-                    Batch b0, b1, b2, b3;
-                    fetch(0, b0);
-                    fetch(1, b1);
-                    fetch(2, b2);
+                    auto run = [&](auto whole) {
+                        Batch b0, b1, b2, b3;
+                        fetch(whole, 0, b0);
+                        fetch(whole, 1, b1);
+                        fetch(whole, 2, b2);
 #pragma unroll 1
-                    for (int f = 0; f < batches && ok; f += 4) {
-                        fetch(f + 3, b3);
-                        park(f, b0);
-                        if (!ok) break;
-                        fetch(f + 4, b0);
-                        park(f + 1, b1);
-                        fetch(f + 5, b1);
-                        park(f + 2, b2);
-                        fetch(f + 6, b2);
-                        park(f + 3, b3);
-                    }
+                        for (int f = 0; f < batches && ok; f += 4) {
+                            fetch(whole, f + 3, b3);
+                            park(f, b0);
+                            if (!ok) break;
+                            fetch(whole, f + 4, b0);
+                            park(f + 1, b1);
+                            fetch(whole, f + 5, b1);
+                            park(f + 2, b2);
+                            fetch(whole, f + 6, b2);
+                            park(f + 3, b3);
+                        }
+                    };
+                    if (inside)
+                        run(std::true_type());
+                    else
+                        run(std::false_type());
                 }
             } else if constexpr (LOOSE) {
                 // -------------------------------------------------------- rows that TMA cannot load
@@ -529,17 +546,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                         src[j] = begin + (uintptr_t)((int64_t)(w.row0 + (in[j] ? at + r : 0)) * p.ldb * 2);
                     }
                     const bool any = __any_sync(0xffffffffu, in[0]), more = __any_sync(0xffffffffu, in[1]);
-                    auto fetch = [&](int kb, uint4 (&x)[4]) {
+                    // all lines of the tile inside the tensor?  (else the loads would meet a branch each, and wait there)
+                    const int rows_here = min(half, w.ntok - at);
+                    const uintptr_t head = begin + (uintptr_t)((int64_t)(w.row0 + at) * p.ldb * 2), tail = head + (uintptr_t)((int64_t)(rows_here - 1) * p.ldb * 2) + 2 * (uintptr_t)depth;
+                    const bool inside = (head & ~uintptr_t(15)) >= begin && ((tail + 15) & ~uintptr_t(15)) <= end;
+                    auto fetch = [&](auto whole, int kb, uint4 (&x)[4]) {
+                        const int off = kb * 128 + c * 16;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int off = kb * 128 + c * 16, s2 = (int)(src[j] & 15);
+                            const int s2 = (int)(src[j] & 15);
+                            const uintptr_t line = src[j] - s2 + off;
                             x[j] = make_uint4(0u, 0u, 0u, 0u);
                             if (in[j] && off < depth * 2 + s2) {
-                                const uintptr_t line = src[j] - s2 + off;
-                                if (line >= begin && line + 16 <= end)
+                                if constexpr (decltype(whole)::value)
                                     x[j] = *reinterpret_cast<const uint4 *>(line);
                                 else
-                                    x[j] = line_by_element_call(line, src[j], src[j] + 2 * (uintptr_t)depth);
+                                    x[j] = load_line(line, begin, end);
                             }
                         }
                     };
@@ -572,24 +594,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                         __syncwarp();
                         if (lane == 0) mbar_arrive(tail0 + 8 * s);
                     };
-                    uint4 x0[4], x1[4], x2[4], x3[4];
-                    fetch(0, x0);
-                    fetch(1, x1);
-                    fetch(2, x2);
+                    auto run = [&](auto whole) {
+                        uint4 x0[4], x1[4], x2[4], x3[4];
+                        fetch(whole, 0, x0);
+                        fetch(whole, 1, x1);
+                        fetch(whole, 2, x2);
 #pragma unroll 1
-                    for (int kb = 0; kb < w.kb1 && ok; kb += 4) {
-                        fetch(kb + 3, x3);
-                        park(kb, x0, x1);
-                        if (kb + 1 >= w.kb1 || !ok) break;
-                        fetch(kb + 4, x0);
-                        park(kb + 1, x1, x2);
-                        if (kb + 2 >= w.kb1 || !ok) break;
-                        fetch(kb + 5, x1);
-                        park(kb + 2, x2, x3);
-                        if (kb + 3 >= w.kb1 || !ok) break;
-                        fetch(kb + 6, x2);
-                        park(kb + 3, x3, x0);
-                    }
+                        for (int kb = 0; kb < w.kb1 && ok; kb += 4) {
+                            fetch(whole, kb + 3, x3);
+                            park(kb, x0, x1);
+                            if (kb + 1 >= w.kb1 || !ok) break;
+                            fetch(whole, kb + 4, x0);
+                            park(kb + 1, x1, x2);
+                            if (kb + 2 >= w.kb1 || !ok) break;
+                            fetch(whole, kb + 5, x1);
+                            park(kb + 2, x2, x3);
+                            if (kb + 3 >= w.kb1 || !ok) break;
+                            fetch(whole, kb + 6, x2);
+                            park(kb + 3, x3, x0);
+                        }
+                    };
+                    if (inside || rows_here <= 0)
+                        run(std::true_type());
+                    else
+                        run(std::false_type());
                 }
             }
             __syncwarp();

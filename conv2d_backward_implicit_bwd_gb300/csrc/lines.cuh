@@ -15,8 +15,6 @@ __device__ __forceinline__ uint4 line_by_element(uintptr_t line, uintptr_t begin
     }
     return make_uint4((uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32));
 }
-// (as a call: in a loop over many loads the code of each would stand in the way)
-static __device__ __noinline__ uint4 line_by_element_call(uintptr_t line, uintptr_t begin, uintptr_t end) { return line_by_element(line, begin, end); }
 // eight elements from element s of lo on, over two lines
 __device__ __forceinline__ uint4 shifted(const uint4 &lo, const uint4 &hi, int s) {
     uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
