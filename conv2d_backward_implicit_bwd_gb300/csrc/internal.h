@@ -186,6 +186,20 @@ enum : int32_t {
     kDevFaultIndex = 0x201,
 };
 
+// Writes `bytes` of new device memory, zeros or a copy of `from` on the host, and
+// returns when they are there.  (cudaMemset and cudaMemcpy only queue the write on
+// the legacy default stream: a stream that is not ordered after it, as every
+// non-blocking one, could run a kernel before.)
+inline cudaError_t write_now(void *to, const void *from, size_t bytes) {
+    cudaStream_t s = nullptr;
+    cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e != cudaSuccess) return e;
+    e = from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyHostToDevice, s) : cudaMemsetAsync(to, 0, bytes, s);
+    const cudaError_t done = cudaStreamSynchronize(s);
+    cudaStreamDestroy(s);
+    return e != cudaSuccess ? e : done;
+}
+
 cudaError_t launch_fill(const FillParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_simt(const SimtParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_grouped(GroupedParams &p, int num_sms, cudaStream_t s);

@@ -56,7 +56,7 @@ struct DevicePart {
             cudaGetLastError();
             clock_khz = 2000000;
         }
-        if (cudaMalloc(&mem, bytes) != cudaSuccess || cudaMemset(mem, 0, bytes) != cudaSuccess) {
+        if (cudaMalloc(&mem, bytes) != cudaSuccess || write_now(mem, nullptr, bytes) != cudaSuccess) {
             cudaGetLastError();
             return CONV_BWD_ERR_CUDA;
         }
@@ -413,9 +413,10 @@ conv_bwd_status conv_bwd_clip_create(int32_t count, const int64_t *sizes, const 
         p.off_chunks = (64 + (size_t)std::max(p.partial_total, p.fused_blocks) * 8 + 15) / 16 * 16;
         const conv_bwd_status st = p.dev.init(p.off_chunks + chunks.size() * sizeof(ClipChunk));
         if (st != CONV_BWD_OK || !p.dev.has_device) return st;
-        if (cudaMemcpy(static_cast<char *>(p.dev.mem) + p.off_chunks, chunks.data(), chunks.size() * sizeof(ClipChunk),
-                       cudaMemcpyHostToDevice) != cudaSuccess)
+        if (write_now(static_cast<char *>(p.dev.mem) + p.off_chunks, chunks.data(), chunks.size() * sizeof(ClipChunk)) != cudaSuccess) {
+            cudaGetLastError();
             return CONV_BWD_ERR_CUDA;
+        }
         return CONV_BWD_OK;
     });
 }
