@@ -373,8 +373,10 @@ __device__ __forceinline__ void clip_one(const ClipParams &p, const T *src, T *d
         *flag = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
     }
     __syncthreads();
+    const bool last = *flag;
+    __syncthreads();  // the flag is written again
     float c = 1.f;
-    if (*flag) {
+    if (last) {
         __threadfence();
         c = finish(p, gridDim.x, sh);
         if (threadIdx.x == 0) {
