@@ -471,10 +471,9 @@ __global__ void __launch_bounds__(WORKERS + 32, RING_BLOCKS) policy_ring_kernel(
         const int tid = threadIdx.x;
         uint32_t it = 0;
         bool ok = true;  // after a wait that ran out: nothing is stored, the barriers are kept
-        int turn = 0;
-        const float upstream = MODE == kPolBackward && p.grad ? *p.grad : 1.f;
+        int turn = 0;    // which of sh's two slots; flips with the barrier that guards it, so not on masked rows
         RowIn next = row_in<MODE>(p, blockIdx.x);
-        for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x, turn ^= 1) {
+        for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
             const RowIn in = next;
             next = row_in<MODE>(p, min(t + gridDim.x, (int64_t)p.tokens - 1));
             const T *z = static_cast<const T *>(p.logits) + t * p.ld;
@@ -547,10 +546,13 @@ __global__ void __launch_bounds__(WORKERS + 32, RING_BLOCKS) policy_ring_kernel(
                 }
                 it += r.chunks;
                 const MaxSum part = join<32>(run.r, c);
-                if (lane == 0) sh[turn][warp] = part;
+                // (a slot is written again two live rows later, after the barrier that warp 0 meets when it has read it)
+                MaxSum *slot = sh[turn];
+                turn ^= 1;
+                if (lane == 0) slot[warp] = part;
                 asm volatile("bar.sync 1, %0;" ::"n"(WORKERS) : "memory");
                 if (warp == 0) {  // one warp ends the row; the others issue nothing meanwhile
-                    const MaxSum m = join<WORKERS / 32>(sh[turn][lane % (WORKERS / 32)], c);
+                    const MaxSum m = join<WORKERS / 32>(slot[lane % (WORKERS / 32)], c);
                     const float logs = log_sum(m, c), logp = fmaf(za - m.m, p.scale, -logs), w = in.w;
                     float l, k;
                     row_loss(p, in, logp, l, k);
