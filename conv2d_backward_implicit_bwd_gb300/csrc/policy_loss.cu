@@ -402,7 +402,7 @@ __device__ __forceinline__ RowAt row_at(const T *z, int V) {
     RowAt r;
     r.head = min(V, (int)((16 - ((uintptr_t)z & 15)) % 16 / sizeof(T)));
     r.nv = (V - r.head) / Vec<T>::N;
-    r.chunks = (r.nv * 16 + CHUNK - 1) / CHUNK;
+    r.chunks = (r.nv + CHUNK / 16 - 1) / (CHUNK / 16);  // (in vectors: a row of 2^30 entries has 2^32 bytes)
     return r;
 }
 template <typename T, int MODE>
@@ -452,12 +452,12 @@ __global__ void __launch_bounds__(WORKERS + 32, RING_BLOCKS) policy_ring_kernel(
                     const uint32_t b = it % RING, ph = (it / RING) & 1;
                     ok = mbar_wait_bounded(empty0 + 8 * b, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
                     if (!ok) break;
-                    const int at = (k >= r.chunks ? k - r.chunks : k) * CHUNK, bytes = min(CHUNK, r.nv * 16 - at);
+                    const int chunk = k >= r.chunks ? k - r.chunks : k, bytes = min(CHUNK / 16, r.nv - chunk * (CHUNK / 16)) * 16;
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full0 + 8 * b), "r"(bytes) : "memory");
                     // the fused form keeps a row in L2 until its second reading
                     const uint64_t policy = MODE == kPolBoth && k < r.chunks ? keep : drop;
                     asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(ring) + b * CHUNK),
-                                 "l"(src + at), "r"(bytes), "r"(full0 + 8 * b), "l"(policy)
+                                 "l"(src + (int64_t)chunk * CHUNK), "r"(bytes), "r"(full0 + 8 * b), "l"(policy)
                                  : "memory");
                 }
             }

@@ -98,3 +98,42 @@ def test_action_out_of_range(T, dtype, v):  # noqa: F811
     loss, logp, dz = plan.forward_backward(z, a, adv, w, o, f)
     assert plan.status()[0] == B.ERR_DEVICE_FAULT and plan.status() == (0, 0)
     assert float(logp[4]) == 0 and (dz[4] == 0).all() and math.isfinite(float(loss))
+
+
+@pytest.mark.parametrize("dtype,v", [("f32", (1 << 29) - 5000), ("f32", 1 << 29), ("f32", 1 << 30), ("bf16", 1 << 30)])
+def test_widest_rows(T, dtype, v):  # noqa: F811
+    """Rows whose bytes reach 2^31 and 2^32.  A thread adds a sum of 16 (32) exponentials to its own v / 4096 (v / 8192) times,
+    each rounding to 2^-24 of a positive sum: the row's sum, and with it lse and every probability, is off by
+    v 2^-36 at most, and by what test_gpu_policy.py has for narrower rows."""
+    z = torch.empty(1, v, dtype=DT[dtype], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for part in z[0].split(1 << 26):
+        part.copy_(torch.randn(len(part), generator=g, device="cuda"))
+    at = v - 7
+    z[0, at] = 12.5
+    a, one = torch.tensor([at], dtype=torch.int32, device="cuda"), torch.ones(1, device="cuda")
+    lse = math.log(sum(float(part.double().exp().sum()) for part in z[0].split(1 << 26)))
+    plan = T.PolicyLoss(v, dtype)
+    loss, logp, got_lse, coef = plan.forward(z, a, one, one)
+    rel = v * 2.0 ** -36 + 2.0 ** -19 * (1 + abs(lse) + abs(12.5 - lse))
+    assert abs(float(got_lse) - lse) <= rel and abs(float(logp) - (12.5 - lse)) <= rel
+    assert float(coef) == -1 and float(loss) == -1
+    rnd = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -22
+
+    def gradient(dz):
+        first = 0
+        for x, d in zip(z[0].split(1 << 26), dz[0].split(1 << 26)):
+            p = (x.double() - lse).exp()
+            want, size = p.clone(), p.clone()
+            if first <= at < first + len(x):
+                want[at - first] -= 1
+                size[at - first] += 1
+            assert ((d.double() - want).abs() <= rnd * want.abs() + 3 * rel * size).all()
+            first += len(x)
+    dz = plan.backward(z, a, got_lse, coef)
+    gradient(dz)
+    dz.fill_(7.0)
+    loss2, logp2, _ = plan.forward_backward(z, a, one, one, out=dz)
+    assert torch.equal(loss, loss2) and torch.equal(logp, logp2)
+    gradient(dz)
+    assert plan.status() == (0, 0)
