@@ -962,7 +962,7 @@ static conv_bwd_status create_impl(const conv_bwd_desc *desc, conv_bwd_plan *out
         if (const char *b = env("CONVBWD_DEBUG_WAIT_SECONDS")) secs = std::atof(b);
         p->wait_budget = (int64_t)(secs * clk_khz * 1000.0);
         if (alloc_status) {
-            if (cudaMalloc(&p->d_status, 16) != cudaSuccess || cudaMemset(p->d_status, 0, 16) != cudaSuccess) {
+            if (cudaMalloc(&p->d_status, 16) != cudaSuccess || write_now(p->d_status, nullptr, 16) != cudaSuccess) {
                 cudaGetLastError();
                 delete p;
                 return CONV_BWD_ERR_CUDA;
@@ -982,7 +982,7 @@ static conv_bwd_status create_impl(const conv_bwd_desc *desc, conv_bwd_plan *out
                 const size_t slots = (size_t)p->max_pairs * 2;
                 if (cudaMalloc(&p->d_partials, slots * 128 * 64 * sizeof(float4)) != cudaSuccess ||
                     cudaMalloc(&p->d_flags, slots * sizeof(int32_t)) != cudaSuccess ||
-                    cudaMemset(p->d_flags, 0, slots * sizeof(int32_t)) != cudaSuccess) {
+                    write_now(p->d_flags, nullptr, slots * sizeof(int32_t)) != cudaSuccess) {
                     cudaGetLastError();
                     cudaFree(p->d_partials);
                     cudaFree(p->d_flags);
@@ -1010,7 +1010,7 @@ static conv_bwd_status create_impl(const conv_bwd_desc *desc, conv_bwd_plan *out
                     const size_t nfl = (size_t)tiles * S * 2;
                     if (tiles * S <= tc2_max_pairs(p->num_sms) && cudaMalloc(&p->d_ws, ws) == cudaSuccess &&
                         cudaMalloc(&p->d_ws_flags, nfl * sizeof(int32_t)) == cudaSuccess &&
-                        cudaMemset(p->d_ws_flags, 0, nfl * sizeof(int32_t)) == cudaSuccess) {
+                        write_now(p->d_ws_flags, nullptr, nfl * sizeof(int32_t)) == cudaSuccess) {
                         p->splitk = S;
                         p->bn = bn_s;
                         schedule(256);

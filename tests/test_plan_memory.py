@@ -72,15 +72,58 @@ def test_new_plan_on_an_unordered_stream(what):
         z, a = normal(2000, 100), torch.randint(0, 100, (2000,), generator=g, device="cuda", dtype=torch.int32)
         adv, w = normal(2000), torch.full((2000,), 1 / 2000, device="cuda")
         make, call = lambda: T.PolicyLoss(100, "f32"), lambda p, s: p.forward(z, a, adv, w, stream=s)
-    want = [t.clone() for t in call(make(), None)]
-    streams = [torch.cuda.Stream() for _ in range(3)]
+    quiet = make()
+    want = [t.clone() for t in call(quiet, None)]
+    streams, kept = [torch.cuda.Stream() for _ in range(3)], []  # (freeing a plan would wait for the default stream)
     torch.cuda.synchronize()
     for s in streams:
         torch.cuda._sleep(100_000_000)  # some 50 ms of the default stream
         plan = make()
+        kept.append(plan)
         got = call(plan, s)
         got = call(plan, s)
         s.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
         assert plan.status(stream=s) == (0, 0)
+        torch.cuda.synchronize()
+
+
+@pytest.fixture(scope="module")
+def conv(tmp_path_factory):
+    return compiled(tmp_path_factory.mktemp("conv"), "capi.cpp")
+
+
+@pytest.mark.parametrize("what", ["status", "split", "streamk"])
+def test_convolution_plans_are_ready_when_made(conv, what):
+    run(conv, what)
+
+
+@pytest.mark.gpu
+def test_new_convolution_plan_on_an_unordered_stream():
+    """A contraction split over SM pairs, whose flags create clears: the same bits as a plan made in quiet."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    cbuild.build()
+    from conv2d_backward_implicit_bwd_gb300 import binding as B
+    make = lambda: B.Plan(32, 512, 512, 28, 28, 3, 3, pad=(1, 1), stride=(2, 2), dil=(2, 2), layout="nhwc", dtype="bf16")  # noqa: E731
+    plan = make()
+    assert plan.k_splits() > 1
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dy = torch.randn(32, plan.Ho, plan.Wo, 512, generator=g, device="cuda").bfloat16()
+    w = torch.randn(512, 3, 3, 512, generator=g, device="cuda").bfloat16()
+    want, dx = (torch.empty(32, 28, 28, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    plan.run(dy, w, want)
+    assert torch.isfinite(want).all() and plan.status() == (0, 0)
+    streams, kept = [torch.cuda.Stream() for _ in range(3)], []  # (freeing a plan would wait for the default stream)
+    torch.cuda.synchronize()
+    for s in streams:
+        torch.cuda._sleep(100_000_000)
+        plan = make()
+        kept.append(plan)
+        plan.run(dy, w, dx, stream=s)
+        plan.run(dy, w, dx, stream=s)
+        s.synchronize()
+        assert torch.equal(dx, want) and plan.status(stream=s) == (0, 0)
+        torch.cuda.synchronize()
+        dx.zero_()
         torch.cuda.synchronize()
