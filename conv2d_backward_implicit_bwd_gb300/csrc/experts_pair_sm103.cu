@@ -155,10 +155,15 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 __device__ __forceinline__ void arrive_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// What this CTA's fence.proxy.async has made visible to the MMA is ready.  (A release at cluster scope would wait for
-// the loads in flight as well.)
+// What this CTA's threads have written to its shared memory, and a fence.proxy.async has made visible to the MMA, is ready:
+// a release at cluster scope, as the other CTA's MMA warp waits for it, of shared memory alone.  (A release of everything
+// waits for the loads that the SM has in flight: 16384 rows by 16 filters of 1024 x 2048 off the lines 130 us forward and
+// 152 data instead of 110 and 117; from four warps in turn 144 and 155.)
 __device__ __forceinline__ void arrive_written(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+        : "memory");
 }
 // mbar_wait_bounded that also acquires what the arriving thread of either CTA of the pair wrote before
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
@@ -711,7 +716,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg<DIR, LOOSE>::THR
                         // one accumulator: the whole depth, or a segment of it (weight)
                         const uint32_t b = use & 1, bph = (use >> 1) & 1, d = tmem_base + b * 256;
                         ++use;
-                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
+                        // (both CTAs' epilogues arrive)
+                        ok = __all_sync(0xffffffffu, wait_cluster(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
                         if (!ok) break;
                         tc_fence_after();
                         uint32_t acc = 0;
