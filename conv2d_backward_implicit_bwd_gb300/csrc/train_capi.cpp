@@ -66,6 +66,11 @@ struct DevicePart {
     ~DevicePart() {
         if (mem) cudaFree(mem);
     }
+    // whether the current device is the plan's: its memory and the caller's tensors are there
+    bool current() const {
+        int now = -1;
+        return cudaGetDevice(&now) == cudaSuccess && now == device;
+    }
     int32_t *status() const { return static_cast<int32_t *>(mem); }
     uint32_t *ticket() const { return static_cast<uint32_t *>(mem) + 4; }
     char *rest() const { return static_cast<char *>(mem) + 64; }
@@ -239,6 +244,7 @@ static conv_bwd_status experts_run(conv_bwd_experts_plan p, int dir, int64_t row
     if (overlap(a, na, out, no) || overlap(b, nb, out, no) || overlap(offsets, (size_t)(d.experts + 1) * 4, out, no))
         return CONV_BWD_ERR_INVALID_ARG;
     if (!p->dev.has_device) return CONV_BWD_ERR_CUDA;
+    if (!p->dev.current()) return CONV_BWD_ERR_INVALID_ARG;
     if (rows == 0 && (!weight || accumulate)) return CONV_BWD_OK;
     // Tensor cores on pairs of SMs where TMA can load the filters or store their gradients (bf16, widths and address on 16 bytes); the rows come
     // by TMA if their strides and addresses are on 16 bytes too, else through registers.
@@ -441,6 +447,7 @@ static conv_bwd_status clip_launch(conv_bwd_clip_plan p, const void *const *grad
     }
     if (bad_align) return CONV_BWD_ERR_MISALIGNED;
     if (!p->dev.has_device) return CONV_BWD_ERR_CUDA;
+    if (!p->dev.current()) return CONV_BWD_ERR_INVALID_ARG;
     std::lock_guard<std::mutex> lock(p->mu);
     char *m = static_cast<char *>(p->dev.mem);
     ClipParams cp;
@@ -545,6 +552,7 @@ static conv_bwd_status policy_run(conv_bwd_policy_plan p, int mode, PolicyParams
     if (bwd && overlap(pp.logits, nz, pp.dlogits, nd) && !(pp.logits == pp.dlogits && ld == ldd))
         return CONV_BWD_ERR_INVALID_ARG;
     if (!p->dev.has_device) return CONV_BWD_ERR_CUDA;
+    if (!p->dev.current()) return CONV_BWD_ERR_INVALID_ARG;
     if (tokens == 0 && !fwd) return CONV_BWD_OK;
     pp.partials = reinterpret_cast<double *>(p->dev.rest());
     pp.ticket = p->dev.ticket();

@@ -4,9 +4,11 @@ clipped policy loss (ctypes binding of include/conv_bwd_train.h).
 Argument checks and marshalling only, as in ``binding``: every step of the
 computation runs in the CUDA library.  Tensors are torch CUDA tensors; shapes,
 types and strides are checked here (ValueError), addresses and the rest by the
-library (ConvBwdError).  Outputs that are not passed in are allocated on the
-call's stream.  A plan owns a workspace that its calls share: calls of one plan
-must not overlap on the GPU, so keep one plan per stream.
+library (ConvBwdError).  A plan belongs to the device that was current when it
+was made: its tensors lie there, and that device is current in every call.
+Outputs that are not passed in are allocated on the call's stream.  A plan owns a
+workspace that its calls share: calls of one plan must not overlap on the GPU, so
+keep one plan per stream.
 """
 from __future__ import annotations
 
@@ -105,11 +107,19 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(t, width, dtype, what):
+# (a tensor's device as a number: -1 on the CPU; a plan made without a device has one that no tensor has)
+_NOWHERE = -2
+
+
+def _on(device):
+    return f"on cuda:{device}" if device >= 0 else "on the plan's CUDA device"
+
+
+def _rows(t, width, dtype, device, what):
     """Checks a matrix of rows with unit column stride; returns (rows, row stride)."""
     shape = t.shape
-    if t.dtype != dtype or len(shape) != 2 or shape[1] != width or not t.is_cuda:
-        raise ValueError(f"{what}: a CUDA {dtype} matrix with {width} columns wanted, got {t.dtype} {tuple(shape)} on {t.device}")
+    if t.dtype != dtype or len(shape) != 2 or shape[1] != width or t.get_device() != device:
+        raise ValueError(f"{what}: a {dtype} matrix with {width} columns {_on(device)} wanted, got {t.dtype} {tuple(shape)} on {t.device}")
     rows = shape[0]
     ld, unit = t.stride()
     if (unit != 1 and width > 1) or (ld < width and rows > 1):
@@ -117,15 +127,18 @@ def _rows(t, width, dtype, what):
     return rows, ld if ld > width else width
 
 
-def _vector(t, n, dtype, what):
-    if t.dtype != dtype or t.shape != (n,) or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous CUDA {dtype} vector of {n} wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+def _vector(t, n, dtype, device, what):
+    if t.dtype != dtype or t.shape != (n,) or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} vector of {n} {_on(device)} wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 class _Plan:
     _destroy = None
     _h = None
+
+    def __init__(self):
+        self._device_index = torch.cuda.current_device() if torch.cuda.is_available() else _NOWHERE
 
     def close(self):
         h, self._h = self._h, None
@@ -154,6 +167,7 @@ class Experts(_Plan):
     _destroy = staticmethod(_lib.conv_bwd_experts_destroy)
 
     def __init__(self, experts, k, n, dtype="bf16"):
+        super().__init__()
         self.experts, self.k, self.n = int(experts), int(k), int(n)
         self._code = _dtype(dtype)
         self.dtype = _TORCH[self._code]
@@ -163,16 +177,17 @@ class Experts(_Plan):
         self._h = h.value
 
     def _product(self, call, name, what, a, wa, w, offsets, out, wo, stream):
-        rows, lda = _rows(a, wa, self.dtype, what)
-        off = _vector(offsets, self.experts + 1, torch.int32, "offsets")
-        if w.dtype != self.dtype or w.shape != self._shape or not w.is_contiguous() or not w.is_cuda:
-            raise ValueError(f"w: a contiguous CUDA {self.dtype} tensor {list(self._shape)} wanted, got {w.dtype} {tuple(w.shape)}")
+        at = self._device_index
+        rows, lda = _rows(a, wa, self.dtype, at, what)
+        off = _vector(offsets, self.experts + 1, torch.int32, at, "offsets")
+        if w.dtype != self.dtype or w.shape != self._shape or not w.is_contiguous() or w.get_device() != at:
+            raise ValueError(f"w: a contiguous {self.dtype} tensor {list(self._shape)} {_on(at)} wanted, got {w.dtype} {tuple(w.shape)} on {w.device}")
         device = a.device
         if out is None:
             out = _empty((rows, wo), self.dtype, device, stream)
             ldo = wo
         else:
-            r, ldo = _rows(out, wo, self.dtype, "out")
+            r, ldo = _rows(out, wo, self.dtype, at, "out")
             if r != rows:
                 raise ValueError(f"out: {rows} rows wanted, got {r}")
         st = call(self._h, rows, a.data_ptr(), lda, w.data_ptr(), off, out.data_ptr(), ldo, _stream(stream, device))
@@ -190,17 +205,18 @@ class Experts(_Plan):
 
     def backward_weight(self, dy, x, offsets, out=None, accumulate=False, stream=None):
         """dw[e] = sum of dy[i] x[i]^T over the rows of e, in fp32 [experts, n, k]; added to ``out`` with ``accumulate``."""
-        rows, lddy = _rows(dy, self.n, self.dtype, "dy")
-        r, ldx = _rows(x, self.k, self.dtype, "x")
+        at = self._device_index
+        rows, lddy = _rows(dy, self.n, self.dtype, at, "dy")
+        r, ldx = _rows(x, self.k, self.dtype, at, "x")
         if r != rows:
             raise ValueError(f"x: {rows} rows wanted as in dy, got {r}")
-        off = _vector(offsets, self.experts + 1, torch.int32, "offsets")
+        off = _vector(offsets, self.experts + 1, torch.int32, at, "offsets")
         if out is None:
             if accumulate:
                 raise ValueError("accumulate wants the gradients to add to in out")
             out = _empty(self._shape, torch.float32, dy.device, stream)
-        elif out.dtype != torch.float32 or out.shape != self._shape or not out.is_contiguous() or not out.is_cuda:
-            raise ValueError(f"out: a contiguous CUDA fp32 tensor {list(self._shape)} wanted, got {out.dtype} {tuple(out.shape)}")
+        elif out.dtype != torch.float32 or out.shape != self._shape or not out.is_contiguous() or out.get_device() != at:
+            raise ValueError(f"out: a contiguous fp32 tensor {list(self._shape)} {_on(at)} wanted, got {out.dtype} {tuple(out.shape)} on {out.device}")
         _check(_lib.conv_bwd_experts_weight(self._h, rows, dy.data_ptr(), lddy, x.data_ptr(), ldx, off, out.data_ptr(),
                                             1 if accumulate else 0, _stream(stream, dy.device)), "conv_bwd_experts_weight")
         return out
@@ -211,8 +227,8 @@ class Experts(_Plan):
 
 
 # (over hundreds of tensors a call, mapped in C)
-_numel, _contiguous, _data_ptr = torch.Tensor.numel, torch.Tensor.is_contiguous, torch.Tensor.data_ptr
-_type_device = operator.attrgetter("dtype", "is_cuda")
+_numel, _contiguous, _data_ptr, _get_device = torch.Tensor.numel, torch.Tensor.is_contiguous, torch.Tensor.data_ptr, torch.Tensor.get_device
+_type = operator.attrgetter("dtype")
 
 
 class GradClip(_Plan):
@@ -224,11 +240,12 @@ class GradClip(_Plan):
     _destroy = staticmethod(_lib.conv_bwd_clip_destroy)
 
     def __init__(self, sizes, dtypes):
+        super().__init__()
         sizes = [int(n) for n in sizes]
         codes = [_dtype(d) for d in dtypes]
         if len(sizes) != len(codes):
             raise ValueError(f"{len(sizes)} sizes and {len(codes)} dtypes")
-        self._sizes, self._types = sizes, [(_TORCH[c], True) for c in codes]
+        self._sizes, self._types, self._devices = sizes, [_TORCH[c] for c in codes], [self._device_index] * len(sizes)
         self.count = n = len(sizes)
         h = _vp()
         _check(_lib.conv_bwd_clip_create(n, (_i64 * max(n, 1))(*sizes), (_i32 * max(n, 1))(*codes), ctypes.byref(h)), "conv_bwd_clip_create")
@@ -240,13 +257,13 @@ class GradClip(_Plan):
         return cls([t.numel() for t in tensors], [t.dtype for t in tensors])
 
     def _pointers(self, tensors, what):
-        if (list(map(_numel, tensors)) != self._sizes or list(map(_type_device, tensors)) != self._types
-                or not all(map(_contiguous, tensors))):
+        if (list(map(_numel, tensors)) != self._sizes or list(map(_type, tensors)) != self._types
+                or list(map(_get_device, tensors)) != self._devices or not all(map(_contiguous, tensors))):
             if len(tensors) != self.count:
                 raise ValueError(f"{what}: {self.count} tensors wanted, got {len(tensors)}")
             for i, t in enumerate(tensors):
-                if t.numel() != self._sizes[i] or _type_device(t) != self._types[i] or not t.is_contiguous():
-                    raise ValueError(f"{what}[{i}]: a contiguous CUDA {self._types[i][0]} tensor of {self._sizes[i]} elements wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+                if t.numel() != self._sizes[i] or t.dtype != self._types[i] or t.get_device() != self._device_index or not t.is_contiguous():
+                    raise ValueError(f"{what}[{i}]: a contiguous {self._types[i]} tensor of {self._sizes[i]} elements {_on(self._device_index)} wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
         return array.array("Q", map(_data_ptr, tensors))
 
     def _device(self, grads):
@@ -287,6 +304,7 @@ class PolicyLoss(_Plan):
     _destroy = staticmethod(_lib.conv_bwd_policy_destroy)
 
     def __init__(self, vocab, dtype="bf16", clip_low=0.2, clip_high=0.2, kl=0.0, scale=1.0):
+        super().__init__()
         self.vocab = int(vocab)
         self._code = _dtype(dtype)
         self.dtype = _TORCH[self._code]
@@ -295,17 +313,18 @@ class PolicyLoss(_Plan):
         self._h = h.value
 
     def _inputs(self, logits, actions, advantage, weight, old_logp, ref_logp):
-        t, ld = _rows(logits, self.vocab, self.dtype, "logits")
+        at = self._device_index
+        t, ld = _rows(logits, self.vocab, self.dtype, at, "logits")
         f = torch.float32
-        return t, (self._h, t, logits.data_ptr(), ld, _vector(actions, t, torch.int32, "actions"),
-                   _vector(advantage, t, f, "advantage"), _vector(weight, t, f, "weight"),
-                   None if old_logp is None else _vector(old_logp, t, f, "old_logp"),
-                   None if ref_logp is None else _vector(ref_logp, t, f, "ref_logp"))
+        return t, (self._h, t, logits.data_ptr(), ld, _vector(actions, t, torch.int32, at, "actions"),
+                   _vector(advantage, t, f, at, "advantage"), _vector(weight, t, f, at, "weight"),
+                   None if old_logp is None else _vector(old_logp, t, f, at, "old_logp"),
+                   None if ref_logp is None else _vector(ref_logp, t, f, at, "ref_logp"))
 
     def _grad_out(self, logits, t, out, stream):
         if out is None:
             return _empty((t, self.vocab), self.dtype, logits.device, stream), self.vocab
-        r, ld = _rows(out, self.vocab, self.dtype, "out")
+        r, ld = _rows(out, self.vocab, self.dtype, self._device_index, "out")
         if r != t:
             raise ValueError(f"out: {t} rows wanted, got {r}")
         return out, ld
@@ -322,10 +341,11 @@ class PolicyLoss(_Plan):
 
     def backward(self, logits, actions, lse, coef, grad=None, out=None, stream=None):
         """dlogits from the forward's lse and coef; ``grad`` [1] is the loss's upstream gradient; ``out`` may be logits."""
-        t, ld = _rows(logits, self.vocab, self.dtype, "logits")
+        at = self._device_index
+        t, ld = _rows(logits, self.vocab, self.dtype, at, "logits")
         f = torch.float32
-        args = (self._h, t, logits.data_ptr(), ld, _vector(actions, t, torch.int32, "actions"), _vector(lse, t, f, "lse"),
-                _vector(coef, t, f, "coef"), None if grad is None else _vector(grad, 1, f, "grad"))
+        args = (self._h, t, logits.data_ptr(), ld, _vector(actions, t, torch.int32, at, "actions"), _vector(lse, t, f, at, "lse"),
+                _vector(coef, t, f, at, "coef"), None if grad is None else _vector(grad, 1, f, at, "grad"))
         out, ldd = self._grad_out(logits, t, out, stream)
         _check(_lib.conv_bwd_policy_backward(*args, out.data_ptr(), ldd, _stream(stream, logits.device)), "conv_bwd_policy_backward")
         return out

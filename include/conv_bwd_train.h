@@ -14,8 +14,9 @@
  * enqueues on `stream` (a cudaStream_t; NULL = legacy default stream),
  * allocates nothing and never synchronises, so it can be captured in a CUDA
  * graph.  A plan owns its workspace and a device status word, allocated by
- * create on the device current then (which must be current in every run);
- * without a device create succeeds and run returns CONV_BWD_ERR_CUDA.  Runs of
+ * create on the device current then (which must be current in every run, else
+ * CONV_BWD_ERR_INVALID_ARG); without a device create succeeds and run returns
+ * CONV_BWD_ERR_CUDA.  Runs of
  * one plan share that workspace and must not overlap on the GPU; use one plan
  * per stream.  Device-side problems (an index out of range, a bounded wait
  * that ran out) are recorded in the status word and read with get_status;

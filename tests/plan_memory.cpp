@@ -2,7 +2,8 @@
 // before it must: copies and memsets wait in their stream's queue until something
 // synchronises that stream, as a busy GPU may let them.  A program for
 // test_plan_memory.py; argv[1] names the plan to make.  Ends with 0 if create left
-// nothing queued and every buffer that create writes was written.
+// nothing queued, every buffer that create writes was written, and a run with
+// another device current is refused.
 #include <stdint.h>
 #include <stdio.h>
 #include <stdlib.h>
@@ -30,7 +31,7 @@ struct Op {
 };
 std::map<cudaStream_t, std::vector<Op>> queued;  // nullptr: the legacy default stream
 std::map<void *, size_t> held;                   // device memory, 0xA5 until written
-int written = 0;
+int written = 0, device = 0;
 
 cudaError_t put(cudaStream_t s, void *dst, std::vector<uint8_t> bytes) {
     queued[s].push_back({dst, std::move(bytes)});
@@ -42,6 +43,9 @@ int pending() {
     return n;
 }
 int encode(...) { return 0; }
+#ifdef TRAIN
+void *at(int i) { return (void *)((uintptr_t)i << 24); }  // an address that nothing reads
+#endif
 
 }  // namespace
 
@@ -51,7 +55,7 @@ void not_reached(void) {
     exit(3);
 }
 cudaError_t cudaGetDeviceCount(int *n) { return *n = 1, cudaSuccess; }
-cudaError_t cudaGetDevice(int *d) { return *d = 0, cudaSuccess; }
+cudaError_t cudaGetDevice(int *d) { return *d = device, cudaSuccess; }
 cudaError_t cudaSetDevice(int) { return cudaSuccess; }
 cudaError_t cudaGetLastError(void) { return cudaSuccess; }
 cudaError_t cudaDeviceGetAttribute(int *v, cudaDeviceAttr a, int) {
@@ -102,6 +106,7 @@ int main(int argc, char **argv) {
     const std::string what = argc > 1 ? argv[1] : "";
     conv_bwd_status st = CONV_BWD_ERR_INVALID_ARG;
     int ops = 1;  // at least
+    int elsewhere = CONV_BWD_ERR_INVALID_ARG;  // a run's status with another device current
     size_t zeros = 0;  // bytes of the plan's first buffer that start as zeros
 #ifdef TRAIN
     if (what == "experts") {
@@ -109,6 +114,8 @@ int main(int argc, char **argv) {
         conv_bwd_experts_plan p;
         st = conv_bwd_experts_create(&d, &p);
         zeros = 64 + 152 * 2 * 4;
+        device = 1;
+        if (!st) elsewhere = conv_bwd_experts_forward(p, 4, at(1), 0, at(2), (const int32_t *)at(3), at(4), 0, nullptr);
     } else if (what == "clip") {
         const int64_t sizes[2] = {70000, 3};
         const int32_t types[2] = {CONV_BWD_F32, CONV_BWD_BF16};
@@ -116,11 +123,17 @@ int main(int argc, char **argv) {
         st = conv_bwd_clip_create(2, sizes, types, &p);
         ops = 2;  // counters, and the table of chunks
         zeros = 64;
+        device = 1;
+        void *const g[2] = {at(1), at(2)};
+        if (!st) elsewhere = conv_bwd_clip_run(p, g, g, 1.f, (float *)at(3), (float *)at(4), nullptr);
     } else if (what == "policy") {
         const conv_bwd_policy_desc d = {100, CONV_BWD_F32, 0.2f, 0.2f, 0.f, 1.f};
         conv_bwd_policy_plan p;
         st = conv_bwd_policy_create(&d, &p);
         zeros = 64;
+        device = 1;
+        const float *f = (const float *)at(3);
+        if (!st) elsewhere = conv_bwd_policy_forward(p, 4, at(1), 0, (const int32_t *)at(2), f, f, f, f, (float *)at(4), (float *)at(5), (float *)at(6), (float *)at(7), nullptr);
     }
 #else
     conv_bwd_desc d = {};
@@ -146,6 +159,7 @@ int main(int argc, char **argv) {
     if (int n = pending()) return printf("%d of the plan's writes still queued when create returned\n", n), 1;
     if (written < ops) return printf("%d writes, %d expected\n", written, ops), 1;
     if (held.empty()) return printf("no device memory\n"), 2;
+    if (elsewhere != CONV_BWD_ERR_INVALID_ARG) return printf("run with another device current: status %d\n", elsewhere), 1;
     if (zeros) {
         if (held.size() != 1 || held.begin()->second < zeros) return printf("unexpected buffers\n"), 2;
         const uint8_t *m = (const uint8_t *)held.begin()->first;
