@@ -8,7 +8,9 @@ library (ConvBwdError).  A plan belongs to the device that was current when it
 was made: its tensors lie there, and that device is current in every call.
 Outputs that are not passed in are allocated on the call's stream.  A plan owns a
 workspace that its calls share: calls of one plan must not overlap on the GPU, so
-keep one plan per stream.
+keep one plan per stream.  The results carry no gradient functions; a tensor that
+a call writes in place (``out``, the gradients of ``clip``) counts a new version, so
+that autograd refuses a backward pass that had saved its old values.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ import ctypes
 import operator
 
 import torch
+from torch.autograd.graph import increment_version as _written  # what the library wrote in place, autograd may have saved
 
 from . import binding as _b
 from .binding import ConvBwdError, BF16, F32, OK  # noqa: F401  (part of this module's interface)
@@ -182,7 +185,7 @@ class Experts(_Plan):
         off = _vector(offsets, self.experts + 1, torch.int32, at, "offsets")
         if w.dtype != self.dtype or w.shape != self._shape or not w.is_contiguous() or w.get_device() != at:
             raise ValueError(f"w: a contiguous {self.dtype} tensor {list(self._shape)} {_on(at)} wanted, got {w.dtype} {tuple(w.shape)} on {w.device}")
-        device = a.device
+        device, given = a.device, out
         if out is None:
             out = _empty((rows, wo), self.dtype, device, stream)
             ldo = wo
@@ -193,6 +196,8 @@ class Experts(_Plan):
         st = call(self._h, rows, a.data_ptr(), lda, w.data_ptr(), off, out.data_ptr(), ldo, _stream(stream, device))
         if st != OK:
             raise ConvBwdError(st, name)
+        if given is not None:
+            _written(given)
         return out
 
     def forward(self, x, w, offsets, out=None, stream=None):
@@ -211,6 +216,7 @@ class Experts(_Plan):
         if r != rows:
             raise ValueError(f"x: {rows} rows wanted as in dy, got {r}")
         off = _vector(offsets, self.experts + 1, torch.int32, at, "offsets")
+        given = out
         if out is None:
             if accumulate:
                 raise ValueError("accumulate wants the gradients to add to in out")
@@ -219,6 +225,8 @@ class Experts(_Plan):
             raise ValueError(f"out: a contiguous fp32 tensor {list(self._shape)} {_on(at)} wanted, got {out.dtype} {tuple(out.shape)} on {out.device}")
         _check(_lib.conv_bwd_experts_weight(self._h, rows, dy.data_ptr(), lddy, x.data_ptr(), ldx, off, out.data_ptr(),
                                             1 if accumulate else 0, _stream(stream, dy.device)), "conv_bwd_experts_weight")
+        if given is not None:
+            _written(given)
         return out
 
     def status(self, stream=None):
@@ -287,6 +295,7 @@ class GradClip(_Plan):
         device = self._device(grads)
         norm, coef = _empty((1,), torch.float32, device, stream), _empty((1,), torch.float32, device, stream)
         _check(_lib.conv_bwd_clip_run(self._h, g.buffer_info()[0], o.buffer_info()[0], max_norm, norm.data_ptr(), coef.data_ptr(), _stream(stream, device)), "conv_bwd_clip_run")
+        _written(grads if out is None else out)
         return norm, coef
 
     def status(self, stream=None):
@@ -346,18 +355,24 @@ class PolicyLoss(_Plan):
         f = torch.float32
         args = (self._h, t, logits.data_ptr(), ld, _vector(actions, t, torch.int32, at, "actions"), _vector(lse, t, f, at, "lse"),
                 _vector(coef, t, f, at, "coef"), None if grad is None else _vector(grad, 1, f, at, "grad"))
+        given = out
         out, ldd = self._grad_out(logits, t, out, stream)
         _check(_lib.conv_bwd_policy_backward(*args, out.data_ptr(), ldd, _stream(stream, logits.device)), "conv_bwd_policy_backward")
+        if given is not None:
+            _written(given)
         return out
 
     def forward_backward(self, logits, actions, advantage, weight, old_logp=None, ref_logp=None, out=None, stream=None):
         """(loss [1], logp [tokens], dlogits) in one launch; ``out`` may be logits."""
         t, args = self._inputs(logits, actions, advantage, weight, old_logp, ref_logp)
+        given = out
         out, ldd = self._grad_out(logits, t, out, stream)
         device = logits.device
         logp = _empty((t,), torch.float32, device, stream)
         loss = _empty((1,), torch.float32, device, stream)
         _check(_lib.conv_bwd_policy_forward_backward(*args, loss.data_ptr(), logp.data_ptr(), out.data_ptr(), ldd, _stream(stream, device)), "conv_bwd_policy_forward_backward")
+        if given is not None:
+            _written(given)
         return loss, logp, out
 
     def status(self, stream=None):
