@@ -33,9 +33,10 @@ template <>
 struct Quad<4> {
     float4 v;
     __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const float4 *>(p); }
-    // of a filter: read once, and not to push the rows out of L1
+    // of a filter: read once, and not to push the rows out of L1  (no read-only load: the launch begins while the kernel
+    // before it, which may still write the filters, runs)
     __device__ __forceinline__ void pass(const float *p) {
-        asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+        asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
     }
     __device__ __forceinline__ float dot(const Quad &o, float s) const { return fmaf(v.w, o.v.w, fmaf(v.z, o.v.z, fmaf(v.y, o.v.y, fmaf(v.x, o.v.x, s)))); }
     __device__ __forceinline__ void add(float a, const Quad &o) {
@@ -51,7 +52,7 @@ template <>
 struct Quad<1> {
     float v;
     __device__ __forceinline__ void load(const float *p) { v = *p; }
-    __device__ __forceinline__ void pass(const float *p) { asm volatile("ld.global.nc.L1::no_allocate.f32 %0, [%1];" : "=f"(v) : "l"(p)); }
+    __device__ __forceinline__ void pass(const float *p) { asm volatile("ld.global.L1::no_allocate.f32 %0, [%1];" : "=f"(v) : "l"(p)); }
     __device__ __forceinline__ float dot(const Quad &o, float s) const { return fmaf(v, o.v, s); }
     __device__ __forceinline__ void add(float a, const Quad &o) { v = fmaf(a, o.v, v); }
     __device__ __forceinline__ void store(float *p) const { *p = v; }
