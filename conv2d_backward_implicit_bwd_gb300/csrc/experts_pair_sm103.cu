@@ -48,9 +48,9 @@
 // rows by 16 filters of 1024 x 2048 47 us (0.74 of the rate), data of 32768 rows
 // by 32 of 2048 x 2048 163 us (0.86, the rows of each expert uneven).  Memory: 256
 // rows by 64 filters of 2048 x 1024 49 us (0.79; four rounds for 3.4 rounds' tiles);
-// weight of the first of these, adding to fp32 gradients, 77 us (0.72).  Adding by
-// reading the old gradient into the epilogue's staging and storing the sum was no
-// faster (82 to 86 us against 78): the mix of reads and writes is the time.
+// weight of the first of these, adding to fp32 gradients, 77 us (0.72; stored without
+// adding 62).  Adding by reading the old gradient into the epilogue's staging and
+// storing the sum was no faster (82 to 86 us against 78).
 //
 // Rows off the 16-byte lines (strides or addresses) cannot come by TMA.  Warps (eight;
 // weight four, for both operands) read them in whole lines, shift them into place in

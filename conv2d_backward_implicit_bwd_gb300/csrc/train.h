@@ -59,7 +59,7 @@ cudaError_t launch_experts_few_f32(const ExpertSimtParams &p, int dir, int num_s
 cudaError_t launch_experts_f32(const ExpertSimtParams &p, int dir, cudaStream_t s);
 cudaError_t launch_experts_b16(const ExpertSimtParams &p, int dir, cudaStream_t s);
 
-// Expert product on tensor cores over pairs of SMs (bf16, 16-byte aligned rows).
+// Expert product on tensor cores over pairs of SMs (bf16; filters or their gradients on 16 bytes, rows at any address).
 struct ExpertPairParams {  // 128-byte aligned through CUtensorMap
     CUtensorMap a;           // forward, data: w {K, N, experts}; weight: dy {N, rows}
     CUtensorMap b;           // forward: x {K, rows}; data: dy {N, rows}; weight: x {K, rows}
