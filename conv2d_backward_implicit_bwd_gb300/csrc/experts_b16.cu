@@ -254,8 +254,9 @@ cudaError_t launch_dir(const ExpertSimtParams &p, cudaStream_t s) {
 cudaError_t launch_experts_b16(const ExpertSimtParams &p, int dir, cudaStream_t s) {
     if (dir == kExpForward) return launch_dir<kExpForward>(p, s);
     if (dir == kExpData) return launch_dir<kExpData>(p, s);
-    // Two neighbours on 4-byte addresses cost less than shifting lines, single ones more: 16384 rows by 16 filters of
-    // 1024 x 2048 342, 547 and 1442 us.  (data, whose rows come in singles or pairs all the same: lines 141 against 122.)
+    // Two neighbours on 4-byte addresses cost less than shifting lines: 8192 rows by 8 filters of 1028 x 1028 125 against
+    // 204 us; single ones more: of 1001 x 1001 171 against 163, 16384 rows by 16 of them 495 against 289.  (data, whose
+    // rows come in singles or pairs all the same: lines 141 against 122.)
     const bool words = (((uintptr_t)p.a | (uintptr_t)p.b) & 3) == 0 && (p.lda | p.ldb) % 2 == 0;
     return words ? launch_dir<kExpWeight>(p, s) : launch_dir<kExpWeight, true>(p, s);
 }
