@@ -45,8 +45,9 @@
 // runs under the other accumulator's MMAs.
 //
 // Bounds, measured at 6.68 TB/s and 1963 TFLOP/s.  Tensor pipe: forward of 16384
-// rows by 16 filters of 1024 x 2048 47 us (0.74 of the rate), data of 32768 rows
-// by 32 of 2048 x 2048 163 us (0.86, the rows of each expert uneven).  Memory: 256
+// rows by 16 filters of 1024 x 2048 47 to 52 us (0.74 to 0.67 of the rate), data of
+// 32768 rows by 32 of 2048 x 2048 163 (0.86, the rows of each expert uneven); called
+// without a pause 54 and 191 under the power cap (1.6 and 1.4 GHz).  Memory: 256
 // rows by 64 filters of 2048 x 1024 49 us (0.79; four rounds for 3.4 rounds' tiles);
 // weight of the first of these, adding to fp32 gradients, 77 us (0.72; stored without
 // adding 62).  Adding by reading the old gradient into the epilogue's staging and
