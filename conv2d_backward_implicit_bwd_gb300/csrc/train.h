@@ -146,4 +146,26 @@ struct PolicyParams {
 int policy_max_blocks(int num_sms);        // upper bound of any launch's blocks
 cudaError_t launch_policy(const PolicyParams &p, int dtype, int mode, int num_sms, cudaStream_t s);
 
+// Log-probabilities of given tokens, entropy, alternatives.
+constexpr int kLogpTop = 32;     // most alternatives of a row
+constexpr int kLogpPart = 272;   // bytes of a row's part in the workspace
+struct LogpParams {
+    const void *logits;
+    void *dlogits;
+    const int32_t *tokens;                               // NULL: no given tokens
+    float *logp, *entropy, *lse, *top_logp;              // forward
+    int32_t *top_tokens;
+    const float *lse_in, *entropy_in, *grad_logp, *grad_entropy;  // backward
+    void *work;                                          // [rows][parts] parts
+    int32_t *arrived;                                    // [rows] parts that are there, 0 between launches
+    int32_t *status;
+    int64_t ld, ldd;
+    int64_t wait_budget;
+    int32_t rows, vocab, top, parts;
+    float scale;
+};
+int logp_most_items(int num_sms);  // upper bound of rows * parts where parts > 1
+int logp_parts(int64_t rows, int64_t vocab, int dtype, int num_sms);
+cudaError_t launch_logp(const LogpParams &p, int dtype, bool backward, int num_sms, cudaStream_t s);
+
 }  // namespace cbd

@@ -7,6 +7,7 @@
 #include <memory>
 #include <mutex>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include <cuda.h>
@@ -182,6 +183,12 @@ struct conv_bwd_clip_plan_s {
 };
 struct conv_bwd_policy_plan_s {
     conv_bwd_policy_desc d;
+    DevicePart dev;
+};
+
+struct conv_bwd_logp_plan_s {
+    conv_bwd_logp_desc d;
+    size_t off_work = 0;
     DevicePart dev;
 };
 
@@ -605,6 +612,114 @@ conv_bwd_status conv_bwd_policy_forward_backward(conv_bwd_policy_plan p, int64_t
     return policy_run(p, kPolBoth, pp, tokens, ld, ldd, stream);
 }
 conv_bwd_status conv_bwd_policy_get_status(conv_bwd_policy_plan p, void *stream, int32_t *detail) {
+    if (!p) return CONV_BWD_ERR_INVALID_ARG;
+    return read_status(p->dev, stream, detail);
+}
+
+// ---- token log-probabilities ----------------------------------------------------
+conv_bwd_status conv_bwd_logp_create(const conv_bwd_logp_desc *d, conv_bwd_logp_plan *out) {
+    if (!out) return CONV_BWD_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!d || d->vocab < 1 || !known_dtype(d->dtype) || d->top < 0 || d->top > d->vocab ||
+        !(d->scale > 0.f && std::isfinite(d->scale)))
+        return CONV_BWD_ERR_INVALID_ARG;
+    if (d->vocab > (1LL << 30) || d->top > kLogpTop) return CONV_BWD_ERR_UNSUPPORTED;
+    return create_plan(out, [&](conv_bwd_logp_plan_s &p) {
+        p.d = *d;
+        int sms = 0, dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+            cudaGetLastError();
+            sms = 0;
+        }
+        const size_t items = (size_t)logp_most_items(sms);
+        p.off_work = 64 + (items * 4 + 63) / 64 * 64;
+        p.dev.counters = p.off_work;
+        return p.dev.init(p.off_work + items * kLogpPart);
+    });
+}
+conv_bwd_status conv_bwd_logp_destroy(conv_bwd_logp_plan p) {
+    delete p;
+    return CONV_BWD_OK;
+}
+
+static conv_bwd_status logp_run(conv_bwd_logp_plan p, bool backward, LogpParams &lp, int64_t rows, int64_t ld, int64_t ldd,
+                                void *stream) {
+    if (!p || rows < 0) return CONV_BWD_ERR_INVALID_ARG;
+    const conv_bwd_logp_desc &d = p->d;
+    const int64_t V = d.vocab;
+    if (ld == 0) ld = V;
+    if (ldd == 0) ldd = V;
+    if (ld < V || ldd < V) return CONV_BWD_ERR_INVALID_ARG;
+    if (rows > 0) {
+        if (!lp.logits) return CONV_BWD_ERR_INVALID_ARG;
+        if (!backward && (!lp.entropy || !lp.lse || !lp.tokens != !lp.logp || (d.top > 0 && (!lp.top_logp || !lp.top_tokens))))
+            return CONV_BWD_ERR_INVALID_ARG;
+        if (backward && (!lp.lse_in || !lp.dlogits || (!lp.grad_logp && !lp.grad_entropy) || (lp.grad_logp && !lp.tokens) ||
+                         (lp.grad_entropy && !lp.entropy_in)))
+            return CONV_BWD_ERR_INVALID_ARG;
+    }
+    const size_t es = esize(d.dtype);
+    const uintptr_t words = (uintptr_t)lp.tokens | (uintptr_t)lp.logp | (uintptr_t)lp.entropy | (uintptr_t)lp.lse |
+                            (uintptr_t)lp.top_logp | (uintptr_t)lp.top_tokens | (uintptr_t)lp.lse_in |
+                            (uintptr_t)lp.entropy_in | (uintptr_t)lp.grad_logp | (uintptr_t)lp.grad_entropy;
+    if (words % 4 || ((uintptr_t)lp.logits | (uintptr_t)lp.dlogits) % es) return CONV_BWD_ERR_MISALIGNED;
+    if (rows > kMostRows || ld > (1LL << 31) || ldd > (1LL << 31)) return CONV_BWD_ERR_UNSUPPORTED;
+    const size_t nz = extent(rows, ld, V, es), nd = extent(rows, ldd, V, es), n = (size_t)rows * 4;
+    if (backward) {
+        if (overlap(lp.logits, nz, lp.dlogits, nd) && !(lp.logits == lp.dlogits && ld == ldd)) return CONV_BWD_ERR_INVALID_ARG;
+        for (const void *in : {(const void *)lp.tokens, (const void *)lp.lse_in, (const void *)lp.entropy_in,
+                               (const void *)lp.grad_logp, (const void *)lp.grad_entropy})
+            if (in && overlap(in, n, lp.dlogits, nd)) return CONV_BWD_ERR_INVALID_ARG;
+    } else {
+        const size_t top = n * (size_t)d.top;
+        const std::pair<const void *, size_t> outs[] = {{lp.logp, n}, {lp.entropy, n}, {lp.lse, n}, {lp.top_logp, top}, {lp.top_tokens, top}};
+        for (const auto &o : outs) {
+            if (!o.first) continue;
+            if (overlap(lp.logits, nz, o.first, o.second) || (lp.tokens && overlap(lp.tokens, n, o.first, o.second))) return CONV_BWD_ERR_INVALID_ARG;
+            for (const auto &q : outs)
+                if (&q != &o && q.first && overlap(q.first, q.second, o.first, o.second)) return CONV_BWD_ERR_INVALID_ARG;
+        }
+    }
+    if (!p->dev.has_device) return CONV_BWD_ERR_CUDA;
+    if (!p->dev.current()) return CONV_BWD_ERR_INVALID_ARG;
+    if (rows == 0) return CONV_BWD_OK;
+    lp.work = static_cast<char *>(p->dev.mem) + p->off_work;
+    lp.arrived = reinterpret_cast<int32_t *>(p->dev.rest());
+    lp.status = p->dev.status();
+    lp.ld = ld;
+    lp.ldd = ldd;
+    lp.wait_budget = (int64_t)p->dev.clock_khz * 2000;
+    lp.rows = (int32_t)rows;
+    lp.vocab = (int32_t)V;
+    lp.top = d.top;
+    lp.parts = logp_parts(rows, V, d.dtype, p->dev.num_sms);
+    lp.scale = d.scale;
+    return launch_logp(lp, d.dtype, backward, p->dev.num_sms, (cudaStream_t)stream) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
+}
+
+conv_bwd_status conv_bwd_logp_forward(conv_bwd_logp_plan p, int64_t rows, const void *logits, int64_t ld, const int32_t *tokens,
+                                      float *logp, float *entropy, float *lse, float *top_logp, int32_t *top_tokens, void *stream) {
+    Range range("conv_bwd_logp_forward");
+    LogpParams lp;
+    std::memset(&lp, 0, sizeof(lp));
+    lp.logits = logits; lp.tokens = tokens;
+    lp.logp = logp; lp.entropy = entropy; lp.lse = lse;
+    if (p && p->d.top) { lp.top_logp = top_logp; lp.top_tokens = top_tokens; }
+    return logp_run(p, false, lp, rows, ld, 0, stream);
+}
+conv_bwd_status conv_bwd_logp_backward(conv_bwd_logp_plan p, int64_t rows, const void *logits, int64_t ld, const int32_t *tokens,
+                                       const float *lse, const float *entropy, const float *grad_logp, const float *grad_entropy,
+                                       void *dlogits, int64_t ldd, void *stream) {
+    Range range("conv_bwd_logp_backward");
+    LogpParams lp;
+    std::memset(&lp, 0, sizeof(lp));
+    lp.logits = logits; lp.tokens = tokens;
+    lp.lse_in = lse; lp.entropy_in = entropy; lp.grad_logp = grad_logp; lp.grad_entropy = grad_entropy;
+    lp.dlogits = dlogits;
+    return logp_run(p, true, lp, rows, ld, ldd, stream);
+}
+conv_bwd_status conv_bwd_logp_get_status(conv_bwd_logp_plan p, void *stream, int32_t *detail) {
     if (!p) return CONV_BWD_ERR_INVALID_ARG;
     return read_status(p->dev, stream, detail);
 }

@@ -33,7 +33,8 @@ EXPORTED = [
     "conv_bwd_experts_weight", "conv_bwd_experts_get_status", "conv_bwd_clip_create", "conv_bwd_clip_destroy",
     "conv_bwd_clip_norm", "conv_bwd_clip_run", "conv_bwd_clip_get_status", "conv_bwd_policy_create", "conv_bwd_policy_destroy",
     "conv_bwd_policy_forward", "conv_bwd_policy_backward", "conv_bwd_policy_forward_backward",
-    "conv_bwd_policy_get_status",
+    "conv_bwd_policy_get_status", "conv_bwd_logp_create", "conv_bwd_logp_destroy", "conv_bwd_logp_forward",
+    "conv_bwd_logp_backward", "conv_bwd_logp_get_status",
 ]
 
 
@@ -44,6 +45,10 @@ class ExpertsDesc(ctypes.Structure):
 class PolicyDesc(ctypes.Structure):
     _fields_ = [("vocab", _i64), ("dtype", _i32), ("clip_low", _f32), ("clip_high", _f32), ("kl", _f32),
                 ("scale", _f32)]
+
+
+class LogpDesc(ctypes.Structure):
+    _fields_ = [("vocab", _i64), ("dtype", _i32), ("top", _i32), ("scale", _f32)]
 
 
 def _declare():
@@ -67,6 +72,11 @@ def _declare():
         "conv_bwd_policy_backward": [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp],
         "conv_bwd_policy_forward_backward": [_vp, _i64, _vp, _i64] + [_vp] * 8 + [_i64, _vp],
         "conv_bwd_policy_get_status": [_vp, _vp, P(_i32)],
+        "conv_bwd_logp_create": [P(LogpDesc), P(_vp)],
+        "conv_bwd_logp_destroy": [_vp],
+        "conv_bwd_logp_forward": [_vp, _i64, _vp, _i64] + [_vp] * 7,
+        "conv_bwd_logp_backward": [_vp, _i64, _vp, _i64] + [_vp] * 6 + [_i64, _vp],
+        "conv_bwd_logp_get_status": [_vp, _vp, P(_i32)],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -378,3 +388,67 @@ class PolicyLoss(_Plan):
     def status(self, stream=None):
         """(status, detail) of the calls since the last one; synchronises the stream."""
         return _status(_lib.conv_bwd_policy_get_status, self._h, stream)
+
+
+class TokenLogp(_Plan):
+    """Log-probabilities of given tokens, entropy and the largest alternatives, from logits.
+
+    logp = log softmax(scale * logits)[token]; entropy of that distribution; the ``top`` largest logits of a row in falling
+    order (ties: the lowest index), as log-probabilities and indices.  Rows with a negative token are masked: zeros, and
+    -1 for their indices.
+    """
+    _destroy = staticmethod(_lib.conv_bwd_logp_destroy)
+
+    def __init__(self, vocab, dtype="bf16", top=0, scale=1.0):
+        super().__init__()
+        self.vocab, self.top = int(vocab), int(top)
+        self._code = _dtype(dtype)
+        self.dtype = _TORCH[self._code]
+        desc, h = LogpDesc(self.vocab, self._code, self.top, scale), _vp()
+        _check(_lib.conv_bwd_logp_create(ctypes.byref(desc), ctypes.byref(h)), "conv_bwd_logp_create")
+        self._h = h.value
+
+    def forward(self, logits, tokens=None, stream=None):
+        """(logp [rows], entropy [rows], lse [rows], top_logp [rows, top], top_tokens [rows, top]); logp is None without
+        ``tokens``, the last two with ``top`` 0.  lse and entropy are what ``backward`` needs."""
+        at = self._device_index
+        t, ld = _rows(logits, self.vocab, self.dtype, at, "logits")
+        given = None if tokens is None else _vector(tokens, t, torch.int32, at, "tokens")
+        device, f = logits.device, torch.float32
+        logp = None if tokens is None else _empty((t,), f, device, stream)
+        entropy, lse = _empty((t,), f, device, stream), _empty((t,), f, device, stream)
+        top_logp = top_tokens = None
+        if self.top:
+            top_logp, top_tokens = _empty((t, self.top), f, device, stream), _empty((t, self.top), torch.int32, device, stream)
+        _check(_lib.conv_bwd_logp_forward(self._h, t, logits.data_ptr(), ld, given, None if logp is None else logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+                                          top_logp.data_ptr() if self.top else None, top_tokens.data_ptr() if self.top else None, _stream(stream, device)), "conv_bwd_logp_forward")
+        return logp, entropy, lse, top_logp, top_tokens
+
+    def backward(self, logits, tokens, lse, entropy=None, grad_logp=None, grad_entropy=None, out=None, stream=None):
+        """dlogits from the forward's lse and entropy and the gradients of logp and entropy, [rows] each (one may be None;
+        ``entropy`` goes with ``grad_entropy``, ``tokens`` with ``grad_logp``); ``out`` may be logits."""
+        at = self._device_index
+        t, ld = _rows(logits, self.vocab, self.dtype, at, "logits")
+        f = torch.float32
+        if grad_logp is None and grad_entropy is None:
+            raise ValueError("grad_logp or grad_entropy wanted")
+        if (grad_logp is not None and tokens is None) or (grad_entropy is not None and entropy is None):
+            raise ValueError("grad_logp wants tokens, grad_entropy wants entropy")
+        args = (self._h, t, logits.data_ptr(), ld, None if tokens is None else _vector(tokens, t, torch.int32, at, "tokens"),
+                _vector(lse, t, f, at, "lse"), None if entropy is None else _vector(entropy, t, f, at, "entropy"),
+                None if grad_logp is None else _vector(grad_logp, t, f, at, "grad_logp"), None if grad_entropy is None else _vector(grad_entropy, t, f, at, "grad_entropy"))
+        given = out
+        if out is None:
+            out, ldd = _empty((t, self.vocab), self.dtype, logits.device, stream), self.vocab
+        else:
+            r, ldd = _rows(out, self.vocab, self.dtype, at, "out")
+            if r != t:
+                raise ValueError(f"out: {t} rows wanted, got {r}")
+        _check(_lib.conv_bwd_logp_backward(*args, out.data_ptr(), ldd, _stream(stream, logits.device)), "conv_bwd_logp_backward")
+        if given is not None:
+            _written(given)
+        return out
+
+    def status(self, stream=None):
+        """(status, detail) of the calls since the last one; synchronises the stream."""
+        return _status(_lib.conv_bwd_logp_get_status, self._h, stream)

@@ -185,6 +185,61 @@ conv_bwd_status conv_bwd_policy_forward_backward(conv_bwd_policy_plan plan, int6
 
 conv_bwd_status conv_bwd_policy_get_status(conv_bwd_policy_plan plan, void *stream, int32_t *detail);
 
+/* ---- log-probabilities of given tokens, entropy, alternatives ------------------
+ *
+ * Per row z [vocab] with given token a (what the policy loss takes as old_logp
+ * and ref_logp, an entropy bonus, what a sampler reports):
+ *   lse = log sum_v exp(scale*z[v]),   p_v = exp(scale*z[v] - lse)
+ *   logp = scale*z[a] - lse
+ *   entropy = -sum_v p_v (scale*z[v] - lse)
+ *   top_tokens, top_logp [rows][top]: the largest logits in falling order, ties by
+ *     the lowest index (-0 and 0 tie), and their log-probabilities
+ *   dlogits[v] = scale*(grad_logp*([v == a] - p_v) - grad_entropy*p_v*(scale*z[v] - lse + entropy))
+ *
+ * tokens may be NULL (no given tokens: logp is NULL too, resp. grad_logp).  A row
+ * with a < 0 is masked: it is not read, its logp, entropy, lse and top_logp are 0,
+ * its top_tokens -1, its dlogits +0.  a >= vocab is recorded as a DEVICE_FAULT and
+ * treated as masked.  A row whose two gradients are 0 gets +0 and is not read.
+ * -inf logits have probability 0 and may be alternatives (where too few others
+ * are left) and given tokens (logp -inf).  A row whose logits are all -inf has no
+ * distribution: its lse is -inf, its logp, entropy, top_logp and gradient NaN.  A NaN or
+ * +inf makes the row's logp, entropy, lse and top_logp NaN; NaNs are no
+ * alternatives, and where fewer than `top` logits are left the last top_tokens are
+ * -1 (top_logp NaN).  All arithmetic is fp32 or wider, dlogits are rounded once.
+ *
+ * logits [rows][ld]; ld >= vocab in elements, any alignment (0 = dense). */
+typedef struct {
+    int64_t vocab;
+    int32_t dtype;   /* conv_bwd_dtype of logits and dlogits */
+    int32_t top;     /* 0 .. 32 alternatives of a row */
+    float scale;     /* > 0, finite */
+} conv_bwd_logp_desc;
+
+typedef struct conv_bwd_logp_plan_s *conv_bwd_logp_plan;
+/* Errors: INVALID_ARG (vocab < 1, unknown dtype, top < 0 or > vocab, scale),
+ * UNSUPPORTED (vocab > 2^30, top > 32), CUDA. */
+conv_bwd_status conv_bwd_logp_create(const conv_bwd_logp_desc *desc, conv_bwd_logp_plan *out);
+conv_bwd_status conv_bwd_logp_destroy(conv_bwd_logp_plan plan);
+
+/* logp, entropy, lse [rows] fp32, top_logp fp32 and top_tokens int32 [rows][top]
+ * (not looked at where top is 0), all fully written.  rows = 0 writes nothing.
+ * Errors: INVALID_ARG (NULL, rows < 0, ld < vocab, tokens without logp or the
+ * reverse, an output that overlaps an input or another output), MISALIGNED,
+ * UNSUPPORTED (rows > 2^31 - 2^16), CUDA. */
+conv_bwd_status conv_bwd_logp_forward(conv_bwd_logp_plan plan, int64_t rows, const void *logits, int64_t ld,
+                                      const int32_t *tokens, float *logp, float *entropy, float *lse,
+                                      float *top_logp, int32_t *top_tokens, void *stream);
+
+/* dlogits from the forward's lse and entropy and the gradients of logp and
+ * entropy [rows]; either gradient may be NULL (then entropy may be, with
+ * grad_entropy), not both.  dlogits [rows][ldd] may be logits itself (with ldd = ld). */
+conv_bwd_status conv_bwd_logp_backward(conv_bwd_logp_plan plan, int64_t rows, const void *logits, int64_t ld,
+                                       const int32_t *tokens, const float *lse, const float *entropy,
+                                       const float *grad_logp, const float *grad_entropy, void *dlogits,
+                                       int64_t ldd, void *stream);
+
+conv_bwd_status conv_bwd_logp_get_status(conv_bwd_logp_plan plan, void *stream, int32_t *detail);
+
 #ifdef __cplusplus
 }
 #endif
