@@ -3,6 +3,8 @@
 #pragma once
 #include <stdint.h>
 #include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace cbd {
@@ -167,5 +169,34 @@ struct LogpParams {
 int logp_most_items(int num_sms);  // upper bound of rows * parts where parts > 1
 int logp_parts(int64_t rows, int64_t vocab, int dtype, int num_sms);
 cudaError_t launch_logp(const LogpParams &p, int dtype, bool backward, int num_sms, cudaStream_t s);
+
+// Orthogonalised updates.
+struct OrthPrepParams {
+    const void *grad;        // [batch] matrices, `ls` elements apart, rows `ld` apart
+    float *momentum;         // dense, or NULL
+    __half *hi, *lo;         // [batch][rows][pitch]
+    double *partial;         // [batch][parts]
+    int64_t ls, ld;
+    int32_t batch, rows, cols, pitch, parts, bf16, nesterov;
+    float beta;
+};
+cudaError_t launch_orth_prep(const OrthPrepParams &p, bool by_four, cudaStream_t s);
+// D [M][N] = sum over K of A B, operands in planes hi and lo, tile 256 x 256 (wide) or 128
+struct OrthGemmParams {
+    CUtensorMap a[2], b[2];
+    CUtensorMap out[2], out_t[2];  // boxes of 32 rows x 64 columns, transposed 64 x 32
+    const __half *old[2];          // square: A
+    void *result;                  // final: the result, or the step on the weights
+    float *weight;
+    __nv_bfloat16 *copy;
+    int32_t *status;
+    int64_t wait_budget;
+    int64_t ldo, lse;              // of the caller's tensors: rows, matrices
+    int32_t M, N, K, batch, tiles; // tiles of a matrix
+    int32_t symmetric, terms, final, bf16, ld_old;
+    float mul, mul_old, diagonal, rate, keep;
+};
+// a_mn, b_mn: the operand's contraction runs along its rows (a_mn only with b_mn)
+cudaError_t launch_orth_gemm(const OrthGemmParams &p, bool a_mn, bool b_mn, bool wide, int num_sms, cudaStream_t s);
 
 }  // namespace cbd

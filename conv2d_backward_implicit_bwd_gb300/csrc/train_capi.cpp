@@ -192,6 +192,22 @@ struct conv_bwd_logp_plan_s {
     DevicePart dev;
 };
 
+struct conv_bwd_orth_plan_s {
+    struct Plane {  // tensor maps of one plane of a matrix, of both tile widths
+        CUtensorMap rows128, rows64, store, store_t;
+    };
+    struct Matrix {
+        __half *at[2] = {};
+        Plane plane[2];
+    };
+    conv_bwd_orth_desc d;
+    std::vector<float> coef;  // a, b, c of every step
+    int32_t pitch = 0, pitch_gram = 0, most_parts = 0;
+    double *partial = nullptr;
+    Matrix x[2], gram, poly;
+    DevicePart dev;
+};
+
 extern "C" {
 
 // ---- expert products --------------------------------------------------------
@@ -720,6 +736,231 @@ conv_bwd_status conv_bwd_logp_backward(conv_bwd_logp_plan p, int64_t rows, const
     return logp_run(p, true, lp, rows, ld, ldd, stream);
 }
 conv_bwd_status conv_bwd_logp_get_status(conv_bwd_logp_plan p, void *stream, int32_t *detail) {
+    if (!p) return CONV_BWD_ERR_INVALID_ARG;
+    return read_status(p->dev, stream, detail);
+}
+
+// ---- orthogonalised updates -------------------------------------------------------
+// A plane [batch][rows][pitch] of fp16 as the products read and write it.
+static bool map_plane(CUtensorMap *m, void *at, int64_t batch, int64_t rows, int64_t cols, int64_t pitch, uint32_t box_cols,
+                      uint32_t box_rows, bool swizzled) {
+    EncodeTiled enc = encode_tiled();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
+    cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)pitch * (cuuint64_t)rows * 2};
+    cuuint32_t box[3] = {box_cols, box_rows, 1}, one[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, at, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_plan *out) {
+    if (!out) return CONV_BWD_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!d || d->batch < 1 || d->rows < 1 || d->cols < 1 || !known_dtype(d->dtype) || d->steps < 1 || !d->coefficients)
+        return CONV_BWD_ERR_INVALID_ARG;
+    if (d->batch > 65535 || d->rows > 65536 || d->cols > 65536 || d->batch * d->rows * d->cols > (1LL << 34) || d->steps > 64)
+        return CONV_BWD_ERR_UNSUPPORTED;
+    for (int i = 0; i < 3 * d->steps; ++i)
+        if (!(std::fabs(d->coefficients[i]) <= 32.f)) return CONV_BWD_ERR_INVALID_ARG;
+    return create_plan(out, [&](conv_bwd_orth_plan_s &p) {
+        p.d = *d;
+        p.coef.assign(d->coefficients, d->coefficients + 3 * d->steps);
+        p.d.coefficients = nullptr;
+        int sms = 0, dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            sms = 0;
+        cudaGetLastError();
+        const int64_t g = std::min(d->rows, d->cols);
+        p.pitch = (int32_t)((d->cols + 7) / 8 * 8);
+        p.pitch_gram = (int32_t)((g + 7) / 8 * 8);
+        p.most_parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>((d->rows * d->cols + 4095) / 4096, 8LL * sms / d->batch));
+        auto lines = [](size_t n) { return (n + 255) / 256 * 256; };
+        const size_t partial = lines((size_t)d->batch * p.most_parts * 8), whole = lines((size_t)d->batch * d->rows * p.pitch * 2),
+                     square = lines((size_t)d->batch * g * p.pitch_gram * 2);
+        const conv_bwd_status st = p.dev.init(256 + partial + 4 * whole + 4 * square);
+        if (st != CONV_BWD_OK || !p.dev.has_device) return st;
+        char *at = static_cast<char *>(p.dev.mem) + 256;
+        p.partial = reinterpret_cast<double *>(at);
+        at += partial;
+        bool ok = true;
+        auto place = [&](conv_bwd_orth_plan_s::Matrix &m, int64_t rows, int64_t cols, int64_t pitch, size_t bytes) {
+            for (int i = 0; i < 2; ++i, at += bytes) {
+                m.at[i] = reinterpret_cast<__half *>(at);
+                auto &q = m.plane[i];
+                ok = ok && map_plane(&q.rows128, at, d->batch, rows, cols, pitch, 64, 128, true) &&
+                     map_plane(&q.rows64, at, d->batch, rows, cols, pitch, 64, 64, true) &&
+                     map_plane(&q.store, at, d->batch, rows, cols, pitch, 64, 32, true) &&
+                     map_plane(&q.store_t, at, d->batch, rows, cols, pitch, 32, 64, false);
+            }
+        };
+        place(p.x[0], d->rows, d->cols, p.pitch, whole);
+        place(p.x[1], d->rows, d->cols, p.pitch, whole);
+        place(p.gram, g, g, p.pitch_gram, square);
+        place(p.poly, g, g, p.pitch_gram, square);
+        return ok ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
+    });
+}
+conv_bwd_status conv_bwd_orth_destroy(conv_bwd_orth_plan p) {
+    delete p;
+    return CONV_BWD_OK;
+}
+
+// What the last product does with its result.
+struct OrthOut {
+    void *result = nullptr;
+    float *weight = nullptr;
+    __nv_bfloat16 *copy = nullptr;
+    int64_t ldo = 0, lse = 0;
+    float rate = 0.f, keep = 1.f;
+};
+static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const OrthOut &o, cudaStream_t s) {
+    const conv_bwd_orth_desc &d = p->d;
+    const bool high = d.rows > d.cols;
+    const int32_t g = (int32_t)std::min(d.rows, d.cols), sms = p->dev.num_sms;
+    pp.hi = p->x[0].at[0];
+    pp.lo = p->x[0].at[1];
+    pp.partial = p->partial;
+    pp.batch = (int32_t)d.batch; pp.rows = (int32_t)d.rows; pp.cols = (int32_t)d.cols; pp.pitch = p->pitch;
+    pp.parts = p->most_parts;
+    pp.bf16 = d.dtype == CONV_BWD_BF16;
+    const bool by_four = d.cols % 4 == 0 && pp.ld % 4 == 0 && pp.ls % 4 == 0 && (uintptr_t)pp.grad % (4 * esize(d.dtype)) == 0 &&
+                         (uintptr_t)pp.momentum % 16 == 0;
+    if (launch_orth_prep(pp, by_four, s) != cudaSuccess) return CONV_BWD_ERR_CUDA;
+    const float up = 1024.f, up_poly = 256.f;  // what the planes' values are multiplied by
+    auto product = [&](const conv_bwd_orth_plan_s::Matrix &a, bool a_mn, const conv_bwd_orth_plan_s::Matrix &b, bool b_mn,
+                       const conv_bwd_orth_plan_s::Matrix *to, int64_t M, int64_t N, int64_t K, bool symmetric, OrthGemmParams &q) {
+        const int64_t mt = (M + 255) / 256;
+        auto tiles = [&](int64_t w) {
+            const int64_t nt = (N + w - 1) / w;
+            int64_t n = mt * nt;
+            if (symmetric)
+                for (int64_t i = 0; i < mt; ++i) n -= i * (256 / w);
+            return n;
+        };
+        const bool wide = tiles(256) * d.batch >= sms / 2;
+        q.tiles = (int32_t)tiles(wide ? 256 : 128);
+        for (int i = 0; i < 2; ++i) {
+            q.a[i] = a_mn ? a.plane[i].rows64 : a.plane[i].rows128;
+            q.b[i] = b_mn || !wide ? b.plane[i].rows64 : b.plane[i].rows128;
+            if (to) {
+                q.out[i] = to->plane[i].store;
+                q.out_t[i] = to->plane[i].store_t;
+            }
+        }
+        q.M = (int32_t)M; q.N = (int32_t)N; q.K = (int32_t)K;
+        q.batch = (int32_t)d.batch;
+        q.symmetric = symmetric;
+        q.terms = 3;
+        q.status = p->dev.status();
+        q.wait_budget = (int64_t)p->dev.clock_khz * 2000;
+        return launch_orth_gemm(q, a_mn, b_mn, wide, sms, s) == cudaSuccess;
+    };
+    for (int32_t i = 0; i < d.steps; ++i) {
+        const float a = p->coef[3 * i], b = p->coef[3 * i + 1], c = p->coef[3 * i + 2];
+        const auto &x = p->x[i & 1];
+        OrthGemmParams q;
+        std::memset(&q, 0, sizeof(q));
+        q.mul = 1.f / up;
+        if (!product(x, high, x, high, &p->gram, g, g, high ? d.rows : d.cols, true, q)) return CONV_BWD_ERR_CUDA;
+        std::memset(&q, 0, sizeof(q));
+        q.mul = c * up_poly / (up * up);
+        q.mul_old = b * up_poly / up;
+        q.diagonal = a * up_poly;
+        q.old[0] = p->gram.at[0];
+        q.old[1] = p->gram.at[1];
+        q.ld_old = p->pitch_gram;
+        if (!product(p->gram, false, p->gram, false, &p->poly, g, g, g, true, q)) return CONV_BWD_ERR_CUDA;
+        std::memset(&q, 0, sizeof(q));
+        const bool last = i + 1 == d.steps;
+        q.mul = last ? 1.f / (up_poly * up) : 1.f / up_poly;
+        if (last) {
+            q.final = 1;
+            q.result = o.result;
+            q.bf16 = pp.bf16;
+            q.weight = o.weight;
+            q.copy = o.copy;
+            q.ldo = o.ldo;
+            q.lse = o.lse;
+            q.rate = o.rate;
+            q.keep = o.keep;
+        }
+        const bool ok = high ? product(x, false, p->poly, false, last ? nullptr : &p->x[(i + 1) & 1], d.rows, d.cols, g, false, q)
+                             : product(p->poly, false, x, true, last ? nullptr : &p->x[(i + 1) & 1], d.rows, d.cols, g, false, q);
+        if (!ok) return CONV_BWD_ERR_CUDA;
+    }
+    return CONV_BWD_OK;
+}
+
+// Checks a stack of matrices with row stride ld and matrix stride ls (0: dense) and fills the strides in.
+static conv_bwd_status orth_strides(const conv_bwd_orth_desc &d, int64_t &ld, int64_t &ls, size_t es, size_t &bytes) {
+    if (ld == 0) ld = d.cols;
+    if (ls == 0) ls = ld * (d.rows - 1) + d.cols;
+    if (ld < d.cols || ls < ld * (d.rows - 1) + d.cols) return CONV_BWD_ERR_INVALID_ARG;
+    if (ld > (1LL << 31) || ls > (1LL << 40)) return CONV_BWD_ERR_UNSUPPORTED;
+    bytes = ((size_t)(d.batch - 1) * (size_t)ls + (size_t)(d.rows - 1) * (size_t)ld + (size_t)d.cols) * es;
+    return CONV_BWD_OK;
+}
+
+conv_bwd_status conv_bwd_orth_apply(conv_bwd_orth_plan p, const void *x, int64_t ldx, int64_t lsx, void *out, int64_t ldo,
+                                    int64_t lso, void *stream) {
+    Range range("conv_bwd_orth_apply");
+    if (!p || !x || !out) return CONV_BWD_ERR_INVALID_ARG;
+    const size_t es = esize(p->d.dtype);
+    size_t nx, no;
+    conv_bwd_status st = orth_strides(p->d, ldx, lsx, es, nx);
+    if (st == CONV_BWD_OK) st = orth_strides(p->d, ldo, lso, es, no);
+    if (st != CONV_BWD_OK) return st;
+    if (((uintptr_t)x | (uintptr_t)out) % es) return CONV_BWD_ERR_MISALIGNED;
+    if (!p->dev.has_device) return CONV_BWD_ERR_CUDA;
+    if (!p->dev.current()) return CONV_BWD_ERR_INVALID_ARG;
+    OrthPrepParams pp;
+    std::memset(&pp, 0, sizeof(pp));
+    pp.grad = x;
+    pp.ld = ldx;
+    pp.ls = lsx;
+    OrthOut o;
+    o.result = out;
+    o.ldo = ldo;
+    o.lse = lso;
+    return orth_run(p, pp, o, (cudaStream_t)stream);
+}
+conv_bwd_status conv_bwd_orth_update(conv_bwd_orth_plan p, float *weight, const void *grad, int64_t ldg, int64_t lsg, float *momentum,
+                                     void *copy, float lr, float beta, int32_t nesterov, float decay, float scale, void *stream) {
+    Range range("conv_bwd_orth_update");
+    if (!p || !weight || !grad || !momentum) return CONV_BWD_ERR_INVALID_ARG;
+    if (!std::isfinite(lr) || !std::isfinite(decay) || !std::isfinite(scale) || !(beta >= 0.f && beta <= 1.f)) return CONV_BWD_ERR_INVALID_ARG;
+    const conv_bwd_orth_desc &d = p->d;
+    const size_t es = esize(d.dtype), n = (size_t)d.batch * d.rows * d.cols;
+    size_t ng;
+    const conv_bwd_status st = orth_strides(d, ldg, lsg, es, ng);
+    if (st != CONV_BWD_OK) return st;
+    if (((uintptr_t)weight | (uintptr_t)momentum) % 4 || (uintptr_t)copy % 2 || (uintptr_t)grad % es) return CONV_BWD_ERR_MISALIGNED;
+    if (overlap(weight, 4 * n, momentum, 4 * n) || overlap(weight, 4 * n, grad, ng) || overlap(momentum, 4 * n, grad, ng))
+        return CONV_BWD_ERR_INVALID_ARG;
+    if (copy && (overlap(copy, 2 * n, weight, 4 * n) || overlap(copy, 2 * n, momentum, 4 * n) || overlap(copy, 2 * n, grad, ng)))
+        return CONV_BWD_ERR_INVALID_ARG;
+    if (!p->dev.has_device) return CONV_BWD_ERR_CUDA;
+    if (!p->dev.current()) return CONV_BWD_ERR_INVALID_ARG;
+    OrthPrepParams pp;
+    std::memset(&pp, 0, sizeof(pp));
+    pp.grad = grad;
+    pp.ld = ldg;
+    pp.ls = lsg;
+    pp.momentum = momentum;
+    pp.beta = beta;
+    pp.nesterov = nesterov ? 1 : 0;
+    OrthOut o;
+    o.weight = weight;
+    o.copy = static_cast<__nv_bfloat16 *>(copy);
+    o.ldo = d.cols;
+    o.lse = d.rows * d.cols;
+    o.rate = lr * scale;
+    o.keep = 1.f - lr * decay;
+    return orth_run(p, pp, o, (cudaStream_t)stream);
+}
+conv_bwd_status conv_bwd_orth_get_status(conv_bwd_orth_plan p, void *stream, int32_t *detail) {
     if (!p) return CONV_BWD_ERR_INVALID_ARG;
     return read_status(p->dev, stream, detail);
 }

@@ -34,7 +34,8 @@ EXPORTED = [
     "conv_bwd_clip_norm", "conv_bwd_clip_run", "conv_bwd_clip_get_status", "conv_bwd_policy_create", "conv_bwd_policy_destroy",
     "conv_bwd_policy_forward", "conv_bwd_policy_backward", "conv_bwd_policy_forward_backward",
     "conv_bwd_policy_get_status", "conv_bwd_logp_create", "conv_bwd_logp_destroy", "conv_bwd_logp_forward",
-    "conv_bwd_logp_backward", "conv_bwd_logp_get_status",
+    "conv_bwd_logp_backward", "conv_bwd_logp_get_status", "conv_bwd_orth_create", "conv_bwd_orth_destroy",
+    "conv_bwd_orth_apply", "conv_bwd_orth_update", "conv_bwd_orth_get_status",
 ]
 
 
@@ -49,6 +50,11 @@ class PolicyDesc(ctypes.Structure):
 
 class LogpDesc(ctypes.Structure):
     _fields_ = [("vocab", _i64), ("dtype", _i32), ("top", _i32), ("scale", _f32)]
+
+
+class OrthDesc(ctypes.Structure):
+    _fields_ = [("batch", _i64), ("rows", _i64), ("cols", _i64), ("dtype", _i32), ("steps", _i32),
+                ("coefficients", ctypes.POINTER(_f32))]
 
 
 def _declare():
@@ -77,6 +83,11 @@ def _declare():
         "conv_bwd_logp_forward": [_vp, _i64, _vp, _i64] + [_vp] * 7,
         "conv_bwd_logp_backward": [_vp, _i64, _vp, _i64] + [_vp] * 6 + [_i64, _vp],
         "conv_bwd_logp_get_status": [_vp, _vp, P(_i32)],
+        "conv_bwd_orth_create": [P(OrthDesc), P(_vp)],
+        "conv_bwd_orth_destroy": [_vp],
+        "conv_bwd_orth_apply": [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp],
+        "conv_bwd_orth_update": [_vp, _vp, _vp, _i64, _i64, _vp, _vp, _f32, _f32, _i32, _f32, _f32, _vp],
+        "conv_bwd_orth_get_status": [_vp, _vp, P(_i32)],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -452,3 +463,78 @@ class TokenLogp(_Plan):
     def status(self, stream=None):
         """(status, detail) of the calls since the last one; synchronises the stream."""
         return _status(_lib.conv_bwd_logp_get_status, self._h, stream)
+
+
+class Orthogonal(_Plan):
+    """Orthogonalised updates of matrices [batch, rows, cols] by Newton-Schulz products, as the Muon optimiser makes them.
+
+    X = u / |u|, then ``steps`` times X <- a X + b (X X^T) X + c (X X^T)^2 X for each matrix.  ``coefficients`` is (a, b, c) or a
+    list of one such triple for each step.  ``dtype`` is that of the matrices of ``apply``, resp. of the gradients.
+    """
+    _destroy = staticmethod(_lib.conv_bwd_orth_destroy)
+
+    def __init__(self, batch, rows, cols, dtype="bf16", steps=5, coefficients=(3.4445, -4.7750, 2.0315)):
+        super().__init__()
+        self.batch, self.rows, self.cols, self.steps = int(batch), int(rows), int(cols), int(steps)
+        self._shape = (self.batch, self.rows, self.cols)
+        self._code = _dtype(dtype)
+        self.dtype = _TORCH[self._code]
+        c = list(coefficients)
+        if c and not hasattr(c[0], "__len__"):
+            c = [c] * max(self.steps, 1)
+        c = [float(v) for triple in c for v in triple]
+        if len(c) != 3 * max(self.steps, 1):
+            raise ValueError(f"coefficients: three numbers, or three for each of {self.steps} steps wanted")
+        desc, h = OrthDesc(*self._shape, self._code, self.steps, (_f32 * len(c))(*c)), _vp()
+        _check(_lib.conv_bwd_orth_create(ctypes.byref(desc), ctypes.byref(h)), "conv_bwd_orth_create")
+        self._h = h.value
+
+    def _matrices(self, t, dtype, what):
+        """Row stride and matrix stride of a batch with unit column stride."""
+        if t.dtype != dtype or t.shape != self._shape or t.get_device() != self._device_index:
+            raise ValueError(f"{what}: a {dtype} tensor {list(self._shape)} {_on(self._device_index)} wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        ls, ld, unit = t.stride()
+        if self.rows == 1:
+            ld = self.cols
+        if self.batch == 1:
+            ls = ld * (self.rows - 1) + self.cols
+        if (unit != 1 and self.cols > 1) or ld < self.cols or ls < ld * (self.rows - 1) + self.cols:
+            raise ValueError(f"{what}: unit column stride, rows and matrices that do not overlap wanted, got strides {t.stride()}")
+        return ld, ls
+
+    def _dense(self, t, dtype, what):
+        if t.dtype != dtype or t.shape != self._shape or t.get_device() != self._device_index or not t.is_contiguous():
+            raise ValueError(f"{what}: a contiguous {dtype} tensor {list(self._shape)} {_on(self._device_index)} wanted, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    def apply(self, x, out=None, stream=None):
+        """The orthogonalised matrices in x's type; ``out`` may be x."""
+        ld, ls = self._matrices(x, self.dtype, "x")
+        given = out
+        if out is None:
+            out = _empty(self._shape, self.dtype, x.device, stream)
+        ldo, lso = self._matrices(out, self.dtype, "out")
+        _check(_lib.conv_bwd_orth_apply(self._h, x.data_ptr(), ld, ls, out.data_ptr(), ldo, lso, _stream(stream, x.device)), "conv_bwd_orth_apply")
+        if given is not None:
+            _written(given)
+        return out
+
+    def update(self, weight, grad, momentum, lr, beta=0.95, nesterov=True, decay=0.0, scale=None, copy=None, stream=None):
+        """One optimiser step, in place on ``weight`` and ``momentum`` (fp32):
+
+        momentum <- beta momentum + grad;  u = grad + beta momentum (``nesterov``) or momentum;  X as in ``apply`` from u;
+        weight <- weight (1 - lr decay) - lr scale X;  ``copy`` (bf16) gets the new weight.
+        ``scale`` is sqrt(max(1, rows / cols)) if not given.
+        """
+        ld, ls = self._matrices(grad, self.dtype, "grad")
+        w, m = self._dense(weight, torch.float32, "weight"), self._dense(momentum, torch.float32, "momentum")
+        c = None if copy is None else self._dense(copy, torch.bfloat16, "copy")
+        if scale is None:
+            scale = max(1.0, self.rows / self.cols) ** 0.5
+        _check(_lib.conv_bwd_orth_update(self._h, w, grad.data_ptr(), ld, ls, m, c, lr, beta, 1 if nesterov else 0, decay, scale,
+                                         _stream(stream, grad.device)), "conv_bwd_orth_update")
+        _written((weight, momentum) if copy is None else (weight, momentum, copy))
+
+    def status(self, stream=None):
+        """(status, detail) of the calls since the last one; synchronises the stream."""
+        return _status(_lib.conv_bwd_orth_get_status, self._h, stream)

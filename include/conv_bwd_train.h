@@ -240,6 +240,56 @@ conv_bwd_status conv_bwd_logp_backward(conv_bwd_logp_plan plan, int64_t rows, co
 
 conv_bwd_status conv_bwd_logp_get_status(conv_bwd_logp_plan plan, void *stream, int32_t *detail);
 
+/* ---- orthogonalised updates -----------------------------------------------------
+ *
+ * For each matrix of a batch, [rows][cols], with X = u / |u| (Frobenius norm):
+ *   `steps` times  X <- a X + b (X X^T) X + c (X X^T)^2 X
+ * which takes the singular values towards 1 and leaves the singular vectors (the
+ * update of the Muon optimiser; (a, b, c) = (3.4445, -4.7750, 2.0315), five steps).
+ *
+ *   apply:   out = X for u = x
+ *   update:  momentum <- beta momentum + grad
+ *            u = grad + beta momentum (nesterov) or momentum
+ *            weight <- weight (1 - lr decay) - lr scale X
+ *            copy = weight in bf16 (where copy is not NULL)
+ *
+ * A matrix of zeros gives zeros; one whose norm is not finite gives NaN
+ * throughout, and the other matrices of the batch are not touched by it.  The norm
+ * neither overflows nor underflows.  The products' operands are held to 22 bits and
+ * summed in fp32: against exact arithmetic X is off by some 2^-16 of its norm
+ * (a rounding of u's size grows by a a step beside a small singular value).  They are
+ * fp16 pairs with a range: where X's singular values leave [0, 60] or a + b s^2 + c s^4 leaves
+ * [-255, 255] between the steps, the result is not finite. */
+typedef struct {
+    int64_t batch, rows, cols;
+    int32_t dtype;               /* conv_bwd_dtype of x and out, resp. of grad */
+    int32_t steps;               /* 1 .. 64 */
+    const float *coefficients;   /* a, b, c of every step, of magnitude 32 at most; read by create */
+} conv_bwd_orth_desc;
+
+typedef struct conv_bwd_orth_plan_s *conv_bwd_orth_plan;
+/* The plan's workspace is 8 bytes an element and 8 bytes for each element of
+ * the smaller side's square.  Errors: INVALID_ARG (a size or steps < 1, unknown dtype, NULL or too
+ * large coefficients), UNSUPPORTED (batch > 65535, a side > 65536, more than
+ * 2^34 elements, steps > 64), CUDA (allocation failed). */
+conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *desc, conv_bwd_orth_plan *out);
+conv_bwd_status conv_bwd_orth_destroy(conv_bwd_orth_plan plan);
+
+/* ld* are row strides, ls* matrix strides in elements (0: dense).  out may be x or
+ * overlap it: it is written after x has been read.  Errors: INVALID_ARG (NULL, rows or matrices
+ * that overlap one another), MISALIGNED (a pointer not aligned to its element),
+ * UNSUPPORTED (a stride > 2^31 or 2^40), CUDA. */
+conv_bwd_status conv_bwd_orth_apply(conv_bwd_orth_plan plan, const void *x, int64_t ldx, int64_t lsx, void *out,
+                                    int64_t ldo, int64_t lso, void *stream);
+
+/* weight and momentum fp32, copy bf16 (may be NULL), dense and without overlap
+ * with one another or grad.  lr, decay and scale finite, 0 <= beta <= 1 (else INVALID_ARG). */
+conv_bwd_status conv_bwd_orth_update(conv_bwd_orth_plan plan, float *weight, const void *grad, int64_t ldg, int64_t lsg,
+                                     float *momentum, void *copy, float lr, float beta, int32_t nesterov, float decay,
+                                     float scale, void *stream);
+
+conv_bwd_status conv_bwd_orth_get_status(conv_bwd_orth_plan plan, void *stream, int32_t *detail);
+
 #ifdef __cplusplus
 }
 #endif
