@@ -5,8 +5,15 @@
 //   gram     A = X X^T                  or X^T X
 //   square   B = c A A + b A + a I
 //   product  X' = B X                   or X B
-// three products a step, each a launch; the first two are symmetric: tiles below the diagonal blocks are not
-// computed but written transposed from those above.
+// three products a step; the first two are symmetric: tiles below the diagonal blocks are not computed but written
+// transposed from those above.
+//
+// Schedule.  One cooperative launch does all the products: a list of tiles in order of step, product, matrix; pair b of P
+// takes tiles b, b + P, ...  A tile begins when its matrix's tiles of the product before are done (a counter for each
+// matrix), which in a batch is long past when the list comes round: no product ends with idle SMs, and there is one launch
+// instead of fifteen.  (The tile with the lowest number that is not done waits for none that is not, and its pair is at it: the
+// waits end.)  Where a product has fewer tiles than there are pairs its contraction is split, and the warp that comes last
+// adds the pieces' sums in order.
 //
 // Precision.  A small singular value grows by a = 3.44 a step, and with it what a rounding has put beside it: one fp16
 // or bf16 product each leaves 0.4 to 4 % (simulated on matrices of falling spectrum), above what a bf16 result holds.
@@ -42,6 +49,7 @@ constexpr int EPI = 8, LOAD_A = 8, LOAD_B = 9, MMA = 10, THREADS = 512;
 constexpr int A_BYTES = 128 * 64 * 2;  // of one plane of a stage
 constexpr int OUT_BYTES = EPI * 4096;
 constexpr int SEGMENT = 2;  // k-blocks (of 64) of one accumulator
+constexpr int MOST_STAGES = 4;
 
 template <int W>
 struct Cfg {
@@ -50,7 +58,7 @@ struct Cfg {
     static constexpr int S = W == 256 ? 3 : 4;
 };
 struct Bars {
-    uint64_t full[4], empty[4], tfull[2], tempty[2];
+    uint64_t full[MOST_STAGES], empty[MOST_STAGES], tfull[2], tempty[2];
     uint32_t tmem;
     int32_t abort;
 };
@@ -60,16 +68,34 @@ constexpr int smem_bytes() {
 }
 static_assert(smem_bytes<256>() <= 232448 && smem_bytes<128>() <= 232448, "shared memory of one CTA");
 
-struct Tile {
-    int e, m0, n0, n;  // matrix, first row and column, columns (a multiple of 32)
+// One piece of the work: of step `step`, its product `kind`, matrix e, a tile's columns of the contraction's blocks [kb0, kb1).
+enum : int { GRAM = 0, SQUARE = 1, PRODUCT = 2 };
+struct Work {
+    int step, kind, e, tile, split;
+    int m0, n0, n;  // first row and column, columns (a multiple of 32)
+    int kb0, kb1;
+    int M, N;
 };
 template <int W>
-__device__ __forceinline__ Tile tile_at(const OrthGemmParams &p, int t) {
-    Tile r;
-    const int nt = (p.N + W - 1) / W;
-    r.e = t / p.tiles;
-    int l = t - r.e * p.tiles, tm, tn;
-    if (p.symmetric) {  // from the diagonal block on
+__device__ __forceinline__ Work work_at(const OrthParams &p, int i) {
+    Work w;
+    const int each[3] = {p.batch * p.tiles_sym * p.splits[0], p.batch * p.tiles_sym * p.splits[1], p.batch * p.tiles_all * p.splits[2]};
+    const int per_step = each[0] + each[1] + each[2];
+    w.step = i / per_step;
+    i -= w.step * per_step;
+    w.kind = i < each[0] ? GRAM : i < each[0] + each[1] ? SQUARE : PRODUCT;
+    i -= w.kind == GRAM ? 0 : w.kind == SQUARE ? each[0] : each[0] + each[1];
+    const int tiles = w.kind == PRODUCT ? p.tiles_all : p.tiles_sym, splits = w.kind == GRAM ? p.splits[0] : w.kind == SQUARE ? p.splits[1] : p.splits[2];
+    w.e = i / (tiles * splits);
+    i -= w.e * tiles * splits;
+    w.tile = i / splits;
+    w.split = i - w.tile * splits;
+    const int g = min(p.rows, p.cols);
+    w.M = w.kind == PRODUCT ? p.rows : g;
+    w.N = w.kind == PRODUCT ? p.cols : g;
+    const int nt = (w.N + W - 1) / W;
+    int l = w.tile, tm, tn;
+    if (w.kind != PRODUCT) {  // from the diagonal block on
         tm = 0;
         for (int len = nt; l >= len; len -= 256 / W) {
             l -= len;
@@ -80,10 +106,34 @@ __device__ __forceinline__ Tile tile_at(const OrthGemmParams &p, int t) {
         tm = l / nt;
         tn = l - tm * nt;
     }
-    r.m0 = tm * 256;
-    r.n0 = tn * W;
-    r.n = min(W, (p.N - r.n0 + 31) & ~31);
-    return r;
+    w.m0 = tm * 256;
+    w.n0 = tn * W;
+    w.n = min(W, (w.N - w.n0 + 31) & ~31);
+    const int kblocks = ((w.kind == GRAM ? max(p.rows, p.cols) : g) + 63) / 64;
+    w.kb0 = (int)((int64_t)kblocks * w.split / splits);
+    w.kb1 = (int)((int64_t)kblocks * (w.split + 1) / splits);
+    return w;
+}
+// warps that have finished with matrix e before w's operands are there
+__device__ __forceinline__ int needed(const OrthParams &p, const Work &w) {
+    return 2 * EPI * (w.step * (2 * p.tiles_sym + p.tiles_all) + w.kind * p.tiles_sym);
+}
+__device__ __forceinline__ bool wait_done(const OrthParams &p, const Work &w, volatile int32_t *abort, int32_t code) {
+    const int want = needed(p, w);
+    const int32_t *at = p.done + w.e;
+    if (ld_acquire_gpu(at) >= want) return true;
+    const long long t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (ld_acquire_gpu(at) >= want) return true;
+        if ((it & 63) == 0) {
+            if (*abort) return false;
+            if (clock64() - t0 > p.wait_budget) {
+                record_status(p.status, code);
+                *abort = 1;
+                return false;
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ uint32_t pack_hi(float x, float y) {
@@ -103,7 +153,7 @@ __device__ __forceinline__ void store_box(const CUtensorMap *map, uint32_t src, 
 
 // One warp's 32 rows x COLS columns of a tile, in registers, to the planes hi and lo (and transposed).
 template <int COLS>
-__device__ __forceinline__ void store_planes(const OrthGemmParams &p, const float (&v)[COLS], uint8_t *slab, int e, int row, int col, bool mirror, int lane) {
+__device__ __forceinline__ void store_planes(const CUtensorMap *out, const CUtensorMap *out_t, const Work &w, const float (&v)[COLS], uint8_t *slab, int row, int col, int lane) {
     const uint32_t sb = smem_u32(slab);
 #pragma unroll
     for (int g = 0; g < COLS / 64; ++g)
@@ -113,39 +163,40 @@ __device__ __forceinline__ void store_planes(const OrthGemmParams &p, const floa
             __syncwarp();
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                uint32_t w[4];
+                uint32_t u[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float x = v[g * 64 + q * 8 + 2 * i], y = v[g * 64 + q * 8 + 2 * i + 1];
-                    w[i] = plane ? pack_lo(x, y) : pack_hi(x, y);
+                    u[i] = plane ? pack_lo(x, y) : pack_hi(x, y);
                 }
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sb + (uint32_t)lane * 128u + (((uint32_t)q ^ (lane & 7)) << 4)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sb + (uint32_t)lane * 128u + (((uint32_t)q ^ (lane & 7)) << 4)), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]) : "memory");
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && row < p.M && col + g * 64 < p.N) store_box(&p.out[plane], sb, col + g * 64, row, e);
-            if (!mirror) continue;
+            if (lane == 0 && row < w.M && col + g * 64 < w.N) store_box(out + plane, sb, col + g * 64, row, w.e);
+            if (!out_t) continue;
             if (lane == 0) bulk_wait_read();
             __syncwarp();
 #pragma unroll
             for (int q = 0; q < 32; ++q) {
                 const float x = v[g * 64 + 2 * q], y = v[g * 64 + 2 * q + 1];
-                const uint32_t w = plane ? pack_lo(x, y) : pack_hi(x, y);
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(sb + (uint32_t)(2 * q) * 64u + (uint32_t)lane * 2u), "h"((uint16_t)w) : "memory");
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(sb + (uint32_t)(2 * q + 1) * 64u + (uint32_t)lane * 2u), "h"((uint16_t)(w >> 16)) : "memory");
+                const uint32_t u = plane ? pack_lo(x, y) : pack_hi(x, y);
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(sb + (uint32_t)(2 * q) * 64u + (uint32_t)lane * 2u), "h"((uint16_t)u) : "memory");
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(sb + (uint32_t)(2 * q + 1) * 64u + (uint32_t)lane * 2u), "h"((uint16_t)(u >> 16)) : "memory");
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && row < p.M && col + g * 64 < p.N) store_box(&p.out_t[plane], sb, row, col + g * 64, e);
+            if (lane == 0 && row < w.M && col + g * 64 < w.N) store_box(out_t + plane, sb, row, col + g * 64, w.e);
         }
 }
 
 // The same to the caller's tensors: the result itself, or the step on the weights.
 template <int COLS>
-__device__ __forceinline__ void store_result(const OrthGemmParams &p, const float (&v)[COLS], uint8_t *slab, int e, int row, int col, int lane) {
+__device__ __forceinline__ void store_result(const OrthParams &p, const Work &w, const float (&v)[COLS], uint8_t *slab, int row, int col, int lane) {
     const uint32_t sb = smem_u32(slab);
 #pragma unroll
     for (int g = 0; g < COLS / 32; ++g) {
+        if (lane == 0) bulk_wait_read();  // (of the product before)
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -154,30 +205,30 @@ __device__ __forceinline__ void store_result(const OrthGemmParams &p, const floa
                          : "memory");
         __syncwarp();
         const int c = col + g * 32 + lane;
-        if (c >= p.N) continue;
-        for (int r0 = 0; r0 < 32 && row + r0 < p.M; r0 += 8) {
-            float x[8], w[8];
+        if (c >= w.N) continue;
+        for (int r0 = 0; r0 < 32 && row + r0 < w.M; r0 += 8) {
+            float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int r = r0 + i;
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[i]) : "r"(sb + (uint32_t)r * 128u + (((uint32_t)(lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4u) : "memory");
             }
+            const int64_t at = (int64_t)w.e * p.lse + (int64_t)(row + r0) * p.ldo + c;
             if (p.weight) {
-                const int64_t at = (int64_t)e * p.lse + (int64_t)(row + r0) * p.ldo + c;
+                float old[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = row + r0 + i < p.M ? p.weight[at + i * p.ldo] : 0.f;
+                for (int i = 0; i < 8; ++i) old[i] = row + r0 + i < w.M ? p.weight[at + i * p.ldo] : 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if (row + r0 + i >= p.M) break;
-                    const float n = fmaf(-p.rate, x[i], w[i] * p.keep);
+                    if (row + r0 + i >= w.M) break;
+                    const float n = fmaf(-p.rate, x[i], old[i] * p.keep);
                     p.weight[at + i * p.ldo] = n;
                     if (p.copy) p.copy[at + i * p.ldo] = __float2bfloat16_rn(n);
                 }
             } else {
-                const int64_t at = (int64_t)e * p.lse + (int64_t)(row + r0) * p.ldo + c;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if (row + r0 + i >= p.M) break;
+                    if (row + r0 + i >= w.M) break;
                     if (p.bf16)
                         static_cast<__nv_bfloat16 *>(p.result)[at + i * p.ldo] = __float2bfloat16_rn(x[i]);
                     else
@@ -188,8 +239,43 @@ __device__ __forceinline__ void store_result(const OrthGemmParams &p, const floa
     }
 }
 
-template <int W, bool A_MN, bool B_MN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_gemm_kernel(const __grid_constant__ OrthGemmParams p) {
+// A tile whose contraction is split: every piece leaves its sums in the workspace, the warp that comes last adds them in
+// order and goes on with the tile; false for the others.
+template <int COLS>
+__device__ __forceinline__ bool join_splits(const OrthParams &p, const Work &w, float (&sum)[COLS], int splits, int slice, int lane) {
+    const int tiles = w.kind == PRODUCT ? p.tiles_all : p.tiles_sym, tile = w.e * tiles + w.tile;
+    float4 *first = p.parts + (int64_t)(tile * splits) * (2 * EPI * 32 * COLS / 4) + slice * (32 * COLS / 4) + lane;
+    constexpr int STEP = 2 * EPI * 32 * COLS / 4;
+    float4 *mine = first + (int64_t)w.split * STEP;
+#pragma unroll
+    for (int q = 0; q < COLS / 4; ++q) __stcg(mine + q * 32, make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]));
+    __threadfence();
+    __syncwarp();
+    int32_t *counter = p.arrived + tile * 2 * EPI + slice;
+    int before = 0;
+    if (lane == 0) before = atomicAdd(counter, 1);
+    before = __shfl_sync(0xffffffffu, before, 0);
+    if (before != splits - 1) return false;
+    __threadfence();
+    if (lane == 0) *counter = 0;
+#pragma unroll
+    for (int q = 0; q < COLS; ++q) sum[q] = 0.f;
+    for (int k = 0; k < splits; ++k) {
+        const float4 *from = first + (int64_t)k * STEP;
+#pragma unroll
+        for (int q = 0; q < COLS / 4; ++q) {
+            const float4 x = __ldcg(from + q * 32);
+            sum[4 * q] += x.x;
+            sum[4 * q + 1] += x.y;
+            sum[4 * q + 2] += x.z;
+            sum[4 * q + 3] += x.w;
+        }
+    }
+    return true;
+}
+
+template <int W>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_kernel(const __grid_constant__ OrthParams p) {
     using C = Cfg<W>;
     constexpr int S = C::S, COLS = W / 2;
     extern __shared__ uint8_t smem_raw[];
@@ -199,11 +285,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_gem
     volatile int32_t *abort_flag = &bars.abort;
 
     const uint32_t rank = cluster_ctarank();
-    const bool leader = rank == 0;
+    const bool leader = rank == 0, high = p.rows > p.cols;
     const uint32_t full0 = smem_u32(bars.full), empty0 = smem_u32(bars.empty), tfull0 = smem_u32(bars.tfull), tempty0 = smem_u32(bars.tempty);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
-    const int kblocks = (p.K + 63) / 64, total = p.batch * p.tiles;
+    const int pair = blockIdx.x / 2, npairs = gridDim.x / 2, total = p.items;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -222,12 +307,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_gem
         tmem_alloc2(smem_u32(&bars.tmem), 512);
         tc_fence_before();
     }
-    if ((warp == LOAD_A || warp == LOAD_B) && lane == 0)
-        for (int i = 0; i < 2; ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(warp == LOAD_A ? &p.a[i] : &p.b[i])) : "memory");
     cluster_sync_all();
     tc_fence_after();
-    pdl_next();
-    pdl_wait();
     const uint32_t tmem_base = bars.tmem;
     if (threadIdx.x == 0 && !leader) {
         // the pair's MMAs write this CTA's rows at the leader's TMEM address
@@ -243,13 +324,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_gem
         uint8_t *slab = stage + warp * 4096;
         uint32_t use = 0;
         bool ok = true;
-        for (int t = pair; t < total; t += npairs) {
-            const Tile w = tile_at<W>(p, t);
+        for (int i = pair; i < total; i += npairs) {
+            const Work w = work_at<W>(p, i);
             const int row = w.m0 + (int)rank * 128 + (warp % 4) * 32, col0 = (warp / 4) * COLS, col = w.n0 + col0;
             float sum[COLS];
 #pragma unroll
             for (int q = 0; q < COLS; ++q) sum[q] = 0.f;
-            for (int left = kblocks; left > 0; left -= SEGMENT, ++use) {
+            for (int left = w.kb1 - w.kb0; left > 0; left -= SEGMENT, ++use) {
                 const uint32_t b = use & 1;
                 if (ok) ok = mbar_wait_bounded(tfull0 + 8 * b, (use >> 1) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
                 ok = __all_sync(0xffffffffu, ok);
@@ -266,75 +347,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_gem
                 if (lane == 0) arrive_relaxed(tempty_leader0 + 8 * b);
             }
             if (!ok) continue;
-            if (p.old[0]) {
-                // square: c sum + b A + a on the diagonal
+            const int splits = w.kind == GRAM ? p.splits[0] : w.kind == SQUARE ? p.splits[1] : p.splits[2];
+            if (splits > 1 && !join_splits<COLS>(p, w, sum, splits, (int)rank * EPI + warp, lane)) continue;
+            const bool final = w.kind == PRODUCT && w.step + 1 == p.steps;
+            if (w.kind == SQUARE) {
+                // c sum + b A + a on the diagonal; A by other SMs in this launch: past L1
+                const float a = p.coef[3 * w.step] * kOrthUpPoly, b = p.coef[3 * w.step + 1] * (kOrthUpPoly / kOrthUp), c = p.coef[3 * w.step + 2] * (kOrthUpPoly / (kOrthUp * kOrthUp));
                 const int r = row + lane;
-                const int64_t at = ((int64_t)w.e * p.M + r) * p.ld_old;
+                const int64_t at = ((int64_t)w.e * w.M + r) * p.pitch_gram;
+                ok = __all_sync(0xffffffffu, wait_done(p, w, abort_flag, kDevTimeoutEpilogue));
+                if (!ok) continue;
 #pragma unroll
                 for (int q = 0; q < COLS / 8; ++q) {
-                    const int c = col + q * 8;
+                    const int cc = col + q * 8;
                     uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
-                    if (r < p.M && c < p.ld_old) {
-                        h = *reinterpret_cast<const uint4 *>(p.old[0] + at + c);
-                        l = *reinterpret_cast<const uint4 *>(p.old[1] + at + c);
+                    if (r < w.M && cc < p.pitch_gram) {
+                        h = __ldcg(reinterpret_cast<const uint4 *>(p.gram[0] + at + cc));
+                        l = __ldcg(reinterpret_cast<const uint4 *>(p.gram[1] + at + cc));
                     }
                     const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&hw[i])), y = __half22float2(*reinterpret_cast<const __half2 *>(&lw[i]));
-                        float &s0 = sum[q * 8 + 2 * i], &s1 = sum[q * 8 + 2 * i + 1];
-                        s0 = fmaf(p.mul, s0, p.mul_old * (x.x + y.x)) + (r == c + 2 * i ? p.diagonal : 0.f);
-                        s1 = fmaf(p.mul, s1, p.mul_old * (x.y + y.y)) + (r == c + 2 * i + 1 ? p.diagonal : 0.f);
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&hw[k])), y = __half22float2(*reinterpret_cast<const __half2 *>(&lw[k]));
+                        float &s0 = sum[q * 8 + 2 * k], &s1 = sum[q * 8 + 2 * k + 1];
+                        s0 = fmaf(c, s0, b * (x.x + y.x)) + (r == cc + 2 * k ? a : 0.f);
+                        s1 = fmaf(c, s1, b * (x.y + y.y)) + (r == cc + 2 * k + 1 ? a : 0.f);
                     }
                 }
             } else {
+                const float mul = w.kind == GRAM ? 1.f / kOrthUp : final ? 1.f / (kOrthUp * kOrthUpPoly) : 1.f / kOrthUpPoly;
 #pragma unroll
-                for (int q = 0; q < COLS; ++q) sum[q] *= p.mul;
+                for (int q = 0; q < COLS; ++q) sum[q] *= mul;
             }
-            if (p.final)
-                store_result<COLS>(p, sum, slab, w.e, row, col, lane);
-            else
-                store_planes<COLS>(p, sum, slab, w.e, row, col, p.symmetric && w.n0 >= w.m0 + 256, lane);
+            if (final) {
+                store_result<COLS>(p, w, sum, slab, row, col, lane);
+                continue;
+            }
+            const bool mirror = w.kind != PRODUCT && w.n0 >= w.m0 + 256;
+            const CUtensorMap *out = w.kind == GRAM ? p.gram_store : w.kind == SQUARE ? p.poly_store : (w.step & 1) ? p.x_store[0] : p.x_store[1];
+            store_planes<COLS>(out, !mirror ? nullptr : w.kind == GRAM ? p.gram_store_t : p.poly_store_t, w, sum, slab, row, col, lane);
+            // written, and known to be
+            if (lane == 0) {
+                bulk_wait_all();
+                fence_proxy_async_global();
+                asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p.done + w.e) : "memory");
+            }
+            __syncwarp();
         }
-        if (lane == 0) bulk_wait_all();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == LOAD_A || warp == LOAD_B) {
             // ------------------------------------------------------------ loads
             if (lane == 0) {
                 const uint32_t full_leader0 = mapa_shared(full0, 0);
-                const int planes = p.terms == 1 ? 1 : 2;
                 uint32_t it = 0;
                 bool ok = true, issued = false;
-                for (int t = pair; t < total && ok; t += npairs) {
-                    const Tile w = tile_at<W>(p, t);
-                    const int m = w.m0 + (int)rank * 128, n = w.n0 + (int)rank * (w.n / 2);
-                    for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                for (int i = pair; i < total && ok; i += npairs) {
+                    const Work w = work_at<W>(p, i);
+                    const int m = w.m0 + (int)rank * 128, n = w.n0 + (int)rank * (w.n / 2), planes = w.step >= p.single_from ? 1 : 2;
+                    // what other SMs have written in this launch
+                    ok = wait_done(p, w, abort_flag, kDevTimeoutProducer);
+                    if (!ok) break;
+                    fence_proxy_async_global();
+                    const CUtensorMap *map;
+                    if (warp == LOAD_A)
+                        map = w.kind == SQUARE ? p.gram_a : w.kind == GRAM ? p.x_gram_a[w.step & 1] : high ? p.x_prod[w.step & 1] : p.poly_prod;
+                    else
+                        map = w.kind == SQUARE ? p.gram_b : w.kind == GRAM ? p.x_gram_b[w.step & 1] : high ? p.poly_prod : p.x_prod[w.step & 1];
+                    const bool mn = warp == LOAD_A ? high && w.kind == GRAM : high ? w.kind == GRAM : w.kind == PRODUCT;
+                    for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                         const uint32_t s = it % S, ph = (it / S) & 1;
                         if (!mbar_wait_bounded(empty0 + 8 * s, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) {
                             ok = false;
                             break;
                         }
                         const uint32_t bar = full_leader0 + 8 * s, to = smem_u32(smem + s * C::STAGE);
-                        if (warp == LOAD_A) {
-                            if (leader) mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(2 * planes * (A_BYTES + C::B_BYTES)));
-                            for (int i = 0; i < planes; ++i) {
-                                const uint32_t dst = to + i * A_BYTES;
-                                if constexpr (A_MN) {
-                                    tma_load_3d_pair(dst, &p.a[i], bar, m, kb * 64, w.e);
-                                    tma_load_3d_pair(dst + 8192, &p.a[i], bar, m + 64, kb * 64, w.e);
-                                } else {
-                                    tma_load_3d_pair(dst, &p.a[i], bar, kb * 64, m, w.e);
-                                }
-                            }
-                        } else {
-                            for (int i = 0; i < planes; ++i) {
-                                const uint32_t dst = to + 2 * A_BYTES + i * C::B_BYTES;
-                                if constexpr (B_MN) {
-                                    for (int h = 0; h < W / 128; ++h) tma_load_3d_pair(dst + 8192 * h, &p.b[i], bar, n + 64 * h, kb * 64, w.e);
-                                } else {
-                                    tma_load_3d_pair(dst, &p.b[i], bar, kb * 64, n, w.e);
-                                }
+                        if (warp == LOAD_A && leader) mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(2 * planes * (A_BYTES + C::B_BYTES)));
+                        for (int k = 0; k < planes; ++k) {
+                            const uint32_t dst = warp == LOAD_A ? to + k * A_BYTES : to + 2 * A_BYTES + k * C::B_BYTES;
+                            const int across = warp == LOAD_A ? m : n;
+                            if (!mn) {
+                                tma_load_3d_pair(dst, map + k, bar, kb * 64, across, w.e);
+                            } else {
+                                tma_load_3d_pair(dst, map + k, bar, across, kb * 64, w.e);
+                                if (warp == LOAD_A || W == 256) tma_load_3d_pair(dst + 8192, map + k, bar, across + 64, kb * 64, w.e);
                             }
                         }
                         issued = true;
@@ -347,16 +443,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_gem
             __syncwarp();
         } else if (warp == MMA && leader) {
             // ------------------------------------------------------------ MMA
-            constexpr uint32_t A_STEP = A_MN ? 128 : 2, B_STEP = B_MN ? 128 : 2;  // a 16-deep step, in 16 bytes
-            const uint32_t idesc0 = (1u << 4) | ((A_MN ? 1u : 0u) << 15) | ((B_MN ? 1u : 0u) << 16) | ((uint32_t)(256 >> 4) << 24);  // fp16 operands, fp32 sums
-            const uint64_t a_desc0 = smem_desc_sw128(smem_u32(smem), A_MN ? 8192 : 16, 1024);
-            const uint64_t b_desc0 = smem_desc_sw128(smem_u32(smem) + 2 * A_BYTES, B_MN ? 8192 : 16, 1024);
-            const uint32_t a_lo = (uint32_t)a_desc0, a_hi = (uint32_t)(a_desc0 >> 32), b_lo = (uint32_t)b_desc0, b_hi = (uint32_t)(b_desc0 >> 32);
+            const uint32_t a_at = (smem_u32(smem) >> 4) & 0x3FFFu, b_at = ((smem_u32(smem) + 2 * A_BYTES) >> 4) & 0x3FFFu;
+            const uint32_t desc_hi = (uint32_t)(smem_desc_sw128(0, 0, 1024) >> 32);
             uint32_t s = 0, ph = 0, use = 0;
             bool ok = true, issued = false;
-            for (int t = pair; t < total && ok; t += npairs) {
-                const uint32_t id = idesc0 | ((uint32_t)(tile_at<W>(p, t).n >> 3) << 17);
-                for (int left = kblocks; left > 0 && ok;) {
+            for (int i = pair; i < total && ok; i += npairs) {
+                const Work w = work_at<W>(p, i);
+                const bool a_mn = high && w.kind == GRAM, b_mn = high ? w.kind == GRAM : w.kind == PRODUCT;
+                // fp16 operands, fp32 sums; a 16-deep step in 16 bytes; the leading offset of the descriptors
+                const uint32_t id = (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(w.n >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+                const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2, a_lead = (a_mn ? 8192u >> 4 : 1u) << 16, b_lead = (b_mn ? 8192u >> 4 : 1u) << 16;
+                const bool single = w.step >= p.single_from;
+                for (int left = w.kb1 - w.kb0; left > 0 && ok;) {
                     const uint32_t b = use & 1, bph = (use >> 1) & 1, d = tmem_base + b * 256;
                     ++use;
                     ok = __all_sync(0xffffffffu, wait_cluster(tempty0 + 8 * b, bph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
@@ -367,18 +465,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_gem
                     for (; left > end; --left) {
                         ok = __all_sync(0xffffffffu, mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
                         if (!ok) break;
-                        const uint32_t ad = a_lo + s * (C::STAGE >> 4), bd = b_lo + s * (C::STAGE >> 4);
-                        if (p.terms > 1) {
+                        const uint32_t ad = (a_at + s * (C::STAGE >> 4)) | a_lead, bd = (b_at + s * (C::STAGE >> 4)) | b_lead;
+                        if (!single) {
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
-                                mma_pair_elect(d, ad + A_STEP * kk, a_hi, bd + (C::B_BYTES >> 4) + B_STEP * kk, b_hi, id, acc);
+                                mma_pair_elect(d, ad + a_step * kk, desc_hi, bd + (C::B_BYTES >> 4) + b_step * kk, desc_hi, id, acc);
                                 acc = 1;
-                                mma_pair_elect(d, ad + (A_BYTES >> 4) + A_STEP * kk, a_hi, bd + B_STEP * kk, b_hi, id, acc);
+                                mma_pair_elect(d, ad + (A_BYTES >> 4) + a_step * kk, desc_hi, bd + b_step * kk, desc_hi, id, acc);
                             }
                         }
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            mma_pair_elect(d, ad + A_STEP * kk, a_hi, bd + B_STEP * kk, b_hi, id, acc);
+                            mma_pair_elect(d, ad + a_step * kk, desc_hi, bd + b_step * kk, desc_hi, id, acc);
                             acc = 1;
                         }
                         issued = true;
@@ -406,19 +504,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_gem
     }
 }
 
-template <int W, bool A_MN, bool B_MN>
-cudaError_t launch_gemm(const OrthGemmParams &p, int num_sms, cudaStream_t s) {
+template <int W>
+cudaError_t prepare_kernel() {
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(orth_gemm_kernel<W, A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<W>());
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) attr_set[dev] = true;
-    }
-    const int64_t tiles = (int64_t)p.batch * p.tiles;
-    const int pairs = num_sms / 2 > 1 ? num_sms / 2 : 1;
-    return launch_early(orth_gemm_kernel<W, A_MN, B_MN>, 2 * (int)(tiles < pairs ? tiles : pairs), THREADS, smem_bytes<W>(), s, p);
+    if (dev >= 0 && dev < 64 && attr_set[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(orth_kernel<W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<W>());
+    if (e == cudaSuccess && dev >= 0 && dev < 64) attr_set[dev] = true;
+    return e;
+}
+template <int W>
+cudaError_t launch_steps(const OrthParams &p, int pairs, cudaStream_t s) {
+    const cudaError_t e = prepare_kernel<W>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem_bytes<W>();
+    cfg.stream = s;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeCooperative;  // the pairs wait for one another: all of them are resident
+    attr.val.cooperative = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, orth_kernel<W>, p);
 }
 
 // ---- what comes before the products --------------------------------------------
@@ -443,6 +553,7 @@ __global__ void __launch_bounds__(NT) orth_norm_kernel(const OrthPrepParams p) {
     pdl_next();
     pdl_wait();
     const int e = blockIdx.y;
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.done[e] = 0;
     const int per_row = (p.cols + V - 1) / V;  // (V divides cols where V > 1)
     const int64_t items = (int64_t)p.rows * per_row;
     double sum = 0.0;
@@ -578,9 +689,27 @@ cudaError_t launch_orth_prep(const OrthPrepParams &p, bool by_four, cudaStream_t
     return by_four ? cudaLaunchKernelEx(&cfg, orth_split_kernel<4>, p) : cudaLaunchKernelEx(&cfg, orth_split_kernel<1>, p);
 }
 
-cudaError_t launch_orth_gemm(const OrthGemmParams &p, bool a_mn, bool b_mn, bool wide, int num_sms, cudaStream_t s) {
-    if (wide) return a_mn ? launch_gemm<256, true, true>(p, num_sms, s) : b_mn ? launch_gemm<256, false, true>(p, num_sms, s) : launch_gemm<256, false, false>(p, num_sms, s);
-    return a_mn ? launch_gemm<128, true, true>(p, num_sms, s) : b_mn ? launch_gemm<128, false, true>(p, num_sms, s) : launch_gemm<128, false, false>(p, num_sms, s);
+// Pairs of SMs that can be resident at once.
+int orth_pairs(int num_sms) {
+    if (prepare_kernel<256>() != cudaSuccess || prepare_kernel<128>() != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(num_sms & ~1));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem_bytes<256>() > smem_bytes<128>() ? smem_bytes<256>() : smem_bytes<128>();
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (prepare_kernel<256>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, orth_kernel<256>, &cfg) != cudaSuccess) return 0;
+    return n < num_sms / 2 ? n : num_sms / 2;
+}
+
+cudaError_t launch_orth_steps(const OrthParams &p, bool wide, int pairs, cudaStream_t s) {
+    return wide ? launch_steps<256>(p, pairs, s) : launch_steps<128>(p, pairs, s);
 }
 
 }  // namespace cbd

@@ -176,27 +176,38 @@ struct OrthPrepParams {
     float *momentum;         // dense, or NULL
     __half *hi, *lo;         // [batch][rows][pitch]
     double *partial;         // [batch][parts]
+    int32_t *done;           // [batch], cleared
     int64_t ls, ld;
     int32_t batch, rows, cols, pitch, parts, bf16, nesterov;
     float beta;
 };
 cudaError_t launch_orth_prep(const OrthPrepParams &p, bool by_four, cudaStream_t s);
-// D [M][N] = sum over K of A B, operands in planes hi and lo, tile 256 x 256 (wide) or 128
-struct OrthGemmParams {
-    CUtensorMap a[2], b[2];
-    CUtensorMap out[2], out_t[2];  // boxes of 32 rows x 64 columns, transposed 64 x 32
-    const __half *old[2];          // square: A
-    void *result;                  // final: the result, or the step on the weights
+// All the products.  Maps: [2] planes hi, lo; x has two buffers.
+constexpr int kOrthMostSteps = 64;
+constexpr float kOrthUp = 1024.f, kOrthUpPoly = 256.f;  // what the planes' values are multiplied by
+struct OrthParams {
+    CUtensorMap x_gram_a[2][2], x_gram_b[2][2], x_prod[2][2], x_store[2][2];
+    CUtensorMap gram_a[2], gram_b[2], gram_store[2], gram_store_t[2], poly_prod[2], poly_store[2], poly_store_t[2];
+    const __half *gram[2];
+    void *result;                  // the result, or the step on the weights
     float *weight;
     __nv_bfloat16 *copy;
+    float4 *parts;                 // sums of tiles whose contraction is split
+    int32_t *arrived;              // their counters, 0 between tiles
+    int32_t *done;                 // [batch] warps that have finished a tile
     int32_t *status;
     int64_t wait_budget;
     int64_t ldo, lse;              // of the caller's tensors: rows, matrices
-    int32_t M, N, K, batch, tiles; // tiles of a matrix
-    int32_t symmetric, terms, final, bf16, ld_old;
-    float mul, mul_old, diagonal, rate, keep;
+    int32_t rows, cols, batch, steps, items;
+    int32_t tiles_sym, tiles_all;  // tiles of a matrix: gram and square, product
+    int32_t splits[3];
+    int32_t single_from;           // first step with one product of hi planes instead of three
+    int32_t bf16, pitch_gram;
+    float rate, keep;
+    float coef[3 * kOrthMostSteps];
 };
-// a_mn, b_mn: the operand's contraction runs along its rows (a_mn only with b_mn)
-cudaError_t launch_orth_gemm(const OrthGemmParams &p, bool a_mn, bool b_mn, bool wide, int num_sms, cudaStream_t s);
+int orth_pairs(int num_sms);
+// wide: tiles of 256 x 256, else 256 x 128
+cudaError_t launch_orth_steps(const OrthParams &p, bool wide, int pairs, cudaStream_t s);
 
 }  // namespace cbd

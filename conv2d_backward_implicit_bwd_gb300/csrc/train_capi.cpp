@@ -201,10 +201,11 @@ struct conv_bwd_orth_plan_s {
         Plane plane[2];
     };
     conv_bwd_orth_desc d;
-    std::vector<float> coef;  // a, b, c of every step
-    int32_t pitch = 0, pitch_gram = 0, most_parts = 0;
+    int32_t pitch = 0, most_parts = 0, pairs = 0;
+    bool wide = false;
     double *partial = nullptr;
     Matrix x[2], gram, poly;
+    OrthParams run;  // all but the caller's tensors
     DevicePart dev;
 };
 
@@ -765,23 +766,57 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         if (!(std::fabs(d->coefficients[i]) <= 32.f)) return CONV_BWD_ERR_INVALID_ARG;
     return create_plan(out, [&](conv_bwd_orth_plan_s &p) {
         p.d = *d;
-        p.coef.assign(d->coefficients, d->coefficients + 3 * d->steps);
         p.d.coefficients = nullptr;
         int sms = 0, dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
+        if (cudaGetDevice(&dev) == cudaSuccess &&
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             sms = 0;
         cudaGetLastError();
-        const int64_t g = std::min(d->rows, d->cols);
+        const int64_t g = std::min(d->rows, d->cols), h = std::max(d->rows, d->cols);
+        const bool high = d->rows > d->cols;
         p.pitch = (int32_t)((d->cols + 7) / 8 * 8);
-        p.pitch_gram = (int32_t)((g + 7) / 8 * 8);
         p.most_parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>((d->rows * d->cols + 4095) / 4096, 8LL * sms / d->batch));
+        OrthParams &q = p.run;
+        std::memset(&q, 0, sizeof(q));
+        q.pitch_gram = (int32_t)((g + 7) / 8 * 8);
+        q.rows = (int32_t)d->rows; q.cols = (int32_t)d->cols; q.batch = (int32_t)d->batch; q.steps = d->steps;
+        std::copy(d->coefficients, d->coefficients + 3 * d->steps, q.coef);
+        p.pairs = sms > 1 ? orth_pairs(sms) : 0;
+        if (sms > 1 && p.pairs < 1) return CONV_BWD_ERR_CUDA;
+        const int64_t pairs = std::max(1, p.pairs);
+        auto tiles_all = [&](int64_t w) { return (d->rows + 255) / 256 * ((d->cols + w - 1) / w); };
+        auto tiles_sym = [&](int64_t w) {
+            const int64_t mt = (g + 255) / 256;
+            return mt * ((g + w - 1) / w) - mt * (mt - 1) / 2 * (256 / w);
+        };
+        p.wide = tiles_sym(256) * d->batch >= pairs;
+        const int64_t w = p.wide ? 256 : 128;
+        q.tiles_sym = (int32_t)tiles_sym(w);
+        q.tiles_all = (int32_t)tiles_all(w);
+        // pieces of a contraction: as many as the pairs that would else be idle, of four k-blocks at least
+        auto splits = [&](int64_t tiles, int64_t depth) { return (int32_t)std::max<int64_t>(1, std::min(pairs / (tiles * d->batch), (depth + 63) / 64 / 4)); };
+        q.splits[0] = splits(q.tiles_sym, h);
+        q.splits[1] = splits(q.tiles_sym, g);
+        q.splits[2] = splits(q.tiles_all, g);
+        const int64_t items = d->batch * (q.tiles_sym * (int64_t)(q.splits[0] + q.splits[1]) + (int64_t)q.tiles_all * q.splits[2]) * d->steps;
+        if (items > kMostRows || 2 * 8 * (2 * (int64_t)q.tiles_sym + q.tiles_all) * d->steps > kMostRows) return CONV_BWD_ERR_UNSUPPORTED;
+        q.items = (int32_t)items;
+        q.single_from = d->steps;
         auto lines = [](size_t n) { return (n + 255) / 256 * 256; };
-        const size_t partial = lines((size_t)d->batch * p.most_parts * 8), whole = lines((size_t)d->batch * d->rows * p.pitch * 2),
-                     square = lines((size_t)d->batch * g * p.pitch_gram * 2);
-        const conv_bwd_status st = p.dev.init(256 + partial + 4 * whole + 4 * square);
+        const bool split = q.splits[0] > 1 || q.splits[1] > 1 || q.splits[2] > 1;
+        const size_t arrived = split ? lines((size_t)pairs * 16 * 4) : 0, parts = split ? (size_t)pairs * 256 * w * 4 : 0;
+        const size_t done = lines((size_t)d->batch * 4), partial = lines((size_t)d->batch * p.most_parts * 8),
+                     whole = lines((size_t)d->batch * d->rows * p.pitch * 2), square = lines((size_t)d->batch * g * q.pitch_gram * 2);
+        p.dev.counters = 256 + arrived;
+        const conv_bwd_status st = p.dev.init(256 + arrived + parts + done + partial + 4 * whole + 4 * square);
         if (st != CONV_BWD_OK || !p.dev.has_device) return st;
         char *at = static_cast<char *>(p.dev.mem) + 256;
+        q.arrived = reinterpret_cast<int32_t *>(at);
+        at += arrived;
+        q.parts = reinterpret_cast<float4 *>(at);
+        at += parts;
+        q.done = reinterpret_cast<int32_t *>(at);
+        at += done;
         p.partial = reinterpret_cast<double *>(at);
         at += partial;
         bool ok = true;
@@ -797,9 +832,30 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         };
         place(p.x[0], d->rows, d->cols, p.pitch, whole);
         place(p.x[1], d->rows, d->cols, p.pitch, whole);
-        place(p.gram, g, g, p.pitch_gram, square);
-        place(p.poly, g, g, p.pitch_gram, square);
-        return ok ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
+        place(p.gram, g, g, q.pitch_gram, square);
+        place(p.poly, g, g, q.pitch_gram, square);
+        if (!ok) return CONV_BWD_ERR_CUDA;
+        // operands that run along the contraction come in boxes of their rows, else in boxes of 64 x 64
+        for (int i = 0; i < 2; ++i) {
+            for (int k = 0; k < 2; ++k) {
+                const auto &x = p.x[k].plane[i];
+                q.x_gram_a[k][i] = high ? x.rows64 : x.rows128;
+                q.x_gram_b[k][i] = high || !p.wide ? x.rows64 : x.rows128;
+                q.x_prod[k][i] = high ? x.rows128 : x.rows64;
+                q.x_store[k][i] = x.store;
+            }
+            q.gram[i] = p.gram.at[i];
+            q.gram_a[i] = p.gram.plane[i].rows128;
+            q.gram_b[i] = p.wide ? p.gram.plane[i].rows128 : p.gram.plane[i].rows64;
+            q.gram_store[i] = p.gram.plane[i].store;
+            q.gram_store_t[i] = p.gram.plane[i].store_t;
+            q.poly_prod[i] = high && !p.wide ? p.poly.plane[i].rows64 : p.poly.plane[i].rows128;
+            q.poly_store[i] = p.poly.plane[i].store;
+            q.poly_store_t[i] = p.poly.plane[i].store_t;
+        }
+        q.status = p.dev.status();
+        q.wait_budget = (int64_t)p.dev.clock_khz * 2000;
+        return CONV_BWD_OK;
     });
 }
 conv_bwd_status conv_bwd_orth_destroy(conv_bwd_orth_plan p) {
@@ -817,80 +873,26 @@ struct OrthOut {
 };
 static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const OrthOut &o, cudaStream_t s) {
     const conv_bwd_orth_desc &d = p->d;
-    const bool high = d.rows > d.cols;
-    const int32_t g = (int32_t)std::min(d.rows, d.cols), sms = p->dev.num_sms;
     pp.hi = p->x[0].at[0];
     pp.lo = p->x[0].at[1];
     pp.partial = p->partial;
+    pp.done = p->run.done;
     pp.batch = (int32_t)d.batch; pp.rows = (int32_t)d.rows; pp.cols = (int32_t)d.cols; pp.pitch = p->pitch;
     pp.parts = p->most_parts;
     pp.bf16 = d.dtype == CONV_BWD_BF16;
     const bool by_four = d.cols % 4 == 0 && pp.ld % 4 == 0 && pp.ls % 4 == 0 && (uintptr_t)pp.grad % (4 * esize(d.dtype)) == 0 &&
                          (uintptr_t)pp.momentum % 16 == 0;
     if (launch_orth_prep(pp, by_four, s) != cudaSuccess) return CONV_BWD_ERR_CUDA;
-    const float up = 1024.f, up_poly = 256.f;  // what the planes' values are multiplied by
-    auto product = [&](const conv_bwd_orth_plan_s::Matrix &a, bool a_mn, const conv_bwd_orth_plan_s::Matrix &b, bool b_mn,
-                       const conv_bwd_orth_plan_s::Matrix *to, int64_t M, int64_t N, int64_t K, bool symmetric, OrthGemmParams &q) {
-        const int64_t mt = (M + 255) / 256;
-        auto tiles = [&](int64_t w) {
-            const int64_t nt = (N + w - 1) / w;
-            int64_t n = mt * nt;
-            if (symmetric)
-                for (int64_t i = 0; i < mt; ++i) n -= i * (256 / w);
-            return n;
-        };
-        const bool wide = tiles(256) * d.batch >= sms / 2;
-        q.tiles = (int32_t)tiles(wide ? 256 : 128);
-        for (int i = 0; i < 2; ++i) {
-            q.a[i] = a_mn ? a.plane[i].rows64 : a.plane[i].rows128;
-            q.b[i] = b_mn || !wide ? b.plane[i].rows64 : b.plane[i].rows128;
-            if (to) {
-                q.out[i] = to->plane[i].store;
-                q.out_t[i] = to->plane[i].store_t;
-            }
-        }
-        q.M = (int32_t)M; q.N = (int32_t)N; q.K = (int32_t)K;
-        q.batch = (int32_t)d.batch;
-        q.symmetric = symmetric;
-        q.terms = 3;
-        q.status = p->dev.status();
-        q.wait_budget = (int64_t)p->dev.clock_khz * 2000;
-        return launch_orth_gemm(q, a_mn, b_mn, wide, sms, s) == cudaSuccess;
-    };
-    for (int32_t i = 0; i < d.steps; ++i) {
-        const float a = p->coef[3 * i], b = p->coef[3 * i + 1], c = p->coef[3 * i + 2];
-        const auto &x = p->x[i & 1];
-        OrthGemmParams q;
-        std::memset(&q, 0, sizeof(q));
-        q.mul = 1.f / up;
-        if (!product(x, high, x, high, &p->gram, g, g, high ? d.rows : d.cols, true, q)) return CONV_BWD_ERR_CUDA;
-        std::memset(&q, 0, sizeof(q));
-        q.mul = c * up_poly / (up * up);
-        q.mul_old = b * up_poly / up;
-        q.diagonal = a * up_poly;
-        q.old[0] = p->gram.at[0];
-        q.old[1] = p->gram.at[1];
-        q.ld_old = p->pitch_gram;
-        if (!product(p->gram, false, p->gram, false, &p->poly, g, g, g, true, q)) return CONV_BWD_ERR_CUDA;
-        std::memset(&q, 0, sizeof(q));
-        const bool last = i + 1 == d.steps;
-        q.mul = last ? 1.f / (up_poly * up) : 1.f / up_poly;
-        if (last) {
-            q.final = 1;
-            q.result = o.result;
-            q.bf16 = pp.bf16;
-            q.weight = o.weight;
-            q.copy = o.copy;
-            q.ldo = o.ldo;
-            q.lse = o.lse;
-            q.rate = o.rate;
-            q.keep = o.keep;
-        }
-        const bool ok = high ? product(x, false, p->poly, false, last ? nullptr : &p->x[(i + 1) & 1], d.rows, d.cols, g, false, q)
-                             : product(p->poly, false, x, true, last ? nullptr : &p->x[(i + 1) & 1], d.rows, d.cols, g, false, q);
-        if (!ok) return CONV_BWD_ERR_CUDA;
-    }
-    return CONV_BWD_OK;
+    OrthParams q = p->run;
+    q.result = o.result;
+    q.bf16 = pp.bf16;
+    q.weight = o.weight;
+    q.copy = o.copy;
+    q.ldo = o.ldo;
+    q.lse = o.lse;
+    q.rate = o.rate;
+    q.keep = o.keep;
+    return launch_orth_steps(q, p->wide, p->pairs, s) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
 }
 
 // Checks a stack of matrices with row stride ld and matrix stride ls (0: dense) and fills the strides in.
