@@ -23,7 +23,7 @@ LIB = os.path.join(LIBDIR, "libconv_bwd_data.so")
 SOURCES = ["capi.cpp", "simt.cu", "tc_sm103.cu", "tc2_sm103.cu", "tc_fwd_sm103.cu", "tf32_sm103.cu", "grouped.cu",
            "tc_grouped_sm103.cu", "tc_band_sm103.cu", "noalloc.cu",
            "train_capi.cpp", "experts_f32.cu", "experts_b16.cu", "experts_few_f32.cu", "experts_pair_sm103.cu", "experts_stream_sm103.cu",
-           "grad_clip.cu", "policy_loss.cu", "token_logp.cu", "orth_sm103.cu"]
+           "grad_clip.cu", "policy_loss.cu", "token_logp.cu", "orth_sm103.cu", "orth_small_sm103.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -20,8 +20,13 @@
 // So the matrices between the products are pairs of fp16, hi + lo (22 bits), times 2^10 (the polynomial B 2^8) so that lo
 // stays a normal number; a product is hi hi + hi lo + lo hi, on the tensor cores in fp32.  (fp16 rather than bf16: 22 bits
 // instead of 16 at the same rate.  Singular values stay below 1.3 with the usual coefficients; B may reach 255, which the
-// host's bound of 32 on each coefficient keeps below singular values of 1.5.)  The accumulator truncates, about 2^-26 of the sum with each instruction; a new one is begun every SEGMENT k-blocks and
-// added in fp32 registers, under the other accumulator's MMAs.
+// host's bound of 32 on each coefficient keeps below singular values of 1.5.)  The
+// accumulator truncates, about 2^-26 of the sum with each instruction; a new one is begun every `segment` k-blocks and
+// added in fp32 registers, under the other accumulator's MMAs.  Every two k-blocks the result's error is that of the same
+// products in fp32 (1024 x 2048, 8 directions over 1 % noise: 4.5e-5; every eight 1.4e-4, never 2.0e-4), but the sums take
+// power, and power is what bounds large batches: 32 of 1024 x 2048 3163, 2889 and 2825 us.  So fp32 results take two, bf16
+// results and steps on weights (of which X is a hundredth) eight.  A bf16 result's last step takes the hi halves alone: what
+// that rounds no later step multiplies (5e-4 beside the 1.7e-3 of bf16; in the last two steps 2.4e-3).
 //
 // The tile is 256 x W on a pair of SMs (tcgen05 cta_group::2), two accumulators in TMEM; a k-block of 64 brings both
 // halves of both operands, 64 KB a CTA for W = 256, and feeds twelve 16-deep MMAs, so loads are a third of what a plain
@@ -48,7 +53,6 @@ namespace {
 constexpr int EPI = 8, LOAD_A = 8, LOAD_B = 9, MMA = 10, THREADS = 512;
 constexpr int A_BYTES = 128 * 64 * 2;  // of one plane of a stage
 constexpr int OUT_BYTES = EPI * 4096;
-constexpr int SEGMENT = 2;  // k-blocks (of 64) of one accumulator
 constexpr int MOST_STAGES = 4;
 
 template <int W>
@@ -330,7 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
             float sum[COLS];
 #pragma unroll
             for (int q = 0; q < COLS; ++q) sum[q] = 0.f;
-            for (int left = w.kb1 - w.kb0; left > 0; left -= SEGMENT, ++use) {
+            for (int left = w.kb1 - w.kb0; left > 0; left -= p.segment, ++use) {
                 const uint32_t b = use & 1;
                 if (ok) ok = mbar_wait_bounded(tfull0 + 8 * b, (use >> 1) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
                 ok = __all_sync(0xffffffffu, ok);
@@ -461,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                     if (!ok) break;
                     tc_fence_after();
                     uint32_t acc = 0;
-                    const int end = left > SEGMENT ? left - SEGMENT : 0;
+                    const int end = left > p.segment ? left - p.segment : 0;
                     for (; left > end; --left) {
                         ok = __all_sync(0xffffffffu, mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
                         if (!ok) break;
@@ -616,22 +620,7 @@ __global__ void __launch_bounds__(NT) orth_split_kernel(const OrthPrepParams p) 
         for (int i = threadIdx.x; i < p.parts; i += 32) s += p.partial[(int64_t)e * p.parts + i];
 #pragma unroll
         for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        if (threadIdx.x == 0) {
-            const double n = sqrt(s);
-            if (!isfinite(n)) {
-                factor[0] = factor[1] = factor[2] = __uint_as_float(0x7fffffffu);
-            } else if (n == 0.0) {
-                factor[0] = factor[1] = factor[2] = 0.f;
-            } else {
-                // 2^10 / n in three factors that neither overflow nor underflow: n is anywhere from 2^-149 on
-                int x;
-                const double f = frexp(n, &x);
-                const int k = 10 - x;
-                factor[0] = ldexpf(1.f, k / 2);
-                factor[1] = ldexpf(1.f, k - k / 2);
-                factor[2] = (float)(1.0 / f);
-            }
-        }
+        if (threadIdx.x == 0) orth_factors(s, factor);
     }
     __syncthreads();
     const float f0 = factor[0], f1 = factor[1], f2 = factor[2];

@@ -202,11 +202,44 @@ struct OrthParams {
     int32_t tiles_sym, tiles_all;  // tiles of a matrix: gram and square, product
     int32_t splits[3];
     int32_t single_from;           // first step with one product of hi planes instead of three
+    int32_t segment;               // k-blocks of one accumulator
     int32_t bf16, pitch_gram;
     float rate, keep;
     float coef[3 * kOrthMostSteps];
 };
 int orth_pairs(int num_sms);
+// Matrices whose smaller side is at most kOrthSmall, their larger side in `cluster` slices of `slice` columns.
+constexpr int kOrthSmall = 128, kOrthSlice = 256;
+struct OrthSmallParams {
+    const void *grad;
+    float *momentum;
+    void *result;
+    float *weight;
+    __nv_bfloat16 *copy;
+    int32_t *status;
+    int64_t wait_budget;
+    int64_t ls, ld, lse, ldo;      // of the input, of the result
+    int32_t rows, cols, batch, steps, cluster, slice;
+    int32_t in_bf16, out_bf16, nesterov, single_from;
+    float beta, rate, keep;
+    float coef[3 * kOrthMostSteps];
+};
+cudaError_t launch_orth_small(const OrthSmallParams &p, cudaStream_t s);
+#ifdef __CUDACC__
+// 2^10 / sqrt(sum of squares) in three factors that neither overflow nor underflow (the norm is anywhere from 2^-149 on):
+// zeros for a matrix of zeros, NaN where the norm is not finite.
+__device__ __forceinline__ void orth_factors(double sum, float *factor) {
+    const double n = sqrt(sum);
+    factor[0] = factor[1] = factor[2] = n == 0.0 ? 0.f : __int_as_float(0x7fffffff);
+    if (n == 0.0 || !isfinite(n)) return;
+    int x;
+    const double f = frexp(n, &x);
+    const int k = 10 - x;
+    factor[0] = ldexpf(1.f, k / 2);
+    factor[1] = ldexpf(1.f, k - k / 2);
+    factor[2] = (float)(1.0 / f);
+}
+#endif
 // wide: tiles of 256 x 256, else 256 x 128
 cudaError_t launch_orth_steps(const OrthParams &p, bool wide, int pairs, cudaStream_t s);
 

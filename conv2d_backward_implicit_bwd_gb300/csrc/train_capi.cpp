@@ -201,8 +201,9 @@ struct conv_bwd_orth_plan_s {
         Plane plane[2];
     };
     conv_bwd_orth_desc d;
-    int32_t pitch = 0, most_parts = 0, pairs = 0;
+    int32_t pitch = 0, most_parts = 0, pairs = 0, cluster = 0;  // cluster: the kernel for small matrices
     bool wide = false;
+    std::vector<float> coef;
     double *partial = nullptr;
     Matrix x[2], gram, poly;
     OrthParams run;  // all but the caller's tensors
@@ -773,6 +774,11 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
             sms = 0;
         cudaGetLastError();
         const int64_t g = std::min(d->rows, d->cols), h = std::max(d->rows, d->cols);
+        if (g <= kOrthSmall && h <= 8 * kOrthSlice) {
+            for (p.cluster = 1; p.cluster * kOrthSlice < h;) p.cluster *= 2;
+            p.coef.assign(d->coefficients, d->coefficients + 3 * d->steps);
+            return p.dev.init(64);
+        }
         const bool high = d->rows > d->cols;
         p.pitch = (int32_t)((d->cols + 7) / 8 * 8);
         p.most_parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>((d->rows * d->cols + 4095) / 4096, 8LL * sms / d->batch));
@@ -801,7 +807,6 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         const int64_t items = d->batch * (q.tiles_sym * (int64_t)(q.splits[0] + q.splits[1]) + (int64_t)q.tiles_all * q.splits[2]) * d->steps;
         if (items > kMostRows || 2 * 8 * (2 * (int64_t)q.tiles_sym + q.tiles_all) * d->steps > kMostRows) return CONV_BWD_ERR_UNSUPPORTED;
         q.items = (int32_t)items;
-        q.single_from = d->steps;
         auto lines = [](size_t n) { return (n + 255) / 256 * 256; };
         const bool split = q.splits[0] > 1 || q.splits[1] > 1 || q.splits[2] > 1;
         const size_t arrived = split ? lines((size_t)pairs * 16 * 4) : 0, parts = split ? (size_t)pairs * 256 * w * 4 : 0;
@@ -873,6 +878,25 @@ struct OrthOut {
 };
 static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const OrthOut &o, cudaStream_t s) {
     const conv_bwd_orth_desc &d = p->d;
+    const bool fp32_result = o.result && d.dtype == CONV_BWD_F32;
+    const int32_t single_from = o.result && !fp32_result ? d.steps - 1 : d.steps;
+    if (p->cluster) {
+        OrthSmallParams q;
+        std::memset(&q, 0, sizeof(q));
+        q.grad = pp.grad; q.ls = pp.ls; q.ld = pp.ld;
+        q.momentum = pp.momentum; q.beta = pp.beta; q.nesterov = pp.nesterov;
+        q.result = o.result; q.weight = o.weight; q.copy = o.copy;
+        q.ldo = o.ldo; q.lse = o.lse; q.rate = o.rate; q.keep = o.keep;
+        q.status = p->dev.status();
+        q.wait_budget = (int64_t)p->dev.clock_khz * 2000;
+        q.rows = (int32_t)d.rows; q.cols = (int32_t)d.cols; q.batch = (int32_t)d.batch; q.steps = d.steps;
+        q.cluster = p->cluster;
+        q.slice = (int32_t)(((std::max(d.rows, d.cols) + p->cluster - 1) / p->cluster + 63) / 64 * 64);
+        q.in_bf16 = q.out_bf16 = d.dtype == CONV_BWD_BF16;
+        q.single_from = single_from;
+        std::copy(p->coef.begin(), p->coef.end(), q.coef);
+        return launch_orth_small(q, s) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
+    }
     pp.hi = p->x[0].at[0];
     pp.lo = p->x[0].at[1];
     pp.partial = p->partial;
@@ -884,6 +908,8 @@ static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const 
                          (uintptr_t)pp.momentum % 16 == 0;
     if (launch_orth_prep(pp, by_four, s) != cudaSuccess) return CONV_BWD_ERR_CUDA;
     OrthParams q = p->run;
+    q.segment = fp32_result ? 2 : 8;
+    q.single_from = single_from;
     q.result = o.result;
     q.bf16 = pp.bf16;
     q.weight = o.weight;
@@ -915,6 +941,7 @@ conv_bwd_status conv_bwd_orth_apply(conv_bwd_orth_plan p, const void *x, int64_t
     if (st == CONV_BWD_OK) st = orth_strides(p->d, ldo, lso, es, no);
     if (st != CONV_BWD_OK) return st;
     if (((uintptr_t)x | (uintptr_t)out) % es) return CONV_BWD_ERR_MISALIGNED;
+    if (overlap(x, nx, out, no) && !(x == out && ldx == ldo && lsx == lso)) return CONV_BWD_ERR_INVALID_ARG;
     if (!p->dev.has_device) return CONV_BWD_ERR_CUDA;
     if (!p->dev.current()) return CONV_BWD_ERR_INVALID_ARG;
     OrthPrepParams pp;

@@ -257,7 +257,8 @@ conv_bwd_status conv_bwd_logp_get_status(conv_bwd_logp_plan plan, void *stream, 
  * throughout, and the other matrices of the batch are not touched by it.  The norm
  * neither overflows nor underflows.  The products' operands are held to 22 bits and
  * summed in fp32: against exact arithmetic X is off by some 2^-16 of its norm
- * (a rounding of u's size grows by a a step beside a small singular value).  They are
+ * (a rounding of u's size grows by a a step beside a small singular value); for a
+ * bf16 result the last step's are held to 11 bits, a third of what bf16 rounds.  They are
  * fp16 pairs with a range: where X's singular values leave [0, 60] or a + b s^2 + c s^4 leaves
  * [-255, 255] between the steps, the result is not finite. */
 typedef struct {
@@ -275,9 +276,9 @@ typedef struct conv_bwd_orth_plan_s *conv_bwd_orth_plan;
 conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *desc, conv_bwd_orth_plan *out);
 conv_bwd_status conv_bwd_orth_destroy(conv_bwd_orth_plan plan);
 
-/* ld* are row strides, ls* matrix strides in elements (0: dense).  out may be x or
- * overlap it: it is written after x has been read.  Errors: INVALID_ARG (NULL, rows or matrices
- * that overlap one another), MISALIGNED (a pointer not aligned to its element),
+/* ld* are row strides, ls* matrix strides in elements (0: dense).  out may be x
+ * itself (with its strides).  Errors: INVALID_ARG (NULL, rows or matrices that overlap one
+ * another, out that overlaps x otherwise), MISALIGNED (a pointer not aligned to its element),
  * UNSUPPORTED (a stride > 2^31 or 2^40), CUDA. */
 conv_bwd_status conv_bwd_orth_apply(conv_bwd_orth_plan plan, const void *x, int64_t ldx, int64_t lsx, void *out,
                                     int64_t ldo, int64_t lso, void *stream);

@@ -75,6 +75,17 @@ def test_apply(T, dtype, shape, kind):
     print(shape, dtype, kind, check(got, *iterate(u, [COEF] * 5)))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 128, 256), (1, 128, 257), (3, 100, 260), (2, 17, 520), (1, 128, 1000), (2, 1, 1024), (3, 128, 2048), (2, 2048, 128), (2, 700, 33), (1, 1100, 128),
+                                   (1, 129, 256), (1, 128, 2049), (200, 128, 300), (300, 20, 16)])
+def test_either_side_of_the_small_kernel(T, dtype, shape):
+    """Smaller sides up to 128 and larger ones up to 2048, in slices of 256 columns."""
+    u = matrices(shape, dtype=DT[dtype])
+    plan = T.Orthogonal(*shape, dtype)
+    check(plan.apply(u), *iterate(u, [COEF] * 5))
+    assert plan.status() == (0, 0)
+
+
 def test_singular_values(T):
     """They come near 1 and the vectors stay: the point of it."""
     u = matrices((1, 96, 160), "flat")
