@@ -11,14 +11,15 @@
 //
 // Alternatives: keys of 64 bits, the value's order above the inverted index, so the
 // largest of any set is unique (ties go to the lowest index) and the result does not
-// depend on the order of work.  A warp keeps its 32 best sorted over its lanes.  A
-// batch whose maximum is below the bound costs a comparison; else its elements at or
-// above the bound go to a queue, and 32 of them at a time are sorted (15 exchanges)
-// and merged (6).  The bound is the larger of the warp's own last place and the
-// smallest of the block's posts: each warp posts its ceil(top / 8)-th best, so
-// `top` elements of the row lie at or above that.  An empty list takes its first bound
-// from the batch's lane maxima (without it every element of the first batch is a
-// candidate).
+// depend on the order of work.  Their search costs the pass nothing: each thread has
+// its elements' maximum anyway.  `top` elements lie at or above the top-th largest of
+// 32 maxima, each of eight threads' elements; only threads whose maximum is there have
+// candidates (twenty to forty for 20 alternatives), mostly in the one chunk that it came
+// from, and that chunk's vectors are read again, from L2, by the warp that ends the row,
+// while the others are at the next one.  It sorts the elements that reach the bound 32 at
+// a time.  (8192 rows of 32768 with 20 alternatives,
+// candidates taken out during the pass against a rising bound 551 us, taken out by the
+// workers after it 188.)
 //
 // Rows above 16 KB stream through a ring of 16 KB buffers that one thread fills with
 // bulk copies, as in the policy loss; where rows are few each is cut into parts, and
@@ -39,7 +40,6 @@ namespace cbd {
 namespace {
 
 constexpr int NT = 256;
-constexpr int UNR = 4;  // 16-byte loads of a thread in flight
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -51,41 +51,140 @@ __device__ __forceinline__ Sums rebased(const Sums &r, float m, float c) {
     const float up = Exps(m, c).shift(r.m, m), f = ex2(up);
     return {m, r.s * f, fmaf(r.s, up, r.t) * f};
 }
+// the largest element of some vectors (what is no number counts last)
+template <typename T, int N>
+__device__ __forceinline__ float largest(const uint4 (&u)[N]) {
+    if constexpr (sizeof(T) == 4) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(u[i].x), __uint_as_float(u[i].y)), fmaxf(__uint_as_float(u[i].z), __uint_as_float(u[i].w))));
+        return m;
+    } else {  // two at a time
+        auto two = [](const uint32_t &w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+        __nv_bfloat162 m = two(u[0].x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i) m = __hmax2(m, two(u[i].x));
+            m = __hmax2(__hmax2(m, two(u[i].y)), __hmax2(two(u[i].z), two(u[i].w)));
+        }
+        const float2 f = __bfloat1622float2(m);
+        return fmaxf(f.x, f.y);
+    }
+}
+
+__device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t b = __float_as_uint(v + 0.f);  // (-0 ties with 0)
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint64_t key) {
+    const uint32_t b = (uint32_t)(key >> 32);
+    return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
+}
+__device__ __forceinline__ uint32_t ordered_number(float v) { return ordered(v == v ? v : -INFINITY); }
+__device__ __forceinline__ float warp_max(float m) { return value_of((uint64_t)__reduce_max_sync(kAll, ordered_number(m)) << 32); }
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 both(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+// A warp's elements: every lane has its own sums over the warp's reference, so that the reference is seldom moved (one for
+// each lane was moved in most batches by some lane, for 1.5 instructions an element).  2^-inf * -inf is not 0: a batch whose
+// t is no number is summed again with d held at -200, and so are the later ones (logits of -inf come many in a row or not at
+// all).  take() is called by the whole warp.
 struct Run {
     Sums r;
     float lim, room;
+    bool held;
     Exps e;
-    __device__ __forceinline__ explicit Run(float c) : r{-INFINITY, 0.f, 0.f}, lim(-INFINITY), room(1.f / c), e(-INFINITY, c) {}
-    template <bool NEAR, int N>
-    __device__ __forceinline__ void add(const float (&v)[N]) {
+    __device__ __forceinline__ explicit Run(float c) : r{-INFINITY, 0.f, 0.f}, lim(-INFINITY), room(1.f / c), held(false), e(-INFINITY, c) {}
+    template <int N>
+    __device__ __forceinline__ float2 plain(const float (&v)[N]) const {
+        const uint64_t c2 = pair(e.c, e.c), off2 = pair(-e.off, -e.off);
+        uint64_t s2 = 0, t2 = 0;
+#pragma unroll
+        for (int i = 0; i + 1 < N; i += 2) {
+            const uint64_t d2 = fma2(pair(v[i], v[i + 1]), c2, off2);
+            const float2 d = both(d2);
+            const uint64_t p2 = pair(ex2(d.x), ex2(d.y));
+            s2 = add2(s2, p2);
+            t2 = fma2(p2, d2, t2);
+        }
+        const float2 s = both(s2), t = both(t2);
+        return make_float2(s.x + s.y, t.x + t.y);
+    }
+    template <int N>
+    __device__ __forceinline__ float2 careful(const float (&v)[N]) const {
         float s = 0.f, t = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const float d = NEAR ? fmaf(v[i], e.c, -e.off) : (v[i] - e.base) * e.c, p = ex2(d);
+            const float d = e.near ? fmaf(v[i], e.c, -e.off) : (v[i] - e.base) * e.c, p = ex2(d);
             s += p;
-            t = fmaf(p, fmaxf(d, -200.f), t);  // (2^-inf * -inf is not 0)
+            t = fmaf(p, fmaxf(d, -200.f), t);
         }
-        r.s += s;
-        r.t += t;
+        return make_float2(s, t);
     }
-    // returns the elements' maximum
+    // a value beside z whose term is 0 and that is not above it
+    __device__ __forceinline__ float nothing(float z) const { return fabsf(z * e.c) < 256.f ? z - 300.f * room : -INFINITY; }
+    // elements and their maximum
     template <int N>
-    __device__ __forceinline__ float take(const float (&v)[N]) {
-        float m = v[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
-        if (m > lim) {
+    __device__ __forceinline__ void take(const float (&v)[N], float m) {
+        if (__any_sync(kAll, m > lim)) {
+            m = warp_max(m);
             r = rebased(r, m, e.c);
             e = Exps(m, e.c);
             lim = m + room;
         }
-        if (e.near)
-            add<true>(v);
-        else
-            add<false>(v);
+        float2 x = make_float2(0.f, __int_as_float(0x7fffffff));
+        if (N % 2 == 0 && e.near && !held) x = plain(v);
+        if (__any_sync(kAll, !(x.y == x.y))) {
+            x = careful(v);
+            held = true;
+        }
+        r.s += x.x;
+        r.t += x.y;
+    }
+    template <typename T, int N>
+    __device__ __forceinline__ float take(const uint4 (&u)[N], bool there = true) {
+        constexpr int VN = Vec<T>::N;
+        float v[N * VN];
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            float w[VN];
+            Vec<T>::unpack(u[q], w);
+#pragma unroll
+            for (int k = 0; k < VN; ++k) v[q * VN + k] = there ? w[k] : nothing(w[k]);
+        }
+        const float m = there ? largest<T>(u) : -INFINITY;
+        take(v, m);
         return m;
     }
 };
+// The lanes' sums over their common reference, in a fixed order; every lane gets them.
+__device__ __forceinline__ Sums total(Sums r) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+        r.s += __shfl_xor_sync(kAll, r.s, d);
+        r.t += __shfl_xor_sync(kAll, r.t, d);
+    }
+    return r;
+}
 // The sums of N neighbouring lanes over one reference, in a fixed order; every lane gets it.
 template <int N>
 __device__ __forceinline__ Sums join(Sums r, float c) {
@@ -109,14 +208,6 @@ __device__ __forceinline__ float entropy(const Sums &r) {
 }
 
 // ---- the largest elements ------------------------------------------------------
-__device__ __forceinline__ uint32_t ordered(float v) {
-    const uint32_t b = __float_as_uint(v + 0.f);  // (-0 ties with 0)
-    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float value_of(uint64_t key) {
-    const uint32_t b = (uint32_t)(key >> 32);
-    return __uint_as_float(b & 0x80000000u ? b ^ 0x80000000u : ~b);
-}
 __device__ __forceinline__ uint64_t key_of(float v, uint32_t index) { return (uint64_t)ordered(v) << 32 | (kAll - index); }
 template <typename K>
 __device__ __forceinline__ K exchange(K x, int d, bool keep_larger) {
@@ -140,14 +231,14 @@ __device__ __forceinline__ uint64_t merged(uint64_t a, uint64_t b, int lane) {
     return a;
 }
 constexpr int kQueue = 64;
-// A warp's list: lane i has the i-th best, 0 where there is none yet.
+// A warp's best: lane i has the i-th, 0 where there is none; what came last waits in the queue.
 struct List {
     uint64_t key, last;  // last: the top-th
     float bound;         // of values that may still enter
     int count;           // queued
     uint64_t *queue;     // [kQueue], the warp's own
     int top, lane;
-    __device__ __forceinline__ List(uint64_t *q, int top_, int lane_) : key(0), last(0), bound(-INFINITY), count(0), queue(q), top(top_), lane(lane_) {}
+    __device__ __forceinline__ List(uint64_t *q, int top_, float bound_, int lane_) : key(0), last(0), bound(bound_), count(0), queue(q), top(top_), lane(lane_) {}
     __device__ __forceinline__ void flush() {
         __syncwarp();
         const int first = count > 32 ? count - 32 : 0;
@@ -155,28 +246,44 @@ struct List {
         __syncwarp();
         count = first;
         key = merged(key, sorted_falling(mine, lane), lane);
-        last = __shfl_sync(kAll, key, top - 1);
-        if (last) bound = fmaxf(bound, value_of(last));
+        const uint64_t place = __shfl_sync(kAll, key, top - 1);
+        if (place > last) {
+            last = place;
+            bound = fmaxf(bound, value_of(last));
+        }
     }
     // (by the whole warp)
-    __device__ __forceinline__ void offer(bool there, float v, int index) {
-        const uint64_t k = key_of(v, (uint32_t)index);
-        const bool in = there && v >= bound && k > last;
+    __device__ __forceinline__ void offer(bool there, float v, int index) { offer(there && v >= bound ? key_of(v, (uint32_t)index) : 0); }
+    __device__ __forceinline__ void offer(uint64_t k) {
+        const bool in = k > last;
         const uint32_t who = __ballot_sync(kAll, in);
         if (who == 0) return;
         if (in) queue[count + __popc(who & ((1u << lane) - 1))] = k;
         count += __popc(who);
         if (count >= 32) flush();
     }
+    // a vector's elements, the first of them with this index; `there` goes by lane
+    template <typename T>
+    __device__ __forceinline__ void offer_vector(bool there, const uint4 &u, int index) {
+        constexpr int VN = Vec<T>::N;
+        const uint4 one[1] = {u};
+        if (!__any_sync(kAll, there && largest<T>(one) >= bound)) return;
+        float v[VN];
+        Vec<T>::unpack(u, v);
+        uint32_t high = 0;
+#pragma unroll
+        for (int k = 0; k < VN; ++k) high |= (there && v[k] >= bound ? 1u : 0u) << k;
+        while (__any_sync(kAll, high != 0)) {  // mostly once or never
+            const int k = high ? __ffs(high) - 1 : 0;
+            float x = v[0];
+#pragma unroll
+            for (int j = 1; j < VN; ++j) x = k == j ? v[j] : x;
+            offer(high != 0, x, index + k);
+            high &= high - 1;
+        }
+    }
     __device__ __forceinline__ void end() {
         while (count > 0) flush();
-    }
-    // a first bound from the maxima of the lanes' elements
-    __device__ __forceinline__ uint32_t first(float m) {
-        const uint32_t by = sorted_falling(m == m ? ordered(m) : 0u, lane);
-        const uint32_t at = __shfl_sync(kAll, by, top - 1);
-        if (at) bound = fmaxf(bound, value_of((uint64_t)at << 32));
-        return by;
     }
 };
 
@@ -211,6 +318,7 @@ template <typename T, bool TOP>
 __global__ void __launch_bounds__(NT) logp_warp_kernel(const LogpParams p) {
     constexpr int ROWS = NT / 32;
     constexpr int VN = Vec<T>::N;
+    constexpr int UNR = 2;  // vectors of a lane in a batch (four: 65536 rows of 4096 bf16 107 us instead of 97, of 1000 69 instead of 46)
     __shared__ uint64_t queues[TOP ? ROWS : 1][kQueue];
     const int lane = threadIdx.x % 32, sub = threadIdx.x / 32;
     const int V = p.vocab;
@@ -218,9 +326,12 @@ __global__ void __launch_bounds__(NT) logp_warp_kernel(const LogpParams p) {
     pdl_next();
     pdl_wait();
     const int64_t step = (int64_t)gridDim.x * ROWS;
+    auto token = [&](int64_t t) { return p.tokens ? p.tokens[min(t, (int64_t)p.rows - 1)] : 0; };  // (read a row ahead)
+    int following = token((int64_t)blockIdx.x * ROWS + sub);
     for (int64_t t = (int64_t)blockIdx.x * ROWS + sub; t < p.rows; t += step) {
         const T *z = static_cast<const T *>(p.logits) + t * p.ld;
-        const int a = p.tokens ? p.tokens[t] : 0;
+        const int a = following;
+        following = token(t + step);
         if (a >= V && lane == 0) record_status(p.status, kDevFaultIndex);
         if (a < 0 || a >= V) {
             put_masked(p, t, lane);
@@ -232,38 +343,45 @@ __global__ void __launch_bounds__(NT) logp_warp_kernel(const LogpParams p) {
         const uint4 *zv = reinterpret_cast<const uint4 *>(z + head);
         const float za = Vec<T>::get(z + a);
         Run run(c);
-        List list(queues[TOP ? sub : 0], TOP ? p.top : 1, lane);
         const bool has_head = lane < head, has_tail = tail + lane < V;
         const float ends[2] = {has_head ? Vec<T>::get(z + lane) : -INFINITY, has_tail ? Vec<T>::get(z + tail + lane) : -INFINITY};
-        for (int i0 = 0; i0 < nv; i0 += UNR * 32) {
-            uint4 u[UNR];
-            float v[UNR * VN];
+        float best = fmaxf(ends[0], ends[1]);
+        uint4 next[UNR];
+        auto fetch = [&](int i) {
 #pragma unroll
-            for (int q = 0; q < UNR; ++q)
-                if (i0 + q * 32 + lane < nv) u[q] = zv[i0 + q * 32 + lane];
+            for (int q = 0; q < UNR; ++q) next[q] = zv[min(i + q * 32, nv - 1)];
+        };
+        if (nv > 0) fetch(lane);
+        for (int i = lane; i - lane < nv; i += UNR * 32) {
+            uint4 u[UNR];
+#pragma unroll
+            for (int q = 0; q < UNR; ++q) u[q] = next[q];
+            if (i - lane + UNR * 32 < nv) fetch(i + UNR * 32);
+            if (i - lane + UNR * 32 <= nv) {
+                best = fmaxf(best, run.template take<T>(u));
+                continue;
+            }
 #pragma unroll
             for (int q = 0; q < UNR; ++q) {
-                float w[VN];
-                Vec<T>::unpack(u[q], w);
-#pragma unroll
-                for (int k = 0; k < VN; ++k) v[q * VN + k] = i0 + q * 32 + lane < nv ? w[k] : -INFINITY;
-            }
-            const float m = run.take(v);
-            if constexpr (TOP) {
-                if (list.last == 0) list.first(m);
-                if (__any_sync(kAll, m >= list.bound)) {
-#pragma unroll
-                    for (int q = 0; q < UNR; ++q)
-#pragma unroll
-                        for (int k = 0; k < VN; ++k) list.offer(i0 + q * 32 + lane < nv, v[q * VN + k], head + (i0 + q * 32 + lane) * VN + k);
-                }
+                if (i - lane + q * 32 >= nv) break;
+                const uint4 one[1] = {u[q]};
+                best = fmaxf(best, run.template take<T>(one, i + q * 32 < nv));
             }
         }
-        run.take(ends);
-        const Sums r = join<32>(run.r, c);
+        if (__any_sync(kAll, has_head || has_tail)) run.take(ends, fmaxf(ends[0], ends[1]));
+        const Sums r = total(run.r);
         if constexpr (TOP) {
+            const uint32_t low = __shfl_sync(kAll, sorted_falling(ordered_number(best), lane), p.top - 1);
+            List list(queues[sub], p.top, value_of((uint64_t)low << 32), lane);
             list.offer(has_head, ends[0], lane);
             list.offer(has_tail, ends[1], tail + lane);
+            for (int i = lane; i - lane < nv; i += 32) {
+                const bool there = best >= list.bound && i < nv;
+                if (!__any_sync(kAll, there)) continue;
+                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                if (there) u = zv[i];
+                list.offer_vector<T>(there, u, head + i * VN);
+            }
             list.end();
             put_list(p, t, r, list.key, lane, c);
         }
@@ -322,6 +440,7 @@ template <typename T>
 __global__ void __launch_bounds__(NT) logp_grad_warp_kernel(const LogpParams p) {
     constexpr int ROWS = NT / 32;
     constexpr int VN = Vec<T>::N;
+    constexpr int UNR = 4;  // 16-byte loads of a thread in flight
     const int lane = threadIdx.x % 32, sub = threadIdx.x / 32;
     const int V = p.vocab;
     pdl_next();
@@ -369,13 +488,21 @@ __global__ void __launch_bounds__(NT) logp_grad_warp_kernel(const LogpParams p) 
 }
 
 // ---- wide rows ---------------------------------------------------------------
-constexpr int CHUNK = 16384, RING = 4, WORKERS = 256, RING_BLOCKS = 3;  // of a block, blocks per SM
+constexpr int CHUNK = 16384, WORKERS = 256;
 constexpr int WARPS = WORKERS / 32;
 constexpr int EACH = CHUNK / 16 / WORKERS;  // vectors of a thread in a chunk
-constexpr int kRingSmem = CHUNK * RING + 64 * 8;
+constexpr int MOST_RING = 6;
+// Blocks per SM, buffers of a block, warps that end items and the slots that they get them in.  (Three blocks of four
+// buffers, 8192 rows of 32768 bf16: 103 us forward; two of six 97.  Without the exponentials 82 and 81.)
+constexpr int BLOCKS = 2;
+template <bool TOP>
+struct Shape {
+    static constexpr int RING = TOP ? 5 : 6, ENDS = TOP ? 4 : 1, SLOTS = TOP ? 4 : 2;
+    static constexpr int THREADS = WORKERS + 32 + 32 * ENDS, SMEM = CHUNK * RING + 256;
+};
+// the gradient's
+constexpr int GRAD_BLOCKS = 3, GRAD_RING = 4, GRAD_SMEM = CHUNK * GRAD_RING + 256;
 
-// The vectors [v0, v1) of row t that an item covers, with the elements before the row's first 16-byte boundary if it is
-// the first part and those after the last vector if it is the last.
 template <typename T>
 struct Item {
     const T *z;
@@ -395,20 +522,26 @@ struct Item {
 };
 
 struct Ring {
-    uint64_t full[RING], empty[RING];
+    uint64_t full[MOST_RING], empty[MOST_RING];
+    uint64_t filled[4], free[4];  // slots of the items' ends
 };
+template <int RING>
 __device__ __forceinline__ void ring_init(Ring &r, int *abort_) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < RING; ++i) {
             mbar_init(smem_u32(&r.full[i]), 1);
             mbar_init(smem_u32(&r.empty[i]), WARPS);
         }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(smem_u32(&r.filled[i]), WARPS);
+            mbar_init(smem_u32(&r.free[i]), 1);
+        }
         *abort_ = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
 }
 // one thread: the item's chunks into the ring
-template <typename T>
+template <int RING, typename T>
 __device__ __forceinline__ bool ring_fill(uint8_t *ring, Ring &bars, const Item<T> &item, uint32_t &it, uint64_t policy, int64_t budget, volatile int32_t *abort_flag, int32_t *status) {
     const char *src = reinterpret_cast<const char *>(item.z + item.head) + (int64_t)item.v0 * 16;
     const int chunks = item.chunks();
@@ -425,6 +558,28 @@ __device__ __forceinline__ bool ring_fill(uint8_t *ring, Ring &bars, const Item<
     return true;
 }
 
+// A block's items: row and part, and the row's token, read an item ahead.
+struct Walk {
+    const LogpParams &p;
+    int64_t at, items;
+    int next;
+    __device__ __forceinline__ explicit Walk(const LogpParams &p_) : p(p_), at(blockIdx.x), items((int64_t)p_.rows * p_.parts), next(token(min(at, items - 1))) {}
+    __device__ __forceinline__ int64_t row(int64_t i) const { return p.parts == 1 ? i : (int64_t)((uint32_t)i / (uint32_t)p.parts); }  // (parts only where items are few)
+    __device__ __forceinline__ int token(int64_t i) const { return p.tokens ? p.tokens[row(i)] : 0; }
+    __device__ __forceinline__ bool take(int64_t &t, int &part, int &of) {
+        if (at >= items) return false;
+        t = row(at);
+        part = (int)(at - t * p.parts);
+        of = next;
+        at += gridDim.x;
+        next = token(min(at, items - 1));
+        return true;
+    }
+    __device__ __forceinline__ bool live(int of) const { return (unsigned)of < (unsigned)p.vocab; }
+};
+
+static_assert(sizeof(Ring) <= 256, "behind the buffers");
+
 // A part's share of its row, in the workspace.
 struct __align__(16) Part {
     Sums r;
@@ -433,37 +588,64 @@ struct __align__(16) Part {
 };
 static_assert(sizeof(Part) == kLogpPart, "workspace");
 
+// The largest of all parts' lists, by one warp, a part to a lane.
+__device__ __forceinline__ uint64_t best_of_parts(const Part *row, int parts, int top, uint64_t *queue, int lane) {
+    List list(queue, top, -INFINITY, lane);
+    for (int q0 = 0; q0 < parts; q0 += 32) {
+        const bool there = q0 + lane < parts;
+        const unsigned long long *from = reinterpret_cast<const unsigned long long *>(row[there ? q0 + lane : 0].key);
+        uint64_t k[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = there ? __ldcg(from + i) : 0;
+        // `top` keys lie at or above the top-th of the parts' first ones
+        const uint64_t low = __shfl_sync(kAll, sorted_falling(k[0], lane), top - 1);
+        if (low > list.last) list.last = low - 1;
+        for (int i = 0; i < 32; ++i) {
+            const uint64_t x = i < 4 ? k[0] : there ? __ldcg(from + i) : 0;
+            k[0] = k[1], k[1] = k[2], k[2] = k[3];
+            if (!__any_sync(kAll, x > list.last)) break;
+            list.offer(x);
+        }
+    }
+    list.end();
+    return list.key;
+}
+
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(WORKERS + 32, RING_BLOCKS) logp_ring_kernel(const LogpParams p) {
-    constexpr int VN = Vec<T>::N;
+__global__ void __launch_bounds__(Shape<TOP>::THREADS, BLOCKS) logp_ring_kernel(const LogpParams p) {
+    using S = Shape<TOP>;
+    constexpr int VN = Vec<T>::N, RING = S::RING;
     extern __shared__ __align__(128) uint8_t ring[];
     Ring &bars = *reinterpret_cast<Ring *>(ring + CHUNK * RING);
-    __shared__ Sums sh[2][WARPS];
-    __shared__ uint64_t lists[TOP ? 2 : 1][TOP ? WARPS : 1][32];
-    __shared__ uint64_t queues[TOP ? WARPS : 1][kQueue];
-    __shared__ float posts[2][WARPS];
+    __shared__ Sums sh[S::SLOTS][WARPS];
+    // of each thread, as ordered(): its largest element, the largest of its other chunks; the chunk
+    __shared__ uint32_t best_of[TOP ? S::SLOTS : 1][TOP ? WORKERS : 1], second_of[TOP ? S::SLOTS : 1][TOP ? WORKERS : 1], chunk_of[TOP ? S::SLOTS : 1][TOP ? WORKERS : 1];
+    __shared__ uint64_t queues[TOP ? S::ENDS : 1][kQueue];
+    __shared__ uint32_t chosen[TOP ? S::ENDS : 1][WORKERS];
     __shared__ int abort_;
     volatile int32_t *abort_flag = &abort_;
     const int V = p.vocab, warp = threadIdx.x / 32, lane = threadIdx.x % 32, parts = p.parts;
     const float c = p.scale * kLog2e;
-    ring_init(bars, &abort_);
-    if (threadIdx.x < 2 * WARPS) (&posts[0][0])[threadIdx.x] = -INFINITY;
+    ring_init<RING>(bars, &abort_);
     pdl_next();
     pdl_wait();
     __syncthreads();
-    const int64_t items = (int64_t)p.rows * parts;
-    auto live = [&](int64_t t) { return !p.tokens || (unsigned)p.tokens[t] < (unsigned)V; };
+    Walk walk(p);
+    int64_t t;
+    int part, token;
     if (warp == WARPS) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
-            uint64_t drop;
-            asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(drop));
+            uint64_t policy;  // alternatives are read again from L2
+            if (TOP)
+                asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+            else
+                asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
             uint32_t it = 0;
             bool ok = true;
-            for (int64_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
-                const int64_t t = w / parts;
-                if (!live(t)) continue;
-                ok = ring_fill(ring, bars, Item<T>(static_cast<const T *>(p.logits) + t * p.ld, V, (int)(w - t * parts), parts), it, drop, p.wait_budget, abort_flag, p.status);
+            while (ok && walk.take(t, part, token)) {
+                if (!walk.live(token)) continue;
+                ok = ring_fill<RING>(ring, bars, Item<T>(static_cast<const T *>(p.logits) + t * p.ld, V, part, parts), it, policy, p.wait_budget, abort_flag, p.status);
             }
             if (!ok) {
                 for (int q = 0; q < 100; ++q) __nanosleep(1000);
@@ -472,119 +654,92 @@ __global__ void __launch_bounds__(WORKERS + 32, RING_BLOCKS) logp_ring_kernel(co
         __syncwarp();
         return;
     }
-    // ---------------------------------------------------------------- workers
-    const int tid = threadIdx.x;
-    uint32_t it = 0;
+    // Workers and the warps that end the items hand the slots to and fro; the n-th live item of a block has slot n % SLOTS
+    // and warp n % ENDS.
+    int n = 0;
     bool ok = true;  // after a wait that ran out: nothing is stored, the barriers are kept
-    int turn = 0;    // which of the two slots; flips with the barrier that guards it, so not on masked rows
-    for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
-        const int64_t t = w / parts;
-        const int part = (int)(w - t * parts);
-        if (!live(t)) {
-            if (part == 0 && warp == 0) {
-                if (lane == 0 && p.tokens[t] >= V) record_status(p.status, kDevFaultIndex);
-                put_masked(p, t, lane);
+    if (warp > WARPS) {
+        // ------------------------------------------------------------ ends of items
+        const int me = warp - WARPS - 1;
+        while (walk.take(t, part, token)) {
+            if (!walk.live(token)) {
+                if (part == 0 && me == 0) {
+                    if (lane == 0 && token >= V) record_status(p.status, kDevFaultIndex);
+                    put_masked(p, t, lane);
+                }
+                continue;
             }
-            continue;
-        }
-        const T *z = static_cast<const T *>(p.logits) + t * p.ld;
-        const Item<T> item(z, V, part, parts);
-        const float za = warp == 0 && p.logp ? Vec<T>::get(z + p.tokens[t]) : 0.f;
-        // the row's ends: at most one element of a thread before and after the vectors
-        const bool has_head = item.first && tid < item.head, has_tail = item.last && item.tail + tid < V;
-        const float ends[2] = {has_head ? Vec<T>::get(z + tid) : -INFINITY, has_tail ? Vec<T>::get(z + item.tail + tid) : -INFINITY};
-        Run run(c);
-        List list(queues[TOP ? warp : 0], TOP ? p.top : 1, lane);
-        volatile float *post = posts[turn];  // (each has one writer and only rises: whatever a reader sees is a bound)
-        const int place = TOP ? (p.top + WARPS - 1) / WARPS - 1 : 0;  // of the posted element
-        // a batch's elements, still in the buffer, that may be among the largest
-        auto pick = [&](const uint4 *buf, int n, float m, int e0) {
-            if (list.last == 0) {
-                const uint32_t by = __shfl_sync(kAll, list.first(m), place);
-                if (by && lane == 0) post[warp] = fmaxf(post[warp], value_of((uint64_t)by << 32));
-                __syncwarp();
-            }
-            float low = post[0];
-#pragma unroll
-            for (int q = 1; q < WARPS; ++q) low = fminf(low, post[q]);
-            list.bound = fmaxf(list.bound, low);
-            list.bound = __shfl_sync(kAll, list.bound, 0);  // (the posts may rise between two lanes' loads)
-            if (!__any_sync(kAll, m >= list.bound)) return;
-#pragma unroll 1
-            for (int i = tid; i - lane < n; i += WORKERS) {
-                const bool there = i < n;
-                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                if (there) u = buf[i];
-                float v[VN];
-                Vec<T>::unpack(u, v);
-                float top = v[0];
-#pragma unroll
-                for (int k = 1; k < VN; ++k) top = fmaxf(top, v[k]);
-                if (!__any_sync(kAll, there && top >= list.bound)) continue;
-#pragma unroll
-                for (int k = 0; k < VN; ++k) list.offer(there, v[k], e0 + i * VN + k);
-            }
-            const uint64_t mine = __shfl_sync(kAll, list.key, place);
-            if (mine && lane == 0) post[warp] = fmaxf(post[warp], value_of(mine));
-        };
-        const int chunks = item.chunks();
-        for (int k = 0; k < chunks; ++k) {
-            const uint32_t b = (it + k) % RING;
-            if (ok) ok = mbar_wait_bounded(smem_u32(&bars.full[b]), ((it + k) / RING) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
+            const int slot = n % S::SLOTS, turn = n % S::ENDS, use = n / S::SLOTS;
+            ++n;
+            if (turn != me) continue;
+            const T *z = static_cast<const T *>(p.logits) + t * p.ld;
+            const float za = p.logp ? Vec<T>::get(z + token) : 0.f;
+            if (ok) ok = mbar_wait_bounded(smem_u32(&bars.filled[slot]), use & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutPartial);
             ok = __all_sync(kAll, ok);
-            const uint4 *buf = reinterpret_cast<const uint4 *>(ring + b * CHUNK);
-            const int n = item.vectors(k);
-            float m;
-            if (n == CHUNK / 16) {
-                float v[EACH * VN];
-#pragma unroll
-                for (int q = 0; q < EACH; ++q) {
-                    float u[VN];
-                    Vec<T>::unpack(buf[tid + q * WORKERS], u);
-#pragma unroll
-                    for (int j = 0; j < VN; ++j) v[q * VN + j] = u[j];
-                }
-                m = run.take(v);
-            } else {
-                m = -INFINITY;
-                for (int i = tid; i < n; i += WORKERS) {
-                    float u[VN];
-                    Vec<T>::unpack(buf[i], u);
-                    m = fmaxf(m, run.take(u));
-                }
-                __syncwarp();
-            }
-            if constexpr (TOP) pick(buf, n, m, item.head + (item.v0 + k * (CHUNK / 16)) * VN);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars.empty[b]));
-        }
-        it += chunks;
-        run.take(ends);
-        const Sums mine = join<32>(run.r, c);
-        // (a slot is written again two live items later, after the barrier that warp 0 meets when it has read it)
-        const int slot = turn;
-        turn ^= 1;
-        if (lane == 0) sh[slot][warp] = mine;
-        if constexpr (TOP) {
-            list.offer(has_head, ends[0], tid);
-            list.offer(has_tail, ends[1], item.tail + tid);
-            list.end();
-            lists[slot][warp][lane] = list.key;
-            if (lane == 0) posts[turn][warp] = -INFINITY;  // for the next item; nobody reads them before the barrier
-        }
-        asm volatile("bar.sync 1, %0;" ::"n"(WORKERS) : "memory");
-        if (warp == 0) {  // one warp ends the item; the others go on
-            const Sums r = join<WARPS>(sh[slot][lane % WARPS], c);
+            Sums r = join<WARPS>(sh[slot][lane % WARPS], c);
             uint64_t key = 0;
             if constexpr (TOP) {
-                key = lists[slot][0][lane];
+                // `top` elements lie at or above the top-th largest of the lanes' maxima over their eight threads
+                const Item<T> item(z, V, part, parts);
+                uint32_t m[WARPS], high = 0;
+#pragma unroll
+                for (int k = 0; k < WARPS; ++k) {
+                    m[k] = best_of[slot][k * 32 + lane];
+                    high = max(high, m[k]);
+                }
+                const uint32_t low = __shfl_sync(kAll, sorted_falling(high, lane), p.top - 1);
+                // where candidates are: mostly one chunk of a thread, else all of its chunks
+                int threads = 0;
+                uint32_t many = 0;  // bit k: thread 32 k + lane has them in several chunks
+#pragma unroll
+                for (int k = 0; k < WARPS; ++k) {
+                    const int of = k * 32 + lane;
+                    const bool in = m[k] >= low, more = in && second_of[slot][of] >= low;
+                    many |= (more ? 1u : 0u) << k;
+                    const uint32_t who = __ballot_sync(kAll, in && !more);
+                    if (who >> lane & 1) chosen[me][threads + __popc(who & ((1u << lane) - 1))] = chunk_of[slot][of] * (CHUNK / 16) + of;
+                    threads += __popc(who);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.free[slot]));
+                List list(queues[me], p.top, value_of((uint64_t)low << 32), lane);
+                const bool has_head = item.first && lane < item.head, has_tail = item.last && item.tail + lane < V;
+                list.offer(has_head, has_head ? Vec<T>::get(z + lane) : 0.f, lane);
+                list.offer(has_tail, has_tail ? Vec<T>::get(z + item.tail + lane) : 0.f, item.tail + lane);
+                const uint4 *row = reinterpret_cast<const uint4 *>(z + item.head) + item.v0;
+                const int nv = item.v1 - item.v0;
+                constexpr int AHEAD = 4;
+                for (int j = lane; j - lane < threads * EACH; j += 32 * AHEAD) {
+                    uint4 u[AHEAD];
+                    int at[AHEAD];
+#pragma unroll
+                    for (int q = 0; q < AHEAD; ++q) {
+                        const int k = j + 32 * q;
+                        at[q] = k < threads * EACH ? (int)chosen[me][k / EACH] + k % EACH * WORKERS : nv;
+                        u[q] = make_uint4(0u, 0u, 0u, 0u);
+                        if (at[q] < nv) u[q] = __ldcg(row + at[q]);
+                    }
+#pragma unroll
+                    for (int q = 0; q < AHEAD; ++q)
+                        if (j - lane + 32 * q < threads * EACH) list.offer_vector<T>(at[q] < nv, u[q], item.head + (item.v0 + at[q]) * VN);
+                }
 #pragma unroll 1
-                for (int q = 1; q < WARPS; ++q) key = merged(key, lists[slot][q][lane], lane);
-            }
-            if (parts == 1) {
-                if (ok && lane == 0) put_sums(p, t, r, za, c);
-                if (TOP && ok) put_list(p, t, r, key, lane, c);
+                for (int k = 0; k < WARPS; ++k)
+                    for (uint32_t who = __ballot_sync(kAll, many >> k & 1); who; who &= who - 1) {
+                        const int of = k * 32 + __ffs(who) - 1;
+                        for (int j = of + lane * WORKERS; j - lane * WORKERS < nv; j += 32 * WORKERS) {
+                            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                            if (j < nv) u = __ldcg(row + j);
+                            list.offer_vector<T>(j < nv, u, item.head + (item.v0 + j) * VN);
+                        }
+                    }
+                list.end();
+                key = list.key;
             } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.free[slot]));
+            }
+            if (parts > 1) {
                 Part *row = static_cast<Part *>(p.work) + t * parts;
                 if (lane == 0) row[part].r = r;
                 if (TOP) row[part].key[lane] = key;
@@ -593,43 +748,95 @@ __global__ void __launch_bounds__(WORKERS + 32, RING_BLOCKS) logp_ring_kernel(co
                 int arrived = 0;
                 if (lane == 0) arrived = atomicAdd(p.arrived + t, 1);
                 arrived = __shfl_sync(kAll, arrived, 0);
-                if (arrived == parts - 1) {
-                    __threadfence();
-                    if (lane == 0) p.arrived[t] = 0;
-                    Sums all = {-INFINITY, 0.f, 0.f};
-                    key = 0;
-                    for (int q0 = 0; q0 < parts; q0 += 32) {
-                        const int q = q0 + lane;
-                        Sums one = {-INFINITY, 0.f, 0.f};
-                        if (q < parts) one = {__ldcg(&row[q].r.m), __ldcg(&row[q].r.s), __ldcg(&row[q].r.t)};
-                        one = join<32>(one, c);
-                        const float m = fmaxf(all.m, one.m);
-                        all = rebased(all, m, c);
-                        one = rebased(one, m, c);
-                        all.s += one.s;
-                        all.t += one.t;
-                    }
-                    if constexpr (TOP) {
-#pragma unroll 1
-                        for (int q = 0; q < parts; ++q) key = merged(key, __ldcg(reinterpret_cast<const unsigned long long *>(&row[q].key[lane])), lane);
-                    }
-                    if (ok && lane == 0) put_sums(p, t, all, za, c);
-                    if (TOP && ok) put_list(p, t, all, key, lane, c);
+                if (arrived != parts - 1) continue;
+                __threadfence();
+                if (lane == 0) p.arrived[t] = 0;
+                r = {-INFINITY, 0.f, 0.f};
+                for (int q0 = 0; q0 < parts; q0 += 32) {
+                    const int q = q0 + lane;
+                    Sums one = {-INFINITY, 0.f, 0.f};
+                    if (q < parts) one = {__ldcg(&row[q].r.m), __ldcg(&row[q].r.s), __ldcg(&row[q].r.t)};
+                    one = join<32>(one, c);
+                    const float m = fmaxf(r.m, one.m);
+                    r = rebased(r, m, c);
+                    one = rebased(one, m, c);
+                    r.s += one.s;
+                    r.t += one.t;
+                }
+                if constexpr (TOP) key = best_of_parts(row, parts, p.top, queues[me], lane);
+            }
+            if (!ok || *abort_flag) continue;
+            if (lane == 0) put_sums(p, t, r, za, c);
+            if (TOP) put_list(p, t, r, key, lane, c);
+        }
+        return;
+    }
+    // ---------------------------------------------------------------- workers
+    const int tid = threadIdx.x;
+    uint32_t it = 0;
+    while (walk.take(t, part, token)) {
+        if (!walk.live(token)) continue;
+        const T *z = static_cast<const T *>(p.logits) + t * p.ld;
+        const Item<T> item(z, V, part, parts);
+        // the row's ends: at most one element of a thread before and after the vectors
+        const bool has_head = item.first && tid < item.head, has_tail = item.last && item.tail + tid < V;
+        const float ends[2] = {has_head ? Vec<T>::get(z + tid) : -INFINITY, has_tail ? Vec<T>::get(z + item.tail + tid) : -INFINITY};
+        Run run(c);
+        float best = -INFINITY, second = -INFINITY;
+        int where = 0;
+        const int chunks = item.chunks();
+        for (int k = 0; k < chunks; ++k, ++it) {
+            const uint32_t b = it % RING;
+            if (ok) ok = mbar_wait_bounded(smem_u32(&bars.full[b]), (it / RING) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
+            ok = __all_sync(kAll, ok);
+            const uint4 *buf = reinterpret_cast<const uint4 *>(ring + b * CHUNK);
+            const int count = item.vectors(k);
+            float m = -INFINITY;
+            if (count == CHUNK / 16) {
+                uint4 u[EACH];
+#pragma unroll
+                for (int q = 0; q < EACH; ++q) u[q] = buf[tid + q * WORKERS];
+                m = run.template take<T>(u);
+            } else {
+                for (int i = tid; i - lane < count; i += WORKERS) {
+                    const uint4 u[1] = {buf[min(i, count - 1)]};
+                    m = fmaxf(m, run.template take<T>(u, i < count));
                 }
             }
+            if constexpr (TOP) {
+                second = fmaxf(second, fminf(best, m));
+                where = m > best ? k : where;
+                best = fmaxf(best, m);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars.empty[b]));
         }
+        if (__any_sync(kAll, has_head || has_tail)) run.take(ends, fmaxf(ends[0], ends[1]));
+        const Sums mine = total(run.r);
+        const int slot = n % S::SLOTS, use = n / S::SLOTS;
+        ++n;
+        if (ok) ok = mbar_wait_bounded(smem_u32(&bars.free[slot]), (use & 1) ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
+        ok = __all_sync(kAll, ok);
+        if (lane == 0) sh[slot][warp] = mine;
+        if constexpr (TOP) {
+            best_of[slot][tid] = ordered_number(best);
+            second_of[slot][tid] = ordered_number(second);
+            chunk_of[slot][tid] = (uint32_t)where;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.filled[slot]));
     }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(WORKERS + 32, RING_BLOCKS) logp_grad_ring_kernel(const LogpParams p) {
-    constexpr int VN = Vec<T>::N;
+__global__ void __launch_bounds__(WORKERS + 32, GRAD_BLOCKS) logp_grad_ring_kernel(const LogpParams p) {
+    constexpr int VN = Vec<T>::N, RING = GRAD_RING;
     extern __shared__ __align__(128) uint8_t ring[];
     Ring &bars = *reinterpret_cast<Ring *>(ring + CHUNK * RING);
     __shared__ int abort_;
     volatile int32_t *abort_flag = &abort_;
     const int V = p.vocab, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    ring_init(bars, &abort_);
+    ring_init<RING>(bars, &abort_);
     pdl_next();
     pdl_wait();
     __syncthreads();
@@ -646,7 +853,7 @@ __global__ void __launch_bounds__(WORKERS + 32, RING_BLOCKS) logp_grad_ring_kern
                 const GradIn in = next;
                 next = grad_in(p, min(t + gridDim.x, last));
                 if (!grad_live(p, in)) continue;
-                ok = ring_fill(ring, bars, Item<T>(static_cast<const T *>(p.logits) + t * p.ld, V, 0, 1), it, drop, p.wait_budget, abort_flag, p.status);
+                ok = ring_fill<RING>(ring, bars, Item<T>(static_cast<const T *>(p.logits) + t * p.ld, V, 0, 1), it, drop, p.wait_budget, abort_flag, p.status);
             }
             if (!ok) {
                 for (int q = 0; q < 100; ++q) __nanosleep(1000);
@@ -713,16 +920,15 @@ __global__ void __launch_bounds__(WORKERS + 32, RING_BLOCKS) logp_grad_ring_kern
 }
 
 template <typename K>
-cudaError_t launch_ring(K kernel, bool (&attr_set)[64], const LogpParams &p, int64_t items, int num_sms, cudaStream_t s) {
+cudaError_t launch_ring(K kernel, bool (&attr_set)[64], const LogpParams &p, int64_t items, int blocks, int threads, int smem, cudaStream_t s) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
-    const int64_t most = (int64_t)RING_BLOCKS * num_sms;
-    return launch_early(kernel, (int)(items < most ? items : most), WORKERS + 32, kRingSmem, s, p);
+    return launch_early(kernel, (int)(items < blocks ? items : blocks), threads, smem, s, p);
 }
 template <typename T, bool TOP>
 cudaError_t launch_forward(const LogpParams &p, bool narrow, int num_sms, cudaStream_t s) {
@@ -731,7 +937,7 @@ cudaError_t launch_forward(const LogpParams &p, bool narrow, int num_sms, cudaSt
         return launch_early(logp_warp_kernel<T, TOP>, (int)(need < most ? need : most), NT, 0, s, p);
     }
     static bool attr_set[64] = {};
-    return launch_ring(logp_ring_kernel<T, TOP>, attr_set, p, (int64_t)p.rows * p.parts, num_sms, s);
+    return launch_ring(logp_ring_kernel<T, TOP>, attr_set, p, (int64_t)p.rows * p.parts, BLOCKS * num_sms, Shape<TOP>::THREADS, Shape<TOP>::SMEM, s);
 }
 template <typename T>
 cudaError_t launch_backward(const LogpParams &p, bool narrow, int num_sms, cudaStream_t s) {
@@ -740,18 +946,19 @@ cudaError_t launch_backward(const LogpParams &p, bool narrow, int num_sms, cudaS
         return launch_early(logp_grad_warp_kernel<T>, (int)(need < most ? need : most), NT, 0, s, p);
     }
     static bool attr_set[64] = {};
-    return launch_ring(logp_grad_ring_kernel<T>, attr_set, p, p.rows, num_sms, s);
+    return launch_ring(logp_grad_ring_kernel<T>, attr_set, p, p.rows, GRAD_BLOCKS * num_sms, WORKERS + 32, GRAD_SMEM, s);
 }
 
 bool narrow_rows(const LogpParams &p, int dtype) { return (int64_t)p.vocab * (dtype == 1 ? 2 : 4) <= 16384; }
 
 }  // namespace
 
-int logp_most_items(int num_sms) { return RING_BLOCKS * num_sms; }
+int logp_most_items(int num_sms) { return BLOCKS * num_sms; }
 
-// Parts of a row: as many as the blocks that would else stay idle, each of 8 KB at least.
+// Parts of a row: as many as the blocks that would else stay idle, each of 8 KB at least.  (64 rows of 128000 bf16 9.5 us, two
+// or three items to a block 11.3 and 13.3; one row in parts of 4 KB, with 20 alternatives, 14.1 instead of 12.0.)
 int logp_parts(int64_t rows, int64_t vocab, int dtype, int num_sms) {
-    const int64_t bytes = vocab * (dtype == 1 ? 2 : 4), slots = (int64_t)RING_BLOCKS * num_sms;
+    const int64_t bytes = vocab * (dtype == 1 ? 2 : 4), slots = (int64_t)BLOCKS * num_sms;
     if (bytes <= 16384 || rows >= slots) return 1;
     return (int)std::max<int64_t>(1, std::min(slots / rows, bytes / 8192));
 }
