@@ -549,18 +549,17 @@ __device__ __forceinline__ float4 load4(const void *x, int64_t i, bool bf16) {
 constexpr int NT = 256;
 
 // Squares of u, summed by block; the momentum is updated on the way.  u = g without momentum, else m' = beta m + g and u =
-// g + beta m' (nesterov) or m'.  (Summed in fp64, four squares at a time in fp32 where they are far from its ends: a
-// conversion and an addition of fp64 for each element would take longer than the memory.)
+// g + beta m' (nesterov) or m'.
 template <int V>
 __global__ void __launch_bounds__(NT) orth_norm_kernel(const OrthPrepParams p) {
-    __shared__ double part[NT / 32];
+    __shared__ double part[NT / 32][2];
     pdl_next();
     pdl_wait();
     const int e = blockIdx.y;
     if (blockIdx.x == 0 && threadIdx.x == 0) p.done[e] = 0;
     const int per_row = (p.cols + V - 1) / V;  // (V divides cols where V > 1)
     const int64_t items = (int64_t)p.rows * per_row;
-    double sum = 0.0;
+    SquareSum sum = {0.f, 0.0};
     for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < items; i += (int64_t)gridDim.x * NT) {
         const int r = (int)(i / per_row), c = (int)(i - (int64_t)r * per_row) * V;
         const int64_t at = (int64_t)e * p.ls + (int64_t)r * p.ld + c;
@@ -587,24 +586,18 @@ __global__ void __launch_bounds__(NT) orth_norm_kernel(const OrthPrepParams p) {
             else
                 *to = m[0];
         }
-        float q = 0.f;
-#pragma unroll
-        for (int k = 0; k < V; ++k) q = fmaf(g[k], g[k], q);
-        if (q > 0x1p-60f && q < 0x1p120f) {  // far from both ends of fp32, each square above 2^-24 of q among them
-            sum += (double)q;
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k) sum += (double)g[k] * (double)g[k];
-        }
+        sum.add(g);
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+    sum.join();
+    if (threadIdx.x % 32 == 0) {
+        part[threadIdx.x / 32][0] = (double)sum.safe;
+        part[threadIdx.x / 32][1] = sum.rest;
+    }
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x < 2) {
         double s = 0.0;
-        for (int i = 0; i < NT / 32; ++i) s += part[i];
-        p.partial[(int64_t)e * gridDim.x + blockIdx.x] = s;
+        for (int i = 0; i < NT / 32; ++i) s += part[i][threadIdx.x];
+        p.partial[((int64_t)e * gridDim.x + blockIdx.x) * 2 + threadIdx.x] = s;
     }
 }
 
@@ -616,11 +609,14 @@ __global__ void __launch_bounds__(NT) orth_split_kernel(const OrthPrepParams p) 
     pdl_wait();
     const int e = blockIdx.y;
     if (threadIdx.x < 32) {
-        double s = 0.0;
-        for (int i = threadIdx.x; i < p.parts; i += 32) s += p.partial[(int64_t)e * p.parts + i];
-#pragma unroll
-        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        if (threadIdx.x == 0) orth_factors(s, factor);
+        double s = 0.0, rest = 0.0;
+        for (int i = threadIdx.x; i < p.parts; i += 32) {
+            s += p.partial[((int64_t)e * p.parts + i) * 2];
+            rest += p.partial[((int64_t)e * p.parts + i) * 2 + 1];
+        }
+        SquareSum sum = {0.f, s + rest};
+        sum.join();
+        if (threadIdx.x == 0) orth_factors(sum, factor[0], factor[1], factor[2]);
     }
     __syncthreads();
     const float f0 = factor[0], f1 = factor[1], f2 = factor[2];

@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "device_util.cuh"
@@ -34,10 +35,6 @@ constexpr int X_PLANE = 4 * BLOCK, G_PLANE = 2 * BLOCK;
 constexpr int SMEM = 1024 + 2 * X_PLANE + 2 * G_PLANE;
 static_assert(2 * X_PLANE == 128 * 256 * 4 && 2 * G_PLANE == 128 * 128 * 4, "a slice and a Gram matrix in fp32 fit their planes");
 
-__device__ __forceinline__ uint32_t half_bits(float x) {
-    const __half h = __float2half_rn(x);
-    return *reinterpret_cast<const uint16_t *>(&h);
-}
 __device__ __forceinline__ uint32_t pack_hi(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -54,9 +51,26 @@ __device__ __forceinline__ float2 unpack(uint32_t h, uint32_t l) {
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(c >> 6) * BLOCK + (uint32_t)r * 128u + (((uint32_t)(c >> 3) ^ (uint32_t)r) & 7u) * 16u; }
 // float of row r, column c in an area of `width` floats a row, 16-byte chunks swapped so that a column's reads spread
 __device__ __forceinline__ uint32_t float_at(int r, int c, int width) { return (uint32_t)r * (uint32_t)width + ((((uint32_t)c >> 2) ^ ((uint32_t)r & 7u)) << 2) + ((uint32_t)c & 3u); }
-__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t a_lead, uint32_t b, uint32_t b_lead, uint32_t hi, uint32_t idesc, uint32_t acc) {
-    tc_mma(d, (uint64_t)hi << 32 | (((a >> 4) & 0x3FFFu) | a_lead << 16), (uint64_t)hi << 32 | (((b >> 4) & 0x3FFFu) | b_lead << 16), idesc, acc);
+// One lane of a warp that runs converged issues (a single thread in a branch takes 80 to 100 clocks for each MMA of 64).
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+        : "memory");
 }
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
+}
+// The low word of a descriptor: 16-byte address and leading offset.
+__device__ __forceinline__ uint32_t desc(uint32_t addr, uint32_t lead) { return ((addr >> 4) & 0x3FFFu) | lead << 16; }
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 __device__ __forceinline__ float load1(const void *x, int64_t i, bool bf16) {
@@ -69,8 +83,7 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
     __shared__ __align__(8) uint64_t bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_;
-    __shared__ double partial[WARPS], mine_sum;
-    __shared__ float factor[3];
+    __shared__ SquareSum partial[WARPS], total;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, c = p.cluster;
     const int rank = c > 1 ? (int)cluster_ctarank() : 0, e = blockIdx.x / c;
     const bool high = p.rows > p.cols;
@@ -98,94 +111,102 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
     const uint32_t tmem = tmem_slot;
 
     // ---- u, its norm, and the planes
-    // Element i of the slice: along the caller's rows, so that a warp's loads are neighbours.
-    const int inner = high ? g : valid, items = g * valid;
-    auto place = [&](int i, int &r, int &cc, int64_t &at, int64_t &at_m) {  // row and column of X; of the caller's tensors
-        const int o = i / inner, k = i - o * inner;
-        r = high ? k : o;
-        cc = high ? o : k;
-        const int row = high ? col0 + o : o, col = high ? k : col0 + k;
-        at = (int64_t)e * p.ls + (int64_t)row * p.ld + col;
-        at_m = ((int64_t)e * p.rows + row) * p.cols + col;
-    };
-    constexpr int U = 8;
-    double sum = 0.0;
-    for (int i0 = tid; i0 < items; i0 += U * NT) {
-        float x[U], m[U];
-        int64_t at_m[U];
+    // (Short code: the start of a launch waits for instructions.)
+    const int inner = high ? g : valid, outer = high ? valid : g;  // of the slice: along the caller's rows, across them
+    const int row0 = high ? col0 : 0, left = high ? 0 : col0;      // its corner in the caller's matrix
+    const int64_t corner = ((int64_t)e * p.rows + row0) * p.cols + left, given = (int64_t)e * p.ls + (int64_t)row0 * p.ld + left;
+    // The sum of squares, an element at a time along the caller's rows.
+    constexpr int U = 8;  // loads of a thread in flight
+    SquareSum sum = {0.f, 0.0};
+    {
+        const int items = inner * outer, over = inner ? NT / inner : 0, rest = inner ? NT % inner : 0;
+        int o = inner ? tid / inner : 0, k = inner ? tid % inner : 0;
+#pragma unroll 1
+        for (int i0 = tid; i0 < items; i0 += U * NT) {
+            float x[U], m[U];
+            int64_t at[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            int r, cc;
-            int64_t at;
-            place(min(i0 + k * NT, items - 1), r, cc, at, at_m[k]);
-            x[k] = load1(p.grad, at, p.in_bf16);
-            if (p.momentum) m[k] = p.momentum[at_m[k]];
-        }
-        float q = 0.f;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (i0 + k * NT >= items) {
-                x[k] = 0.f;
-                continue;
+            for (int j = 0; j < U; ++j) {
+                x[j] = m[j] = 0.f;
+                at[j] = corner + (int64_t)o * p.cols + k;
+                if (i0 + j * NT < items) {
+                    x[j] = load1(p.grad, given + (int64_t)o * p.ld + k, p.in_bf16);
+                    if (p.momentum) m[j] = p.momentum[at[j]];
+                }
+                o += over;
+                k += rest;
+                if (k >= inner) {
+                    k -= inner;
+                    ++o;
+                }
             }
             if (p.momentum) {
-                m[k] = fmaf(p.beta, m[k], x[k]);
-                p.momentum[at_m[k]] = m[k];
-                x[k] = p.nesterov ? fmaf(p.beta, m[k], x[k]) : m[k];
-            }
-            q = fmaf(x[k], x[k], q);
-        }
-        if (q > 0x1p-60f && q < 0x1p120f) {  // far from both ends of fp32
-            sum += (double)q;
-        } else {
 #pragma unroll
-            for (int k = 0; k < U; ++k) sum += (double)x[k] * (double)x[k];
+                for (int j = 0; j < U; ++j) {
+                    m[j] = fmaf(p.beta, m[j], x[j]);
+                    x[j] = p.nesterov ? fmaf(p.beta, m[j], x[j]) : m[j];
+                    if (i0 + j * NT < items) p.momentum[at[j]] = m[j];
+                }
+            }
+            sum.add(x);
         }
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    sum.join();
     if (lane == 0) partial[warp] = sum;
     __syncthreads();
-    if (tid == 0) {
-        sum = 0.0;
-        for (int i = 0; i < WARPS; ++i) sum += partial[i];
-        mine_sum = sum;
+    if (warp == 0) {
+        sum = lane < WARPS ? partial[lane] : SquareSum{0.f, 0.0};
+        sum.join();
+        if (lane == 0) total = sum;
     }
     sync_all();
-    if (tid == 0) {
-        sum = 0.0;
+    sum = total;
+    if (c > 1) {  // of the whole matrix, in order
+        sum = {0.f, 0.0};
         for (int k = 0; k < c; ++k) {
-            double x = mine_sum;
-            if (c > 1) asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(x) : "r"(mapa_shared(smem_u32(&mine_sum), k)) : "memory");
-            sum += x;
+            const uint32_t from = mapa_shared(smem_u32(&total), k);
+            float x;
+            double y;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(from + (uint32_t)offsetof(SquareSum, safe)) : "memory");
+            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(y) : "r"(from + (uint32_t)offsetof(SquareSum, rest)) : "memory");
+            sum.safe += x;
+            if (y != 0.0) sum.rest += y;
         }
-        orth_factors(sum, factor);
     }
-    __syncthreads();
-    const float f0 = factor[0], f1 = factor[1], f2 = factor[2];
-    for (int i0 = tid; i0 < items; i0 += U * NT) {
-        float x[U];
-        uint32_t to[U];
+    float f0, f1, f2;
+    orth_factors(sum, f0, f1, f2);
+    // The planes, eight columns of a row at a time, neighbouring threads along the caller's rows.
+    {
+        const int chunks = (valid + 7) / 8, fast = high ? g : chunks, items = g * chunks;
+        const int64_t next_in = high ? p.ld : 1, next_m = high ? p.cols : 1;
+#pragma unroll 1
+        for (int i = tid; i < items; i += NT) {
+            const int s = i / fast, f = i - s * fast, r = high ? f : s, cc = (high ? s : f) * 8;
+            const int o = high ? cc : r, k = high ? r : cc;
+            const int64_t in = given + (int64_t)o * p.ld + k, at = corner + (int64_t)o * p.cols + k;
+            float x[8], m[8];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            int r, cc;
-            int64_t at, at_m;
-            place(min(i0 + k * NT, items - 1), r, cc, at, at_m);
-            to[k] = chunk_at(r, cc & ~7) + (uint32_t)(cc & 7) * 2u;
-            x[k] = p.momentum && !p.nesterov ? 0.f : load1(p.grad, at, p.in_bf16);
-            if (p.momentum) {
-                const float m = p.momentum[at_m];  // (this thread's own)
-                x[k] = p.nesterov ? fmaf(p.beta, m, x[k]) : m;
+            for (int j = 0; j < 8; ++j) {
+                x[j] = m[j] = 0.f;
+                if (cc + j < valid) {
+                    if (!p.momentum || p.nesterov) x[j] = load1(p.grad, in + j * next_in, p.in_bf16);
+                    if (p.momentum) m[j] = __ldcg(p.momentum + at + j * next_m);  // (written by another thread of this CTA)
+                }
             }
-        }
+            uint32_t h[4], l[4];
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (i0 + k * NT >= items) break;
-            const float v = x[k] * f0 * f1 * f2;
-            const uint32_t h = half_bits(v);
-            *reinterpret_cast<uint16_t *>(sx + to[k]) = (uint16_t)h;
-            const uint16_t hb = (uint16_t)h;
-            *reinterpret_cast<uint16_t *>(sx + X_PLANE + to[k]) = (uint16_t)half_bits(v - __half2float(*reinterpret_cast<const __half *>(&hb)));
+            for (int j = 0; j < 8; ++j) {
+                if (p.momentum) x[j] = p.nesterov ? fmaf(p.beta, m[j], x[j]) : m[j];
+                x[j] = x[j] * f0 * f1 * f2;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                h[j] = pack_hi(x[2 * j], x[2 * j + 1]);
+                l[j] = pack_lo(x[2 * j], x[2 * j + 1]);
+            }
+            const uint32_t to = chunk_at(r, cc);
+            *reinterpret_cast<uint4 *>(sx + to) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(sx + X_PLANE + to) = make_uint4(l[0], l[1], l[2], l[3]);
         }
     }
 
@@ -196,14 +217,16 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
     const uint32_t desc_hi = (uint32_t)(smem_desc_sw128(0, 0, 1024) >> 32);
     uint32_t phase = 0;
     bool ok = true;
-    auto product = [&](auto &&issue) {  // by one thread, then waited for by all
+    auto product = [&](auto &&issue) {  // by one warp, then waited for by all
         fence_proxy_async();
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if (tid == 0) {
+        if (warp == 0) {
+            __syncwarp();
             issue();
-            tc_commit(bar_at);
+            commit(bar_at);
+            __syncwarp();
         }
         if (ok) ok = mbar_wait_bounded(bar_at, phase, p.wait_budget, &abort_, p.status, kDevTimeoutMma);
         phase ^= 1;
@@ -211,30 +234,42 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
         __syncwarp();
     };
     const int deep = (g + 15) / 16;  // 16-deep steps of a contraction over the smaller side
+    const int along = max(1, (valid + 15) / 16);  // over the slice
+    const uint32_t x_k = desc(x_at, 1), x_mn = desc(x_at, BLOCK >> 4), g_k = desc(g_at, 1);
+    // hi hi and, before it, hi lo and lo hi: the small ones first
+    auto terms = [&](bool single, uint32_t a, uint32_t a_plane, uint32_t b, uint32_t b_plane, int steps, auto &&a_step, auto &&b_step, uint32_t id) {
+        uint32_t acc = 0;
+        if (!single) {
+#pragma unroll 4
+            for (int k = 0; k < steps; ++k, acc = 1) mma(tmem, a + a_step(k), b + b_plane + b_step(k), desc_hi, id, acc);
+#pragma unroll 4
+            for (int k = 0; k < steps; ++k) mma(tmem, a + a_plane + a_step(k), b + b_step(k), desc_hi, id, 1);
+        }
+#pragma unroll 4
+        for (int k = 0; k < steps; ++k, acc = 1) mma(tmem, a + a_step(k), b + b_step(k), desc_hi, id, acc);
+    };
+    auto k_step = [](int k) { return (uint32_t)(k >> 2) * (BLOCK >> 4) + (uint32_t)(k & 3) * 2u; };
+    auto mn_step = [](int k) { return (uint32_t)k * 128u; };
+    constexpr uint32_t XP = X_PLANE >> 4, GP = G_PLANE >> 4;
     for (int step = 0; step < p.steps; ++step) {
         const bool single = step >= p.single_from, final = step + 1 == p.steps;
-        const int terms = single ? 1 : 3;
+        constexpr uint32_t square_id = (1u << 4) | (128u >> 3) << 17 | (128u >> 4) << 24;
         // gram
-        product([&] {
-            const uint32_t id = (1u << 4) | (128u >> 3) << 17 | (128u >> 4) << 24;
-            uint32_t acc = 0;
-            for (int kb = 0; kb < width / 64; ++kb)
-                for (int t = terms; t--;)  // the small terms first
-                    for (int kk = 0; kk < 4; ++kk, acc = 1)
-                        mma(tmem, x_at + (t == 1 ? X_PLANE : 0) + kb * BLOCK + kk * 32, 1, x_at + (t == 2 ? X_PLANE : 0) + kb * BLOCK + kk * 32, 1, desc_hi, id, acc);
-        });
+        product([&] { terms(single, x_k, XP, x_k, XP, along, k_step, k_step, square_id); });
+        float old[32];  // this thread's part of A
         {
             uint32_t v[32];
             tmem_ld32(lane_base + part * 32, v);
             if (c == 1) {
 #pragma unroll
+                for (int q = 0; q < 32; ++q) old[q] = __uint_as_float(v[q]) * (1.f / kOrthUp);
+#pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t h[4], l[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float x = __uint_as_float(v[q * 8 + 2 * i]) * (1.f / kOrthUp), y = __uint_as_float(v[q * 8 + 2 * i + 1]) * (1.f / kOrthUp);
-                        h[i] = pack_hi(x, y);
-                        l[i] = pack_lo(x, y);
+                        h[i] = pack_hi(old[q * 8 + 2 * i], old[q * 8 + 2 * i + 1]);
+                        l[i] = pack_lo(old[q * 8 + 2 * i], old[q * 8 + 2 * i + 1]);
                     }
                     const uint32_t to = chunk_at(row, part * 32 + q * 8);
                     *reinterpret_cast<uint4 *>(sg + to) = make_uint4(h[0], h[1], h[2], h[3]);
@@ -256,13 +291,17 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
                     s[q] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (j < rows_here * 32) {
                         const uint32_t from = smem_u32(f + float_at(r, cc, 128));
-                        for (int k = 0; k < c; ++k) {
-                            float4 x;
-                            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(mapa_shared(from, k)) : "memory");
-                            s[q].x += x.x;
-                            s[q].y += x.y;
-                            s[q].z += x.z;
-                            s[q].w += x.w;
+                        float4 x[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (k < c) asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[k].x), "=f"(x[k].y), "=f"(x[k].z), "=f"(x[k].w) : "r"(mapa_shared(from, k)) : "memory");
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            if (k >= c) break;
+                            s[q].x += x[k].x;
+                            s[q].y += x[k].y;
+                            s[q].z += x[k].z;
+                            s[q].w += x[k].w;
                         }
                     }
                 }
@@ -283,49 +322,47 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
                 }
                 fence_proxy_async();
                 cluster_sync_all();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint4 h = *reinterpret_cast<const uint4 *>(sg + chunk_at(row, part * 32 + q * 8)), l = *reinterpret_cast<const uint4 *>(sg + G_PLANE + chunk_at(row, part * 32 + q * 8));
+                    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 x = unpack(hw[i], lw[i]);
+                        old[q * 8 + 2 * i] = x.x;
+                        old[q * 8 + 2 * i + 1] = x.y;
+                    }
+                }
             }
         }
         // square
-        product([&] {
-            const uint32_t id = (1u << 4) | (128u >> 3) << 17 | (128u >> 4) << 24;
-            uint32_t acc = 0;
-            for (int t = terms; t--;)
-                for (int k = 0; k < deep; ++k, acc = 1) {
-                    const uint32_t at = g_at + (k >> 2) * BLOCK + (k & 3) * 32;
-                    mma(tmem, at + (t == 1 ? G_PLANE : 0), 1, at + (t == 2 ? G_PLANE : 0), 1, desc_hi, id, acc);
-                }
-        });
+        product([&] { terms(single, g_k, GP, g_k, GP, deep, k_step, k_step, square_id); });
         {
             const float a = p.coef[3 * step] * kOrthUpPoly, b = p.coef[3 * step + 1] * (kOrthUpPoly / kOrthUp), cq = p.coef[3 * step + 2] * (kOrthUpPoly / (kOrthUp * kOrthUp));
             uint32_t v[32];
             tmem_ld32(lane_base + part * 32, v);
 #pragma unroll
+            for (int q = 0; q < 32; ++q) old[q] = fmaf(cq, __uint_as_float(v[q]), b * old[q]);
+            if (warp % 4 == part) {  // the diagonal's warps
+#pragma unroll
+                for (int q = 0; q < 32; ++q)
+                    if (q == lane) old[q] += a;
+            }
+#pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int col = part * 32 + q * 8;
-                uint4 *at_h = reinterpret_cast<uint4 *>(sg + chunk_at(row, col)), *at_l = reinterpret_cast<uint4 *>(sg + G_PLANE + chunk_at(row, col));
-                const uint4 oh = *at_h, ol = *at_l;
-                const uint32_t hw[4] = {oh.x, oh.y, oh.z, oh.w}, lw[4] = {ol.x, ol.y, ol.z, ol.w};
                 uint32_t h[4], l[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 old = unpack(hw[i], lw[i]);
-                    const float x = fmaf(cq, __uint_as_float(v[q * 8 + 2 * i]), b * old.x) + (row == col + 2 * i ? a : 0.f);
-                    const float y = fmaf(cq, __uint_as_float(v[q * 8 + 2 * i + 1]), b * old.y) + (row == col + 2 * i + 1 ? a : 0.f);
-                    h[i] = pack_hi(x, y);
-                    l[i] = pack_lo(x, y);
+                    h[i] = pack_hi(old[q * 8 + 2 * i], old[q * 8 + 2 * i + 1]);
+                    l[i] = pack_lo(old[q * 8 + 2 * i], old[q * 8 + 2 * i + 1]);
                 }
-                *at_h = make_uint4(h[0], h[1], h[2], h[3]);
-                *at_l = make_uint4(l[0], l[1], l[2], l[3]);
+                const uint32_t to = chunk_at(row, part * 32 + q * 8);
+                *reinterpret_cast<uint4 *>(sg + to) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(sg + G_PLANE + to) = make_uint4(l[0], l[1], l[2], l[3]);
             }
         }
         // product
-        product([&] {
-            const uint32_t id = (1u << 4) | 1u << 16 | (uint32_t)(width >> 3) << 17 | (128u >> 4) << 24;
-            uint32_t acc = 0;
-            for (int t = terms; t--;)
-                for (int k = 0; k < deep; ++k, acc = 1)
-                    mma(tmem, g_at + (t == 1 ? G_PLANE : 0) + (k >> 2) * BLOCK + (k & 3) * 32, 1, x_at + (t == 2 ? X_PLANE : 0) + k * 2048, BLOCK >> 4, desc_hi, id, acc);
-        });
+        product([&] { terms(single, g_k, GP, x_mn, XP, deep, k_step, mn_step, (1u << 4) | 1u << 16 | (uint32_t)(width >> 3) << 17 | (128u >> 4) << 24); });
         const int each = width / 4;  // columns of a thread, a multiple of 16
         const float mul = final ? 1.f / (kOrthUp * kOrthUpPoly) : 1.f / kOrthUpPoly;
         for (int q = 0; q < each; q += 16) {
@@ -358,33 +395,37 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
     // ---- the result, along the caller's rows
     tc_fence_before();
     __syncthreads();
-    const float *fx = reinterpret_cast<const float *>(sx);
-    for (int i0 = tid; ok && i0 < items; i0 += U * NT) {
-        float x[U], old[U];
-        int64_t at[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            int r, cc;
-            int64_t skip;
-            const int i = min(i0 + k * NT, items - 1);
-            place(i, r, cc, skip, at[k]);
-            x[k] = fx[float_at(r, cc, width)];
-            if (p.weight)
-                old[k] = p.weight[at[k]];
-            else
-                at[k] = (int64_t)e * p.lse + (int64_t)(high ? col0 + cc : r) * p.ldo + (high ? r : col0 + cc);
-        }
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (i0 + k * NT >= items) break;
+    {
+        const float *fx = reinterpret_cast<const float *>(sx);
+        const int chunks = (valid + 3) / 4, fast = high ? g : chunks, items = g * chunks;
+        const int64_t ld = p.weight ? p.cols : p.ldo, first = p.weight ? corner : (int64_t)e * p.lse + (int64_t)row0 * p.ldo + left, next = high ? ld : 1;
+#pragma unroll 2
+        for (int i = tid; ok && i < items; i += NT) {
+            const int s = i / fast, f = i - s * fast, r = high ? f : s, cc = (high ? s : f) * 4;
+            const float4 v = *reinterpret_cast<const float4 *>(fx + float_at(r, cc, width));
+            const float x[4] = {v.x, v.y, v.z, v.w};
+            const int64_t at = first + (int64_t)(high ? cc : r) * ld + (high ? r : cc);
             if (p.weight) {
-                const float w = fmaf(-p.rate, x[k], old[k] * p.keep);
-                p.weight[at[k]] = w;
-                if (p.copy) p.copy[at[k]] = __float2bfloat16_rn(w);
-            } else if (p.out_bf16) {
-                static_cast<__nv_bfloat16 *>(p.result)[at[k]] = __float2bfloat16_rn(x[k]);
+                float was[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) was[j] = cc + j < valid ? p.weight[at + j * next] : 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float n = fmaf(-p.rate, x[j], was[j] * p.keep);
+                    if (cc + j < valid) {
+                        p.weight[at + j * next] = n;
+                        if (p.copy) p.copy[at + j * next] = __float2bfloat16_rn(n);
+                    }
+                }
             } else {
-                static_cast<float *>(p.result)[at[k]] = x[k];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (cc + j >= valid) break;
+                    if (p.out_bf16)
+                        static_cast<__nv_bfloat16 *>(p.result)[at + j * next] = __float2bfloat16_rn(x[j]);
+                    else
+                        static_cast<float *>(p.result)[at + j * next] = x[j];
+                }
             }
         }
     }

@@ -175,7 +175,7 @@ struct OrthPrepParams {
     const void *grad;        // [batch] matrices, `ls` elements apart, rows `ld` apart
     float *momentum;         // dense, or NULL
     __half *hi, *lo;         // [batch][rows][pitch]
-    double *partial;         // [batch][parts]
+    double *partial;         // [batch][parts][2]: SquareSum's two
     int32_t *done;           // [batch], cleared
     int64_t ls, ld;
     int32_t batch, rows, cols, pitch, parts, bf16, nesterov;
@@ -226,18 +226,66 @@ struct OrthSmallParams {
 };
 cudaError_t launch_orth_small(const OrthSmallParams &p, cudaStream_t s);
 #ifdef __CUDACC__
+// A sum of squares: of those far from both ends of fp32 in fp32, of the others in fp64 (a conversion and an addition of fp64
+// for every element would take longer than the memory).
+struct SquareSum {
+    float safe;
+    double rest;
+    template <int N>
+    __device__ __forceinline__ void add(const float (&x)[N]) {
+        float q = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) q = fmaf(x[j], x[j], q);
+        if (q > 0x1p-60f && q < 0x1p100f) {
+            safe += q;
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < N; ++j) {
+                float y = x[0];
+#pragma unroll
+                for (int l = 1; l < N; ++l) y = l == j ? x[l] : y;
+                if (y != 0.f) rest += (double)y * (double)y;
+            }
+        }
+    }
+    // over the lanes of a warp
+    __device__ __forceinline__ void join() {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) safe += __shfl_xor_sync(0xffffffffu, safe, d);
+        if (__any_sync(0xffffffffu, rest != 0.0)) {
+#pragma unroll
+            for (int d = 16; d; d >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, d);
+        }
+    }
+};
 // 2^10 / sqrt(sum of squares) in three factors that neither overflow nor underflow (the norm is anywhere from 2^-149 on):
-// zeros for a matrix of zeros, NaN where the norm is not finite.
-__device__ __forceinline__ void orth_factors(double sum, float *factor) {
-    const double n = sqrt(sum);
-    factor[0] = factor[1] = factor[2] = n == 0.0 ? 0.f : __int_as_float(0x7fffffff);
-    if (n == 0.0 || !isfinite(n)) return;
+// zeros for a matrix of zeros, NaN where the norm is not finite.  (Exponent and mantissa by hand, the root in fp32 with one
+// step of Newton, good to 2^-23: in fp64 it took some thousand clocks, which in a small matrix everyone waits for.)
+__device__ __forceinline__ void orth_factors(const SquareSum &s, float &f0, float &f1, float &f2) {
     int x;
-    const double f = frexp(n, &x);
-    const int k = 10 - x;
-    factor[0] = ldexpf(1.f, k / 2);
-    factor[1] = ldexpf(1.f, k - k / 2);
-    factor[2] = (float)(1.0 / f);
+    float m;  // sum = m 2^x, m in [1, 4), x even
+    if (s.rest == 0.0 && s.safe > 0x1p-100f && s.safe < 0x1p120f) {
+        const int bits = __float_as_int(s.safe);
+        x = (bits >> 23) - 127;
+        x -= x & 1;
+        m = __int_as_float(bits - (x << 23));
+    } else {
+        const double sum = (double)s.safe + s.rest;
+        if (!(sum > 0.0) || sum > 1e300) {
+            f0 = f1 = f2 = sum == 0.0 ? 0.f : __int_as_float(0x7fffffff);
+            return;
+        }
+        const long long bits = __double_as_longlong(sum);
+        x = (int)(bits >> 52) - 1023;  // (squares of fp32 numbers are normal fp64 numbers)
+        x -= x & 1;
+        m = (float)__longlong_as_double(bits - ((long long)x << 52));
+    }
+    float r = rsqrtf(m);
+    r = r * fmaf(-0.5f * m * r, r, 1.5f);
+    const int k = 10 - x / 2, h = k / 2;
+    f0 = __int_as_float((127 + h) << 23);
+    f1 = __int_as_float((127 + k - h) << 23);
+    f2 = r;
 }
 #endif
 // wide: tiles of 256 x 256, else 256 x 128

@@ -810,7 +810,7 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         auto lines = [](size_t n) { return (n + 255) / 256 * 256; };
         const bool split = q.splits[0] > 1 || q.splits[1] > 1 || q.splits[2] > 1;
         const size_t arrived = split ? lines((size_t)pairs * 16 * 4) : 0, parts = split ? (size_t)pairs * 256 * w * 4 : 0;
-        const size_t done = lines((size_t)d->batch * 4), partial = lines((size_t)d->batch * p.most_parts * 8),
+        const size_t done = lines((size_t)d->batch * 4), partial = lines((size_t)d->batch * p.most_parts * 16),
                      whole = lines((size_t)d->batch * d->rows * p.pitch * 2), square = lines((size_t)d->batch * g * q.pitch_gram * 2);
         p.dev.counters = 256 + arrived;
         const conv_bwd_status st = p.dev.init(256 + arrived + parts + done + partial + 4 * whole + 4 * square);
