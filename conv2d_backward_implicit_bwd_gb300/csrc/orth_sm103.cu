@@ -5,8 +5,9 @@
 //   gram     A = X X^T                  or X^T X
 //   square   B = c A A + b A + a I
 //   product  X' = B X                   or X B
-// three products a step; the first two are symmetric: tiles below the diagonal blocks are not computed but written
-// transposed from those above.
+// three products a step; the first two are symmetric: of their results only the blocks of 256 from the diagonal on are
+// computed and kept, and where an operand lies below it the block above is read across.  (Written transposed as well, each
+// tile took 2 to 5 us longer.)
 //
 // Schedule.  One cooperative launch does all the products: a list of tiles in order of step, product, matrix; pair b of P
 // takes tiles b, b + P, ...  A tile begins when its matrix's tiles of the product before are done (a counter for each
@@ -54,6 +55,8 @@ constexpr int EPI = 8, LOAD_A = 8, LOAD_B = 9, MMA = 10, THREADS = 512;
 constexpr int A_BYTES = 128 * 64 * 2;  // of one plane of a stage
 constexpr int OUT_BYTES = EPI * 4096;
 constexpr int MOST_STAGES = 4;
+constexpr int READY = 8;  // more than the pieces that the A loads can be ahead of the epilogue (a piece fills a stage at least)
+static_assert(READY > MOST_STAGES + 2, "a barrier is not used again before everyone has seen it");
 
 template <int W>
 struct Cfg {
@@ -63,6 +66,7 @@ struct Cfg {
 };
 struct Bars {
     uint64_t full[MOST_STAGES], empty[MOST_STAGES], tfull[2], tempty[2];
+    uint64_t ready[READY];  // the operands of a piece are there, pieces in turn
     uint32_t tmem;
     int32_t abort;
 };
@@ -118,6 +122,10 @@ __device__ __forceinline__ Work work_at(const OrthParams &p, int i) {
     w.kb1 = (int)((int64_t)kblocks * (w.split + 1) / splits);
     return w;
 }
+// Whether an operand's lines run across the contraction in its k-block kb: x in two of the products, and the symmetric
+// matrices, of which only the blocks of 256 from the diagonal on are there, below it.
+__device__ __forceinline__ bool a_across(const Work &w, bool high, int kb) { return w.kind == GRAM ? high : (w.kind == SQUARE || !high) && (kb >> 2) < (w.m0 >> 8); }
+__device__ __forceinline__ bool b_across(const Work &w, bool high, int kb) { return w.kind == GRAM ? high : w.kind == SQUARE || high ? (kb >> 2) < (w.n0 >> 8) : true; }
 // warps that have finished with matrix e before w's operands are there
 __device__ __forceinline__ int needed(const OrthParams &p, const Work &w) {
     return 2 * EPI * (w.step * (2 * p.tiles_sym + p.tiles_all) + w.kind * p.tiles_sym);
@@ -155,9 +163,9 @@ __device__ __forceinline__ void store_box(const CUtensorMap *map, uint32_t src, 
     bulk_commit();
 }
 
-// One warp's 32 rows x COLS columns of a tile, in registers, to the planes hi and lo (and transposed).
+// One warp's 32 rows x COLS columns of a tile, in registers, to the planes hi and lo.
 template <int COLS>
-__device__ __forceinline__ void store_planes(const CUtensorMap *out, const CUtensorMap *out_t, const Work &w, const float (&v)[COLS], uint8_t *slab, int row, int col, int lane) {
+__device__ __forceinline__ void store_planes(const CUtensorMap *out, const Work &w, const float (&v)[COLS], uint8_t *slab, int row, int col, int lane) {
     const uint32_t sb = smem_u32(slab);
 #pragma unroll
     for (int g = 0; g < COLS / 64; ++g)
@@ -178,19 +186,6 @@ __device__ __forceinline__ void store_planes(const CUtensorMap *out, const CUten
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0 && row < w.M && col + g * 64 < w.N) store_box(out + plane, sb, col + g * 64, row, w.e);
-            if (!out_t) continue;
-            if (lane == 0) bulk_wait_read();
-            __syncwarp();
-#pragma unroll
-            for (int q = 0; q < 32; ++q) {
-                const float x = v[g * 64 + 2 * q], y = v[g * 64 + 2 * q + 1];
-                const uint32_t u = plane ? pack_lo(x, y) : pack_hi(x, y);
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(sb + (uint32_t)(2 * q) * 64u + (uint32_t)lane * 2u), "h"((uint16_t)u) : "memory");
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(sb + (uint32_t)(2 * q + 1) * 64u + (uint32_t)lane * 2u), "h"((uint16_t)(u >> 16)) : "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && row < w.M && col + g * 64 < w.N) store_box(out_t + plane, sb, row, col + g * 64, w.e);
         }
 }
 
@@ -248,31 +243,39 @@ __device__ __forceinline__ void store_result(const OrthParams &p, const Work &w,
 template <int COLS>
 __device__ __forceinline__ bool join_splits(const OrthParams &p, const Work &w, float (&sum)[COLS], int splits, int slice, int lane) {
     const int tiles = w.kind == PRODUCT ? p.tiles_all : p.tiles_sym, tile = w.e * tiles + w.tile;
-    float4 *first = p.parts + (int64_t)(tile * splits) * (2 * EPI * 32 * COLS / 4) + slice * (32 * COLS / 4) + lane;
     constexpr int STEP = 2 * EPI * 32 * COLS / 4;
-    float4 *mine = first + (int64_t)w.split * STEP;
+    float4 *first = p.parts + (int64_t)(tile * splits) * STEP + slice * (32 * COLS / 4) + lane;
 #pragma unroll
-    for (int q = 0; q < COLS / 4; ++q) __stcg(mine + q * 32, make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]));
-    __threadfence();
+    for (int q = 0; q < COLS / 4; ++q) __stcg(first + w.split * STEP + q * 32, make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]));
     __syncwarp();
     int32_t *counter = p.arrived + tile * 2 * EPI + slice;
     int before = 0;
-    if (lane == 0) before = atomicAdd(counter, 1);
+    if (lane == 0) asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
     before = __shfl_sync(0xffffffffu, before, 0);
     if (before != splits - 1) return false;
-    __threadfence();
     if (lane == 0) *counter = 0;
+    // 32 columns of all pieces at once, so that one latency covers them
 #pragma unroll
-    for (int q = 0; q < COLS; ++q) sum[q] = 0.f;
-    for (int k = 0; k < splits; ++k) {
-        const float4 *from = first + (int64_t)k * STEP;
+    for (int g = 0; g < COLS / 32; ++g) {
+        float4 x[kOrthSplits][8];
 #pragma unroll
-        for (int q = 0; q < COLS / 4; ++q) {
-            const float4 x = __ldcg(from + q * 32);
-            sum[4 * q] += x.x;
-            sum[4 * q + 1] += x.y;
-            sum[4 * q + 2] += x.z;
-            sum[4 * q + 3] += x.w;
+        for (int k = 0; k < kOrthSplits; ++k)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[k][q] = k < splits ? __ldcg(first + k * STEP + (g * 8 + q) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float4 t = x[0][q];
+#pragma unroll
+            for (int k = 1; k < kOrthSplits; ++k) {
+                t.x += x[k][q].x;
+                t.y += x[k][q].y;
+                t.z += x[k][q].z;
+                t.w += x[k][q].w;
+            }
+            sum[g * 32 + 4 * q] = t.x;
+            sum[g * 32 + 4 * q + 1] = t.y;
+            sum[g * 32 + 4 * q + 2] = t.z;
+            sum[g * 32 + 4 * q + 3] = t.w;
         }
     }
     return true;
@@ -290,7 +293,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
 
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0, high = p.rows > p.cols;
-    const uint32_t full0 = smem_u32(bars.full), empty0 = smem_u32(bars.empty), tfull0 = smem_u32(bars.tfull), tempty0 = smem_u32(bars.tempty);
+    const uint32_t full0 = smem_u32(bars.full), empty0 = smem_u32(bars.empty), tfull0 = smem_u32(bars.tfull), tempty0 = smem_u32(bars.tempty), ready0 = smem_u32(bars.ready);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int pair = blockIdx.x / 2, npairs = gridDim.x / 2, total = p.items;
 
@@ -303,6 +306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
             mbar_init(tfull0 + 8 * b, 1);
             mbar_init(tempty0 + 8 * b, 2 * EPI);  // epilogue warps of both CTAs
         }
+        for (int i = 0; i < READY; ++i) mbar_init(ready0 + 8 * i, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -310,6 +314,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
     if (warp == MMA) {
         tmem_alloc2(smem_u32(&bars.tmem), 512);
         tc_fence_before();
+    }
+    if (warp == LOAD_A) {  // every map that the steps load by: they stand together
+        const CUtensorMap *m = &p.x_gram_a[0][0];
+        if (lane < kOrthLoadMaps) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m + lane)) : "memory");
+        __syncwarp();
     }
     cluster_sync_all();
     tc_fence_after();
@@ -326,11 +335,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
         const uint32_t tempty_leader0 = mapa_shared(tempty0, 0);
         const uint32_t lane_base = tmem_base + ((uint32_t)((warp % 4) * 32) << 16);
         uint8_t *slab = stage + warp * 4096;
-        uint32_t use = 0;
+        uint32_t use = 0, piece = 0;
         bool ok = true;
-        for (int i = pair; i < total; i += npairs) {
+        for (int i = pair; i < total; i += npairs, ++piece) {
             const Work w = work_at<W>(p, i);
             const int row = w.m0 + (int)rank * 128 + (warp % 4) * 32, col0 = (warp / 4) * COLS, col = w.n0 + col0;
+            // square adds to A: by other SMs in this launch, so past L1; narrow tiles have the registers to read it ahead
+            constexpr int AHEAD = W == 256 ? 1 : COLS / 8;
+            uint4 old_hi[AHEAD], old_lo[AHEAD];
+            auto old_at = [&](int plane, int q) {
+                const int r = row + lane, c = col + q * 8;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (r < w.M && c < p.pitch_gram) v = __ldcg(reinterpret_cast<const uint4 *>(p.gram[plane] + ((int64_t)w.e * w.M + r) * p.pitch_gram + c));
+                return v;
+            };
+            if (w.kind == SQUARE) {
+                if (ok) ok = mbar_wait_bounded(ready0 + 8 * (piece % READY), (piece / READY) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
+                ok = __all_sync(0xffffffffu, ok);
+                if constexpr (W != 256) {
+#pragma unroll
+                    for (int q = 0; q < AHEAD; ++q) {
+                        old_hi[q] = old_at(0, q);
+                        old_lo[q] = old_at(1, q);
+                    }
+                }
+            }
             float sum[COLS];
 #pragma unroll
             for (int q = 0; q < COLS; ++q) sum[q] = 0.f;
@@ -352,31 +381,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
             }
             if (!ok) continue;
             const int splits = w.kind == GRAM ? p.splits[0] : w.kind == SQUARE ? p.splits[1] : p.splits[2];
-            if (splits > 1 && !join_splits<COLS>(p, w, sum, splits, (int)rank * EPI + warp, lane)) continue;
+            if (W != 256 && splits > 1 && !join_splits<COLS>(p, w, sum, splits, (int)rank * EPI + warp, lane)) continue;
             const bool final = w.kind == PRODUCT && w.step + 1 == p.steps;
             if (w.kind == SQUARE) {
-                // c sum + b A + a on the diagonal; A by other SMs in this launch: past L1
+                // c sum + b A + a on the diagonal
                 const float a = p.coef[3 * w.step] * kOrthUpPoly, b = p.coef[3 * w.step + 1] * (kOrthUpPoly / kOrthUp), c = p.coef[3 * w.step + 2] * (kOrthUpPoly / (kOrthUp * kOrthUp));
                 const int r = row + lane;
-                const int64_t at = ((int64_t)w.e * w.M + r) * p.pitch_gram;
-                ok = __all_sync(0xffffffffu, wait_done(p, w, abort_flag, kDevTimeoutEpilogue));
-                if (!ok) continue;
 #pragma unroll
                 for (int q = 0; q < COLS / 8; ++q) {
-                    const int cc = col + q * 8;
-                    uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
-                    if (r < w.M && cc < p.pitch_gram) {
-                        h = __ldcg(reinterpret_cast<const uint4 *>(p.gram[0] + at + cc));
-                        l = __ldcg(reinterpret_cast<const uint4 *>(p.gram[1] + at + cc));
-                    }
+                    const uint4 h = W == 256 ? old_at(0, q) : old_hi[q % AHEAD], l = W == 256 ? old_at(1, q) : old_lo[q % AHEAD];
                     const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&hw[k])), y = __half22float2(*reinterpret_cast<const __half2 *>(&lw[k]));
                         float &s0 = sum[q * 8 + 2 * k], &s1 = sum[q * 8 + 2 * k + 1];
-                        s0 = fmaf(c, s0, b * (x.x + y.x)) + (r == cc + 2 * k ? a : 0.f);
-                        s1 = fmaf(c, s1, b * (x.y + y.y)) + (r == cc + 2 * k + 1 ? a : 0.f);
+                        s0 = fmaf(c, s0, b * (x.x + y.x));
+                        s1 = fmaf(c, s1, b * (x.y + y.y));
                     }
+                }
+                if (col < row + 32 && row < col + COLS) {  // the diagonal's warps
+#pragma unroll
+                    for (int q = 0; q < COLS; ++q) sum[q] += r == col + q ? a : 0.f;
                 }
             } else {
                 const float mul = w.kind == GRAM ? 1.f / kOrthUp : final ? 1.f / (kOrthUp * kOrthUpPoly) : 1.f / kOrthUpPoly;
@@ -387,9 +412,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                 store_result<COLS>(p, w, sum, slab, row, col, lane);
                 continue;
             }
-            const bool mirror = w.kind != PRODUCT && w.n0 >= w.m0 + 256;
             const CUtensorMap *out = w.kind == GRAM ? p.gram_store : w.kind == SQUARE ? p.poly_store : (w.step & 1) ? p.x_store[0] : p.x_store[1];
-            store_planes<COLS>(out, !mirror ? nullptr : w.kind == GRAM ? p.gram_store_t : p.poly_store_t, w, sum, slab, row, col, lane);
+            store_planes<COLS>(out, w, sum, slab, row, col, lane);
             // written, and known to be
             if (lane == 0) {
                 bulk_wait_all();
@@ -404,21 +428,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
             // ------------------------------------------------------------ loads
             if (lane == 0) {
                 const uint32_t full_leader0 = mapa_shared(full0, 0);
-                uint32_t it = 0;
+                uint32_t it = 0, piece = 0;
                 bool ok = true, issued = false;
-                for (int i = pair; i < total && ok; i += npairs) {
+                for (int i = pair; i < total && ok; i += npairs, ++piece) {
                     const Work w = work_at<W>(p, i);
                     const int m = w.m0 + (int)rank * 128, n = w.n0 + (int)rank * (w.n / 2), planes = w.step >= p.single_from ? 1 : 2;
-                    // what other SMs have written in this launch
-                    ok = wait_done(p, w, abort_flag, kDevTimeoutProducer);
+                    // What other SMs have written in this launch.  (One thread of a CTA asks for it: with every lane of the
+                    // epilogue asking too, loads and counters took 3 us longer.)
+                    const uint32_t bar_ready = ready0 + 8 * (piece % READY);
+                    ok = warp == LOAD_A ? wait_done(p, w, abort_flag, kDevTimeoutProducer)
+                                        : mbar_wait_bounded(bar_ready, (piece / READY) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
                     if (!ok) break;
+                    if (warp == LOAD_A) mbar_arrive(bar_ready);
                     fence_proxy_async_global();
-                    const CUtensorMap *map;
-                    if (warp == LOAD_A)
-                        map = w.kind == SQUARE ? p.gram_a : w.kind == GRAM ? p.x_gram_a[w.step & 1] : high ? p.x_prod[w.step & 1] : p.poly_prod;
-                    else
-                        map = w.kind == SQUARE ? p.gram_b : w.kind == GRAM ? p.x_gram_b[w.step & 1] : high ? p.poly_prod : p.x_prod[w.step & 1];
-                    const bool mn = warp == LOAD_A ? high && w.kind == GRAM : high ? w.kind == GRAM : w.kind == PRODUCT;
+                    // by lines along the contraction, and across it
+                    const CUtensorMap *along, *cross;
+                    if (warp == LOAD_A) {
+                        along = w.kind == SQUARE ? p.gram_a : w.kind == GRAM ? p.x_gram_a[w.step & 1] : high ? p.x_prod[w.step & 1] : p.poly_a;
+                        cross = w.kind == SQUARE ? p.gram_cross : w.kind == GRAM ? p.x_gram_a[w.step & 1] : p.poly_cross;
+                    } else {
+                        along = w.kind == SQUARE ? p.gram_b : w.kind == GRAM ? p.x_gram_b[w.step & 1] : p.poly_b;
+                        cross = w.kind == SQUARE ? p.gram_cross : w.kind == GRAM ? p.x_gram_b[w.step & 1] : high ? p.poly_cross : p.x_prod[w.step & 1];
+                    }
                     for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                         const uint32_t s = it % S, ph = (it / S) & 1;
                         if (!mbar_wait_bounded(empty0 + 8 * s, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) {
@@ -427,14 +458,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                         }
                         const uint32_t bar = full_leader0 + 8 * s, to = smem_u32(smem + s * C::STAGE);
                         if (warp == LOAD_A && leader) mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(2 * planes * (A_BYTES + C::B_BYTES)));
+                        const bool mn = warp == LOAD_A ? a_across(w, high, kb) : b_across(w, high, kb);
                         for (int k = 0; k < planes; ++k) {
                             const uint32_t dst = warp == LOAD_A ? to + k * A_BYTES : to + 2 * A_BYTES + k * C::B_BYTES;
-                            const int across = warp == LOAD_A ? m : n;
+                            const int at = warp == LOAD_A ? m : n;
                             if (!mn) {
-                                tma_load_3d_pair(dst, map + k, bar, kb * 64, across, w.e);
+                                tma_load_3d_pair(dst, along + k, bar, kb * 64, at, w.e);
                             } else {
-                                tma_load_3d_pair(dst, map + k, bar, across, kb * 64, w.e);
-                                if (warp == LOAD_A || W == 256) tma_load_3d_pair(dst + 8192, map + k, bar, across + 64, kb * 64, w.e);
+                                tma_load_3d_pair(dst, cross + k, bar, at, kb * 64, w.e);
+                                if (warp == LOAD_A || W == 256) tma_load_3d_pair(dst + 8192, cross + k, bar, at + 64, kb * 64, w.e);
                             }
                         }
                         issued = true;
@@ -453,10 +485,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
             bool ok = true, issued = false;
             for (int i = pair; i < total && ok; i += npairs) {
                 const Work w = work_at<W>(p, i);
-                const bool a_mn = high && w.kind == GRAM, b_mn = high ? w.kind == GRAM : w.kind == PRODUCT;
-                // fp16 operands, fp32 sums; a 16-deep step in 16 bytes; the leading offset of the descriptors
-                const uint32_t id = (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(w.n >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
-                const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2, a_lead = (a_mn ? 8192u >> 4 : 1u) << 16, b_lead = (b_mn ? 8192u >> 4 : 1u) << 16;
                 const bool single = w.step >= p.single_from;
                 for (int left = w.kb1 - w.kb0; left > 0 && ok;) {
                     const uint32_t b = use & 1, bph = (use >> 1) & 1, d = tmem_base + b * 256;
@@ -469,6 +497,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                     for (; left > end; --left) {
                         ok = __all_sync(0xffffffffu, mbar_wait_bounded(full0 + 8 * s, ph, p.wait_budget, abort_flag, p.status, kDevTimeoutMma));
                         if (!ok) break;
+                        const bool a_mn = a_across(w, high, w.kb1 - left), b_mn = b_across(w, high, w.kb1 - left);
+                        // fp16 operands, fp32 sums; a 16-deep step in 16 bytes; the leading offset of the descriptors
+                        const uint32_t id = (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(w.n >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+                        const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2, a_lead = (a_mn ? 8192u >> 4 : 1u) << 16, b_lead = (b_mn ? 8192u >> 4 : 1u) << 16;
                         const uint32_t ad = (a_at + s * (C::STAGE >> 4)) | a_lead, bd = (b_at + s * (C::STAGE >> 4)) | b_lead;
                         if (!single) {
 #pragma unroll

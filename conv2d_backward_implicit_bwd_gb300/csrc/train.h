@@ -183,11 +183,13 @@ struct OrthPrepParams {
 };
 cudaError_t launch_orth_prep(const OrthPrepParams &p, bool by_four, cudaStream_t s);
 // All the products.  Maps: [2] planes hi, lo; x has two buffers.
-constexpr int kOrthMostSteps = 64;
+constexpr int kOrthMostSteps = 64, kOrthLoadMaps = 24;
+constexpr int kOrthSplits = 3;  // most pieces of a tile's contraction
 constexpr float kOrthUp = 1024.f, kOrthUpPoly = 256.f;  // what the planes' values are multiplied by
 struct OrthParams {
-    CUtensorMap x_gram_a[2][2], x_gram_b[2][2], x_prod[2][2], x_store[2][2];
-    CUtensorMap gram_a[2], gram_b[2], gram_store[2], gram_store_t[2], poly_prod[2], poly_store[2], poly_store_t[2];
+    CUtensorMap x_gram_a[2][2], x_gram_b[2][2], x_prod[2][2];
+    CUtensorMap gram_a[2], gram_b[2], gram_cross[2], poly_a[2], poly_b[2], poly_cross[2];
+    CUtensorMap x_store[2][2], gram_store[2], poly_store[2];
     const __half *gram[2];
     void *result;                  // the result, or the step on the weights
     float *weight;

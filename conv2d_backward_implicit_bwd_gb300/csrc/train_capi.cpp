@@ -194,7 +194,7 @@ struct conv_bwd_logp_plan_s {
 
 struct conv_bwd_orth_plan_s {
     struct Plane {  // tensor maps of one plane of a matrix, of both tile widths
-        CUtensorMap rows128, rows64, store, store_t;
+        CUtensorMap rows128, rows64, store;
     };
     struct Matrix {
         __half *at[2] = {};
@@ -745,15 +745,14 @@ conv_bwd_status conv_bwd_logp_get_status(conv_bwd_logp_plan p, void *stream, int
 // ---- orthogonalised updates -------------------------------------------------------
 // A plane [batch][rows][pitch] of fp16 as the products read and write it.
 static bool map_plane(CUtensorMap *m, void *at, int64_t batch, int64_t rows, int64_t cols, int64_t pitch, uint32_t box_cols,
-                      uint32_t box_rows, bool swizzled) {
+                      uint32_t box_rows) {
     EncodeTiled enc = encode_tiled();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
     cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)pitch * (cuuint64_t)rows * 2};
     cuuint32_t box[3] = {box_cols, box_rows, 1}, one[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, at, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_plan *out) {
@@ -799,8 +798,10 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         const int64_t w = p.wide ? 256 : 128;
         q.tiles_sym = (int32_t)tiles_sym(w);
         q.tiles_all = (int32_t)tiles_all(w);
-        // pieces of a contraction: as many as the pairs that would else be idle, of four k-blocks at least
-        auto splits = [&](int64_t tiles, int64_t depth) { return (int32_t)std::max<int64_t>(1, std::min(pairs / (tiles * d->batch), (depth + 63) / 64 / 4)); };
+        // Pieces of a contraction: where pairs would else be idle, and of eight k-blocks at least.  (A k-block takes 0.6 us, the
+        // joining of pieces 3.  1000 x 1000 in pieces of eight 216 us, of five 213, whole 235; 300 x 513 whole 143, in pieces of
+        // four 149; 200 x 2000 in pieces of eight 152, whole 177.)
+        auto splits = [&](int64_t tiles, int64_t depth) { return (int32_t)std::max<int64_t>(1, std::min({pairs / (tiles * d->batch), (depth + 63) / 64 / 8, (int64_t)kOrthSplits})); };
         q.splits[0] = splits(q.tiles_sym, h);
         q.splits[1] = splits(q.tiles_sym, g);
         q.splits[2] = splits(q.tiles_all, g);
@@ -829,10 +830,9 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
             for (int i = 0; i < 2; ++i, at += bytes) {
                 m.at[i] = reinterpret_cast<__half *>(at);
                 auto &q = m.plane[i];
-                ok = ok && map_plane(&q.rows128, at, d->batch, rows, cols, pitch, 64, 128, true) &&
-                     map_plane(&q.rows64, at, d->batch, rows, cols, pitch, 64, 64, true) &&
-                     map_plane(&q.store, at, d->batch, rows, cols, pitch, 64, 32, true) &&
-                     map_plane(&q.store_t, at, d->batch, rows, cols, pitch, 32, 64, false);
+                ok = ok && map_plane(&q.rows128, at, d->batch, rows, cols, pitch, 64, 128) &&
+                     map_plane(&q.rows64, at, d->batch, rows, cols, pitch, 64, 64) &&
+                     map_plane(&q.store, at, d->batch, rows, cols, pitch, 64, 32);
             }
         };
         place(p.x[0], d->rows, d->cols, p.pitch, whole);
@@ -849,14 +849,16 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
                 q.x_prod[k][i] = high ? x.rows128 : x.rows64;
                 q.x_store[k][i] = x.store;
             }
+            const auto &gram = p.gram.plane[i], &poly = p.poly.plane[i];
             q.gram[i] = p.gram.at[i];
-            q.gram_a[i] = p.gram.plane[i].rows128;
-            q.gram_b[i] = p.wide ? p.gram.plane[i].rows128 : p.gram.plane[i].rows64;
-            q.gram_store[i] = p.gram.plane[i].store;
-            q.gram_store_t[i] = p.gram.plane[i].store_t;
-            q.poly_prod[i] = high && !p.wide ? p.poly.plane[i].rows64 : p.poly.plane[i].rows128;
-            q.poly_store[i] = p.poly.plane[i].store;
-            q.poly_store_t[i] = p.poly.plane[i].store_t;
+            q.gram_a[i] = gram.rows128;
+            q.gram_b[i] = p.wide ? gram.rows128 : gram.rows64;
+            q.gram_cross[i] = gram.rows64;
+            q.gram_store[i] = gram.store;
+            q.poly_a[i] = poly.rows128;
+            q.poly_b[i] = p.wide ? poly.rows128 : poly.rows64;
+            q.poly_cross[i] = poly.rows64;
+            q.poly_store[i] = poly.store;
         }
         q.status = p.dev.status();
         q.wait_budget = (int64_t)p.dev.clock_khz * 2000;
