@@ -43,6 +43,7 @@
 
 #include "device_util.cuh"
 #include "internal.h"
+#include "rows_io.cuh"
 #include "tc_common.cuh"
 #include "tc_pair.cuh"
 #include "train.h"
@@ -568,21 +569,11 @@ cudaError_t launch_steps(const OrthParams &p, int pairs, cudaStream_t s) {
 }
 
 // ---- what comes before the products --------------------------------------------
-// Elements four at a time where every row starts on four elements' bytes, else one at a time.
-__device__ __forceinline__ float load1(const void *x, int64_t i, bool bf16) {
-    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(x)[i]) : static_cast<const float *>(x)[i];
-}
-__device__ __forceinline__ float4 load4(const void *x, int64_t i, bool bf16) {
-    if (!bf16) return *reinterpret_cast<const float4 *>(static_cast<const float *>(x) + i);
-    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(x) + i);
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
-
 constexpr int NT = 256;
 
 // Squares of u, summed by block; the momentum is updated on the way.  u = g without momentum, else m' = beta m + g and u =
 // g + beta m' (nesterov) or m'.
-template <int V>
+template <int V, bool LINES, bool BF16>
 __global__ void __launch_bounds__(NT) orth_norm_kernel(const OrthPrepParams p) {
     __shared__ double part[NT / 32][2];
     pdl_next();
@@ -596,27 +587,16 @@ __global__ void __launch_bounds__(NT) orth_norm_kernel(const OrthPrepParams p) {
         const int r = (int)(i / per_row), c = (int)(i - (int64_t)r * per_row) * V;
         const int64_t at = (int64_t)e * p.ls + (int64_t)r * p.ld + c;
         float g[V], m[V];
-        if constexpr (V == 4) {
-            const float4 x = load4(p.grad, at, p.bf16);
-            g[0] = x.x, g[1] = x.y, g[2] = x.z, g[3] = x.w;
-        } else {
-            g[0] = load1(p.grad, at, p.bf16);
-        }
+        load_v<V, LINES, BF16>(p.grad, at, g);
         if (p.momentum) {
-            float *to = p.momentum + ((int64_t)e * p.rows + r) * p.cols + c;
-            if constexpr (V == 4)
-                *reinterpret_cast<float4 *>(m) = *reinterpret_cast<const float4 *>(to);
-            else
-                m[0] = *to;
+            const int64_t to = ((int64_t)e * p.rows + r) * p.cols + c;
+            load_v<V, LINES, false>(p.momentum, to, m);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 m[k] = fmaf(p.beta, m[k], g[k]);
                 g[k] = p.nesterov ? fmaf(p.beta, m[k], g[k]) : m[k];
             }
-            if constexpr (V == 4)
-                *reinterpret_cast<float4 *>(to) = *reinterpret_cast<const float4 *>(m);
-            else
-                *to = m[0];
+            store_v<V, LINES, false>(p.momentum, to, m);
         }
         sum.add(g);
     }
@@ -634,7 +614,7 @@ __global__ void __launch_bounds__(NT) orth_norm_kernel(const OrthPrepParams p) {
 }
 
 // X = u 2^10 / |u| as hi + lo.  A matrix of zeros stays one; one whose norm is not finite becomes NaN throughout.
-template <int V>
+template <int V, bool LINES, bool BF16>
 __global__ void __launch_bounds__(NT) orth_split_kernel(const OrthPrepParams p) {
     __shared__ float factor[3];
     pdl_next();
@@ -657,21 +637,12 @@ __global__ void __launch_bounds__(NT) orth_split_kernel(const OrthPrepParams p) 
     for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < items; i += (int64_t)gridDim.x * NT) {
         const int r = (int)(i / per_row), c = (int)(i - (int64_t)r * per_row) * V;
         const int64_t at = (int64_t)e * p.ls + (int64_t)r * p.ld + c;
-        float g[V];
-        const float *from = p.momentum ? p.momentum + ((int64_t)e * p.rows + r) * p.cols + c : nullptr;
-        const bool grad = !from || p.nesterov;
-        if constexpr (V == 4) {
-            const float4 x = grad ? load4(p.grad, at, p.bf16) : make_float4(0.f, 0.f, 0.f, 0.f);
-            g[0] = x.x, g[1] = x.y, g[2] = x.z, g[3] = x.w;
-        } else {
-            g[0] = grad ? load1(p.grad, at, p.bf16) : 0.f;
-        }
-        if (from) {
-            float m[V];
-            if constexpr (V == 4)
-                *reinterpret_cast<float4 *>(m) = *reinterpret_cast<const float4 *>(from);
-            else
-                m[0] = *from;
+        float g[V], m[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) g[k] = 0.f;
+        if (!p.momentum || p.nesterov) load_v<V, LINES, BF16>(p.grad, at, g);
+        if (p.momentum) {
+            load_v<V, LINES, false>(p.momentum, ((int64_t)e * p.rows + r) * p.cols + c, m);
 #pragma unroll
             for (int k = 0; k < V; ++k) g[k] = p.nesterov ? fmaf(p.beta, m[k], g[k]) : m[k];
         }
@@ -689,9 +660,8 @@ __global__ void __launch_bounds__(NT) orth_split_kernel(const OrthPrepParams p) 
     }
 }
 
-}  // namespace
-
-cudaError_t launch_orth_prep(const OrthPrepParams &p, bool by_four, cudaStream_t s) {
+template <int V, bool LINES, bool BF16>
+cudaError_t launch_prep(const OrthPrepParams &p, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.parts, (unsigned)p.batch);
     cfg.blockDim = dim3(NT);
@@ -701,9 +671,17 @@ cudaError_t launch_orth_prep(const OrthPrepParams &p, bool by_four, cudaStream_t
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = by_four ? cudaLaunchKernelEx(&cfg, orth_norm_kernel<4>, p) : cudaLaunchKernelEx(&cfg, orth_norm_kernel<1>, p);
-    if (e != cudaSuccess) return e;
-    return by_four ? cudaLaunchKernelEx(&cfg, orth_split_kernel<4>, p) : cudaLaunchKernelEx(&cfg, orth_split_kernel<1>, p);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, orth_norm_kernel<V, LINES, BF16>, p);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, orth_split_kernel<V, LINES, BF16>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_orth_prep(const OrthPrepParams &p, cudaStream_t s) {
+    const bool lines = rows_on_lines(p.bf16, {p.grad}, {p.momentum}, nullptr, p.ld | p.ls);
+    if (p.cols % 4) return p.bf16 ? launch_prep<1, false, true>(p, s) : launch_prep<1, false, false>(p, s);
+    if (lines) return p.bf16 ? launch_prep<4, true, true>(p, s) : launch_prep<4, true, false>(p, s);
+    return p.bf16 ? launch_prep<4, false, true>(p, s) : launch_prep<4, false, false>(p, s);
 }
 
 // Pairs of SMs that can be resident at once.

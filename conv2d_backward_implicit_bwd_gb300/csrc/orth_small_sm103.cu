@@ -22,6 +22,7 @@
 
 #include "device_util.cuh"
 #include "internal.h"
+#include "rows_io.cuh"
 #include "tc_common.cuh"
 #include "train.h"
 
@@ -73,10 +74,10 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 __device__ __forceinline__ uint32_t desc(uint32_t addr, uint32_t lead) { return ((addr >> 4) & 0x3FFFu) | lead << 16; }
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-__device__ __forceinline__ float load1(const void *x, int64_t i, bool bf16) {
-    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(x)[i]) : static_cast<const float *>(x)[i];
-}
-
+// V: elements that a thread takes at a time along the caller's rows, by rows_io.cuh.
+// (Loads beyond the slice's end take an element inside: with a branch at each the loads waited for one another, 5 thousand
+// clocks for 13 thousand elements.)
+template <int V, bool LINES, bool BF16>
 __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sx = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023)), *sg = sx + 2 * X_PLANE;
@@ -115,40 +116,52 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
     const int inner = high ? g : valid, outer = high ? valid : g;  // of the slice: along the caller's rows, across them
     const int row0 = high ? col0 : 0, left = high ? 0 : col0;      // its corner in the caller's matrix
     const int64_t corner = ((int64_t)e * p.rows + row0) * p.cols + left, given = (int64_t)e * p.ls + (int64_t)row0 * p.ld + left;
-    // The sum of squares, an element at a time along the caller's rows.
-    constexpr int U = 8;  // loads of a thread in flight
+    if (p.weight)  // needed last, and from memory: on its way to L2 meanwhile
+        for (int i = tid; i < outer; i += NT)
+            for (int k = 0; k < inner; k += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.weight + corner + (int64_t)i * p.cols + k));
+    // The sum of squares, along the caller's rows.
+    constexpr int U = 8 / V;  // loads of a thread in flight
     SquareSum sum = {0.f, 0.0};
     {
-        const int items = inner * outer, over = inner ? NT / inner : 0, rest = inner ? NT % inner : 0;
-        int o = inner ? tid / inner : 0, k = inner ? tid % inner : 0;
+        const int fast = inner / V, items = fast * outer, over = fast ? NT / fast : 0, rest = fast ? NT % fast : 0;
+        const int k0 = fast ? tid % fast : 0, o0 = fast ? tid / fast : 0;
+        int k = k0, o = o0;
 #pragma unroll 1
         for (int i0 = tid; i0 < items; i0 += U * NT) {
-            float x[U], m[U];
-            int64_t at[U];
+            float x[U][V], m[U][V];
+            int to[U];  // (a slice of a small matrix)
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                x[j] = m[j] = 0.f;
-                at[j] = corner + (int64_t)o * p.cols + k;
-                if (i0 + j * NT < items) {
-                    x[j] = load1(p.grad, given + (int64_t)o * p.ld + k, p.in_bf16);
-                    if (p.momentum) m[j] = p.momentum[at[j]];
-                }
+#pragma unroll
+                for (int l = 0; l < V; ++l) x[j][l] = m[j][l] = 0.f;
+                const bool there = i0 + j * NT < items;
+                to[j] = there ? o * p.cols + k * V : 0;
+                load_v<V, LINES, BF16>(p.grad, there ? given + (int64_t)o * p.ld + k * V : given, x[j]);
+                if (p.momentum) load_v<V, LINES, false>(p.momentum, corner + to[j], m[j]);
+#pragma unroll
+                for (int l = 0; l < V; ++l) x[j][l] = there ? x[j][l] : 0.f, m[j][l] = there ? m[j][l] : 0.f;
                 o += over;
                 k += rest;
-                if (k >= inner) {
-                    k -= inner;
+                if (k >= fast) {
+                    k -= fast;
                     ++o;
                 }
             }
             if (p.momentum) {
 #pragma unroll
                 for (int j = 0; j < U; ++j) {
-                    m[j] = fmaf(p.beta, m[j], x[j]);
-                    x[j] = p.nesterov ? fmaf(p.beta, m[j], x[j]) : m[j];
-                    if (i0 + j * NT < items) p.momentum[at[j]] = m[j];
+#pragma unroll
+                    for (int l = 0; l < V; ++l) {
+                        m[j][l] = fmaf(p.beta, m[j][l], x[j][l]);
+                        x[j][l] = p.nesterov ? fmaf(p.beta, m[j][l], x[j][l]) : m[j][l];
+                    }
+                    if (i0 + j * NT < items) store_v<V, LINES, false>(p.momentum, corner + to[j], m[j]);
                 }
             }
-            sum.add(x);
+            float all[U * V];
+#pragma unroll
+            for (int j = 0; j < U * V; ++j) all[j] = x[j / V][j % V];
+            sum.add(all);
         }
     }
     sum.join();
@@ -175,30 +188,13 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
     }
     float f0, f1, f2;
     orth_factors(sum, f0, f1, f2);
-    // The planes, eight columns of a row at a time, neighbouring threads along the caller's rows.
+    // The planes, eight columns of a row at a time (of V rows where the caller's rows are X's columns), neighbouring threads
+    // along the caller's rows.
     {
-        const int chunks = (valid + 7) / 8, fast = high ? g : chunks, items = g * chunks;
-        const int64_t next_in = high ? p.ld : 1, next_m = high ? p.cols : 1;
-#pragma unroll 1
-        for (int i = tid; i < items; i += NT) {
-            const int s = i / fast, f = i - s * fast, r = high ? f : s, cc = (high ? s : f) * 8;
-            const int o = high ? cc : r, k = high ? r : cc;
-            const int64_t in = given + (int64_t)o * p.ld + k, at = corner + (int64_t)o * p.cols + k;
-            float x[8], m[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = m[j] = 0.f;
-                if (cc + j < valid) {
-                    if (!p.momentum || p.nesterov) x[j] = load1(p.grad, in + j * next_in, p.in_bf16);
-                    if (p.momentum) m[j] = __ldcg(p.momentum + at + j * next_m);  // (written by another thread of this CTA)
-                }
-            }
+        const int chunks = (valid + 7) / 8, fast = high ? g / V : chunks, items = high ? fast * chunks : g * chunks;
+        auto value = [&](const float x, const float m) { return (p.momentum ? (p.nesterov ? fmaf(p.beta, m, x) : m) : x) * f0 * f1 * f2; };
+        auto put = [&](int r, int cc, const float (&x)[8]) {
             uint32_t h[4], l[4];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (p.momentum) x[j] = p.nesterov ? fmaf(p.beta, m[j], x[j]) : m[j];
-                x[j] = x[j] * f0 * f1 * f2;
-            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 h[j] = pack_hi(x[2 * j], x[2 * j + 1]);
@@ -207,6 +203,44 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
             const uint32_t to = chunk_at(r, cc);
             *reinterpret_cast<uint4 *>(sx + to) = make_uint4(h[0], h[1], h[2], h[3]);
             *reinterpret_cast<uint4 *>(sx + X_PLANE + to) = make_uint4(l[0], l[1], l[2], l[3]);
+        };
+        const bool grad = !p.momentum || p.nesterov;
+#pragma unroll 1
+        for (int i = tid; i < items; i += NT) {
+            const int s = i / fast, f = i - s * fast;
+            if (high) {
+                const int64_t in = given + (int64_t)s * 8 * p.ld + f * V, at = corner + (int64_t)s * 8 * p.cols + f * V;
+                float x[8][V], m[8][V];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                    for (int l = 0; l < V; ++l) x[j][l] = m[j][l] = 0.f;
+                    const int q = min(j, valid - 1 - s * 8);
+                    if (grad) load_v<V, LINES, BF16>(p.grad, in + q * p.ld, x[j]);
+                    if (p.momentum) load_fresh<V, LINES>(p.momentum + at + q * p.cols, m[j]);
+                }
+#pragma unroll
+                for (int l = 0; l < V; ++l) {
+                    float row[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) row[j] = s * 8 + j < valid ? value(x[j][l], m[j][l]) : 0.f;
+                    put(f * V + l, s * 8, row);
+                }
+            } else {
+                const int64_t in = given + (int64_t)s * p.ld + f * 8, at = corner + (int64_t)s * p.cols + f * 8;
+                float x[8 / V][V], m[8 / V][V], row[8];
+#pragma unroll
+                for (int j = 0; j < 8 / V; ++j) {
+#pragma unroll
+                    for (int l = 0; l < V; ++l) x[j][l] = m[j][l] = 0.f;
+                    const int q = min(j * V, valid - V - f * 8);
+                    if (grad) load_v<V, LINES, BF16>(p.grad, in + q, x[j]);
+                    if (p.momentum) load_fresh<V, LINES>(p.momentum + at + q, m[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) row[j] = f * 8 + j < valid ? value(x[j / V][j % V], m[j / V][j % V]) : 0.f;
+                put(s, f * 8, row);
+            }
         }
     }
 
@@ -397,35 +431,47 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
     __syncthreads();
     {
         const float *fx = reinterpret_cast<const float *>(sx);
-        const int chunks = (valid + 3) / 4, fast = high ? g : chunks, items = g * chunks;
-        const int64_t ld = p.weight ? p.cols : p.ldo, first = p.weight ? corner : (int64_t)e * p.lse + (int64_t)row0 * p.ldo + left, next = high ? ld : 1;
-#pragma unroll 2
-        for (int i = tid; ok && i < items; i += NT) {
-            const int s = i / fast, f = i - s * fast, r = high ? f : s, cc = (high ? s : f) * 4;
-            const float4 v = *reinterpret_cast<const float4 *>(fx + float_at(r, cc, width));
-            const float x[4] = {v.x, v.y, v.z, v.w};
-            const int64_t at = first + (int64_t)(high ? cc : r) * ld + (high ? r : cc);
+        const int64_t ld = p.weight ? p.cols : p.ldo, first = p.weight ? corner : (int64_t)e * p.lse + (int64_t)row0 * p.ldo + left;
+        // M vectors of a row or column, `step` apart, those before `many`; every load before the first store
+        auto put = [&](auto &x, int64_t at, int64_t step, int many) {
+            constexpr int M = sizeof(x) / sizeof(x[0]);
             if (p.weight) {
-                float was[4];
+                float w[M][V];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) was[j] = cc + j < valid ? p.weight[at + j * next] : 0.f;
+                for (int j = 0; j < M; ++j)
+                    load_v<V, LINES, false>(p.weight, at + min(j, many - 1) * step, w[j]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float n = fmaf(-p.rate, x[j], was[j] * p.keep);
-                    if (cc + j < valid) {
-                        p.weight[at + j * next] = n;
-                        if (p.copy) p.copy[at + j * next] = __float2bfloat16_rn(n);
-                    }
+                for (int j = 0; j < M; ++j) {
+                    if (j >= many) break;
+#pragma unroll
+                    for (int l = 0; l < V; ++l) w[j][l] = fmaf(-p.rate, x[j][l], w[j][l] * p.keep);
+                    store_v<V, LINES, false>(p.weight, at + j * step, w[j]);
+                    if (p.copy) store_v<V, LINES, true>(p.copy, at + j * step, w[j]);
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (cc + j >= valid) break;
-                    if (p.out_bf16)
-                        static_cast<__nv_bfloat16 *>(p.result)[at + j * next] = __float2bfloat16_rn(x[j]);
-                    else
-                        static_cast<float *>(p.result)[at + j * next] = x[j];
-                }
+                for (int j = 0; j < M; ++j)
+                    if (j < many) store_v<V, LINES, BF16>(p.result, at + j * step, x[j]);
+            }
+        };
+        // four columns of X at a time, of V rows
+        const int chunks = (valid + 3) / 4, fast = high ? g / V : chunks, items = high ? fast * chunks : g * chunks;
+#pragma unroll 4
+        for (int i = tid; ok && i < items; i += NT) {
+            const int s = i / fast, f = i - s * fast;
+            if (high) {
+                float x[V][4], y[4][V];
+#pragma unroll
+                for (int l = 0; l < V; ++l) *reinterpret_cast<float4 *>(x[l]) = *reinterpret_cast<const float4 *>(fx + float_at(f * V + l, s * 4, width));
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int l = 0; l < V; ++l) y[j][l] = x[l][j];
+                put(y, first + (int64_t)(s * 4) * ld + f * V, ld, valid - s * 4);
+            } else {
+                float y[4 / V][V];
+                *reinterpret_cast<float4 *>(y[0]) = *reinterpret_cast<const float4 *>(fx + float_at(s, f * 4, width));
+                put(y, first + (int64_t)s * ld + f * 4, V, (valid - f * 4 + V - 1) / V);
             }
         }
     }
@@ -436,14 +482,13 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
     }
 }
 
-}  // namespace
-
-cudaError_t launch_orth_small(const OrthSmallParams &p, cudaStream_t s) {
+template <int V, bool LINES, bool BF16>
+cudaError_t launch_small(const OrthSmallParams &p, cudaStream_t s) {
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64 || !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(orth_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(orth_small_kernel<V, LINES, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_set[dev] = true;
     }
@@ -460,7 +505,16 @@ cudaError_t launch_orth_small(const OrthSmallParams &p, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, orth_small_kernel, p);
+    return cudaLaunchKernelEx(&cfg, orth_small_kernel<V, LINES, BF16>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_orth_small(const OrthSmallParams &p, cudaStream_t s) {
+    const bool lines = rows_on_lines(p.bf16, {p.grad, p.result}, {p.momentum, p.weight}, p.copy, p.ld | p.ls | p.ldo | p.lse);
+    if (p.cols % 4) return p.bf16 ? launch_small<1, false, true>(p, s) : launch_small<1, false, false>(p, s);
+    if (lines) return p.bf16 ? launch_small<4, true, true>(p, s) : launch_small<4, true, false>(p, s);
+    return p.bf16 ? launch_small<4, false, true>(p, s) : launch_small<4, false, false>(p, s);
 }
 
 }  // namespace cbd

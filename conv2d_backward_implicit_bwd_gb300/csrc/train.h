@@ -181,7 +181,7 @@ struct OrthPrepParams {
     int32_t batch, rows, cols, pitch, parts, bf16, nesterov;
     float beta;
 };
-cudaError_t launch_orth_prep(const OrthPrepParams &p, bool by_four, cudaStream_t s);
+cudaError_t launch_orth_prep(const OrthPrepParams &p, cudaStream_t s);
 // All the products.  Maps: [2] planes hi, lo; x has two buffers.
 constexpr int kOrthMostSteps = 64, kOrthLoadMaps = 24;
 constexpr int kOrthSplits = 3;  // most pieces of a tile's contraction
@@ -222,7 +222,7 @@ struct OrthSmallParams {
     int64_t wait_budget;
     int64_t ls, ld, lse, ldo;      // of the input, of the result
     int32_t rows, cols, batch, steps, cluster, slice;
-    int32_t in_bf16, out_bf16, nesterov, single_from;
+    int32_t bf16, nesterov, single_from;  // bf16: of the input and the result
     float beta, rate, keep;
     float coef[3 * kOrthMostSteps];
 };

@@ -894,7 +894,7 @@ static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const 
         q.rows = (int32_t)d.rows; q.cols = (int32_t)d.cols; q.batch = (int32_t)d.batch; q.steps = d.steps;
         q.cluster = p->cluster;
         q.slice = (int32_t)(((std::max(d.rows, d.cols) + p->cluster - 1) / p->cluster + 63) / 64 * 64);
-        q.in_bf16 = q.out_bf16 = d.dtype == CONV_BWD_BF16;
+        q.bf16 = d.dtype == CONV_BWD_BF16;
         q.single_from = single_from;
         std::copy(p->coef.begin(), p->coef.end(), q.coef);
         return launch_orth_small(q, s) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
@@ -906,9 +906,7 @@ static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const 
     pp.batch = (int32_t)d.batch; pp.rows = (int32_t)d.rows; pp.cols = (int32_t)d.cols; pp.pitch = p->pitch;
     pp.parts = p->most_parts;
     pp.bf16 = d.dtype == CONV_BWD_BF16;
-    const bool by_four = d.cols % 4 == 0 && pp.ld % 4 == 0 && pp.ls % 4 == 0 && (uintptr_t)pp.grad % (4 * esize(d.dtype)) == 0 &&
-                         (uintptr_t)pp.momentum % 16 == 0;
-    if (launch_orth_prep(pp, by_four, s) != cudaSuccess) return CONV_BWD_ERR_CUDA;
+    if (launch_orth_prep(pp, s) != cudaSuccess) return CONV_BWD_ERR_CUDA;
     OrthParams q = p->run;
     q.segment = fp32_result ? 2 : 8;
     q.single_from = single_from;
