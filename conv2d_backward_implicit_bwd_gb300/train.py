@@ -531,7 +531,7 @@ class Orthogonal(_Plan):
         c = None if copy is None else self._dense(copy, torch.bfloat16, "copy")
         if scale is None:
             scale = max(1.0, self.rows / self.cols) ** 0.5
-        _check(_lib.conv_bwd_orth_update(self._h, w, grad.data_ptr(), ld, ls, m, c, lr, beta, 1 if nesterov else 0, decay, scale,
+        _check(_lib.conv_bwd_orth_update(self._h, w, grad.data_ptr(), ld, ls, m, c, float(lr), float(beta), 1 if nesterov else 0, float(decay), float(scale),
                                          _stream(stream, grad.device)), "conv_bwd_orth_update")
         _written((weight, momentum) if copy is None else (weight, momentum, copy))
 

@@ -5,10 +5,16 @@
     Experts.backward_data / backward_weight --> gradients of both layers (fp32, added over inner steps)
     GradClip.clip --> clipped gradients --> SGD on fp32 masters, bf16 copies for the products
 
+With ``--orthogonal`` (``ExpertPolicy(orthogonal=True)``) the step uses the operators around these as well:
+
+    TokenLogp.forward --> log-probabilities of the sampled actions, entropy
+    TokenLogp.backward --> gradient of an entropy bonus, added to the loss's
+    Orthogonal.update --> momentum and an orthogonalised step on the masters, instead of SGD
+
 The task: every row belongs to an expert and has a hidden right action; the policy samples actions and is rewarded for
 the right one.  Each batch is used for a few inner steps, so the ratio to the sampling policy moves and is clipped.
 
-    python examples/expert_policy_step.py [--steps 200]
+    python examples/expert_policy_step.py [--steps 200] [--orthogonal]
 """
 import argparse
 import os
@@ -21,7 +27,7 @@ from conv2d_backward_implicit_bwd_gb300 import train  # noqa: E402
 
 
 class ExpertPolicy:
-    def __init__(self, experts=4, width=64, hidden=128, vocab=64, rows=1024, seed=0, lr=2.0, max_norm=1.0, kl=0.01):
+    def __init__(self, experts=4, width=64, hidden=128, vocab=64, rows=1024, seed=0, lr=2.0, max_norm=1.0, kl=0.01, orthogonal=False, bonus=0.01):
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.gen, self.vocab, self.rows, self.lr, self.max_norm = g, vocab, rows, lr, max_norm
         normal = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
@@ -33,6 +39,12 @@ class ExpertPolicy:
         self.head = train.Experts(1, hidden, vocab)
         self.loss = train.PolicyLoss(vocab, clip_low=0.2, clip_high=0.2, kl=kl)
         self.clip = train.GradClip.like(self.grads)
+        self.logp, self.bonus = None, bonus
+        if orthogonal:
+            self.lr = 0.02 if lr == 2.0 else lr
+            self.logp = train.TokenLogp(vocab)
+            self.step_plans = [train.Orthogonal(*m.shape, "f32") for m in self.masters]
+            self.momenta = [torch.zeros_like(m) for m in self.masters]
         # the task: rows sorted by expert (ragged), each with a right action that is linear in the row
         share = torch.rand(experts, generator=g, device="cuda") + 0.2
         cuts = (share.cumsum(0) / share.sum() * rows).round().int()
@@ -48,7 +60,12 @@ class ExpertPolicy:
     def gradients(self, actions, advantage, weight, old_logp, ref_logp):
         """Forward, loss, backward; adds to self.grads.  Returns (loss, logp)."""
         z = self.logits()
-        loss, logp, dz = self.loss.forward_backward(z, actions, advantage, weight, old_logp, ref_logp, out=z)
+        if self.logp is None:
+            loss, logp, dz = self.loss.forward_backward(z, actions, advantage, weight, old_logp, ref_logp, out=z)
+        else:
+            _, entropy, lse, _, _ = self.logp.forward(z)
+            loss, logp, dz = self.loss.forward_backward(z, actions, advantage, weight, old_logp, ref_logp)
+            dz += self.logp.backward(z, None, lse, entropy, grad_entropy=-self.bonus * weight, out=z)
         dh = self.head.backward_data(dz, self.w[1], self.one) * (self.hidden > 0)
         self.head.backward_weight(dz, self.hidden, self.one, out=self.grads[1], accumulate=True)
         self.layer.backward_weight(dh, self.x, self.offsets, out=self.grads[0], accumulate=True)
@@ -57,6 +74,11 @@ class ExpertPolicy:
     def update(self):
         """Clips the gradients in place and steps; returns their norm before clipping."""
         norm, _ = self.clip.clip(self.grads, self.max_norm)
+        if self.logp is not None:
+            for plan, m, g, v, w in zip(self.step_plans, self.masters, self.grads, self.momenta, self.w):
+                plan.update(m, g, v, self.lr, copy=w)
+            torch._foreach_zero_(self.grads)
+            return norm
         torch._foreach_add_(self.masters, self.grads, alpha=-self.lr)
         torch._foreach_copy_(self.w, self.masters)
         torch._foreach_zero_(self.grads)
@@ -64,9 +86,10 @@ class ExpertPolicy:
 
     def batch(self):
         """Samples actions; returns (actions, advantage, weight, old_logp, mean reward)."""
-        p = torch.softmax(self.logits().float(), 1)
+        z = self.logits()
+        p = torch.softmax(z.float(), 1)
         actions = torch.multinomial(p, 1, generator=self.gen)[:, 0]
-        old = torch.log(p.gather(1, actions[:, None])[:, 0])
+        old = torch.log(p.gather(1, actions[:, None])[:, 0]) if self.logp is None else self.logp.forward(z, actions.int())[0]
         reward = (actions == self.right).float()
         weight = torch.full((self.rows,), 1.0 / self.rows, device="cuda")
         return actions.int(), (reward - reward.mean()) / (reward.std() + 1e-4), weight, old, reward.mean()
@@ -79,7 +102,7 @@ class ExpertPolicy:
         return dict(loss=loss, reward=reward, norm=norm)
 
     def check(self):
-        for plan in (self.layer, self.head, self.loss, self.clip):
+        for plan in (self.layer, self.head, self.loss, self.clip, *([] if self.logp is None else [self.logp, *self.step_plans])):
             status, detail = plan.status()
             if status != train.OK:
                 raise train.ConvBwdError(status, f"device status {detail:#x}")
@@ -88,8 +111,9 @@ class ExpertPolicy:
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=200)
+    ap.add_argument("--orthogonal", action="store_true", help="entropy bonus and orthogonalised updates")
     a = ap.parse_args()
-    model = ExpertPolicy()
+    model = ExpertPolicy(orthogonal=a.orthogonal)
     for i in range(a.steps):
         out = model.step()
         if i % 20 == 0 or i == a.steps - 1:
