@@ -267,7 +267,9 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
         tc_fence_after();
         __syncwarp();
     };
-    const int deep = (g + 15) / 16;  // 16-deep steps of a contraction over the smaller side
+    // What lies beyond the next 16 of the smaller side is zeros in X and never asked for in the Gram matrices.
+    const int deep = (g + 15) / 16, gn = deep * 16;  // 16-deep steps of a contraction over the smaller side
+    const bool rows_live = warp % 4 * 32 < gn, live = rows_live && part * 32 < gn;
     const int along = max(1, (valid + 15) / 16);  // over the slice
     const uint32_t x_k = desc(x_at, 1), x_mn = desc(x_at, BLOCK >> 4), g_k = desc(g_at, 1);
     // hi hi and, before it, hi lo and lo hi: the small ones first
@@ -285,77 +287,82 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
     auto k_step = [](int k) { return (uint32_t)(k >> 2) * (BLOCK >> 4) + (uint32_t)(k & 3) * 2u; };
     auto mn_step = [](int k) { return (uint32_t)k * 128u; };
     constexpr uint32_t XP = X_PLANE >> 4, GP = G_PLANE >> 4;
+    auto put_gram = [&](const float (&x)[32]) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                h[i] = pack_hi(x[q * 8 + 2 * i], x[q * 8 + 2 * i + 1]);
+                l[i] = pack_lo(x[q * 8 + 2 * i], x[q * 8 + 2 * i + 1]);
+            }
+            const uint32_t to = chunk_at(row, part * 32 + q * 8);
+            *reinterpret_cast<uint4 *>(sg + to) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(sg + G_PLANE + to) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+    };
     for (int step = 0; step < p.steps; ++step) {
         const bool single = step >= p.single_from, final = step + 1 == p.steps;
-        constexpr uint32_t square_id = (1u << 4) | (128u >> 3) << 17 | (128u >> 4) << 24;
+        const uint32_t square_id = (1u << 4) | (uint32_t)(gn >> 3) << 17 | (128u >> 4) << 24;
         // gram
         product([&] { terms(single, x_k, XP, x_k, XP, along, k_step, k_step, square_id); });
         float old[32];  // this thread's part of A
-        {
+        if (live) {
             uint32_t v[32];
             tmem_ld32(lane_base + part * 32, v);
-            if (c == 1) {
 #pragma unroll
-                for (int q = 0; q < 32; ++q) old[q] = __uint_as_float(v[q]) * (1.f / kOrthUp);
+            for (int q = 0; q < 32; ++q) old[q] = __uint_as_float(v[q]) * (1.f / kOrthUp);
+        }
+        if (c == 1) {
+            if (live) put_gram(old);
+        } else {
+            // this CTA's part, then the sums of gn / c rows from every CTA, then those to every CTA
+            float *f = reinterpret_cast<float *>(sg);
+            if (live) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t h[4], l[4];
+                for (int q = 0; q < 8; ++q) *reinterpret_cast<float4 *>(f + float_at(row, part * 32 + q * 4, 128)) = make_float4(old[4 * q], old[4 * q + 1], old[4 * q + 2], old[4 * q + 3]);
+            }
+            cluster_sync_all();
+            constexpr int MOST = 128 * 32 / 2 / NT;  // chunks of a thread, two CTAs
+            const int rows_here = (gn + c - 1) / c, first = rank * rows_here, across = gn / 4, chunks = max(0, min(rows_here, gn - first)) * across;
+            float4 s[MOST];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        h[i] = pack_hi(old[q * 8 + 2 * i], old[q * 8 + 2 * i + 1]);
-                        l[i] = pack_lo(old[q * 8 + 2 * i], old[q * 8 + 2 * i + 1]);
-                    }
-                    const uint32_t to = chunk_at(row, part * 32 + q * 8);
-                    *reinterpret_cast<uint4 *>(sg + to) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4 *>(sg + G_PLANE + to) = make_uint4(l[0], l[1], l[2], l[3]);
-                }
-            } else {
-                // this CTA's part, then the sums of 128 / c rows from every CTA, then those to every CTA
-                float *f = reinterpret_cast<float *>(sg);
+            for (int q = 0; q < MOST; ++q) {
+                const int j = q * NT + tid, r = first + j / across, cc = j % across * 4;
+                s[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j < chunks) {
+                    const uint32_t from = smem_u32(f + float_at(r, cc, 128));
+                    float4 x[8];
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    *reinterpret_cast<uint4 *>(f + float_at(row, part * 32 + q * 4, 128)) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-                cluster_sync_all();
-                constexpr int MOST = 128 * 32 / 2 / NT;  // chunks of a thread, two CTAs
-                const int rows_here = 128 / c;
-                float4 s[MOST];
+                    for (int k = 0; k < 8; ++k)
+                        if (k < c) asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[k].x), "=f"(x[k].y), "=f"(x[k].z), "=f"(x[k].w) : "r"(mapa_shared(from, k)) : "memory");
 #pragma unroll
-                for (int q = 0; q < MOST; ++q) {
-                    const int j = q * NT + tid, r = rank * rows_here + j / 32, cc = j % 32 * 4;
-                    s[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (j < rows_here * 32) {
-                        const uint32_t from = smem_u32(f + float_at(r, cc, 128));
-                        float4 x[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (k < c) asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[k].x), "=f"(x[k].y), "=f"(x[k].z), "=f"(x[k].w) : "r"(mapa_shared(from, k)) : "memory");
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            if (k >= c) break;
-                            s[q].x += x[k].x;
-                            s[q].y += x[k].y;
-                            s[q].z += x[k].z;
-                            s[q].w += x[k].w;
-                        }
+                    for (int k = 0; k < 8; ++k) {
+                        if (k >= c) break;
+                        s[q].x += x[k].x;
+                        s[q].y += x[k].y;
+                        s[q].z += x[k].z;
+                        s[q].w += x[k].w;
                     }
                 }
-                cluster_sync_all();
+            }
+            cluster_sync_all();
 #pragma unroll
-                for (int q = 0; q < MOST; ++q) {
-                    const int j = q * NT + tid, r = rank * rows_here + j / 32, cc = j % 32 * 4;
-                    if (j < rows_here * 32) {
-                        const float m = 1.f / kOrthUp;
-                        const uint32_t h0 = pack_hi(s[q].x * m, s[q].y * m), h1 = pack_hi(s[q].z * m, s[q].w * m), l0 = pack_lo(s[q].x * m, s[q].y * m), l1 = pack_lo(s[q].z * m, s[q].w * m);
-                        const uint32_t to = g_at + chunk_at(r, cc & ~7) + (uint32_t)(cc & 4) * 2u;
-                        for (int k = 0; k < c; ++k) {
-                            const uint32_t there = mapa_shared(to, k);
-                            asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(there), "r"(h0), "r"(h1) : "memory");
-                            asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(there + G_PLANE), "r"(l0), "r"(l1) : "memory");
-                        }
+            for (int q = 0; q < MOST; ++q) {
+                const int j = q * NT + tid, r = first + j / across, cc = j % across * 4;
+                if (j < chunks) {
+                    const uint32_t h0 = pack_hi(s[q].x, s[q].y), h1 = pack_hi(s[q].z, s[q].w), l0 = pack_lo(s[q].x, s[q].y), l1 = pack_lo(s[q].z, s[q].w);
+                    const uint32_t to = g_at + chunk_at(r, cc & ~7) + (uint32_t)(cc & 4) * 2u;
+                    for (int k = 0; k < c; ++k) {
+                        const uint32_t there = mapa_shared(to, k);
+                        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(there), "r"(h0), "r"(h1) : "memory");
+                        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(there + G_PLANE), "r"(l0), "r"(l1) : "memory");
                     }
                 }
-                fence_proxy_async();
-                cluster_sync_all();
+            }
+            fence_proxy_async();
+            cluster_sync_all();
+            if (live) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint4 h = *reinterpret_cast<const uint4 *>(sg + chunk_at(row, part * 32 + q * 8)), l = *reinterpret_cast<const uint4 *>(sg + G_PLANE + chunk_at(row, part * 32 + q * 8));
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
         }
         // square
         product([&] { terms(single, g_k, GP, g_k, GP, deep, k_step, k_step, square_id); });
-        {
+        if (live) {
             const float a = p.coef[3 * step] * kOrthUpPoly, b = p.coef[3 * step + 1] * (kOrthUpPoly / kOrthUp), cq = p.coef[3 * step + 2] * (kOrthUpPoly / (kOrthUp * kOrthUp));
             uint32_t v[32];
             tmem_ld32(lane_base + part * 32, v);
@@ -382,24 +389,13 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
                 for (int q = 0; q < 32; ++q)
                     if (q == lane) old[q] += a;
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t h[4], l[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[i] = pack_hi(old[q * 8 + 2 * i], old[q * 8 + 2 * i + 1]);
-                    l[i] = pack_lo(old[q * 8 + 2 * i], old[q * 8 + 2 * i + 1]);
-                }
-                const uint32_t to = chunk_at(row, part * 32 + q * 8);
-                *reinterpret_cast<uint4 *>(sg + to) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4 *>(sg + G_PLANE + to) = make_uint4(l[0], l[1], l[2], l[3]);
-            }
+            put_gram(old);
         }
         // product
         product([&] { terms(single, g_k, GP, x_mn, XP, deep, k_step, mn_step, (1u << 4) | 1u << 16 | (uint32_t)(width >> 3) << 17 | (128u >> 4) << 24); });
         const int each = width / 4;  // columns of a thread, a multiple of 16
         const float mul = final ? 1.f / (kOrthUp * kOrthUpPoly) : 1.f / kOrthUpPoly;
-        for (int q = 0; q < each; q += 16) {
+        for (int q = 0; rows_live && q < each; q += 16) {
             uint32_t v[16];
             const int col = part * each + q;
             tmem_ld16(lane_base + col, v);
