@@ -26,8 +26,9 @@
 // added in fp32 registers, under the other accumulator's MMAs.  Every two k-blocks the result's error is that of the same
 // products in fp32 (1024 x 2048, 8 directions over 1 % noise: 4.5e-5; every eight 1.4e-4, never 2.0e-4), but the sums take
 // power, and power is what bounds large batches: 32 of 1024 x 2048 3163, 2889 and 2825 us.  So fp32 results take two, bf16
-// results and steps on weights (of which X is a hundredth) eight.  A bf16 result's last step takes the hi halves alone: what
-// that rounds no later step multiplies (5e-4 beside the 1.7e-3 of bf16; in the last two steps 2.4e-3).
+// results and steps on weights (of which X is a hundredth) eight.  A bf16 result's last product takes the hi halves alone: what
+// that rounds no later step multiplies (the result's error 1.04 times bf16's own at most; the whole last step so 1.55 times,
+// at 79 x 2800; 32 of 1024 x 2048 2585 instead of 2716 us).
 //
 // The tile is 256 x W on a pair of SMs (tcgen05 cta_group::2), two accumulators in TMEM; a k-block of 64 brings both
 // halves of both operands, 64 KB a CTA for W = 256, and feeds twelve 16-deep MMAs, so loads are a third of what a plain
@@ -123,6 +124,8 @@ __device__ __forceinline__ Work work_at(const OrthParams &p, int i) {
     w.kb1 = (int)((int64_t)kblocks * (w.split + 1) / splits);
     return w;
 }
+// Whether a product takes one term instead of three.
+__device__ __forceinline__ bool hi_alone(const OrthParams &p, const Work &w) { return p.last_hi && w.kind == PRODUCT && w.step + 1 == p.steps; }
 // Whether an operand's lines run across the contraction in its k-block kb: x in two of the products, and the symmetric
 // matrices, of which only the blocks of 256 from the diagonal on are there, below it.
 __device__ __forceinline__ bool a_across(const Work &w, bool high, int kb) { return w.kind == GRAM ? high : (w.kind == SQUARE || !high) && (kb >> 2) < (w.m0 >> 8); }
@@ -433,7 +436,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                 bool ok = true, issued = false;
                 for (int i = pair; i < total && ok; i += npairs, ++piece) {
                     const Work w = work_at<W>(p, i);
-                    const int m = w.m0 + (int)rank * 128, n = w.n0 + (int)rank * (w.n / 2), planes = w.step >= p.single_from ? 1 : 2;
+                    const int m = w.m0 + (int)rank * 128, n = w.n0 + (int)rank * (w.n / 2), planes = hi_alone(p, w) ? 1 : 2;
                     // What other SMs have written in this launch.  (One thread of a CTA asks for it: with every lane of the
                     // epilogue asking too, loads and counters took 3 us longer.)
                     const uint32_t bar_ready = ready0 + 8 * (piece % READY);
@@ -486,7 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
             bool ok = true, issued = false;
             for (int i = pair; i < total && ok; i += npairs) {
                 const Work w = work_at<W>(p, i);
-                const bool single = w.step >= p.single_from;
+                const bool single = hi_alone(p, w);
                 for (int left = w.kb1 - w.kb0; left > 0 && ok;) {
                     const uint32_t b = use & 1, bph = (use >> 1) & 1, d = tmem_base + b * 256;
                     ++use;

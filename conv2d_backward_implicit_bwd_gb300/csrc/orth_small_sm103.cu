@@ -273,16 +273,14 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
     const int along = max(1, (valid + 15) / 16);  // over the slice
     const uint32_t x_k = desc(x_at, 1), x_mn = desc(x_at, BLOCK >> 4), g_k = desc(g_at, 1);
     // hi hi and, before it, hi lo and lo hi: the small ones first
-    auto terms = [&](bool single, uint32_t a, uint32_t a_plane, uint32_t b, uint32_t b_plane, int steps, auto &&a_step, auto &&b_step, uint32_t id) {
+    auto terms = [&](uint32_t a, uint32_t a_plane, uint32_t b, uint32_t b_plane, int steps, auto &&a_step, auto &&b_step, uint32_t id) {
         uint32_t acc = 0;
-        if (!single) {
 #pragma unroll 4
-            for (int k = 0; k < steps; ++k, acc = 1) mma(tmem, a + a_step(k), b + b_plane + b_step(k), desc_hi, id, acc);
+        for (int k = 0; k < steps; ++k, acc = 1) mma(tmem, a + a_step(k), b + b_plane + b_step(k), desc_hi, id, acc);
 #pragma unroll 4
-            for (int k = 0; k < steps; ++k) mma(tmem, a + a_plane + a_step(k), b + b_step(k), desc_hi, id, 1);
-        }
+        for (int k = 0; k < steps; ++k) mma(tmem, a + a_plane + a_step(k), b + b_step(k), desc_hi, id, 1);
 #pragma unroll 4
-        for (int k = 0; k < steps; ++k, acc = 1) mma(tmem, a + a_step(k), b + b_step(k), desc_hi, id, acc);
+        for (int k = 0; k < steps; ++k) mma(tmem, a + a_step(k), b + b_step(k), desc_hi, id, 1);
     };
     auto k_step = [](int k) { return (uint32_t)(k >> 2) * (BLOCK >> 4) + (uint32_t)(k & 3) * 2u; };
     auto mn_step = [](int k) { return (uint32_t)k * 128u; };
@@ -302,10 +300,10 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
         }
     };
     for (int step = 0; step < p.steps; ++step) {
-        const bool single = step >= p.single_from, final = step + 1 == p.steps;
+        const bool final = step + 1 == p.steps;
         const uint32_t square_id = (1u << 4) | (uint32_t)(gn >> 3) << 17 | (128u >> 4) << 24;
         // gram
-        product([&] { terms(single, x_k, XP, x_k, XP, along, k_step, k_step, square_id); });
+        product([&] { terms(x_k, XP, x_k, XP, along, k_step, k_step, square_id); });
         float old[32];  // this thread's part of A
         if (live) {
             uint32_t v[32];
@@ -377,7 +375,7 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
             }
         }
         // square
-        product([&] { terms(single, g_k, GP, g_k, GP, deep, k_step, k_step, square_id); });
+        product([&] { terms(g_k, GP, g_k, GP, deep, k_step, k_step, square_id); });
         if (live) {
             const float a = p.coef[3 * step] * kOrthUpPoly, b = p.coef[3 * step + 1] * (kOrthUpPoly / kOrthUp), cq = p.coef[3 * step + 2] * (kOrthUpPoly / (kOrthUp * kOrthUp));
             uint32_t v[32];
@@ -392,7 +390,7 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
             put_gram(old);
         }
         // product
-        product([&] { terms(single, g_k, GP, x_mn, XP, deep, k_step, mn_step, (1u << 4) | 1u << 16 | (uint32_t)(width >> 3) << 17 | (128u >> 4) << 24); });
+        product([&] { terms(g_k, GP, x_mn, XP, deep, k_step, mn_step, (1u << 4) | 1u << 16 | (uint32_t)(width >> 3) << 17 | (128u >> 4) << 24); });
         const int each = width / 4;  // columns of a thread, a multiple of 16
         const float mul = final ? 1.f / (kOrthUp * kOrthUpPoly) : 1.f / kOrthUpPoly;
         for (int q = 0; rows_live && q < each; q += 16) {

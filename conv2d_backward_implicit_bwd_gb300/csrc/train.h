@@ -203,7 +203,7 @@ struct OrthParams {
     int32_t rows, cols, batch, steps, items;
     int32_t tiles_sym, tiles_all;  // tiles of a matrix: gram and square, product
     int32_t splits[3];
-    int32_t single_from;           // first step with one product of hi planes instead of three
+    int32_t last_hi;               // the last product takes the hi planes alone
     int32_t segment;               // k-blocks of one accumulator
     int32_t bf16, pitch_gram;
     float rate, keep;
@@ -222,7 +222,7 @@ struct OrthSmallParams {
     int64_t wait_budget;
     int64_t ls, ld, lse, ldo;      // of the input, of the result
     int32_t rows, cols, batch, steps, cluster, slice;
-    int32_t bf16, nesterov, single_from;  // bf16: of the input and the result
+    int32_t bf16, nesterov;        // bf16: of the input and the result
     float beta, rate, keep;
     float coef[3 * kOrthMostSteps];
 };

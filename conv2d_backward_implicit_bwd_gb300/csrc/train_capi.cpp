@@ -883,7 +883,6 @@ struct OrthOut {
 static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const OrthOut &o, cudaStream_t s) {
     const conv_bwd_orth_desc &d = p->d;
     const bool fp32_result = o.result && d.dtype == CONV_BWD_F32;
-    const int32_t single_from = o.result && !fp32_result ? d.steps - 1 : d.steps;
     if (p->cluster) {
         OrthSmallParams q;
         std::memset(&q, 0, sizeof(q));
@@ -897,7 +896,6 @@ static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const 
         q.cluster = p->cluster;
         q.slice = (int32_t)(((std::max(d.rows, d.cols) + p->cluster - 1) / p->cluster + 63) / 64 * 64);
         q.bf16 = d.dtype == CONV_BWD_BF16;
-        q.single_from = single_from;
         std::copy(p->coef.begin(), p->coef.end(), q.coef);
         return launch_orth_small(q, s) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
     }
@@ -911,7 +909,7 @@ static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const 
     if (launch_orth_prep(pp, s) != cudaSuccess) return CONV_BWD_ERR_CUDA;
     OrthParams q = p->run;
     q.segment = fp32_result ? 2 : 8;
-    q.single_from = single_from;
+    q.last_hi = o.result && !fp32_result;
     q.result = o.result;
     q.bf16 = pp.bf16;
     q.weight = o.weight;
