@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(NT) orth_norm_kernel(const OrthPrepParams p) {
     if (blockIdx.x == 0 && threadIdx.x == 0) p.done[e] = 0;
     const int per_row = (p.cols + V - 1) / V;  // (V divides cols where V > 1)
     const int64_t items = (int64_t)p.rows * per_row;
-    SquareSum sum = {0.f, 0.0};
+    SquareSum sum = {0.f, 0.f, 0.0};
     for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < items; i += (int64_t)gridDim.x * NT) {
         const int r = (int)(i / per_row), c = (int)(i - (int64_t)r * per_row) * V;
         const int64_t at = (int64_t)e * p.ls + (int64_t)r * p.ld + c;
@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(NT) orth_split_kernel(const OrthPrepParams p) 
             s += p.partial[((int64_t)e * p.parts + i) * 2];
             rest += p.partial[((int64_t)e * p.parts + i) * 2 + 1];
         }
-        SquareSum sum = {0.f, s + rest};
+        SquareSum sum = {0.f, 0.f, s + rest};
         sum.join();
         if (threadIdx.x == 0) orth_factors(sum, factor[0], factor[1], factor[2]);
     }

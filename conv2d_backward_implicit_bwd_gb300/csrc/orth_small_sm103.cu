@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
             for (int k = 0; k < inner; k += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.weight + corner + (int64_t)i * p.cols + k));
     // The sum of squares, along the caller's rows.
     constexpr int U = 8 / V;  // loads of a thread in flight
-    SquareSum sum = {0.f, 0.0};
+    SquareSum sum = {0.f, 0.f, 0.0};
     {
         const int fast = inner / V, items = fast * outer, over = fast ? NT / fast : 0, rest = fast ? NT % fast : 0;
         const int k0 = fast ? tid % fast : 0, o0 = fast ? tid / fast : 0;
@@ -168,14 +168,14 @@ __global__ void __launch_bounds__(NT, 1) orth_small_kernel(const OrthSmallParams
     if (lane == 0) partial[warp] = sum;
     __syncthreads();
     if (warp == 0) {
-        sum = lane < WARPS ? partial[lane] : SquareSum{0.f, 0.0};
+        sum = lane < WARPS ? partial[lane] : SquareSum{0.f, 0.f, 0.0};
         sum.join();
         if (lane == 0) total = sum;
     }
     sync_all();
     sum = total;
     if (c > 1) {  // of the whole matrix, in order
-        sum = {0.f, 0.0};
+        sum = {0.f, 0.f, 0.0};
         for (int k = 0; k < c; ++k) {
             const uint32_t from = mapa_shared(smem_u32(&total), k);
             float x;

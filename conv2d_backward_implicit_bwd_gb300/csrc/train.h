@@ -229,9 +229,10 @@ struct OrthSmallParams {
 cudaError_t launch_orth_small(const OrthSmallParams &p, cudaStream_t s);
 #ifdef __CUDACC__
 // A sum of squares: of those far from both ends of fp32 in fp32, of the others in fp64 (a conversion and an addition of fp64
-// for every element would take longer than the memory).
+// for every element would take longer than the memory).  What an addition in fp32 leaves goes into the next one: a thread
+// adds up to 2^14 numbers, equal ones with errors that all point one way.
 struct SquareSum {
-    float safe;
+    float safe, lost;
     double rest;
     template <int N>
     __device__ __forceinline__ void add(const float (&x)[N]) {
@@ -239,7 +240,9 @@ struct SquareSum {
 #pragma unroll
         for (int j = 0; j < N; ++j) q = fmaf(x[j], x[j], q);
         if (q > 0x1p-60f && q < 0x1p100f) {
-            safe += q;
+            const float y = q - lost, t = safe + y;
+            lost = (t - safe) - y;
+            safe = t;
         } else {
 #pragma unroll 1
             for (int j = 0; j < N; ++j) {

@@ -6,7 +6,12 @@ of 2^-24, at most 24 truncations of 2^-25 in one accumulator, fp32 sums), so X' 
 or three products that make it: 2 * 1.7, 3 * 2.9 at most).  A later step multiplies an error by at most
 L = max |p'|, |p(s) / s| = a (p(s) = a s + b s^3 + c s^5, the usual coefficients).  So after T steps the error is below
 D = sum_k L^(T-1-k) (|a| + 3.4 |b| + 8.7 |c|) 2^-20 |X_k|_F, which the test sums over the iterates in 64 bits; a result in bf16 adds half a step of each
-element, the norm at the start 2^-23.  (One product of fp16 or bf16 operands each would be off by 2^8 to 2^11 times as much.)"""
+element, the norm at the start 2^-23.  (One product of fp16 or bf16 operands each would be off by 2^8 to 2^11 times as much.)
+
+Results in bf16 come of accumulators with 96 truncations, which is D's 2^-20 in the steps before the last 2^-18 instead, and of
+a last product B X of fp16 operands alone, off by 2^-12 (|B|_F |X|_2 + |B|_2 |X|_F) < 2^-9.2 |X'|_F in the worst case (|B| < 3.5,
+|X|_2 < 1.3).  They have no room of their own: rounding to the nearest bf16 is off by 0.42 half steps in the root mean square (uniform
+within the half step, which is 2^-9 to 2^-8 of an element), the two together by less than 0.65 of the half step that is given."""
 import math
 
 import pytest
@@ -150,6 +155,17 @@ def test_zero_and_broken_matrices(T):
     assert torch.isnan(got[2]).all() and torch.isnan(got[3]).all()
     assert torch.equal(got[0], want[0]) and torch.equal(got[5], want[5])
     assert torch.equal(plan.apply(u), want) and plan.status() == (0, 0)
+
+
+def test_norm_of_equal_elements(T):
+    """Squares of 1 + 0.45 * 2^-14 lose 0.45 * 2^-14 with each addition to a sum of 512 to 1024 of them, all one way: 2^-17 of the
+    norm of these matrices, whose threads add 978 each.  One step with (1, 0, 0) is u / |u|; room for operands of 22 bits, the
+    sum's and the root's roundings."""
+    c = 1 + 0.9 * 2.0 ** -16
+    u = torch.full((304, 1000, 1001), c, device="cuda")
+    u[:, 1::2] = -c
+    x = T.Orthogonal(304, 1000, 1001, "f32", steps=1, coefficients=(1.0, 0.0, 0.0)).apply(u)
+    assert (x.abs() * 1001000 ** 0.5 - 1).abs().max() <= 2.0 ** -20
 
 
 def test_low_rank(T):

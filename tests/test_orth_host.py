@@ -59,6 +59,7 @@ def test_arguments(T):
     assert run(p._h, x + 2, 0, 0, o, 0, 0, None) == 3 and run(p._h, x, 0, 0, o + 1, 0, 0, None) == 3
     assert run(p._h, x, 0, 0, x + 4, 0, 0, None) == 1 and run(p._h, x, 20, 0, x, 16, 0, None) == 1  # overlaps, not in place
     assert run(p._h, x, (1 << 31) + 1, 0, o, 0, 0, None) == 2 and run(p._h, x, 0, (1 << 40) + 1, o, 0, 0, None) == 2
+    assert run(p._h, x, 1 << 62, 0, o, 0, 0, None) == 2 and run(p._h, x, 0, 0, o, 1 << 60, 0, None) == 2 and run(p._h, x, -16, 0, o, 0, 0, None) == 1
     w, g, m, c = (i << 20 for i in range(1, 5))
     good = lambda **k: step(*[{"p": p._h, "w": w, "g": g, "ldg": 0, "lsg": 0, "m": m, "c": c, "lr": .1, "beta": .9, "nes": 1, "decay": 0., "scale": 1., "s": None, **k}[n]  # noqa: E731
                               for n in ("p", "w", "g", "ldg", "lsg", "m", "c", "lr", "beta", "nes", "decay", "scale", "s")])
