@@ -78,34 +78,37 @@ constexpr int smem_bytes() {
 }
 static_assert(smem_bytes<256>() <= 232448 && smem_bytes<128>() <= 232448, "shared memory of one CTA");
 
-// One piece of the work: of step `step`, its product `kind`, matrix e, a tile's columns of the contraction's blocks [kb0, kb1).
-enum : int { GRAM = 0, SQUARE = 1, PRODUCT = 2 };
+// One piece of the work: matrix e's tile in a phase, the contraction's blocks [kb0, kb1).
 struct Work {
-    int step, kind, e, tile, split;
+    int kind, a, b, e, tile, split;
     int m0, n0, n;  // first row and column, columns (a multiple of 32)
     int kb0, kb1;
     int M, N;
+    bool poly, last;
 };
+// The i-th piece; ph: the phase of an earlier one.
 template <int W>
-__device__ __forceinline__ Work work_at(const OrthParams &p, int i) {
+__device__ __forceinline__ Work work_at(const OrthParams &p, int i, int &ph) {
     Work w;
-    const int each[3] = {p.batch * p.tiles_sym * p.splits[0], p.batch * p.tiles_sym * p.splits[1], p.batch * p.tiles_all * p.splits[2]};
-    const int per_step = each[0] + each[1] + each[2];
-    w.step = i / per_step;
-    i -= w.step * per_step;
-    w.kind = i < each[0] ? GRAM : i < each[0] + each[1] ? SQUARE : PRODUCT;
-    i -= w.kind == GRAM ? 0 : w.kind == SQUARE ? each[0] : each[0] + each[1];
-    const int tiles = w.kind == PRODUCT ? p.tiles_all : p.tiles_sym, splits = w.kind == GRAM ? p.splits[0] : w.kind == SQUARE ? p.splits[1] : p.splits[2];
+    while (i >= p.phase[ph + 1].first) ++ph;
+    const OrthPhase &f = p.phase[ph];
+    i -= f.first;
+    w.kind = f.kind;
+    w.a = f.a;
+    w.b = f.b;
+    w.poly = f.poly;
+    w.last = f.last;
+    const int tiles = w.kind == kOrthProduct ? p.tiles_all : p.tiles_sym, splits = p.splits[w.kind];
     w.e = i / (tiles * splits);
     i -= w.e * tiles * splits;
     w.tile = i / splits;
     w.split = i - w.tile * splits;
     const int g = min(p.rows, p.cols);
-    w.M = w.kind == PRODUCT ? p.rows : g;
-    w.N = w.kind == PRODUCT ? p.cols : g;
+    w.M = w.kind == kOrthProduct ? p.rows : g;
+    w.N = w.kind == kOrthProduct ? p.cols : g;
     const int nt = (w.N + W - 1) / W;
     int l = w.tile, tm, tn;
-    if (w.kind != PRODUCT) {  // from the diagonal block on
+    if (w.kind != kOrthProduct) {  // from the diagonal block on
         tm = 0;
         for (int len = nt; l >= len; len -= 256 / W) {
             l -= len;
@@ -119,23 +122,18 @@ __device__ __forceinline__ Work work_at(const OrthParams &p, int i) {
     w.m0 = tm * 256;
     w.n0 = tn * W;
     w.n = min(W, (w.N - w.n0 + 31) & ~31);
-    const int kblocks = ((w.kind == GRAM ? max(p.rows, p.cols) : g) + 63) / 64;
+    const int kblocks = ((w.kind == kOrthGram ? max(p.rows, p.cols) : g) + 63) / 64;
     w.kb0 = (int)((int64_t)kblocks * w.split / splits);
     w.kb1 = (int)((int64_t)kblocks * (w.split + 1) / splits);
     return w;
 }
 // Whether a product takes one term instead of three.
-__device__ __forceinline__ bool hi_alone(const OrthParams &p, const Work &w) { return p.last_hi && w.kind == PRODUCT && w.step + 1 == p.steps; }
-// Whether an operand's lines run across the contraction in its k-block kb: x in two of the products, and the symmetric
-// matrices, of which only the blocks of 256 from the diagonal on are there, below it.
-__device__ __forceinline__ bool a_across(const Work &w, bool high, int kb) { return w.kind == GRAM ? high : (w.kind == SQUARE || !high) && (kb >> 2) < (w.m0 >> 8); }
-__device__ __forceinline__ bool b_across(const Work &w, bool high, int kb) { return w.kind == GRAM ? high : w.kind == SQUARE || high ? (kb >> 2) < (w.n0 >> 8) : true; }
-// warps that have finished with matrix e before w's operands are there
-__device__ __forceinline__ int needed(const OrthParams &p, const Work &w) {
-    return 2 * EPI * (w.step * (2 * p.tiles_sym + p.tiles_all) + w.kind * p.tiles_sym);
-}
-__device__ __forceinline__ bool wait_done(const OrthParams &p, const Work &w, volatile int32_t *abort, int32_t code) {
-    const int want = needed(p, w);
+__device__ __forceinline__ bool hi_alone(const OrthParams &p, const Work &w) { return p.last_hi && w.last; }
+// Whether an operand's lines run across the contraction in its k-block kb: X's in X^T X, and where it is multiplied from the
+// left; those of the symmetric matrices, of which only the blocks of 256 from the diagonal on are there, below it.
+__device__ __forceinline__ bool a_across(const Work &w, bool high, int kb) { return w.a > 1 ? (kb >> 2) < (w.m0 >> 8) : w.kind == kOrthGram && high; }
+__device__ __forceinline__ bool b_across(const Work &w, bool high, int kb) { return w.b > 1 ? (kb >> 2) < (w.n0 >> 8) : w.kind == kOrthProduct || high; }
+__device__ __forceinline__ bool wait_done(const OrthParams &p, const Work &w, int want, volatile int32_t *abort, int32_t code) {
     const int32_t *at = p.done + w.e;
     if (ld_acquire_gpu(at) >= want) return true;
     const long long t0 = clock64();
@@ -246,7 +244,7 @@ __device__ __forceinline__ void store_result(const OrthParams &p, const Work &w,
 // order and goes on with the tile; false for the others.
 template <int COLS>
 __device__ __forceinline__ bool join_splits(const OrthParams &p, const Work &w, float (&sum)[COLS], int splits, int slice, int lane) {
-    const int tiles = w.kind == PRODUCT ? p.tiles_all : p.tiles_sym, tile = w.e * tiles + w.tile;
+    const int tiles = w.kind == kOrthProduct ? p.tiles_all : p.tiles_sym, tile = w.e * tiles + w.tile;
     constexpr int STEP = 2 * EPI * 32 * COLS / 4;
     float4 *first = p.parts + (int64_t)(tile * splits) * STEP + slice * (32 * COLS / 4) + lane;
 #pragma unroll
@@ -299,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
     const bool leader = rank == 0, high = p.rows > p.cols;
     const uint32_t full0 = smem_u32(bars.full), empty0 = smem_u32(bars.empty), tfull0 = smem_u32(bars.tfull), tempty0 = smem_u32(bars.tempty), ready0 = smem_u32(bars.ready);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int pair = blockIdx.x / 2, npairs = gridDim.x / 2, total = p.items;
+    const int pair = blockIdx.x / 2, npairs = gridDim.x / 2, total = p.phase[p.phases].first;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -319,9 +317,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
         tmem_alloc2(smem_u32(&bars.tmem), 512);
         tc_fence_before();
     }
-    if (warp == LOAD_A) {  // every map that the steps load by: they stand together
-        const CUtensorMap *m = &p.x_gram_a[0][0];
-        if (lane < kOrthLoadMaps) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m + lane)) : "memory");
+    if (warp == LOAD_A) {  // the maps of the matrices that there are stand together
+        const CUtensorMap *m = &p.maps[0].rows128[0];
+        for (int i = lane; i < p.matrices * 6; i += 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m + i)) : "memory");
         __syncwarp();
     }
     cluster_sync_all();
@@ -340,20 +338,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
         const uint32_t lane_base = tmem_base + ((uint32_t)((warp % 4) * 32) << 16);
         uint8_t *slab = stage + warp * 4096;
         uint32_t use = 0, piece = 0;
+        int ph = 0;
         bool ok = true;
         for (int i = pair; i < total; i += npairs, ++piece) {
-            const Work w = work_at<W>(p, i);
+            const Work w = work_at<W>(p, i, ph);
+            const OrthPhase &f = p.phase[ph];
             const int row = w.m0 + (int)rank * 128 + (warp % 4) * 32, col0 = (warp / 4) * COLS, col = w.n0 + col0;
-            // square adds to A: by other SMs in this launch, so past L1; narrow tiles have the registers to read it ahead
+            // a polynomial adds to A: by other SMs in this launch, so past L1; narrow tiles have the registers to read it ahead
             constexpr int AHEAD = W == 256 ? 1 : COLS / 8;
             uint4 old_hi[AHEAD], old_lo[AHEAD];
             auto old_at = [&](int plane, int q) {
                 const int r = row + lane, c = col + q * 8;
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (r < w.M && c < p.pitch_gram) v = __ldcg(reinterpret_cast<const uint4 *>(p.gram[plane] + ((int64_t)w.e * w.M + r) * p.pitch_gram + c));
+                if (r < w.M && c < p.pitch_gram) v = __ldcg(reinterpret_cast<const uint4 *>(p.at[w.a][plane] + ((int64_t)w.e * w.M + r) * p.pitch_gram + c));
                 return v;
             };
-            if (w.kind == SQUARE) {
+            if (w.poly) {
                 if (ok) ok = mbar_wait_bounded(ready0 + 8 * (piece % READY), (piece / READY) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
                 ok = __all_sync(0xffffffffu, ok);
                 if constexpr (W != 256) {
@@ -384,12 +384,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                 if (lane == 0) arrive_relaxed(tempty_leader0 + 8 * b);
             }
             if (!ok) continue;
-            const int splits = w.kind == GRAM ? p.splits[0] : w.kind == SQUARE ? p.splits[1] : p.splits[2];
+            const int splits = p.splits[w.kind];
             if (W != 256 && splits > 1 && !join_splits<COLS>(p, w, sum, splits, (int)rank * EPI + warp, lane)) continue;
-            const bool final = w.kind == PRODUCT && w.step + 1 == p.steps;
-            if (w.kind == SQUARE) {
+            if (w.poly) {
                 // c sum + b A + a on the diagonal
-                const float a = p.coef[3 * w.step] * kOrthUpPoly, b = p.coef[3 * w.step + 1] * (kOrthUpPoly / kOrthUp), c = p.coef[3 * w.step + 2] * (kOrthUpPoly / (kOrthUp * kOrthUp));
+                const float a = f.diag, b = f.add, c = f.mul;
                 const int r = row + lane;
 #pragma unroll
                 for (int q = 0; q < COLS / 8; ++q) {
@@ -408,16 +407,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                     for (int q = 0; q < COLS; ++q) sum[q] += r == col + q ? a : 0.f;
                 }
             } else {
-                const float mul = w.kind == GRAM ? 1.f / kOrthUp : final ? 1.f / (kOrthUp * kOrthUpPoly) : 1.f / kOrthUpPoly;
+                const float mul = f.mul;
 #pragma unroll
                 for (int q = 0; q < COLS; ++q) sum[q] *= mul;
             }
-            if (final) {
+            if (w.last) {
                 store_result<COLS>(p, w, sum, slab, row, col, lane);
                 continue;
             }
-            const CUtensorMap *out = w.kind == GRAM ? p.gram_store : w.kind == SQUARE ? p.poly_store : (w.step & 1) ? p.x_store[0] : p.x_store[1];
-            store_planes<COLS>(out, w, sum, slab, row, col, lane);
+            store_planes<COLS>(p.maps[f.out].store, w, sum, slab, row, col, lane);
             // written, and known to be
             if (lane == 0) {
                 bulk_wait_all();
@@ -433,27 +431,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
             if (lane == 0) {
                 const uint32_t full_leader0 = mapa_shared(full0, 0);
                 uint32_t it = 0, piece = 0;
+                int phase = 0;
                 bool ok = true, issued = false;
                 for (int i = pair; i < total && ok; i += npairs, ++piece) {
-                    const Work w = work_at<W>(p, i);
+                    const Work w = work_at<W>(p, i, phase);
                     const int m = w.m0 + (int)rank * 128, n = w.n0 + (int)rank * (w.n / 2), planes = hi_alone(p, w) ? 1 : 2;
                     // What other SMs have written in this launch.  (One thread of a CTA asks for it: with every lane of the
                     // epilogue asking too, loads and counters took 3 us longer.)
                     const uint32_t bar_ready = ready0 + 8 * (piece % READY);
-                    ok = warp == LOAD_A ? wait_done(p, w, abort_flag, kDevTimeoutProducer)
+                    ok = warp == LOAD_A ? wait_done(p, w, p.phase[phase].need, abort_flag, kDevTimeoutProducer)
                                         : mbar_wait_bounded(bar_ready, (piece / READY) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer);
                     if (!ok) break;
                     if (warp == LOAD_A) mbar_arrive(bar_ready);
                     fence_proxy_async_global();
-                    // by lines along the contraction, and across it
-                    const CUtensorMap *along, *cross;
-                    if (warp == LOAD_A) {
-                        along = w.kind == SQUARE ? p.gram_a : w.kind == GRAM ? p.x_gram_a[w.step & 1] : high ? p.x_prod[w.step & 1] : p.poly_a;
-                        cross = w.kind == SQUARE ? p.gram_cross : w.kind == GRAM ? p.x_gram_a[w.step & 1] : p.poly_cross;
-                    } else {
-                        along = w.kind == SQUARE ? p.gram_b : w.kind == GRAM ? p.x_gram_b[w.step & 1] : p.poly_b;
-                        cross = w.kind == SQUARE ? p.gram_cross : w.kind == GRAM ? p.x_gram_b[w.step & 1] : high ? p.poly_cross : p.x_prod[w.step & 1];
-                    }
+                    // by lines along the contraction (this CTA's half of the tile in one box), and across it (in boxes of 64 x 64)
+                    const OrthMaps &maps = p.maps[warp == LOAD_A ? w.a : w.b];
+                    const CUtensorMap *along = warp == LOAD_A || W == 256 ? maps.rows128 : maps.rows64, *cross = maps.rows64;
                     for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
                         const uint32_t s = it % S, ph = (it / S) & 1;
                         if (!mbar_wait_bounded(empty0 + 8 * s, ph ^ 1, p.wait_budget, abort_flag, p.status, kDevTimeoutProducer)) {
@@ -486,9 +479,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
             const uint32_t a_at = (smem_u32(smem) >> 4) & 0x3FFFu, b_at = ((smem_u32(smem) + 2 * A_BYTES) >> 4) & 0x3FFFu;
             const uint32_t desc_hi = (uint32_t)(smem_desc_sw128(0, 0, 1024) >> 32);
             uint32_t s = 0, ph = 0, use = 0;
+            int phase = 0;
             bool ok = true, issued = false;
             for (int i = pair; i < total && ok; i += npairs) {
-                const Work w = work_at<W>(p, i);
+                const Work w = work_at<W>(p, i, phase);
                 const bool single = hi_alone(p, w);
                 for (int left = w.kb1 - w.kb0; left > 0 && ok;) {
                     const uint32_t b = use & 1, bph = (use >> 1) & 1, d = tmem_base + b * 256;

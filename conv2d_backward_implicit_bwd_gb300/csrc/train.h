@@ -182,15 +182,25 @@ struct OrthPrepParams {
     float beta;
 };
 cudaError_t launch_orth_prep(const OrthPrepParams &p, cudaStream_t s);
-// All the products.  Maps: [2] planes hi, lo; x has two buffers.
-constexpr int kOrthMostSteps = 64, kOrthLoadMaps = 24;
+// All the products, as a list of phases over the plan's matrices: 0 and 1 hold X in turn, the others are symmetric.
+constexpr int kOrthMostSteps = 64, kOrthJoined = 3;  // kOrthJoined: steps of one polynomial
+constexpr int kOrthMostPhases = 240;                 // of 64 steps: 11 for three joined, 3 for one
+constexpr int kOrthMatrices = 8;
 constexpr int kOrthSplits = 3;  // most pieces of a tile's contraction
 constexpr float kOrthUp = 1024.f, kOrthUpPoly = 256.f;  // what the planes' values are multiplied by
+enum : int8_t { kOrthGram = 0, kOrthSquare = 1, kOrthProduct = 2 };  // over the larger side; of symmetric matrices; X's
+struct OrthPhase {
+    int32_t first, need;           // its first item; warps that have finished with a matrix before
+    int8_t kind, a, b, out;
+    int8_t poly, last;             // mul a b + add a + diag; the result
+    float mul, add, diag;
+};
+struct OrthMaps {
+    CUtensorMap rows128[2], rows64[2], store[2];  // of planes hi and lo: boxes of 128 and 64 rows, of a warp's 32
+};
 struct OrthParams {
-    CUtensorMap x_gram_a[2][2], x_gram_b[2][2], x_prod[2][2];
-    CUtensorMap gram_a[2], gram_b[2], gram_cross[2], poly_a[2], poly_b[2], poly_cross[2];
-    CUtensorMap x_store[2][2], gram_store[2], poly_store[2];
-    const __half *gram[2];
+    OrthMaps maps[kOrthMatrices];
+    const __half *at[kOrthMatrices][2];
     void *result;                  // the result, or the step on the weights
     float *weight;
     __nv_bfloat16 *copy;
@@ -200,14 +210,14 @@ struct OrthParams {
     int32_t *status;
     int64_t wait_budget;
     int64_t ldo, lse;              // of the caller's tensors: rows, matrices
-    int32_t rows, cols, batch, steps, items;
-    int32_t tiles_sym, tiles_all;  // tiles of a matrix: gram and square, product
-    int32_t splits[3];
+    int32_t rows, cols, batch, matrices, phases;
+    int32_t tiles_sym, tiles_all;  // tiles of a matrix: symmetric, X
+    int32_t splits[3];             // by kind
     int32_t last_hi;               // the last product takes the hi planes alone
     int32_t segment;               // k-blocks of one accumulator
     int32_t bf16, pitch_gram;
     float rate, keep;
-    float coef[3 * kOrthMostSteps];
+    OrthPhase phase[kOrthMostPhases + 1];  // and the end
 };
 int orth_pairs(int num_sms);
 // Matrices whose smaller side is at most kOrthSmall, their larger side in `cluster` slices of `slice` columns.

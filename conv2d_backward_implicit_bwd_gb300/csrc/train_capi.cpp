@@ -193,20 +193,13 @@ struct conv_bwd_logp_plan_s {
 };
 
 struct conv_bwd_orth_plan_s {
-    struct Plane {  // tensor maps of one plane of a matrix, of both tile widths
-        CUtensorMap rows128, rows64, store;
-    };
-    struct Matrix {
-        __half *at[2] = {};
-        Plane plane[2];
-    };
     conv_bwd_orth_desc d;
     int32_t pitch = 0, most_parts = 0, pairs = 0, cluster = 0;  // cluster: the kernel for small matrices
     bool wide = false;
     std::vector<float> coef;
     double *partial = nullptr;
-    Matrix x[2], gram, poly;
-    OrthParams run;  // all but the caller's tensors
+    __half *x[2] = {};  // planes of the first X
+    OrthParams run;     // all but the caller's tensors
     DevicePart dev;
 };
 
@@ -755,6 +748,83 @@ static bool map_plane(CUtensorMap *m, void *at, int64_t batch, int64_t rows, int
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether `steps` steps may go by polynomials of several of them, `joined` at most in one.  X^T X's rounding reaches a
+// direction of singular value s by |dQ/d(s^2)| s, which for three steps with a = 3.4445 is what three steps apart lose and for
+// five ten times as much; it grows by the fifth power of a.  And all matrices must stay within the planes' range: X
+// begins with singular values in [0, 1], and what becomes of those is followed.
+static bool orth_may_join(const float *coef, int steps, int joined) {
+    for (int k = 0; k < steps; ++k)
+        if (std::fabs(coef[3 * k]) > 4.f || std::fabs(coef[3 * k + 1]) > 6.f || std::fabs(coef[3 * k + 2]) > 6.f) return false;
+    constexpr int POINTS = 4096;
+    for (int i = 0; i <= POINTS; ++i) {
+        double x = (double)i / POINTS;
+        for (int k0 = 0; k0 < steps; k0 += joined) {
+            double gram = x * x, q = 1.0;
+            for (int k = k0; k < std::min(k0 + joined, steps); ++k) {
+                const double b = coef[3 * k] + (coef[3 * k + 1] + coef[3 * k + 2] * gram) * gram;
+                q *= b;
+                if (!(std::fabs(b) < 100.0 && std::fabs(q) < 100.0 && std::fabs(b * gram) < 30.0 && gram < 30.0)) return false;
+                gram *= b * b;
+            }
+            x *= q;
+        }
+    }
+    return true;
+}
+// The products of all steps: joined ones first multiply the symmetric polynomials, and X by their product.
+static bool orth_phases(OrthParams &q, const float *coef, int steps, int joined) {
+    int64_t first = 0, need = 0, next = 0;
+    int n = 0;
+    auto add = [&](int kind, int a, int b, int out, float mul, const float *poly = nullptr, bool beside = false) {
+        if (!beside) need = next;
+        OrthPhase &f = q.phase[n++];
+        std::memset(&f, 0, sizeof(f));
+        f.first = (int32_t)first;
+        f.need = (int32_t)need;
+        f.kind = (int8_t)kind; f.a = (int8_t)a; f.b = (int8_t)b; f.out = (int8_t)out;
+        f.mul = mul;
+        if (poly) {
+            f.poly = 1;
+            f.mul = poly[2] * (kOrthUpPoly / (kOrthUp * kOrthUp));
+            f.add = poly[1] * (kOrthUpPoly / kOrthUp);
+            f.diag = poly[0] * kOrthUpPoly;
+        }
+        const int tiles = kind == kOrthProduct ? q.tiles_all : q.tiles_sym;
+        first += (int64_t)q.batch * tiles * q.splits[kind];
+        next += 16 * tiles;  // the epilogue warps of a pair
+    };
+    enum { GRAM = 2, POLY = 3, GRAM2 = 4, TEMP = 5, FACTOR = 6, POLY2 = 7 };
+    int x = 0;
+    for (int k0 = 0; k0 < steps; k0 += joined) {
+        const int m = std::min(joined, steps - k0);
+        int gram = GRAM, poly = POLY;
+        add(kOrthGram, x, x, gram, 1.f / kOrthUp);
+        for (int k = 0; k < m; ++k) {
+            const int factor = k ? FACTOR : POLY;  // this step's own
+            add(kOrthSquare, gram, gram, factor, 0.f, coef + 3 * (k0 + k));
+            if (k + 1 < m) add(kOrthSquare, factor, gram, TEMP, 1.f / kOrthUpPoly);
+            if (k) {  // (the pieces of a split tile have one place in the workspace)
+                const int to = poly == POLY ? POLY2 : POLY;
+                add(kOrthSquare, factor, poly, to, 1.f / kOrthUpPoly, nullptr, k + 1 < m && q.splits[kOrthSquare] == 1);
+                poly = to;
+            }
+            if (k + 1 < m) {
+                const int to = gram == GRAM ? GRAM2 : GRAM;
+                add(kOrthSquare, TEMP, factor, to, 1.f / kOrthUpPoly);
+                gram = to;
+            }
+        }
+        const bool last = k0 + m >= steps, high = q.rows > q.cols;
+        add(kOrthProduct, high ? x : poly, high ? poly : x, 1 - x, last ? 1.f / (kOrthUp * kOrthUpPoly) : 1.f / kOrthUpPoly);
+        q.phase[n - 1].last = last;
+        x = 1 - x;
+    }
+    q.phases = n;
+    q.phase[n].first = (int32_t)first;
+    q.matrices = joined > 1 ? kOrthMatrices : 4;
+    return first <= kMostRows && next <= kMostRows;
+}
+
 conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_plan *out) {
     if (!out) return CONV_BWD_ERR_INVALID_ARG;
     *out = nullptr;
@@ -784,8 +854,7 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         OrthParams &q = p.run;
         std::memset(&q, 0, sizeof(q));
         q.pitch_gram = (int32_t)((g + 7) / 8 * 8);
-        q.rows = (int32_t)d->rows; q.cols = (int32_t)d->cols; q.batch = (int32_t)d->batch; q.steps = d->steps;
-        std::copy(d->coefficients, d->coefficients + 3 * d->steps, q.coef);
+        q.rows = (int32_t)d->rows; q.cols = (int32_t)d->cols; q.batch = (int32_t)d->batch;
         p.pairs = sms > 1 ? orth_pairs(sms) : 0;
         if (sms > 1 && p.pairs < 1) return CONV_BWD_ERR_CUDA;
         const int64_t pairs = std::max(1, p.pairs);
@@ -807,16 +876,16 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         q.splits[0] = splits(q.tiles_sym, h);
         q.splits[1] = splits(q.tiles_sym, g);
         q.splits[2] = splits(q.tiles_all, g);
-        const int64_t items = d->batch * (q.tiles_sym * (int64_t)(q.splits[0] + q.splits[1]) + (int64_t)q.tiles_all * q.splits[2]) * d->steps;
-        if (items > kMostRows || 2 * 8 * (2 * (int64_t)q.tiles_sym + q.tiles_all) * d->steps > kMostRows) return CONV_BWD_ERR_UNSUPPORTED;
-        q.items = (int32_t)items;
+        // Three steps at a time where X is large beside its Gram matrix.
+        const int joined = h >= 2 * g && orth_may_join(d->coefficients, d->steps, kOrthJoined) ? kOrthJoined : 1;
+        if (!orth_phases(q, d->coefficients, d->steps, joined)) return CONV_BWD_ERR_UNSUPPORTED;
         auto lines = [](size_t n) { return (n + 255) / 256 * 256; };
         const bool split = q.splits[0] > 1 || q.splits[1] > 1 || q.splits[2] > 1;
         const size_t arrived = split ? lines((size_t)pairs * 16 * 4) : 0, parts = split ? (size_t)pairs * 256 * w * 4 : 0;
         const size_t done = lines((size_t)d->batch * 4), partial = lines((size_t)d->batch * p.most_parts * 16),
                      whole = lines((size_t)d->batch * d->rows * p.pitch * 2), square = lines((size_t)d->batch * g * q.pitch_gram * 2);
         p.dev.counters = 256 + arrived;
-        const conv_bwd_status st = p.dev.init(256 + arrived + parts + done + partial + 4 * whole + 4 * square);
+        const conv_bwd_status st = p.dev.init(256 + arrived + parts + done + partial + 4 * whole + (q.matrices - 2) * 2 * square);
         if (st != CONV_BWD_OK || !p.dev.has_device) return st;
         char *at = static_cast<char *>(p.dev.mem) + 256;
         q.arrived = reinterpret_cast<int32_t *>(at);
@@ -828,40 +897,18 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         p.partial = reinterpret_cast<double *>(at);
         at += partial;
         bool ok = true;
-        auto place = [&](conv_bwd_orth_plan_s::Matrix &m, int64_t rows, int64_t cols, int64_t pitch, size_t bytes) {
-            for (int i = 0; i < 2; ++i, at += bytes) {
-                m.at[i] = reinterpret_cast<__half *>(at);
-                auto &q = m.plane[i];
-                ok = ok && map_plane(&q.rows128, at, d->batch, rows, cols, pitch, 64, 128) &&
-                     map_plane(&q.rows64, at, d->batch, rows, cols, pitch, 64, 64) &&
-                     map_plane(&q.store, at, d->batch, rows, cols, pitch, 64, 32);
+        for (int i = 0; i < q.matrices; ++i) {
+            const bool x = i < 2;
+            const int64_t rows = x ? d->rows : g, cols = x ? d->cols : g, pitch = x ? p.pitch : q.pitch_gram;
+            for (int plane = 0; plane < 2; ++plane, at += x ? whole : square) {
+                q.at[i][plane] = reinterpret_cast<__half *>(at);
+                ok = ok && map_plane(&q.maps[i].rows128[plane], at, d->batch, rows, cols, pitch, 64, 128) &&
+                     map_plane(&q.maps[i].rows64[plane], at, d->batch, rows, cols, pitch, 64, 64) &&
+                     map_plane(&q.maps[i].store[plane], at, d->batch, rows, cols, pitch, 64, 32);
+                if (i == 0) p.x[plane] = reinterpret_cast<__half *>(at);
             }
-        };
-        place(p.x[0], d->rows, d->cols, p.pitch, whole);
-        place(p.x[1], d->rows, d->cols, p.pitch, whole);
-        place(p.gram, g, g, q.pitch_gram, square);
-        place(p.poly, g, g, q.pitch_gram, square);
-        if (!ok) return CONV_BWD_ERR_CUDA;
-        // operands that run along the contraction come in boxes of their rows, else in boxes of 64 x 64
-        for (int i = 0; i < 2; ++i) {
-            for (int k = 0; k < 2; ++k) {
-                const auto &x = p.x[k].plane[i];
-                q.x_gram_a[k][i] = high ? x.rows64 : x.rows128;
-                q.x_gram_b[k][i] = high || !p.wide ? x.rows64 : x.rows128;
-                q.x_prod[k][i] = high ? x.rows128 : x.rows64;
-                q.x_store[k][i] = x.store;
-            }
-            const auto &gram = p.gram.plane[i], &poly = p.poly.plane[i];
-            q.gram[i] = p.gram.at[i];
-            q.gram_a[i] = gram.rows128;
-            q.gram_b[i] = p.wide ? gram.rows128 : gram.rows64;
-            q.gram_cross[i] = gram.rows64;
-            q.gram_store[i] = gram.store;
-            q.poly_a[i] = poly.rows128;
-            q.poly_b[i] = p.wide ? poly.rows128 : poly.rows64;
-            q.poly_cross[i] = poly.rows64;
-            q.poly_store[i] = poly.store;
         }
+        if (!ok) return CONV_BWD_ERR_CUDA;
         q.status = p.dev.status();
         q.wait_budget = (int64_t)p.dev.clock_khz * 2000;
         return CONV_BWD_OK;
@@ -899,8 +946,8 @@ static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const 
         std::copy(p->coef.begin(), p->coef.end(), q.coef);
         return launch_orth_small(q, s) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
     }
-    pp.hi = p->x[0].at[0];
-    pp.lo = p->x[0].at[1];
+    pp.hi = p->x[0];
+    pp.lo = p->x[1];
     pp.partial = p->partial;
     pp.done = p->run.done;
     pp.batch = (int32_t)d.batch; pp.rows = (int32_t)d.rows; pp.cols = (int32_t)d.cols; pp.pitch = p->pitch;

@@ -11,7 +11,10 @@ element, the norm at the start 2^-23.  (One product of fp16 or bf16 operands eac
 Results in bf16 come of accumulators with 96 truncations, which is D's 2^-20 in the steps before the last 2^-18 instead, and of
 a last product B X of fp16 operands alone, off by 2^-12 (|B|_F |X|_2 + |B|_2 |X|_F) < 2^-9.2 |X'|_F in the worst case (|B| < 3.5,
 |X|_2 < 1.3).  They have no room of their own: rounding to the nearest bf16 is off by 0.42 half steps in the root mean square (uniform
-within the half step, which is 2^-9 to 2^-8 of an element), the two together by less than 0.65 of the half step that is given."""
+within the half step, which is 2^-9 to 2^-8 of an element), the two together by less than 0.65 of the half step that is given.
+
+Where the larger side is twice the smaller one, three steps are one polynomial of the Gram matrix; they are held to the D of
+steps apart."""
 import math
 
 import pytest
@@ -107,6 +110,36 @@ def test_coefficients(T, coefs, shape):
     # (a later step multiplies an error by at most |a| + 3 |b| s^2 + 5 |c| s^4, s below 1.3)
     grow = max(1.0, max(abs(a) + 5.1 * abs(b) + 14.3 * abs(c) for a, b, c in coefs)) if len(coefs) == 3 else 1.0
     check(plan.apply(u), x, off * grow ** 2)
+
+
+# the larger side at least twice the smaller one, or not quite
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 150, 300), (2, 150, 299), (3, 1300, 200), (1, 257, 2000), (30, 300, 1024), (30, 1100, 520), (1, 3000, 1400), (2, 130, 5000)])
+@pytest.mark.parametrize("kind", ["falling", "flat"])
+def test_steps_joined_in_one_polynomial(T, dtype, shape, kind):
+    """Held to what steps apart are held to."""
+    x = matrices(shape, kind, 3, DT[dtype])
+    plan = T.Orthogonal(*shape, dtype)
+    check(plan.apply(x), *iterate(x, [COEF] * 5), shape)
+    assert plan.status() == (0, 0)
+
+
+@pytest.mark.parametrize("shape", [(2, 160, 400), (2, 700, 140), (40, 260, 530)])
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 7, 12])
+def test_any_number_of_joined_steps(T, shape, steps):
+    x = matrices(shape, "falling", 5)
+    check(T.Orthogonal(*shape, "f32", steps).apply(x), *iterate(x, [COEF] * steps))
+
+
+@pytest.mark.parametrize("coefs", [[(1.5, -0.5, 0.0)] * 9, [(8.2, -23.0, 16.0), (4.0, -2.9, 0.5), (1.875, -1.25, 0.375)], [(4.0, -6.0, 3.0)] * 3, [(0.0, 0.0, 6.0)] * 3, [(4.0, 6.0, 6.0), (1.0, 0.0, 0.0), (0.5, 0.0, 0.0)],
+                                   [(2.0, -1.5, 0.5), (0.0, 1.0, 0.0), (-2.0, 0.5, 0.0), (3.0, -3.2, 1.2)]])
+@pytest.mark.parametrize("shape", [(2, 140, 300), (2, 300, 140)])
+def test_coefficients_of_joined_steps(T, coefs, shape):
+    """Large ones, and ones whose products would leave the planes' range, among them: those steps go apart."""
+    x = matrices(shape, "flat", 7)
+    plan = T.Orthogonal(*shape, "f32", len(coefs), coefs)
+    check(plan.apply(x), *iterate(x, coefs))
+    assert plan.status() == (0, 0)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
