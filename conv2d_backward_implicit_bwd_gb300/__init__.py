@@ -5,7 +5,8 @@ Modules:
   binding    ctypes binding of the C ABI (loads lib/libconv_bwd_data.so; raises
              if it is missing -- there is no CPU fallback)
   train      training-step operators on the same library (include/conv_bwd_train.h):
-             products grouped by expert, gradient clipping, the clipped policy loss
+             products grouped by expert, gradient clipping, the clipped policy loss,
+             token log-probabilities, orthogonalised updates
   build      in-tree nvcc build of the library
   workloads  seeded synthetic inputs and the named problem shapes
 

@@ -5,12 +5,19 @@
 //   gram     A = X X^T                  or X^T X
 //   square   B = c A A + b A + a I
 //   product  X' = B X                   or X B
-// three products a step; the first two are symmetric: of their results only the blocks of 256 from the diagonal on are
+// three products a step; where X is large beside A, up to three steps go together: all is polynomials of A, which commute, so
+//   T = B A, A' = T B, B' = c A' A' + b A' + a I, Q = B' B (, T' = B' A', A'' = T' B', B'' = ..., Q' = B'' Q)
+//   X' = Q X                 or X Q
+// with two products over the larger side where there were four (six), and symmetric ones instead.  (1024 x 2048, five steps
+// in fp32: the error of three and two joined is that of steps apart on spectra flat, falling and of few directions over
+// noise; all five joined lose ten times as much beside small singular values.)
+//
+// The products of polynomials are symmetric: of their results only the blocks of 256 from the diagonal on are
 // computed and kept, and where an operand lies below it the block above is read across.  (Written transposed as well, each
 // tile took 2 to 5 us longer.)
 //
-// Schedule.  One cooperative launch does all the products: a list of tiles in order of step, product, matrix; pair b of P
-// takes tiles b, b + P, ...  A tile begins when its matrix's tiles of the product before are done (a counter for each
+// Schedule.  One cooperative launch does all the products: a list of tiles in order of product, then matrix; pair b of P
+// takes tiles b, b + P, ...  A tile begins when its matrix's tiles of the products before are done (a counter for each
 // matrix), which in a batch is long past when the list comes round: no product ends with idle SMs, and there is one launch
 // instead of fifteen.  (The tile with the lowest number that is not done waits for none that is not, and its pair is at it: the
 // waits end.)  Where a product has fewer tiles than there are pairs its contraction is split, and the warp that comes last
@@ -21,14 +28,14 @@
 // So the matrices between the products are pairs of fp16, hi + lo (22 bits), times 2^10 (the polynomial B 2^8) so that lo
 // stays a normal number; a product is hi hi + hi lo + lo hi, on the tensor cores in fp32.  (fp16 rather than bf16: 22 bits
 // instead of 16 at the same rate.  Singular values stay below 1.3 with the usual coefficients; B may reach 255, which the
-// host's bound of 32 on each coefficient keeps below singular values of 1.5.)  The
+// host's bound of 32 on each coefficient keeps below singular values of 1.5; what is joined the host has followed.)  The
 // accumulator truncates, about 2^-26 of the sum with each instruction; a new one is begun every `segment` k-blocks and
 // added in fp32 registers, under the other accumulator's MMAs.  Every two k-blocks the result's error is that of the same
 // products in fp32 (1024 x 2048, 8 directions over 1 % noise: 4.5e-5; every eight 1.4e-4, never 2.0e-4), but the sums take
-// power, and power is what bounds large batches: 32 of 1024 x 2048 3163, 2889 and 2825 us.  So fp32 results take two, bf16
+// power, and power is what bounds large batches: 32 of 1024 x 2048, steps apart, 2859, 2598 and 2553 us.  So fp32 results take two, bf16
 // results and steps on weights (of which X is a hundredth) eight.  A bf16 result's last product takes the hi halves alone: what
-// that rounds no later step multiplies (the result's error 1.04 times bf16's own at most; the whole last step so 1.55 times,
-// at 79 x 2800; 32 of 1024 x 2048 2585 instead of 2716 us).
+// that rounds no later step multiplies (the result's error 1.07 times bf16's own at most, the whole last step so 1.55 times;
+// 32 of 1024 x 2048, steps apart, 2598 instead of 2728 us).
 //
 // The tile is 256 x W on a pair of SMs (tcgen05 cta_group::2), two accumulators in TMEM; a k-block of 64 brings both
 // halves of both operands, 64 KB a CTA for W = 256, and feeds twelve 16-deep MMAs, so loads are a third of what a plain

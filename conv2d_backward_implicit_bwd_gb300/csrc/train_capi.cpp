@@ -876,8 +876,13 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         q.splits[0] = splits(q.tiles_sym, h);
         q.splits[1] = splits(q.tiles_sym, g);
         q.splits[2] = splits(q.tiles_all, g);
-        // Three steps at a time where X is large beside its Gram matrix.
-        const int joined = h >= 2 * g && orth_may_join(d->coefficients, d->steps, kOrthJoined) ? kOrthJoined : 1;
+        // Three steps at a time (two products over the larger side instead of six, ten symmetric ones instead of three) where
+        // X is large beside its Gram matrix, and sooner where products fill the machine than where each is a round of tiles.
+        // (Joined, apart: 32 of 1024 x 2048 2109, 2632 us, x 1536 1904, 2118, x 1280 1794, 1846, x 1024 1676, 1556; 2 of 1024 x
+        // 4096 356, 443; 1 of 200 x 4096 168, 190; 1000 x 1500 274, 235; 20 of 300 x 512 200, 184, of 256 x 600 163, 167.  Two
+        // at a time: 2284, 394, 180 for those of 1024 x 2048, 1024 x 4096, 200 x 4096.)
+        const bool join = h >= 2 * g || (p.wide && 4 * h >= 5 * g);
+        const int joined = join && orth_may_join(d->coefficients, d->steps, kOrthJoined) ? kOrthJoined : 1;
         if (!orth_phases(q, d->coefficients, d->steps, joined)) return CONV_BWD_ERR_UNSUPPORTED;
         auto lines = [](size_t n) { return (n + 255) / 256 * 256; };
         const bool split = q.splits[0] > 1 || q.splits[1] > 1 || q.splits[2] > 1;

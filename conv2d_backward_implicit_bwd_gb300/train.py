@@ -1,5 +1,6 @@
 """Training-step operators: products grouped by expert, gradient clipping, the
-clipped policy loss (ctypes binding of include/conv_bwd_train.h).
+clipped policy loss, token log-probabilities with entropy and alternatives,
+orthogonalised updates (ctypes binding of include/conv_bwd_train.h).
 
 Argument checks and marshalling only, as in ``binding``: every step of the
 computation runs in the CUDA library.  Tensors are torch CUDA tensors; shapes,

@@ -2,11 +2,14 @@
  * conv_bwd_train.h -- C ABI of the training-step operators that surround a
  * backward-data pass: matrix products grouped by expert with ragged sizes
  * (forward, data gradient, weight gradient), the global gradient norm with
- * clipping, and the clipped policy loss with a KL term (forward, backward).
+ * clipping, the clipped policy loss with a KL term (forward, backward), the
+ * log-probabilities of given tokens with entropy and the largest alternatives
+ * (forward, backward), and orthogonalised updates of weight matrices.
  *
- * They chain as one step of a policy-tuned expert model: the loss gives
+ * They chain as one step of a policy-tuned expert model: the log-probabilities
+ * of the answers are the loss's old and reference ones, the loss gives
  * dlogits, the expert products carry it to the rows and to the filters, the
- * clip scales the gradients that come out.
+ * clip scales the gradients that come out, the updates take them to the weights.
  *
  * Conventions are those of conv_bwd_data.h: every call returns a
  * conv_bwd_status and throws nothing; tensors are row-major device memory
@@ -259,8 +262,8 @@ conv_bwd_status conv_bwd_logp_get_status(conv_bwd_logp_plan plan, void *stream, 
  * summed in fp32: against exact arithmetic X is off by some 2^-16 of its norm
  * (a rounding of u's size grows by a a step beside a small singular value); for a
  * bf16 result the last product's are held to 11 bits, a fourth of what bf16 rounds.  They are
- * fp16 pairs with a range: where X's singular values leave [0, 60] or a + b s^2 + c s^4 leaves
- * [-255, 255] between the steps, the result is not finite. */
+ * fp16 pairs with a range: where X's singular values s leave [0, 8) or a + b s^2 + c s^4 leaves
+ * [-255, 255] between the steps, the result may not be finite. */
 typedef struct {
     int64_t batch, rows, cols;
     int32_t dtype;               /* conv_bwd_dtype of x and out, resp. of grad */
@@ -269,8 +272,8 @@ typedef struct {
 } conv_bwd_orth_desc;
 
 typedef struct conv_bwd_orth_plan_s *conv_bwd_orth_plan;
-/* The plan's workspace is 8 bytes an element and 8 bytes for each element of
- * the smaller side's square.  Errors: INVALID_ARG (a size or steps < 1, unknown dtype, NULL or too
+/* The plan's workspace is 8 bytes an element and 8, where the larger side is far
+ * the larger one 24, bytes for each element of the smaller side's square.  Errors: INVALID_ARG (a size or steps < 1, unknown dtype, NULL or too
  * large coefficients), UNSUPPORTED (batch > 65535, a side > 65536, more than
  * 2^34 elements, steps > 64), CUDA (allocation failed). */
 conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *desc, conv_bwd_orth_plan *out);

@@ -114,7 +114,7 @@ def test_coefficients(T, coefs, shape):
 
 # the larger side at least twice the smaller one, or not quite
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("shape", [(2, 150, 300), (2, 150, 299), (3, 1300, 200), (1, 257, 2000), (30, 300, 1024), (30, 1100, 520), (1, 3000, 1400), (2, 130, 5000)])
+@pytest.mark.parametrize("shape", [(2, 150, 300), (2, 150, 299), (3, 1300, 200), (1, 257, 2000), (30, 300, 1024), (30, 1100, 520), (1, 3000, 1400), (2, 130, 5000), (90, 300, 375), (90, 380, 300)])
 @pytest.mark.parametrize("kind", ["falling", "flat"])
 def test_steps_joined_in_one_polynomial(T, dtype, shape, kind):
     """Held to what steps apart are held to."""
