@@ -76,6 +76,7 @@ struct Cfg {
 struct Bars {
     uint64_t full[MOST_STAGES], empty[MOST_STAGES], tfull[2], tempty[2];
     uint64_t ready[READY];  // the operands of a piece are there, pieces in turn
+    uint64_t old[EPI];      // a warp's part of A has come
     uint32_t tmem;
     int32_t abort;
 };
@@ -170,6 +171,12 @@ __device__ __forceinline__ void store_box(const CUtensorMap *map, uint32_t src, 
                  "r"(c0), "r"(c1), "r"(c2), "r"(src)
                  : "memory");
     bulk_commit();
+}
+
+__device__ __forceinline__ void load_box(const CUtensorMap *map, uint32_t dst, uint32_t bar, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
 }
 
 // One warp's 32 rows x COLS columns of a tile, in registers, to the planes hi and lo.
@@ -316,6 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
             mbar_init(tempty0 + 8 * b, 2 * EPI);  // epilogue warps of both CTAs
         }
         for (int i = 0; i < READY; ++i) mbar_init(ready0 + 8 * i, 1);
+        for (int i = 0; i < EPI; ++i) mbar_init(smem_u32(&bars.old[i]), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async_smem();
@@ -346,15 +354,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
         uint8_t *slab = stage + warp * 4096;
         uint32_t use = 0, piece = 0;
         int ph = 0;
-        bool ok = true;
+        bool ok = true, fetching = false;
+        const uint32_t old_bar = smem_u32(&bars.old[warp]);
         for (int i = pair; i < total; i += npairs, ++piece) {
             const Work w = work_at<W>(p, i, ph);
             const OrthPhase &f = p.phase[ph];
             const int row = w.m0 + (int)rank * 128 + (warp % 4) * 32, col0 = (warp / 4) * COLS, col = w.n0 + col0;
-            // a polynomial adds to A: by other SMs in this launch, so past L1; narrow tiles have the registers to read it ahead
-            constexpr int AHEAD = W == 256 ? 1 : COLS / 8;
-            uint4 old_hi[AHEAD], old_lo[AHEAD];
-            auto old_at = [&](int plane, int q) {
+            // A polynomial adds to A, by other SMs in this launch.  Narrow tiles fetch their part under the MMAs, plane by plane
+            // through the box that their results leave by; the hi half then waits in registers.  (Read from global memory, 16
+            // bytes of a row to a lane, it held up the operands' loads: 300 x 300 137 us.)  Wide tiles, whose sums leave no
+            // registers, read it past L1 afterwards, under the next tile's MMAs.
+            constexpr bool AHEAD = W != 256;
+            uint4 old_hi[AHEAD ? COLS / 8 : 1];
+            auto fetch_old = [&](int plane) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    bulk_wait_read();
+                    mbar_arrive_expect_tx(old_bar, 4096);
+                    load_box(p.maps[w.a].store + plane, smem_u32(slab), old_bar, col, row, w.e);
+                }
+                __syncwarp();
+            };
+            auto wait_old = [&](int plane) {
+                if (ok) ok = mbar_wait_bounded(old_bar, plane, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
+                ok = __all_sync(0xffffffffu, ok);
+            };
+            auto from_slab = [&](int q) { return *reinterpret_cast<const uint4 *>(slab + lane * 128 + ((q ^ (lane & 7)) << 4)); };
+            auto from_memory = [&](int plane, int q) {
                 const int r = row + lane, c = col + q * 8;
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
                 if (r < w.M && c < p.pitch_gram) v = __ldcg(reinterpret_cast<const uint4 *>(p.at[w.a][plane] + ((int64_t)w.e * w.M + r) * p.pitch_gram + c));
@@ -363,11 +390,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
             if (w.poly) {
                 if (ok) ok = mbar_wait_bounded(ready0 + 8 * (piece % READY), (piece / READY) & 1, p.wait_budget, abort_flag, p.status, kDevTimeoutEpilogue);
                 ok = __all_sync(0xffffffffu, ok);
-                if constexpr (W != 256) {
+                if constexpr (AHEAD) {
+                    static_assert(W == 256 || COLS == 64, "a box for each plane");
+                    if (ok) {
+                        fence_proxy_async_global();
+                        fetch_old(0);
+                        fetching = true;
+                        wait_old(0);
 #pragma unroll
-                    for (int q = 0; q < AHEAD; ++q) {
-                        old_hi[q] = old_at(0, q);
-                        old_lo[q] = old_at(1, q);
+                        for (int q = 0; q < COLS / 8; ++q) old_hi[q] = from_slab(q);
+                        if (ok) fetch_old(1);
                     }
                 }
             }
@@ -390,6 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                 __syncwarp();
                 if (lane == 0) arrive_relaxed(tempty_leader0 + 8 * b);
             }
+            if (AHEAD && w.poly) wait_old(1);
             if (!ok) continue;
             const int splits = p.splits[w.kind];
             if (W != 256 && splits > 1 && !join_splits<COLS>(p, w, sum, splits, (int)rank * EPI + warp, lane)) continue;
@@ -399,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                 const int r = row + lane;
 #pragma unroll
                 for (int q = 0; q < COLS / 8; ++q) {
-                    const uint4 h = W == 256 ? old_at(0, q) : old_hi[q % AHEAD], l = W == 256 ? old_at(1, q) : old_lo[q % AHEAD];
+                    const uint4 h = AHEAD ? old_hi[AHEAD ? q : 0] : from_memory(0, q), l = AHEAD ? from_slab(q) : from_memory(1, q);
                     const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -430,6 +463,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                 asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p.done + w.e) : "memory");
             }
             __syncwarp();
+        }
+        if (!ok && fetching) {
+            for (int q = 0; q < 100; ++q) __nanosleep(1000);
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
