@@ -248,6 +248,7 @@ def test_captured(T, t, v):
         out = plan.forward(z, a)
         return [*out, plan.backward(z, a, out[2], out[1], grad_logp=g, grad_entropy=g)]
     s = torch.cuda.Stream()
+    torch.cuda.synchronize()
     with torch.cuda.stream(s):
         step()
     s.synchronize()

@@ -265,6 +265,7 @@ def test_captured(T):
     w, mom, g, copy = matrices(shape, seed=5), matrices(shape, seed=6), matrices(shape, seed=7, dtype=torch.bfloat16), torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
     start = [t.clone() for t in (w, mom, g, copy)]
     graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
     with torch.cuda.stream(side):
         plan.update(w, g, mom, 0.1, copy=copy)
     side.synchronize()

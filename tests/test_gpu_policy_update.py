@@ -84,6 +84,7 @@ def test_the_step_as_a_graph(step):
         loss, _ = m.gradients(*args, args[3])
         return [loss, m.update()]
     s = torch.cuda.Stream()
+    torch.cuda.synchronize()
     with torch.cuda.stream(s):
         whole()
     s.synchronize()
