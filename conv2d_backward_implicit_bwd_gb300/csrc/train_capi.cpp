@@ -863,24 +863,25 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
             const int64_t mt = (g + 255) / 256;
             return mt * ((g + w - 1) / w) - mt * (mt - 1) / 2 * (256 / w);
         };
-        // Wide tiles where the symmetric products have one for every pair.  (50 of 489 x 1142: 915 us, narrow ones 1055; 2 of
-        // 1024 x 4096, in pieces: 430, 413; 1000 x 1000: 322, 217.)
+        // Wide tiles where the symmetric products have one for every pair.  (50 of 489 x 1142: 823 us, narrow ones 841; 32 of
+        // 1024 x 2048 2061, 2314.  In pieces where they are fewer: 2 of 1024 x 4096, steps apart, 430, narrow ones 413; 1000 x
+        // 1000 322, 217.)
         p.wide = tiles_sym(256) * d->batch >= pairs;
         const int64_t w = p.wide ? 256 : 128;
         q.tiles_sym = (int32_t)tiles_sym(w);
         q.tiles_all = (int32_t)tiles_all(w);
-        // Pieces of a contraction: where pairs would else be idle, and of eight k-blocks at least.  (A k-block takes 0.6 us, the
-        // joining of pieces 3.  1000 x 1000 in pieces of eight 216 us, of five 213, whole 235; 300 x 513 whole 143, in pieces of
-        // four 149; 200 x 2000 in pieces of eight 152, whole 177.)
-        auto splits = [&](int64_t tiles, int64_t depth) { return (int32_t)std::max<int64_t>(1, std::min({pairs / (tiles * d->batch), (depth + 63) / 64 / 8, (int64_t)kOrthSplits})); };
+        // Pieces of a contraction: where pairs would else be idle, and of five k-blocks at least.  (A k-block takes 0.6 us, the
+        // joining of pieces 3.  1000 x 1000 in pieces of five 207 us, of eight 213, whole 240; 300 x 513 whole 138, in pieces of
+        // four 142; 200 x 4096 148, whole 177.)
+        auto splits = [&](int64_t tiles, int64_t depth) { return (int32_t)std::max<int64_t>(1, std::min({pairs / (tiles * d->batch), (depth + 63) / 64 / 5, (int64_t)kOrthSplits})); };
         q.splits[0] = splits(q.tiles_sym, h);
         q.splits[1] = splits(q.tiles_sym, g);
         q.splits[2] = splits(q.tiles_all, g);
         // Three steps at a time (two products over the larger side instead of six, ten symmetric ones instead of three) where
         // X is large beside its Gram matrix, and sooner where products fill the machine than where each is a round of tiles.
-        // (Joined, apart: 32 of 1024 x 2048 2109, 2632 us, x 1536 1904, 2118, x 1280 1794, 1846, x 1024 1676, 1556; 2 of 1024 x
-        // 4096 356, 443; 1 of 200 x 4096 168, 190; 1000 x 1500 274, 235; 20 of 300 x 512 200, 184, of 256 x 600 163, 167.  Two
-        // at a time: 2284, 394, 180 for those of 1024 x 2048, 1024 x 4096, 200 x 4096.)
+        // (Joined, apart: 32 of 1024 x 2048 2061, 2572 us, x 1536 1849, 2056, x 1280 1755, 1799, x 1024 1649, 1531; 2 of 1024 x
+        // 4096 338, 424; 1 of 200 x 4096 148, 168; 1000 x 1500 256, 219; 20 of 300 x 512 171, 159, of 256 x 600 144, 147.  Two
+        // at a time took 8 to 10 % more than three.)
         const bool join = h >= 2 * g || (p.wide && 4 * h >= 5 * g);
         const int joined = join && orth_may_join(d->coefficients, d->steps, kOrthJoined) ? kOrthJoined : 1;
         if (!orth_phases(q, d->coefficients, d->steps, joined)) return CONV_BWD_ERR_UNSUPPORTED;

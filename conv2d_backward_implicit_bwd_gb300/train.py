@@ -123,9 +123,15 @@ def _stream(stream, device):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+# 0.9 us instead of 1.5 for a tensor on the current device, which in a call is the plan's (the library refuses others)
+_new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
 def _empty(shape, dtype, device, stream):
     """A new tensor whose memory belongs to the call's stream."""
     if stream is None:
+        if _new is not None and device.type == "cuda" and len(shape) < 3:
+            return _new(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype)
         return torch.empty(shape, dtype=dtype, device=device)
     s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
     with torch.cuda.stream(s):
