@@ -270,28 +270,27 @@ __device__ __forceinline__ bool join_splits(const OrthParams &p, const Work &w, 
     before = __shfl_sync(0xffffffffu, before, 0);
     if (before != splits - 1) return false;
     if (lane == 0) *counter = 0;
-    // 32 columns of all pieces at once, so that one latency covers them
+    // 32 columns of the other pieces at once, so that one latency covers them
 #pragma unroll
     for (int g = 0; g < COLS / 32; ++g) {
-        float4 x[kOrthSplits][8];
+        float4 x[kOrthSplits - 1][8];
 #pragma unroll
-        for (int k = 0; k < kOrthSplits; ++k)
+        for (int k = 0; k < kOrthSplits - 1; ++k) {
+            const int from = k + (k >= w.split);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) x[k][q] = k < splits ? __ldcg(first + k * STEP + (g * 8 + q) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int q = 0; q < 8; ++q) x[k][q] = from < splits ? __ldcg(first + from * STEP + (g * 8 + q) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            float4 t = x[0][q];
-#pragma unroll
-            for (int k = 1; k < kOrthSplits; ++k) {
-                t.x += x[k][q].x;
-                t.y += x[k][q].y;
-                t.z += x[k][q].z;
-                t.w += x[k][q].w;
-            }
-            sum[g * 32 + 4 * q] = t.x;
-            sum[g * 32 + 4 * q + 1] = t.y;
-            sum[g * 32 + 4 * q + 2] = t.z;
-            sum[g * 32 + 4 * q + 3] = t.w;
+            const int at = g * 32 + 4 * q;
+            // ((piece 0 + piece 1) + piece 2): the sum of the first two does not depend on their order
+            const float4 a = x[0][q], b = kOrthSplits > 2 ? x[kOrthSplits - 2][q] : make_float4(0.f, 0.f, 0.f, 0.f);
+            static_assert(kOrthSplits == 3, "order of the pieces");
+            auto in_order = [&](float own, float p, float r) { return w.split < 2 ? (own + p) + r : (p + r) + own; };
+            sum[at] = in_order(sum[at], a.x, b.x);
+            sum[at + 1] = in_order(sum[at + 1], a.y, b.y);
+            sum[at + 2] = in_order(sum[at + 2], a.z, b.z);
+            sum[at + 3] = in_order(sum[at + 3], a.w, b.w);
         }
     }
     return true;

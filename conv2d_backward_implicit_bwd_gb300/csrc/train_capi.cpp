@@ -870,10 +870,19 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         const int64_t w = p.wide ? 256 : 128;
         q.tiles_sym = (int32_t)tiles_sym(w);
         q.tiles_all = (int32_t)tiles_all(w);
-        // Pieces of a contraction: where pairs would else be idle, and of five k-blocks at least.  (A k-block takes 0.6 us, the
-        // joining of pieces 3.  1000 x 1000 in pieces of five 207 us, of eight 213, whole 240; 300 x 513 whole 138, in pieces of
-        // four 142; 200 x 4096 148, whole 177.)
-        auto splits = [&](int64_t tiles, int64_t depth) { return (int32_t)std::max<int64_t>(1, std::min({pairs / (tiles * d->batch), (depth + 63) / 64 / 5, (int64_t)kOrthSplits})); };
+        // Pieces of a contraction, where pairs would else be idle: as many as make the shortest round.  (A k-block takes 0.65
+        // us, the joining of two pieces 3.3, of three 3.7.  1000 x 1000 203 us, never in pieces 240; 600 x 600 in three of four
+        // k-blocks 172, whole 176; 700 x 700 in three 164, in two 170; 300 x 513 in two of five 142, whole 138.)
+        auto splits = [&](int64_t tiles, int64_t depth) {
+            const int64_t blocks = (depth + 63) / 64, most = std::min(pairs / (tiles * d->batch), (int64_t)kOrthSplits);
+            int32_t best = 1;
+            double least = 0.65 * (double)blocks;
+            for (int32_t k = 2; k <= most && k <= blocks; ++k) {
+                const double takes = 0.65 * (double)((blocks + k - 1) / k) + 3.3 + 0.4 * (k - 2);
+                if (takes < least) least = takes, best = k;
+            }
+            return best;
+        };
         q.splits[0] = splits(q.tiles_sym, h);
         q.splits[1] = splits(q.tiles_sym, g);
         q.splits[2] = splits(q.tiles_all, g);
