@@ -12,19 +12,20 @@
 // Alternatives: keys of 64 bits, the value's order above the inverted index, so the
 // largest of any set is unique (ties go to the lowest index) and the result does not
 // depend on the order of work.  Their search costs the pass nothing: each thread has
-// its elements' maximum anyway.  `top` elements lie at or above the top-th largest of
-// 32 maxima, each of eight threads' elements; only threads whose maximum is there have
-// candidates (twenty to forty for 20 alternatives), mostly in the one chunk that it came
-// from, and that chunk's vectors are read again, from L2, by the warp that ends the row,
-// while the others are at the next one.  It sorts the elements that reach the bound 32 at
-// a time.  (8192 rows of 32768 with 20 alternatives,
-// candidates taken out during the pass against a rising bound 551 us, taken out by the
-// workers after it 188.)
+// its elements' maximum anyway, and that of its other chunks.  `top` elements lie at or
+// above the top-th largest of 32 maxima, each of eight threads' elements (or of 64, of four);
+// only threads whose maximum is there have candidates (some two dozen for 20
+// alternatives), mostly in the one chunk that it came from, and that chunk's vectors are
+// read again, from L2, by the warp that ends the row, while the others are at the next
+// one.  It sorts the elements that reach the bound 32 at a time.  (8192 rows of 32768
+// with 20 alternatives 136 us, without any 97; candidates taken out during the pass
+// against a rising bound 551, taken out by the workers after it 188.)
 //
-// Rows above 16 KB stream through a ring of 16 KB buffers that one thread fills with
+// Wide rows stream through a ring of 16 KB buffers that one thread fills with
 // bulk copies, as in the policy loss; where rows are few each is cut into parts, and
 // the block that ends a row last joins the parts' sums and lists in their order.
-// Narrower rows take a warp each.
+// Rows up to 16 KB, many rows up to 32 KB, take a warp each (20000 rows of 12000 bf16 91 us,
+// through the ring 155; 1500 of them 17, 15).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -223,12 +224,20 @@ __device__ __forceinline__ K sorted_falling(K x, int lane) {
     return x;
 }
 // the 32 largest of two falling lists, falling
-__device__ __forceinline__ uint64_t merged(uint64_t a, uint64_t b, int lane) {
-    const uint64_t o = __shfl_sync(kAll, b, 31 - lane);
+template <typename K>
+__device__ __forceinline__ K merged(K a, K b, int lane) {
+    const K o = __shfl_sync(kAll, b, 31 - lane);
     a = a > o ? a : o;
 #pragma unroll
     for (int j = 16; j; j >>= 1) a = exchange(a, j, (lane & j) == 0);
     return a;
+}
+// A bound of the `top` largest from two elements of each lane (as ordered()): the top-th of the lanes' larger ones; for many
+// the top-th of all 64, above which there are 64 ln(64 / (64 - top)) elements to expect instead of 32 ln(32 / (32 - top)): 24, 31
+// at 20, 44, 130 at 32.
+__device__ __forceinline__ uint32_t bound_of(uint32_t a, uint32_t b, int top, int lane) {
+    const uint32_t s = sorted_falling(top > 16 ? a : max(a, b), lane);
+    return __shfl_sync(kAll, top > 16 ? merged(s, sorted_falling(b, lane), lane) : s, top - 1);
 }
 constexpr int kQueue = 64;
 // A warp's best: lane i has the i-th, 0 where there is none; what came last waits in the queue.
@@ -345,7 +354,15 @@ __global__ void __launch_bounds__(NT) logp_warp_kernel(const LogpParams p) {
         Run run(c);
         const bool has_head = lane < head, has_tail = tail + lane < V;
         const float ends[2] = {has_head ? Vec<T>::get(z + lane) : -INFINITY, has_tail ? Vec<T>::get(z + tail + lane) : -INFINITY};
-        float best = fmaxf(ends[0], ends[1]);
+        float best = -INFINITY, second = -INFINITY;  // of the batches, and of the others
+        int where = 0;
+        auto seen = [&](float m, int i) {
+            if constexpr (TOP) {
+                second = fmaxf(second, fminf(best, m));
+                where = m > best ? i : where;
+                best = fmaxf(best, m);
+            }
+        };
         uint4 next[UNR];
         auto fetch = [&](int i) {
 #pragma unroll
@@ -358,29 +375,55 @@ __global__ void __launch_bounds__(NT) logp_warp_kernel(const LogpParams p) {
             for (int q = 0; q < UNR; ++q) u[q] = next[q];
             if (i - lane + UNR * 32 < nv) fetch(i + UNR * 32);
             if (i - lane + UNR * 32 <= nv) {
-                best = fmaxf(best, run.template take<T>(u));
+                seen(run.template take<T>(u), i);
                 continue;
             }
+            float m = -INFINITY;
 #pragma unroll
             for (int q = 0; q < UNR; ++q) {
                 if (i - lane + q * 32 >= nv) break;
                 const uint4 one[1] = {u[q]};
-                best = fmaxf(best, run.template take<T>(one, i + q * 32 < nv));
+                m = fmaxf(m, run.template take<T>(one, i + q * 32 < nv));
             }
+            seen(m, i);
         }
         if (__any_sync(kAll, has_head || has_tail)) run.take(ends, fmaxf(ends[0], ends[1]));
         const Sums r = total(run.r);
         if constexpr (TOP) {
-            const uint32_t low = __shfl_sync(kAll, sorted_falling(ordered_number(best), lane), p.top - 1);
+            // Candidates are the lanes' ends, and mostly one batch of a lane, else all of its vectors, read by the warp
+            // or, where these are few beside the lanes, by the lane (20000 rows of 1000 bf16 with 20 alternatives 47 us, else 51; with
+            // five 40, else 35).
+            const uint32_t mine = ordered_number(best), other = ordered_number(second);
+            const uint32_t low = bound_of(ordered_number(fmaxf(best, fmaxf(ends[0], ends[1]))), other, p.top, lane);
+            const bool in = mine >= low, few = nv <= 128 && p.top > 16, more = in && (few || other >= low);
             List list(queues[sub], p.top, value_of((uint64_t)low << 32), lane);
             list.offer(has_head, ends[0], lane);
             list.offer(has_tail, ends[1], tail + lane);
-            for (int i = lane; i - lane < nv; i += 32) {
-                const bool there = best >= list.bound && i < nv;
-                if (!__any_sync(kAll, there)) continue;
-                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                if (there) u = zv[i];
-                list.offer_vector<T>(there, u, head + i * VN);
+            uint4 u[UNR];
+#pragma unroll
+            for (int q = 0; q < UNR; ++q) {
+                u[q] = make_uint4(0u, 0u, 0u, 0u);
+                if (in && !more && where + q * 32 < nv) u[q] = zv[where + q * 32];
+            }
+#pragma unroll
+            for (int q = 0; q < UNR; ++q) list.offer_vector<T>(in && !more && where + q * 32 < nv, u[q], head + (where + q * 32) * VN);
+            uint32_t who = __ballot_sync(kAll, more);
+            if (few || __popc(who) * ((nv + 1023) / 1024) > (nv + 31) / 32) {
+                for (int k = lane; k - lane < nv; k += 32) {
+                    const bool there = more && k < nv;
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (there) w = zv[k];
+                    list.offer_vector<T>(there, w, head + k * VN);
+                }
+                who = 0;
+            }
+            for (; who; who &= who - 1) {
+                const int of = __ffs(who) - 1;
+                for (int k = of + lane * 32; k - lane * 32 < nv; k += 1024) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (k < nv) w = zv[k];
+                    list.offer_vector<T>(k < nv, w, head + k * VN);
+                }
             }
             list.end();
             put_list(p, t, r, list.key, lane, c);
@@ -493,11 +536,13 @@ constexpr int WARPS = WORKERS / 32;
 constexpr int EACH = CHUNK / 16 / WORKERS;  // vectors of a thread in a chunk
 constexpr int MOST_RING = 6;
 // Blocks per SM, buffers of a block, warps that end items and the slots that they get them in.  (Three blocks of four
-// buffers, 8192 rows of 32768 bf16: 103 us forward; two of six 97.  Without the exponentials 82 and 81.)
+// buffers, 8192 rows of 32768 bf16: 103 us forward; two of six 97.  Without the exponentials 82 and 81.  With 20 alternatives
+// and four, three or two warps to end them, beside five buffers: 161, 153, 176.)
 constexpr int BLOCKS = 2;
 template <bool TOP>
 struct Shape {
-    static constexpr int RING = TOP ? 5 : 6, ENDS = TOP ? 4 : 1, SLOTS = TOP ? 4 : 2;
+    static constexpr int RING = 6, ENDS = TOP ? 3 : 1, SLOTS = TOP ? 3 : 2;
+    static_assert(ENDS <= SLOTS, "a warp waits for the use of a slot that comes next (the parity of a later one reads as done)");
     static constexpr int THREADS = WORKERS + 32 + 32 * ENDS, SMEM = CHUNK * RING + 256;
 };
 // the gradient's
@@ -679,15 +724,14 @@ __global__ void __launch_bounds__(Shape<TOP>::THREADS, BLOCKS) logp_ring_kernel(
             Sums r = join<WARPS>(sh[slot][lane % WARPS], c);
             uint64_t key = 0;
             if constexpr (TOP) {
-                // `top` elements lie at or above the top-th largest of the lanes' maxima over their eight threads
                 const Item<T> item(z, V, part, parts);
-                uint32_t m[WARPS], high = 0;
+                uint32_t m[WARPS], high[2] = {0, 0};
 #pragma unroll
                 for (int k = 0; k < WARPS; ++k) {
                     m[k] = best_of[slot][k * 32 + lane];
-                    high = max(high, m[k]);
+                    high[k % 2] = max(high[k % 2], m[k]);
                 }
-                const uint32_t low = __shfl_sync(kAll, sorted_falling(high, lane), p.top - 1);
+                const uint32_t low = bound_of(high[0], high[1], p.top, lane);
                 // where candidates are: mostly one chunk of a thread, else all of its chunks
                 int threads = 0;
                 uint32_t many = 0;  // bit k: thread 32 k + lane has them in several chunks
@@ -949,7 +993,11 @@ cudaError_t launch_backward(const LogpParams &p, bool narrow, int num_sms, cudaS
     return launch_ring(logp_grad_ring_kernel<T>, attr_set, p, p.rows, GRAD_BLOCKS * num_sms, WORKERS + 32, GRAD_SMEM, s);
 }
 
-bool narrow_rows(const LogpParams &p, int dtype) { return (int64_t)p.vocab * (dtype == 1 ? 2 : 4) <= 16384; }
+// A warp each: rows of up to 16 KB, and of up to 32 KB where there are sixteen to an SM.
+bool narrow_rows(const LogpParams &p, int dtype, int num_sms) {
+    const int64_t bytes = (int64_t)p.vocab * (dtype == 1 ? 2 : 4);
+    return bytes <= 16384 || (bytes <= 32768 && p.rows >= 16 * num_sms);
+}
 
 }  // namespace
 
@@ -964,7 +1012,7 @@ int logp_parts(int64_t rows, int64_t vocab, int dtype, int num_sms) {
 }
 
 cudaError_t launch_logp(const LogpParams &p, int dtype, bool backward, int num_sms, cudaStream_t s) {
-    const bool narrow = narrow_rows(p, dtype);
+    const bool narrow = narrow_rows(p, dtype, num_sms);
     if (backward) return dtype == 1 ? launch_backward<__nv_bfloat16>(p, narrow, num_sms, s) : launch_backward<float>(p, narrow, num_sms, s);
     if (p.top) return dtype == 1 ? launch_forward<__nv_bfloat16, true>(p, narrow, num_sms, s) : launch_forward<float, true>(p, narrow, num_sms, s);
     return dtype == 1 ? launch_forward<__nv_bfloat16, false>(p, narrow, num_sms, s) : launch_forward<float, false>(p, narrow, num_sms, s);
