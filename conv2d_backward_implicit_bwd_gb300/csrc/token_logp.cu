@@ -235,7 +235,18 @@ __device__ __forceinline__ K merged(K a, K b, int lane) {
 // A bound of the `top` largest from two elements of each lane (as ordered()): the top-th of the lanes' larger ones; for many
 // the top-th of all 64, above which there are 64 ln(64 / (64 - top)) elements to expect instead of 32 ln(32 / (32 - top)): 24, 31
 // at 20, 44, 130 at 32.
+// For few the maximum is taken off again and again, which takes less than a sorting network (8192 rows of 32768 bf16, five: 122
+// us, sorted 124).
 __device__ __forceinline__ uint32_t bound_of(uint32_t a, uint32_t b, int top, int lane) {
+    if (top <= 10) {
+        uint32_t x = max(a, b), m = 0;
+#pragma unroll 1
+        for (int i = 0; i < top; ++i) {
+            m = __reduce_max_sync(kAll, x);
+            if (lane == __ffs(__ballot_sync(kAll, x == m)) - 1) x = 0;
+        }
+        return m;
+    }
     const uint32_t s = sorted_falling(top > 16 ? a : max(a, b), lane);
     return __shfl_sync(kAll, top > 16 ? merged(s, sorted_falling(b, lane), lane) : s, top - 1);
 }
@@ -633,7 +644,9 @@ struct __align__(16) Part {
 };
 static_assert(sizeof(Part) == kLogpPart, "workspace");
 
-// The largest of all parts' lists, by one warp, a part to a lane.
+constexpr int kFewParts = 4;
+// The largest of all parts' lists, by one warp, a part to a lane.  (Of a few parts, whose lists are read beside their sums: merged one by
+// one; 64 rows of 128000 bf16, five alternatives: 13.1 us, the other way 15.7.)
 __device__ __forceinline__ uint64_t best_of_parts(const Part *row, int parts, int top, uint64_t *queue, int lane) {
     List list(queue, top, -INFINITY, lane);
     for (int q0 = 0; q0 < parts; q0 += 32) {
@@ -795,6 +808,11 @@ __global__ void __launch_bounds__(Shape<TOP>::THREADS, BLOCKS) logp_ring_kernel(
                 if (arrived != parts - 1) continue;
                 __threadfence();
                 if (lane == 0) p.arrived[t] = 0;
+                uint64_t lists[TOP ? kFewParts : 1];
+                if constexpr (TOP) {
+#pragma unroll
+                    for (int q = 0; q < kFewParts; ++q) lists[q] = parts <= kFewParts && q < parts ? __ldcg(reinterpret_cast<const unsigned long long *>(&row[q].key[lane])) : 0;
+                }
                 r = {-INFINITY, 0.f, 0.f};
                 for (int q0 = 0; q0 < parts; q0 += 32) {
                     const int q = q0 + lane;
@@ -807,7 +825,16 @@ __global__ void __launch_bounds__(Shape<TOP>::THREADS, BLOCKS) logp_ring_kernel(
                     r.s += one.s;
                     r.t += one.t;
                 }
-                if constexpr (TOP) key = best_of_parts(row, parts, p.top, queues[me], lane);
+                if constexpr (TOP) {
+                    if (parts <= kFewParts) {
+                        key = lists[0];
+#pragma unroll
+                        for (int q = 1; q < kFewParts; ++q)
+                            if (q < parts) key = merged(key, lists[q], lane);
+                    } else {
+                        key = best_of_parts(row, parts, p.top, queues[me], lane);
+                    }
+                }
             }
             if (!ok || *abort_flag) continue;
             if (lane == 0) put_sums(p, t, r, za, c);
