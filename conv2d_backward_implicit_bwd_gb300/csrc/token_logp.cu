@@ -1031,7 +1031,7 @@ bool narrow_rows(const LogpParams &p, int dtype, int num_sms) {
 int logp_most_items(int num_sms) { return BLOCKS * num_sms; }
 
 // Parts of a row: as many as the blocks that would else stay idle, each of 8 KB at least.  (64 rows of 128000 bf16 9.5 us, two
-// or three items to a block 11.3 and 13.3; one row in parts of 4 KB, with 20 alternatives, 14.1 instead of 12.0.)
+// or three items to a block 11.3 and 13.3; one row with 20 alternatives 11.4, in parts of 4 KB 13.5, of 16 KB 12.4.)
 int logp_parts(int64_t rows, int64_t vocab, int dtype, int num_sms) {
     const int64_t bytes = vocab * (dtype == 1 ? 2 : 4), slots = (int64_t)BLOCKS * num_sms;
     if (bytes <= 16384 || rows >= slots) return 1;
