@@ -96,6 +96,36 @@ def test_any_address(T, dtype, v, ld, shift, t):
 @pytest.mark.parametrize("t,v", [(3, 50), (4, 3000), (4, 60000), (600, 9000)])
 @pytest.mark.parametrize("kind", ["equal", "few values", "rising", "falling", "banned", "signed zeros", "one hot", "wide", "rising groups"])
 def test_alternatives_of_hard_rows(T, dtype, t, v, kind):
+    hard_rows(T, dtype, t, v, kind, 20)
+
+
+# rows of up to 32 KB, of which there are enough for a warp each
+MANY = [("bf16", 2500, 8200), ("bf16", 2433, 16384), ("bf16", 2500, 11003), ("f32", 2500, 5001), ("f32", 2440, 8192)]
+
+
+@pytest.mark.parametrize("dtype,t,v", MANY)
+@pytest.mark.parametrize("top", [0, 3, 12, 20, 32])
+def test_many_rows(T, dtype, t, v, top):
+    z, a = rows_of(t, v, dtype, seed=top, ld=v + top % 2, shift=top % 5)
+    a[1::5] = -1
+    check_forward(T.TokenLogp(v, dtype, top=top), z, a)
+
+
+@pytest.mark.parametrize("dtype,t,v", MANY[1:4])
+@pytest.mark.parametrize("kind", ["equal", "few values", "rising", "falling", "banned", "signed zeros", "one hot", "rising groups"])
+@pytest.mark.parametrize("top", [7, 30])
+def test_alternatives_of_many_hard_rows(T, dtype, t, v, kind, top):
+    hard_rows(T, dtype, t, v, kind, top)
+
+
+@pytest.mark.parametrize("v", [1024, 1023, 400])
+@pytest.mark.parametrize("top", [9, 11, 17, 32])
+def test_alternatives_of_short_hard_rows(T, v, top):
+    for kind in ("few values", "rising groups", "banned"):
+        hard_rows(T, "bf16", 50, v, kind, top)
+
+
+def hard_rows(T, dtype, t, v, kind, top):
     z, a = rows_of(t, v, dtype)
     i = torch.arange(v, device="cuda").float()
     if kind == "equal":
@@ -118,7 +148,7 @@ def test_alternatives_of_hard_rows(T, dtype, t, v, kind):
         z[:, v // 2] = 60.0
     elif kind == "wide":  # scale z c above 256: differences are taken first
         z.mul_(300)
-    check_forward(T.TokenLogp(v, dtype, top=20), z, a)
+    check_forward(T.TokenLogp(v, dtype, top=top), z, a)
 
 
 @pytest.mark.parametrize("v", [40, 5000, 50000])
@@ -172,7 +202,7 @@ def gradient(z, a, lse, h, gl, ge, scale):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("t,v,ld,shift", [(1, 1, 0, 0), (5, 33, 0, 0), (9, 1009, 0, 0), (40, 4096, 0, 0), (3, 8193, 0, 0), (7, 40001, 0, 0), (2, 128000, 0, 0), (600, 9000, 9003, 1), (20, 1000, 1001, 3)])
+@pytest.mark.parametrize("t,v,ld,shift", [(1, 1, 0, 0), (5, 33, 0, 0), (9, 1009, 0, 0), (40, 4096, 0, 0), (3, 8193, 0, 0), (7, 40001, 0, 0), (2, 128000, 0, 0), (600, 9000, 9003, 1), (20, 1000, 1001, 3), (2500, 8001, 8003, 1)])
 @pytest.mark.parametrize("which", ["both", "logp", "entropy", "in place"])
 def test_backward(T, dtype, t, v, ld, shift, which):
     plan = T.TokenLogp(v, dtype, scale=0.7)

@@ -124,6 +124,19 @@ def test_steps_joined_in_one_polynomial(T, dtype, shape, kind):
     assert plan.status() == (0, 0)
 
 
+@pytest.mark.parametrize("shape", [(2, 200, 450), (1, 1500, 300), (20, 300, 700)])
+@pytest.mark.parametrize("rank,noise", [(1, 0.0), (3, 0.0), (8, 1e-2), (8, 1e-3), (8, 1e-5), (2, 1e-1)])
+def test_joined_steps_beside_few_directions(T, shape, rank, noise):
+    """Small singular values, which the Gram matrix holds as squares."""
+    g = torch.Generator(device="cuda").manual_seed(rank)
+    b, m, n = shape
+    u = torch.randn(b, m, rank, generator=g, device="cuda") @ torch.randn(b, rank, n, generator=g, device="cuda")
+    e = torch.randn(shape, generator=g, device="cuda")
+    u = u / torch.linalg.matrix_norm(u)[:, None, None] + noise * e / torch.linalg.matrix_norm(e)[:, None, None]
+    check(T.Orthogonal(*shape, "f32").apply(u), *iterate(u, [COEF] * 5))
+    check(T.Orthogonal(*shape, "bf16").apply(u.bfloat16()), *iterate(u.bfloat16(), [COEF] * 5))
+
+
 @pytest.mark.parametrize("shape", [(2, 160, 400), (2, 700, 140), (40, 260, 530)])
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 7, 12])
 def test_any_number_of_joined_steps(T, shape, steps):
