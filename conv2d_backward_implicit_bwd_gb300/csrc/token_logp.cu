@@ -18,7 +18,7 @@
 // alternatives), mostly in the one chunk that it came from, and that chunk's vectors are
 // read again, from L2, by the warp that ends the row, while the others are at the next
 // one.  It sorts the elements that reach the bound 32 at a time.  (8192 rows of 32768
-// with 20 alternatives 136 us, without any 97; candidates taken out during the pass
+// with 20 alternatives 125 us, without any 90; candidates taken out during the pass
 // against a rising bound 551, taken out by the workers after it 188.)
 //
 // Wide rows stream through a ring of 16 KB buffers that one thread fills with
@@ -114,7 +114,7 @@ struct Run {
     float lim, room;
     bool held;
     Exps e;
-    __device__ __forceinline__ explicit Run(float c) : r{-INFINITY, 0.f, 0.f}, lim(-INFINITY), room(1.f / c), held(false), e(-INFINITY, c) {}
+    __device__ __forceinline__ Run(float c, float room_) : r{-INFINITY, 0.f, 0.f}, lim(-INFINITY), room(room_), held(false), e(-INFINITY, c) {}
     template <int N>
     __device__ __forceinline__ float2 plain(const float (&v)[N]) const {
         const uint64_t c2 = pair(e.c, e.c), off2 = pair(-e.off, -e.off);
@@ -235,8 +235,8 @@ __device__ __forceinline__ K merged(K a, K b, int lane) {
 // A bound of the `top` largest from two elements of each lane (as ordered()): the top-th of the lanes' larger ones; for many
 // the top-th of all 64, above which there are 64 ln(64 / (64 - top)) elements to expect instead of 32 ln(32 / (32 - top)): 24, 31
 // at 20, 44, 130 at 32.
-// For few the maximum is taken off again and again, which takes less than a sorting network (8192 rows of 32768 bf16, five: 122
-// us, sorted 124).
+// For few the maximum is taken off again and again, which takes less than a sorting network (8192 rows of 32768 bf16, five: 105
+// us, sorted 108).
 __device__ __forceinline__ uint32_t bound_of(uint32_t a, uint32_t b, int top, int lane) {
     if (top <= 10) {
         uint32_t x = max(a, b), m = 0;
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(NT) logp_warp_kernel(const LogpParams p) {
     __shared__ uint64_t queues[TOP ? ROWS : 1][kQueue];
     const int lane = threadIdx.x % 32, sub = threadIdx.x / 32;
     const int V = p.vocab;
-    const float c = p.scale * kLog2e;
+    const float c = p.scale * kLog2e, room = 1.f / c;
     pdl_next();
     pdl_wait();
     const int64_t step = (int64_t)gridDim.x * ROWS;
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(NT) logp_warp_kernel(const LogpParams p) {
         const int nv = (V - head) / VN, tail = head + nv * VN;
         const uint4 *zv = reinterpret_cast<const uint4 *>(z + head);
         const float za = Vec<T>::get(z + a);
-        Run run(c);
+        Run run(c, room);
         const bool has_head = lane < head, has_tail = tail + lane < V;
         const float ends[2] = {has_head ? Vec<T>::get(z + lane) : -INFINITY, has_tail ? Vec<T>::get(z + tail + lane) : -INFINITY};
         float best = -INFINITY, second = -INFINITY;  // of the batches, and of the others
@@ -546,9 +546,9 @@ constexpr int CHUNK = 16384, WORKERS = 256;
 constexpr int WARPS = WORKERS / 32;
 constexpr int EACH = CHUNK / 16 / WORKERS;  // vectors of a thread in a chunk
 constexpr int MOST_RING = 6;
-// Blocks per SM, buffers of a block, warps that end items and the slots that they get them in.  (Three blocks of four
-// buffers, 8192 rows of 32768 bf16: 103 us forward; two of six 97.  Without the exponentials 82 and 81.  With 20 alternatives
-// and four, three or two warps to end them, beside five buffers: 161, 153, 176.)
+// Blocks per SM, buffers of a block, warps that end items and the slots that they get them in.  (8192 rows of 32768 bf16: two
+// blocks of six buffers 90 us, without the exponentials 83; three of four 96.  With 20 alternatives and three warps to end
+// them 125, with two 147.)
 constexpr int BLOCKS = 2;
 template <bool TOP>
 struct Shape {
@@ -567,8 +567,13 @@ struct Item {
     __device__ __forceinline__ Item(const T *z_, int V, int part, int parts) : z(z_) {
         head = min(V, (int)((16 - ((uintptr_t)z & 15)) % 16 / sizeof(T)));
         const int nv = (V - head) / Vec<T>::N;
-        v0 = (int)((int64_t)nv * part / parts);
-        v1 = (int)((int64_t)nv * (part + 1) / parts);
+        v0 = 0;
+        v1 = nv;
+        if (parts > 1) {
+            const int each = nv / parts, more = nv - each * parts;  // the first `more` parts have one more
+            v0 = each * part + min(part, more);
+            v1 = v0 + each + (part < more ? 1 : 0);
+        }
         tail = head + nv * Vec<T>::N;
         first = part == 0;
         last = part == parts - 1;
@@ -683,7 +688,7 @@ __global__ void __launch_bounds__(Shape<TOP>::THREADS, BLOCKS) logp_ring_kernel(
     __shared__ int abort_;
     volatile int32_t *abort_flag = &abort_;
     const int V = p.vocab, warp = threadIdx.x / 32, lane = threadIdx.x % 32, parts = p.parts;
-    const float c = p.scale * kLog2e;
+    const float c = p.scale * kLog2e, room = 1.f / c;
     ring_init<RING>(bars, &abort_);
     pdl_next();
     pdl_wait();
@@ -852,7 +857,7 @@ __global__ void __launch_bounds__(Shape<TOP>::THREADS, BLOCKS) logp_ring_kernel(
         // the row's ends: at most one element of a thread before and after the vectors
         const bool has_head = item.first && tid < item.head, has_tail = item.last && item.tail + tid < V;
         const float ends[2] = {has_head ? Vec<T>::get(z + tid) : -INFINITY, has_tail ? Vec<T>::get(z + item.tail + tid) : -INFINITY};
-        Run run(c);
+        Run run(c, room);
         float best = -INFINITY, second = -INFINITY;
         int where = 0;
         const int chunks = item.chunks();
