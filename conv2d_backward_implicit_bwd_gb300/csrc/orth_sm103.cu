@@ -610,6 +610,27 @@ cudaError_t launch_steps(const OrthParams &p, int pairs, cudaStream_t s) {
 // ---- what comes before the products --------------------------------------------
 constexpr int NT = 256;
 
+// A thread's places in a matrix, V elements each: every (blocks x NT)-th.  (A 64-bit division for each place took a sixth of the time.)
+struct Places {
+    int r, c, per_row, rows_on, on;
+    __device__ __forceinline__ Places(const OrthPrepParams &p, int v) {
+        per_row = (p.cols + v - 1) / v;  // (v divides cols where v > 1)
+        const uint32_t first = blockIdx.x * NT + threadIdx.x, step = gridDim.x * NT;
+        r = (int)(first / (uint32_t)per_row);
+        c = (int)(first - (uint32_t)r * (uint32_t)per_row);
+        rows_on = (int)(step / (uint32_t)per_row);
+        on = (int)(step - (uint32_t)rows_on * (uint32_t)per_row);
+    }
+    __device__ __forceinline__ void next() {
+        r += rows_on;
+        c += on;
+        if (c >= per_row) {
+            c -= per_row;
+            ++r;
+        }
+    }
+};
+
 // Squares of u, summed by block; the momentum is updated on the way.  u = g without momentum, else m' = beta m + g and u =
 // g + beta m' (nesterov) or m'.
 template <int V, bool LINES, bool BF16>
@@ -619,11 +640,9 @@ __global__ void __launch_bounds__(NT) orth_norm_kernel(const OrthPrepParams p) {
     pdl_wait();
     const int e = blockIdx.y;
     if (blockIdx.x == 0 && threadIdx.x == 0) p.done[e] = 0;
-    const int per_row = (p.cols + V - 1) / V;  // (V divides cols where V > 1)
-    const int64_t items = (int64_t)p.rows * per_row;
     SquareSum sum = {0.f, 0.f, 0.0};
-    for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < items; i += (int64_t)gridDim.x * NT) {
-        const int r = (int)(i / per_row), c = (int)(i - (int64_t)r * per_row) * V;
+    for (Places places(p, V); places.r < p.rows; places.next()) {
+        const int r = places.r, c = places.c * V;
         const int64_t at = (int64_t)e * p.ls + (int64_t)r * p.ld + c;
         float g[V], m[V];
         load_v<V, LINES, BF16>(p.grad, at, g);
@@ -671,10 +690,8 @@ __global__ void __launch_bounds__(NT) orth_split_kernel(const OrthPrepParams p) 
     }
     __syncthreads();
     const float f0 = factor[0], f1 = factor[1], f2 = factor[2];
-    const int per_row = (p.cols + V - 1) / V;
-    const int64_t items = (int64_t)p.rows * per_row;
-    for (int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x; i < items; i += (int64_t)gridDim.x * NT) {
-        const int r = (int)(i / per_row), c = (int)(i - (int64_t)r * per_row) * V;
+    for (Places places(p, V); places.r < p.rows; places.next()) {
+        const int r = places.r, c = places.c * V;
         const int64_t at = (int64_t)e * p.ls + (int64_t)r * p.ld + c;
         float g[V], m[V];
 #pragma unroll
