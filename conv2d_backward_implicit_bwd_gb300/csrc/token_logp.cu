@@ -141,17 +141,18 @@ struct Run {
         }
         return make_float2(s, t);
     }
-    // a value beside z whose term is 0 and that is not above it
-    __device__ __forceinline__ float nothing(float z) const { return fabsf(z * e.c) < 256.f ? z - 300.f * room : -INFINITY; }
-    // elements and their maximum
+    // elements and their maximum; lanes without any take part with values whose terms are 0
     template <int N>
-    __device__ __forceinline__ void take(const float (&v)[N], float m) {
+    __device__ __forceinline__ void take(float (&v)[N], float m, bool there = true) {
         if (__any_sync(kAll, m > lim)) {
             m = warp_max(m);
             r = rebased(r, m, e.c);
             e = Exps(m, e.c);
             lim = m + room;
         }
+        const float dead = e.near && r.m != -INFINITY ? r.m - 300.f * room : -INFINITY;
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = there ? v[k] : dead;
         float2 x = make_float2(0.f, __int_as_float(0x7fffffff));
         if (N % 2 == 0 && e.near && !held) x = plain(v);
         if (__any_sync(kAll, !(x.y == x.y))) {
@@ -170,10 +171,10 @@ struct Run {
             float w[VN];
             Vec<T>::unpack(u[q], w);
 #pragma unroll
-            for (int k = 0; k < VN; ++k) v[q * VN + k] = there ? w[k] : nothing(w[k]);
+            for (int k = 0; k < VN; ++k) v[q * VN + k] = w[k];
         }
         const float m = there ? largest<T>(u) : -INFINITY;
-        take(v, m);
+        take(v, m, there);
         return m;
     }
 };
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(NT) logp_warp_kernel(const LogpParams p) {
         const float za = Vec<T>::get(z + a);
         Run run(c, room);
         const bool has_head = lane < head, has_tail = tail + lane < V;
-        const float ends[2] = {has_head ? Vec<T>::get(z + lane) : -INFINITY, has_tail ? Vec<T>::get(z + tail + lane) : -INFINITY};
+        float ends[2] = {has_head ? Vec<T>::get(z + lane) : -INFINITY, has_tail ? Vec<T>::get(z + tail + lane) : -INFINITY};
         float best = -INFINITY, second = -INFINITY;  // of the batches, and of the others
         int where = 0;
         auto seen = [&](float m, int i) {
@@ -856,7 +857,7 @@ __global__ void __launch_bounds__(Shape<TOP>::THREADS, BLOCKS) logp_ring_kernel(
         const Item<T> item(z, V, part, parts);
         // the row's ends: at most one element of a thread before and after the vectors
         const bool has_head = item.first && tid < item.head, has_tail = item.last && item.tail + tid < V;
-        const float ends[2] = {has_head ? Vec<T>::get(z + tid) : -INFINITY, has_tail ? Vec<T>::get(z + item.tail + tid) : -INFINITY};
+        float ends[2] = {has_head ? Vec<T>::get(z + tid) : -INFINITY, has_tail ? Vec<T>::get(z + item.tail + tid) : -INFINITY};
         Run run(c, room);
         float best = -INFINITY, second = -INFINITY;
         int where = 0;
