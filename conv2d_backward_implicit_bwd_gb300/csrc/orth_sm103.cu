@@ -610,7 +610,8 @@ cudaError_t launch_steps(const OrthParams &p, int pairs, cudaStream_t s) {
 // ---- what comes before the products --------------------------------------------
 constexpr int NT = 256;
 
-// A thread's places in a matrix, V elements each: every (blocks x NT)-th.  (A 64-bit division for each place took a sixth of the time.)
+// A thread's places in a matrix, V elements each: every (blocks x NT)-th.  (With a 64-bit division for each place the norm of 4 of
+// 2048 x 1024 took 17 us instead of 14.)
 struct Places {
     int r, c, per_row, rows_on, on;
     __device__ __forceinline__ Places(const OrthPrepParams &p, int v) {
