@@ -33,9 +33,9 @@
 // added in fp32 registers, under the other accumulator's MMAs.  Every two k-blocks the result's error is that of the same
 // products in fp32 (1024 x 2048, 8 directions over 1 % noise: 4.5e-5; every eight 1.4e-4, never 2.0e-4), but the sums take
 // power, and power is what bounds large batches: 32 of 1024 x 2048, steps apart, 2859, 2598 and 2553 us.  So fp32 results take two, bf16
-// results and steps on weights (of which X is a hundredth) eight.  A bf16 result's last product takes the hi halves alone: what
-// that rounds no later step multiplies (the result's error 1.07 times bf16's own at most, the whole last step so 1.55 times;
-// 32 of 1024 x 2048, steps apart, 2598 instead of 2728 us).
+// results and steps on weights (of which X is a hundredth) eight.  (A last product of the hi halves alone would be 5 to 7 % of
+// the time less, 32 of 1024 x 2048 2101 instead of 2226 us, but a bf16 result would be off by more than its own rounding:
+// by 1.3e-3 of its norm from the rounded exact one, like this by 2e-4.)
 //
 // The tile is 256 x W on a pair of SMs (tcgen05 cta_group::2), two accumulators in TMEM; a k-block of 64 brings both
 // halves of both operands, 64 KB a CTA for W = 256, and feeds twelve 16-deep MMAs, so loads are a third of what a plain
@@ -135,8 +135,6 @@ __device__ __forceinline__ Work work_at(const OrthParams &p, int i, int &ph) {
     w.kb1 = (int)((int64_t)kblocks * (w.split + 1) / splits);
     return w;
 }
-// Whether a product takes one term instead of three.
-__device__ __forceinline__ bool hi_alone(const OrthParams &p, const Work &w) { return p.last_hi && w.last; }
 // Whether an operand's lines run across the contraction in its k-block kb: X's in X^T X, and where it is multiplied from the
 // left; those of the symmetric matrices, of which only the blocks of 256 from the diagonal on are there, below it.
 __device__ __forceinline__ bool a_across(const Work &w, bool high, int kb) { return w.a > 1 ? (kb >> 2) < (w.m0 >> 8) : w.kind == kOrthGram && high; }
@@ -477,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                 bool ok = true, issued = false;
                 for (int i = pair; i < total && ok; i += npairs, ++piece) {
                     const Work w = work_at<W>(p, i, phase);
-                    const int m = w.m0 + (int)rank * 128, n = w.n0 + (int)rank * (w.n / 2), planes = hi_alone(p, w) ? 1 : 2;
+                    const int m = w.m0 + (int)rank * 128, n = w.n0 + (int)rank * (w.n / 2);
                     // What other SMs have written in this launch.  (One thread of a CTA asks for it: with every lane of the
                     // epilogue asking too, loads and counters took 3 us longer.)
                     const uint32_t bar_ready = ready0 + 8 * (piece % READY);
@@ -496,9 +494,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                             break;
                         }
                         const uint32_t bar = full_leader0 + 8 * s, to = smem_u32(smem + s * C::STAGE);
-                        if (warp == LOAD_A && leader) mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(2 * planes * (A_BYTES + C::B_BYTES)));
+                        if (warp == LOAD_A && leader) mbar_arrive_expect_tx(full0 + 8 * s, (uint32_t)(4 * (A_BYTES + C::B_BYTES)));
                         const bool mn = warp == LOAD_A ? a_across(w, high, kb) : b_across(w, high, kb);
-                        for (int k = 0; k < planes; ++k) {
+                        for (int k = 0; k < 2; ++k) {
                             const uint32_t dst = warp == LOAD_A ? to + k * A_BYTES : to + 2 * A_BYTES + k * C::B_BYTES;
                             const int at = warp == LOAD_A ? m : n;
                             if (!mn) {
@@ -525,7 +523,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
             bool ok = true, issued = false;
             for (int i = pair; i < total && ok; i += npairs) {
                 const Work w = work_at<W>(p, i, phase);
-                const bool single = hi_alone(p, w);
                 for (int left = w.kb1 - w.kb0; left > 0 && ok;) {
                     const uint32_t b = use & 1, bph = (use >> 1) & 1, d = tmem_base + b * 256;
                     ++use;
@@ -542,19 +539,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) orth_ker
                         const uint32_t id = (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(w.n >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
                         const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2, a_lead = (a_mn ? 8192u >> 4 : 1u) << 16, b_lead = (b_mn ? 8192u >> 4 : 1u) << 16;
                         const uint32_t ad = (a_at + s * (C::STAGE >> 4)) | a_lead, bd = (b_at + s * (C::STAGE >> 4)) | b_lead;
-                        if (!single) {
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                mma_pair_elect(d, ad + a_step * kk, desc_hi, bd + (C::B_BYTES >> 4) + b_step * kk, desc_hi, id, acc);
-                                acc = 1;
-                                mma_pair_elect(d, ad + (A_BYTES >> 4) + a_step * kk, desc_hi, bd + b_step * kk, desc_hi, id, acc);
-                            }
-                        }
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            mma_pair_elect(d, ad + a_step * kk, desc_hi, bd + b_step * kk, desc_hi, id, acc);
+                            mma_pair_elect(d, ad + a_step * kk, desc_hi, bd + (C::B_BYTES >> 4) + b_step * kk, desc_hi, id, acc);
                             acc = 1;
+                            mma_pair_elect(d, ad + (A_BYTES >> 4) + a_step * kk, desc_hi, bd + b_step * kk, desc_hi, id, acc);
                         }
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) mma_pair_elect(d, ad + a_step * kk, desc_hi, bd + b_step * kk, desc_hi, id, acc);
                         issued = true;
                         commit_pair_elect(empty0 + 8 * s);
                         if (++s == (uint32_t)S) {

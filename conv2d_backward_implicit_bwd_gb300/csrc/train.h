@@ -213,7 +213,6 @@ struct OrthParams {
     int32_t rows, cols, batch, matrices, phases;
     int32_t tiles_sym, tiles_all;  // tiles of a matrix: symmetric, X
     int32_t splits[3];             // by kind
-    int32_t last_hi;               // the last product takes the hi planes alone
     int32_t segment;               // k-blocks of one accumulator
     int32_t bf16, pitch_gram;
     float rate, keep;

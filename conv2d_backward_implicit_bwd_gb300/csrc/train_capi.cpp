@@ -971,7 +971,6 @@ static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const 
     if (launch_orth_prep(pp, s) != cudaSuccess) return CONV_BWD_ERR_CUDA;
     OrthParams q = p->run;
     q.segment = fp32_result ? 2 : 8;
-    q.last_hi = o.result && !fp32_result;
     q.result = o.result;
     q.bf16 = pp.bf16;
     q.weight = o.weight;

@@ -260,9 +260,8 @@ conv_bwd_status conv_bwd_logp_get_status(conv_bwd_logp_plan plan, void *stream, 
  * throughout, and the other matrices of the batch are not touched by it.  The norm
  * neither overflows nor underflows.  The products' operands are held to 22 bits and
  * summed in fp32: against exact arithmetic X is off by some 2^-16 of its norm
- * (a rounding of u's size grows by a a step beside a small singular value); for a
- * bf16 result the last product's are held to 11 bits, a fourth of what bf16 rounds.  They are
- * fp16 pairs with a range: where X's singular values s leave [0, 8) or a + b s^2 + c s^4 leaves
+ * (a rounding of u's size grows by a a step beside a small singular value), and a bf16
+ * result is rounded once, at the end.  They are fp16 pairs with a range: where X's singular values s leave [0, 8) or a + b s^2 + c s^4 leaves
  * [-255, 255] between the steps, the result may not be finite. */
 typedef struct {
     int64_t batch, rows, cols;
