@@ -256,13 +256,12 @@ __device__ __forceinline__ void store_result(const OrthParams &p, const Work &w,
 // order and goes on with the tile; false for the others.
 template <int COLS>
 __device__ __forceinline__ bool join_splits(const OrthParams &p, const Work &w, float (&sum)[COLS], int splits, int slice, int lane) {
-    const int tiles = w.kind == kOrthProduct ? p.tiles_all : p.tiles_sym, tile = w.e * tiles + w.tile;
     constexpr int STEP = 2 * EPI * 32 * COLS / 4;
-    float4 *first = p.parts + (int64_t)(tile * splits) * STEP + slice * (32 * COLS / 4) + lane;
+    float4 *first = p.parts + (int64_t)orth_piece_place(p, w.e, w.tile, splits) * STEP + slice * (32 * COLS / 4) + lane;
 #pragma unroll
     for (int q = 0; q < COLS / 4; ++q) __stcg(first + w.split * STEP + q * 32, make_float4(sum[4 * q], sum[4 * q + 1], sum[4 * q + 2], sum[4 * q + 3]));
     __syncwarp();
-    int32_t *counter = p.arrived + tile * 2 * EPI + slice;
+    int32_t *counter = p.arrived + orth_counter_place(p, w.e, w.tile) * 2 * EPI + slice;
     int before = 0;
     if (lane == 0) asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(counter) : "memory");
     before = __shfl_sync(0xffffffffu, before, 0);

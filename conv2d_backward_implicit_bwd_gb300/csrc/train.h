@@ -213,11 +213,16 @@ struct OrthParams {
     int32_t rows, cols, batch, matrices, phases;
     int32_t tiles_sym, tiles_all;  // tiles of a matrix: symmetric, X
     int32_t splits[3];             // by kind
+    int32_t own_tiles, own_pieces; // split tiles and their pieces: the most that a matrix has of one kind
     int32_t segment;               // k-blocks of one accumulator
     int32_t bf16, pitch_gram;
     float rate, keep;
     OrthPhase phase[kOrthMostPhases + 1];  // and the end
 };
+// The places of a split tile's counters and of its pieces' sums.  A matrix has its own: one may be in another product than the
+// next, and a place has another tile in every kind of product.
+__host__ __device__ inline int orth_counter_place(const OrthParams &p, int e, int tile) { return e * p.own_tiles + tile; }
+__host__ __device__ inline int orth_piece_place(const OrthParams &p, int e, int tile, int splits) { return e * p.own_pieces + tile * splits; }
 int orth_pairs(int num_sms);
 // Matrices whose smaller side is at most kOrthSmall, their larger side in `cluster` slices of `slice` columns.
 constexpr int kOrthSmall = 128, kOrthSlice = 256;

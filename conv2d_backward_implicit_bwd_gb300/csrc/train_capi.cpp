@@ -886,6 +886,12 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         q.splits[0] = splits(q.tiles_sym, h);
         q.splits[1] = splits(q.tiles_sym, g);
         q.splits[2] = splits(q.tiles_all, g);
+        for (int kind = 0; kind < 3; ++kind) {
+            if (q.splits[kind] == 1) continue;
+            const int32_t tiles = kind == kOrthProduct ? q.tiles_all : q.tiles_sym;
+            q.own_tiles = std::max(q.own_tiles, tiles);
+            q.own_pieces = std::max(q.own_pieces, tiles * q.splits[kind]);
+        }
         // Three steps at a time (two products over the larger side instead of six, ten symmetric ones instead of three) where
         // X is large beside its Gram matrix, and sooner where products fill the machine than where each is a round of tiles.
         // (Joined, apart: 32 of 1024 x 2048 2061, 2572 us, x 1536 1849, 2056, x 1280 1755, 1799, x 1024 1649, 1531; 2 of 1024 x
