@@ -47,9 +47,10 @@ constexpr uint32_t kAll = 0xffffffffu;
 struct Sums {
     float m, s, t;
 };
-// r over the reference m instead of its own
+// r over the reference m instead of its own, which lies no higher.  (Between the type's lowest value and others the exponent
+// is -inf in fp32: held where 2^up is 0 already, as 0 * -inf is not 0.)
 __device__ __forceinline__ Sums rebased(const Sums &r, float m, float c) {
-    const float up = Exps(m, c).shift(r.m, m), f = ex2(up);
+    const float up = fmaxf(Exps(m, c).shift(r.m, m), -200.f), f = ex2(up);
     return {m, r.s * f, fmaf(r.s, up, r.t) * f};
 }
 // the largest element of some vectors (what is no number counts last)
