@@ -446,12 +446,13 @@ __global__ void __launch_bounds__(NT) logp_warp_kernel(const LogpParams p) {
     }
 }
 
-// dz = p (a + b u) + cs [chosen], u = scale z - lse
+// dz = p (a + b u) + cs [chosen], u = scale z - lse with scale z rounded first, as it is in lse where that is large: u does not
+// pass 0 there.  (With one rounding, rows of the type's lowest value had u anywhere within the last bit of lse, 2^103, and p infinite.)
 struct Slope {
     float scale, lse, a, b, cs;
     int chosen;
     __device__ __forceinline__ float at(float z) const {
-        const float u = fmaf(z, scale, -lse);
+        const float u = __fmul_rn(z, scale) - lse;
         return ex2(u * kLog2e) * fmaf(b, fmaxf(u, -1e4f), a);  // (2^-inf * -inf is not 0)
     }
     __device__ __forceinline__ float one(float z, int i) const { return i == chosen ? at(z) + cs : at(z); }

@@ -209,6 +209,8 @@ conv_bwd_status conv_bwd_policy_get_status(conv_bwd_policy_plan plan, void *stre
  * +inf makes the row's logp, entropy, lse and top_logp NaN; NaNs are no
  * alternatives, and where fewer than `top` logits are left the last top_tokens are
  * -1 (top_logp NaN).  All arithmetic is fp32 or wider, dlogits are rounded once.
+ * The gradient knows p_v by lse: past |lse| = 2^16, as in a row whose logits are all
+ * the type's lowest value, only as exactly as lse's last bit, and never above 1.
  *
  * logits [rows][ld]; ld >= vocab in elements, any alignment (0 = dense). */
 typedef struct {

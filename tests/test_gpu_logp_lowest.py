@@ -40,3 +40,38 @@ def test_statistics(T, dtype, t, v, scale, top):  # noqa: F811
             assert torch.equal(tt[live], order[live].int()), kind
             want = u.gather(1, order)
             assert ((tlp.double() - want).abs() <= 2.0 ** -19 * (1 + lse.double().abs().clamp(max=1e30)[:, None] + want.abs()))[live & (want > 0.9 * lowest).all(1)].all(), kind
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("t,v", [(4, 50), (3, 9001), (400, 20000)])
+def test_gradients_of_rows_that_are_lowest_throughout(T, dtype, t, v):  # noqa: F811
+    """lse cannot hold log v beside them, but no probability is above 1: |dz| <= scale (2 |gl| + |ge| H), and three roundings."""
+    z = torch.full((t, v), torch.finfo(DT[dtype]).min, dtype=DT[dtype], device="cuda")
+    a = torch.arange(t, dtype=torch.int32, device="cuda") % v
+    g = torch.Generator(device="cuda").manual_seed(1)
+    gl, ge = torch.randn(t, generator=g, device="cuda"), torch.randn(t, generator=g, device="cuda")
+    for scale in (1.0, 0.9, 0.8, 0.77, 0.7, 0.6, 0.55, 0.3, 0.1, 0.01):
+        plan = T.TokenLogp(v, dtype, scale=scale)
+        _, h, lse, _, _ = plan.forward(z, a)
+        dz = plan.backward(z, a, lse, h, grad_logp=gl, grad_entropy=ge)
+        assert plan.status() == (0, 0)
+        room = scale * (2 * gl.abs() + ge.abs() * h) * (1 + 3 * torch.finfo(DT[dtype]).eps)
+        assert (dz.float().abs() <= room[:, None]).all(), scale
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("t,v", [(4, 50), (4, 60000), (600, 9000)])
+@pytest.mark.parametrize("kind", ["first half", "tail", "all but one", "every other"])
+def test_gradients_beside_lowest_values(T, dtype, t, v, kind):  # noqa: F811
+    from test_gpu_logp import gradient
+    z, a = rows_of(t, v, dtype)
+    z[:, KINDS[kind](v)] = torch.finfo(DT[dtype]).min
+    scale = torch.tensor(0.7).item()
+    plan = T.TokenLogp(v, dtype, scale=0.7)
+    _, h, lse, _, _ = plan.forward(z, a)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    gl, ge = torch.randn(t, generator=g, device="cuda"), torch.randn(t, generator=g, device="cuda")
+    want, size = gradient(z, a, lse, h, gl, ge, scale)
+    got = plan.backward(z, a, lse, h, grad_logp=gl, grad_entropy=ge)
+    # (size has 0 * inf in lowest places, where p is 0)
+    assert ((got.double() - want).abs() <= size.nan_to_num(0.0) + want.abs() * torch.finfo(DT[dtype]).eps / 2 + 1e-37).all()
