@@ -476,7 +476,7 @@ __device__ __forceinline__ GradIn grad_in(const LogpParams &p, int64_t t) {
     GradIn r;
     r.a = p.tokens ? p.tokens[t] : 0;
     r.lse = p.lse_in[t];
-    r.h = p.entropy_in ? p.entropy_in[t] : 0.f;
+    r.h = p.grad_entropy ? p.entropy_in[t] : 0.f;  // (unasked for otherwise, whatever it holds)
     r.gl = p.grad_logp ? p.grad_logp[t] : 0.f;
     r.ge = p.grad_entropy ? p.grad_entropy[t] : 0.f;
     return r;
