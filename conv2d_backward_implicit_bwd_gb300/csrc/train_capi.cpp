@@ -631,8 +631,9 @@ conv_bwd_status conv_bwd_policy_get_status(conv_bwd_policy_plan p, void *stream,
 conv_bwd_status conv_bwd_logp_create(const conv_bwd_logp_desc *d, conv_bwd_logp_plan *out) {
     if (!out) return CONV_BWD_ERR_INVALID_ARG;
     *out = nullptr;
+    // (scale log2(e) is finite)
     if (!d || d->vocab < 1 || !known_dtype(d->dtype) || d->top < 0 || d->top > d->vocab ||
-        !(d->scale > 0.f && std::isfinite(d->scale)))
+        !(d->scale > 0.f && d->scale <= 0x1p127f))
         return CONV_BWD_ERR_INVALID_ARG;
     if (d->vocab > (1LL << 30) || d->top > kLogpTop) return CONV_BWD_ERR_UNSUPPORTED;
     return create_plan(out, [&](conv_bwd_logp_plan_s &p) {

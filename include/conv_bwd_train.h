@@ -217,7 +217,7 @@ typedef struct {
     int64_t vocab;
     int32_t dtype;   /* conv_bwd_dtype of logits and dlogits */
     int32_t top;     /* 0 .. 32 alternatives of a row */
-    float scale;     /* > 0, finite */
+    float scale;     /* > 0, at most 2^127 */
 } conv_bwd_logp_desc;
 
 typedef struct conv_bwd_logp_plan_s *conv_bwd_logp_plan;
