@@ -123,19 +123,34 @@ def _stream(stream, device):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-# 0.9 us instead of 1.5 for a tensor on the current device, which in a call is the plan's (the library refuses others)
-_new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
-
-
 def _empty(shape, dtype, device, stream):
     """A new tensor whose memory belongs to the call's stream."""
     if stream is None:
-        if _new is not None and device.type == "cuda" and len(shape) < 3:
-            return _new(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype)
         return torch.empty(shape, dtype=dtype, device=device)
     s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
     with torch.cuda.stream(s):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+# The allocator's own entry, on the current device and past dispatch modes.
+_new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+_current, _modes = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_len_torch_dispatch_stack", None)
+
+
+def _outputs(device, stream):
+    """What makes a call's new vectors and matrices of (shape, dtype): `_empty`, or, for calls with many of them, the allocator's own
+    entry (1.1 us each instead of 1.5) where neither of its liberties makes a difference: the current device is the tensors', and
+    no mode (one that follows shapes or memory, say) is on."""
+    if stream is not None or _new is None or _current is None or _modes is None or device.index != _current() or _modes():
+        return lambda shape, dtype: _empty(shape, dtype, device, stream)
+    return _own_entry
+
+
+def _own_entry(shape, dtype):
+    try:
+        return _new(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype)
+    except TypeError:  # it takes other arguments in this version
+        return torch.empty(shape, dtype=dtype, device="cuda")
 
 
 # (a tensor's device as a number: -1 on the CPU; a plan made without a device has one that no tensor has)
@@ -433,11 +448,12 @@ class TokenLogp(_Plan):
         t, ld = _rows(logits, self.vocab, self.dtype, at, "logits")
         given = None if tokens is None else _vector(tokens, t, torch.int32, at, "tokens")
         device, f = logits.device, torch.float32
-        logp = None if tokens is None else _empty((t,), f, device, stream)
-        entropy, lse = _empty((t,), f, device, stream), _empty((t,), f, device, stream)
+        new = _outputs(device, stream)
+        logp = None if tokens is None else new((t,), f)
+        entropy, lse = new((t,), f), new((t,), f)
         top_logp = top_tokens = None
         if self.top:
-            top_logp, top_tokens = _empty((t, self.top), f, device, stream), _empty((t, self.top), torch.int32, device, stream)
+            top_logp, top_tokens = new((t, self.top), f), new((t, self.top), torch.int32)
         _check(_lib.conv_bwd_logp_forward(self._h, t, logits.data_ptr(), ld, given, None if logp is None else logp.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
                                           top_logp.data_ptr() if self.top else None, top_tokens.data_ptr() if self.top else None, _stream(stream, device)), "conv_bwd_logp_forward")
         return logp, entropy, lse, top_logp, top_tokens
