@@ -989,12 +989,12 @@ static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const 
     return launch_orth_steps(q, p->wide, p->pairs, s) == cudaSuccess ? CONV_BWD_OK : CONV_BWD_ERR_CUDA;
 }
 
-// Checks a stack of matrices with row stride ld and matrix stride ls (0: dense) and fills the strides in.
+// Checks a stack of matrices with row stride ld (0: cols) and matrix stride ls (0: rows ld) and fills the strides in.
 static conv_bwd_status orth_strides(const conv_bwd_orth_desc &d, int64_t &ld, int64_t &ls, size_t es, size_t &bytes) {
     if (ld == 0) ld = d.cols;
     if (ld < d.cols) return CONV_BWD_ERR_INVALID_ARG;
     if (ld > (1LL << 31)) return CONV_BWD_ERR_UNSUPPORTED;
-    if (ls == 0) ls = ld * (d.rows - 1) + d.cols;
+    if (ls == 0) ls = ld * d.rows;
     if (ls < ld * (d.rows - 1) + d.cols) return CONV_BWD_ERR_INVALID_ARG;
     if (ls > (1LL << 40)) return CONV_BWD_ERR_UNSUPPORTED;
     bytes = ((size_t)(d.batch - 1) * (size_t)ls + (size_t)(d.rows - 1) * (size_t)ld + (size_t)d.cols) * es;

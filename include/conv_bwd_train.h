@@ -280,7 +280,7 @@ typedef struct conv_bwd_orth_plan_s *conv_bwd_orth_plan;
 conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *desc, conv_bwd_orth_plan *out);
 conv_bwd_status conv_bwd_orth_destroy(conv_bwd_orth_plan plan);
 
-/* ld* are row strides, ls* matrix strides in elements (0: dense).  out may be x
+/* ld* are row strides, ls* matrix strides in elements (0: cols, resp. rows * ld*).  out may be x
  * itself (with its strides).  Errors: INVALID_ARG (NULL, rows or matrices that overlap one
  * another, out that overlaps x otherwise), MISALIGNED (a pointer not aligned to its element),
  * UNSUPPORTED (a stride > 2^31 or 2^40), CUDA. */
