@@ -31,9 +31,9 @@
 // host's bound of 32 on each coefficient keeps below singular values of 1.5; what is joined the host has followed.)  The
 // accumulator truncates, about 2^-26 of the sum with each instruction; a new one is begun every `segment` k-blocks and
 // added in fp32 registers, under the other accumulator's MMAs.  Every two k-blocks the result's error is that of the same
-// products in fp32 (1024 x 2048, 8 directions over 1 % noise: 4.5e-5; every eight 1.4e-4, never 2.0e-4), but the sums take
-// power, and power is what bounds large batches: 32 of 1024 x 2048, steps apart, 2859, 2598 and 2553 us.  So fp32 results take two, bf16
-// results and steps on weights (of which X is a hundredth) eight.  (A last product of the hi halves alone would be 5 to 7 % of
+// products in fp32 (8 directions over 1 % noise, 1024 x 1024: 4.6e-5, in fp32 4.5e-5; every eight 1.4e-4), but the sums take
+// power, and power is what bounds large batches: 32 of 1024 x 2048 2226 us every eight, 2443 every two.  So plans of fp32 take two, and
+// those of bf16, whose inputs were rounded by 1.7e-3 of their norm, eight.  (A last product of the hi halves alone would be 5 to 7 % of
 // the time less, 32 of 1024 x 2048 2101 instead of 2226 us, but a bf16 result would be off by more than its own rounding:
 // by 1.3e-3 of its norm from the rounded exact one, like this by 2e-4.)
 //

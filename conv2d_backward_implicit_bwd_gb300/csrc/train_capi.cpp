@@ -951,7 +951,6 @@ struct OrthOut {
 };
 static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const OrthOut &o, cudaStream_t s) {
     const conv_bwd_orth_desc &d = p->d;
-    const bool fp32_result = o.result && d.dtype == CONV_BWD_F32;
     if (p->cluster) {
         OrthSmallParams q;
         std::memset(&q, 0, sizeof(q));
@@ -977,7 +976,7 @@ static conv_bwd_status orth_run(conv_bwd_orth_plan p, OrthPrepParams &pp, const 
     pp.bf16 = d.dtype == CONV_BWD_BF16;
     if (launch_orth_prep(pp, s) != cudaSuccess) return CONV_BWD_ERR_CUDA;
     OrthParams q = p->run;
-    q.segment = fp32_result ? 2 : 8;
+    q.segment = pp.bf16 ? 8 : 2;  // (of what a plan is given: bf16 has been rounded by more than the longer sums lose)
     q.result = o.result;
     q.bf16 = pp.bf16;
     q.weight = o.weight;

@@ -1,7 +1,7 @@
 """What the results of the orthogonalised updates are off by, against the iteration in 64 bits."""
 import pytest
 import torch
-from test_gpu_orth import T, iterate, matrices  # noqa: F401
+from test_gpu_orth import COEF, DT, T, iterate, matrices  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -19,3 +19,26 @@ def test_bf16_results_are_rounded_once(T, shape, coef):  # noqa: F811
     e = coef[0] * 2.0 ** -23 + (abs(coef[0]) + 3.4 * abs(coef[1])) * 2.0 ** -18
     off, own = (torch.linalg.matrix_norm(t.double() - x) for t in (got, x.bfloat16()))
     assert (off <= own + 2 * e).all(), (off - own).max()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1024, 2048), (1, 1024, 1024), (1, 512, 4096), (2, 2048, 300), (16, 1024, 768), (1, 100, 131), (1, 128, 2048)])
+@pytest.mark.parametrize("kind", ["few directions", "flat"])
+def test_five_steps(T, dtype, shape, kind):  # noqa: F811
+    """What the header says of them: below 2^-14 of X's norm in plans of fp32, 2^-12 in plans of bf16, in steps on weights as in results."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    b, m, n = shape
+    u = torch.randn(shape, generator=g, device="cuda")
+    if kind == "few directions":
+        u = torch.randn(b, m, 8, generator=g, device="cuda") @ torch.randn(b, 8, n, generator=g, device="cuda") + 0.01 * u
+    u = u.to(DT[dtype])
+    x, _ = iterate(u, [COEF] * 5)
+    plan, w, mom = T.Orthogonal(*shape, dtype), torch.zeros(shape, device="cuda"), torch.zeros(shape, device="cuda")
+    plan.update(w, u, mom, 1.0, beta=0.0, scale=1.0)  # w = -X
+    room = {"f32": 2.0 ** -14, "bf16": 2.0 ** -12}[dtype] * torch.linalg.matrix_norm(x)
+    off = torch.linalg.matrix_norm(-w.double() - x)
+    assert (off <= room).all(), (off / room).max()
+    if dtype == "f32":
+        off = torch.linalg.matrix_norm(plan.apply(u).double() - x)
+        assert (off <= room).all(), (off / room).max()
+    assert plan.status() == (0, 0)
