@@ -107,6 +107,11 @@ def _dtype(d):
         raise ValueError(f"dtype {d!r}: f32 or bf16 wanted") from None
 
 
+def _int32(n):
+    """For a 32-bit field: what does not fit stays out of range there (ctypes takes the low bits), and the library refuses it."""
+    return min(max(n, -(1 << 31)), (1 << 31) - 1)
+
+
 def _check(status, what):
     if status != OK:
         raise ConvBwdError(status, what)
@@ -437,7 +442,7 @@ class TokenLogp(_Plan):
         self.vocab, self.top = int(vocab), int(top)
         self._code = _dtype(dtype)
         self.dtype = _TORCH[self._code]
-        desc, h = LogpDesc(self.vocab, self._code, self.top, scale), _vp()
+        desc, h = LogpDesc(self.vocab, self._code, _int32(self.top), scale), _vp()
         _check(_lib.conv_bwd_logp_create(ctypes.byref(desc), ctypes.byref(h)), "conv_bwd_logp_create")
         self._h = h.value
 
@@ -503,12 +508,14 @@ class Orthogonal(_Plan):
         self._code = _dtype(dtype)
         self.dtype = _TORCH[self._code]
         c = list(coefficients)
+        n = max(self.steps, 1)
         if c and not hasattr(c[0], "__len__"):
-            c = [c] * max(self.steps, 1)
+            n = min(n, 64)  # (the library refuses more)
+            c = [c] * n
         c = [float(v) for triple in c for v in triple]
-        if len(c) != 3 * max(self.steps, 1):
+        if len(c) != 3 * n:
             raise ValueError(f"coefficients: three numbers, or three for each of {self.steps} steps wanted")
-        desc, h = OrthDesc(*self._shape, self._code, self.steps, (_f32 * len(c))(*c)), _vp()
+        desc, h = OrthDesc(*self._shape, self._code, _int32(self.steps), (_f32 * len(c))(*c)), _vp()
         _check(_lib.conv_bwd_orth_create(ctypes.byref(desc), ctypes.byref(h)), "conv_bwd_orth_create")
         self._h = h.value
 
