@@ -1029,6 +1029,7 @@ conv_bwd_status conv_bwd_orth_update(conv_bwd_orth_plan p, float *weight, const 
     Range range("conv_bwd_orth_update");
     if (!p || !weight || !grad || !momentum) return CONV_BWD_ERR_INVALID_ARG;
     if (!std::isfinite(lr) || !std::isfinite(decay) || !std::isfinite(scale) || !(beta >= 0.f && beta <= 1.f)) return CONV_BWD_ERR_INVALID_ARG;
+    if (!std::isfinite(lr * scale) || !std::isfinite(lr * decay)) return CONV_BWD_ERR_INVALID_ARG;  // (times a zero of X: NaN)
     const conv_bwd_orth_desc &d = p->d;
     const size_t es = esize(d.dtype), n = (size_t)d.batch * d.rows * d.cols;
     size_t ng;

@@ -292,7 +292,8 @@ conv_bwd_status conv_bwd_orth_apply(conv_bwd_orth_plan plan, const void *x, int6
                                     int64_t ldo, int64_t lso, void *stream);
 
 /* weight and momentum fp32, copy bf16 (may be NULL), dense and without overlap
- * with one another or grad.  lr, decay and scale finite, 0 <= beta <= 1 (else INVALID_ARG). */
+ * with one another or grad.  lr, decay, scale, lr scale and lr decay finite, 0 <= beta <= 1
+ * (else INVALID_ARG). */
 conv_bwd_status conv_bwd_orth_update(conv_bwd_orth_plan plan, float *weight, const void *grad, int64_t ldg, int64_t lsg,
                                      float *momentum, void *copy, float lr, float beta, int32_t nesterov, float decay,
                                      float scale, void *stream);
