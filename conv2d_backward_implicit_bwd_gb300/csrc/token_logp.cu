@@ -11,15 +11,20 @@
 //
 // Alternatives: keys of 64 bits, the value's order above the inverted index, so the
 // largest of any set is unique (ties go to the lowest index) and the result does not
-// depend on the order of work.  Their search costs the pass nothing: each thread has
+// depend on the order of work.  The pass itself keeps little for them: each thread has
 // its elements' maximum anyway, and that of its other chunks.  `top` elements lie at or
 // above the top-th largest of 32 maxima, each of eight threads' elements (or of 64, of four);
 // only threads whose maximum is there have candidates (some two dozen for 20
 // alternatives), mostly in the one chunk that it came from, and that chunk's vectors are
 // read again, from L2, by the warp that ends the row, while the others are at the next
 // one.  It sorts the elements that reach the bound 32 at a time.  (8192 rows of 32768
-// with 20 alternatives 125 us, without any 90; candidates taken out during the pass
-// against a rising bound 551, taken out by the workers after it 188.)
+// with 20 alternatives 125 us, without any 90: what the ending warps issue, and their
+// second reading; candidates taken out during the pass against a rising bound 551,
+// taken out by the workers after it 188.)
+//
+// Which lane sums which element goes by the row's address (what precedes its first 16
+// bytes), and how many blocks take part by the number of rows: lse, logp and entropy of a
+// row may differ in their last bits between addresses, row strides and batches.
 //
 // Wide rows stream through a ring of 16 KB buffers that one thread fills with
 // bulk copies, as in the policy loss; where rows are few each is cut into parts, and
@@ -237,8 +242,9 @@ __device__ __forceinline__ K merged(K a, K b, int lane) {
 // A bound of the `top` largest from two elements of each lane (as ordered()): the top-th of the lanes' larger ones; for many
 // the top-th of all 64, above which there are 64 ln(64 / (64 - top)) elements to expect instead of 32 ln(32 / (32 - top)): 24, 31
 // at 20, 44, 130 at 32.
-// For few the maximum is taken off again and again, which takes less than a sorting network (8192 rows of 32768 bf16, five: 105
-// us, sorted 108).
+// For few the maximum is taken off again and again, which takes less than a sorting network (8192 rows of 32768 bf16, one
+// alternative 104 us, sorted 108; eight 110, 114; ten 112, 115; by the maximum sixteen 122, sorted 120.  4000 rows of 4096 fp32,
+// three 24.9, 25.2; ten 27.8, 27.3.)
 __device__ __forceinline__ uint32_t bound_of(uint32_t a, uint32_t b, int top, int lane) {
     if (top <= 10) {
         uint32_t x = max(a, b), m = 0;
@@ -404,8 +410,9 @@ __global__ void __launch_bounds__(NT) logp_warp_kernel(const LogpParams p) {
         const Sums r = total(run.r);
         if constexpr (TOP) {
             // Candidates are the lanes' ends, and mostly one batch of a lane, else all of its vectors, read by the warp
-            // or, where these are few beside the lanes, by the lane (20000 rows of 1000 bf16 with 20 alternatives 47 us, else 51; with
-            // five 40, else 35).
+            // or, where these are few beside the lanes and the candidates many, by the lane (20000 rows of bf16, by the lane and by the
+            // warp: 1000 columns with five alternatives 39 and 35 us, with 20 47 and 51, with 32 54 and 59; 500 with 20 42 and 41;
+            // 2000 with 20 66 and 62).
             const uint32_t mine = ordered_number(best), other = ordered_number(second);
             const uint32_t low = bound_of(ordered_number(fmaxf(best, fmaxf(ends[0], ends[1]))), other, p.top, lane);
             const bool in = mine >= low, few = nv <= 128 && p.top > 16, more = in && (few || other >= low);
@@ -654,7 +661,9 @@ static_assert(sizeof(Part) == kLogpPart, "workspace");
 
 constexpr int kFewParts = 4;
 // The largest of all parts' lists, by one warp, a part to a lane.  (Of a few parts, whose lists are read beside their sums: merged one by
-// one; 64 rows of 128000 bf16, five alternatives: 13.1 us, the other way 15.7.)
+// one.  Rows of 128000 bf16, five alternatives, the other way: 150 rows of two parts 15.6, 18.0 us; 100 of three 13.6, 15.9; 76 of four
+// 13.0, 15.3.  Merging would still be ahead at five to eight, 60 rows of five 12.4, 13.8, 38 of eight 11.7, 12.2, for eight more
+// registers a lane.)
 __device__ __forceinline__ uint64_t best_of_parts(const Part *row, int parts, int top, uint64_t *queue, int lane) {
     List list(queue, top, -INFINITY, lane);
     for (int q0 = 0; q0 < parts; q0 += 32) {

@@ -243,8 +243,8 @@ struct OrthSmallParams {
 cudaError_t launch_orth_small(const OrthSmallParams &p, cudaStream_t s);
 #ifdef __CUDACC__
 // A sum of squares: of those far from both ends of fp32 in fp32, of the others in fp64 (a conversion and an addition of fp64
-// for every element would take longer than the memory).  What an addition in fp32 leaves goes into the next one: a thread
-// adds up to 2^14 numbers, equal ones with errors that all point one way.
+// for every element would take longer than the memory).  What an addition in fp32 leaves goes into the next one: a thread may
+// add 2^16 numbers (2^34 elements by 304 blocks), equal ones with errors that all point one way.
 struct SquareSum {
     float safe, lost;
     double rest;

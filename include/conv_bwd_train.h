@@ -230,14 +230,15 @@ conv_bwd_status conv_bwd_logp_destroy(conv_bwd_logp_plan plan);
  * (not looked at where top is 0), all fully written.  rows = 0 writes nothing.
  * Errors: INVALID_ARG (NULL, rows < 0, ld < vocab, tokens without logp or the
  * reverse, an output that overlaps an input or another output), MISALIGNED,
- * UNSUPPORTED (rows > 2^31 - 2^16), CUDA. */
+ * UNSUPPORTED (rows > 2^31 - 2^16, ld > 2^31), CUDA. */
 conv_bwd_status conv_bwd_logp_forward(conv_bwd_logp_plan plan, int64_t rows, const void *logits, int64_t ld,
                                       const int32_t *tokens, float *logp, float *entropy, float *lse,
                                       float *top_logp, int32_t *top_tokens, void *stream);
 
 /* dlogits from the forward's lse and entropy and the gradients of logp and
  * entropy [rows]; either gradient may be NULL (then entropy may be, with
- * grad_entropy), not both.  dlogits [rows][ldd] may be logits itself (with ldd = ld). */
+ * grad_entropy), not both; entropy without grad_entropy is not read.  dlogits
+ * [rows][ldd] may be logits itself (with ldd = ld).  Errors as forward's (ldd too). */
 conv_bwd_status conv_bwd_logp_backward(conv_bwd_logp_plan plan, int64_t rows, const void *logits, int64_t ld,
                                        const int32_t *tokens, const float *lse, const float *entropy,
                                        const float *grad_logp, const float *grad_entropy, void *dlogits,
