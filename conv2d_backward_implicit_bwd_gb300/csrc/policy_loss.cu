@@ -95,7 +95,10 @@ struct Grad {
     __device__ __forceinline__ Grad() : cs(0.f), csi(0.f), e(0.f, 1.f), lse(0.f), scale(0.f) {}
     template <bool NEAR>
     __device__ __forceinline__ float other(float z) const {
-        return -csi * (MODE == kPolBackward ? ex2(fmaf(z, scale, -lse) * kLog2e) : e.at<NEAR>(z));
+        if (MODE != kPolBackward) return -csi * e.at<NEAR>(z);
+        // log p is not above 0; in a row of the type's lowest value it comes out anywhere within lse's last bit, 2^103
+        const float u = fmaf(z, scale, -lse);
+        return -csi * ex2((u > 1.f ? 0.f : u) * kLog2e);
     }
     __device__ __forceinline__ float one(float z, bool chosen) const {
         const float g = e.near ? other<true>(z) : other<false>(z);
