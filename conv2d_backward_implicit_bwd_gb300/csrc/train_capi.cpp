@@ -864,16 +864,17 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
             const int64_t mt = (g + 255) / 256;
             return mt * ((g + w - 1) / w) - mt * (mt - 1) / 2 * (256 / w);
         };
-        // Wide tiles where the symmetric products have one for every pair.  (50 of 489 x 1142: 823 us, narrow ones 841; 32 of
-        // 1024 x 2048 2061, 2314.  In pieces where they are fewer: 2 of 1024 x 4096, steps apart, 430, narrow ones 413; 1000 x
-        // 1000 322, 217.)
+        // Wide tiles where the symmetric products have one for every pair.  (32 of 1024 x 2048 2197 us, narrow ones 2368; 50 of 489
+        // x 1142 792 both ways.  Where they are fewer, in pieces, in an earlier form: 2 of 1024 x 4096, steps apart, 430, narrow ones
+        // 413; 1000 x 1000 322, 217.)
         p.wide = tiles_sym(256) * d->batch >= pairs;
         const int64_t w = p.wide ? 256 : 128;
         q.tiles_sym = (int32_t)tiles_sym(w);
         q.tiles_all = (int32_t)tiles_all(w);
         // Pieces of a contraction, where pairs would else be idle: as many as make the shortest round.  (A k-block takes 0.65
-        // us, the joining of two pieces 3.3, of three 3.7.  1000 x 1000 203 us, never in pieces 240; 600 x 600 in three of four
-        // k-blocks 172, whole 176; 700 x 700 in three 164, in two 170; 300 x 513 in two of five 142, whole 138.)
+        // us, the joining of two pieces 3.3, of three 3.7.  1000 x 1000 207 us, never in pieces 243; 600 x 600 in three of four
+        // k-blocks 175, whole 177; 300 x 513 in two of five 142, whole 138.  700 x 700, whose rows are whole lines of memory, would be
+        // faster whole than in three: 150, 161.)
         auto splits = [&](int64_t tiles, int64_t depth) {
             const int64_t blocks = (depth + 63) / 64, most = std::min(pairs / (tiles * d->batch), (int64_t)kOrthSplits);
             int32_t best = 1;
@@ -895,8 +896,8 @@ conv_bwd_status conv_bwd_orth_create(const conv_bwd_orth_desc *d, conv_bwd_orth_
         }
         // Three steps at a time (two products over the larger side instead of six, ten symmetric ones instead of three) where
         // X is large beside its Gram matrix, and sooner where products fill the machine than where each is a round of tiles.
-        // (Joined, apart: 32 of 1024 x 2048 2061, 2572 us, x 1536 1849, 2056, x 1280 1755, 1799, x 1024 1649, 1531; 2 of 1024 x
-        // 4096 338, 424; 1 of 200 x 4096 148, 168; 1000 x 1500 256, 219; 20 of 300 x 512 171, 159, of 256 x 600 144, 147.  Two
+        // (Joined, apart: 32 of 1024 x 2048 2197, 2702 us, x 1536 1971, 2171, x 1280 1852, 1907, x 1024 1720, 1606; 2 of 1024 x
+        // 4096 303, 384; 1 of 200 x 4096 148, 166; 1000 x 1500 242, 215; 20 of 300 x 512 173, 155, of 256 x 600 142, 143.  Two
         // at a time took 8 to 10 % more than three.)
         const bool join = h >= 2 * g || (p.wide && 4 * h >= 5 * g);
         const int joined = join && orth_may_join(d->coefficients, d->steps, kOrthJoined) ? kOrthJoined : 1;
